@@ -56,6 +56,7 @@ extern "C" {
 #define COLI_E_NONFINITE -6  /* (device) non-finite activation or router score */
 #define COLI_E_ROUTE -7      /* (device) expert index outside the table or naming an unset entry */
 #define COLI_E_TIMEOUT -8    /* (device) a bounded wait inside a kernel gave up (never expected) */
+#define COLI_E_RANGE -9      /* (device) a cache length, page index or row range outside its array */
 
 #define COLI_DTYPE_F32 0     /* IEEE binary32 */
 #define COLI_DTYPE_BF16 1    /* bfloat16 (upper half of a binary32) */
@@ -68,6 +69,10 @@ extern "C" {
 #define COLI_MAX_GROUP_TOKENS 1024  /* S for coli_expert_group */
 #define COLI_MAX_GROUP_DIM 8192     /* D (model width) for coli_expert_group */
 #define COLI_MAX_ISSUES 16          /* pending coli_expert_group_issue calls per round */
+#define COLI_MAX_KV_ROWS 16777216   /* T (token rows) of the cache calls */
+#define COLI_MAX_KV_SEQS 65536      /* B (sequences) of the cache calls */
+#define COLI_MAX_KV_HEADS 256       /* key/value heads of a cache */
+#define COLI_MAX_KV_GROUP 64        /* query heads per key/value head */
 
 typedef struct coli_ctx coli_ctx;
 
@@ -98,13 +103,16 @@ COLI_API int coli_reserve(coli_ctx *ctx, int max_S, int max_E, int max_K, int ma
 
 /* Per-kernel timing: when on, every kernel launch of this context is bracketed by two CUDA events
  * recorded on the context's stream (off by default). Kinds: COLI_KERNEL_ROUTER, _GATEUP, _DOWN,
- * _COMBINE, _LINEAR. coli_profile_read synchronises the stream and returns, for one kind, the summed event
+ * _COMBINE, _LINEAR, _CACHE, _ATTENTION, _NORM. coli_profile_read synchronises the stream and returns, for one kind, the summed event
  * time in milliseconds and the number of launches since the previous read of that kind. */
 #define COLI_KERNEL_ROUTER 0
 #define COLI_KERNEL_GATEUP 1
 #define COLI_KERNEL_DOWN 2
 #define COLI_KERNEL_COMBINE 3
 #define COLI_KERNEL_LINEAR 4
+#define COLI_KERNEL_CACHE 5
+#define COLI_KERNEL_ATTENTION 6
+#define COLI_KERNEL_NORM 7
 COLI_API int coli_profile_enable(coli_ctx *ctx, int on);
 COLI_API int coli_profile_read(coli_ctx *ctx, int kind, double *total_ms, long long *launches);
 
@@ -336,6 +344,102 @@ COLI_API int coli_ans_free(coli_ctx *ctx, uint64_t handle);
  */
 COLI_API int coli_ans_w4_linear(coli_ctx *ctx, uint64_t handle, const float *scales, int O, int I, int gs,
                                 const void *x, int x_dtype, const void *resid, void *y);
+
+/*
+ * Key/value cache in 4 bits: pages of tokens, written as they come and attended to in place.
+ *
+ * Format. A group of gs neighbouring channels of one token and head holds a scale s and an offset o
+ * (both bfloat16) and a 4-bit code n per channel, which stands for  o + s (n - 8) -- the offset-8
+ * nibble of the int4 tensors with an offset added, since keys are not centred. For a group x of a
+ * token's channels, every step rounded to binary32:
+ *   s = bf16((max x - min x) * (1/15)),  0 if that is below the smallest normal number
+ *   o = bf16(min x + 8 s)
+ *   n = clamp(rint((x - o) * (1/s)) + 8, 0, 15),  8 where s = 0
+ * A group that holds a non-finite value (or whose span overflows) is kept as NaN (s = 0, o = NaN)
+ * and sets COLI_E_NONFINITE. Keys and values have the same format.
+ *
+ * The cache is one device allocation of coli_kv4_bytes() bytes that the caller owns (16-byte
+ * aligned, contents need no clearing); its inner layout belongs to the library. head_dim is 64, 128
+ * or 256; gs is 32, 64 or 128 with gs <= head_dim <= 4 gs; page_tokens is 16, 32, 64, 128 or 256;
+ * heads <= COLI_MAX_KV_HEADS; pages * page_tokens < 2^31. A (page, token, head) takes
+ * head_dim + 8 head_dim / gs bytes for its key and value.
+ *
+ * Plan. The calls describe a batch of B sequences by device arrays (int32):
+ *   lens [B]: tokens of each sequence, those of this call included;
+ *   table [B x table_stride]: page of each run of page_tokens tokens of a sequence;
+ *   q_start [B + 1] or NULL: sequence b owns the rows q_start[b] .. q_start[b+1] of the call's
+ *     T-row arrays, in increasing order, and they are its LAST positions: row i of its m rows is at
+ *     position lens[b] - m + i. NULL: one row per sequence, T == B. Rows outside every sequence's
+ *     range are left alone. A row with a negative position (a sequence shorter than its rows)
+ *     stores nothing and reads zeros.
+ * A length that does not fit the table (lens < 0 or > table_stride * page_tokens), a page index
+ * outside the cache, or a row range outside 0..T sets COLI_E_RANGE; nothing outside the arrays is
+ * touched, the length is clamped, rows of a bad page are not written and read as zeros, and an
+ * attention over one has undefined (finite or NaN) values for that sequence.
+ * Sequences may share pages that no call in flight writes.
+ */
+typedef struct coli_kv4_cache {
+  void *base;          /* device pointer, 16-byte aligned, coli_kv4_bytes() bytes */
+  int pages;
+  int page_tokens;
+  int heads;
+  int head_dim;
+  int gs;
+} coli_kv4_cache;
+
+/* Bytes of a cache of this shape; 0 if the shape is not supported. Host only. */
+COLI_API uint64_t coli_kv4_bytes(int pages, int page_tokens, int heads, int head_dim, int gs);
+
+/* Quantise T rows of keys and values into the cache. k, v: [T x heads x head_dim] in dtype, the
+ * channels and heads of a row contiguous, rows k_stride / v_stride elements apart (so slices of a
+ * fused projection's output serve as they are); strides of at least heads * head_dim. Any alignment
+ * that the dtype has. COLI_E_INVAL for a bad argument. Profiled as COLI_KERNEL_CACHE. */
+COLI_API int coli_kv4_append(coli_ctx *ctx, const coli_kv4_cache *cache, const void *k, long long k_stride,
+                             const void *v, long long v_stride, int dtype, int T, const int32_t *q_start,
+                             const int32_t *lens, int B, const int32_t *table, int table_stride);
+
+/* Read rows back: the values that the codes stand for, computed in binary32 and rounded to dtype
+ * once. The same plan as coli_kv4_append, so a call with the same arguments gives back what that
+ * call wrote; with q_start the running sum of lens it gives whole sequences. k, v: outputs. */
+COLI_API int coli_kv4_read(coli_ctx *ctx, const coli_kv4_cache *cache, void *k, long long k_stride, void *v,
+                           long long v_stride, int dtype, int T, const int32_t *q_start, const int32_t *lens, int B,
+                           const int32_t *table, int table_stride);
+
+/*
+ * Attention of T query rows over the cache, which already holds the rows' own keys and values
+ * (coli_kv4_append first). For a row at position p of sequence b and query head h,
+ *   out = sum_t a_t V_t / sum_t a_t,  a_t = exp(scale * q . K_t),
+ * over the positions t <= p of its sequence, with window > 0 only the last `window` of them
+ * (t > p - window), of key/value head h / (q_heads / heads). A row that sees nothing gives zeros.
+ * q, out: [T x q_heads x head_dim] in dtype, rows q_stride / out_stride elements apart; q_heads a
+ * multiple of heads, at most COLI_MAX_KV_GROUP times it; scale finite; out must not overlap q.
+ * Scores, the softmax's maximum and sum, and the output are held in binary32 (bf16 queries: weights
+ * enter the product with V in 11 bits; f32: queries and weights in 22; weights below 2^-38 of a row's
+ * largest count as nothing). Results do not change from run to run. A non-finite query sets COLI_E_NONFINITE and gives NaN in its row.
+ * Profiled as COLI_KERNEL_ATTENTION.
+ */
+COLI_API int coli_kv4_attention(coli_ctx *ctx, const coli_kv4_cache *cache, const void *q, long long q_stride,
+                                int dtype, int q_heads, int T, const int32_t *q_start, const int32_t *lens, int B,
+                                const int32_t *table, int table_stride, float scale, int window, void *out,
+                                long long out_stride);
+
+/*
+ * Norms around a block, fused with its gate, residual scale and residual:
+ *   b = block                                                    (w_post NULL)
+ *   b = block * rsqrt(mean(block^2) + eps) * w_post              (otherwise)
+ *   h = resid + alpha * g * b,   g = 1 (gate NULL), gate, or sigmoid(gate) if gate_sigmoid
+ *   x = h * rsqrt(mean(h^2) + eps) * w_pre                       (w_pre NULL: x is not computed)
+ * per row, in binary32; x is formed from h before h is rounded to dtype. block, resid, h, x:
+ * [S x D] in dtype; gate: [gate_rows x D] in dtype, gate_rows = S, or 1 for one gate per channel;
+ * w_post, w_pre: [D] f32. block NULL: h = resid (then gate, w_post must be NULL) -- the norm before
+ * a first block. resid NULL: h = alpha * g * b. h_out NULL: h is not stored; h_out may be resid or
+ * block, x may be block or resid if h_out is not the same array; no other overlap. eps >= 0.
+ * 1 <= S <= COLI_MAX_TOKENS, 1 <= D <= COLI_MAX_DIM. A row whose mean square is not finite sets
+ * COLI_E_NONFINITE. Profiled as COLI_KERNEL_NORM.
+ */
+COLI_API int coli_norm_residual(coli_ctx *ctx, const void *block, const void *resid, const void *gate, int gate_rows,
+                                int gate_sigmoid, float alpha, const float *w_post, const float *w_pre, float eps,
+                                int dtype, int S, int D, void *h_out, void *x_out);
 
 #ifdef __cplusplus
 }

@@ -38,6 +38,7 @@ COLI_E_FORMAT = _C["COLI_E_FORMAT"]
 COLI_E_NONFINITE = _C["COLI_E_NONFINITE"]
 COLI_E_ROUTE = _C["COLI_E_ROUTE"]
 COLI_E_TIMEOUT = _C["COLI_E_TIMEOUT"]
+COLI_E_RANGE = _C["COLI_E_RANGE"]
 COLI_DTYPE_F32 = _C["COLI_DTYPE_F32"]
 COLI_DTYPE_BF16 = _C["COLI_DTYPE_BF16"]
 COLI_MAX_EXPERTS = _C["COLI_MAX_EXPERTS"]
@@ -47,6 +48,7 @@ COLI_MAX_ISSUES = _C["COLI_MAX_ISSUES"]
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_L = ctypes.c_longlong
 _U64 = ctypes.c_uint64
 
 SIGNATURES = {
@@ -77,6 +79,11 @@ SIGNATURES = {
     "coli_expert_group": (_I, [_P, _P, _I, _I, _P, _P, _P, _I, _P, _P]),
     "coli_expert_group_issue": (_I, [_P, _P, _I, _I, _P, _P, _P, _I]),
     "coli_expert_group_take": (_I, [_P, _P, _P]),
+    "coli_kv4_bytes": (_U64, [_I, _I, _I, _I, _I]),
+    "coli_kv4_append": (_I, [_P, _P, _P, _L, _P, _L, _I, _I, _P, _P, _I, _P, _I]),
+    "coli_kv4_read": (_I, [_P, _P, _P, _L, _P, _L, _I, _I, _P, _P, _I, _P, _I]),
+    "coli_kv4_attention": (_I, [_P, _P, _P, _L, _I, _I, _I, _P, _P, _I, _P, _I, _F, _I, _P, _L]),
+    "coli_norm_residual": (_I, [_P, _P, _P, _P, _I, _I, _F, _P, _P, _F, _I, _I, _I, _P, _P]),
     "coli_profile_enable": (_I, [_P, _I]),
     "coli_profile_read": (_I, [_P, _I, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_longlong)]),
 }
@@ -86,6 +93,9 @@ COLI_KERNEL_GATEUP = _C["COLI_KERNEL_GATEUP"]
 COLI_KERNEL_DOWN = _C["COLI_KERNEL_DOWN"]
 COLI_KERNEL_COMBINE = _C["COLI_KERNEL_COMBINE"]
 COLI_KERNEL_LINEAR = _C["COLI_KERNEL_LINEAR"]
+COLI_KERNEL_CACHE = _C["COLI_KERNEL_CACHE"]
+COLI_KERNEL_ATTENTION = _C["COLI_KERNEL_ATTENTION"]
+COLI_KERNEL_NORM = _C["COLI_KERNEL_NORM"]
 
 
 class ColiError(RuntimeError):
@@ -391,6 +401,113 @@ def coli_ans_decode(ctx, handle, out):
 
 def coli_ans_free(ctx, handle):
     return _check(ctx, library().coli_ans_free(ctx, handle), "coli_ans_free")
+
+
+class KV4Cache:
+    """A 4-bit key/value cache: the device memory (``data``, a uint8 tensor that this object owns) and its shape."""
+
+    class _Struct(ctypes.Structure):
+        _fields_ = [("base", _P), ("pages", _I), ("page_tokens", _I), ("heads", _I), ("head_dim", _I), ("gs", _I)]
+
+    def __init__(self, data, pages, page_tokens, heads, head_dim, gs):
+        self.data, self.pages, self.page_tokens = data, pages, page_tokens
+        self.heads, self.head_dim, self.gs = heads, head_dim, gs
+        self._struct = self._Struct(data.data_ptr(), pages, page_tokens, heads, head_dim, gs)
+        self._as_parameter_ = ctypes.addressof(self._struct)
+
+
+def coli_kv4_bytes(pages, page_tokens, heads, head_dim, gs):
+    """Bytes of a cache of this shape; 0 if the shape is not supported."""
+    return library().coli_kv4_bytes(pages, page_tokens, heads, head_dim, gs)
+
+
+def coli_kv4_cache(pages, page_tokens, heads, head_dim, gs, device="cuda"):
+    """Allocate a 4-bit cache of ``pages`` pages of ``page_tokens`` tokens (contents undefined until written)."""
+    n = coli_kv4_bytes(pages, page_tokens, heads, head_dim, gs)
+    if n == 0:
+        raise ValueError("kv4_cache: shape not supported")
+    return KV4Cache(torch.empty(n, dtype=torch.uint8, device=device), pages, page_tokens, heads, head_dim, gs)
+
+
+def _rows3(t, heads, head_dim, name):
+    """A [T x heads x head_dim] CUDA tensor whose rows may be apart; returns its row stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+        raise ValueError(f"{name} must be [T x {heads} x {head_dim}]")
+    row, h, d = t.stride()
+    if (d != 1 and head_dim > 1) or (h != head_dim and heads > 1):
+        raise ValueError(f"{name}: the heads and channels of a row must be contiguous")
+    return heads * head_dim if t.shape[0] == 1 else row
+
+
+def _kv4_plan(T, lens, table, q_start):
+    _dev(lens, torch.int32, "lens")
+    _dev(table, torch.int32, "table")
+    _dev(q_start, torch.int32, "q_start")
+    n = lens.numel()
+    if table.dim() != 2 or table.shape[0] != n or (q_start is not None and q_start.numel() != n + 1):
+        raise ValueError("plan: lens [B], table [B x pages per sequence] and q_start [B + 1] or None")
+    if q_start is None and T != n:
+        raise ValueError("plan: without q_start there is one row per sequence")
+    return _ptr(q_start), lens.data_ptr(), n, table.data_ptr(), table.shape[1]
+
+
+def _kv4_pair(name, ctx, cache, k, v, lens, table, q_start):
+    if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must have the same rows and dtype")
+    T = k.shape[0]
+    ks, vs = _rows3(k, cache.heads, cache.head_dim, "k"), _rows3(v, cache.heads, cache.head_dim, "v")
+    qs, ln, n, tb, width = _kv4_plan(T, lens, table, q_start)
+    rc = getattr(library(), name)(ctx, cache, k.data_ptr(), ks, v.data_ptr(), vs, act_dtype(k), T, qs, ln, n, tb, width)
+    return rc if rc == COLI_OK else _check(ctx, rc, name)
+
+
+def coli_kv4_append(ctx, cache, k, v, lens, table, q_start=None):
+    """Quantise rows k, v [T x heads x head_dim] into the cache: the last rows of each sequence (lens counts them)."""
+    return _kv4_pair("coli_kv4_append", ctx, cache, k, v, lens, table, q_start)
+
+
+def coli_kv4_read(ctx, cache, k, v, lens, table, q_start=None):
+    """Read the same rows back into k, v."""
+    return _kv4_pair("coli_kv4_read", ctx, cache, k, v, lens, table, q_start)
+
+
+def coli_kv4_attention(ctx, cache, q, lens, table, out, q_start=None, scale=None, window=0):
+    """out = softmax(scale q K) V over each row's sequence up to its own position (the last ``window`` of it);
+    q, out [T x q_heads x head_dim]; scale defaults to head_dim ** -0.5."""
+    if q.dim() != 3 or out.dtype != q.dtype or out.shape != q.shape:
+        raise ValueError("kv4_attention: q and out must be [T x q_heads x head_dim] of one dtype")
+    T, heads, _ = q.shape
+    qs, os_ = _rows3(q, heads, cache.head_dim, "q"), _rows3(out, heads, cache.head_dim, "out")
+    st, ln, n, tb, width = _kv4_plan(T, lens, table, q_start)
+    rc = library().coli_kv4_attention(ctx, cache, q.data_ptr(), qs, act_dtype(q), heads, T, st, ln, n, tb, width,
+                                      cache.head_dim ** -0.5 if scale is None else scale, window, out.data_ptr(), os_)
+    return rc if rc == COLI_OK else _check(ctx, rc, "coli_kv4_attention")
+
+
+def coli_norm_residual(ctx, block, resid, gate, alpha, w_post, w_pre, eps, h, x, gate_sigmoid=False):
+    """h = resid + alpha * gate * rmsnorm(block, w_post), x = rmsnorm(h, w_pre), [S x D]; gate [S x D] or [D]. Any of
+    block, resid, gate, w_post, (w_pre and x), h may be None, as coli_moe.h says."""
+    first = block if block is not None else resid
+    if first is None or first.dim() != 2:
+        raise ValueError("norm_residual: block or resid must be given, [S x D]")
+    S, D = first.shape
+    for t, name in ((block, "block"), (resid, "resid"), (h, "h"), (x, "x")):
+        if t is not None and _dev(t, first.dtype, name).shape != first.shape:
+            raise ValueError(f"norm_residual: {name} must be [S x D]")
+    rows = 0
+    if gate is not None:
+        _dev(gate, first.dtype, "gate")
+        rows = 1 if gate.numel() == D else S
+        if gate.numel() != rows * D:
+            raise ValueError("norm_residual: gate must be [S x D] or [D]")
+    for t, name in ((w_post, "w_post"), (w_pre, "w_pre")):
+        if t is not None and _dev(t, torch.float32, name).numel() != D:
+            raise ValueError(f"norm_residual: {name} must be [D]")
+    rc = library().coli_norm_residual(ctx, _ptr(block), _ptr(resid), _ptr(gate), rows, int(gate_sigmoid), alpha,
+                                      _ptr(w_post), _ptr(w_pre), eps, act_dtype(first), S, D, _ptr(h), _ptr(x))
+    return rc if rc == COLI_OK else _check(ctx, rc, "coli_norm_residual")
 
 
 def coli_profile_enable(ctx, on):

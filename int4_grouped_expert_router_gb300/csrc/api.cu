@@ -9,6 +9,8 @@
 #include "coli_internal.h"
 #include "ans.h"
 #include "ep.h"
+#include "kv4.h"
+#include "norm.h"
 
 namespace coli {
 
@@ -315,8 +317,9 @@ int coli_check_error(coli_ctx* ctx) {
     e = cudaMemset(ctx->d_status, 0, code == COLI_E_TIMEOUT ? kStatusBytes : sizeof(int));
     if (e != cudaSuccess) return cuda_fail(ctx, e, "coli_check_error: clear error word");
     ctx->last_error = code == COLI_E_ROUTE ? "device: expert index out of range or unset table entry"
-                      : code == COLI_E_NONFINITE ? "device: non-finite activation or router score"
+                      : code == COLI_E_NONFINITE ? "device: non-finite activation, router score or cache entry"
                       : code == COLI_E_TIMEOUT   ? "device: a bounded wait inside a kernel gave up"
+                      : code == COLI_E_RANGE     ? "device: a cache length, page index or row range outside its array"
                                                  : "device error";
   }
   return code;
@@ -329,7 +332,7 @@ int coli_profile_enable(coli_ctx* ctx, int on) {
 }
 
 int coli_profile_read(coli_ctx* ctx, int kind, double* total_ms, long long* launches) {
-  if (!ctx || kind < 0 || kind > COLI_KERNEL_LINEAR || !total_ms || !launches) return COLI_E_INVAL;
+  if (!ctx || kind < 0 || kind > COLI_KERNEL_NORM || !total_ms || !launches) return COLI_E_INVAL;
   cudaSetDevice(ctx->device);
   cudaError_t e = cudaStreamSynchronize(ctx->stream);
   if (e != cudaSuccess) return cuda_fail(ctx, e, "coli_profile_read: stream sync");
@@ -776,6 +779,126 @@ int coli_expert_group_take(coli_ctx* ctx, const void* resid, void* y) {
   ctx->compute_calls++;
   ctx->n_issued = 0;
   return COLI_OK;
+}
+
+uint64_t coli_kv4_bytes(int pages, int page_tokens, int heads, int head_dim, int gs) {
+  if (pages < 1 || heads < 1 || heads > COLI_MAX_KV_HEADS) return 0;
+  if (page_tokens != 16 && page_tokens != 32 && page_tokens != 64 && page_tokens != 128 && page_tokens != 256) return 0;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+  if ((gs != 32 && gs != 64 && gs != 128) || gs > head_dim || head_dim > 4 * gs) return 0;
+  if ((uint64_t)pages * (uint64_t)page_tokens >= (1ull << 31)) return 0;
+  return (uint64_t)pages * heads * (page_tokens / kKvUnit) * kv4_unit_bytes(head_dim, head_dim / gs);
+}
+
+// Checks shared by the three cache calls.
+static int kv4_check(coli_ctx* ctx, const char* who, const coli_kv4_cache* cache, const void* a, const void* b, int dtype,
+                     int T, const int32_t* q_start, const int32_t* lens, int B, const int32_t* table, int table_stride) {
+  const std::string w = who;
+  if (!cache || !cache->base || !a || !b || !lens || !table) return fail(ctx, COLI_E_INVAL, w + ": NULL pointer");
+  if (coli_kv4_bytes(cache->pages, cache->page_tokens, cache->heads, cache->head_dim, cache->gs) == 0)
+    return fail(ctx, COLI_E_INVAL, w + ": cache shape not supported");
+  if (((uintptr_t)cache->base & 15) != 0) return fail(ctx, COLI_E_INVAL, w + ": cache memory must be 16-byte aligned");
+  if (dtype != COLI_DTYPE_F32 && dtype != COLI_DTYPE_BF16) return fail(ctx, COLI_E_INVAL, w + ": dtype");
+  const uintptr_t elem = dtype == COLI_DTYPE_F32 ? 4 : 2;
+  if (((uintptr_t)a | (uintptr_t)b) % elem != 0) return fail(ctx, COLI_E_INVAL, w + ": array not aligned to its dtype");
+  if (T < 1 || T > COLI_MAX_KV_ROWS || B < 1 || B > COLI_MAX_KV_SEQS || table_stride < 1)
+    return fail(ctx, COLI_E_INVAL, w + ": size out of range");
+  if (!q_start && T != B) return fail(ctx, COLI_E_INVAL, w + ": without q_start there is one row per sequence (T == B)");
+  return COLI_OK;
+}
+
+static Kv4View kv4_view(const coli_kv4_cache* c) {
+  Kv4View v;
+  v.base = static_cast<uint8_t*>(c->base);
+  v.pages = c->pages;
+  v.heads = c->heads;
+  v.page_log2 = 4;
+  while ((1 << v.page_log2) < c->page_tokens) v.page_log2++;
+  v.hd = c->head_dim;
+  v.ng = c->head_dim / c->gs;
+  return v;
+}
+
+int coli_kv4_append(coli_ctx* ctx, const coli_kv4_cache* cache, const void* k, long long k_stride, const void* v,
+                    long long v_stride, int dtype, int T, const int32_t* q_start, const int32_t* lens, int B,
+                    const int32_t* table, int table_stride) {
+  if (!ctx) return COLI_E_INVAL;
+  int rc = kv4_check(ctx, "kv4_append", cache, k, v, dtype, T, q_start, lens, B, table, table_stride);
+  if (rc != COLI_OK) return rc;
+  const long long row = (long long)cache->heads * cache->head_dim;
+  if (k_stride < row || v_stride < row) return fail(ctx, COLI_E_INVAL, "kv4_append: row stride below heads * head_dim");
+  if (injected(ctx)) return COLI_E_INJECTED;
+  cudaSetDevice(ctx->device);
+  rc = launch_kv4_append(ctx, kv4_view(cache), Kv4Plan{q_start, lens, table, T, B, table_stride}, k, k_stride, v, v_stride,
+                         dtype);
+  if (rc == COLI_OK) ctx->compute_calls++;
+  return rc;
+}
+
+int coli_kv4_read(coli_ctx* ctx, const coli_kv4_cache* cache, void* k, long long k_stride, void* v, long long v_stride,
+                  int dtype, int T, const int32_t* q_start, const int32_t* lens, int B, const int32_t* table,
+                  int table_stride) {
+  if (!ctx) return COLI_E_INVAL;
+  int rc = kv4_check(ctx, "kv4_read", cache, k, v, dtype, T, q_start, lens, B, table, table_stride);
+  if (rc != COLI_OK) return rc;
+  const long long row = (long long)cache->heads * cache->head_dim;
+  if (k_stride < row || v_stride < row) return fail(ctx, COLI_E_INVAL, "kv4_read: row stride below heads * head_dim");
+  if (injected(ctx)) return COLI_E_INJECTED;
+  cudaSetDevice(ctx->device);
+  rc = launch_kv4_read(ctx, kv4_view(cache), Kv4Plan{q_start, lens, table, T, B, table_stride}, k, k_stride, v, v_stride,
+                       dtype);
+  if (rc == COLI_OK) ctx->compute_calls++;
+  return rc;
+}
+
+int coli_kv4_attention(coli_ctx* ctx, const coli_kv4_cache* cache, const void* q, long long q_stride, int dtype, int q_heads,
+                       int T, const int32_t* q_start, const int32_t* lens, int B, const int32_t* table, int table_stride,
+                       float scale, int window, void* out, long long out_stride) {
+  if (!ctx) return COLI_E_INVAL;
+  int rc = kv4_check(ctx, "kv4_attention", cache, q, out, dtype, T, q_start, lens, B, table, table_stride);
+  if (rc != COLI_OK) return rc;
+  if (q_heads < 1 || q_heads % cache->heads != 0 || q_heads / cache->heads > COLI_MAX_KV_GROUP)
+    return fail(ctx, COLI_E_INVAL, "kv4_attention: q_heads must be a multiple of the cache's heads, at most COLI_MAX_KV_GROUP of them each");
+  const long long row = (long long)q_heads * cache->head_dim;
+  if (q_stride < row || out_stride < row)
+    return fail(ctx, COLI_E_INVAL, "kv4_attention: row stride below q_heads * head_dim");
+  if (!(scale == scale) || scale - scale != 0.f) return fail(ctx, COLI_E_INVAL, "kv4_attention: scale must be finite");
+  if (window < 0) return fail(ctx, COLI_E_INVAL, "kv4_attention: window must not be negative");
+  if (injected(ctx)) return COLI_E_INJECTED;
+  cudaSetDevice(ctx->device);
+  rc = launch_kv4_attention(ctx, kv4_view(cache), Kv4Plan{q_start, lens, table, T, B, table_stride}, q, q_stride, dtype,
+                            q_heads, scale, window, out, out_stride);
+  if (rc == COLI_OK) ctx->compute_calls++;
+  return rc;
+}
+
+int coli_norm_residual(coli_ctx* ctx, const void* block, const void* resid, const void* gate, int gate_rows,
+                       int gate_sigmoid, float alpha, const float* w_post, const float* w_pre, float eps, int dtype, int S,
+                       int D, void* h_out, void* x_out) {
+  if (!ctx) return COLI_E_INVAL;
+  if (!block && (!resid || gate || w_post))
+    return fail(ctx, COLI_E_INVAL, "norm_residual: without a block there is a residual and neither gate nor w_post");
+  if (!h_out && !x_out) return fail(ctx, COLI_E_INVAL, "norm_residual: no output");
+  if ((x_out != nullptr) != (w_pre != nullptr))
+    return fail(ctx, COLI_E_INVAL, "norm_residual: x_out and w_pre come together");
+  if (dtype != COLI_DTYPE_F32 && dtype != COLI_DTYPE_BF16) return fail(ctx, COLI_E_INVAL, "norm_residual: dtype");
+  if (S < 1 || S > COLI_MAX_TOKENS || D < 1 || D > COLI_MAX_DIM)
+    return fail(ctx, COLI_E_INVAL, "norm_residual: size out of range");
+  if (gate && gate_rows != 1 && gate_rows != S)
+    return fail(ctx, COLI_E_INVAL, "norm_residual: gate_rows must be 1 or S");
+  if (!(eps >= 0.f) || eps - eps != 0.f || alpha - alpha != 0.f)
+    return fail(ctx, COLI_E_INVAL, "norm_residual: alpha must be finite and eps finite and not negative");
+  if (x_out && x_out == h_out) return fail(ctx, COLI_E_INVAL, "norm_residual: h_out and x_out are the same array");
+  const uintptr_t elem = dtype == COLI_DTYPE_F32 ? 4 : 2;
+  if (((uintptr_t)block | (uintptr_t)resid | (uintptr_t)gate | (uintptr_t)h_out | (uintptr_t)x_out) % elem != 0 ||
+      ((uintptr_t)w_post | (uintptr_t)w_pre) % 4 != 0)
+    return fail(ctx, COLI_E_INVAL, "norm_residual: array not aligned to its dtype");
+  if (injected(ctx)) return COLI_E_INJECTED;
+  cudaSetDevice(ctx->device);
+  NormArgs a{block, resid, gate, gate && gate_rows > 1, gate_sigmoid != 0, alpha, w_post, w_pre, eps, dtype, S, D, h_out, x_out};
+  int rc = launch_norm_residual(ctx, a);
+  if (rc == COLI_OK) ctx->compute_calls++;
+  return rc;
 }
 
 }  // extern "C"

@@ -151,8 +151,8 @@ struct coli_ctx {
   };
   std::vector<ProfRec> prof_pending;
   std::vector<cudaEvent_t> prof_free;
-  double prof_ms[5] = {0, 0, 0, 0, 0};
-  long long prof_n[5] = {0, 0, 0, 0, 0};
+  double prof_ms[COLI_KERNEL_NORM + 1] = {};
+  long long prof_n[COLI_KERNEL_NORM + 1] = {};
 };
 
 namespace coli {
