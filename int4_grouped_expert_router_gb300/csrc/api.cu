@@ -249,6 +249,9 @@ int coli_init(coli_ctx** out, int device, void* cuda_stream) {
   if ((e = cudaMalloc(&p, kStatusBytes)) != cudaSuccess) goto fail;
   ctx->d_status = static_cast<int*>(p);
   if ((e = cudaMemset(ctx->d_status, 0, kStatusBytes)) != cudaSuccess) goto fail;
+  if ((e = cudaMalloc(&p, kKvCounters * sizeof(int))) != cudaSuccess) goto fail;
+  ctx->d_kv_count = static_cast<int*>(p);
+  if ((e = cudaMemset(ctx->d_kv_count, 0, kKvCounters * sizeof(int))) != cudaSuccess) goto fail;
   if ((e = cudaMalloc(&ctx->d_router, kRouterScratchBytes)) != cudaSuccess) goto fail;
   if ((e = cudaMemset(ctx->d_router, 0, kRouterScratchBytes)) != cudaSuccess) goto fail;
   {
@@ -282,6 +285,7 @@ void coli_destroy(coli_ctx* ctx) {
   if (ctx->d_table) cudaFree(ctx->d_table);
   if (ctx->d_status) cudaFree(ctx->d_status);
   if (ctx->d_router) cudaFree(ctx->d_router);
+  if (ctx->d_kv_count) cudaFree(ctx->d_kv_count);
   if (ctx->ws.base) cudaFree(ctx->ws.base);
   if (ctx->slots) cudaFree(ctx->slots);
   for (auto& r : ctx->prof_pending) {

@@ -32,6 +32,9 @@ constexpr int kPanelCols = 16;
 // logits of at most 15 tokens x 1024 (column part, expert) pairs.
 constexpr size_t kRouterScratchBytes = 256 + (size_t)15 * 1024 * 8;
 
+// Arrival counters of split work in the cache attention (one per CTA of its grid), zero between calls.
+constexpr int kKvCounters = 4096;
+
 // Device status words of a context: [0] error code, [1] unused, [2..] the opt-in fused decode
 // kernel's synchronisation words (grid barrier at [2], [3]; row-range counters from
 // [2 + kSyncRanges]). All start at zero, and the grid barrier's count only grows.
@@ -135,6 +138,7 @@ struct coli_ctx {
   void* d_router = nullptr;
   int router_rows = 0, router_parts = 0;
   int test_withhold_router = 0;
+  int* d_kv_count = nullptr;  // coli::kKvCounters arrival counters of the cache attention, zero between calls
   coli::Workspace ws;
   // resident issue/take: f32 partial sums [COLI_MAX_ISSUES][S x D] of the current round's issues
   float* slots = nullptr;

@@ -1,8 +1,32 @@
-// Attention over the 4-bit key/value cache (layout: kv4.h).
+// Attention over the 4-bit key/value cache (layout: kv4.h), for decode steps, drafts and short prompts.
 //
 // For a query row q at position p of its sequence and the visible positions t,
 //   x_t = scale sum_g [ s_tg q_g . (n_tg - 8) + o_tg sum(q_g) ],   out = sum_t a_t V_t / sum_t a_t,
-// a_t = exp(x_t - max x), one pass over the tokens with a running maximum and sum.
+//   a_t = exp(x_t - max x),   sum_t a_t V_t = sum_t (a_t s_tg) (n_tg - 8) + sum_t a_t o_tg,
+// one pass over the tokens with a running maximum and sum. The codes enter the matrix instructions as
+// the small integers n - 8 that they are (exact in 16 bits), so nothing is dequantised: a group's
+// scale and offset are applied to the score of its token, and to the weight a_t before V.
+//
+// What bounds it: the cache's bytes, read once (a key/value head's codes serve all of its query heads).
+//
+// Work split. An item is (sequence, key/value head, tile of 8 NT query rows); its tokens are cut into
+// stages of 64, and all items' stages, end to end, are dealt out evenly and contiguously to a grid that
+// fills the device: whatever the lengths, every CTA streams the same number of bytes. An item that
+// spans CTAs leaves partial (maximum, sum, output) triples in the workspace, and the CTA that arrives
+// last adds them up in CTA order, so that results do not depend on who is last.
+//
+// In a CTA a producer warp fills a ring of stages with bulk copies, a run of units of a page each (64
+// tokens are 8.7 KB at hd = 128, gs = 128: codes and scales of keys and values together), and four
+// consumer warps take one unit (16 tokens) of each stage, with their own running maximum and sum; they
+// are joined in shared memory when the item ends.
+//
+// Consumer, per unit: S^T = K q^T with m16n8k16 (rows = 16 tokens, columns = 8 query rows: group sizes
+// up to 8 fill the instruction, where queries as rows would leave half of it empty), the softmax on the
+// accumulators, the weights transposed in registers (movmatrix), O^T += V^T a (rows = 16 channels).
+#include <cuda_fp16.h>
+
+#include <atomic>
+
 #include "kv4.h"
 #include "pipe.h"
 
@@ -10,110 +34,852 @@ namespace coli {
 
 namespace {
 
-constexpr int kTile = 128;  // tokens per step: one per thread
+constexpr int kStageUnits = 4;                    // consumer warps, and units of a stage
+constexpr int kStageTok = kStageUnits * kKvUnit;  // tokens of a stage
+constexpr int kConsumers = kStageUnits * 32;
+constexpr int kAttnThreads = kConsumers + 32;
+// A row's running maximum follows the scores only when one exceeds it by this much (log2): weights stay
+// below 2^kSlack.
+constexpr float kSlack = 1.f;
+constexpr float kInf = __builtin_huge_valf();
 
-__device__ __forceinline__ float value_of(uint32_t par, uint32_t n) {
-  return __uint_as_float(par & 0xffff0000u) + __uint_as_float(par << 16) * (float)((int)n - 8);
+template <int HD, int NG, int NT, bool F32>
+struct Cfg {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kWords = HD / 32;       // code words of a token a lane holds (keys); as many per token pair (values)
+  static constexpr int kWpg = kWords / NG;     // of which a group takes
+  static constexpr int kMt = HD / 16;          // 16-channel tiles of the output
+  static constexpr int kPad = HD + 4;          // floats of a row in the join buffer: no bank conflicts at 8-byte stores
+  static constexpr uint32_t kUnit = kv4_unit_bytes(HD, NG);
+  static constexpr uint32_t kStage = kStageUnits * kUnit;
+  static constexpr int kCtas = NT == 1 ? (HD == 256 ? 2 : 3) : (NT * HD <= 256 ? 2 : 1);  // resident per SM (registers)
+  static constexpr uint32_t kJoin = kStageUnits * kRows * (kPad + 2) * 4;
+  static constexpr uint32_t kQ = NT * (HD / 16) * 32 * 8 * (F32 ? 2 : 1);
+  static constexpr uint32_t kBudget = (kCtas == 3 ? 74 : kCtas == 2 ? 112 : 200) * 1024;
+  static constexpr int kRoom = (int)((kBudget - kJoin - kQ - 1024) / kStage);
+  static constexpr int kStages = kRoom > 12 ? 12 : kRoom;
+  static constexpr uint32_t kSmem = kStages * kStage + kJoin + kQ;
+  static_assert(kStages >= 3, "the ring needs a few stages");
+};
+
+// Where an item starts in the dealt-out stages, and what a CTA needs to know of it.
+struct Item {
+  int b, head, tile;     // sequence, key/value head, tile of query rows
+  int r0, m, len;        // the sequence's first row, its rows and its length
+  int first, stages;     // first stage of 64 tokens, number of stages (at least 1)
+};
+
+__device__ __forceinline__ void load_seq(const Kv4View& c, const Kv4Plan& p, int window, Item& it, int* err) {
+  int r1;
+  kv4_rows(p, it.b, it.r0, r1, err);
+  it.m = r1 - it.r0;
+  it.len = kv4_len(p, c.page_log2, it.b, err);
+  // the first row's window starts the sequence's visible part
+  const int lo = window > 0 ? max(0, it.len - it.m - window + 1) : 0;
+  it.first = lo / kStageTok;
+  it.stages = max(1, (it.len + kStageTok - 1) / kStageTok - it.first);
 }
 
-// One CTA per (row, query head): a thread scores one token of a tile; then a thread owns channels.
-template <bool BF16>
-__global__ void __launch_bounds__(kTile) kv4_attn_kernel(Kv4View c, Kv4Plan p, const void* q, long long q_stride,
-                                                         int q_heads, float scale, int window, void* out,
-                                                         long long out_stride, int* err) {
+__device__ __forceinline__ int tiles_of(int m, int group, int rows) { return (int)(((long long)m * group + rows - 1) / rows); }
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Four codes of word w as two registers' worth each: pair m of (w >> 4 m) & 0x000f000f, as the 16-bit
+// integers n - 8. The bits 0x6400 put a nibble at the end of 1024's mantissa (one logic operation), and at
+// bit 4 as sixteen times itself, which the multiply-add undoes.
+__device__ __forceinline__ void expand(uint32_t w, uint32_t (&a)[4]) {
+  const __half2 bias = __floats2half2_rn(1032.f, 1032.f);
+  const __half2 sixteenth = __floats2half2_rn(0.0625f, 0.0625f), bias16 = __floats2half2_rn(-72.f, -72.f);
+  const uint32_t w8 = w >> 8;
+  uint32_t t[4] = {(w & 0x000f000fu) | 0x64006400u, (w & 0x00f000f0u) | 0x64006400u, (w8 & 0x000f000fu) | 0x64006400u,
+                   (w8 & 0x00f000f0u) | 0x64006400u};
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const __half2 h = *reinterpret_cast<__half2*>(&t[i]);
+    const __half2 v = (i & 1) ? __hfma2(h, sixteenth, bias16) : __hsub2(h, bias);
+    a[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// N words of a lane from shared memory.
+template <int N>
+__device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 v = lds128(p + 4 * i);
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    }
+  } else if constexpr (N == 2) {
+    const uint2 v = lds64(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    static_assert(N == 1, "1, 2 or a multiple of 4 words");
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(smem_u32(p)) : "memory");
+  }
+}
+
+// A lane's code words of one 16-token key row or value pair row, kv4.h: iw words per access, accesses
+// `apart` bytes from each other.
+template <int WORDS>
+__device__ __forceinline__ void lds_codes(const uint8_t* p, int apart, uint32_t (&w)[WORDS]) {
+  if constexpr (WORDS <= 4) {
+    lds_words(p, w);
+  } else {
+    uint32_t lo[4], hi[4];
+    lds_words(p, lo);
+    lds_words(p + apart, hi);
+#pragma unroll
+    for (int i = 0; i < 4; i++) w[i] = lo[i], w[4 + i] = hi[i];
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ void load_q8(const void* q, size_t at, float (&v)[8], bool vec) {
+  if constexpr (F32) {
+    const float* s = static_cast<const float*>(q) + at;
+    if (vec) {
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(s)), b = __ldcg(reinterpret_cast<const float4*>(s) + 1);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i++) v[i] = __ldcg(s + i);
+    }
+  } else {
+    const unsigned short* s = static_cast<const unsigned short*>(q) + at;
+    if (vec) {
+      const uint4 a = __ldcg(reinterpret_cast<const uint4*>(s));
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; i++) v[2 * i] = lo_bf16(w[i]), v[2 * i + 1] = hi_bf16(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i++) v[i] = bf16_to_f32(__ldcg(s + i));
+    }
+  }
+}
+
+struct AttnArgs {
+  Kv4View c;
+  Kv4Plan p;
+  const void* q;
+  long long q_stride;
+  int group;      // query heads per key/value head
+  float scale;
+  int window;
+  void* out;
+  long long out_stride;
+  bool vec;       // q rows start at 16-byte boundaries
+  bool vec_out;   // out rows start at a boundary of four values
+  float* part;    // partial results: 2 per CTA, each kRows x HD outputs and kRows (maximum, sum) pairs
+  int* count;     // one per CTA: parts of the item that starts in it which have arrived
+  int* err;
+  uint64_t wait_ns;
+};
+
+template <bool F32>
+__device__ __forceinline__ void store4(void* out, size_t at, float4 v, bool vec) {
+  if constexpr (F32) {
+    float* o = static_cast<float*>(out) + at;
+    if (vec)
+      *reinterpret_cast<float4*>(o) = v;
+    else
+      o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(out) + at;
+    const uint16_t h[4] = {f32_to_bf16_rn(v.x), f32_to_bf16_rn(v.y), f32_to_bf16_rn(v.z), f32_to_bf16_rn(v.w)};
+    if (vec)
+      *reinterpret_cast<uint2*>(o) = make_uint2(h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16));
+    else
+      o[0] = h[0], o[1] = h[1], o[2] = h[2], o[3] = h[3];
+  }
+}
+
+template <int HD, int NG, int NT, bool F32>
+__global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4_attn_kernel(AttnArgs a) {
+  using C = Cfg<HD, NG, NT, F32>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* ring = smem;
+  float* s_join = reinterpret_cast<float*>(smem + C::kStages * C::kStage);  // [4][kRows][kPad], then maxima and sums
+  float* s_m = s_join + kStageUnits * C::kRows * C::kPad;                   // [4][kRows]
+  float* s_l = s_m + kStageUnits * C::kRows;
+  uint2* s_q = reinterpret_cast<uint2*>(smem + C::kStages * C::kStage + C::kJoin);  // query fragments [hi, lo][NT][HD / 16][32]
+  __shared__ __align__(8) uint64_t s_full[C::kStages], s_empty[C::kStages];
+  __shared__ long long s_sum[kAttnThreads / 32];
+  __shared__ long long s_at;
+  __shared__ int s_start, s_last;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; i++) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], kStageUnits);
+    }
+    mbar_fence_init();
+    s_start = a.p.B;
+  }
   griddep_launch_dependents();
   griddep_wait();
-  __shared__ float s_q[256], s_a[kTile], s_red[8];
-  __shared__ const uint8_t* s_unit[kTile];
-  const int row = blockIdx.x / q_heads, qh = blockIdx.x % q_heads, head = qh / (q_heads / c.heads);
-  const int tid = threadIdx.x, gs = c.hd / c.ng;
-  const int b = kv4_seq_of(p, row);
-  int r0, r1;
-  kv4_rows(p, b, r0, r1, err);
-  if (row < r0 || row >= r1) return;
-  const int pos = kv4_len(p, c.page_log2, b, err) - (r1 - row);
-  bool finite = true;
-  for (int d = tid; d < c.hd; d += kTile) {
-    s_q[d] = load_act(q, BF16 ? COLI_DTYPE_BF16 : COLI_DTYPE_F32, (size_t)(row * q_stride + qh * c.hd + d));
-    finite = finite && fabsf(s_q[d]) < __int_as_float(0x7f800000);
-  }
-  if (!finite) set_error(err, COLI_E_NONFINITE);
+
+  // ---- deal the stages out: total, then the sequence in which this CTA's share starts ----
+  const int heads = a.c.heads;
+  auto stages_in = [&](int b) -> long long {
+    Item t;
+    t.b = b;
+    load_seq(a.c, a.p, a.window, t, a.err);
+    return (long long)tiles_of(t.m, a.group, C::kRows) * heads * t.stages;
+  };
+  long long total = 0;
+  for (int b = tid; b < a.p.B; b += kAttnThreads) total += stages_in(b);
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) s_sum[warp] = total;
   __syncthreads();
-  float m = -__int_as_float(0x7f800000), l = 0.f, acc[2] = {0.f, 0.f};
-  const int first = window > 0 && pos - window + 1 > 0 ? pos - window + 1 : 0;
-  for (int t0 = first / 16 * 16; t0 <= pos; t0 += kTile) {
-    const int t = t0 + tid;
-    float x = -__int_as_float(0x7f800000);
-    const uint8_t* unit = nullptr;
-    if (t >= first && t <= pos) {
-      const int page = __ldcg(p.table + (size_t)b * p.table_stride + (t >> c.page_log2));
-      if (page < 0 || page >= c.pages) {
-        set_error(err, COLI_E_RANGE);
-      } else {
-        unit = kv4_unit(c, page, head, t & ((1 << c.page_log2) - 1));
-        x = 0.f;
-        for (int d = 0; d < c.hd; d += 8) {
-          const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(unit + kv4_k_word(c.hd, t & 15, d / 32, d % 32 / 8)));
-          const uint32_t par = __ldcg(reinterpret_cast<const uint32_t*>(unit + kv4_kscale_at(c.hd) + ((t & 15) * c.ng + d / gs) * 4));
-          for (int j = 0; j < 8; j++) x += s_q[d + j] * value_of(par, (w >> (4 * j)) & 15u);
+  total = 0;
+  for (int i = 0; i < kAttnThreads / 32; i++) total += s_sum[i];
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long w0 = per * blockIdx.x, w1 = w0 + per < total ? w0 + per : total;
+  if (w0 >= w1) return;  // uniform in the CTA; nothing in flight
+  long long before = 0;
+  for (int base = 0; base < a.p.B; base += kAttnThreads) {
+    const int b = base + tid;
+    const long long mine = b < a.p.B ? stages_in(b) : 0;
+    long long inc = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long n = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += n;
+    }
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = inc;
+    __syncthreads();
+    long long off = before, all = 0;
+    for (int i = 0; i < kAttnThreads / 32; i++) {
+      if (i < warp) off += s_sum[i];
+      all += s_sum[i];
+    }
+    const long long start = off + inc - mine;
+    if (mine > 0 && start <= w0 && w0 < start + mine) {
+      s_start = b;
+      s_at = start;
+    }
+    before += all;
+    if (before > w0) break;  // uniform
+  }
+  __syncthreads();
+
+  // ---- the cursor that producer and consumers walk on their own ----
+  Item it;
+  it.b = s_start;
+  load_seq(a.c, a.p, a.window, it, a.err);
+  const long long local = w0 - s_at;  // stages of this sequence before the share
+  const int tiles0 = tiles_of(it.m, a.group, C::kRows);
+  const long long item0 = local / it.stages;
+  it.head = (int)(item0 / tiles0);
+  it.tile = (int)(item0 % tiles0);
+  int stage = (int)(local % it.stages);  // within the item
+  long long w = w0;
+  auto next_item = [&]() {  // after the last stage of an item; w < w1 guarantees that there is one
+    if (++it.tile < tiles_of(it.m, a.group, C::kRows)) return;
+    it.tile = 0;
+    if (++it.head < heads) return;
+    it.head = 0;
+    do {
+      it.b++;
+      load_seq(a.c, a.p, a.window, it, a.err);
+    } while (it.m == 0 && it.b + 1 < a.p.B);
+  };
+
+  if (warp == kStageUnits) {
+    // ------------------------------------ producer ------------------------------------
+    const uint64_t policy = l2_evict_first_policy();
+    const int page_tok = 1 << a.c.page_log2;
+    int cached_b = -1, cached_from = 0, pages = 0;  // this lane's entry of 32 consecutive page numbers
+    int slot = 0;
+    uint32_t phase = 1;
+    while (w < w1) {
+      const int tok = (it.first + stage) * kStageTok;
+      const int units = min(kStageUnits, max(0, (it.len - tok + kKvUnit - 1) / kKvUnit));
+      const int page = tok >> a.c.page_log2;
+      const int copies = page_tok >= kStageTok ? (units > 0) : (units * kKvUnit + page_tok - 1) >> a.c.page_log2;
+      if (copies > 0 && (it.b != cached_b || page < cached_from || page + copies > cached_from + 32)) {
+        cached_b = it.b;
+        cached_from = page;
+        const int at = page + lane;
+        pages = at < a.p.table_stride ? __ldcg(a.p.table + (size_t)it.b * a.p.table_stride + at) : 0;
+      }
+      if (!mbar_wait_suspend(&s_empty[slot], phase, a.wait_ns)) {
+        if (lane == 0) set_error(a.err, COLI_E_TIMEOUT);
+        break;  // what was issued is still awaited by the consumers
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&s_full[slot], units * C::kUnit);
+      __syncwarp();
+      int pg = __shfl_sync(0xffffffffu, pages, (page - cached_from + lane) & 31);
+      if (lane < copies) {
+        if (pg < 0 || pg >= a.c.pages) {
+          set_error(a.err, COLI_E_RANGE);
+          pg = 0;  // some page of the cache in its place
         }
-        x *= scale;
+        const int per_copy = page_tok >= kStageTok ? kStageUnits : page_tok / kKvUnit;  // units
+        const int n = min(per_copy, units - lane * per_copy);
+        const uint8_t* src = a.c.base + (((size_t)pg * heads + it.head) * (size_t)(page_tok / kKvUnit) +
+                                         (tok & (page_tok - 1)) / kKvUnit) * C::kUnit;
+        bulk_g2s_stream(ring + slot * C::kStage + lane * per_copy * C::kUnit, src, n * C::kUnit, &s_full[slot], policy);
+      }
+      if (++slot == C::kStages) {
+        slot = 0;
+        phase ^= 1;
+      }
+      w++;
+      if (++stage == it.stages) {
+        stage = 0;
+        if (w < w1) next_item();
       }
     }
-    s_unit[tid] = unit;
-    float mx = x;
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if ((tid & 31) == 0) s_red[tid >> 5] = mx;
-    __syncthreads();
-    mx = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
-    const float mn = fmaxf(m, mx);
-    const float base = mn == -__int_as_float(0x7f800000) ? 0.f : mn;
-    const float a = expf(x - base);
-    s_a[tid] = a;
-    float sum = a;
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((tid & 31) == 0) s_red[4 + (tid >> 5)] = sum;
-    __syncthreads();
-    const float f = expf(m - base);
-    l = l * f + (s_red[4] + s_red[5] + s_red[6] + s_red[7]);
-    m = mn;
-    for (int h = 0, d = tid; d < c.hd; d += kTile, h++) {
-      const int i = d / 32, j = (d % 32) / 16 * 2 + d % 2, r = d % 16 / 2;
-      float y = acc[h] * f;
-      for (int s = 0; s < kTile && t0 + s <= pos; s++) {
-        const uint8_t* un = s_unit[s];
-        if (!un) continue;
-        const int tt = (t0 + s) & 15;
-        const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(un + kv4_v_at(c.hd, c.ng) + kv4_v_word(c.hd, tt >> 1, r, i)));
-        const uint32_t par = __ldcg(reinterpret_cast<const uint32_t*>(un + kv4_vscale_at(c.hd, c.ng) + (tt * c.ng + d / gs) * 4));
-        y += s_a[s] * value_of(par, (w >> (16 * (tt & 1) + 4 * j)) & 15u);
+    return;
+  }
+
+  // -------------------------------------- consumers --------------------------------------
+  const int r = lane >> 2, cc = lane & 3;
+  int slot = 0;
+  uint32_t phase = 0;
+  bool alive = true;
+  while (w < w1) {
+    // ---- a segment: this CTA's stages of one item ----
+    const long long item_at = w - stage;  // where the item starts in the dealt-out stages
+    const int n_here = (int)min((long long)(it.stages - stage), w1 - w);
+    const int tile_row = it.tile * C::kRows;
+    const int rows_all = it.m * a.group;  // this sequence's query rows per key/value head
+    const int row_n = min(C::kRows, rows_all - tile_row);
+
+    // queries: fragments of 16-bit integers-friendly values (each row scaled by a power of two so that its
+    // largest element lies in [2^14, 2^15): bf16 elements down to 2^-29 of it stay exact), their sums per
+    // group, and the factor that takes a row's scores to log2 units.
+    float fac[NT][2], sumq[NT][2][NG];
+    int pos[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+      const int row = tile_row + nt * 8 + r;
+      float v[C::kWords][8];
+      float amax = 0.f;
+      bool fin = true;
+      if (nt * 8 + r < row_n) {
+        const size_t at = (size_t)((it.r0 + row / a.group) * a.q_stride) + (size_t)(it.head * a.group + row % a.group) * HD;
+#pragma unroll
+        for (int i = 0; i < C::kWords; i++) {
+          load_q8<F32>(a.q, at + 32 * i + 8 * cc, v[i], a.vec);
+#pragma unroll
+          for (int j = 0; j < 8; j++) {
+            amax = fmaxf(amax, fabsf(v[i][j]));
+            fin = fin && fabsf(v[i][j]) < kInf;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < C::kWords; i++)
+#pragma unroll
+          for (int j = 0; j < 8; j++) v[i][j] = 0.f;
       }
-      acc[h] = y;
+      if (!fin) {
+        set_error(a.err, COLI_E_NONFINITE);
+        amax = kInf;
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // 2^(14 - floor(log2 amax)), its exponent kept within what binary32 has
+      const int ex = min(253, max(1, 127 + 14 + 127 - (int)(__float_as_uint(amax) >> 23)));
+      float mult = amax == 0.f ? 1.f : __uint_as_float((uint32_t)ex << 23);
+      const float inv = amax == 0.f ? 1.f : __uint_as_float((uint32_t)(254 - ex) << 23);
+      if (a.scale < 0.f) mult = -mult;
+      if (!(amax < kInf)) mult = __uint_as_float(0x7fc00000u);
+      float sum[NG];
+#pragma unroll
+      for (int g = 0; g < NG; g++) sum[g] = 0.f;
+#pragma unroll
+      for (int i = 0; i < C::kWords; i++)
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          v[i][j] *= mult;
+          sum[i / C::kWpg] += v[i][j];
+        }
+#pragma unroll
+      for (int g = 0; g < NG; g++) {
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+#pragma unroll
+        for (int e = 0; e < 2; e++) sumq[nt][e][g] = __shfl_sync(0xffffffffu, sum[g], (2 * cc + e) * 4);
+      }
+      const float f = fabsf(a.scale) * 1.4426950408889634f * inv;
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        fac[nt][e] = __shfl_sync(0xffffffffu, f, (2 * cc + e) * 4);
+        const int qr = min(tile_row + nt * 8 + 2 * cc + e, rows_all - 1);  // rows past the end count like the last
+        pos[nt][e] = it.len - it.m + qr / a.group;
+      }
+      // step 2 i + h of the contraction: k slots (2 c, 2 c + 1) and (2 c + 8, 2 c + 9) are channels
+      // (2 h, 2 h + 4) and (2 h + 1, 2 h + 5) of this lane's eight. Warp w keeps the steps of its share.
+#pragma unroll
+      for (int i = 0; i < C::kWords; i++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          if ((2 * i + h) % kStageUnits != warp) continue;
+          const int at = (nt * (HD / 16) + 2 * i + h) * 32 + lane;
+          const uint32_t b0 = pack_half2(v[i][2 * h], v[i][2 * h + 4]), b1 = pack_half2(v[i][2 * h + 1], v[i][2 * h + 5]);
+          s_q[at] = make_uint2(b0, b1);
+          if constexpr (F32) {
+            const __half2 h0 = *reinterpret_cast<const __half2*>(&b0), h1 = *reinterpret_cast<const __half2*>(&b1);
+            s_q[NT * (HD / 16) * 32 + at] =
+                make_uint2(pack_half2(v[i][2 * h] - __low2float(h0), v[i][2 * h + 4] - __high2float(h0)),
+                           pack_half2(v[i][2 * h + 1] - __low2float(h1), v[i][2 * h + 5] - __high2float(h1)));
+          }
+        }
     }
-    __syncthreads();
+    named_sync(1, kConsumers);
+    uint2 qf[NT == 1 ? HD / 16 : 1];  // one tile's fragments stay in registers
+    if constexpr (NT == 1) {
+#pragma unroll
+      for (int s = 0; s < HD / 16; s++) qf[s] = s_q[s * 32 + lane];
+    }
+
+    float o[NT][C::kMt][4], lsum[NT][2], bias[NT][2][NG], mf[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+#pragma unroll
+      for (int i = 0; i < C::kMt; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) o[nt][i][j] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        lsum[nt][e] = 0.f;
+        mf[nt][e] = -kInf;
+#pragma unroll
+        for (int g = 0; g < NG; g++) bias[nt][e][g] = 0.f;
+      }
+    }
+    // value scales are multiplied by vmul, a power of two that keeps them (and so weight x scale in 16 bits)
+    // below 2^14; it only shrinks, and the outputs with it.
+    float vmul = 0.f;
+    const int pos_min = it.len - it.m + tile_row / a.group;  // first row's position
+    const int lo_max = a.window > 0 ? it.len - it.m + (tile_row + row_n - 1) / a.group - a.window + 1 : 0;
+    const int pos_max = it.len - it.m + (tile_row + row_n - 1) / a.group;
+    const int lo_min = a.window > 0 ? pos_min - a.window + 1 : 0;
+
+    for (int n = 0; n < n_here; n++, w++, stage++) {
+      const int t0 = (it.first + stage) * kStageTok + warp * kKvUnit;
+      if (alive && !mbar_wait_suspend(&s_full[slot], phase, a.wait_ns)) {
+        set_error(a.err, COLI_E_TIMEOUT);
+        alive = false;  // whatever the ring holds is used: the result is void, but nothing hangs
+      }
+      const uint8_t* unit = ring + slot * C::kStage + warp * C::kUnit;
+      if (t0 <= pos_max && t0 + kKvUnit > lo_min) {  // some row of the tile sees some token of the unit
+        const bool masked = t0 + kKvUnit - 1 > pos_min || t0 < lo_max;
+        uint32_t kp[2][NG], vp[2][NG];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          lds_words(unit + kv4_kscale_at(HD) + (r + 8 * h) * NG * 4, kp[h]);
+          lds_words(unit + kv4_vscale_at(HD, NG) + (r + 8 * h) * NG * 4, vp[h]);
+        }
+        if (masked) {  // tokens past the sequence hold anything
+#pragma unroll
+          for (int h = 0; h < 2; h++)
+            if (t0 + r + 8 * h >= it.len) {
+#pragma unroll
+              for (int g = 0; g < NG; g++) vp[h][g] = 0;
+            }
+        }
+        // ---- scores ----
+        float x[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int j = 0; j < 4; j++) x[nt][j] = 0.f;
+        {
+          uint32_t kw[2][C::kWords];
+          lds_codes(unit + lane * (C::kWords < 4 ? C::kWords : 4) * 4, 1024, kw[0]);
+          lds_codes(unit + (C::kWords < 4 ? 32 * C::kWords * 4 : 512) + lane * (C::kWords < 4 ? C::kWords : 4) * 4, 1024, kw[1]);
+#pragma unroll
+          for (int g = 0; g < NG; g++) {
+            float acc[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+              for (int j = 0; j < 4; j++) acc[nt][j] = 0.f;
+#pragma unroll
+            for (int i = g * C::kWpg; i < (g + 1) * C::kWpg; i++) {
+              uint32_t a0[4], a1[4];
+              expand(kw[0][i], a0);
+              expand(kw[1][i], a1);
+#pragma unroll
+              for (int h = 0; h < 2; h++)
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                  uint2 b;
+                  if constexpr (NT == 1)
+                    b = qf[2 * i + h];
+                  else
+                    b = s_q[(nt * (HD / 16) + 2 * i + h) * 32 + lane];
+                  mma16816(acc[nt], a0[2 * h], a1[2 * h], a0[2 * h + 1], a1[2 * h + 1], b.x, b.y);
+                  if constexpr (F32) {
+                    const uint2 l = s_q[((NT + nt) * (HD / 16) + 2 * i + h) * 32 + lane];
+                    mma16816(acc[nt], a0[2 * h], a1[2 * h], a0[2 * h + 1], a1[2 * h + 1], l.x, l.y);
+                  }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+              for (int j = 0; j < 4; j++) {
+                const uint32_t kpar = kp[j >> 1][g];
+                x[nt][j] = fmaf(lo_bf16(kpar), acc[nt][j], fmaf(hi_bf16(kpar), sumq[nt][j & 1][g], x[nt][j]));
+              }
+          }
+        }
+        uint32_t vis = 0xffffffffu;  // bit 4 nt + j: row sees token
+        if (masked) {
+          vis = 0;
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+              const int t = t0 + r + 8 * (j >> 1);
+              const bool see = t <= pos[nt][j & 1] && (a.window <= 0 || t > pos[nt][j & 1] - a.window);
+              if (see)
+                vis |= 1u << (4 * nt + j);
+              else
+                x[nt][j] = -kInf;
+            }
+        }
+        // ---- running maximum: moves only when a score passes it by kSlack ----
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int j = 0; j < 4; j++) grow = grow || fmaf(fac[nt][j & 1], x[nt][j], -mf[nt][j & 1]) > kSlack;
+        float top = 0.f;  // largest value scale of the unit
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+          for (int g = 0; g < NG; g++) top = fmaxf(top, lo_bf16(vp[h][g]));
+        grow = grow || (vmul == 0.f ? top > 0.f : top * vmul >= 16384.f);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float seen = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+          float shrink = 1.f;
+          if (seen > 0.f && (vmul == 0.f || seen * vmul >= 16384.f)) {
+            // 2^(13 - floor(log2 seen)): seen * vmul in [2^13, 2^14)
+            const int ex = min(253, max(1, 127 + 13 + 127 - (int)(__float_as_uint(seen) >> 23)));
+            const float now = __uint_as_float((uint32_t)ex << 23);
+            shrink = vmul == 0.f ? 1.f : now / vmul;
+            vmul = now;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              float mx = fmaxf(x[nt][e], x[nt][2 + e]);
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              const float now = mx == -kInf ? mf[nt][e] : fmaxf(mf[nt][e], fac[nt][e] * mx);
+              const float f = mf[nt][e] == -kInf ? 1.f : exp2_fast(mf[nt][e] - now);
+              mf[nt][e] = now;
+              lsum[nt][e] *= f;
+#pragma unroll
+              for (int g = 0; g < NG; g++) bias[nt][e][g] *= f;
+#pragma unroll
+              for (int i = 0; i < C::kMt; i++) {
+                o[nt][i][e] *= f * shrink;
+                o[nt][i][2 + e] *= f * shrink;
+              }
+            }
+        }
+        // ---- weights, transposed into B fragments per group ----
+        // A bf16 call's weight enters the product as h = round(a s vmul) in 11 bits. The offset takes the same
+        // rounded weight, as h (o / (s vmul)): rounding it then scales the token's V as a whole, however far o is
+        // from it. The quotient gets a correction step, so that it is exact where V = 0 is. Where the scale is
+        // nothing beside the largest, the offset is V. With the 22 bits of an f32 call's weights a itself serves.
+        float vs[2][NG], vo[2][NG];
+        bool faint[2][NG];
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+          for (int g = 0; g < NG; g++) {
+            vs[h][g] = lo_bf16(vp[h][g]) * vmul;
+            vo[h][g] = hi_bf16(vp[h][g]);
+            faint[h][g] = F32 || vs[h][g] < 9.3132257e-10f;  // 2^-30
+            if (!faint[h][g]) {
+              const float inv = rcp_fast(vs[h][g]), q = vo[h][g] * inv;
+              vo[h][g] = fmaf(fmaf(-q, vs[h][g], vo[h][g]), inv, q);
+            }
+          }
+        uint32_t pb[NT][NG][2], pl[F32 ? NT : 1][NG][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+          float pr[4];
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            pr[j] = exp2_fast(fmaf(fac[nt][j & 1], x[nt][j], -mf[nt][j & 1]));
+            if (masked && !(vis >> (4 * nt + j) & 1)) pr[j] = 0.f;
+          }
+          lsum[nt][0] += pr[0] + pr[2];
+          lsum[nt][1] += pr[1] + pr[3];
+#pragma unroll
+          for (int g = 0; g < NG; g++) {
+            float pv[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) pv[j] = pr[j] * vs[j >> 1][g];
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              const uint32_t hi = pack_half2(pv[2 * h], pv[2 * h + 1]);
+              const __half2 hh = *reinterpret_cast<const __half2*>(&hi);
+              const float kept[2] = {__low2float(hh), __high2float(hh)};
+              pb[nt][g][h] = transpose8x8(hi);
+              if constexpr (F32) {
+                pl[nt][g][h] = transpose8x8(pack_half2(pv[2 * h] - kept[0], pv[2 * h + 1] - kept[1]));
+              }
+#pragma unroll
+              for (int e = 0; e < 2; e++) {
+                const int j = 2 * h + e;
+                float off = vo[h][g];
+                if (masked && !(vis >> (4 * nt + j) & 1)) off = 0.f;  // an unseen NaN stays unseen
+                bias[nt][e][g] = fmaf(faint[h][g] ? pr[j] : kept[e], off, bias[nt][e][g]);
+              }
+            }
+          }
+        }
+        // ---- output ----
+        {
+          const uint8_t* vb = unit + kv4_v_at(HD, NG) + lane * (C::kWords < 4 ? C::kWords : 4) * 4;
+          uint32_t vw[2][C::kWords];
+          lds_codes(vb, 512, vw[0]);
+          lds_codes(vb + 4 * HD, 512, vw[1]);
+#pragma unroll
+          for (int i = 0; i < C::kWords; i++) {
+            uint32_t a0[4], a1[4];
+            expand(vw[0][i], a0);
+            expand(vw[1][i], a1);
+            const int g = i / C::kWpg;
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+              for (int nt = 0; nt < NT; nt++) {
+                float(&d)[4] = o[nt][2 * i + h];
+                if constexpr (F32) {
+                  // the instruction's own accumulator is cut, not rounded: a unit's sum is formed from zero and
+                  // added in binary32
+                  float t[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma16816(t, a0[2 * h], a0[2 * h + 1], a1[2 * h], a1[2 * h + 1], pl[nt][g][0], pl[nt][g][1]);
+                  mma16816(t, a0[2 * h], a0[2 * h + 1], a1[2 * h], a1[2 * h + 1], pb[nt][g][0], pb[nt][g][1]);
+#pragma unroll
+                  for (int j = 0; j < 4; j++) d[j] += t[j];
+                } else {
+                  mma16816(d, a0[2 * h], a0[2 * h + 1], a1[2 * h], a1[2 * h + 1], pb[nt][g][0], pb[nt][g][1]);
+                }
+              }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_empty[slot]);
+      if (++slot == C::kStages) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
+
+    // ---- join the four warps ----
+    const float unscale = vmul == 0.f ? 0.f : 1.f / vmul;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        float l = lsum[nt][e];
+        for (int s = 4; s < 32; s <<= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+#pragma unroll
+        for (int g = 0; g < NG; g++) {
+          float t = bias[nt][e][g];
+          for (int s = 4; s < 32; s <<= 1) t += __shfl_xor_sync(0xffffffffu, t, s);
+          bias[nt][e][g] = t;
+        }
+        const int row = nt * 8 + 2 * cc + e;
+        if (r == 0) {
+          s_m[warp * C::kRows + row] = mf[nt][e];
+          s_l[warp * C::kRows + row] = l;
+        }
+        float* dst = s_join + (warp * C::kRows + row) * C::kPad + 2 * r;
+#pragma unroll
+        for (int i = 0; i < C::kMt; i++) {
+          const float add = bias[nt][e][(i / 2) / C::kWpg];
+          *reinterpret_cast<float2*>(dst + 16 * i) =
+              make_float2(fmaf(o[nt][i][e], unscale, add), fmaf(o[nt][i][2 + e], unscale, add));
+        }
+      }
+    named_sync(1, kConsumers);
+    const bool whole = n_here == it.stages;
+    const bool starts_here = item_at >= w0;
+    float* part = a.part + (size_t)(2 * blockIdx.x + starts_here) * C::kRows * (HD + 2);
+    auto out_at = [&](int row) {
+      const int q = tile_row + row;
+      return (size_t)((it.r0 + q / a.group) * a.out_stride) + (size_t)(it.head * a.group + q % a.group) * HD;
+    };
+    for (int i = tid; i < row_n * (HD / 4); i += kConsumers) {
+      const int row = i / (HD / 4), d = (i % (HD / 4)) * 4;
+      float mm = -kInf;
+#pragma unroll
+      for (int k = 0; k < kStageUnits; k++) mm = fmaxf(mm, s_m[k * C::kRows + row]);
+      float l = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kStageUnits; k++) {
+        const float f = s_m[k * C::kRows + row] == -kInf ? 0.f : exp2_fast(s_m[k * C::kRows + row] - mm);
+        // a warp without a maximum saw nothing, or only what is not a number
+        const float lk = s_l[k * C::kRows + row];
+        const float4 v = *reinterpret_cast<const float4*>(s_join + (k * C::kRows + row) * C::kPad + d);
+        if (f != 0.f || lk != 0.f) {
+          const float ff = lk == lk ? f : 1.f;
+          l += ff * lk;
+          y.x += ff * v.x, y.y += ff * v.y, y.z += ff * v.z, y.w += ff * v.w;
+        }
+      }
+      if (whole) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        store4<F32>(a.out, out_at(row) + d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv), a.vec_out);
+      } else {
+        __stcg(reinterpret_cast<float4*>(part + row * HD + d), y);
+        if (d == 0) __stcg(reinterpret_cast<float2*>(part + C::kRows * HD + 2 * row), make_float2(mm, l));
+      }
+    }
+    if (!whole) {
+      const int c0 = (int)(item_at / per), c1 = (int)((item_at + it.stages - 1) / per);
+      __threadfence();
+      named_sync(1, kConsumers);
+      if (tid == 0) {
+        const int old = atomicAdd(a.count + c0, 1);
+        s_last = old == c1 - c0;
+        if (old == c1 - c0) atomicExch(a.count + c0, 0);  // as the next launch expects it
+        __threadfence();
+      }
+      named_sync(1, kConsumers);
+      if (s_last) {
+        const float* parts = a.part;
+        for (int i = tid; i < row_n * (HD / 4); i += kConsumers) {
+          const int row = i / (HD / 4), d = (i % (HD / 4)) * 4;
+          float mm = -kInf, l = 0.f;
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int k = c0; k <= c1; k++) {
+            const float* pk = parts + (size_t)(2 * k + (k == c0)) * C::kRows * (HD + 2);
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pk + C::kRows * HD + 2 * row));
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(pk + row * HD + d));
+            const float now = fmaxf(mm, ml.x);
+            const float fo = mm == -kInf ? 0.f : exp2_fast(mm - now), fn = ml.x == -kInf ? 0.f : exp2_fast(ml.x - now);
+            const float gn = ml.y == ml.y ? fn : 1.f, go = l == l ? fo : 1.f;
+            mm = now;
+            l = l * go + ml.y * gn;
+            y.x = y.x * go + v.x * gn, y.y = y.y * go + v.y * gn, y.z = y.z * go + v.z * gn, y.w = y.w * go + v.w * gn;
+          }
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          store4<F32>(a.out, out_at(row) + d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv), a.vec_out);
+        }
+      }
+    }
+    named_sync(1, kConsumers);  // the join buffer and the query fragments are free
+    if (stage == it.stages) {
+      stage = 0;
+      if (w < w1) next_item();
+    }
   }
-  for (int h = 0, d = tid; d < c.hd; d += kTile, h++) {
-    const float y = l == 0.f ? 0.f : acc[h] / l;
-    const size_t at = (size_t)(row * out_stride + qh * c.hd + d);
-    if (BF16)
-      static_cast<uint16_t*>(out)[at] = f32_to_bf16_rn(y);
-    else
-      static_cast<float*>(out)[at] = y;
+}
+
+template <int HD, int NG, int NT, bool F32>
+int launch_one(coli_ctx* ctx, AttnArgs& a, long long most_stages) {
+  using C = Cfg<HD, NG, NT, F32>;
+  int grid = ctx->num_sms * C::kCtas;
+  if (most_stages < grid) grid = (int)most_stages;
+  if (grid > kKvCounters) grid = kKvCounters;
+  int rc = ensure_workspace(ctx, (size_t)2 * grid * C::kRows * (HD + 2) * sizeof(float));
+  if (rc != COLI_OK) return rc;
+  a.part = reinterpret_cast<float*>(ctx->ws.base);
+  auto kern = kv4_attn_kernel<HD, NG, NT, F32>;
+  static std::atomic<uint64_t> ready{0};  // devices (below 64) on which this instance has its attribute
+  const uint64_t bit = ctx->device < 64 ? 1ull << ctx->device : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "kv4_attention attribute");
+    ready.fetch_or(bit, std::memory_order_relaxed);
   }
+  ProfScope prof(ctx, COLI_KERNEL_ATTENTION);
+  cudaError_t e = launch_k(kern, grid, kAttnThreads, C::kSmem, ctx->stream, true, false, a);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "kv4_attention launch");
+  return COLI_OK;
+}
+
+// Query rows per tile: enough for the rows that a sequence has on average, since a tile's padding costs
+// instructions and each further tile reads the cache again. Widths beyond the registers are cut into tiles.
+template <int HD, int NG, bool F32>
+int launch_rows(coli_ctx* ctx, AttnArgs& a) {
+  const long long rows = (long long)((a.p.T + a.p.B - 1) / a.p.B) * a.group;
+  const long long width = ((long long)a.p.table_stride << a.c.page_log2) / kStageTok + 1;
+  constexpr int kWide = F32 || HD == 256 ? 2 : 4;
+  auto most = [&](int nt) { return ((long long)a.p.T * a.group / (8 * nt) + a.p.B) * a.c.heads * width; };
+  if (rows <= 8) return launch_one<HD, NG, 1, F32>(ctx, a, most(1));
+  if (rows <= 16 || kWide == 2) return launch_one<HD, NG, 2, F32>(ctx, a, most(2));
+  return launch_one<HD, NG, kWide, F32>(ctx, a, most(kWide));
+}
+
+template <bool F32>
+int launch_shape(coli_ctx* ctx, AttnArgs& a) {
+  const int ng = a.c.ng;
+  if (a.c.hd == 64) return ng == 1 ? launch_rows<64, 1, F32>(ctx, a) : launch_rows<64, 2, F32>(ctx, a);
+  if (a.c.hd == 128)
+    return ng == 1   ? launch_rows<128, 1, F32>(ctx, a)
+           : ng == 2 ? launch_rows<128, 2, F32>(ctx, a)
+                     : launch_rows<128, 4, F32>(ctx, a);
+  return ng == 2 ? launch_rows<256, 2, F32>(ctx, a) : launch_rows<256, 4, F32>(ctx, a);
 }
 
 }  // namespace
 
 int launch_kv4_attention(coli_ctx* ctx, const Kv4View& c, const Kv4Plan& p, const void* q, long long q_stride, int dtype,
                          int q_heads, float scale, int window, void* out, long long out_stride) {
-  const long long grid = (long long)p.T * q_heads;
-  if (grid > 0x7fffffffll) return fail(ctx, COLI_E_INVAL, "kv4_attention: too many rows for one call");
-  ProfScope prof(ctx, COLI_KERNEL_ATTENTION);
-  auto kern = dtype == COLI_DTYPE_BF16 ? kv4_attn_kernel<true> : kv4_attn_kernel<false>;
-  cudaError_t e = launch_k(kern, (int)grid, kTile, 0, ctx->stream, true, false, c, p, q, q_stride, q_heads, scale, window,
-                           out, out_stride, ctx->d_status);
-  if (e != cudaSuccess) return cuda_fail(ctx, e, "kv4_attention launch");
-  return COLI_OK;
+  const bool f32 = dtype == COLI_DTYPE_F32;
+  const size_t elem = f32 ? 4 : 2;
+  AttnArgs a{c, p, q, q_stride, q_heads / c.heads, scale, window, out, out_stride};
+  a.vec = ((uintptr_t)q % 16 == 0) && (q_stride * elem) % 16 == 0;
+  a.vec_out = ((uintptr_t)out % (4 * elem) == 0) && out_stride % 4 == 0;
+  a.count = ctx->d_kv_count;
+  a.err = ctx->d_status;
+  a.wait_ns = ctx->wait_ns ? ctx->wait_ns : kWaitLimitNs;
+  return f32 ? launch_shape<true>(ctx, a) : launch_shape<false>(ctx, a);
 }
 
 }  // namespace coli
