@@ -98,21 +98,6 @@ __device__ __forceinline__ int kv4_len(const Kv4Plan& p, int page_log2, int b, i
   return len;
 }
 
-// The sequence that owns a row, or -1: the largest b with q_start[b] <= row, if its range holds the row.
-__device__ __forceinline__ int kv4_seq_of(const Kv4Plan& p, int row) {
-  if (!p.q_start) return row;
-  int lo = 0, hi = p.B;  // q_start[lo] <= row < q_start[hi], if q_start is what it should be
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldcg(p.q_start + mid) <= row) {
-      lo = mid;
-    } else {
-      hi = mid;
-    }
-  }
-  return lo;
-}
-
 #endif
 
 }  // namespace coli
