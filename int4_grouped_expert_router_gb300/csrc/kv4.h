@@ -64,6 +64,10 @@ int launch_kv4_read(coli_ctx* ctx, const Kv4View& c, const Kv4Plan& p, void* k, 
 int launch_kv4_attention(coli_ctx* ctx, const Kv4View& c, const Kv4Plan& p, const void* q, long long q_stride, int dtype,
                          int q_heads, float scale, int window, void* out, long long out_stride);
 
+// The tensor-core form for many query rows per sequence (kv4_tile.cu): bf16, hd 64 or 128.
+int launch_kv4_tiles(coli_ctx* ctx, const Kv4View& c, const Kv4Plan& p, const void* q, long long q_stride, int q_heads,
+                     float scale, int window, void* out, long long out_stride);
+
 #ifdef __CUDACC__
 
 __device__ __forceinline__ const uint8_t* kv4_unit(const Kv4View& c, int page, int head, int off) {

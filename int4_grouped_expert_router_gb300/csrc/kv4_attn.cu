@@ -42,6 +42,8 @@ constexpr int kAttnThreads = kConsumers + 32;
 // below 2^kSlack.
 constexpr float kSlack = 1.f;
 constexpr float kInf = __builtin_huge_valf();
+// Query rows per sequence and key/value head, on average, from which the 256-row tiles of kv4_tile.cu take over.
+constexpr int kTileFrom = 96;
 
 template <int HD, int NG, int NT, bool F32>
 struct Cfg {
@@ -872,6 +874,8 @@ int launch_shape(coli_ctx* ctx, AttnArgs& a) {
 int launch_kv4_attention(coli_ctx* ctx, const Kv4View& c, const Kv4Plan& p, const void* q, long long q_stride, int dtype,
                          int q_heads, float scale, int window, void* out, long long out_stride) {
   const bool f32 = dtype == COLI_DTYPE_F32;
+  if (!f32 && c.hd <= 128 && (long long)p.T * (q_heads / c.heads) >= (long long)kTileFrom * p.B)
+    return launch_kv4_tiles(ctx, c, p, q, q_stride, q_heads, scale, window, out, out_stride);
   const size_t elem = f32 ? 4 : 2;
   AttnArgs a{c, p, q, q_stride, q_heads / c.heads, scale, window, out, out_stride};
   a.vec = ((uintptr_t)q % 16 == 0) && (q_stride * elem) % 16 == 0;

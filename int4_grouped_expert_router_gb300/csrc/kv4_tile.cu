@@ -1,0 +1,858 @@
+// Attention over the 4-bit key/value cache (layout: kv4.h) for many query rows of a sequence: prompts and
+// chunks of them, bf16, on the fifth-generation tensor cores.
+//
+// The same formula as kv4_attn.cu, arranged for a bound of arithmetic instead of bytes. An item is a
+// (sequence, tile of 256 query rows, key/value head): a row is a (token, query head) pair, so the heads of a
+// group share the keys and values of their tile. Its visible tokens are cut into stages of 128; all items'
+// stages, end to end, are dealt out evenly and contiguously to one CTA per SM, and an item that spans CTAs is
+// joined by the CTA that arrives last, in CTA order.
+//
+// One CTA, 14 warps:
+//   producer      bulk copies of the stage's packed units into a ring of two
+//   4 converters  codes to 16-bit values o + s (n - 8) in the 128-byte-swizzled operand layout: K with a token
+//                 per row, V^T with a channel per row (the packed value words hold two neighbouring tokens, which
+//                 is the order that operand wants). Rounded once, to 11 bits, after a power of two has brought the
+//                 stage's largest key (value) below 2^14, so that no size of the keys and values is lost.
+//   MMA           one thread: S_x = Q_x K^T, O_x += P_x V for the two halves x of 128 rows
+//   2 x 4 softmax a thread per row: running maximum (it moves only when passed by kSlack), weights
+//                 p = 2^(y - m + 13) in 16 bits, written over S in tensor memory as the next product's operand
+// While one half's softmax runs, the tensor core works on the other half. Tensor memory is full: S (128
+// columns) and O (hd columns) of both halves.
+//
+// K's channels lie in the order 0 4 1 5 2 6 3 7 within every eight, as the codes unpack, and Q's with them; V^T's
+// rows, the output's columns, in the order 0 2 .. 14 1 3 .. 15 within every sixteen, which the store undoes.
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "kv4.h"
+#include "pipe.h"
+#include "tc.h"
+
+namespace coli {
+
+namespace {
+
+constexpr int kTileTok = 128;                      // tokens of a stage
+constexpr int kTileUnits = kTileTok / kKvUnit;     // 8
+constexpr int kHalf = 128;                         // rows of a half (the instruction's M)
+constexpr int kTileRows = 2 * kHalf;
+constexpr int kConvWarps = 4;
+constexpr int kSoftThreads = 2 * kHalf;
+constexpr int kWarpConv = 8, kWarpMma = 12, kWarpLoad = 13;
+constexpr int kTileThreads = 14 * 32;
+constexpr int kSeqChunk = 512;                     // sequences whose stage counts are kept at a time
+constexpr float kSlack = 1.f;                      // log2; weights stay below 2^(13 + kSlack)
+constexpr float kLift = 13.f;
+constexpr float kInf = __builtin_huge_valf();
+
+template <int HD, int NG>
+struct Tile {
+  static constexpr uint32_t kUnit = kv4_unit_bytes(HD, NG);
+  static constexpr uint32_t kRaw = kTileUnits * kUnit;
+  static constexpr uint32_t kQ = kHalf * HD * 2;     // one half's queries
+  static constexpr uint32_t kK = kTileTok * HD * 2;  // keys, and values, of a stage
+  static constexpr uint32_t kSmem = 1024 + 2 * kQ + kK + 2 * kK + 2 * kRaw;
+  static constexpr int kWords = HD / 32, kWpg = kWords / NG;
+};
+
+struct TileArgs {
+  Kv4View c;
+  Kv4Plan p;
+  const void* q;
+  long long q_stride;
+  int group;
+  float scale;
+  int window;
+  void* out;
+  long long out_stride;
+  bool vec, vec_out;
+  float* part;  // 2 per CTA: kTileRows x HD outputs, then kTileRows (maximum, sum) pairs
+  int* count;
+  int* err;
+  uint64_t wait_ns;
+};
+
+struct Item {
+  int b, tile, head;
+  int r0, m, len;
+  int first, stages;  // first stage of kTileTok tokens, number of stages (at least 1)
+};
+
+__device__ __forceinline__ int tiles_of(int m, int group) { return (int)(((long long)m * group + kTileRows - 1) / kTileRows); }
+
+// Stages of tile k of a sequence: from the window of its first row to the position of its last.
+__device__ __forceinline__ void tile_span(const TileArgs& a, int m, int len, int k, int& first, int& stages) {
+  const long long row0 = (long long)k * kTileRows;
+  const long long all = (long long)m * a.group;
+  const long long last_row = row0 + kTileRows - 1 < all - 1 ? row0 + kTileRows - 1 : all - 1;
+  const int last = len - m + (int)(last_row / a.group);
+  const int lo = a.window > 0 ? max(0, len - m + (int)(row0 / a.group) - a.window + 1) : 0;
+  first = last < 0 ? 0 : lo / kTileTok;
+  stages = last < 0 ? 1 : last / kTileTok - first + 1;
+}
+
+__device__ __forceinline__ void load_seq(const TileArgs& a, Item& it) {
+  int r1;
+  kv4_rows(a.p, it.b, it.r0, r1, a.err);
+  it.m = r1 - it.r0;
+  it.len = kv4_len(a.p, a.c.page_log2, it.b, a.err);
+}
+
+// Stages of a whole sequence per head, by a warp.
+__device__ __forceinline__ long long seq_stages(const TileArgs& a, int b) {
+  Item it;
+  it.b = b;
+  load_seq(a, it);
+  long long sum = 0;
+  for (int k = threadIdx.x & 31, n = tiles_of(it.m, a.group); k < n; k += 32) {
+    int first, stages;
+    tile_span(a, it.m, it.len, k, first, stages);
+    sum += stages;
+  }
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T for one K step of 16, 16-bit A held two elements per column.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.u32 p, %4, 0; "
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// f16 A and B (K-major), f32 accumulator.
+__host__ __device__ constexpr uint32_t f16_f32_idesc(uint32_t M, uint32_t N) {
+  return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+#define COLI_R4(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3])
+#define COLI_S4(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3])
+
+// 32 consecutive 32-bit columns of this thread's lane; the load completes at tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+      : COLI_R4(r, 0), COLI_R4(r, 4), COLI_R4(r, 8), COLI_R4(r, 12), COLI_R4(r, 16), COLI_R4(r, 20), COLI_R4(r, 24),
+        COLI_R4(r, 28)
+      : "r"(at)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::COLI_S4(r, 0),
+      COLI_S4(r, 4), COLI_S4(r, 8), COLI_S4(r, 12), COLI_S4(r, 16), COLI_S4(r, 20), COLI_S4(r, 24), COLI_S4(r, 28), "r"(at)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::COLI_S4(r, 0),
+      COLI_S4(r, 4), COLI_S4(r, 8), COLI_S4(r, 12), "r"(at)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+
+// The four code pairs of a word, (w >> 4 m) & 0x000f000f, as o + s (n - 8).
+__device__ __forceinline__ void dequantise(uint32_t w, __half2 s, __half2 o, uint32_t (&v)[4]) {
+  const __half2 bias = __floats2half2_rn(1032.f, 1032.f);
+  const __half2 sixteenth = __floats2half2_rn(0.0625f, 0.0625f), bias16 = __floats2half2_rn(-72.f, -72.f);
+  const uint32_t w8 = w >> 8;
+  v[0] = bits(__hfma2(__hsub2(as_half2((w & 0x000f000fu) | 0x64006400u), bias), s, o));
+  v[1] = bits(__hfma2(__hfma2(as_half2((w & 0x00f000f0u) | 0x64006400u), sixteenth, bias16), s, o));
+  v[2] = bits(__hfma2(__hsub2(as_half2((w8 & 0x000f000fu) | 0x64006400u), bias), s, o));
+  v[3] = bits(__hfma2(__hfma2(as_half2((w8 & 0x00f000f0u) | 0x64006400u), sixteenth, bias16), s, o));
+}
+
+template <int N>
+__device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 v = lds128(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = lds64(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    static_assert(N == 1, "1, 2 or 4 words");
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(smem_u32(p)) : "memory");
+  }
+}
+
+__device__ __forceinline__ void sts128(uint32_t at, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
+// 2^(13 - floor(log2 x)), within what binary32 has: x times it lies in [2^13, 2^14).
+__device__ __forceinline__ float below_2_14(float x) {
+  const int ex = min(253, max(1, 127 + 13 + 127 - (int)(__float_as_uint(x) >> 23)));
+  return __uint_as_float((uint32_t)ex << 23);
+}
+
+template <int HD, int NG>
+__global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
+  using T = Tile<HD, NG>;
+  extern __shared__ uint8_t smem_raw[];
+  // operand tiles on 1024-byte boundaries
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* s_q = smem;                    // [2 halves][HD / 64][128 rows][128 bytes]
+  uint8_t* s_k = s_q + 2 * T::kQ;         // [HD / 64][128 tokens][128 bytes]
+  uint8_t* s_v = s_k + T::kK;             // [2 stages][2][HD channels][128 bytes = 64 tokens]
+  uint8_t* s_raw = s_v + 2 * T::kK;       // [2][kTileUnits] packed units
+  __shared__ __align__(8) uint64_t raw_full[2], raw_empty[2], k_full, k_empty, v_full[2], v_empty[2], par_full[2],
+      q_full[2], s_full[2], p_full[2], o_full[2];
+  __shared__ float s_par[2][3];           // per stage: 1 / key factor, change of the value factor, 1 / value factor
+  __shared__ uint32_t s_tmem;
+  __shared__ long long s_w[kSeqChunk];
+  __shared__ long long s_at;
+  __shared__ int s_start, s_start_tile, s_last;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < 2; i++) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], kConvWarps);
+      mbar_init(&v_full[i], kConvWarps);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&par_full[i], 1);
+      mbar_init(&q_full[i], 4);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_init(&k_full, kConvWarps);
+    mbar_init(&k_empty, 1);
+    mbar_fence_init();
+  }
+  griddep_launch_dependents();
+  griddep_wait();
+
+  // ---- deal the stages out ----
+  const int heads = a.c.heads;
+  long long total = 0;
+  for (int base = 0; base < a.p.B; base += kSeqChunk) {
+    const int n = min(kSeqChunk, a.p.B - base);
+    for (int i = warp; i < n; i += kTileThreads / 32) {
+      const long long s = seq_stages(a, base + i) * heads;
+      if (lane == 0) s_w[i] = s;
+    }
+    __syncthreads();
+    long long sum = 0;
+    for (int i = lane; i < n; i += 32) sum += s_w[i];
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    total += sum;
+    if (base + kSeqChunk < a.p.B) __syncthreads();
+  }
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long w0 = per * blockIdx.x, w1 = w0 + per < total ? w0 + per : total;
+  if (w0 >= w1) return;  // uniform in the CTA: nothing allocated, nothing in flight
+  {
+    long long before = 0;
+    bool found = false;
+    for (int base = 0; base < a.p.B && !found; base += kSeqChunk) {
+      const int n = min(kSeqChunk, a.p.B - base);
+      if (a.p.B > kSeqChunk) {  // otherwise s_w still holds them
+        __syncthreads();
+        for (int i = warp; i < n; i += kTileThreads / 32) {
+          const long long s = seq_stages(a, base + i) * heads;
+          if (lane == 0) s_w[i] = s;
+        }
+        __syncthreads();
+      }
+      for (int i0 = 0; i0 < n && !found; i0 += 32) {
+        const long long mine = i0 + lane < n ? s_w[i0 + lane] : 0;
+        long long inc = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
+        }
+        const bool here = mine > 0 && before + inc - mine <= w0 && w0 < before + inc;
+        const unsigned who = __ballot_sync(0xffffffffu, here);
+        if (who) {
+          found = true;
+          if (here && warp == 0) {
+            s_start = base + i0 + lane;
+            s_at = before + inc - mine;
+          }
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+      }
+    }
+  }
+  __syncthreads();
+  Item it;
+  it.b = s_start;
+  load_seq(a, it);
+  if (warp == 0) {  // the tile of the sequence in which the share starts
+    long long at = s_at;
+    const int n = tiles_of(it.m, a.group);
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      int first, stages = 0;
+      if (k0 + lane < n) tile_span(a, it.m, it.len, k0 + lane, first, stages);
+      const long long mine = (long long)stages * heads;
+      long long inc = mine;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      const bool here = mine > 0 && at + inc - mine <= w0 && w0 < at + inc;
+      if (here) {
+        s_start_tile = k0 + lane;
+        s_at = at + inc - mine;
+      }
+      if (__any_sync(0xffffffffu, here)) break;
+      at += __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  if (warp == kWarpMma) tmem_alloc(&s_tmem, 512);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = s_tmem;
+
+  it.tile = s_start_tile;
+  tile_span(a, it.m, it.len, it.tile, it.first, it.stages);
+  const long long local = w0 - s_at;
+  it.head = (int)(local / it.stages);
+  int stage = (int)(local % it.stages);
+  long long w = w0;
+  auto next_item = [&]() {  // w < w1 guarantees that there is one
+    if (++it.head < heads) return;
+    it.head = 0;
+    if (++it.tile >= tiles_of(it.m, a.group)) {
+      it.tile = 0;
+      do {
+        it.b++;
+        load_seq(a, it);
+      } while (it.m == 0 && it.b + 1 < a.p.B);
+    }
+    tile_span(a, it.m, it.len, it.tile, it.first, it.stages);
+  };
+  auto rows_here = [&]() { return (int)min((long long)kTileRows, (long long)it.m * a.group - (long long)it.tile * kTileRows); };
+  bool alive = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (alive && !mbar_wait_suspend(bar, parity, a.wait_ns)) {
+      set_error(a.err, COLI_E_TIMEOUT);
+      alive = false;  // void from here on, but nothing hangs
+    }
+  };
+
+  if (warp == kWarpLoad) {
+    // ------------------------------------ producer ------------------------------------
+    const int page_tok = 1 << a.c.page_log2;
+    int cached_b = -1, cached_from = 0, pages = 0;
+    for (uint32_t n = 0; w < w1; n++) {
+      const int tok = (it.first + stage) * kTileTok;
+      const int units = min(kTileUnits, max(0, (it.len - tok + kKvUnit - 1) / kKvUnit));
+      const int page = tok >> a.c.page_log2;
+      const int per_copy = min(kTileUnits, page_tok / kKvUnit);  // units
+      const int copies = (units + per_copy - 1) / per_copy;      // at most 8
+      if (copies > 0 && (it.b != cached_b || page < cached_from || page + copies > cached_from + 32)) {
+        cached_b = it.b;
+        cached_from = page;
+        pages = page + lane < a.p.table_stride ? __ldcg(a.p.table + (size_t)it.b * a.p.table_stride + page + lane) : 0;
+      }
+      wait(&raw_empty[n & 1], ((n >> 1) & 1) ^ 1);
+      if (!alive) break;  // what was issued is still awaited by the converters
+      if (lane == 0) mbar_arrive_expect_tx(&raw_full[n & 1], units * T::kUnit);
+      __syncwarp();
+      int pg = __shfl_sync(0xffffffffu, pages, (page - cached_from + lane) & 31);
+      if (lane < copies) {
+        if (pg < 0 || pg >= a.c.pages) {
+          set_error(a.err, COLI_E_RANGE);
+          pg = 0;  // some page of the cache in its place
+        }
+        const int take = min(per_copy, units - lane * per_copy);
+        const uint8_t* src = a.c.base + (((size_t)pg * heads + it.head) * (size_t)(page_tok / kKvUnit) +
+                                         (tok & (page_tok - 1)) / kKvUnit) * T::kUnit;
+        bulk_g2s(s_raw + (n & 1) * T::kRaw + lane * per_copy * T::kUnit, src, take * T::kUnit, &raw_full[n & 1]);
+      }
+      w++;
+      if (++stage == it.stages) {
+        stage = 0;
+        if (w < w1) next_item();
+      }
+    }
+  } else if (warp == kWarpMma) {
+    // -------------------------------------- MMA --------------------------------------
+    if (lane == 0) {
+      constexpr uint32_t kIdS = f16_f32_idesc(kHalf, kTileTok), kIdO = f16_f32_idesc(kHalf, HD);
+      uint32_t n = 0, ns[2] = {0, 0}, nseg[2] = {0, 0};  // stages, stages and segments of each half
+      auto scores = [&](int x) {
+#pragma unroll
+        for (int k = 0; k < HD / 16; k++) {
+          const uint64_t da = sw128_kmajor_desc(s_q + x * T::kQ + (k / 4) * (kHalf * 128)) + (k % 4) * 2;
+          const uint64_t db = sw128_kmajor_desc(s_k + (k / 4) * (kTileTok * 128)) + (k % 4) * 2;
+          tc_mma_bf16(tmem + x * kTileTok, da, db, kIdS, k != 0);
+        }
+        tc_commit(&s_full[x]);
+      };
+      auto output = [&](int x, uint32_t stage_n, bool fresh) {
+        const uint8_t* v = s_v + (stage_n & 1) * T::kK;
+#pragma unroll
+        for (int k = 0; k < kTileTok / 16; k++) {
+          const uint64_t db = sw128_kmajor_desc(v + (k / 4) * (HD * 128)) + (k % 4) * 2;
+          mma_ts(tmem + 2 * kTileTok + x * HD, tmem + x * kTileTok + k * 8, db, kIdO, !(fresh && k == 0));
+        }
+      };
+      while (w < w1) {
+        const int n_here = (int)min((long long)(it.stages - stage), w1 - w);
+        const int halves = rows_here() > kHalf ? 2 : 1;
+        for (int x = 0; x < halves; x++) {
+          wait(&q_full[x], nseg[x] & 1);
+          nseg[x]++;
+        }
+        wait(&k_full, n & 1);
+        tc_fence_after_sync();
+        for (int x = 0; x < halves; x++) scores(x);
+        tc_commit(&k_empty);
+        for (int j = 0; j < n_here; j++, n++) {
+          wait(&v_full[n & 1], (n >> 1) & 1);
+          for (int x = 0; x < halves; x++) {
+            wait(&p_full[x], ns[x] & 1);
+            ns[x]++;
+            tc_fence_after_sync();
+            output(x, n, j == 0);
+            if (j + 1 == n_here) tc_commit(&o_full[x]);
+            if (x + 1 == halves) tc_commit(&v_empty[n & 1]);
+            if (j + 1 < n_here) {  // the next stage's scores go over the weights that the product above reads first
+              if (x == 0) {
+                wait(&k_full, (n + 1) & 1);
+                tc_fence_after_sync();
+              }
+              scores(x);
+              if (x + 1 == halves) tc_commit(&k_empty);
+            }
+          }
+        }
+        w += n_here;
+        stage += n_here;
+        if (stage == it.stages) {
+          stage = 0;
+          if (w < w1) next_item();
+        }
+      }
+      // the last arrivals on these barriers come before the CTA's memory goes
+      wait(&k_empty, (n - 1) & 1);
+      wait(&v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp >= kWarpConv) {
+    // ----------------------------------- converters -----------------------------------
+    const int cw = warp - kWarpConv, r = lane >> 2, cc = lane & 3;
+    const uint32_t k_base = smem_u32(s_k), v_base0 = smem_u32(s_v);
+    float vmul = 0.f;  // values are multiplied by it; it only shrinks within a segment
+    for (uint32_t n = 0; w < w1; n++) {
+      if (n == 0 || stage == 0) vmul = 0.f;
+      const int tok = (it.first + stage) * kTileTok;
+      const uint8_t* raw = s_raw + (n & 1) * T::kRaw;
+      wait(&raw_full[n & 1], (n >> 1) & 1);
+      float kmax = 0.f, vmax = 0.f;
+#pragma unroll
+      for (int i = 0; i < kTileTok / 32; i++) {
+        const int t = i * 32 + lane;
+        if (tok + t < it.len) {
+          uint32_t kp[NG], vp[NG];
+          lds_words(raw + (t / 16) * T::kUnit + kv4_kscale_at(HD) + (t % 16) * NG * 4, kp);
+          lds_words(raw + (t / 16) * T::kUnit + kv4_vscale_at(HD, NG) + (t % 16) * NG * 4, vp);
+#pragma unroll
+          for (int g = 0; g < NG; g++) {
+            kmax = fmaxf(kmax, fmaf(8.f, lo_bf16(kp[g]), fabsf(hi_bf16(kp[g]))));
+            vmax = fmaxf(vmax, fmaf(8.f, lo_bf16(vp[g]), fabsf(hi_bf16(vp[g]))));
+          }
+        }
+      }
+      kmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(kmax)));
+      vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
+      const float kmul = kmax > 0.f ? below_2_14(kmax) : 1.f;
+      float shrink = 1.f;
+      if (vmax > 0.f && (vmul == 0.f || vmax * vmul >= 16384.f)) {
+        const float now = below_2_14(vmax);
+        shrink = vmul == 0.f ? 1.f : now / vmul;
+        vmul = now;
+      }
+      // ---- keys: this warp's two units; a lane holds tokens r, r + 8 and a quarter of each 32 channels ----
+      wait(&k_empty, (n & 1) ^ 1);
+      // the previous stage's scores are done, so the weights of the one before it are: its s_par may go
+      if (cw == 0 && lane == 0) {
+        s_par[n & 1][0] = 1.f / kmul;
+        s_par[n & 1][1] = shrink;
+        s_par[n & 1][2] = vmul == 0.f ? 0.f : 1.f / vmul;
+        mbar_arrive(&par_full[n & 1]);
+      }
+#pragma unroll
+      for (int u = 0; u < kTileUnits / kConvWarps; u++) {
+        const int un = cw * (kTileUnits / kConvWarps) + u;
+        const uint8_t* unit = raw + un * T::kUnit;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const int t = un * 16 + r + 8 * h;
+          uint32_t kw[T::kWords], kp[NG], vp[NG];
+          lds_words(unit + h * 32 * T::kWords * 4 + lane * T::kWords * 4, kw);
+          lds_words(unit + kv4_kscale_at(HD) + (r + 8 * h) * NG * 4, kp);
+          lds_words(unit + kv4_vscale_at(HD, NG) + (r + 8 * h) * NG * 4, vp);
+          bool broken = false;  // a value that is not finite is shown by its key: weights of rows that do not see it are 0
+#pragma unroll
+          for (int g = 0; g < NG; g++) broken = broken || hi_bf16(vp[g]) != hi_bf16(vp[g]);
+          __half2 s[NG], o[NG];
+#pragma unroll
+          for (int g = 0; g < NG; g++) {
+            const float live = tok + t < it.len ? kmul : 0.f;
+            s[g] = __float2half2_rn(live == 0.f ? 0.f : lo_bf16(kp[g]) * live);
+            o[g] = __float2half2_rn(live == 0.f ? 0.f : broken ? __uint_as_float(0x7fc00000u) : hi_bf16(kp[g]) * live);
+          }
+          // odd tokens store the words of a pair in the other order: eight lanes then cover all banks
+          const uint32_t row = k_base + t * 128;
+#pragma unroll
+          for (int i = 0; i < T::kWords; i += 2) {
+            const int odd = r & 1;
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              const int which = e ^ odd;
+              const uint32_t word = which ? kw[i + 1] : kw[i];
+              const __half2 sg = which ? s[(i + 1) / T::kWpg] : s[i / T::kWpg], og = which ? o[(i + 1) / T::kWpg] : o[i / T::kWpg];
+              dequantise(word, sg, og, v);
+              sts128(row + (i / 2) * (kTileTok * 128) + (((which * 4 + cc) ^ r) << 4), v);
+            }
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_full);
+      // ---- values: a lane holds tokens 2 c, 2 c + 1 (and + 8) of row r's channels ----
+      wait(&v_empty[n & 1], ((n >> 1) & 1) ^ 1);
+      const uint32_t v_base = v_base0 + (n & 1) * T::kK;
+#pragma unroll
+      for (int u = 0; u < kTileUnits / kConvWarps; u++) {
+        const int un = cw * (kTileUnits / kConvWarps) + u;
+        const uint8_t* unit = raw + un * T::kUnit;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const int t = 2 * cc + 8 * h;  // in the unit
+          uint32_t vw[T::kWords], p0[NG], p1[NG];
+          lds_words(unit + kv4_v_at(HD, NG) + h * 4 * HD + lane * T::kWords * 4, vw);
+          lds_words(unit + kv4_vscale_at(HD, NG) + t * NG * 4, p0);
+          lds_words(unit + kv4_vscale_at(HD, NG) + (t + 1) * NG * 4, p1);
+          const float live0 = tok + un * 16 + t < it.len ? vmul : 0.f, live1 = tok + un * 16 + t + 1 < it.len ? vmul : 0.f;
+          __half2 s[NG], o[NG];
+#pragma unroll
+          for (int g = 0; g < NG; g++) {
+            const float o0 = hi_bf16(p0[g]), o1 = hi_bf16(p1[g]);
+            s[g] = __floats2half2_rn(live0 == 0.f ? 0.f : lo_bf16(p0[g]) * live0, live1 == 0.f ? 0.f : lo_bf16(p1[g]) * live1);
+            o[g] = __floats2half2_rn(live0 == 0.f || o0 != o0 ? 0.f : o0 * live0, live1 == 0.f || o1 != o1 ? 0.f : o1 * live1);
+          }
+          const int chunk = (un % 4) * 2 + h;  // of eight tokens within the 64 of a tile
+          const uint32_t at = v_base + (un / 4) * (HD * 128) + r * 128 + ((chunk ^ r) << 4) + cc * 4;
+#pragma unroll
+          for (int i = 0; i < T::kWords; i++) {
+            uint32_t v[4];
+            dequantise(vw[i], s[i / T::kWpg], o[i / T::kWpg], v);
+#pragma unroll
+            for (int j = 0; j < 4; j++) sts32(at + ((2 * i + (j >> 1)) * 16 + (j & 1) * 8) * 128, v[j]);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&v_full[n & 1]);
+        mbar_arrive(&raw_empty[n & 1]);
+      }
+      w++;
+      if (++stage == it.stages) {
+        stage = 0;
+        if (w < w1) next_item();
+      }
+    }
+  } else {
+    // ------------------------------------- softmax -------------------------------------
+    const int x = warp >> 2;                 // half
+    const int row = tid & (kTileRows - 1);   // of the tile
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + x * kTileTok, t_o = tmem + lanes + 2 * kTileTok + x * HD;
+    uint32_t n = 0, ns = 0, nseg = 0;
+    while (w < w1) {
+      const long long item_at = w - stage;
+      const int n_here = (int)min((long long)(it.stages - stage), w1 - w);
+      const int row_n = rows_here();
+      const bool active = x == 0 || row_n > kHalf;
+      const long long q_row = (long long)it.tile * kTileRows + min(row, row_n - 1);  // rows past the end repeat the last
+      const int pos = it.len - it.m + (int)(q_row / a.group);
+      float mf = -kInf, l = 0.f, unscale = 0.f;
+      if (active) {
+        // ---- this row's queries: a power of two brings the largest to [2^14, 2^15) ----
+        const size_t at = (size_t)((it.r0 + q_row / a.group) * a.q_stride) + (size_t)(it.head * a.group + q_row % a.group) * HD;
+        const unsigned short* src = static_cast<const unsigned short*>(a.q) + at;
+        uint32_t qw[HD / 2];
+        uint32_t amax = 0;
+        if (a.vec) {
+#pragma unroll
+          for (int i = 0; i < HD / 8; i++) {
+            const uint4 v = __ldcg(reinterpret_cast<const uint4*>(src) + i);
+            qw[4 * i] = v.x, qw[4 * i + 1] = v.y, qw[4 * i + 2] = v.z, qw[4 * i + 3] = v.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < HD / 2; i++) qw[i] = __ldcg(src + 2 * i) | ((uint32_t)__ldcg(src + 2 * i + 1) << 16);
+        }
+#pragma unroll
+        for (int i = 0; i < HD / 2; i++) amax = max(amax, max(qw[i] & 0x7fffu, qw[i] >> 16 & 0x7fffu));
+        const float big = __uint_as_float(amax << 16);
+        if (amax >= 0x7f80u && row < row_n) set_error(a.err, COLI_E_NONFINITE);
+        const int ex = min(253, max(1, 127 + 14 + 127 - (int)(amax >> 7)));
+        float mult = amax == 0 ? 1.f : __uint_as_float((uint32_t)ex << 23);
+        const float inv = amax == 0 ? 1.f : __uint_as_float((uint32_t)(254 - ex) << 23);
+        if (a.scale < 0.f) mult = -mult;
+        if (!(big < kInf)) mult = __uint_as_float(0x7fc00000u);
+        const uint32_t dst = smem_u32(s_q) + x * T::kQ + (row & (kHalf - 1)) * 128;
+#pragma unroll
+        for (int ch = 0; ch < HD / 8; ch++) {
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 4; j++) f[2 * j] = lo_bf16(qw[4 * ch + j]) * mult, f[2 * j + 1] = hi_bf16(qw[4 * ch + j]) * mult;
+          uint32_t v[4];
+#pragma unroll
+          for (int j = 0; j < 4; j++) v[j] = bits(__floats2half2_rn(f[j], f[j + 4]));
+          sts128(dst + (ch / 8) * (kHalf * 128) + (((ch % 8) ^ (row & 7)) << 4), v);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[x]);
+        const float fac0 = fabsf(a.scale) * 1.4426950408889634f * inv;
+
+        for (int j = 0; j < n_here; j++, n++, ns++) {
+          const int t0 = (it.first + stage + j) * kTileTok;
+          wait(&par_full[n & 1], (n >> 1) & 1);
+          const float fac = fac0 * s_par[n & 1][0], shrink = s_par[n & 1][1];
+          unscale = s_par[n & 1][2];
+          wait(&s_full[x], ns & 1);
+          tc_fence_after_sync();
+          // columns [c0, c1) are visible to this row
+          const int c1 = min(kTileTok, max(0, pos - t0 + 1));
+          const int c0 = a.window > 0 ? min(kTileTok, max(0, pos - a.window + 1 - t0)) : 0;
+          const bool masked = __any_sync(0xffffffffu, c1 < kTileTok || c0 > 0);
+          uint32_t sv[32];
+          float mx = -kInf;
+#pragma unroll
+          for (int k = 0; k < kTileTok / 32; k++) {
+            tmem_ld32(t_s + k * 32, sv);
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < 32; i++)
+                if (k * 32 + i >= c0 && k * 32 + i < c1) mx = fmaxf(mx, __uint_as_float(sv[i]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i++) mx = fmaxf(mx, __uint_as_float(sv[i]));
+            }
+          }
+          const float top = mx == -kInf ? -kInf : fac * mx;
+          const bool grow = top > mf + kSlack;
+          const bool first = j == 0;
+          if (__any_sync(0xffffffffu, grow) || shrink != 1.f) {
+            const float now = grow ? top : mf;
+            const float f = mf == -kInf ? 1.f : exp2_fast(mf - now);
+            mf = now;
+            l *= f;
+            if (!first) {
+#pragma unroll 1
+              for (int k = 0; k < HD / 32; k++) {
+                tmem_ld32(t_o + k * 32, sv);
+#pragma unroll
+                for (int i = 0; i < 32; i++) sv[i] = __float_as_uint(__uint_as_float(sv[i]) * f * shrink);
+                tmem_st32(t_o + k * 32, sv);
+              }
+            }
+          }
+          const float add = mf == -kInf ? 0.f : kLift - mf;
+#pragma unroll
+          for (int k = 0; k < kTileTok / 32; k++) {
+            uint32_t pw[16];
+            tmem_ld32(t_s + k * 32, sv);
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+              float e0 = exp2_fast(fmaf(fac, __uint_as_float(sv[2 * i]), add));
+              float e1 = exp2_fast(fmaf(fac, __uint_as_float(sv[2 * i + 1]), add));
+              if (masked) {
+                const int c = k * 32 + 2 * i;
+                e0 = c >= c0 && c < c1 ? e0 : 0.f;
+                e1 = c + 1 >= c0 && c + 1 < c1 ? e1 : 0.f;
+              }
+              l += e0 + e1;
+              pw[i] = bits(__floats2half2_rn(e0, e1));
+            }
+            tmem_st16(t_s + k * 16, pw);
+          }
+          tmem_wait_st();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[x]);
+        }
+      } else {
+        n += n_here;
+      }
+      w += n_here;
+      stage += n_here;
+
+      // ---- the segment's result ----
+      const bool whole = n_here == it.stages;
+      const bool starts_here = item_at >= w0;
+      float* part = a.part + (size_t)(2 * blockIdx.x + starts_here) * kTileRows * (HD + 2);
+      if (active) {
+        wait(&o_full[x], nseg & 1);
+        nseg++;
+        tc_fence_after_sync();
+        const float inv = whole ? (l == 0.f ? 0.f : unscale / l) : unscale;
+        const size_t out_row = (size_t)((it.r0 + q_row / a.group) * a.out_stride) + (size_t)(it.head * a.group + q_row % a.group) * HD;
+#pragma unroll 1
+        for (int k = 0; k < HD / 32; k++) {
+          uint32_t sv[32];
+          tmem_ld32(t_o + k * 32, sv);
+          if (row < row_n) {
+            float y[32];
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+              for (int i = 0; i < 16; i++) y[16 * h + 2 * (i % 8) + i / 8] = __uint_as_float(sv[16 * h + i]) * inv;
+            if (l != l) {
+#pragma unroll
+              for (int i = 0; i < 32; i++) y[i] = l;
+            }
+            if (whole) {
+              uint16_t* o = static_cast<uint16_t*>(a.out) + out_row + k * 32;
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                uint32_t v[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                  v[e] = f32_to_bf16_rn(y[i + 2 * e]) | ((uint32_t)f32_to_bf16_rn(y[i + 2 * e + 1]) << 16);
+                if (a.vec_out) {
+                  *reinterpret_cast<uint4*>(o + i) = make_uint4(v[0], v[1], v[2], v[3]);
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 8; e++) o[i + e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+                }
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                __stcg(reinterpret_cast<float4*>(part + (size_t)row * HD + k * 32 + i),
+                       make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]));
+            }
+          }
+        }
+        tc_fence_before_sync();
+        if (!whole && row < row_n)
+          __stcg(reinterpret_cast<float2*>(part + (size_t)kTileRows * HD + 2 * row), make_float2(mf - kLift, l));
+      }
+      if (!whole) {
+        const int b0 = (int)(item_at / per), b1 = (int)((item_at + it.stages - 1) / per);
+        __threadfence();
+        named_sync(1, kSoftThreads);
+        if (tid == 0) {
+          const int old = atomicAdd(a.count + b0, 1);
+          s_last = old == b1 - b0;
+          if (old == b1 - b0) atomicExch(a.count + b0, 0);
+          __threadfence();
+        }
+        named_sync(1, kSoftThreads);
+        if (s_last) {
+          for (int i = tid; i < row_n * (HD / 4); i += kSoftThreads) {
+            const int rr = i / (HD / 4), d = (i % (HD / 4)) * 4;
+            float mm = -kInf, ll = 0.f;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int k = b0; k <= b1; k++) {
+              const float* pk = a.part + (size_t)(2 * k + (k == b0)) * kTileRows * (HD + 2);
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(pk + (size_t)kTileRows * HD + 2 * rr));
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(pk + (size_t)rr * HD + d));
+              const float now = fmaxf(mm, ml.x);
+              const float fo = mm == -kInf ? 0.f : exp2_fast(mm - now), fn = ml.x == -kInf ? 0.f : exp2_fast(ml.x - now);
+              const float gn = ml.y == ml.y ? fn : 1.f, go = ll == ll ? fo : 1.f;
+              mm = now;
+              ll = ll * go + ml.y * gn;
+              y.x = y.x * go + v.x * gn, y.y = y.y * go + v.y * gn, y.z = y.z * go + v.z * gn, y.w = y.w * go + v.w * gn;
+            }
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
+            const long long qr = (long long)it.tile * kTileRows + rr;
+            uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)((it.r0 + qr / a.group) * a.out_stride) +
+                          (size_t)(it.head * a.group + qr % a.group) * HD + d;
+            o[0] = f32_to_bf16_rn(y.x * inv);
+            o[1] = f32_to_bf16_rn(y.y * inv);
+            o[2] = f32_to_bf16_rn(y.z * inv);
+            o[3] = f32_to_bf16_rn(y.w * inv);
+          }
+        }
+        named_sync(1, kSoftThreads);
+      }
+      if (stage == it.stages) {
+        stage = 0;
+        if (w < w1) next_item();
+      }
+    }
+  }
+
+  // every product and copy has been waited for: the softmax saw the last o_full, the converters the last copy
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+template <int HD, int NG>
+int launch_one(coli_ctx* ctx, TileArgs& a) {
+  using T = Tile<HD, NG>;
+  const int grid = ctx->num_sms < kKvCounters ? ctx->num_sms : kKvCounters;
+  int rc = ensure_workspace(ctx, (size_t)2 * grid * kTileRows * (HD + 2) * sizeof(float));
+  if (rc != COLI_OK) return rc;
+  a.part = reinterpret_cast<float*>(ctx->ws.base);
+  auto kern = kv4_tile_kernel<HD, NG>;
+  static std::atomic<uint64_t> ready{0};  // devices (below 64) on which this instance has its attribute
+  const uint64_t bit = ctx->device < 64 ? 1ull << ctx->device : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "kv4_attention attribute");
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  ProfScope prof(ctx, COLI_KERNEL_ATTENTION);
+  cudaError_t e = launch_k(kern, grid, kTileThreads, T::kSmem, ctx->stream, true, false, a);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "kv4_attention launch");
+  return COLI_OK;
+}
+
+}  // namespace
+
+int launch_kv4_tiles(coli_ctx* ctx, const Kv4View& c, const Kv4Plan& p, const void* q, long long q_stride, int q_heads,
+                     float scale, int window, void* out, long long out_stride) {
+  TileArgs a{c, p, q, q_stride, q_heads / c.heads, scale, window, out, out_stride};
+  a.vec = ((uintptr_t)q % 16 == 0) && q_stride % 8 == 0;
+  a.vec_out = ((uintptr_t)out % 16 == 0) && out_stride % 8 == 0;
+  a.count = ctx->d_kv_count;
+  a.err = ctx->d_status;
+  a.wait_ns = ctx->wait_ns ? ctx->wait_ns : kWaitLimitNs;
+  if (c.hd == 64) return c.ng == 1 ? launch_one<64, 1>(ctx, a) : launch_one<64, 2>(ctx, a);
+  return c.ng == 1 ? launch_one<128, 1>(ctx, a) : c.ng == 2 ? launch_one<128, 2>(ctx, a) : launch_one<128, 4>(ctx, a);
+}
+
+}  // namespace coli
