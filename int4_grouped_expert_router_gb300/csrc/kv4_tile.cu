@@ -165,6 +165,25 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
+// Two binary32 values as one 64-bit register pair, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  return (uint64_t)__float_as_uint(x) | (uint64_t)__float_as_uint(y) << 32;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+  x = __uint_as_float((uint32_t)v);
+  y = __uint_as_float((uint32_t)(v >> 32));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2_f32(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+
 __device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
@@ -424,10 +443,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         }
         wait(&k_full, n & 1);
         tc_fence_after_sync();
+#pragma unroll 1
         for (int x = 0; x < halves; x++) scores(x);
         tc_commit(&k_empty);
         for (int j = 0; j < n_here; j++, n++) {
           wait(&v_full[n & 1], (n >> 1) & 1);
+#pragma unroll 1
           for (int x = 0; x < halves; x++) {
             wait(&p_full[x], ns[x] & 1);
             ns[x]++;
@@ -500,7 +521,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         s_par[n & 1][2] = vmul == 0.f ? 0.f : 1.f / vmul;
         mbar_arrive(&par_full[n & 1]);
       }
-#pragma unroll
+#pragma unroll 1
       for (int u = 0; u < kTileUnits / kConvWarps; u++) {
         const int un = cw * (kTileUnits / kConvWarps) + u;
         const uint8_t* unit = raw + un * T::kUnit;
@@ -544,7 +565,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
       // ---- values: a lane holds tokens 2 c, 2 c + 1 (and + 8) of row r's channels ----
       wait(&v_empty[n & 1], ((n >> 1) & 1) ^ 1);
       const uint32_t v_base = v_base0 + (n & 1) * T::kK;
-#pragma unroll
+#pragma unroll 1
       for (int u = 0; u < kTileUnits / kConvWarps; u++) {
         const int un = cw * (kTileUnits / kConvWarps) + u;
         const uint8_t* unit = raw + un * T::kUnit;
@@ -645,64 +666,73 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         for (int j = 0; j < n_here; j++, n++, ns++) {
           const int t0 = (it.first + stage + j) * kTileTok;
           wait(&par_full[n & 1], (n >> 1) & 1);
-          const float fac = fac0 * s_par[n & 1][0], shrink = s_par[n & 1][1];
+          // kept above 0, so that struck-out scores (minus infinity) stay so
+          const float fac = fmaxf(fac0 * s_par[n & 1][0], 1e-37f), shrink = s_par[n & 1][1];
           unscale = s_par[n & 1][2];
           wait(&s_full[x], ns & 1);
           tc_fence_after_sync();
-          // columns [c0, c1) are visible to this row
+          // columns [c0, c1) are visible to this row; the others are struck out where they lie
           const int c1 = min(kTileTok, max(0, pos - t0 + 1));
           const int c0 = a.window > 0 ? min(kTileTok, max(0, pos - a.window + 1 - t0)) : 0;
-          const bool masked = __any_sync(0xffffffffu, c1 < kTileTok || c0 > 0);
           uint32_t sv[32];
-          float mx = -kInf;
-#pragma unroll
-          for (int k = 0; k < kTileTok / 32; k++) {
-            tmem_ld32(t_s + k * 32, sv);
-            if (masked) {
+          if (__any_sync(0xffffffffu, c1 < kTileTok || c0 > 0)) {
+#pragma unroll 1
+            for (int k = 0; k < kTileTok; k += 32) {
+              tmem_ld32(t_s + k, sv);
 #pragma unroll
               for (int i = 0; i < 32; i++)
-                if (k * 32 + i >= c0 && k * 32 + i < c1) mx = fmaxf(mx, __uint_as_float(sv[i]));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i++) mx = fmaxf(mx, __uint_as_float(sv[i]));
+                if (k + i < c0 || k + i >= c1) sv[i] = 0xff800000u;
+              tmem_st32(t_s + k, sv);
             }
+            tmem_wait_st();
+          }
+          float mx = -kInf;
+#pragma unroll 1
+          for (int k = 0; k < kTileTok; k += 32) {
+            tmem_ld32(t_s + k, sv);
+            float m4[4] = {mx, -kInf, -kInf, -kInf};
+#pragma unroll
+            for (int i = 0; i < 32; i++) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(sv[i]));
+            mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           }
           const float top = mx == -kInf ? -kInf : fac * mx;
           const bool grow = top > mf + kSlack;
-          const bool first = j == 0;
           if (__any_sync(0xffffffffu, grow) || shrink != 1.f) {
             const float now = grow ? top : mf;
             const float f = mf == -kInf ? 1.f : exp2_fast(mf - now);
             mf = now;
             l *= f;
-            if (!first) {
+            if (j != 0) {
 #pragma unroll 1
-              for (int k = 0; k < HD / 32; k++) {
-                tmem_ld32(t_o + k * 32, sv);
+              for (int k = 0; k < HD; k += 32) {
+                tmem_ld32(t_o + k, sv);
 #pragma unroll
                 for (int i = 0; i < 32; i++) sv[i] = __float_as_uint(__uint_as_float(sv[i]) * f * shrink);
-                tmem_st32(t_o + k * 32, sv);
+                tmem_st32(t_o + k, sv);
               }
             }
           }
-          const float add = mf == -kInf ? 0.f : kLift - mf;
-#pragma unroll
-          for (int k = 0; k < kTileTok / 32; k++) {
+          const uint64_t fac2 = pack2(fac, fac), add2 = pack2(mf == -kInf ? 0.f : kLift - mf, mf == -kInf ? 0.f : kLift - mf);
+          uint64_t l2 = 0;
+#pragma unroll 1
+          for (int k = 0; k < kTileTok; k += 32) {
             uint32_t pw[16];
-            tmem_ld32(t_s + k * 32, sv);
+            tmem_ld32(t_s + k, sv);
 #pragma unroll
             for (int i = 0; i < 16; i++) {
-              float e0 = exp2_fast(fmaf(fac, __uint_as_float(sv[2 * i]), add));
-              float e1 = exp2_fast(fmaf(fac, __uint_as_float(sv[2 * i + 1]), add));
-              if (masked) {
-                const int c = k * 32 + 2 * i;
-                e0 = c >= c0 && c < c1 ? e0 : 0.f;
-                e1 = c + 1 >= c0 && c + 1 < c1 ? e1 : 0.f;
-              }
-              l += e0 + e1;
+              float e0, e1;
+              unpack2(fma2((uint64_t)sv[2 * i] | (uint64_t)sv[2 * i + 1] << 32, fac2, add2), e0, e1);
+              e0 = exp2_fast(e0);
+              e1 = exp2_fast(e1);
+              l2 = add2_f32(l2, pack2(e0, e1));
               pw[i] = bits(__floats2half2_rn(e0, e1));
             }
-            tmem_st16(t_s + k * 16, pw);
+            tmem_st16(t_s + k / 2, pw);
+          }
+          {
+            float e0, e1;
+            unpack2(l2, e0, e1);
+            l += e0 + e1;
           }
           tmem_wait_st();
           tc_fence_before_sync();
