@@ -123,6 +123,17 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
+// One lane of a converged warp, the same in every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+  return (uint64_t)__shfl_sync(0xffffffffu, (uint32_t)v, 0) | (uint64_t)__shfl_sync(0xffffffffu, (uint32_t)(v >> 32), 0) << 32;
+}
+
 // f16 A and B (K-major), f32 accumulator.
 __host__ __device__ constexpr uint32_t f16_f32_idesc(uint32_t M, uint32_t N) {
   return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
@@ -414,25 +425,28 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
     }
   } else if (warp == kWarpMma) {
     // -------------------------------------- MMA --------------------------------------
-    if (lane == 0) {
+    // One elected lane issues. Its operands are the same in the whole warp, and made so visibly (shuffles): they
+    // then live in uniform registers, where the instruction wants them.
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t dq0 = uniform(sw128_kmajor_desc(s_q)), dk = uniform(sw128_kmajor_desc(s_k)), dv0 = uniform(sw128_kmajor_desc(s_v));
+    if (elect_one()) {
       constexpr uint32_t kIdS = f16_f32_idesc(kHalf, kTileTok), kIdO = f16_f32_idesc(kHalf, HD);
       uint32_t n = 0, ns[2] = {0, 0}, nseg[2] = {0, 0};  // stages, stages and segments of each half
       auto scores = [&](int x) {
 #pragma unroll
         for (int k = 0; k < HD / 16; k++) {
-          const uint64_t da = sw128_kmajor_desc(s_q + x * T::kQ + (k / 4) * (kHalf * 128)) + (k % 4) * 2;
-          const uint64_t db = sw128_kmajor_desc(s_k + (k / 4) * (kTileTok * 128)) + (k % 4) * 2;
-          tc_mma_bf16(tmem + x * kTileTok, da, db, kIdS, k != 0);
+          // a descriptor's address field counts 16 bytes
+          const uint64_t da = dq0 + (uint32_t)(x * (T::kQ >> 4)) + (k / 4) * (kHalf * 8) + (k % 4) * 2;
+          tc_mma_bf16(tm + x * kTileTok, da, dk + (k / 4) * (kTileTok * 8) + (k % 4) * 2, kIdS, k != 0);
         }
         tc_commit(&s_full[x]);
       };
       auto output = [&](int x, uint32_t stage_n, bool fresh) {
-        const uint8_t* v = s_v + (stage_n & 1) * T::kK;
+        const uint64_t dv = dv0 + (stage_n & 1) * (T::kK >> 4);
 #pragma unroll
-        for (int k = 0; k < kTileTok / 16; k++) {
-          const uint64_t db = sw128_kmajor_desc(v + (k / 4) * (HD * 128)) + (k % 4) * 2;
-          mma_ts(tmem + 2 * kTileTok + x * HD, tmem + x * kTileTok + k * 8, db, kIdO, !(fresh && k == 0));
-        }
+        for (int k = 0; k < kTileTok / 16; k++)
+          mma_ts(tm + 2 * kTileTok + x * HD, tm + x * kTileTok + k * 8, dv + (k / 4) * (HD * 8) + (k % 4) * 2, kIdO,
+                 !(fresh && k == 0));
       };
       while (w < w1) {
         const int n_here = (int)min((long long)(it.stages - stage), w1 - w);
