@@ -7,9 +7,9 @@
 // stages, end to end, are dealt out evenly and contiguously to one CTA per SM, and an item that spans CTAs is
 // joined by the CTA that arrives last, in CTA order.
 //
-// One CTA, 14 warps:
+// One CTA, 18 warps:
 //   producer      bulk copies of the stage's packed units into a ring of two
-//   4 converters  codes to 16-bit values o + s (n - 8) in the 128-byte-swizzled operand layout: K with a token
+//   8 converters  codes to 16-bit values o + s (n - 8) in the 128-byte-swizzled operand layout: K with a token
 //                 per row, V^T with a channel per row (the packed value words hold two neighbouring tokens, which
 //                 is the order that operand wants). Rounded once, to 11 bits, after a power of two has brought the
 //                 stage's largest key (value) below 2^14, so that no size of the keys and values is lost.
@@ -37,10 +37,10 @@ constexpr int kTileTok = 128;                      // tokens of a stage
 constexpr int kTileUnits = kTileTok / kKvUnit;     // 8
 constexpr int kHalf = 128;                         // rows of a half (the instruction's M)
 constexpr int kTileRows = 2 * kHalf;
-constexpr int kConvWarps = 4;
+constexpr int kConvWarps = kTileUnits;            // one unit each
 constexpr int kSoftThreads = 2 * kHalf;
-constexpr int kWarpConv = 8, kWarpMma = 12, kWarpLoad = 13;
-constexpr int kTileThreads = 14 * 32;
+constexpr int kWarpConv = 8, kWarpMma = 16, kWarpLoad = 17;
+constexpr int kTileThreads = 18 * 32;
 constexpr int kSeqChunk = 512;                     // sequences whose stage counts are kept at a time
 constexpr float kSlack = 1.f;                      // log2; weights stay below 2^(13 + kSlack)
 constexpr float kLift = 13.f;
@@ -195,6 +195,12 @@ __device__ __forceinline__ uint64_t add2_f32(uint64_t x, uint64_t y) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
 __device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
@@ -252,6 +258,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
   __shared__ __align__(8) uint64_t raw_full[2], raw_empty[2], k_full, k_empty, v_full[2], v_empty[2], par_full[2],
       q_full[2], s_full[2], p_full[2], o_full[2];
   __shared__ float s_par[2][3];           // per stage: 1 / key factor, change of the value factor, 1 / value factor
+  __shared__ float s_big[2][2][kConvWarps];  // per stage: largest key and value of each unit
   __shared__ uint32_t s_tmem;
   __shared__ long long s_w[kSeqChunk];
   __shared__ long long s_at;
@@ -494,31 +501,41 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
     __syncwarp();
   } else if (warp >= kWarpConv) {
     // ----------------------------------- converters -----------------------------------
+    // A warp converts one unit. Everything up to the stores is done before the operand's buffer is free: the
+    // tensor core waits only for the stores.
     const int cw = warp - kWarpConv, r = lane >> 2, cc = lane & 3;
-    const uint32_t k_base = smem_u32(s_k), v_base0 = smem_u32(s_v);
+    const uint32_t k_base = smem_u32(s_k) + (cw * 16 + r) * 128;
+    const uint32_t v_base0 = smem_u32(s_v) + (cw / 4) * (HD * 128) + r * 128 + cc * 4;
     float vmul = 0.f;  // values are multiplied by it; it only shrinks within a segment
     for (uint32_t n = 0; w < w1; n++) {
       if (n == 0 || stage == 0) vmul = 0.f;
-      const int tok = (it.first + stage) * kTileTok;
-      const uint8_t* raw = s_raw + (n & 1) * T::kRaw;
+      const int left = it.len - (it.first + stage) * kTileTok - cw * 16;  // tokens of this unit that exist
+      const uint8_t* unit = s_raw + (n & 1) * T::kRaw + cw * T::kUnit;
       wait(&raw_full[n & 1], (n >> 1) & 1);
+      // ---- the stage's largest |o| + 8 s of keys (lanes 0..15: a token each) and of values (16..31) ----
+      float big = 0.f;
+      if ((lane & 15) < left) {
+        uint32_t par[NG];
+        lds_words(unit + (lane < 16 ? kv4_kscale_at(HD) : kv4_vscale_at(HD, NG)) + (lane & 15) * NG * 4, par);
+#pragma unroll
+        for (int g = 0; g < NG; g++) big = fmaxf(big, fmaf(8.f, lo_bf16(par[g]), fabsf(hi_bf16(par[g]))));
+      }
+      const float kbig = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 16 ? __float_as_uint(big) : 0u));
+      const float vbig = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 16 ? 0u : __float_as_uint(big)));
+      if (lane == 0) {
+        s_big[n & 1][0][cw] = kbig;
+        s_big[n & 1][1][cw] = vbig;
+      }
+      uint32_t kw[2][T::kWords];
+#pragma unroll
+      for (int h = 0; h < 2; h++) lds_words(unit + h * 32 * T::kWords * 4 + lane * T::kWords * 4, kw[h]);
+      named_sync(2, kConvWarps * 32);
       float kmax = 0.f, vmax = 0.f;
 #pragma unroll
-      for (int i = 0; i < kTileTok / 32; i++) {
-        const int t = i * 32 + lane;
-        if (tok + t < it.len) {
-          uint32_t kp[NG], vp[NG];
-          lds_words(raw + (t / 16) * T::kUnit + kv4_kscale_at(HD) + (t % 16) * NG * 4, kp);
-          lds_words(raw + (t / 16) * T::kUnit + kv4_vscale_at(HD, NG) + (t % 16) * NG * 4, vp);
-#pragma unroll
-          for (int g = 0; g < NG; g++) {
-            kmax = fmaxf(kmax, fmaf(8.f, lo_bf16(kp[g]), fabsf(hi_bf16(kp[g]))));
-            vmax = fmaxf(vmax, fmaf(8.f, lo_bf16(vp[g]), fabsf(hi_bf16(vp[g]))));
-          }
-        }
+      for (int i = 0; i < kConvWarps; i++) {
+        kmax = fmaxf(kmax, s_big[n & 1][0][i]);
+        vmax = fmaxf(vmax, s_big[n & 1][1][i]);
       }
-      kmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(kmax)));
-      vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
       const float kmul = kmax > 0.f ? below_2_14(kmax) : 1.f;
       float shrink = 1.f;
       if (vmax > 0.f && (vmul == 0.f || vmax * vmul >= 16384.f)) {
@@ -526,8 +543,41 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         shrink = vmul == 0.f ? 1.f : now / vmul;
         vmul = now;
       }
-      // ---- keys: this warp's two units; a lane holds tokens r, r + 8 and a quarter of each 32 channels ----
-      wait(&k_empty, (n & 1) ^ 1);
+      // ---- keys: a lane holds tokens r, r + 8 and a quarter of each 32 channels. Odd tokens store the words of a
+      // pair in the other order: eight lanes then cover all banks. ----
+      {
+        uint32_t v[2][T::kWords][4];
+        const int odd = r & 1;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          uint32_t kp[NG], vp[NG];
+          lds_words(unit + kv4_kscale_at(HD) + (r + 8 * h) * NG * 4, kp);
+          lds_words(unit + kv4_vscale_at(HD, NG) + (r + 8 * h) * NG * 4, vp);
+          const bool live = r + 8 * h < left;
+          bool broken = false;  // a value that is not finite is shown by its key: weights of rows that do not see it are 0
+#pragma unroll
+          for (int g = 0; g < NG; g++) broken = broken || hi_bf16(vp[g]) != hi_bf16(vp[g]);
+          __half2 s[NG], o[NG];
+#pragma unroll
+          for (int g = 0; g < NG; g++) {
+            s[g] = __float2half2_rn(live ? lo_bf16(kp[g]) * kmul : 0.f);
+            o[g] = __float2half2_rn(!live ? 0.f : broken ? __uint_as_float(0x7fc00000u) : hi_bf16(kp[g]) * kmul);
+          }
+#pragma unroll
+          for (int i = 0; i < T::kWords; i += 2) {
+            const __half2 s0 = s[i / T::kWpg], s1 = s[(i + 1) / T::kWpg], o0 = o[i / T::kWpg], o1 = o[(i + 1) / T::kWpg];
+            dequantise(odd ? kw[h][i + 1] : kw[h][i], odd ? s1 : s0, odd ? o1 : o0, v[h][i]);
+            dequantise(odd ? kw[h][i] : kw[h][i + 1], odd ? s0 : s1, odd ? o0 : o1, v[h][i + 1]);
+          }
+        }
+        wait(&k_empty, (n & 1) ^ 1);
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+          for (int i = 0; i < T::kWords; i++)
+            sts128(k_base + h * 8 * 128 + (i / 2) * (kTileTok * 128) + (((((i & 1) ^ odd) * 4 + cc) ^ r) << 4), v[h][i]);
+      }
+      fence_proxy_async_smem();
       // the previous stage's scores are done, so the weights of the one before it are: its s_par may go
       if (cw == 0 && lane == 0) {
         s_par[n & 1][0] = 1.f / kmul;
@@ -535,86 +585,45 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         s_par[n & 1][2] = vmul == 0.f ? 0.f : 1.f / vmul;
         mbar_arrive(&par_full[n & 1]);
       }
-#pragma unroll 1
-      for (int u = 0; u < kTileUnits / kConvWarps; u++) {
-        const int un = cw * (kTileUnits / kConvWarps) + u;
-        const uint8_t* unit = raw + un * T::kUnit;
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-          const int t = un * 16 + r + 8 * h;
-          uint32_t kw[T::kWords], kp[NG], vp[NG];
-          lds_words(unit + h * 32 * T::kWords * 4 + lane * T::kWords * 4, kw);
-          lds_words(unit + kv4_kscale_at(HD) + (r + 8 * h) * NG * 4, kp);
-          lds_words(unit + kv4_vscale_at(HD, NG) + (r + 8 * h) * NG * 4, vp);
-          bool broken = false;  // a value that is not finite is shown by its key: weights of rows that do not see it are 0
-#pragma unroll
-          for (int g = 0; g < NG; g++) broken = broken || hi_bf16(vp[g]) != hi_bf16(vp[g]);
-          __half2 s[NG], o[NG];
-#pragma unroll
-          for (int g = 0; g < NG; g++) {
-            const float live = tok + t < it.len ? kmul : 0.f;
-            s[g] = __float2half2_rn(live == 0.f ? 0.f : lo_bf16(kp[g]) * live);
-            o[g] = __float2half2_rn(live == 0.f ? 0.f : broken ? __uint_as_float(0x7fc00000u) : hi_bf16(kp[g]) * live);
-          }
-          // odd tokens store the words of a pair in the other order: eight lanes then cover all banks
-          const uint32_t row = k_base + t * 128;
-#pragma unroll
-          for (int i = 0; i < T::kWords; i += 2) {
-            const int odd = r & 1;
-            uint32_t v[4];
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-              const int which = e ^ odd;
-              const uint32_t word = which ? kw[i + 1] : kw[i];
-              const __half2 sg = which ? s[(i + 1) / T::kWpg] : s[i / T::kWpg], og = which ? o[(i + 1) / T::kWpg] : o[i / T::kWpg];
-              dequantise(word, sg, og, v);
-              sts128(row + (i / 2) * (kTileTok * 128) + (((which * 4 + cc) ^ r) << 4), v);
-            }
-          }
-        }
-      }
-      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&k_full);
       // ---- values: a lane holds tokens 2 c, 2 c + 1 (and + 8) of row r's channels ----
-      wait(&v_empty[n & 1], ((n >> 1) & 1) ^ 1);
-      const uint32_t v_base = v_base0 + (n & 1) * T::kK;
-#pragma unroll 1
-      for (int u = 0; u < kTileUnits / kConvWarps; u++) {
-        const int un = cw * (kTileUnits / kConvWarps) + u;
-        const uint8_t* unit = raw + un * T::kUnit;
+      {
+        uint32_t v[2][T::kWords][4];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-          const int t = 2 * cc + 8 * h;  // in the unit
+          const int t = 2 * cc + 8 * h;
           uint32_t vw[T::kWords], p0[NG], p1[NG];
           lds_words(unit + kv4_v_at(HD, NG) + h * 4 * HD + lane * T::kWords * 4, vw);
           lds_words(unit + kv4_vscale_at(HD, NG) + t * NG * 4, p0);
           lds_words(unit + kv4_vscale_at(HD, NG) + (t + 1) * NG * 4, p1);
-          const float live0 = tok + un * 16 + t < it.len ? vmul : 0.f, live1 = tok + un * 16 + t + 1 < it.len ? vmul : 0.f;
+          const bool live0 = t < left && vmul != 0.f, live1 = t + 1 < left && vmul != 0.f;
           __half2 s[NG], o[NG];
 #pragma unroll
           for (int g = 0; g < NG; g++) {
             const float o0 = hi_bf16(p0[g]), o1 = hi_bf16(p1[g]);
-            s[g] = __floats2half2_rn(live0 == 0.f ? 0.f : lo_bf16(p0[g]) * live0, live1 == 0.f ? 0.f : lo_bf16(p1[g]) * live1);
-            o[g] = __floats2half2_rn(live0 == 0.f || o0 != o0 ? 0.f : o0 * live0, live1 == 0.f || o1 != o1 ? 0.f : o1 * live1);
+            s[g] = __floats2half2_rn(live0 ? lo_bf16(p0[g]) * vmul : 0.f, live1 ? lo_bf16(p1[g]) * vmul : 0.f);
+            o[g] = __floats2half2_rn(live0 && o0 == o0 ? o0 * vmul : 0.f, live1 && o1 == o1 ? o1 * vmul : 0.f);
           }
-          const int chunk = (un % 4) * 2 + h;  // of eight tokens within the 64 of a tile
-          const uint32_t at = v_base + (un / 4) * (HD * 128) + r * 128 + ((chunk ^ r) << 4) + cc * 4;
 #pragma unroll
-          for (int i = 0; i < T::kWords; i++) {
-            uint32_t v[4];
-            dequantise(vw[i], s[i / T::kWpg], o[i / T::kWpg], v);
+          for (int i = 0; i < T::kWords; i++) dequantise(vw[i], s[i / T::kWpg], o[i / T::kWpg], v[h][i]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&raw_empty[n & 1]);  // the packed unit is in registers
+        wait(&v_empty[n & 1], ((n >> 1) & 1) ^ 1);
+        const uint32_t v_base = v_base0 + (n & 1) * T::kK;
 #pragma unroll
-            for (int j = 0; j < 4; j++) sts32(at + ((2 * i + (j >> 1)) * 16 + (j & 1) * 8) * 128, v[j]);
-          }
+        for (int h = 0; h < 2; h++) {
+          const uint32_t at = v_base + ((((cw % 4) * 2 + h) ^ r) << 4);  // the chunk of eight tokens
+#pragma unroll
+          for (int i = 0; i < T::kWords; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) sts32(at + ((2 * i + (j >> 1)) * 16 + (j & 1) * 8) * 128, v[h][i][j]);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&v_full[n & 1]);
-        mbar_arrive(&raw_empty[n & 1]);
-      }
+      if (lane == 0) mbar_arrive(&v_full[n & 1]);
       w++;
       if (++stage == it.stages) {
         stage = 0;
@@ -640,20 +649,21 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         // ---- this row's queries: a power of two brings the largest to [2^14, 2^15) ----
         const size_t at = (size_t)((it.r0 + q_row / a.group) * a.q_stride) + (size_t)(it.head * a.group + q_row % a.group) * HD;
         const unsigned short* src = static_cast<const unsigned short*>(a.q) + at;
-        uint32_t qw[HD / 2];
+        auto eight = [&](int ch) {  // channels 8 ch .. 8 ch + 7
+          if (a.vec) return __ldcg(reinterpret_cast<const uint4*>(src) + ch);
+          uint32_t v[4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) v[i] = __ldcg(src + 8 * ch + 2 * i) | ((uint32_t)__ldcg(src + 8 * ch + 2 * i + 1) << 16);
+          return make_uint4(v[0], v[1], v[2], v[3]);
+        };
         uint32_t amax = 0;
-        if (a.vec) {
+#pragma unroll 4
+        for (int ch = 0; ch < HD / 8; ch++) {
+          const uint4 v = eight(ch);
+          const uint32_t qw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int i = 0; i < HD / 8; i++) {
-            const uint4 v = __ldcg(reinterpret_cast<const uint4*>(src) + i);
-            qw[4 * i] = v.x, qw[4 * i + 1] = v.y, qw[4 * i + 2] = v.z, qw[4 * i + 3] = v.w;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < HD / 2; i++) qw[i] = __ldcg(src + 2 * i) | ((uint32_t)__ldcg(src + 2 * i + 1) << 16);
+          for (int i = 0; i < 4; i++) amax = max(amax, max(qw[i] & 0x7fffu, qw[i] >> 16 & 0x7fffu));
         }
-#pragma unroll
-        for (int i = 0; i < HD / 2; i++) amax = max(amax, max(qw[i] & 0x7fffu, qw[i] >> 16 & 0x7fffu));
         const float big = __uint_as_float(amax << 16);
         if (amax >= 0x7f80u && row < row_n) set_error(a.err, COLI_E_NONFINITE);
         const int ex = min(253, max(1, 127 + 14 + 127 - (int)(amax >> 7)));
@@ -662,11 +672,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         if (a.scale < 0.f) mult = -mult;
         if (!(big < kInf)) mult = __uint_as_float(0x7fc00000u);
         const uint32_t dst = smem_u32(s_q) + x * T::kQ + (row & (kHalf - 1)) * 128;
-#pragma unroll
+#pragma unroll 4
         for (int ch = 0; ch < HD / 8; ch++) {
+          const uint4 u = eight(ch);
+          const uint32_t qw[4] = {u.x, u.y, u.z, u.w};
           float f[8];
 #pragma unroll
-          for (int j = 0; j < 4; j++) f[2 * j] = lo_bf16(qw[4 * ch + j]) * mult, f[2 * j + 1] = hi_bf16(qw[4 * ch + j]) * mult;
+          for (int j = 0; j < 4; j++) f[2 * j] = lo_bf16(qw[j]) * mult, f[2 * j + 1] = hi_bf16(qw[j]) * mult;
           uint32_t v[4];
 #pragma unroll
           for (int j = 0; j < 4; j++) v[j] = bits(__floats2half2_rn(f[j], f[j + 4]));
@@ -706,8 +718,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
             tmem_ld32(t_s + k, sv);
             float m4[4] = {mx, -kInf, -kInf, -kInf};
 #pragma unroll
-            for (int i = 0; i < 32; i++) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(sv[i]));
-            mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            for (int i = 0; i < 32; i += 2)
+              m4[i >> 1 & 3] = max3(m4[i >> 1 & 3], __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
+            mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
           }
           const float top = mx == -kInf ? -kInf : fac * mx;
           const bool grow = top > mf + kSlack;
