@@ -42,7 +42,9 @@ constexpr int kSoftThreads = 2 * kHalf;
 constexpr int kWarpConv = 8, kWarpMma = 16, kWarpLoad = 17;
 constexpr int kTileThreads = 18 * 32;
 constexpr int kSeqChunk = 512;                     // sequences whose stage counts are kept at a time
-constexpr float kSlack = 1.f;                      // log2; weights stay below 2^(13 + kSlack)
+// Weights are 2^(y - m + kLift); the maximum m moves when a score passes it by kSlack (log2). 16 bits hold
+// 2^(kLift + kSlack), and a move costs a pass over the output.
+constexpr float kSlack = 2.5f;
 constexpr float kLift = 13.f;
 constexpr float kInf = __builtin_huge_valf();
 
@@ -52,7 +54,7 @@ struct Tile {
   static constexpr uint32_t kRaw = kTileUnits * kUnit;
   static constexpr uint32_t kQ = kHalf * HD * 2;     // one half's queries
   static constexpr uint32_t kK = kTileTok * HD * 2;  // keys, and values, of a stage
-  static constexpr uint32_t kSmem = 1024 + 2 * kQ + kK + 2 * kK + 2 * kRaw;
+  static constexpr uint32_t kSmem = 1024 + 2 * kQ + 2 * kK + 2 * kK + kRaw;
   static constexpr int kWords = HD / 32, kWpg = kWords / NG;
 };
 
@@ -252,13 +254,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
   // operand tiles on 1024-byte boundaries
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* s_q = smem;                    // [2 halves][HD / 64][128 rows][128 bytes]
-  uint8_t* s_k = s_q + 2 * T::kQ;         // [HD / 64][128 tokens][128 bytes]
-  uint8_t* s_v = s_k + T::kK;             // [2 stages][2][HD channels][128 bytes = 64 tokens]
-  uint8_t* s_raw = s_v + 2 * T::kK;       // [2][kTileUnits] packed units
-  __shared__ __align__(8) uint64_t raw_full[2], raw_empty[2], k_full, k_empty, v_full[2], v_empty[2], par_full[2],
+  uint8_t* s_k = s_q + 2 * T::kQ;         // [2 stages][HD / 64][128 tokens][128 bytes]
+  uint8_t* s_v = s_k + 2 * T::kK;         // [2 stages][2][HD channels][128 bytes = 64 tokens]
+  uint8_t* s_raw = s_v + 2 * T::kK;       // [kTileUnits] packed units
+  __shared__ __align__(8) uint64_t raw_full, raw_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], par_full[4],
       q_full[2], s_full[2], p_full[2], o_full[2];
-  __shared__ float s_par[2][3];           // per stage: 1 / key factor, change of the value factor, 1 / value factor
-  __shared__ float s_big[2][2][kConvWarps];  // per stage: largest key and value of each unit
+  __shared__ float s_par[4][3];           // per stage: 1 / key factor, change of the value factor, 1 / value factor
+  __shared__ float s_big[2][kConvWarps];  // largest key and value of each unit, when a factor has to move
   __shared__ uint32_t s_tmem;
   __shared__ long long s_w[kSeqChunk];
   __shared__ long long s_at;
@@ -267,18 +269,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < 2; i++) {
-      mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], kConvWarps);
+      mbar_init(&k_full[i], kConvWarps);
+      mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], kConvWarps);
       mbar_init(&v_empty[i], 1);
       mbar_init(&par_full[i], 1);
+      mbar_init(&par_full[2 + i], 1);
       mbar_init(&q_full[i], 4);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1);
     }
-    mbar_init(&k_full, kConvWarps);
-    mbar_init(&k_empty, 1);
+    mbar_init(&raw_full, 1);
+    mbar_init(&raw_empty, kConvWarps);
     mbar_fence_init();
   }
   griddep_launch_dependents();
@@ -409,9 +412,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         cached_from = page;
         pages = page + lane < a.p.table_stride ? __ldcg(a.p.table + (size_t)it.b * a.p.table_stride + page + lane) : 0;
       }
-      wait(&raw_empty[n & 1], ((n >> 1) & 1) ^ 1);
+      wait(&raw_empty, (n & 1) ^ 1);
       if (!alive) break;  // what was issued is still awaited by the converters
-      if (lane == 0) mbar_arrive_expect_tx(&raw_full[n & 1], units * T::kUnit);
+      if (lane == 0) mbar_arrive_expect_tx(&raw_full, units * T::kUnit);
       __syncwarp();
       int pg = __shfl_sync(0xffffffffu, pages, (page - cached_from + lane) & 31);
       if (lane < copies) {
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         const int take = min(per_copy, units - lane * per_copy);
         const uint8_t* src = a.c.base + (((size_t)pg * heads + it.head) * (size_t)(page_tok / kKvUnit) +
                                          (tok & (page_tok - 1)) / kKvUnit) * T::kUnit;
-        bulk_g2s(s_raw + (n & 1) * T::kRaw + lane * per_copy * T::kUnit, src, take * T::kUnit, &raw_full[n & 1]);
+        bulk_g2s(s_raw + lane * per_copy * T::kUnit, src, take * T::kUnit, &raw_full);
       }
       w++;
       if (++stage == it.stages) {
@@ -439,12 +442,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
     if (elect_one()) {
       constexpr uint32_t kIdS = f16_f32_idesc(kHalf, kTileTok), kIdO = f16_f32_idesc(kHalf, HD);
       uint32_t n = 0, ns[2] = {0, 0}, nseg[2] = {0, 0};  // stages, stages and segments of each half
-      auto scores = [&](int x) {
+      auto scores = [&](int x, uint32_t stage_n) {
 #pragma unroll
         for (int k = 0; k < HD / 16; k++) {
           // a descriptor's address field counts 16 bytes
           const uint64_t da = dq0 + (uint32_t)(x * (T::kQ >> 4)) + (k / 4) * (kHalf * 8) + (k % 4) * 2;
-          tc_mma_bf16(tm + x * kTileTok, da, dk + (k / 4) * (kTileTok * 8) + (k % 4) * 2, kIdS, k != 0);
+          tc_mma_bf16(tm + x * kTileTok, da, dk + (stage_n & 1) * (T::kK >> 4) + (k / 4) * (kTileTok * 8) + (k % 4) * 2, kIdS, k != 0);
         }
         tc_commit(&s_full[x]);
       };
@@ -462,11 +465,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
           wait(&q_full[x], nseg[x] & 1);
           nseg[x]++;
         }
-        wait(&k_full, n & 1);
+        wait(&k_full[n & 1], (n >> 1) & 1);
         tc_fence_after_sync();
 #pragma unroll 1
-        for (int x = 0; x < halves; x++) scores(x);
-        tc_commit(&k_empty);
+        for (int x = 0; x < halves; x++) scores(x, n);
+        tc_commit(&k_empty[n & 1]);
         for (int j = 0; j < n_here; j++, n++) {
           wait(&v_full[n & 1], (n >> 1) & 1);
 #pragma unroll 1
@@ -479,11 +482,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
             if (x + 1 == halves) tc_commit(&v_empty[n & 1]);
             if (j + 1 < n_here) {  // the next stage's scores go over the weights that the product above reads first
               if (x == 0) {
-                wait(&k_full, (n + 1) & 1);
+                wait(&k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
                 tc_fence_after_sync();
               }
-              scores(x);
-              if (x + 1 == halves) tc_commit(&k_empty);
+              scores(x, n + 1);
+              if (x + 1 == halves) tc_commit(&k_empty[(n + 1) & 1]);
             }
           }
         }
@@ -495,130 +498,121 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         }
       }
       // the last arrivals on these barriers come before the CTA's memory goes
-      wait(&k_empty, (n - 1) & 1);
+      wait(&k_empty[(n - 1) & 1], ((n - 1) >> 1) & 1);
       wait(&v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1);
     }
     __syncwarp();
   } else if (warp >= kWarpConv) {
     // ----------------------------------- converters -----------------------------------
-    // A warp converts one unit. Everything up to the stores is done before the operand's buffer is free: the
-    // tensor core waits only for the stores.
+    // A warp converts one unit, which it first takes into registers, so that the next copy can start.
     const int cw = warp - kWarpConv, r = lane >> 2, cc = lane & 3;
-    const uint32_t k_base = smem_u32(s_k) + (cw * 16 + r) * 128;
+    const uint32_t k_base0 = smem_u32(s_k) + (cw * 16 + r) * 128;
     const uint32_t v_base0 = smem_u32(s_v) + (cw / 4) * (HD * 128) + r * 128 + cc * 4;
-    float vmul = 0.f;  // values are multiplied by it; it only shrinks within a segment
+    const uint8_t* unit = s_raw + cw * T::kUnit;
+    float kmul = 0.f, vmul = 0.f;  // keys and values are multiplied by them; they only shrink within a segment
     for (uint32_t n = 0; w < w1; n++) {
-      if (n == 0 || stage == 0) vmul = 0.f;
+      if (n == 0 || stage == 0) kmul = vmul = 0.f;
       const int left = it.len - (it.first + stage) * kTileTok - cw * 16;  // tokens of this unit that exist
-      const uint8_t* unit = s_raw + (n & 1) * T::kRaw + cw * T::kUnit;
-      wait(&raw_full[n & 1], (n >> 1) & 1);
-      // ---- the stage's largest |o| + 8 s of keys (lanes 0..15: a token each) and of values (16..31) ----
-      float big = 0.f;
-      if ((lane & 15) < left) {
-        uint32_t par[NG];
-        lds_words(unit + (lane < 16 ? kv4_kscale_at(HD) : kv4_vscale_at(HD, NG)) + (lane & 15) * NG * 4, par);
+      wait(&raw_full, n & 1);
+      // codes of tokens r, r + 8 (keys) and of token pairs c, c + 4 (values), with their scales and offsets
+      uint32_t kw[2][T::kWords], vw[2][T::kWords], kp[2][NG], vp[2][NG], p0[2][NG], p1[2][NG];
 #pragma unroll
-        for (int g = 0; g < NG; g++) big = fmaxf(big, fmaf(8.f, lo_bf16(par[g]), fabsf(hi_bf16(par[g]))));
-      }
-      const float kbig = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 16 ? __float_as_uint(big) : 0u));
-      const float vbig = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 16 ? 0u : __float_as_uint(big)));
-      if (lane == 0) {
-        s_big[n & 1][0][cw] = kbig;
-        s_big[n & 1][1][cw] = vbig;
-      }
-      uint32_t kw[2][T::kWords];
-#pragma unroll
-      for (int h = 0; h < 2; h++) lds_words(unit + h * 32 * T::kWords * 4 + lane * T::kWords * 4, kw[h]);
-      named_sync(2, kConvWarps * 32);
-      float kmax = 0.f, vmax = 0.f;
-#pragma unroll
-      for (int i = 0; i < kConvWarps; i++) {
-        kmax = fmaxf(kmax, s_big[n & 1][0][i]);
-        vmax = fmaxf(vmax, s_big[n & 1][1][i]);
-      }
-      const float kmul = kmax > 0.f ? below_2_14(kmax) : 1.f;
-      float shrink = 1.f;
-      if (vmax > 0.f && (vmul == 0.f || vmax * vmul >= 16384.f)) {
-        const float now = below_2_14(vmax);
-        shrink = vmul == 0.f ? 1.f : now / vmul;
-        vmul = now;
-      }
-      // ---- keys: a lane holds tokens r, r + 8 and a quarter of each 32 channels. Odd tokens store the words of a
-      // pair in the other order: eight lanes then cover all banks. ----
-      {
-        uint32_t v[2][T::kWords][4];
-        const int odd = r & 1;
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-          uint32_t kp[NG], vp[NG];
-          lds_words(unit + kv4_kscale_at(HD) + (r + 8 * h) * NG * 4, kp);
-          lds_words(unit + kv4_vscale_at(HD, NG) + (r + 8 * h) * NG * 4, vp);
-          const bool live = r + 8 * h < left;
-          bool broken = false;  // a value that is not finite is shown by its key: weights of rows that do not see it are 0
-#pragma unroll
-          for (int g = 0; g < NG; g++) broken = broken || hi_bf16(vp[g]) != hi_bf16(vp[g]);
-          __half2 s[NG], o[NG];
-#pragma unroll
-          for (int g = 0; g < NG; g++) {
-            s[g] = __float2half2_rn(live ? lo_bf16(kp[g]) * kmul : 0.f);
-            o[g] = __float2half2_rn(!live ? 0.f : broken ? __uint_as_float(0x7fc00000u) : hi_bf16(kp[g]) * kmul);
-          }
-#pragma unroll
-          for (int i = 0; i < T::kWords; i += 2) {
-            const __half2 s0 = s[i / T::kWpg], s1 = s[(i + 1) / T::kWpg], o0 = o[i / T::kWpg], o1 = o[(i + 1) / T::kWpg];
-            dequantise(odd ? kw[h][i + 1] : kw[h][i], odd ? s1 : s0, odd ? o1 : o0, v[h][i]);
-            dequantise(odd ? kw[h][i] : kw[h][i + 1], odd ? s0 : s1, odd ? o0 : o1, v[h][i + 1]);
-          }
-        }
-        wait(&k_empty, (n & 1) ^ 1);
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-#pragma unroll
-          for (int i = 0; i < T::kWords; i++)
-            sts128(k_base + h * 8 * 128 + (i / 2) * (kTileTok * 128) + (((((i & 1) ^ odd) * 4 + cc) ^ r) << 4), v[h][i]);
-      }
-      fence_proxy_async_smem();
-      // the previous stage's scores are done, so the weights of the one before it are: its s_par may go
-      if (cw == 0 && lane == 0) {
-        s_par[n & 1][0] = 1.f / kmul;
-        s_par[n & 1][1] = shrink;
-        s_par[n & 1][2] = vmul == 0.f ? 0.f : 1.f / vmul;
-        mbar_arrive(&par_full[n & 1]);
+      for (int h = 0; h < 2; h++) {
+        lds_words(unit + h * 32 * T::kWords * 4 + lane * T::kWords * 4, kw[h]);
+        lds_words(unit + kv4_v_at(HD, NG) + h * 4 * HD + lane * T::kWords * 4, vw[h]);
+        lds_words(unit + kv4_kscale_at(HD) + (r + 8 * h) * NG * 4, kp[h]);
+        lds_words(unit + kv4_vscale_at(HD, NG) + (r + 8 * h) * NG * 4, vp[h]);
+        lds_words(unit + kv4_vscale_at(HD, NG) + (2 * cc + 8 * h) * NG * 4, p0[h]);
+        lds_words(unit + kv4_vscale_at(HD, NG) + (2 * cc + 8 * h + 1) * NG * 4, p1[h]);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&k_full);
-      // ---- values: a lane holds tokens 2 c, 2 c + 1 (and + 8) of row r's channels ----
-      {
-        uint32_t v[2][T::kWords][4];
+      if (lane == 0) mbar_arrive(&raw_empty);
+      float kbig = 0.f, vbig = 0.f;  // the largest |o| + 8 s of this lane's tokens
+      bool broken[2];                // a value that is not finite is shown by its key: rows that do not see it have weight 0
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          const int t = 2 * cc + 8 * h;
-          uint32_t vw[T::kWords], p0[NG], p1[NG];
-          lds_words(unit + kv4_v_at(HD, NG) + h * 4 * HD + lane * T::kWords * 4, vw);
-          lds_words(unit + kv4_vscale_at(HD, NG) + t * NG * 4, p0);
-          lds_words(unit + kv4_vscale_at(HD, NG) + (t + 1) * NG * 4, p1);
-          const bool live0 = t < left && vmul != 0.f, live1 = t + 1 < left && vmul != 0.f;
-          __half2 s[NG], o[NG];
+      for (int h = 0; h < 2; h++) {
+        broken[h] = false;
+        const bool live = r + 8 * h < left;
 #pragma unroll
-          for (int g = 0; g < NG; g++) {
-            const float o0 = hi_bf16(p0[g]), o1 = hi_bf16(p1[g]);
-            s[g] = __floats2half2_rn(live0 ? lo_bf16(p0[g]) * vmul : 0.f, live1 ? lo_bf16(p1[g]) * vmul : 0.f);
-            o[g] = __floats2half2_rn(live0 && o0 == o0 ? o0 * vmul : 0.f, live1 && o1 == o1 ? o1 * vmul : 0.f);
-          }
-#pragma unroll
-          for (int i = 0; i < T::kWords; i++) dequantise(vw[i], s[i / T::kWpg], o[i / T::kWpg], v[h][i]);
+        for (int g = 0; g < NG; g++) {
+          broken[h] = broken[h] || hi_bf16(vp[h][g]) != hi_bf16(vp[h][g]);
+          kbig = fmaxf(kbig, live ? fmaf(8.f, lo_bf16(kp[h][g]), fabsf(hi_bf16(kp[h][g]))) : 0.f);
+          vbig = fmaxf(vbig, live ? fmaf(8.f, lo_bf16(vp[h][g]), fabsf(hi_bf16(vp[h][g]))) : 0.f);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&raw_empty[n & 1]);  // the packed unit is in registers
-        wait(&v_empty[n & 1], ((n >> 1) & 1) ^ 1);
-        const uint32_t v_base = v_base0 + (n & 1) * T::kK;
+      }
+      auto too_big = [](float x, float mul) { return mul == 0.f ? x > 0.f : x * mul >= 16384.f; };
+      float shrink = 1.f;
+      if (named_sync_or(2, kConvWarps * 32, too_big(kbig, kmul) || too_big(vbig, vmul))) {
+        kbig = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(kbig)));
+        vbig = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vbig)));
+        if (lane == 0) {
+          s_big[0][cw] = kbig;
+          s_big[1][cw] = vbig;
+        }
+        named_sync(2, kConvWarps * 32);
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          const uint32_t at = v_base + ((((cw % 4) * 2 + h) ^ r) << 4);  // the chunk of eight tokens
+        for (int i = 0; i < kConvWarps; i++) {
+          kbig = fmaxf(kbig, s_big[0][i]);
+          vbig = fmaxf(vbig, s_big[1][i]);
+        }
+        if (too_big(kbig, kmul)) kmul = below_2_14(kbig);
+        if (too_big(vbig, vmul)) {
+          const float now = below_2_14(vbig);
+          shrink = vmul == 0.f ? 1.f : now / vmul;
+          vmul = now;
+        }
+      }
+      // ---- keys: odd tokens store the words of a pair in the other order: eight lanes then cover all banks ----
+      wait(&k_empty[n & 1], ((n >> 1) & 1) ^ 1);
+      if (cw == 0 && lane == 0) {  // the softmax of four stages ago is long done
+        s_par[n & 3][0] = kmul == 0.f ? 1.f : 1.f / kmul;
+        s_par[n & 3][1] = shrink;
+        s_par[n & 3][2] = vmul == 0.f ? 0.f : 1.f / vmul;
+        mbar_arrive(&par_full[n & 3]);
+      }
+      const uint32_t k_base = k_base0 + (n & 1) * T::kK;
+      const int odd = r & 1;
 #pragma unroll
-          for (int i = 0; i < T::kWords; i++)
+      for (int h = 0; h < 2; h++) {
+        const bool live = r + 8 * h < left;
+        __half2 s[NG], o[NG];
 #pragma unroll
-            for (int j = 0; j < 4; j++) sts32(at + ((2 * i + (j >> 1)) * 16 + (j & 1) * 8) * 128, v[h][i][j]);
+        for (int g = 0; g < NG; g++) {
+          s[g] = __float2half2_rn(live ? lo_bf16(kp[h][g]) * kmul : 0.f);
+          o[g] = __float2half2_rn(!live ? 0.f : broken[h] ? __uint_as_float(0x7fc00000u) : hi_bf16(kp[h][g]) * kmul);
+        }
+#pragma unroll
+        for (int i = 0; i < T::kWords; i++) {
+          const int j = i ^ 1;
+          uint32_t v[4];
+          dequantise(odd ? kw[h][j] : kw[h][i], odd ? s[j / T::kWpg] : s[i / T::kWpg], odd ? o[j / T::kWpg] : o[i / T::kWpg], v);
+          sts128(k_base + h * 8 * 128 + (i / 2) * (kTileTok * 128) + (((((i & 1) ^ odd) * 4 + cc) ^ r) << 4), v);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_full[n & 1]);
+      // ---- values ----
+      wait(&v_empty[n & 1], ((n >> 1) & 1) ^ 1);
+      const uint32_t v_base = v_base0 + (n & 1) * T::kK;
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const int t = 2 * cc + 8 * h;
+        const bool live0 = t < left && vmul != 0.f, live1 = t + 1 < left && vmul != 0.f;
+        __half2 s[NG], o[NG];
+#pragma unroll
+        for (int g = 0; g < NG; g++) {
+          const float o0 = hi_bf16(p0[h][g]), o1 = hi_bf16(p1[h][g]);
+          s[g] = __floats2half2_rn(live0 ? lo_bf16(p0[h][g]) * vmul : 0.f, live1 ? lo_bf16(p1[h][g]) * vmul : 0.f);
+          o[g] = __floats2half2_rn(live0 && o0 == o0 ? o0 * vmul : 0.f, live1 && o1 == o1 ? o1 * vmul : 0.f);
+        }
+        const uint32_t at = v_base + ((((cw % 4) * 2 + h) ^ r) << 4);  // the chunk of eight tokens
+#pragma unroll
+        for (int i = 0; i < T::kWords; i++) {
+          uint32_t v[4];
+          dequantise(vw[h][i], s[i / T::kWpg], o[i / T::kWpg], v);
+#pragma unroll
+          for (int j = 0; j < 4; j++) sts32(at + ((2 * i + (j >> 1)) * 16 + (j & 1) * 8) * 128, v[j]);
         }
       }
       fence_proxy_async_smem();
@@ -691,10 +685,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
 
         for (int j = 0; j < n_here; j++, n++, ns++) {
           const int t0 = (it.first + stage + j) * kTileTok;
-          wait(&par_full[n & 1], (n >> 1) & 1);
+          wait(&par_full[n & 3], (n >> 2) & 1);
           // kept above 0, so that struck-out scores (minus infinity) stay so
-          const float fac = fmaxf(fac0 * s_par[n & 1][0], 1e-37f), shrink = s_par[n & 1][1];
-          unscale = s_par[n & 1][2];
+          const float fac = fmaxf(fac0 * s_par[n & 3][0], 1e-37f), shrink = s_par[n & 3][1];
+          unscale = s_par[n & 3][2];
           wait(&s_full[x], ns & 1);
           tc_fence_after_sync();
           // columns [c0, c1) are visible to this row; the others are struck out where they lie
