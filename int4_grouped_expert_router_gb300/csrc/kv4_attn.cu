@@ -26,6 +26,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "kv4.h"
 #include "pipe.h"
@@ -50,11 +51,15 @@ struct Cfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kWords = HD / 32;       // code words of a token a lane holds (keys); as many per token pair (values)
   static constexpr int kWpg = kWords / NG;     // of which a group takes
+  static constexpr int kIw = kWords < 4 ? kWords : 4;
   static constexpr int kMt = HD / 16;          // 16-channel tiles of the output
   static constexpr int kPad = HD + 4;          // floats of a row in the join buffer: no bank conflicts at 8-byte stores
   static constexpr uint32_t kUnit = kv4_unit_bytes(HD, NG);
   static constexpr uint32_t kStage = kStageUnits * kUnit;
-  static constexpr int kCtas = NT == 1 ? (HD == 256 ? 2 : 3) : (NT * HD <= 256 ? 2 : 1);  // resident per SM (registers)
+  // Values enter the product dequantised where several tiles of rows share the work of it (bf16: 11 bits); otherwise as
+  // codes, with a group's scale on the weight.
+  static constexpr bool kDeq = !F32 && NT > 1;
+  static constexpr int kCtas = HD == 256 ? (NT == 1 ? 2 : 1) : NT == 1 ? 3 : 2;  // resident per SM (registers)
   static constexpr uint32_t kJoin = kStageUnits * kRows * (kPad + 2) * 4;
   static constexpr uint32_t kQ = NT * (HD / 16) * 32 * 8 * (F32 ? 2 : 1);
   static constexpr uint32_t kBudget = (kCtas == 3 ? 74 : kCtas == 2 ? 112 : 200) * 1024;
@@ -114,6 +119,15 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same from a zero accumulator.
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -132,39 +146,40 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
 __device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// N words of a lane from shared memory.
+// N words of a lane from shared memory (32-bit addresses: no 64-bit arithmetic in the loop).
+__device__ __forceinline__ void lds4(uint32_t p, uint32_t* w) {
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(p) : "memory");
+}
 template <int N>
-__device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
-  if constexpr (N % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const uint4 v = lds128(p + 4 * i);
-      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
-    }
+__device__ __forceinline__ void lds_words(uint32_t p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    lds4(p, w);
   } else if constexpr (N == 2) {
-    const uint2 v = lds64(p);
-    w[0] = v.x, w[1] = v.y;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(p) : "memory");
   } else {
-    static_assert(N == 1, "1, 2 or a multiple of 4 words");
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(smem_u32(p)) : "memory");
+    static_assert(N == 1, "1, 2 or 4 words");
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(p) : "memory");
   }
 }
 
 // A lane's code words of one 16-token key row or value pair row, kv4.h: iw words per access, accesses
 // `apart` bytes from each other.
 template <int WORDS>
-__device__ __forceinline__ void lds_codes(const uint8_t* p, int apart, uint32_t (&w)[WORDS]) {
+__device__ __forceinline__ void lds_codes(uint32_t p, int apart, uint32_t (&w)[WORDS]) {
   if constexpr (WORDS <= 4) {
     lds_words(p, w);
   } else {
-    uint32_t lo[4], hi[4];
-    lds_words(p, lo);
-    lds_words(p + apart, hi);
-#pragma unroll
-    for (int i = 0; i < 4; i++) w[i] = lo[i], w[4 + i] = hi[i];
+    lds4(p, w);
+    lds4(p + apart, w + 4);
   }
 }
 
@@ -373,6 +388,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
 
   // -------------------------------------- consumers --------------------------------------
   const int r = lane >> 2, cc = lane & 3;
+  const uint32_t ring_at = smem_u32(ring);
   int slot = 0;
   uint32_t phase = 0;
   bool alive = true;
@@ -441,7 +457,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
 #pragma unroll
         for (int e = 0; e < 2; e++) sumq[nt][e][g] = __shfl_sync(0xffffffffu, sum[g], (2 * cc + e) * 4);
       }
-      const float f = fabsf(a.scale) * 1.4426950408889634f * inv;
+      const float f = fmaxf(fabsf(a.scale) * 1.4426950408889634f * inv, 1e-37f);  // not 0: minus infinity stays it
 #pragma unroll
       for (int e = 0; e < 2; e++) {
         fac[nt][e] = __shfl_sync(0xffffffffu, f, (2 * cc + e) * 4);
@@ -488,13 +504,261 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         for (int g = 0; g < NG; g++) bias[nt][e][g] = 0.f;
       }
     }
-    // value scales are multiplied by vmul, a power of two that keeps them (and so weight x scale in 16 bits)
-    // below 2^14; it only shrinks, and the outputs with it.
-    float vmul = 0.f;
+    // value scales (dequantised: values) are multiplied by vmul, a power of two that keeps them below 2^14; it
+    // only shrinks, and the outputs with it.
+    float vmul = __uint_as_float(253u << 23);
     const int pos_min = it.len - it.m + tile_row / a.group;  // first row's position
-    const int lo_max = a.window > 0 ? it.len - it.m + (tile_row + row_n - 1) / a.group - a.window + 1 : 0;
     const int pos_max = it.len - it.m + (tile_row + row_n - 1) / a.group;
+    const int lo_max = a.window > 0 ? pos_max - a.window + 1 : 0;
     const int lo_min = a.window > 0 ? pos_min - a.window + 1 : 0;
+
+    // One unit; `masked`: some row does not see some token of it.
+    auto process = [&](auto masked, uint32_t unit, int t0) {
+      constexpr bool kMasked = decltype(masked)::value;
+      const uint32_t codes = unit + lane * (C::kIw * 4);
+      uint32_t kp[2][NG], vp[2][NG];
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        lds_words(unit + kv4_kscale_at(HD) + (r + 8 * h) * NG * 4, kp[h]);
+        lds_words(unit + kv4_vscale_at(HD, NG) + (r + 8 * h) * NG * 4, vp[h]);
+        if (kMasked && t0 + r + 8 * h >= it.len) {  // tokens past the sequence hold anything
+#pragma unroll
+          for (int g = 0; g < NG; g++) vp[h][g] = 0;
+        }
+      }
+      // ---- scores ----
+      float x[NT][4];
+      {
+        uint32_t kw[2][C::kWords];
+        lds_codes(codes, 1024, kw[0]);
+        lds_codes(codes + 128 * C::kIw, 1024, kw[1]);
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int j = 0; j < 4; j++) x[nt][j] = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; g++) {
+          float acc[2][NT][4];  // two chains: even and odd steps
+#pragma unroll
+          for (int i = g * C::kWpg; i < (g + 1) * C::kWpg; i++) {
+            uint32_t a0[4], a1[4];
+            expand(kw[0][i], a0);
+            expand(kw[1][i], a1);
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+              for (int nt = 0; nt < NT; nt++) {
+                uint2 b;
+                if constexpr (NT == 1)
+                  b = qf[2 * i + h];
+                else
+                  b = s_q[(nt * (HD / 16) + 2 * i + h) * 32 + lane];
+                if (i == g * C::kWpg)
+                  mma16816_zero(acc[h][nt], a0[2 * h], a1[2 * h], a0[2 * h + 1], a1[2 * h + 1], b.x, b.y);
+                else
+                  mma16816(acc[h][nt], a0[2 * h], a1[2 * h], a0[2 * h + 1], a1[2 * h + 1], b.x, b.y);
+                if constexpr (F32) {
+                  const uint2 l = s_q[((NT + nt) * (HD / 16) + 2 * i + h) * 32 + lane];
+                  mma16816(acc[h][nt], a0[2 * h], a1[2 * h], a0[2 * h + 1], a1[2 * h + 1], l.x, l.y);
+                }
+              }
+          }
+          const float ks[2] = {lo_bf16(kp[0][g]), lo_bf16(kp[1][g])}, ko[2] = {hi_bf16(kp[0][g]), hi_bf16(kp[1][g])};
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+              x[nt][j] = fmaf(ks[j >> 1], acc[0][nt][j] + acc[1][nt][j], fmaf(ko[j >> 1], sumq[nt][j & 1][g], x[nt][j]));
+        }
+      }
+      if constexpr (C::kDeq) {
+        // a value that is not finite is kept out of the product and shown by its token's score: rows that do not see
+        // the token have weight 0
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          bool broken = false;
+#pragma unroll
+          for (int g = 0; g < NG; g++) broken = broken || (vp[h][g] & 0x7fff0000u) > 0x7f800000u;
+          if (broken) {
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) x[nt][2 * h] = x[nt][2 * h + 1] = __uint_as_float(0x7fc00000u);
+          }
+        }
+      }
+      if constexpr (kMasked) {
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const int t = t0 + r + 8 * (j >> 1);
+            if (t > pos[nt][j & 1] || (a.window > 0 && t <= pos[nt][j & 1] - a.window)) x[nt][j] = -kInf;
+          }
+      }
+      // ---- running maximum: moves only when a score passes it by kSlack ----
+      float y[NT][4], most = -kInf;
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) y[nt][j] = fmaf(fac[nt][j & 1], x[nt][j], -mf[nt][j & 1]);
+        most = max3(max3(most, y[nt][0], y[nt][1]), y[nt][2], y[nt][3]);
+      }
+      float top = 0.f;  // largest value scale (dequantised: bound of the values) of the unit
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+#pragma unroll
+        for (int g = 0; g < NG; g++)
+          top = fmaxf(top, C::kDeq ? fmaf(8.f, lo_bf16(vp[h][g]), fabsf(hi_bf16(vp[h][g]))) : lo_bf16(vp[h][g]));
+      if (__any_sync(0xffffffffu, most > kSlack || top * vmul >= 16384.f)) {
+        const float seen = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+        float shrink = 1.f;
+        if (seen * vmul >= 16384.f) {
+          // 2^(13 - floor(log2 seen)): seen * vmul in [2^13, 2^14)
+          const int ex = min(253, max(1, 127 + 13 + 127 - (int)(__float_as_uint(seen) >> 23)));
+          const float now = __uint_as_float((uint32_t)ex << 23);
+          shrink = now / vmul;
+          vmul = now;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            float mx = fmaxf(x[nt][e], x[nt][2 + e]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float now = mx == -kInf ? mf[nt][e] : fmaxf(mf[nt][e], fac[nt][e] * mx);
+            const float f = mf[nt][e] == -kInf ? 1.f : exp2_fast(mf[nt][e] - now);
+            mf[nt][e] = now;
+            lsum[nt][e] *= f;
+#pragma unroll
+            for (int g = 0; g < NG; g++) bias[nt][e][g] *= f;
+#pragma unroll
+            for (int i = 0; i < C::kMt; i++) {
+              o[nt][i][e] *= f * shrink;
+              o[nt][i][2 + e] *= f * shrink;
+            }
+#pragma unroll
+            for (int j = e; j < 4; j += 2) y[nt][j] = fmaf(fac[nt][e], x[nt][j], -now);
+          }
+      }
+      // ---- weights, transposed into B fragments ----
+      float pr[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          pr[nt][j] = exp2_fast(y[nt][j]);
+          if (kMasked && x[nt][j] == -kInf) pr[nt][j] = 0.f;  // a row that has seen nothing has no maximum
+        }
+        lsum[nt][0] += pr[nt][0] + pr[nt][2];
+        lsum[nt][1] += pr[nt][1] + pr[nt][3];
+      }
+      constexpr int kPg = C::kDeq ? 1 : NG;  // weights per group
+      uint32_t pb[NT][kPg][2];
+      [[maybe_unused]] uint32_t pl[F32 ? NT : 1][kPg][2];
+      if constexpr (C::kDeq) {
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int h = 0; h < 2; h++) pb[nt][0][h] = transpose8x8(pack_half2(pr[nt][2 * h] * 8192.f, pr[nt][2 * h + 1] * 8192.f));
+      } else {
+        // A bf16 call's weight enters the product as h = round(a s vmul) in 11 bits. The offset takes the same
+        // rounded weight, as h (o / (s vmul)): rounding it then scales the token's V as a whole, however far o is
+        // from it. The quotient gets a correction step, so that it is exact where V = 0 is. Where the scale is
+        // nothing beside the largest, the offset is V. With the 22 bits of an f32 call's weights a itself serves.
+#pragma unroll
+        for (int g = 0; g < NG; g++) {
+          float vs[2], vo[2];
+          bool faint[2];
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            vs[h] = lo_bf16(vp[h][g]) * vmul;
+            vo[h] = hi_bf16(vp[h][g]);
+            faint[h] = F32 || vs[h] < 9.3132257e-10f;  // 2^-30
+            if (!F32) {
+              const float inv = rcp_fast(vs[h]), q = vo[h] * inv;
+              const float quotient = fmaf(fmaf(-q, vs[h], vo[h]), inv, q);
+              vo[h] = faint[h] ? vo[h] : quotient;
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              const float pv[2] = {pr[nt][2 * h] * vs[h], pr[nt][2 * h + 1] * vs[h]};
+              const uint32_t hi = pack_half2(pv[0], pv[1]);
+              const __half2 hh = *reinterpret_cast<const __half2*>(&hi);
+              const float kept[2] = {__low2float(hh), __high2float(hh)};
+              pb[nt][g][h] = transpose8x8(hi);
+              if constexpr (F32) pl[nt][g][h] = transpose8x8(pack_half2(pv[0] - kept[0], pv[1] - kept[1]));
+#pragma unroll
+              for (int e = 0; e < 2; e++) {
+                float off = vo[h];
+                if (kMasked && x[nt][2 * h + e] == -kInf) off = 0.f;  // an unseen NaN stays unseen
+                bias[nt][e][g] = fmaf(faint[h] ? pr[nt][2 * h + e] : kept[e], off, bias[nt][e][g]);
+              }
+            }
+        }
+      }
+      // ---- output ----
+      {
+        const uint32_t vb = codes + kv4_v_at(HD, NG);
+        uint32_t vw[2][C::kWords];
+        lds_codes(vb, 512, vw[0]);
+        lds_codes(vb + 4 * HD, 512, vw[1]);
+        [[maybe_unused]] __half2 s[C::kDeq ? 2 : 1][NG], off[C::kDeq ? 2 : 1][NG];
+        if constexpr (C::kDeq) {
+#pragma unroll
+          for (int h = 0; h < 2; h++) {  // tokens 2 c, 2 c + 1 and the eight after
+            uint32_t p0[NG], p1[NG];
+            const uint32_t at = unit + kv4_vscale_at(HD, NG) + (2 * cc + 8 * h) * NG * 4;
+            lds_words(at, p0);
+            lds_words(at + NG * 4, p1);
+            const bool live0 = !kMasked || t0 + 2 * cc + 8 * h < it.len, live1 = !kMasked || t0 + 2 * cc + 8 * h + 1 < it.len;
+#pragma unroll
+            for (int g = 0; g < NG; g++) {
+              const float o0 = hi_bf16(p0[g]), o1 = hi_bf16(p1[g]);
+              s[h][g] = __floats2half2_rn(live0 ? lo_bf16(p0[g]) * vmul : 0.f, live1 ? lo_bf16(p1[g]) * vmul : 0.f);
+              off[h][g] = __floats2half2_rn(live0 && o0 == o0 ? o0 * vmul : 0.f, live1 && o1 == o1 ? o1 * vmul : 0.f);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < C::kWords; i++) {
+          const int g = i / C::kWpg;
+          uint32_t a0[4], a1[4];
+          expand(vw[0][i], a0);
+          expand(vw[1][i], a1);
+          if constexpr (C::kDeq) {
+#pragma unroll
+            for (int m = 0; m < 4; m++) {
+              const __half2 v0 = __hfma2(*reinterpret_cast<const __half2*>(&a0[m]), s[0][g], off[0][g]);
+              const __half2 v1 = __hfma2(*reinterpret_cast<const __half2*>(&a1[m]), s[1][g], off[1][g]);
+              a0[m] = *reinterpret_cast<const uint32_t*>(&v0);
+              a1[m] = *reinterpret_cast<const uint32_t*>(&v1);
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+              float(&d)[4] = o[nt][2 * i + h];
+              const int pg = C::kDeq ? 0 : g;
+              if constexpr (F32) {
+                // the instruction's own accumulator is cut, not rounded: a unit's sum is formed from zero and
+                // added in binary32
+                float t[4];
+                mma16816_zero(t, a0[2 * h], a0[2 * h + 1], a1[2 * h], a1[2 * h + 1], pl[nt][pg][0], pl[nt][pg][1]);
+                mma16816(t, a0[2 * h], a0[2 * h + 1], a1[2 * h], a1[2 * h + 1], pb[nt][pg][0], pb[nt][pg][1]);
+#pragma unroll
+                for (int j = 0; j < 4; j++) d[j] += t[j];
+              } else {
+                mma16816(d, a0[2 * h], a0[2 * h + 1], a1[2 * h], a1[2 * h + 1], pb[nt][pg][0], pb[nt][pg][1]);
+              }
+            }
+        }
+      }
+    };
 
     for (int n = 0; n < n_here; n++, w++, stage++) {
       const int t0 = (it.first + stage) * kStageTok + warp * kKvUnit;
@@ -502,213 +766,12 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         set_error(a.err, COLI_E_TIMEOUT);
         alive = false;  // whatever the ring holds is used: the result is void, but nothing hangs
       }
-      const uint8_t* unit = ring + slot * C::kStage + warp * C::kUnit;
+      const uint32_t unit = ring_at + slot * C::kStage + warp * C::kUnit;
       if (t0 <= pos_max && t0 + kKvUnit > lo_min) {  // some row of the tile sees some token of the unit
-        const bool masked = t0 + kKvUnit - 1 > pos_min || t0 < lo_max;
-        uint32_t kp[2][NG], vp[2][NG];
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-          lds_words(unit + kv4_kscale_at(HD) + (r + 8 * h) * NG * 4, kp[h]);
-          lds_words(unit + kv4_vscale_at(HD, NG) + (r + 8 * h) * NG * 4, vp[h]);
-        }
-        if (masked) {  // tokens past the sequence hold anything
-#pragma unroll
-          for (int h = 0; h < 2; h++)
-            if (t0 + r + 8 * h >= it.len) {
-#pragma unroll
-              for (int g = 0; g < NG; g++) vp[h][g] = 0;
-            }
-        }
-        // ---- scores ----
-        float x[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-          for (int j = 0; j < 4; j++) x[nt][j] = 0.f;
-        {
-          uint32_t kw[2][C::kWords];
-          lds_codes(unit + lane * (C::kWords < 4 ? C::kWords : 4) * 4, 1024, kw[0]);
-          lds_codes(unit + (C::kWords < 4 ? 32 * C::kWords * 4 : 512) + lane * (C::kWords < 4 ? C::kWords : 4) * 4, 1024, kw[1]);
-#pragma unroll
-          for (int g = 0; g < NG; g++) {
-            float acc[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-              for (int j = 0; j < 4; j++) acc[nt][j] = 0.f;
-#pragma unroll
-            for (int i = g * C::kWpg; i < (g + 1) * C::kWpg; i++) {
-              uint32_t a0[4], a1[4];
-              expand(kw[0][i], a0);
-              expand(kw[1][i], a1);
-#pragma unroll
-              for (int h = 0; h < 2; h++)
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++) {
-                  uint2 b;
-                  if constexpr (NT == 1)
-                    b = qf[2 * i + h];
-                  else
-                    b = s_q[(nt * (HD / 16) + 2 * i + h) * 32 + lane];
-                  mma16816(acc[nt], a0[2 * h], a1[2 * h], a0[2 * h + 1], a1[2 * h + 1], b.x, b.y);
-                  if constexpr (F32) {
-                    const uint2 l = s_q[((NT + nt) * (HD / 16) + 2 * i + h) * 32 + lane];
-                    mma16816(acc[nt], a0[2 * h], a1[2 * h], a0[2 * h + 1], a1[2 * h + 1], l.x, l.y);
-                  }
-                }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-              for (int j = 0; j < 4; j++) {
-                const uint32_t kpar = kp[j >> 1][g];
-                x[nt][j] = fmaf(lo_bf16(kpar), acc[nt][j], fmaf(hi_bf16(kpar), sumq[nt][j & 1][g], x[nt][j]));
-              }
-          }
-        }
-        uint32_t vis = 0xffffffffu;  // bit 4 nt + j: row sees token
-        if (masked) {
-          vis = 0;
-#pragma unroll
-          for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-              const int t = t0 + r + 8 * (j >> 1);
-              const bool see = t <= pos[nt][j & 1] && (a.window <= 0 || t > pos[nt][j & 1] - a.window);
-              if (see)
-                vis |= 1u << (4 * nt + j);
-              else
-                x[nt][j] = -kInf;
-            }
-        }
-        // ---- running maximum: moves only when a score passes it by kSlack ----
-        bool grow = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-          for (int j = 0; j < 4; j++) grow = grow || fmaf(fac[nt][j & 1], x[nt][j], -mf[nt][j & 1]) > kSlack;
-        float top = 0.f;  // largest value scale of the unit
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-#pragma unroll
-          for (int g = 0; g < NG; g++) top = fmaxf(top, lo_bf16(vp[h][g]));
-        grow = grow || (vmul == 0.f ? top > 0.f : top * vmul >= 16384.f);
-        if (__any_sync(0xffffffffu, grow)) {
-          const float seen = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-          float shrink = 1.f;
-          if (seen > 0.f && (vmul == 0.f || seen * vmul >= 16384.f)) {
-            // 2^(13 - floor(log2 seen)): seen * vmul in [2^13, 2^14)
-            const int ex = min(253, max(1, 127 + 13 + 127 - (int)(__float_as_uint(seen) >> 23)));
-            const float now = __uint_as_float((uint32_t)ex << 23);
-            shrink = vmul == 0.f ? 1.f : now / vmul;
-            vmul = now;
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-              float mx = fmaxf(x[nt][e], x[nt][2 + e]);
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              const float now = mx == -kInf ? mf[nt][e] : fmaxf(mf[nt][e], fac[nt][e] * mx);
-              const float f = mf[nt][e] == -kInf ? 1.f : exp2_fast(mf[nt][e] - now);
-              mf[nt][e] = now;
-              lsum[nt][e] *= f;
-#pragma unroll
-              for (int g = 0; g < NG; g++) bias[nt][e][g] *= f;
-#pragma unroll
-              for (int i = 0; i < C::kMt; i++) {
-                o[nt][i][e] *= f * shrink;
-                o[nt][i][2 + e] *= f * shrink;
-              }
-            }
-        }
-        // ---- weights, transposed into B fragments per group ----
-        // A bf16 call's weight enters the product as h = round(a s vmul) in 11 bits. The offset takes the same
-        // rounded weight, as h (o / (s vmul)): rounding it then scales the token's V as a whole, however far o is
-        // from it. The quotient gets a correction step, so that it is exact where V = 0 is. Where the scale is
-        // nothing beside the largest, the offset is V. With the 22 bits of an f32 call's weights a itself serves.
-        float vs[2][NG], vo[2][NG];
-        bool faint[2][NG];
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-#pragma unroll
-          for (int g = 0; g < NG; g++) {
-            vs[h][g] = lo_bf16(vp[h][g]) * vmul;
-            vo[h][g] = hi_bf16(vp[h][g]);
-            faint[h][g] = F32 || vs[h][g] < 9.3132257e-10f;  // 2^-30
-            if (!faint[h][g]) {
-              const float inv = rcp_fast(vs[h][g]), q = vo[h][g] * inv;
-              vo[h][g] = fmaf(fmaf(-q, vs[h][g], vo[h][g]), inv, q);
-            }
-          }
-        uint32_t pb[NT][NG][2], pl[F32 ? NT : 1][NG][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
-          float pr[4];
-#pragma unroll
-          for (int j = 0; j < 4; j++) {
-            pr[j] = exp2_fast(fmaf(fac[nt][j & 1], x[nt][j], -mf[nt][j & 1]));
-            if (masked && !(vis >> (4 * nt + j) & 1)) pr[j] = 0.f;
-          }
-          lsum[nt][0] += pr[0] + pr[2];
-          lsum[nt][1] += pr[1] + pr[3];
-#pragma unroll
-          for (int g = 0; g < NG; g++) {
-            float pv[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) pv[j] = pr[j] * vs[j >> 1][g];
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-              const uint32_t hi = pack_half2(pv[2 * h], pv[2 * h + 1]);
-              const __half2 hh = *reinterpret_cast<const __half2*>(&hi);
-              const float kept[2] = {__low2float(hh), __high2float(hh)};
-              pb[nt][g][h] = transpose8x8(hi);
-              if constexpr (F32) {
-                pl[nt][g][h] = transpose8x8(pack_half2(pv[2 * h] - kept[0], pv[2 * h + 1] - kept[1]));
-              }
-#pragma unroll
-              for (int e = 0; e < 2; e++) {
-                const int j = 2 * h + e;
-                float off = vo[h][g];
-                if (masked && !(vis >> (4 * nt + j) & 1)) off = 0.f;  // an unseen NaN stays unseen
-                bias[nt][e][g] = fmaf(faint[h][g] ? pr[j] : kept[e], off, bias[nt][e][g]);
-              }
-            }
-          }
-        }
-        // ---- output ----
-        {
-          const uint8_t* vb = unit + kv4_v_at(HD, NG) + lane * (C::kWords < 4 ? C::kWords : 4) * 4;
-          uint32_t vw[2][C::kWords];
-          lds_codes(vb, 512, vw[0]);
-          lds_codes(vb + 4 * HD, 512, vw[1]);
-#pragma unroll
-          for (int i = 0; i < C::kWords; i++) {
-            uint32_t a0[4], a1[4];
-            expand(vw[0][i], a0);
-            expand(vw[1][i], a1);
-            const int g = i / C::kWpg;
-#pragma unroll
-            for (int h = 0; h < 2; h++)
-#pragma unroll
-              for (int nt = 0; nt < NT; nt++) {
-                float(&d)[4] = o[nt][2 * i + h];
-                if constexpr (F32) {
-                  // the instruction's own accumulator is cut, not rounded: a unit's sum is formed from zero and
-                  // added in binary32
-                  float t[4] = {0.f, 0.f, 0.f, 0.f};
-                  mma16816(t, a0[2 * h], a0[2 * h + 1], a1[2 * h], a1[2 * h + 1], pl[nt][g][0], pl[nt][g][1]);
-                  mma16816(t, a0[2 * h], a0[2 * h + 1], a1[2 * h], a1[2 * h + 1], pb[nt][g][0], pb[nt][g][1]);
-#pragma unroll
-                  for (int j = 0; j < 4; j++) d[j] += t[j];
-                } else {
-                  mma16816(d, a0[2 * h], a0[2 * h + 1], a1[2 * h], a1[2 * h + 1], pb[nt][g][0], pb[nt][g][1]);
-                }
-              }
-          }
-        }
+        if (t0 + kKvUnit - 1 > pos_min || t0 < lo_max)
+          process(std::true_type{}, unit, t0);
+        else
+          process(std::false_type{}, unit, t0);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_empty[slot]);
@@ -719,7 +782,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
     }
 
     // ---- join the four warps ----
-    const float unscale = vmul == 0.f ? 0.f : 1.f / vmul;
+    const float unscale = (C::kDeq ? 1.f / 8192.f : 1.f) / vmul;  // exact: powers of two
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
@@ -740,7 +803,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         float* dst = s_join + (warp * C::kRows + row) * C::kPad + 2 * r;
 #pragma unroll
         for (int i = 0; i < C::kMt; i++) {
-          const float add = bias[nt][e][(i / 2) / C::kWpg];
+          const float add = C::kDeq ? 0.f : bias[nt][e][(i / 2) / C::kWpg];
           *reinterpret_cast<float2*>(dst + 16 * i) =
               make_float2(fmaf(o[nt][i][e], unscale, add), fmaf(o[nt][i][2 + e], unscale, add));
         }
@@ -792,25 +855,57 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
       }
       named_sync(1, kConsumers);
       if (s_last) {
-        const float* parts = a.part;
-        for (int i = tid; i < row_n * (HD / 4); i += kConsumers) {
-          const int row = i / (HD / 4), d = (i % (HD / 4)) * 4;
-          float mm = -kInf, l = 0.f;
-          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int k = c0; k <= c1; k++) {
-            const float* pk = parts + (size_t)(2 * k + (k == c0)) * C::kRows * (HD + 2);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pk + C::kRows * HD + 2 * row));
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(pk + row * HD + d));
-            const float now = fmaxf(mm, ml.x);
-            const float fo = mm == -kInf ? 0.f : exp2_fast(mm - now), fn = ml.x == -kInf ? 0.f : exp2_fast(ml.x - now);
-            const float gn = ml.y == ml.y ? fn : 1.f, go = l == l ? fo : 1.f;
-            mm = now;
-            l = l * go + ml.y * gn;
-            y.x = y.x * go + v.x * gn, y.y = y.y * go + v.y * gn, y.z = y.z * go + v.z * gn, y.w = y.w * go + v.w * gn;
+        // kBatch parts at a time: their maxima and sums go to shared memory, as weights beside the batch's maximum;
+        // then every load of the outputs is independent of the others.
+        constexpr int kBatch = 64;
+        static_assert(2 * kBatch * C::kRows * 4 <= C::kJoin, "the join buffer holds a batch");
+        constexpr int kItems = (C::kRows * (HD / 4) + kConsumers - 1) / kConsumers;
+        float* s_pm = s_join;  // [kBatch][kRows] maxima, then sums
+        float* s_pl = s_join + kBatch * C::kRows;
+        float mm[kItems], ll[kItems];
+        float4 y[kItems];
+#pragma unroll
+        for (int k = 0; k < kItems; k++) mm[k] = -kInf, ll[k] = 0.f, y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int from = c0; from <= c1; from += kBatch) {
+          const int n = min(kBatch, c1 - from + 1);
+          named_sync(1, kConsumers);
+          for (int i = tid; i < n * C::kRows; i += kConsumers) {
+            const int k = from + i / C::kRows;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part + (size_t)(2 * k + (k == c0)) * C::kRows * (HD + 2) +
+                                                                     C::kRows * HD + 2 * (i % C::kRows)));
+            s_pm[i] = ml.x;
+            s_pl[i] = ml.y;
           }
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          store4<F32>(a.out, out_at(row) + d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv), a.vec_out);
+          named_sync(1, kConsumers);
+#pragma unroll
+          for (int q = 0; q < kItems; q++) {
+            const int i = tid + q * kConsumers, row = i / (HD / 4), d = (i % (HD / 4)) * 4;
+            if (row >= row_n) continue;
+            float now = mm[q];
+            for (int k = 0; k < n; k++) now = fmaxf(now, s_pm[k * C::kRows + row]);
+            const float fo = mm[q] == -kInf ? 0.f : exp2_fast(mm[q] - now), go = ll[q] == ll[q] ? fo : 1.f;
+            mm[q] = now;
+            ll[q] *= go;
+            y[q].x *= go, y[q].y *= go, y[q].z *= go, y[q].w *= go;
+#pragma unroll 8
+            for (int k = 0; k < n; k++) {
+              const int kk = from + k;
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(
+                  a.part + (size_t)(2 * kk + (kk == c0)) * C::kRows * (HD + 2) + row * HD + d));
+              const float pm = s_pm[k * C::kRows + row], pl = s_pl[k * C::kRows + row];
+              const float f = pl != pl ? 1.f : pm == -kInf ? 0.f : exp2_fast(pm - now);
+              ll[q] = fmaf(pl, f, ll[q]);
+              y[q].x = fmaf(v.x, f, y[q].x), y[q].y = fmaf(v.y, f, y[q].y);
+              y[q].z = fmaf(v.z, f, y[q].z), y[q].w = fmaf(v.w, f, y[q].w);
+            }
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kItems; q++) {
+          const int i = tid + q * kConsumers, row = i / (HD / 4), d = (i % (HD / 4)) * 4;
+          if (row >= row_n) continue;
+          const float inv = ll[q] == 0.f ? 0.f : 1.f / ll[q];
+          store4<F32>(a.out, out_at(row) + d, make_float4(y[q].x * inv, y[q].y * inv, y[q].z * inv, y[q].w * inv), a.vec_out);
         }
       }
     }
@@ -851,11 +946,9 @@ template <int HD, int NG, bool F32>
 int launch_rows(coli_ctx* ctx, AttnArgs& a) {
   const long long rows = (long long)((a.p.T + a.p.B - 1) / a.p.B) * a.group;
   const long long width = ((long long)a.p.table_stride << a.c.page_log2) / kStageTok + 1;
-  constexpr int kWide = F32 || HD == 256 ? 2 : 4;
   auto most = [&](int nt) { return ((long long)a.p.T * a.group / (8 * nt) + a.p.B) * a.c.heads * width; };
   if (rows <= 8) return launch_one<HD, NG, 1, F32>(ctx, a, most(1));
-  if (rows <= 16 || kWide == 2) return launch_one<HD, NG, 2, F32>(ctx, a, most(2));
-  return launch_one<HD, NG, kWide, F32>(ctx, a, most(kWide));
+  return launch_one<HD, NG, 2, F32>(ctx, a, most(2));
 }
 
 template <bool F32>
