@@ -43,6 +43,7 @@ constexpr int kAttnThreads = kConsumers + 32;
 // below 2^kSlack.
 constexpr float kSlack = 1.f;
 constexpr float kInf = __builtin_huge_valf();
+constexpr int kGroup = 8;  // parts summed at once
 // Query rows per sequence and key/value head, on average, from which the 256-row tiles of kv4_tile.cu take over.
 constexpr int kTileFrom = 96;
 
@@ -221,7 +222,7 @@ struct AttnArgs {
   bool vec;       // q rows start at 16-byte boundaries
   bool vec_out;   // out rows start at a boundary of four values
   float* part;    // partial results: 2 per CTA, each kRows x HD outputs and kRows (maximum, sum) pairs
-  int* count;     // one per CTA: parts of the item that starts in it which have arrived
+  int* count;     // arrivals: 2 per CTA for the run of parts whose sum its slot takes, then 1 per CTA for the runs of an item
   int* err;
   uint64_t wait_ns;
 };
@@ -256,7 +257,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
   __shared__ __align__(8) uint64_t s_full[C::kStages], s_empty[C::kStages];
   __shared__ long long s_sum[kAttnThreads / 32];
   __shared__ long long s_at;
-  __shared__ int s_start, s_last;
+  __shared__ int s_last;
+  __shared__ Item s_item;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -265,21 +267,21 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
       mbar_init(&s_empty[i], kStageUnits);
     }
     mbar_fence_init();
-    s_start = a.p.B;
   }
   griddep_launch_dependents();
   griddep_wait();
 
   // ---- deal the stages out: total, then the sequence in which this CTA's share starts ----
   const int heads = a.c.heads;
+  Item t;
   auto stages_in = [&](int b) -> long long {
-    Item t;
     t.b = b;
     load_seq(a.c, a.p, a.window, t, a.err);
     return (long long)tiles_of(t.m, a.group, C::kRows) * heads * t.stages;
   };
-  long long total = 0;
-  for (int b = tid; b < a.p.B; b += kAttnThreads) total += stages_in(b);
+  long long total = 0, own = 0;
+  for (int b = tid; b < a.p.B; b += kAttnThreads) total += own = stages_in(b);
+  const bool once = a.p.B <= kAttnThreads;  // then a thread still has its sequence
   for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   if (lane == 0) s_sum[warp] = total;
   __syncthreads();
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
   long long before = 0;
   for (int base = 0; base < a.p.B; base += kAttnThreads) {
     const int b = base + tid;
-    const long long mine = b < a.p.B ? stages_in(b) : 0;
+    const long long mine = once ? own : b < a.p.B ? stages_in(b) : 0;
     long long inc = mine;
     for (int o = 1; o < 32; o <<= 1) {
       const long long n = __shfl_up_sync(0xffffffffu, inc, o);
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
     }
     const long long start = off + inc - mine;
     if (mine > 0 && start <= w0 && w0 < start + mine) {
-      s_start = b;
+      s_item = t;
       s_at = start;
     }
     before += all;
@@ -316,9 +318,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
   __syncthreads();
 
   // ---- the cursor that producer and consumers walk on their own ----
-  Item it;
-  it.b = s_start;
-  load_seq(a.c, a.p, a.window, it, a.err);
+  Item it = s_item;
   const long long local = w0 - s_at;  // stages of this sequence before the share
   const int tiles0 = tiles_of(it.m, a.group, C::kRows);
   const long long item0 = local / it.stages;
@@ -844,62 +844,82 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
       }
     }
     if (!whole) {
-      const int c0 = (int)(item_at / per), c1 = (int)((item_at + it.stages - 1) / per);
-      __threadfence();
-      named_sync(1, kConsumers);
-      if (tid == 0) {
-        const int old = atomicAdd(a.count + c0, 1);
-        s_last = old == c1 - c0;
-        if (old == c1 - c0) atomicExch(a.count + c0, 0);  // as the next launch expects it
+      // Parts are summed in CTA order, in two levels where there are many: the last to arrive of each run of kGroup
+      // CTAs sums the run into its first slot, the last run to arrive sums the runs. Every load of a level is
+      // independent of the others.
+      const int c0 = (int)(item_at / per), c1 = (int)((item_at + it.stages - 1) / per), parts = c1 - c0 + 1;
+      const int me = blockIdx.x, lead = parts > kGroup ? c0 + (me - c0) / kGroup * kGroup : c0;
+      const int runs = parts > kGroup ? (parts + kGroup - 1) / kGroup : 1;
+      const int run = min(kGroup, c1 - lead + 1);  // parts of this CTA's run
+      constexpr int kItems = (C::kRows * (HD / 4) + kConsumers - 1) / kConsumers;
+      auto slot_of = [&](int k) { return a.part + (size_t)(2 * k + (k == c0)) * C::kRows * (HD + 2); };
+      auto last_of = [&](int* count, int n) {  // this CTA's parts are written; true in the last of n to say so
         __threadfence();
-      }
-      named_sync(1, kConsumers);
-      if (s_last) {
-        // kBatch parts at a time: their maxima and sums go to shared memory, as weights beside the batch's maximum;
-        // then every load of the outputs is independent of the others.
-        constexpr int kBatch = 64;
-        static_assert(2 * kBatch * C::kRows * 4 <= C::kJoin, "the join buffer holds a batch");
-        constexpr int kItems = (C::kRows * (HD / 4) + kConsumers - 1) / kConsumers;
-        float* s_pm = s_join;  // [kBatch][kRows] maxima, then sums
-        float* s_pl = s_join + kBatch * C::kRows;
-        float mm[kItems], ll[kItems];
-        float4 y[kItems];
+        named_sync(1, kConsumers);
+        if (tid == 0) {
+          const int old = atomicAdd(count, 1);
+          s_last = old == n - 1;
+          if (old == n - 1) atomicExch(count, 0);  // as the next launch expects it
+          __threadfence();
+        }
+        named_sync(1, kConsumers);
+        return s_last != 0;
+      };
+      // the sum of n slots, from `from` on, `step` CTAs apart: maximum, sum and output of this thread's values
+      float mm[kItems], ll[kItems];
+      float4 y[kItems];
+      auto gather = [&](int from, int step, int n) {
 #pragma unroll
-        for (int k = 0; k < kItems; k++) mm[k] = -kInf, ll[k] = 0.f, y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int from = c0; from <= c1; from += kBatch) {
-          const int n = min(kBatch, c1 - from + 1);
-          named_sync(1, kConsumers);
-          for (int i = tid; i < n * C::kRows; i += kConsumers) {
-            const int k = from + i / C::kRows;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part + (size_t)(2 * k + (k == c0)) * C::kRows * (HD + 2) +
-                                                                     C::kRows * HD + 2 * (i % C::kRows)));
-            s_pm[i] = ml.x;
-            s_pl[i] = ml.y;
-          }
-          named_sync(1, kConsumers);
+        for (int q = 0; q < kItems; q++) {
+          const int i = tid + q * kConsumers, row = i / (HD / 4), d = (i % (HD / 4)) * 4;
+          mm[q] = -kInf, ll[q] = 0.f, y[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (row >= row_n) continue;
+          for (int k0 = 0; k0 < n; k0 += kGroup) {
+            float2 ml[kGroup];
+            float4 v[kGroup];
 #pragma unroll
-          for (int q = 0; q < kItems; q++) {
-            const int i = tid + q * kConsumers, row = i / (HD / 4), d = (i % (HD / 4)) * 4;
-            if (row >= row_n) continue;
+            for (int k = 0; k < kGroup; k++)
+              if (k0 + k < n) {
+                const float* p = slot_of(from + (k0 + k) * step);
+                ml[k] = __ldcg(reinterpret_cast<const float2*>(p + C::kRows * HD + 2 * row));
+                v[k] = __ldcg(reinterpret_cast<const float4*>(p + row * HD + d));
+              } else {
+                ml[k] = make_float2(-kInf, 0.f);
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+              }
             float now = mm[q];
-            for (int k = 0; k < n; k++) now = fmaxf(now, s_pm[k * C::kRows + row]);
-            const float fo = mm[q] == -kInf ? 0.f : exp2_fast(mm[q] - now), go = ll[q] == ll[q] ? fo : 1.f;
+#pragma unroll
+            for (int k = 0; k < kGroup; k++) now = fmaxf(now, ml[k].x);
+            const float go = ll[q] != ll[q] ? 1.f : mm[q] == -kInf ? 0.f : exp2_fast(mm[q] - now);
             mm[q] = now;
             ll[q] *= go;
             y[q].x *= go, y[q].y *= go, y[q].z *= go, y[q].w *= go;
-#pragma unroll 8
-            for (int k = 0; k < n; k++) {
-              const int kk = from + k;
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                  a.part + (size_t)(2 * kk + (kk == c0)) * C::kRows * (HD + 2) + row * HD + d));
-              const float pm = s_pm[k * C::kRows + row], pl = s_pl[k * C::kRows + row];
-              const float f = pl != pl ? 1.f : pm == -kInf ? 0.f : exp2_fast(pm - now);
-              ll[q] = fmaf(pl, f, ll[q]);
-              y[q].x = fmaf(v.x, f, y[q].x), y[q].y = fmaf(v.y, f, y[q].y);
-              y[q].z = fmaf(v.z, f, y[q].z), y[q].w = fmaf(v.w, f, y[q].w);
+#pragma unroll
+            for (int k = 0; k < kGroup; k++) {
+              const float f = ml[k].y != ml[k].y ? 1.f : ml[k].x == -kInf ? 0.f : exp2_fast(ml[k].x - now);
+              ll[q] = fmaf(ml[k].y, f, ll[q]);
+              y[q].x = fmaf(v[k].x, f, y[q].x), y[q].y = fmaf(v[k].y, f, y[q].y);
+              y[q].z = fmaf(v[k].z, f, y[q].z), y[q].w = fmaf(v[k].w, f, y[q].w);
             }
           }
         }
+      };
+      bool final = last_of(a.count + 2 * lead + (lead == c0), run);
+      if (final && runs > 1) {
+        gather(lead, 1, run);
+        named_sync(1, kConsumers);  // everyone has read the slot that the sum goes to
+        float* p = slot_of(lead);
+#pragma unroll
+        for (int q = 0; q < kItems; q++) {
+          const int i = tid + q * kConsumers, row = i / (HD / 4), d = (i % (HD / 4)) * 4;
+          if (row >= row_n) continue;
+          __stcg(reinterpret_cast<float4*>(p + row * HD + d), y[q]);
+          if (d == 0) __stcg(reinterpret_cast<float2*>(p + C::kRows * HD + 2 * row), make_float2(mm[q], ll[q]));
+        }
+        final = last_of(a.count + 2 * gridDim.x + c0, runs);
+      }
+      if (final) {
+        gather(c0, runs > 1 ? kGroup : 1, runs > 1 ? runs : run);
 #pragma unroll
         for (int q = 0; q < kItems; q++) {
           const int i = tid + q * kConsumers, row = i / (HD / 4), d = (i % (HD / 4)) * 4;
@@ -922,7 +942,7 @@ int launch_one(coli_ctx* ctx, AttnArgs& a, long long most_stages) {
   using C = Cfg<HD, NG, NT, F32>;
   int grid = ctx->num_sms * C::kCtas;
   if (most_stages < grid) grid = (int)most_stages;
-  if (grid > kKvCounters) grid = kKvCounters;
+  if (grid > kKvCounters / 3) grid = kKvCounters / 3;
   int rc = ensure_workspace(ctx, (size_t)2 * grid * C::kRows * (HD + 2) * sizeof(float));
   if (rc != COLI_OK) return rc;
   a.part = reinterpret_cast<float*>(ctx->ws.base);
