@@ -60,6 +60,10 @@ struct Cfg {
   // Values enter the product dequantised where several tiles of rows share the work of it (bf16: 11 bits); otherwise as
   // codes, with a group's scale on the weight.
   static constexpr bool kDeq = !F32 && NT > 1;
+  // Value codes enter as they lie (0..15), which needs the sums cut short: the instruction cuts its accumulator off
+  // instead of rounding it, and codes that are not centred make the sum large beside the result.
+  static constexpr bool kRawV = !F32 && NT == 1;
+  static constexpr int kSumUnits = 64;  // units after which a sum moves to shared memory
   static constexpr int kCtas = HD == 256 ? (NT == 1 ? 2 : 1) : NT == 1 ? 3 : 2;  // resident per SM (registers)
   static constexpr uint32_t kJoin = kStageUnits * kRows * (kPad + 2) * 4;
   static constexpr uint32_t kQ = NT * (HD / 16) * 32 * 8 * (F32 ? 2 : 1);
@@ -110,6 +114,16 @@ __device__ __forceinline__ void expand(uint32_t w, uint32_t (&a)[4]) {
     const __half2 v = (i & 1) ? __hfma2(h, sixteenth, bias16) : __hsub2(h, bias);
     a[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
+}
+
+// The same pairs as they lie, one logic operation each: a nibble at the end of a 16-bit float's mantissa is the
+// subnormal number n 2^-24, at bit 4 n 2^-20, and the matrix instruction takes subnormal operands at full precision.
+__device__ __forceinline__ void expand_raw(uint32_t w, uint32_t (&a)[4]) {
+  const uint32_t w8 = w >> 8;
+  a[0] = w & 0x000f000fu;
+  a[1] = w & 0x00f000f0u;
+  a[2] = w8 & 0x000f000fu;
+  a[3] = w8 & 0x00f000f0u;
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -455,9 +469,10 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
         sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
 #pragma unroll
-        for (int e = 0; e < 2; e++) sumq[nt][e][g] = __shfl_sync(0xffffffffu, sum[g], (2 * cc + e) * 4);
+        for (int e = 0; e < 2; e++) sumq[nt][e][g] = 5.9604645e-8f * __shfl_sync(0xffffffffu, sum[g], (2 * cc + e) * 4);
       }
-      const float f = fmaxf(fabsf(a.scale) * 1.4426950408889634f * inv, 1e-37f);  // not 0: minus infinity stays it
+      // scores come in units of 2^-24 (expand_raw); not 0: minus infinity stays it
+      const float f = fmaxf(fabsf(a.scale) * 1.4426950408889634f * inv * 16777216.f, 1e-37f);
 #pragma unroll
       for (int e = 0; e < 2; e++) {
         fac[nt][e] = __shfl_sync(0xffffffffu, f, (2 * cc + e) * 4);
@@ -472,13 +487,15 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         for (int h = 0; h < 2; h++) {
           if ((2 * i + h) % kStageUnits != warp) continue;
           const int at = (nt * (HD / 16) + 2 * i + h) * 32 + lane;
-          const uint32_t b0 = pack_half2(v[i][2 * h], v[i][2 * h + 4]), b1 = pack_half2(v[i][2 * h + 1], v[i][2 * h + 5]);
+          // codes at bit 4 count sixteenfold (expand_raw)
+          const float v1 = v[i][2 * h + 1] * 0.0625f, v5 = v[i][2 * h + 5] * 0.0625f;
+          const uint32_t b0 = pack_half2(v[i][2 * h], v[i][2 * h + 4]), b1 = pack_half2(v1, v5);
           s_q[at] = make_uint2(b0, b1);
           if constexpr (F32) {
             const __half2 h0 = *reinterpret_cast<const __half2*>(&b0), h1 = *reinterpret_cast<const __half2*>(&b1);
             s_q[NT * (HD / 16) * 32 + at] =
                 make_uint2(pack_half2(v[i][2 * h] - __low2float(h0), v[i][2 * h + 4] - __high2float(h0)),
-                           pack_half2(v[i][2 * h + 1] - __low2float(h1), v[i][2 * h + 5] - __high2float(h1)));
+                           pack_half2(v1 - __low2float(h1), v5 - __high2float(h1)));
           }
         }
     }
@@ -506,7 +523,9 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
     }
     // value scales (dequantised: values) are multiplied by vmul, a power of two that keeps them below 2^14; it
     // only shrinks, and the outputs with it.
-    float vmul = __uint_as_float(253u << 23);
+    float vmul = __uint_as_float(253u << 23), eight = 0.f;  // eight: 8 / vmul
+    bool stashed = false;                                  // part of the sums lies in the join buffer
+    float* stash = s_join + warp * C::kRows * C::kPad + 2 * r;
     const int pos_min = it.len - it.m + tile_row / a.group;  // first row's position
     const int pos_max = it.len - it.m + (tile_row + row_n - 1) / a.group;
     const int lo_max = a.window > 0 ? pos_max - a.window + 1 : 0;
@@ -542,8 +561,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
 #pragma unroll
           for (int i = g * C::kWpg; i < (g + 1) * C::kWpg; i++) {
             uint32_t a0[4], a1[4];
-            expand(kw[0][i], a0);
-            expand(kw[1][i], a1);
+            expand_raw(kw[0][i], a0);
+            expand_raw(kw[1][i], a1);
 #pragma unroll
             for (int h = 0; h < 2; h++)
 #pragma unroll
@@ -563,7 +582,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
                 }
               }
           }
-          const float ks[2] = {lo_bf16(kp[0][g]), lo_bf16(kp[1][g])}, ko[2] = {hi_bf16(kp[0][g]), hi_bf16(kp[1][g])};
+          const float ks[2] = {lo_bf16(kp[0][g]), lo_bf16(kp[1][g])};
+          const float ko[2] = {fmaf(-8.f, ks[0], hi_bf16(kp[0][g])), fmaf(-8.f, ks[1], hi_bf16(kp[1][g]))};  // of code 0
 #pragma unroll
           for (int nt = 0; nt < NT; nt++)
 #pragma unroll
@@ -617,6 +637,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
           const float now = __uint_as_float((uint32_t)ex << 23);
           shrink = now / vmul;
           vmul = now;
+          eight = 8.f / vmul;
         }
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
@@ -636,6 +657,13 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
             for (int i = 0; i < C::kMt; i++) {
               o[nt][i][e] *= f * shrink;
               o[nt][i][2 + e] *= f * shrink;
+            }
+            if (C::kRawV && stashed) {
+#pragma unroll 1
+              for (int i = 0; i < C::kMt; i++) {
+                float2* at = reinterpret_cast<float2*>(stash + (nt * 8 + 2 * cc + e) * C::kPad + 16 * i);
+                *at = make_float2(at->x * (f * shrink), at->y * (f * shrink));
+              }
             }
 #pragma unroll
             for (int j = e; j < 4; j += 2) y[nt][j] = fmaf(fac[nt][e], x[nt][j], -now);
@@ -677,7 +705,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
             faint[h] = F32 || vs[h] < 9.3132257e-10f;  // 2^-30
             if (!F32) {
               const float inv = rcp_fast(vs[h]), q = vo[h] * inv;
-              const float quotient = fmaf(fmaf(-q, vs[h], vo[h]), inv, q);
+              const float quotient = fmaf(fmaf(-q, vs[h], vo[h]), inv, q) - eight;  // of code 0
               vo[h] = faint[h] ? vo[h] : quotient;
             }
           }
@@ -727,8 +755,13 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         for (int i = 0; i < C::kWords; i++) {
           const int g = i / C::kWpg;
           uint32_t a0[4], a1[4];
-          expand(vw[0][i], a0);
-          expand(vw[1][i], a1);
+          if constexpr (C::kRawV) {
+            expand_raw(vw[0][i], a0);
+            expand_raw(vw[1][i], a1);
+          } else {
+            expand(vw[0][i], a0);
+            expand(vw[1][i], a1);
+          }
           if constexpr (C::kDeq) {
 #pragma unroll
             for (int m = 0; m < 4; m++) {
@@ -773,6 +806,20 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         else
           process(std::false_type{}, unit, t0);
       }
+      if (C::kRawV && n % C::kSumUnits == C::kSumUnits - 1) {
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int e = 0; e < 2; e++)
+#pragma unroll
+            for (int i = 0; i < C::kMt; i++) {
+              float2* at = reinterpret_cast<float2*>(stash + (nt * 8 + 2 * cc + e) * C::kPad + 16 * i);
+              const float2 had = stashed ? *at : make_float2(0.f, 0.f);
+              *at = make_float2(had.x + o[nt][i][e], had.y + o[nt][i][2 + e]);
+              o[nt][i][e] = o[nt][i][2 + e] = 0.f;
+            }
+        stashed = true;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_empty[slot]);
       if (++slot == C::kStages) {
@@ -782,7 +829,9 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
     }
 
     // ---- join the four warps ----
-    const float unscale = (C::kDeq ? 1.f / 8192.f : 1.f) / vmul;  // exact: powers of two
+    // exact: powers of two; the channels whose codes lie at bit 4 count sixteenfold
+    const float unscale = (C::kDeq ? 1.f / 8192.f : C::kRawV ? 16777216.f : 1.f) / vmul;
+    const float unscale1 = C::kRawV ? unscale * 0.0625f : unscale;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
@@ -804,8 +853,9 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
 #pragma unroll
         for (int i = 0; i < C::kMt; i++) {
           const float add = C::kDeq ? 0.f : bias[nt][e][(i / 2) / C::kWpg];
-          *reinterpret_cast<float2*>(dst + 16 * i) =
-              make_float2(fmaf(o[nt][i][e], unscale, add), fmaf(o[nt][i][2 + e], unscale, add));
+          float2* at = reinterpret_cast<float2*>(dst + 16 * i);
+          const float2 had = C::kRawV && stashed ? *at : make_float2(0.f, 0.f);
+          *at = make_float2(fmaf(had.x + o[nt][i][e], unscale, add), fmaf(had.y + o[nt][i][2 + e], unscale1, add));
         }
       }
     named_sync(1, kConsumers);
