@@ -414,8 +414,8 @@ COLI_API int coli_kv4_read(coli_ctx *ctx, const coli_kv4_cache *cache, void *k, 
  * q, out: [T x q_heads x head_dim] in dtype, rows q_stride / out_stride elements apart; q_heads a
  * multiple of heads, at most COLI_MAX_KV_GROUP times it; scale finite; out must not overlap q.
  * Scores, the softmax's maximum and sum, and the output are held in binary32 (bf16 queries: weights
- * enter the product with V in 11 bits; f32: queries and weights in 22; weights below 2^-38 of a row's
- * largest count as nothing). Results do not change from run to run. A non-finite query sets COLI_E_NONFINITE and gives NaN in its row.
+ * enter the product with V in 11 bits; f32: queries and weights in 22; what weighs less than 2^-32 of a
+ * row's heaviest value may count as nothing). Results do not change from run to run. A non-finite query sets COLI_E_NONFINITE and gives NaN in its row.
  * Profiled as COLI_KERNEL_ATTENTION.
  */
 COLI_API int coli_kv4_attention(coli_ctx *ctx, const coli_kv4_cache *cache, const void *q, long long q_stride,

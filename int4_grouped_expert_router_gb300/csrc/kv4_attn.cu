@@ -39,9 +39,11 @@ constexpr int kStageUnits = 4;                    // consumer warps, and units o
 constexpr int kStageTok = kStageUnits * kKvUnit;  // tokens of a stage
 constexpr int kConsumers = kStageUnits * 32;
 constexpr int kAttnThreads = kConsumers + 32;
-// A row's running maximum follows the scores only when one exceeds it by this much (log2): weights stay
-// below 2^kSlack.
-constexpr float kSlack = 1.f;
+// A row's running maximum follows the scores only when one exceeds it by this much (log2), so weights stay below
+// 2^kSlack: moving it costs a pass over the unit's sums, and at kSlack = 1 did so often enough to take a fifth of
+// the time. The scales (or values) that a weight meets in 16 bits are kept below 2^9.
+constexpr float kSlack = 6.f;
+constexpr float kTopScale = 512.f;
 constexpr float kInf = __builtin_huge_valf();
 constexpr int kGroup = 8;  // parts summed at once
 // Query rows per sequence and key/value head, on average, from which the 256-row tiles of kv4_tile.cu take over.
@@ -63,6 +65,7 @@ struct Cfg {
   // Value codes enter as they lie (0..15), which needs the sums cut short: the instruction cuts its accumulator off
   // instead of rounding it, and codes that are not centred make the sum large beside the result.
   static constexpr bool kRawV = !F32 && NT == 1;
+  static constexpr float kTop = kDeq ? 16384.f : kTopScale;  // dequantised values and weights are rounded apart
   static constexpr int kSumUnits = 64;  // units after which a sum moves to shared memory
   static constexpr int kCtas = HD == 256 ? (NT == 1 ? 2 : 1) : NT == 1 ? 3 : 2;  // resident per SM (registers)
   static constexpr uint32_t kJoin = kStageUnits * kRows * (kPad + 2) * 4;
@@ -353,46 +356,62 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
 
   if (warp == kStageUnits) {
     // ------------------------------------ producer ------------------------------------
+    // A lane per stage, several stages at a time: their page numbers are one round trip, and each lane issues as
+    // soon as its slot is free.
     const uint64_t policy = l2_evict_first_policy();
     const int page_tok = 1 << a.c.page_log2;
-    int cached_b = -1, cached_from = 0, pages = 0;  // this lane's entry of 32 consecutive page numbers
+    const int per_copy = min(kStageUnits, page_tok / kKvUnit);  // units
+    const size_t page_bytes = (size_t)heads * (page_tok / kKvUnit) * C::kUnit;
     int slot = 0;
     uint32_t phase = 1;
-    while (w < w1) {
-      const int tok = (it.first + stage) * kStageTok;
-      const int units = min(kStageUnits, max(0, (it.len - tok + kKvUnit - 1) / kKvUnit));
-      const int page = tok >> a.c.page_log2;
-      const int copies = page_tok >= kStageTok ? (units > 0) : (units * kKvUnit + page_tok - 1) >> a.c.page_log2;
-      if (copies > 0 && (it.b != cached_b || page < cached_from || page + copies > cached_from + 32)) {
-        cached_b = it.b;
-        cached_from = page;
-        const int at = page + lane;
-        pages = at < a.p.table_stride ? __ldcg(a.p.table + (size_t)it.b * a.p.table_stride + at) : 0;
-      }
-      if (!mbar_wait_suspend(&s_empty[slot], phase, a.wait_ns)) {
-        if (lane == 0) set_error(a.err, COLI_E_TIMEOUT);
-        break;  // what was issued is still awaited by the consumers
-      }
-      if (lane == 0) mbar_arrive_expect_tx(&s_full[slot], units * C::kUnit);
-      __syncwarp();
-      int pg = __shfl_sync(0xffffffffu, pages, (page - cached_from + lane) & 31);
-      if (lane < copies) {
+    bool lost = false;
+    while (w < w1 && !lost) {
+      const int n = (int)min((long long)min(C::kStages, it.stages - stage), w1 - w);
+      const int tok = (it.first + stage + lane) * kStageTok;
+      const int units = lane < n ? min(kStageUnits, max(0, (it.len - tok + kKvUnit - 1) / kKvUnit)) : 0;
+      const uint8_t* src[kStageUnits];
+#pragma unroll
+      for (int k = 0; k < kStageUnits; k++) {
+        if (k * per_copy >= units) continue;
+        const int at = tok + k * per_copy * kKvUnit;
+        int pg = __ldcg(a.p.table + (size_t)it.b * a.p.table_stride + (at >> a.c.page_log2));
         if (pg < 0 || pg >= a.c.pages) {
           set_error(a.err, COLI_E_RANGE);
           pg = 0;  // some page of the cache in its place
         }
-        const int per_copy = page_tok >= kStageTok ? kStageUnits : page_tok / kKvUnit;  // units
-        const int n = min(per_copy, units - lane * per_copy);
-        const uint8_t* src = a.c.base + (((size_t)pg * heads + it.head) * (size_t)(page_tok / kKvUnit) +
-                                         (tok & (page_tok - 1)) / kKvUnit) * C::kUnit;
-        bulk_g2s_stream(ring + slot * C::kStage + lane * per_copy * C::kUnit, src, n * C::kUnit, &s_full[slot], policy);
+        src[k] = a.c.base + pg * page_bytes + (uint32_t)(it.head * (page_tok / kKvUnit) + (at & (page_tok - 1)) / kKvUnit) * C::kUnit;
       }
-      if (++slot == C::kStages) {
-        slot = 0;
+      int mine = slot + lane;
+      uint32_t my_phase = phase;
+      if (mine >= C::kStages) {
+        mine -= C::kStages;
+        my_phase ^= 1;
+      }
+      bool done = lane >= n;
+      const uint64_t t0 = globaltimer_ns();
+      while (!done) {
+        if (mbar_test_wait(&s_empty[mine], my_phase)) {
+          mbar_arrive_expect_tx(&s_full[mine], units * C::kUnit);
+#pragma unroll
+          for (int k = 0; k < kStageUnits; k++)
+            if (k * per_copy < units)
+              bulk_g2s_stream(ring + mine * C::kStage + k * per_copy * C::kUnit, src[k],
+                              min(per_copy, units - k * per_copy) * C::kUnit, &s_full[mine], policy);
+          done = true;
+        } else if (globaltimer_ns() - t0 > a.wait_ns) {
+          set_error(a.err, COLI_E_TIMEOUT);
+          lost = done = true;  // what was issued is still awaited by the consumers
+        }
+      }
+      lost = __any_sync(0xffffffffu, lost);
+      slot += n;
+      if (slot >= C::kStages) {
+        slot -= C::kStages;
         phase ^= 1;
       }
-      w++;
-      if (++stage == it.stages) {
+      w += n;
+      stage += n;
+      if (stage == it.stages) {
         stage = 0;
         if (w < w1) next_item();
       }
@@ -521,8 +540,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         for (int g = 0; g < NG; g++) bias[nt][e][g] = 0.f;
       }
     }
-    // value scales (dequantised: values) are multiplied by vmul, a power of two that keeps them below 2^14; it
-    // only shrinks, and the outputs with it.
+    // value scales (dequantised: values) are multiplied by vmul, a power of two that keeps them below kTop; it only
+    // shrinks, and the outputs with it.
     float vmul = __uint_as_float(253u << 23), eight = 0.f;  // eight: 8 / vmul
     bool stashed = false;                                  // part of the sums lies in the join buffer
     float* stash = s_join + warp * C::kRows * C::kPad + 2 * r;
@@ -628,12 +647,12 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
 #pragma unroll
         for (int g = 0; g < NG; g++)
           top = fmaxf(top, C::kDeq ? fmaf(8.f, lo_bf16(vp[h][g]), fabsf(hi_bf16(vp[h][g]))) : lo_bf16(vp[h][g]));
-      if (__any_sync(0xffffffffu, most > kSlack || top * vmul >= 16384.f)) {
+      if (__any_sync(0xffffffffu, most > kSlack || top * vmul >= C::kTop)) {
         const float seen = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
         float shrink = 1.f;
-        if (seen * vmul >= 16384.f) {
-          // 2^(13 - floor(log2 seen)): seen * vmul in [2^13, 2^14)
-          const int ex = min(253, max(1, 127 + 13 + 127 - (int)(__float_as_uint(seen) >> 23)));
+        if (seen * vmul >= C::kTop) {
+          // the power of two that brings seen into the upper half of [0, kTop)
+          const int ex = min(253, max(1, (int)(__float_as_uint(C::kTop) >> 23) - 1 + 127 - (int)(__float_as_uint(seen) >> 23)));
           const float now = __uint_as_float((uint32_t)ex << 23);
           shrink = now / vmul;
           vmul = now;
@@ -688,7 +707,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-          for (int h = 0; h < 2; h++) pb[nt][0][h] = transpose8x8(pack_half2(pr[nt][2 * h] * 8192.f, pr[nt][2 * h + 1] * 8192.f));
+          for (int h = 0; h < 2; h++) pb[nt][0][h] = transpose8x8(pack_half2(pr[nt][2 * h] * kTopScale, pr[nt][2 * h + 1] * kTopScale));
       } else {
         // A bf16 call's weight enters the product as h = round(a s vmul) in 11 bits. The offset takes the same
         // rounded weight, as h (o / (s vmul)): rounding it then scales the token's V as a whole, however far o is
@@ -830,7 +849,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
 
     // ---- join the four warps ----
     // exact: powers of two; the channels whose codes lie at bit 4 count sixteenfold
-    const float unscale = (C::kDeq ? 1.f / 8192.f : C::kRawV ? 16777216.f : 1.f) / vmul;
+    const float unscale = (C::kDeq ? 1.f / kTopScale : C::kRawV ? 16777216.f : 1.f) / vmul;
     const float unscale1 = C::kRawV ? unscale * 0.0625f : unscale;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)

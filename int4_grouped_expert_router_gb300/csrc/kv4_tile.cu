@@ -15,7 +15,7 @@
 //                 stage's largest key (value) below 2^14, so that no size of the keys and values is lost.
 //   MMA           one thread: S_x = Q_x K^T, O_x += P_x V for the two halves x of 128 rows
 //   2 x 4 softmax a thread per row: running maximum (it moves only when passed by kSlack), weights
-//                 p = 2^(y - m + 13) in 16 bits, written over S in tensor memory as the next product's operand
+//                 p = 2^(y - m + 9) in 16 bits, written over S in tensor memory as the next product's operand
 // While one half's softmax runs, the tensor core works on the other half. Tensor memory is full: S (128
 // columns) and O (hd columns) of both halves.
 //
@@ -44,8 +44,8 @@ constexpr int kTileThreads = 18 * 32;
 constexpr int kSeqChunk = 512;                     // sequences whose stage counts are kept at a time
 // Weights are 2^(y - m + kLift); the maximum m moves when a score passes it by kSlack (log2). 16 bits hold
 // 2^(kLift + kSlack), and a move costs a pass over the output.
-constexpr float kSlack = 2.5f;
-constexpr float kLift = 13.f;
+constexpr float kSlack = 6.f;
+constexpr float kLift = 9.f;
 constexpr float kInf = __builtin_huge_valf();
 
 template <int HD, int NG>
