@@ -46,6 +46,12 @@ constexpr float kSlack = 6.f;
 constexpr float kTopScale = 512.f;
 constexpr float kInf = __builtin_huge_valf();
 constexpr int kGroup = 8;  // parts summed at once
+// What an item costs beside its stages (queries in, the warps' results joined), in stages: it counts in the shares,
+// ahead of the item's first stage.
+#ifndef COLI_KV4_ITEM_COST
+#define COLI_KV4_ITEM_COST 4
+#endif
+constexpr int kItemCost = COLI_KV4_ITEM_COST;
 // Query rows per sequence and key/value head, on average, from which the 256-row tiles of kv4_tile.cu take over.
 constexpr int kTileFrom = 96;
 
@@ -294,7 +300,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
   auto stages_in = [&](int b) -> long long {
     t.b = b;
     load_seq(a.c, a.p, a.window, t, a.err);
-    return (long long)tiles_of(t.m, a.group, C::kRows) * heads * t.stages;
+    return (long long)tiles_of(t.m, a.group, C::kRows) * heads * (t.stages + kItemCost);
   };
   long long total = 0, own = 0;
   for (int b = tid; b < a.p.B; b += kAttnThreads) total += own = stages_in(b);
@@ -338,10 +344,12 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
   Item it = s_item;
   const long long local = w0 - s_at;  // stages of this sequence before the share
   const int tiles0 = tiles_of(it.m, a.group, C::kRows);
-  const long long item0 = local / it.stages;
+  const long long item0 = local / (it.stages + kItemCost);
   it.head = (int)(item0 / tiles0);
   it.tile = (int)(item0 % tiles0);
-  int stage = (int)(local % it.stages);  // within the item
+  // within the item; below 0: in its cost. w counts stages and costs: stage s of the item at `item_at` is at
+  // item_at + kItemCost + s.
+  int stage = (int)(local % (it.stages + kItemCost)) - kItemCost;
   long long w = w0;
   auto next_item = [&]() {  // after the last stage of an item; w < w1 guarantees that there is one
     if (++it.tile < tiles_of(it.m, a.group, C::kRows)) return;
@@ -365,7 +373,9 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
     int slot = 0;
     uint32_t phase = 1;
     bool lost = false;
-    while (w < w1 && !lost) {
+    while (!lost) {
+      if (stage < 0) w -= stage, stage = 0;
+      if (w >= w1) break;
       const int n = (int)min((long long)min(C::kStages, it.stages - stage), w1 - w);
       const int tok = (it.first + stage + lane) * kStageTok;
       const int units = lane < n ? min(kStageUnits, max(0, (it.len - tok + kKvUnit - 1) / kKvUnit)) : 0;
@@ -412,7 +422,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
       w += n;
       stage += n;
       if (stage == it.stages) {
-        stage = 0;
+        stage = -kItemCost;
         if (w < w1) next_item();
       }
     }
@@ -425,9 +435,11 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
   int slot = 0;
   uint32_t phase = 0;
   bool alive = true;
-  while (w < w1) {
+  while (true) {
     // ---- a segment: this CTA's stages of one item ----
-    const long long item_at = w - stage;  // where the item starts in the dealt-out stages
+    if (stage < 0) w -= stage, stage = 0;
+    if (w >= w1) break;
+    const long long item_at = w - stage;  // where the item's first stage is in what was dealt out
     const int n_here = (int)min((long long)(it.stages - stage), w1 - w);
     const int tile_row = it.tile * C::kRows;
     const int rows_all = it.m * a.group;  // this sequence's query rows per key/value head
@@ -1000,7 +1012,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
     }
     named_sync(1, kConsumers);  // the join buffer and the query fragments are free
     if (stage == it.stages) {
-      stage = 0;
+      stage = -kItemCost;
       if (w < w1) next_item();
     }
   }
