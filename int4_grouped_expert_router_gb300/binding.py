@@ -429,37 +429,42 @@ def coli_kv4_cache(pages, page_tokens, heads, head_dim, gs, device="cuda"):
     return KV4Cache(torch.empty(n, dtype=torch.uint8, device=device), pages, page_tokens, heads, head_dim, gs)
 
 
-def _rows3(t, heads, head_dim, name):
-    """A [T x heads x head_dim] CUDA tensor whose rows may be apart; returns its row stride."""
+def _rows3(t, T, heads, head_dim, name):
+    """The row stride of a [T x heads x head_dim] CUDA tensor whose rows may be apart."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
-        raise ValueError(f"{name} must be [T x {heads} x {head_dim}]")
+    if tuple(t.shape) != (T, heads, head_dim):
+        raise ValueError(f"{name} must be [{T} x {heads} x {head_dim}]")
     row, h, d = t.stride()
-    if (d != 1 and head_dim > 1) or (h != head_dim and heads > 1):
+    if d != 1 or (h != head_dim and heads > 1):
         raise ValueError(f"{name}: the heads and channels of a row must be contiguous")
-    return heads * head_dim if t.shape[0] == 1 else row
+    return heads * head_dim if T == 1 else row
 
 
 def _kv4_plan(T, lens, table, q_start):
-    _dev(lens, torch.int32, "lens")
-    _dev(table, torch.int32, "table")
-    _dev(q_start, torch.int32, "q_start")
-    n = lens.numel()
-    if table.dim() != 2 or table.shape[0] != n or (q_start is not None and q_start.numel() != n + 1):
-        raise ValueError("plan: lens [B], table [B x pages per sequence] and q_start [B + 1] or None")
-    if q_start is None and T != n:
-        raise ValueError("plan: without q_start there is one row per sequence")
-    return _ptr(q_start), lens.data_ptr(), n, table.data_ptr(), table.shape[1]
+    i32 = torch.int32
+    if lens.dtype != i32 or table.dtype != i32 or not (lens.is_cuda and table.is_cuda and lens.is_contiguous() and
+                                                       table.is_contiguous()):
+        raise ValueError("plan: lens and table must be contiguous int32 CUDA tensors")
+    n, shape = lens.numel(), table.shape
+    if len(shape) != 2 or shape[0] != n:
+        raise ValueError("plan: lens [B] and table [B x pages per sequence]")
+    if q_start is None:
+        if T != n:
+            raise ValueError("plan: without q_start there is one row per sequence")
+        return None, lens.data_ptr(), n, table.data_ptr(), shape[1]
+    if q_start.numel() != n + 1:
+        raise ValueError("plan: q_start must have B + 1 entries")
+    return _dev(q_start, i32, "q_start").data_ptr(), lens.data_ptr(), n, table.data_ptr(), shape[1]
 
 
 def _kv4_pair(name, ctx, cache, k, v, lens, table, q_start):
-    if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
-        raise ValueError("k and v must have the same rows and dtype")
-    T = k.shape[0]
-    ks, vs = _rows3(k, cache.heads, cache.head_dim, "k"), _rows3(v, cache.heads, cache.head_dim, "v")
-    qs, ln, n, tb, width = _kv4_plan(T, lens, table, q_start)
-    rc = getattr(library(), name)(ctx, cache, k.data_ptr(), ks, v.data_ptr(), vs, act_dtype(k), T, qs, ln, n, tb, width)
+    if k.dtype != v.dtype:
+        raise ValueError("k and v must have the same dtype")
+    T, heads, hd = k.shape[0], cache.heads, cache.head_dim
+    ks, vs = _rows3(k, T, heads, hd, "k"), _rows3(v, T, heads, hd, "v")
+    rc = getattr(_lib or library(), name)(ctx, cache, k.data_ptr(), ks, v.data_ptr(), vs, act_dtype(k), T,
+                                          *_kv4_plan(T, lens, table, q_start))
     return rc if rc == COLI_OK else _check(ctx, rc, name)
 
 
@@ -476,13 +481,13 @@ def coli_kv4_read(ctx, cache, k, v, lens, table, q_start=None):
 def coli_kv4_attention(ctx, cache, q, lens, table, out, q_start=None, scale=None, window=0):
     """out = softmax(scale q K) V over each row's sequence up to its own position (the last ``window`` of it);
     q, out [T x q_heads x head_dim]; scale defaults to head_dim ** -0.5."""
-    if q.dim() != 3 or out.dtype != q.dtype or out.shape != q.shape:
+    if q.dim() != 3 or out.dtype != q.dtype:
         raise ValueError("kv4_attention: q and out must be [T x q_heads x head_dim] of one dtype")
-    T, heads, _ = q.shape
-    qs, os_ = _rows3(q, heads, cache.head_dim, "q"), _rows3(out, heads, cache.head_dim, "out")
-    st, ln, n, tb, width = _kv4_plan(T, lens, table, q_start)
-    rc = library().coli_kv4_attention(ctx, cache, q.data_ptr(), qs, act_dtype(q), heads, T, st, ln, n, tb, width,
-                                      cache.head_dim ** -0.5 if scale is None else scale, window, out.data_ptr(), os_)
+    T, heads, hd = q.shape[0], q.shape[1], cache.head_dim
+    qs, os_ = _rows3(q, T, heads, hd, "q"), _rows3(out, T, heads, hd, "out")
+    rc = (_lib or library()).coli_kv4_attention(ctx, cache, q.data_ptr(), qs, act_dtype(q), heads, T,
+                                                *_kv4_plan(T, lens, table, q_start),
+                                                hd ** -0.5 if scale is None else scale, window, out.data_ptr(), os_)
     return rc if rc == COLI_OK else _check(ctx, rc, "coli_kv4_attention")
 
 
@@ -492,21 +497,26 @@ def coli_norm_residual(ctx, block, resid, gate, alpha, w_post, w_pre, eps, h, x,
     first = block if block is not None else resid
     if first is None or first.dim() != 2:
         raise ValueError("norm_residual: block or resid must be given, [S x D]")
-    S, D = first.shape
-    for t, name in ((block, "block"), (resid, "resid"), (h, "h"), (x, "x")):
-        if t is not None and _dev(t, first.dtype, name).shape != first.shape:
-            raise ValueError(f"norm_residual: {name} must be [S x D]")
-    rows = 0
-    if gate is not None:
-        _dev(gate, first.dtype, "gate")
-        rows = 1 if gate.numel() == D else S
-        if gate.numel() != rows * D:
-            raise ValueError("norm_residual: gate must be [S x D] or [D]")
-    for t, name in ((w_post, "w_post"), (w_pre, "w_pre")):
-        if t is not None and _dev(t, torch.float32, name).numel() != D:
-            raise ValueError(f"norm_residual: {name} must be [D]")
-    rc = library().coli_norm_residual(ctx, _ptr(block), _ptr(resid), _ptr(gate), rows, int(gate_sigmoid), alpha,
-                                      _ptr(w_post), _ptr(w_pre), eps, act_dtype(first), S, D, _ptr(h), _ptr(x))
+    shape, dtype = first.shape, first.dtype
+    S, D = shape
+    at = []
+    for t in (block, resid, h, x):
+        if t is None:
+            at.append(None)
+        elif t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+            at.append(t.data_ptr())
+        else:
+            raise ValueError("norm_residual: block, resid, h and x must be contiguous [S x D] CUDA tensors of one dtype")
+    for t, dt in ((gate, dtype), (w_post, torch.float32), (w_pre, torch.float32)):
+        if t is None:
+            at.append(None)
+        elif t.is_cuda and t.dtype == dt and t.is_contiguous() and (t.numel() == D or (t is gate and t.shape == shape)):
+            at.append(t.data_ptr())
+        else:
+            raise ValueError("norm_residual: gate must be [S x D] or [D] in the rows' dtype, w_post and w_pre [D] float32")
+    rows = 0 if gate is None else 1 if gate.numel() == D else S
+    rc = (_lib or library()).coli_norm_residual(ctx, at[0], at[1], at[4], rows, gate_sigmoid, alpha, at[5], at[6], eps,
+                                                act_dtype(first), S, D, at[2], at[3])
     return rc if rc == COLI_OK else _check(ctx, rc, "coli_norm_residual")
 
 

@@ -1,11 +1,12 @@
 // Writing tokens into the 4-bit key/value cache and reading them back (layout: kv4.h).
 //
-// Both are bound by memory: the plain rows dominate. A warp takes one row's next 512 channels (up to four
-// chunks of 128, four neighbouring channels per lane, all loads issued first), finds the row's place once,
-// and writes or reads the codes as the 16-bit pieces that the layout gives a token. In a chunk, lane group
-// u / 8 holds the 32 channels of one code word index, so a group of gs channels is gs / 4 neighbouring
-// lanes for keys and values alike, and the two halves of a value piece are four lanes apart.
+// Both are bound by memory: the plain rows dominate. A warp takes one row's next 512 channels (up to two
+// chunks of 256, eight neighbouring channels per lane, all loads issued first), finds the row's place once,
+// and writes or reads the codes as the layout gives them to a token: a whole word of keys, and of values the
+// halves of two words. A group of gs channels is gs / 8 neighbouring lanes for keys and values alike. The
+// two lanes whose channels share the value words of a token are two apart.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "kv4.h"
 #include "pipe.h"
@@ -16,8 +17,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kChunk = 128;  // channels of a warp's pass
-constexpr int kChunks = 4;   // passes whose loads are in flight together
+constexpr int kChunk = 256;  // channels of a warp's pass
+constexpr int kChunks = 2;   // passes whose loads are in flight together
 constexpr float kInf = __builtin_huge_valf();
 
 struct RowArgs {
@@ -26,7 +27,7 @@ struct RowArgs {
   void* k;
   void* v;
   long long k_stride, v_stride;
-  bool vec;    // rows start at a boundary of four elements
+  bool vec;    // rows start at a 16-byte boundary
   int groups;  // warps per row
   int* err;
 };
@@ -80,22 +81,95 @@ __device__ __forceinline__ float max_nan(float x, float y) {
   return r;
 }
 
-// Least and largest of a group's channels (GL neighbouring lanes, four channels each); not a number if one
-// of them is not. bf16 values travel as one register, the largest and the negated least.
-template <bool BF16, int GL>
-__device__ __forceinline__ void group_range(const float (&x)[4], float& lo, float& hi) {
-  hi = max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3]));
-  lo = max_nan(max_nan(-x[0], -x[1]), max_nan(-x[2], -x[3]));
-  if constexpr (BF16) {
-    __nv_bfloat162 m = __floats2bfloat162_rn(lo, hi);  // exact
+// A lane's eight channels as they lie in memory, and as binary32.
+template <bool BF16>
+struct Eight {
+  uint32_t w[BF16 ? 4 : 8];
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (BF16)
+      return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    else
+      return __uint_as_float(w[i]);
+  }
+};
+
+template <bool BF16>
+__device__ __forceinline__ Eight<BF16> load8(const void* p, long long at, bool vec) {
+  Eight<BF16> x;
+  constexpr int kWords = BF16 ? 4 : 8;
+  if (vec) {
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * (BF16 ? 2 : 4));
 #pragma unroll
-    for (int s = 1; s < GL; s <<= 1) {
-      const uint32_t o = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<uint32_t*>(&m), s);
-      m = __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(&o));
+    for (int i = 0; i < kWords; i += 4) {
+      const uint4 v = __ldcg(s + i / 4);
+      x.w[i] = v.x, x.w[i + 1] = v.y, x.w[i + 2] = v.z, x.w[i + 3] = v.w;
     }
-    lo = -__low2float(m);
-    hi = __high2float(m);
+  } else if constexpr (BF16) {
+    const unsigned short* s = static_cast<const unsigned short*>(p) + at;
+#pragma unroll
+    for (int i = 0; i < 4; i++) x.w[i] = __ldcg(s + 2 * i) | ((uint32_t)__ldcg(s + 2 * i + 1) << 16);
   } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++) x.w[i] = __ldcg(static_cast<const uint32_t*>(p) + at + i);
+  }
+  return x;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store8(void* p, long long at, bool vec, const float (&x)[8]) {
+  if constexpr (BF16) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    uint16_t* d = static_cast<uint16_t*>(p) + at;
+    if (vec)
+      *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+    else
+#pragma unroll
+      for (int j = 0; j < 8; j++) d[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+  } else {
+    float* d = static_cast<float*>(p) + at;
+    if (vec) {
+      *reinterpret_cast<float4*>(d) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4*>(d + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; j++) d[j] = x[j];
+    }
+  }
+}
+
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+__device__ __forceinline__ uint32_t bits(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+
+// Least and largest of a group's channels (GL neighbouring lanes); not a number if one of them is not. bf16
+// values are compared two at a time and travel as one register, the largest and the negated least.
+template <bool BF16, int GL>
+__device__ __forceinline__ void group_range(const Eight<BF16>& x, float& lo, float& hi) {
+  if constexpr (BF16) {
+    __nv_bfloat162 most = as_bf162(x.w[0]), least = most;
+#pragma unroll
+    for (int i = 1; i < 4; i++) {
+      most = __hmax2_nan(most, as_bf162(x.w[i]));
+      least = __hmin2_nan(least, as_bf162(x.w[i]));
+    }
+    // (largest, -least) of the even channels, and of the odd ones
+    const uint32_t neg = bits(least) ^ 0x80008000u;
+    __nv_bfloat162 m = __hmax2_nan(as_bf162(__byte_perm(bits(most), neg, 0x5410)), as_bf162(__byte_perm(bits(most), neg, 0x7632)));
+#pragma unroll
+    for (int s = 1; s < GL; s <<= 1) m = __hmax2_nan(m, as_bf162(__shfl_xor_sync(0xffffffffu, bits(m), s)));
+    hi = __low2float(m);
+    lo = -__high2float(m);
+  } else {
+    hi = x[0], lo = -x[0];
+#pragma unroll
+    for (int i = 1; i < 8; i++) {
+      hi = max_nan(hi, x[i]);
+      lo = max_nan(lo, -x[i]);
+    }
 #pragma unroll
     for (int s = 1; s < GL; s <<= 1) {
       hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, s));
@@ -105,80 +179,40 @@ __device__ __forceinline__ void group_range(const float (&x)[4], float& lo, floa
   }
 }
 
-// Codes of this lane's four channels, 4 bits each in order; the group's scale | offset << 16.
+__device__ __forceinline__ uint32_t bf16_bits(float x) {  // of a number that is one
+  return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
+
+// Codes of this lane's eight channels, 4 bits each in order; the group's scale | offset << 16.
 template <bool BF16, int GL>
-__device__ __forceinline__ uint32_t quantise(const float (&x)[4], uint32_t& par, bool report, int* err) {
+__device__ __forceinline__ uint32_t quantise(const Eight<BF16>& x, uint32_t& par, bool report, int* err) {
   float lo, hi;
   group_range<BF16, GL>(x, lo, hi);
   const float span = __fsub_rn(hi, lo);
   uint32_t sb = 0, ob = 0x7fc0u;
   float inv = 0.f, o = 0.f;
   if (span < kInf) {
-    sb = f32_to_bf16_rn(__fmul_rn(span, 1.0f / 15.0f));
+    sb = bf16_bits(__fmul_rn(span, 1.0f / 15.0f));
     if (sb < 0x0080u) sb = 0;  // below the smallest normal number
-    const float s = bf16_to_f32((uint16_t)sb);
-    ob = f32_to_bf16_rn(__fadd_rn(lo, __fmul_rn(8.0f, s)));
-    o = bf16_to_f32((uint16_t)ob);
+    const float s = __uint_as_float(sb << 16);
+    ob = bf16_bits(__fadd_rn(lo, __fmul_rn(8.0f, s)));
+    o = __uint_as_float(ob << 16);
     inv = sb ? __frcp_rn(s) : 0.f;
   } else if (report) {
     set_error(err, COLI_E_NONFINITE);
   }
   par = sb | (ob << 16);
+  // The quotient is clamped before it is rounded (the bounds are whole numbers). Adding 1.5 2^23 + 8 rounds it to the
+  // nearest integer, ties to even, and leaves its bits as 0x4b400000 + code; sixteenfold sums of those collect the
+  // codes, and the constant's share comes off at the end.
+  constexpr uint32_t kOnes = 0x11111111u;
   uint32_t n = 0;
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    // clamped before it is rounded (the bounds are whole numbers); adding 1.5 2^23 + 8 rounds to the nearest
-    // integer, ties to even, and leaves it, 8 added, in the low bits
+  for (int i = 7; i >= 0; i--) {
     const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], o), inv), -8.f), 7.f);
-    const uint32_t code = inv == 0.f ? 8u : __float_as_uint(__fadd_rn(q, 12582920.f)) & 15u;
-    n |= code << (4 * i);
+    n = n * 16u + __float_as_uint(__fadd_rn(q, 12582920.f));
   }
-  return n;
-}
-
-template <bool BF16>
-__device__ __forceinline__ void load4(const void* p, long long i, bool vec, float (&x)[4]) {
-  if constexpr (BF16) {
-    const unsigned short* s = static_cast<const unsigned short*>(p) + i;
-    if (vec) {
-      const uint2 w = __ldcg(reinterpret_cast<const uint2*>(s));
-      x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xffff0000u);
-      x[2] = __uint_as_float(w.y << 16), x[3] = __uint_as_float(w.y & 0xffff0000u);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; j++) x[j] = bf16_to_f32(__ldcg(s + j));
-    }
-  } else {
-    const float* s = static_cast<const float*>(p) + i;
-    if (vec) {
-      const float4 w = __ldcg(reinterpret_cast<const float4*>(s));
-      x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; j++) x[j] = __ldcg(s + j);
-    }
-  }
-}
-
-template <bool BF16>
-__device__ __forceinline__ void store4(void* p, long long i, bool vec, const float (&x)[4]) {
-  if constexpr (BF16) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-    const uint32_t w[2] = {*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b)};
-    uint16_t* d = static_cast<uint16_t*>(p) + i;
-    if (vec)
-      *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
-    else
-#pragma unroll
-      for (int j = 0; j < 4; j++) d[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-  } else {
-    float* d = static_cast<float*>(p) + i;
-    if (vec)
-      *reinterpret_cast<float4*>(d) = make_float4(x[0], x[1], x[2], x[3]);
-    else
-#pragma unroll
-      for (int j = 0; j < 4; j++) d[j] = x[j];
-  }
+  return n - 0x4b400000u * kOnes;
 }
 
 // A lane's place in its chunk: head and the lane's number u within it.
@@ -187,32 +221,29 @@ struct Spot {
   int head, u;
   bool in;
   __device__ __forceinline__ Spot(int chunk, int heads) {
-    const int x = chunk * kChunk + (threadIdx.x & 31) * 4;
+    const int x = chunk * kChunk + (threadIdx.x & 31) * 8;
     head = x / HD;
-    u = x % HD / 4;
+    u = x % HD / 8;
     in = head < heads;
   }
 };
 
 template <bool BF16, int HD, int NG>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(RowArgs a) {
-  constexpr int kGl = HD / NG / 4;  // lanes of a group
+  constexpr int kGl = HD / NG / 8;  // lanes of a group
   griddep_launch_dependents();
   griddep_wait();
   kv4_check_plan(a);
   const int item = blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int row = item / a.groups, chunk0 = item % a.groups * kChunks;
   if (row >= a.p.T) return;  // uniform in the warp
-  float xk[kChunks][4], xv[kChunks][4];
+  Eight<BF16> xk[kChunks] = {}, xv[kChunks] = {};
 #pragma unroll
   for (int n = 0; n < kChunks; n++) {
     const Spot<HD> s(chunk0 + n, a.c.heads);
     if (s.in) {
-      load4<BF16>(a.k, row * a.k_stride + s.head * HD + 4 * s.u, a.vec, xk[n]);
-      load4<BF16>(a.v, row * a.v_stride + s.head * HD + 4 * s.u, a.vec, xv[n]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; j++) xk[n][j] = xv[n][j] = 0.f;
+      xk[n] = load8<BF16>(a.k, row * a.k_stride + s.head * HD + 8 * s.u, a.vec);
+      xv[n] = load8<BF16>(a.v, row * a.v_stride + s.head * HD + 8 * s.u, a.vec);
     }
   }
   int page = 0, off = 0;
@@ -227,16 +258,18 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(RowArgs a) {
     const Spot<HD> s(chunk0 + n, a.c.heads);
     uint32_t pk, pv;
     const uint32_t nk = quantise<BF16, kGl>(xk[n], pk, s.in, a.err), nv = quantise<BF16, kGl>(xv[n], pv, s.in, a.err);
-    // value pieces: the low byte from the lane with channels 0..15 of the 32, the high byte from 16..31;
-    // each of the two lanes puts one of its two rows together
-    const int i = s.u >> 3, half = s.u >> 2 & 1;
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, half ? nv & 0xffu : nv >> 8, 4);
-    const uint32_t piece = half ? other | (nv & 0xff00u) : (nv & 0xffu) | (other << 8);
+    // A token's half of a value word holds two channels below 16 of a run of 32 and the two 16 above: bytes of two
+    // lanes, each of which puts two of the four words together.
+    const int i = s.u >> 2, c = s.u & 3, upper = c >> 1;
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? nv & 0xffffu : nv >> 16, 2);
+    const uint32_t two = upper ? __byte_perm(nv, other, 0x3524) : __byte_perm(nv, other, 0x5140);
     if (!s.in) continue;
     uint8_t* unit = at + s.head * head_bytes;
-    *reinterpret_cast<uint16_t*>(unit + kv4_k_word(HD, t, i, s.u >> 1 & 3) + 2 * (s.u & 1)) = (uint16_t)nk;
-    *reinterpret_cast<uint16_t*>(unit + kv4_v_at(HD, NG) + kv4_v_word(HD, t >> 1, 2 * (s.u & 3) + half, i) + 2 * (t & 1)) =
-        (uint16_t)piece;
+    *reinterpret_cast<uint32_t*>(unit + kv4_k_word(HD, t, i, c)) = nk;
+    uint8_t* v = unit + kv4_v_at(HD, NG) + 2 * (t & 1);
+    const int r = 4 * (c & 1) + 2 * upper;
+    *reinterpret_cast<uint16_t*>(v + kv4_v_word(HD, t >> 1, r, i)) = (uint16_t)two;
+    *reinterpret_cast<uint16_t*>(v + kv4_v_word(HD, t >> 1, r + 1, i)) = (uint16_t)(two >> 16);
     if (s.u % kGl == 0) {
       const int g = s.u / kGl;
       *reinterpret_cast<uint32_t*>(unit + kv4_kscale_at(HD) + (t * NG + g) * 4) = pk;
@@ -245,17 +278,22 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(RowArgs a) {
   }
 }
 
-// o + s (n - 8): the product is exact, so one rounding.
-__device__ __forceinline__ void values(uint32_t n, uint32_t par, float (&x)[4]) {
+// o + s (n - 8) of a word's eight codes: the product is exact, so one rounding.
+__device__ __forceinline__ void values(uint32_t w, uint32_t par, float (&x)[8]) {
   const float s = __uint_as_float(par << 16), o = __uint_as_float(par & 0xffff0000u);
+  const __half2 bias = __floats2half2_rn(1032.f, 1032.f);
 #pragma unroll
-  for (int j = 0; j < 4; j++)
-    x[j] = fmaf(s, __uint_as_float(0x4b000000u | (n >> (4 * j) & 15u)) - 8388616.f, o);
+  for (int m = 0; m < 4; m++) {
+    const uint32_t t = ((w >> (4 * m)) & 0x000f000fu) | 0x64006400u;  // 1024 + n in 16 bits
+    const __half2 n = __hsub2(*reinterpret_cast<const __half2*>(&t), bias);
+    x[m] = fmaf(s, __low2float(n), o);
+    x[m + 4] = fmaf(s, __high2float(n), o);
+  }
 }
 
 template <bool BF16, int HD, int NG>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(RowArgs a) {
-  constexpr int kGl = HD / NG / 4;
+  constexpr int kGl = HD / NG / 8;
   griddep_launch_dependents();
   griddep_wait();
   kv4_check_plan(a);
@@ -275,11 +313,12 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(RowArgs a) {
     const Spot<HD> s(chunk0 + n, a.c.heads);
     nk[n] = nv[n] = pk[n] = pv[n] = 0;
     if (!s.in || !there) continue;
-    const int i = s.u >> 3, half = s.u >> 2 & 1, g = s.u / kGl;
+    const int i = s.u >> 2, c = s.u & 3, r = 4 * (c & 1) + (c & 2), g = s.u / kGl;
     const uint8_t* unit = at + s.head * head_bytes;
-    nk[n] = __ldcg(reinterpret_cast<const unsigned short*>(unit + kv4_k_word(HD, t, i, s.u >> 1 & 3) + 2 * (s.u & 1)));
-    nv[n] = __ldcg(reinterpret_cast<const unsigned short*>(
-        unit + kv4_v_at(HD, NG) + kv4_v_word(HD, t >> 1, 2 * (s.u & 3) + half, i) + 2 * (t & 1)));
+    const uint8_t* v = unit + kv4_v_at(HD, NG) + 2 * (t & 1);
+    nk[n] = __ldcg(reinterpret_cast<const uint32_t*>(unit + kv4_k_word(HD, t, i, c)));
+    nv[n] = __ldcg(reinterpret_cast<const unsigned short*>(v + kv4_v_word(HD, t >> 1, r, i))) |
+            ((uint32_t)__ldcg(reinterpret_cast<const unsigned short*>(v + kv4_v_word(HD, t >> 1, r + 1, i))) << 16);
     pk[n] = __ldcg(reinterpret_cast<const uint32_t*>(unit + kv4_kscale_at(HD) + (t * NG + g) * 4));
     pv[n] = __ldcg(reinterpret_cast<const uint32_t*>(unit + kv4_vscale_at(HD, NG) + (t * NG + g) * 4));
   }
@@ -287,15 +326,15 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(RowArgs a) {
   for (int n = 0; n < kChunks; n++) {
     if ((chunk0 + n) * kChunk >= a.c.heads * HD) break;  // uniform
     const Spot<HD> s(chunk0 + n, a.c.heads);
-    const int half = s.u >> 2 & 1;
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, half ? nv[n] & 0xffu : nv[n] >> 8, 4);
-    const uint32_t mine = half ? other | (nv[n] & 0xff00u) : (nv[n] & 0xffu) | (other << 8);
+    const bool upper = s.u & 2;  // as in the append
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, __byte_perm(nv[n], 0, upper ? 0x4420 : 0x4431), 2);
+    const uint32_t mine = __byte_perm(nv[n], other, upper ? 0x3154 : 0x5420);
     if (!s.in) continue;
-    float x[4];
+    float x[8];
     values(nk[n], pk[n], x);
-    store4<BF16>(a.k, row * a.k_stride + s.head * HD + 4 * s.u, a.vec, x);
+    store8<BF16>(a.k, row * a.k_stride + s.head * HD + 8 * s.u, a.vec, x);
     values(mine, pv[n], x);
-    store4<BF16>(a.v, row * a.v_stride + s.head * HD + 4 * s.u, a.vec, x);
+    store8<BF16>(a.v, row * a.v_stride + s.head * HD + 8 * s.u, a.vec, x);
   }
 }
 
@@ -311,9 +350,9 @@ void (*kernel_of(int hd, int ng))(RowArgs) {
 template <bool READ>
 int launch_rows(coli_ctx* ctx, const char* who, const Kv4View& c, const Kv4Plan& p, void* k, long long k_stride, void* v,
                 long long v_stride, int dtype) {
-  const uintptr_t four = dtype == COLI_DTYPE_BF16 ? 8 : 16;
   RowArgs a{c, p, k, v, k_stride, v_stride};
-  a.vec = (((uintptr_t)k | (uintptr_t)v) % four) == 0 && k_stride % 4 == 0 && v_stride % 4 == 0;
+  const int per16 = dtype == COLI_DTYPE_BF16 ? 8 : 4;
+  a.vec = (((uintptr_t)k | (uintptr_t)v) & 15) == 0 && k_stride % per16 == 0 && v_stride % per16 == 0;
   a.groups = (c.heads * c.hd + kChunk * kChunks - 1) / (kChunk * kChunks);
   a.err = ctx->d_status;
   const long long grid = ((long long)p.T * a.groups + kWarps - 1) / kWarps;

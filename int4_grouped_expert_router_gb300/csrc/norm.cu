@@ -37,6 +37,10 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
 template <int V>
 using Raw = std::conditional_t<V == 1, uint32_t, uint4>;
 
+// To a few units in the last place: beside the gate's own rounding (bf16) or the sums (f32) that is nothing, and the
+// exact exponential and division cost as many instructions as all the rest of the kernel.
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
 // V consecutive elements from e0 of a row that starts at `row`; those outside 0..D are 0.
 template <bool BF16, int V>
 __device__ __forceinline__ Raw<V> load_raw(const void* p, size_t row, int e0, int D, bool whole) {
@@ -169,7 +173,7 @@ __global__ void __launch_bounds__(max_threads(N * V)) norm_kernel(NormArgs a, in
       if constexpr (!kEarly) gt[0] = load_raw<BF16, V>(a.gate, a.gate_per_row ? row : 0, e0, D, whole && g_aligned);
       unpack<BF16, V>(gt[kEarly ? n : 0], t);
 #pragma unroll
-      for (int i = 0; i < V; i++) b[n][i] *= a.gate_sigmoid ? 1.f / (1.f + expf(-t[i])) : t[i];
+      for (int i = 0; i < V; i++) b[n][i] *= a.gate_sigmoid ? sigmoid(t[i]) : t[i];
     }
     if (a.resid) {
       if constexpr (!kEarly) rs[0] = load_raw<BF16, V>(a.resid, row, e0, D, whole);
