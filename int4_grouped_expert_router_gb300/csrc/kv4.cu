@@ -1,10 +1,11 @@
 // Writing tokens into the 4-bit key/value cache and reading them back (layout: kv4.h).
 //
-// Both are bound by memory: the plain rows dominate. A warp takes one row's next 512 channels (up to two
-// chunks of 256, eight neighbouring channels per lane, all loads issued first), finds the row's place once,
-// and writes or reads the codes as the layout gives them to a token: a whole word of keys, and of values the
-// halves of two words. A group of gs channels is gs / 8 neighbouring lanes for keys and values alike. The
-// two lanes whose channels share the value words of a token are two apart.
+// Both are bound by memory: the plain rows dominate. A warp takes up to four slots, a slot being 256 channels of a
+// row (eight neighbouring channels per lane): four rows of up to 256 channels, two of up to 512, or 1024 channels
+// of one; one slot where there are too few to fill the device. All its loads are issued together, and the places
+// of its rows are found by as many lanes at once. Codes are written as the layout gives them to a token: a whole
+// word of keys, and of values the halves of two words. A group of gs channels is gs / 8 neighbouring lanes for keys
+// and values alike. The two lanes whose channels share the value words of a token are two apart.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -18,7 +19,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 256;  // channels of a warp's pass
-constexpr int kChunks = 2;   // passes whose loads are in flight together
+constexpr int kSlots = 4;    // passes whose loads are in flight together
 constexpr float kInf = __builtin_huge_valf();
 
 struct RowArgs {
@@ -28,7 +29,9 @@ struct RowArgs {
   void* v;
   long long k_stride, v_stride;
   bool vec;    // rows start at a 16-byte boundary
-  int groups;  // warps per row
+  int groups;  // warps across a row
+  int slots;   // per warp: kSlots or 1
+  int across;  // log2 of the slots that lie across a row; the others are further rows
   int* err;
 };
 
@@ -56,23 +59,41 @@ __device__ __forceinline__ int warp_seq_of(const Kv4Plan& p, int row) {
   return lo;
 }
 
-// Where row `row` of the plan lives: false if it has no place (no sequence, a negative position, a page
-// outside the cache). owned: the row belongs to a sequence.
-__device__ __forceinline__ bool kv4_place(const RowArgs& a, int row, int& page, int& off, bool& owned) {
-  const int b = warp_seq_of(a.p, row);
+// Where a row lives.
+struct Place {
+  int page, off;
+  bool owned;  // the row belongs to a sequence
+  bool there;  // and has a place: a position that is not negative, a page of the cache
+};
+
+// The places of rows row0, row0 + 1, ..: lane l finds that of row0 + l, l < n.
+__device__ __forceinline__ Place kv4_places(const RowArgs& a, int row0, int n) {
+  const int lane = threadIdx.x & 31, row = row0 + lane;
+  Place at{0, 0, false, false};
+  int b = warp_seq_of(a.p, row0);
+  if (lane >= n || row >= a.p.T) return at;
+  if (a.p.q_start) {
+    while (b + 1 < a.p.B && __ldcg(a.p.q_start + b + 1) <= row) b++;  // a few steps: rows are neighbours
+  } else {
+    b = row;
+  }
   int r0, r1;
   kv4_rows(a.p, b, r0, r1, a.err);
-  owned = row >= r0 && row < r1;
-  if (!owned) return false;
+  at.owned = row >= r0 && row < r1;
+  if (!at.owned) return at;
   const int pos = kv4_len(a.p, a.c.page_log2, b, a.err) - (r1 - row);
-  if (pos < 0) return false;
-  page = __ldcg(a.p.table + (size_t)b * a.p.table_stride + (pos >> a.c.page_log2));
-  off = pos & ((1 << a.c.page_log2) - 1);
-  if (page < 0 || page >= a.c.pages) {
-    set_error(a.err, COLI_E_RANGE);
-    return false;
-  }
-  return true;
+  if (pos < 0) return at;
+  at.page = __ldcg(a.p.table + (size_t)b * a.p.table_stride + (pos >> a.c.page_log2));
+  at.off = pos & ((1 << a.c.page_log2) - 1);
+  at.there = at.page >= 0 && at.page < a.c.pages;
+  if (!at.there) set_error(a.err, COLI_E_RANGE);
+  return at;
+}
+
+// Lane l's place, in every lane.
+__device__ __forceinline__ Place place_of(const Place& at, int l) {
+  const int flags = __shfl_sync(0xffffffffu, (int)at.owned | (int)at.there << 1, l);
+  return Place{__shfl_sync(0xffffffffu, at.page, l), __shfl_sync(0xffffffffu, at.off, l), (flags & 1) != 0, (flags & 2) != 0};
 }
 
 __device__ __forceinline__ float max_nan(float x, float y) {
@@ -228,34 +249,46 @@ struct Spot {
   }
 };
 
+// A warp's slots.
+struct Share {
+  int row0, rows, chunk0, across;
+  __device__ __forceinline__ explicit Share(const RowArgs& a) : across(a.across) {
+    const int item = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    rows = a.slots >> a.across;
+    row0 = item / a.groups * rows;
+    chunk0 = (item % a.groups) << a.across;
+  }
+  __device__ __forceinline__ int row(int n) const { return row0 + (n >> across); }
+  __device__ __forceinline__ int chunk(int n) const { return chunk0 + (n & ((1 << across) - 1)); }
+};
+
 template <bool BF16, int HD, int NG>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(RowArgs a) {
   constexpr int kGl = HD / NG / 8;  // lanes of a group
   griddep_launch_dependents();
   griddep_wait();
   kv4_check_plan(a);
-  const int item = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int row = item / a.groups, chunk0 = item % a.groups * kChunks;
-  if (row >= a.p.T) return;  // uniform in the warp
-  Eight<BF16> xk[kChunks] = {}, xv[kChunks] = {};
+  const Share w(a);
+  if (w.row0 >= a.p.T) return;  // uniform in the warp
+  Eight<BF16> xk[kSlots] = {}, xv[kSlots] = {};
 #pragma unroll
-  for (int n = 0; n < kChunks; n++) {
-    const Spot<HD> s(chunk0 + n, a.c.heads);
-    if (s.in) {
+  for (int n = 0; n < kSlots; n++) {
+    const Spot<HD> s(w.chunk(n), a.c.heads);
+    const long long row = w.row(n);
+    if (n < a.slots && row < a.p.T && s.in) {
       xk[n] = load8<BF16>(a.k, row * a.k_stride + s.head * HD + 8 * s.u, a.vec);
       xv[n] = load8<BF16>(a.v, row * a.v_stride + s.head * HD + 8 * s.u, a.vec);
     }
   }
-  int page = 0, off = 0;
-  bool owned;
-  if (!kv4_place(a, row, page, off, owned)) return;  // uniform in the warp
-  uint8_t* at = const_cast<uint8_t*>(kv4_unit(a.c, page, 0, off));
+  const Place places = kv4_places(a, w.row0, w.rows);
   const uint32_t head_bytes = (uint32_t)(1 << (a.c.page_log2 - 4)) * kv4_unit_bytes(HD, NG);
-  const int t = off & 15;
 #pragma unroll
-  for (int n = 0; n < kChunks; n++) {
-    if ((chunk0 + n) * kChunk >= a.c.heads * HD) break;  // uniform
-    const Spot<HD> s(chunk0 + n, a.c.heads);
+  for (int n = 0; n < kSlots; n++) {
+    const Place to = place_of(places, n >> a.across);
+    if (n >= a.slots || !to.there || w.chunk(n) * kChunk >= a.c.heads * HD) continue;  // uniform
+    const Spot<HD> s(w.chunk(n), a.c.heads);
+    uint8_t* at = const_cast<uint8_t*>(kv4_unit(a.c, to.page, 0, to.off));
+    const int t = to.off & 15;
     uint32_t pk, pv;
     const uint32_t nk = quantise<BF16, kGl>(xk[n], pk, s.in, a.err), nv = quantise<BF16, kGl>(xv[n], pv, s.in, a.err);
     // A token's half of a value word holds two channels below 16 of a run of 32 and the two 16 above: bytes of two
@@ -297,22 +330,19 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(RowArgs a) {
   griddep_launch_dependents();
   griddep_wait();
   kv4_check_plan(a);
-  const int item = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int row = item / a.groups, chunk0 = item % a.groups * kChunks;
-  if (row >= a.p.T) return;
-  int page = 0, off = 0;
-  bool owned;
-  const bool there = kv4_place(a, row, page, off, owned);
-  if (!owned) return;
-  const uint8_t* at = kv4_unit(a.c, page, 0, off);
+  const Share w(a);
+  if (w.row0 >= a.p.T) return;
+  const Place places = kv4_places(a, w.row0, w.rows);
   const uint32_t head_bytes = (uint32_t)(1 << (a.c.page_log2 - 4)) * kv4_unit_bytes(HD, NG);
-  const int t = off & 15;
-  uint32_t nk[kChunks], nv[kChunks], pk[kChunks], pv[kChunks];
+  uint32_t nk[kSlots], nv[kSlots], pk[kSlots], pv[kSlots];
 #pragma unroll
-  for (int n = 0; n < kChunks; n++) {
-    const Spot<HD> s(chunk0 + n, a.c.heads);
+  for (int n = 0; n < kSlots; n++) {
+    const Place from = place_of(places, n >> a.across);
+    const Spot<HD> s(w.chunk(n), a.c.heads);
     nk[n] = nv[n] = pk[n] = pv[n] = 0;
-    if (!s.in || !there) continue;
+    if (n >= a.slots || !s.in || !from.there) continue;
+    const uint8_t* at = kv4_unit(a.c, from.page, 0, from.off);
+    const int t = from.off & 15;
     const int i = s.u >> 2, c = s.u & 3, r = 4 * (c & 1) + (c & 2), g = s.u / kGl;
     const uint8_t* unit = at + s.head * head_bytes;
     const uint8_t* v = unit + kv4_v_at(HD, NG) + 2 * (t & 1);
@@ -323,13 +353,14 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(RowArgs a) {
     pv[n] = __ldcg(reinterpret_cast<const uint32_t*>(unit + kv4_vscale_at(HD, NG) + (t * NG + g) * 4));
   }
 #pragma unroll
-  for (int n = 0; n < kChunks; n++) {
-    if ((chunk0 + n) * kChunk >= a.c.heads * HD) break;  // uniform
-    const Spot<HD> s(chunk0 + n, a.c.heads);
+  for (int n = 0; n < kSlots; n++) {
+    const Spot<HD> s(w.chunk(n), a.c.heads);
+    const bool owned = place_of(places, n >> a.across).owned;
+    const long long row = w.row(n);
     const bool upper = s.u & 2;  // as in the append
     const uint32_t other = __shfl_xor_sync(0xffffffffu, __byte_perm(nv[n], 0, upper ? 0x4420 : 0x4431), 2);
     const uint32_t mine = __byte_perm(nv[n], other, upper ? 0x3154 : 0x5420);
-    if (!s.in) continue;
+    if (n >= a.slots || !s.in || !owned) continue;
     float x[8];
     values(nk[n], pk[n], x);
     store8<BF16>(a.k, row * a.k_stride + s.head * HD + 8 * s.u, a.vec, x);
@@ -353,9 +384,14 @@ int launch_rows(coli_ctx* ctx, const char* who, const Kv4View& c, const Kv4Plan&
   RowArgs a{c, p, k, v, k_stride, v_stride};
   const int per16 = dtype == COLI_DTYPE_BF16 ? 8 : 4;
   a.vec = (((uintptr_t)k | (uintptr_t)v) & 15) == 0 && k_stride % per16 == 0 && v_stride % per16 == 0;
-  a.groups = (c.heads * c.hd + kChunk * kChunks - 1) / (kChunk * kChunks);
+  // four slots a warp where that still gives every SM's schedulers a few warps
+  const int chunks = (c.heads * c.hd + kChunk - 1) / kChunk;
+  a.slots = (long long)p.T * chunks >= (long long)kSlots * 16 * ctx->num_sms ? kSlots : 1;
+  a.across = a.slots == 1 || chunks == 1 ? 0 : chunks == 2 ? 1 : 2;
+  a.groups = (chunks + (1 << a.across) - 1) >> a.across;
   a.err = ctx->d_status;
-  const long long grid = ((long long)p.T * a.groups + kWarps - 1) / kWarps;
+  const int rows = a.slots >> a.across;
+  const long long grid = (((long long)p.T + rows - 1) / rows * a.groups + kWarps - 1) / kWarps;
   if (grid * kWarps > 0x7fffffffll) return fail(ctx, COLI_E_INVAL, std::string(who) + ": too many rows for one call");
   ProfScope prof(ctx, COLI_KERNEL_CACHE);
   auto kern = dtype == COLI_DTYPE_BF16 ? kernel_of<READ, true>(c.hd, c.ng) : kernel_of<READ, false>(c.hd, c.ng);

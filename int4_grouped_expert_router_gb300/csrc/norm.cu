@@ -120,7 +120,7 @@ __device__ __forceinline__ void load_weight(const float* w, int e0, int D, bool 
 
 // V elements per vector (16 bytes, or 1 where the arrays do not share their alignment), N vectors per thread.
 template <bool BF16, int V, int N>
-__global__ void __launch_bounds__(max_threads(N * V)) norm_kernel(NormArgs a, int shift_step, int* err) {
+__global__ void __launch_bounds__(max_threads(N * V), N * V > 16 && N <= 4 ? 2 : 1) norm_kernel(NormArgs a, int shift_step, int* err) {
   constexpr bool kEarly = V > 1 && N <= 4;  // residual and gate wait in registers too
   griddep_launch_dependents();
   griddep_wait();
@@ -132,28 +132,30 @@ __global__ void __launch_bounds__(max_threads(N * V)) norm_kernel(NormArgs a, in
   const bool w_aligned = shift == 0 && (((uintptr_t)a.w_post | (uintptr_t)a.w_pre) & 15) == 0;
   const bool g_aligned = a.gate_per_row || (shift == 0 && ((uintptr_t)a.gate & 15) == 0);
   float b[N][V];
-  Raw<V> rs[kEarly ? N : 1], gt[kEarly ? N : 1];
+  Raw<V> raw[N], rs[kEarly ? N : 1], gt[kEarly ? N : 1];
   auto at = [&](int n) { return (n * (int)blockDim.x + (int)threadIdx.x) * V - shift; };
   auto is_whole = [&](int e0) { return e0 >= 0 && e0 + V <= D; };
 #pragma unroll
   for (int n = 0; n < N; n++) {
     const int e0 = at(n);
     const bool whole = is_whole(e0);
-    Raw<V> raw{};
-    if (a.block) raw = load_raw<BF16, V>(a.block, row, e0, D, whole);
+    raw[n] = Raw<V>{};
+    if (a.block) raw[n] = load_raw<BF16, V>(a.block, row, e0, D, whole);
     if constexpr (kEarly) {
       if (a.resid) rs[n] = load_raw<BF16, V>(a.resid, row, e0, D, whole);
       if (a.gate) gt[n] = load_raw<BF16, V>(a.gate, a.gate_per_row ? row : 0, e0, D, whole && g_aligned);
     }
-    unpack<BF16, V>(raw, b[n]);
   }
   float r = a.alpha;
   if (a.w_post) {
     float ss = 0.f;
 #pragma unroll
-    for (int n = 0; n < N; n++)
+    for (int n = 0; n < N; n++) {
+      float t[V];
+      unpack<BF16, V>(raw[n], t);
 #pragma unroll
-      for (int i = 0; i < V; i++) ss = fmaf(b[n][i], b[n][i], ss);
+      for (int i = 0; i < V; i++) ss = fmaf(t[i], t[i], ss);
+    }
     ss = block_sum(ss, s_red[0]);
     if (!(ss < kInf) && threadIdx.x == 0) set_error(err, COLI_E_NONFINITE);
     r = rsqrtf(ss / (float)D + a.eps);
@@ -164,6 +166,7 @@ __global__ void __launch_bounds__(max_threads(N * V)) norm_kernel(NormArgs a, in
     const int e0 = at(n);
     const bool whole = is_whole(e0);
     float w[V], t[V];
+    unpack<BF16, V>(raw[n], b[n]);
     if (a.w_post) {
       load_weight<V>(a.w_post, e0, D, whole, w_aligned, w);
 #pragma unroll
