@@ -19,7 +19,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 256;  // channels of a warp's pass
-constexpr int kSlots = 4;    // passes whose loads are in flight together
+// Passes of a warp whose loads are in flight together, where there are enough rows (registers: twice as many for bf16).
+constexpr int most_slots(bool bf16) { return bf16 ? 4 : 2; }
 constexpr float kInf = __builtin_huge_valf();
 
 struct RowArgs {
@@ -30,7 +31,6 @@ struct RowArgs {
   long long k_stride, v_stride;
   bool vec;    // rows start at a 16-byte boundary
   int groups;  // warps across a row
-  int slots;   // per warp: kSlots or 1
   int across;  // log2 of the slots that lie across a row; the others are further rows
   int* err;
 };
@@ -252,9 +252,9 @@ struct Spot {
 // A warp's slots.
 struct Share {
   int row0, rows, chunk0, across;
-  __device__ __forceinline__ explicit Share(const RowArgs& a) : across(a.across) {
+  __device__ __forceinline__ Share(const RowArgs& a, int slots) : across(a.across) {
     const int item = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    rows = a.slots >> a.across;
+    rows = slots >> a.across;
     row0 = item / a.groups * rows;
     chunk0 = (item % a.groups) << a.across;
   }
@@ -262,20 +262,20 @@ struct Share {
   __device__ __forceinline__ int chunk(int n) const { return chunk0 + (n & ((1 << across) - 1)); }
 };
 
-template <bool BF16, int HD, int NG>
+template <bool BF16, int HD, int NG, int kSlots>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(RowArgs a) {
   constexpr int kGl = HD / NG / 8;  // lanes of a group
   griddep_launch_dependents();
   griddep_wait();
   kv4_check_plan(a);
-  const Share w(a);
+  const Share w(a, kSlots);
   if (w.row0 >= a.p.T) return;  // uniform in the warp
   Eight<BF16> xk[kSlots] = {}, xv[kSlots] = {};
 #pragma unroll
   for (int n = 0; n < kSlots; n++) {
     const Spot<HD> s(w.chunk(n), a.c.heads);
     const long long row = w.row(n);
-    if (n < a.slots && row < a.p.T && s.in) {
+    if (row < a.p.T && s.in) {
       xk[n] = load8<BF16>(a.k, row * a.k_stride + s.head * HD + 8 * s.u, a.vec);
       xv[n] = load8<BF16>(a.v, row * a.v_stride + s.head * HD + 8 * s.u, a.vec);
     }
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(RowArgs a) {
 #pragma unroll
   for (int n = 0; n < kSlots; n++) {
     const Place to = place_of(places, n >> a.across);
-    if (n >= a.slots || !to.there || w.chunk(n) * kChunk >= a.c.heads * HD) continue;  // uniform
+    if (!to.there || w.chunk(n) * kChunk >= a.c.heads * HD) continue;  // uniform
     const Spot<HD> s(w.chunk(n), a.c.heads);
     uint8_t* at = const_cast<uint8_t*>(kv4_unit(a.c, to.page, 0, to.off));
     const int t = to.off & 15;
@@ -324,13 +324,13 @@ __device__ __forceinline__ void values(uint32_t w, uint32_t par, float (&x)[8]) 
   }
 }
 
-template <bool BF16, int HD, int NG>
+template <bool BF16, int HD, int NG, int kSlots>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(RowArgs a) {
   constexpr int kGl = HD / NG / 8;
   griddep_launch_dependents();
   griddep_wait();
   kv4_check_plan(a);
-  const Share w(a);
+  const Share w(a, kSlots);
   if (w.row0 >= a.p.T) return;
   const Place places = kv4_places(a, w.row0, w.rows);
   const uint32_t head_bytes = (uint32_t)(1 << (a.c.page_log2 - 4)) * kv4_unit_bytes(HD, NG);
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(RowArgs a) {
     const Place from = place_of(places, n >> a.across);
     const Spot<HD> s(w.chunk(n), a.c.heads);
     nk[n] = nv[n] = pk[n] = pv[n] = 0;
-    if (n >= a.slots || !s.in || !from.there) continue;
+    if (!s.in || !from.there) continue;
     const uint8_t* at = kv4_unit(a.c, from.page, 0, from.off);
     const int t = from.off & 15;
     const int i = s.u >> 2, c = s.u & 3, r = 4 * (c & 1) + (c & 2), g = s.u / kGl;
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(RowArgs a) {
     const bool upper = s.u & 2;  // as in the append
     const uint32_t other = __shfl_xor_sync(0xffffffffu, __byte_perm(nv[n], 0, upper ? 0x4420 : 0x4431), 2);
     const uint32_t mine = __byte_perm(nv[n], other, upper ? 0x3154 : 0x5420);
-    if (n >= a.slots || !s.in || !owned) continue;
+    if (!s.in || !owned) continue;
     float x[8];
     values(nk[n], pk[n], x);
     store8<BF16>(a.k, row * a.k_stride + s.head * HD + 8 * s.u, a.vec, x);
@@ -369,9 +369,9 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(RowArgs a) {
   }
 }
 
-template <bool READ, bool BF16>
+template <bool READ, bool BF16, int SLOTS>
 void (*kernel_of(int hd, int ng))(RowArgs) {
-#define COLI_KV4_KERNEL(HD, NG) (READ ? kv4_read_kernel<BF16, HD, NG> : kv4_append_kernel<BF16, HD, NG>)
+#define COLI_KV4_KERNEL(HD, NG) (READ ? kv4_read_kernel<BF16, HD, NG, SLOTS> : kv4_append_kernel<BF16, HD, NG, SLOTS>)
   if (hd == 64) return ng == 1 ? COLI_KV4_KERNEL(64, 1) : COLI_KV4_KERNEL(64, 2);
   if (hd == 128) return ng == 1 ? COLI_KV4_KERNEL(128, 1) : ng == 2 ? COLI_KV4_KERNEL(128, 2) : COLI_KV4_KERNEL(128, 4);
   return ng == 2 ? COLI_KV4_KERNEL(256, 2) : COLI_KV4_KERNEL(256, 4);
@@ -384,17 +384,20 @@ int launch_rows(coli_ctx* ctx, const char* who, const Kv4View& c, const Kv4Plan&
   RowArgs a{c, p, k, v, k_stride, v_stride};
   const int per16 = dtype == COLI_DTYPE_BF16 ? 8 : 4;
   a.vec = (((uintptr_t)k | (uintptr_t)v) & 15) == 0 && k_stride % per16 == 0 && v_stride % per16 == 0;
-  // four slots a warp where that still gives every SM's schedulers a few warps
+  // several slots a warp where that still gives every SM's schedulers a few warps
+  const bool bf16 = dtype == COLI_DTYPE_BF16;
   const int chunks = (c.heads * c.hd + kChunk - 1) / kChunk;
-  a.slots = (long long)p.T * chunks >= (long long)kSlots * 16 * ctx->num_sms ? kSlots : 1;
-  a.across = a.slots == 1 || chunks == 1 ? 0 : chunks == 2 ? 1 : 2;
+  const int slots = (long long)p.T * chunks >= (long long)most_slots(bf16) * 16 * ctx->num_sms ? most_slots(bf16) : 1;
+  a.across = 0;
+  while ((2 << a.across) <= slots && (1 << a.across) < chunks) a.across++;
   a.groups = (chunks + (1 << a.across) - 1) >> a.across;
   a.err = ctx->d_status;
-  const int rows = a.slots >> a.across;
+  const int rows = slots >> a.across;
   const long long grid = (((long long)p.T + rows - 1) / rows * a.groups + kWarps - 1) / kWarps;
   if (grid * kWarps > 0x7fffffffll) return fail(ctx, COLI_E_INVAL, std::string(who) + ": too many rows for one call");
   ProfScope prof(ctx, COLI_KERNEL_CACHE);
-  auto kern = dtype == COLI_DTYPE_BF16 ? kernel_of<READ, true>(c.hd, c.ng) : kernel_of<READ, false>(c.hd, c.ng);
+  auto kern = bf16 ? (slots > 1 ? kernel_of<READ, true, most_slots(true)>(c.hd, c.ng) : kernel_of<READ, true, 1>(c.hd, c.ng))
+                   : (slots > 1 ? kernel_of<READ, false, most_slots(false)>(c.hd, c.ng) : kernel_of<READ, false, 1>(c.hd, c.ng));
   cudaError_t e = launch_k(kern, (int)grid, kThreads, 0, ctx->stream, true, false, a);
   if (e != cudaSuccess) return cuda_fail(ctx, e, who);
   return COLI_OK;
