@@ -531,12 +531,6 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         }
     }
     named_sync(1, kConsumers);
-    uint2 qf[NT == 1 ? HD / 16 : 1];  // one tile's fragments stay in registers
-    if constexpr (NT == 1) {
-#pragma unroll
-      for (int s = 0; s < HD / 16; s++) qf[s] = s_q[s * 32 + lane];
-    }
-
     float o[NT][C::kMt][4], lsum[NT][2], bias[NT][2][NG], mf[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
@@ -598,11 +592,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
             for (int h = 0; h < 2; h++)
 #pragma unroll
               for (int nt = 0; nt < NT; nt++) {
-                uint2 b;
-                if constexpr (NT == 1)
-                  b = qf[2 * i + h];
-                else
-                  b = s_q[(nt * (HD / 16) + 2 * i + h) * 32 + lane];
+                const uint2 b = s_q[(nt * (HD / 16) + 2 * i + h) * 32 + lane];
                 if (i == g * C::kWpg)
                   mma16816_zero(acc[h][nt], a0[2 * h], a1[2 * h], a0[2 * h + 1], a1[2 * h + 1], b.x, b.y);
                 else
