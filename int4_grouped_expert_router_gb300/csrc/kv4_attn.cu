@@ -53,7 +53,7 @@ constexpr int kGroup = 8;  // parts summed at once
 #endif
 constexpr int kItemCost = COLI_KV4_ITEM_COST;
 // Query rows per sequence and key/value head, on average, from which the 256-row tiles of kv4_tile.cu take over.
-constexpr int kTileFrom = 96;
+constexpr int kTileFrom = 17;
 
 template <int HD, int NG, int NT, bool F32>
 struct Cfg {

@@ -47,6 +47,11 @@ constexpr int kSeqChunk = 512;                     // sequences whose stage coun
 constexpr float kSlack = 6.f;
 constexpr float kLift = 9.f;
 constexpr float kInf = __builtin_huge_valf();
+// What an item costs beside its stages, in stages: it counts in the shares, ahead of the item's first stage.
+#ifndef COLI_KV4_TILE_COST
+#define COLI_KV4_TILE_COST 2
+#endif
+constexpr int kItemCost = COLI_KV4_TILE_COST;
 
 template <int HD, int NG>
 struct Tile {
@@ -101,7 +106,7 @@ __device__ __forceinline__ void load_seq(const TileArgs& a, Item& it) {
   it.len = kv4_len(a.p, a.c.page_log2, it.b, a.err);
 }
 
-// Stages of a whole sequence per head, by a warp.
+// Stages (and item costs) of a whole sequence per head, by a warp.
 __device__ __forceinline__ long long seq_stages(const TileArgs& a, int b) {
   Item it;
   it.b = b;
@@ -110,7 +115,7 @@ __device__ __forceinline__ long long seq_stages(const TileArgs& a, int b) {
   for (int k = threadIdx.x & 31, n = tiles_of(it.m, a.group); k < n; k += 32) {
     int first, stages;
     tile_span(a, it.m, it.len, k, first, stages);
-    sum += stages;
+    sum += stages + kItemCost;
   }
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum;
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
   uint8_t* s_raw = s_v + 2 * T::kK;       // [kTileUnits] packed units
   __shared__ __align__(8) uint64_t raw_full, raw_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], par_full[4],
       q_full[2], s_full[2], p_full[2], o_full[2];
-  __shared__ float s_par[4][3];           // per stage: 1 / key factor, change of the value factor, 1 / value factor
+  __shared__ float s_par[4][3];           // per stage: 1 / key factor, value factor (0: none yet), 1 / value factor
   __shared__ float s_big[2][kConvWarps];  // largest key and value of each unit, when a factor has to move
   __shared__ uint32_t s_tmem;
   __shared__ long long s_w[kSeqChunk];
@@ -349,7 +354,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
     for (int k0 = 0; k0 < n; k0 += 32) {
       int first, stages = 0;
       if (k0 + lane < n) tile_span(a, it.m, it.len, k0 + lane, first, stages);
-      const long long mine = (long long)stages * heads;
+      const long long mine = k0 + lane < n ? (long long)(stages + kItemCost) * heads : 0;
       long long inc = mine;
       for (int o = 1; o < 32; o <<= 1) {
         const long long v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -373,9 +378,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
   it.tile = s_start_tile;
   tile_span(a, it.m, it.len, it.tile, it.first, it.stages);
   const long long local = w0 - s_at;
-  it.head = (int)(local / it.stages);
-  int stage = (int)(local % it.stages);
+  it.head = (int)(local / (it.stages + kItemCost));
+  // below 0: in the item's cost. w counts stages and costs.
+  int stage = (int)(local % (it.stages + kItemCost)) - kItemCost;
   long long w = w0;
+  auto more = [&]() {  // past the item's cost; false at the end of the share
+    if (stage < 0) w -= stage, stage = 0;
+    return w < w1;
+  };
   auto next_item = [&]() {  // w < w1 guarantees that there is one
     if (++it.head < heads) return;
     it.head = 0;
@@ -401,7 +411,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
     // ------------------------------------ producer ------------------------------------
     const int page_tok = 1 << a.c.page_log2;
     int cached_b = -1, cached_from = 0, pages = 0;
-    for (uint32_t n = 0; w < w1; n++) {
+    for (uint32_t n = 0; more(); n++) {
       const int tok = (it.first + stage) * kTileTok;
       const int units = min(kTileUnits, max(0, (it.len - tok + kKvUnit - 1) / kKvUnit));
       const int page = tok >> a.c.page_log2;
@@ -429,7 +439,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
       }
       w++;
       if (++stage == it.stages) {
-        stage = 0;
+        stage = -kItemCost;
         if (w < w1) next_item();
       }
     }
@@ -458,42 +468,72 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
           mma_ts(tm + 2 * kTileTok + x * HD, tm + x * kTileTok + k * 8, dv + (k / 4) * (HD * 8) + (k % 4) * 2, kIdO,
                  !(fresh && k == 0));
       };
-      while (w < w1) {
+      while (more()) {
         const int n_here = (int)min((long long)(it.stages - stage), w1 - w);
-        const int halves = rows_here() > kHalf ? 2 : 1;
+        const bool split = rows_here() <= kHalf;
+        const int halves = split && n_here == 1 ? 1 : 2;  // with work here
         for (int x = 0; x < halves; x++) {
           wait(&q_full[x], nseg[x] & 1);
           nseg[x]++;
         }
-        wait(&k_full[n & 1], (n >> 1) & 1);
-        tc_fence_after_sync();
-#pragma unroll 1
-        for (int x = 0; x < halves; x++) scores(x, n);
-        tc_commit(&k_empty[n & 1]);
-        for (int j = 0; j < n_here; j++, n++) {
-          wait(&v_full[n & 1], (n >> 1) & 1);
+        if (split) {
 #pragma unroll 1
           for (int x = 0; x < halves; x++) {
+            wait(&k_full[(n + x) & 1], ((n + x) >> 1) & 1);
+            tc_fence_after_sync();
+            scores(x, n + x);
+            tc_commit(&k_empty[(n + x) & 1]);
+          }
+#pragma unroll 1
+          for (int j = 0; j < n_here; j++, n++) {
+            const int x = j & 1;
+            wait(&v_full[n & 1], (n >> 1) & 1);
             wait(&p_full[x], ns[x] & 1);
             ns[x]++;
             tc_fence_after_sync();
-            output(x, n, j == 0);
-            if (j + 1 == n_here) tc_commit(&o_full[x]);
-            if (x + 1 == halves) tc_commit(&v_empty[n & 1]);
-            if (j + 1 < n_here) {  // the next stage's scores go over the weights that the product above reads first
-              if (x == 0) {
-                wait(&k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
-                tc_fence_after_sync();
+            output(x, n, j < 2);
+            tc_commit(&v_empty[n & 1]);
+            if (j + 2 < n_here) {
+              wait(&k_full[n & 1], ((n + 2) >> 1) & 1);
+              tc_fence_after_sync();
+              scores(x, n + 2);
+              tc_commit(&k_empty[n & 1]);
+            } else {
+              tc_commit(&o_full[x]);
+            }
+          }
+        } else {
+          wait(&k_full[n & 1], (n >> 1) & 1);
+          tc_fence_after_sync();
+#pragma unroll 1
+          for (int x = 0; x < 2; x++) scores(x, n);
+          tc_commit(&k_empty[n & 1]);
+#pragma unroll 1
+          for (int j = 0; j < n_here; j++, n++) {
+            wait(&v_full[n & 1], (n >> 1) & 1);
+#pragma unroll 1
+            for (int x = 0; x < 2; x++) {
+              wait(&p_full[x], ns[x] & 1);
+              ns[x]++;
+              tc_fence_after_sync();
+              output(x, n, j == 0);
+              if (j + 1 == n_here) tc_commit(&o_full[x]);
+              if (x == 1) tc_commit(&v_empty[n & 1]);
+              if (j + 1 < n_here) {  // the next stage's scores go over the weights that the product above reads first
+                if (x == 0) {
+                  wait(&k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
+                  tc_fence_after_sync();
+                }
+                scores(x, n + 1);
+                if (x == 1) tc_commit(&k_empty[(n + 1) & 1]);
               }
-              scores(x, n + 1);
-              if (x + 1 == halves) tc_commit(&k_empty[(n + 1) & 1]);
             }
           }
         }
         w += n_here;
         stage += n_here;
         if (stage == it.stages) {
-          stage = 0;
+          stage = -kItemCost;
           if (w < w1) next_item();
         }
       }
@@ -510,7 +550,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
     const uint32_t v_base0 = smem_u32(s_v) + (cw / 4) * (HD * 128) + r * 128 + cc * 4;
     const uint8_t* unit = s_raw + cw * T::kUnit;
     float kmul = 0.f, vmul = 0.f;  // keys and values are multiplied by them; they only shrink within a segment
-    for (uint32_t n = 0; w < w1; n++) {
+    for (uint32_t n = 0; more(); n++) {
       if (n == 0 || stage == 0) kmul = vmul = 0.f;
       const int left = it.len - (it.first + stage) * kTileTok - cw * 16;  // tokens of this unit that exist
       wait(&raw_full, n & 1);
@@ -541,7 +581,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         }
       }
       auto too_big = [](float x, float mul) { return mul == 0.f ? x > 0.f : x * mul >= 16384.f; };
-      float shrink = 1.f;
       if (named_sync_or(2, kConvWarps * 32, too_big(kbig, kmul) || too_big(vbig, vmul))) {
         kbig = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(kbig)));
         vbig = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vbig)));
@@ -556,17 +595,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
           vbig = fmaxf(vbig, s_big[1][i]);
         }
         if (too_big(kbig, kmul)) kmul = below_2_14(kbig);
-        if (too_big(vbig, vmul)) {
-          const float now = below_2_14(vbig);
-          shrink = vmul == 0.f ? 1.f : now / vmul;
-          vmul = now;
-        }
+        if (too_big(vbig, vmul)) vmul = below_2_14(vbig);
       }
       // ---- keys: odd tokens store the words of a pair in the other order: eight lanes then cover all banks ----
       wait(&k_empty[n & 1], ((n >> 1) & 1) ^ 1);
       if (cw == 0 && lane == 0) {  // the softmax of four stages ago is long done
         s_par[n & 3][0] = kmul == 0.f ? 1.f : 1.f / kmul;
-        s_par[n & 3][1] = shrink;
+        s_par[n & 3][1] = vmul;
         s_par[n & 3][2] = vmul == 0.f ? 0.f : 1.f / vmul;
         mbar_arrive(&par_full[n & 3]);
       }
@@ -620,7 +655,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
       if (lane == 0) mbar_arrive(&v_full[n & 1]);
       w++;
       if (++stage == it.stages) {
-        stage = 0;
+        stage = -kItemCost;
         if (w < w1) next_item();
       }
     }
@@ -631,66 +666,85 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + x * kTileTok, t_o = tmem + lanes + 2 * kTileTok + x * HD;
     uint32_t n = 0, ns = 0, nseg = 0;
-    while (w < w1) {
-      const long long item_at = w - stage;
+    float fac0 = 0.f;
+    // This row's queries of the item at the cursor, into shared memory: a power of two brings the largest to
+    // [2^14, 2^15), and fac0 takes the scores back, in log2 units.
+    auto load_queries = [&]() {
+      const int row_n = rows_here(), n_here = (int)min((long long)(it.stages - stage), w1 - w);
+      const bool split = row_n <= kHalf;
+      if (split && x == 1 && n_here == 1) return;
+      const int lrow = split ? row & (kHalf - 1) : row;
+      const long long q_row = (long long)it.tile * kTileRows + min(lrow, row_n - 1);
+      const size_t at = (size_t)((it.r0 + q_row / a.group) * a.q_stride) + (size_t)(it.head * a.group + q_row % a.group) * HD;
+      const unsigned short* src = static_cast<const unsigned short*>(a.q) + at;
+      uint4 v[HD / 8];  // all in flight
+#pragma unroll
+      for (int ch = 0; ch < HD / 8; ch++) {
+        if (a.vec) {
+          v[ch] = __ldcg(reinterpret_cast<const uint4*>(src) + ch);
+        } else {
+          uint32_t e[4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) e[i] = __ldcg(src + 8 * ch + 2 * i) | ((uint32_t)__ldcg(src + 8 * ch + 2 * i + 1) << 16);
+          v[ch] = make_uint4(e[0], e[1], e[2], e[3]);
+        }
+      }
+      uint32_t amax = 0;
+#pragma unroll
+      for (int ch = 0; ch < HD / 8; ch++) {
+        const uint32_t qw[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) amax = max(amax, max(qw[i] & 0x7fffu, qw[i] >> 16 & 0x7fffu));
+      }
+      if (amax >= 0x7f80u && lrow < row_n) set_error(a.err, COLI_E_NONFINITE);
+      const int ex = min(253, max(1, 127 + 14 + 127 - (int)(amax >> 7)));
+      float mult = amax == 0 ? 1.f : __uint_as_float((uint32_t)ex << 23);
+      const float inv = amax == 0 ? 1.f : __uint_as_float((uint32_t)(254 - ex) << 23);
+      if (a.scale < 0.f) mult = -mult;
+      if (amax >= 0x7f80u) mult = __uint_as_float(0x7fc00000u);
+      const uint32_t dst = smem_u32(s_q) + x * T::kQ + (row & (kHalf - 1)) * 128;
+#pragma unroll
+      for (int ch = 0; ch < HD / 8; ch++) {
+        const uint32_t qw[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; j++) f[2 * j] = lo_bf16(qw[j]) * mult, f[2 * j + 1] = hi_bf16(qw[j]) * mult;
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) o[j] = bits(__floats2half2_rn(f[j], f[j + 4]));
+        sts128(dst + (ch / 8) * (kHalf * 128) + (((ch % 8) ^ (row & 7)) << 4), o);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[x]);
+      fac0 = fabsf(a.scale) * 1.4426950408889634f * inv;
+    };
+    if (more()) load_queries();
+    while (more()) {
+      const Item at = it;  // the item of this segment; the cursor moves on before its results are stored
+      const long long item_at = w - stage;  // where the item's first stage is in what was dealt out
       const int n_here = (int)min((long long)(it.stages - stage), w1 - w);
       const int row_n = rows_here();
-      const bool active = x == 0 || row_n > kHalf;
-      const long long q_row = (long long)it.tile * kTileRows + min(row, row_n - 1);  // rows past the end repeat the last
-      const int pos = it.len - it.m + (int)(q_row / a.group);
-      float mf = -kInf, l = 0.f, unscale = 0.f;
+      // A tile of at most 128 rows: both halves hold its queries and take alternate stages.
+      const bool split = row_n <= kHalf;
+      const bool active = !split || x == 0 || n_here > 1;
+      const int lrow = split ? row & (kHalf - 1) : row;
+      const long long q_row = (long long)at.tile * kTileRows + min(lrow, row_n - 1);  // rows past the end repeat the last
+      const int pos = at.len - at.m + (int)(q_row / a.group);
+      float mf = -kInf, l = 0.f, vmul = 0.f, unscale = 0.f;
       if (active) {
-        // ---- this row's queries: a power of two brings the largest to [2^14, 2^15) ----
-        const size_t at = (size_t)((it.r0 + q_row / a.group) * a.q_stride) + (size_t)(it.head * a.group + q_row % a.group) * HD;
-        const unsigned short* src = static_cast<const unsigned short*>(a.q) + at;
-        auto eight = [&](int ch) {  // channels 8 ch .. 8 ch + 7
-          if (a.vec) return __ldcg(reinterpret_cast<const uint4*>(src) + ch);
-          uint32_t v[4];
-#pragma unroll
-          for (int i = 0; i < 4; i++) v[i] = __ldcg(src + 8 * ch + 2 * i) | ((uint32_t)__ldcg(src + 8 * ch + 2 * i + 1) << 16);
-          return make_uint4(v[0], v[1], v[2], v[3]);
-        };
-        uint32_t amax = 0;
-#pragma unroll 4
-        for (int ch = 0; ch < HD / 8; ch++) {
-          const uint4 v = eight(ch);
-          const uint32_t qw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int i = 0; i < 4; i++) amax = max(amax, max(qw[i] & 0x7fffu, qw[i] >> 16 & 0x7fffu));
-        }
-        const float big = __uint_as_float(amax << 16);
-        if (amax >= 0x7f80u && row < row_n) set_error(a.err, COLI_E_NONFINITE);
-        const int ex = min(253, max(1, 127 + 14 + 127 - (int)(amax >> 7)));
-        float mult = amax == 0 ? 1.f : __uint_as_float((uint32_t)ex << 23);
-        const float inv = amax == 0 ? 1.f : __uint_as_float((uint32_t)(254 - ex) << 23);
-        if (a.scale < 0.f) mult = -mult;
-        if (!(big < kInf)) mult = __uint_as_float(0x7fc00000u);
-        const uint32_t dst = smem_u32(s_q) + x * T::kQ + (row & (kHalf - 1)) * 128;
-#pragma unroll 4
-        for (int ch = 0; ch < HD / 8; ch++) {
-          const uint4 u = eight(ch);
-          const uint32_t qw[4] = {u.x, u.y, u.z, u.w};
-          float f[8];
-#pragma unroll
-          for (int j = 0; j < 4; j++) f[2 * j] = lo_bf16(qw[j]) * mult, f[2 * j + 1] = hi_bf16(qw[j]) * mult;
-          uint32_t v[4];
-#pragma unroll
-          for (int j = 0; j < 4; j++) v[j] = bits(__floats2half2_rn(f[j], f[j + 4]));
-          sts128(dst + (ch / 8) * (kHalf * 128) + (((ch % 8) ^ (row & 7)) << 4), v);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[x]);
-        const float fac0 = fabsf(a.scale) * 1.4426950408889634f * inv;
-
-        for (int j = 0; j < n_here; j++, n++, ns++) {
-          const int t0 = (it.first + stage + j) * kTileTok;
-          wait(&par_full[n & 3], (n >> 2) & 1);
-          // kept above 0, so that struck-out scores (minus infinity) stay so
-          const float fac = fmaxf(fac0 * s_par[n & 3][0], 1e-37f), shrink = s_par[n & 3][1];
-          unscale = s_par[n & 3][2];
+        const int step = split ? 2 : 1, j0 = split ? x : 0;
+        for (int j = j0; j < n_here; j += step, ns++) {
+          const int t0 = (at.first + stage + j) * kTileTok;
           wait(&s_full[x], ns & 1);
           tc_fence_after_sync();
+          // The scores are there, so their stage's factors are: this wait does not wait, and comes second because a
+          // half that has skipped stages could take an earlier phase of the barrier for this one.
+          const uint32_t par = (n + j) & 3;
+          wait(&par_full[par], ((n + j) >> 2) & 1);
+          // kept above 0, so that struck-out scores (minus infinity) stay so
+          const float fac = fmaxf(fac0 * s_par[par][0], 1e-37f), vnow = s_par[par][1];
+          unscale = s_par[par][2];
           // columns [c0, c1) are visible to this row; the others are struck out where they lie
           const int c1 = min(kTileTok, max(0, pos - t0 + 1));
           const int c0 = a.window > 0 ? min(kTileTok, max(0, pos - a.window + 1 - t0)) : 0;
@@ -718,12 +772,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
           }
           const float top = mx == -kInf ? -kInf : fac * mx;
           const bool grow = top > mf + kSlack;
-          if (__any_sync(0xffffffffu, grow) || shrink != 1.f) {
+          if (__any_sync(0xffffffffu, grow) || vnow != vmul) {
+            const float shrink = vmul == 0.f ? 1.f : vnow / vmul;
+            vmul = vnow;
             const float now = grow ? top : mf;
             const float f = mf == -kInf ? 1.f : exp2_fast(mf - now);
             mf = now;
             l *= f;
-            if (j != 0) {
+            if (j != j0) {
 #pragma unroll 1
               for (int k = 0; k < HD; k += 32) {
                 tmem_ld32(t_o + k, sv);
@@ -760,27 +816,32 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[x]);
         }
-      } else {
-        n += n_here;
       }
+      n += n_here;
       w += n_here;
       stage += n_here;
+      if (stage == it.stages) {
+        stage = -kItemCost;
+        if (w < w1) next_item();
+      }
+      // the scores have been read for the last time, so the next segment's can start beside what follows
+      if (more()) load_queries();
 
       // ---- the segment's result ----
-      const bool whole = n_here == it.stages;
+      const bool whole = n_here == at.stages, direct = whole && !split;
       const bool starts_here = item_at >= w0;
-      float* part = a.part + (size_t)(2 * blockIdx.x + starts_here) * kTileRows * (HD + 2);
+      float* mine = a.part + (size_t)(2 * blockIdx.x + starts_here) * kTileRows * (HD + 2);
       if (active) {
         wait(&o_full[x], nseg & 1);
         nseg++;
         tc_fence_after_sync();
-        const float inv = whole ? (l == 0.f ? 0.f : unscale / l) : unscale;
-        const size_t out_row = (size_t)((it.r0 + q_row / a.group) * a.out_stride) + (size_t)(it.head * a.group + q_row % a.group) * HD;
+        const float inv = direct ? (l == 0.f ? 0.f : unscale / l) : unscale;
+        const size_t out_row = (size_t)((at.r0 + q_row / a.group) * a.out_stride) + (size_t)(at.head * a.group + q_row % a.group) * HD;
 #pragma unroll 1
         for (int k = 0; k < HD / 32; k++) {
           uint32_t sv[32];
           tmem_ld32(t_o + k * 32, sv);
-          if (row < row_n) {
+          if (lrow < row_n) {
             float y[32];
 #pragma unroll
             for (int h = 0; h < 2; h++)
@@ -790,7 +851,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
 #pragma unroll
               for (int i = 0; i < 32; i++) y[i] = l;
             }
-            if (whole) {
+            if (direct) {
               uint16_t* o = static_cast<uint16_t*>(a.out) + out_row + k * 32;
 #pragma unroll
               for (int i = 0; i < 32; i += 8) {
@@ -808,58 +869,84 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
             } else {
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
-                __stcg(reinterpret_cast<float4*>(part + (size_t)row * HD + k * 32 + i),
+                __stcg(reinterpret_cast<float4*>(mine + (size_t)row * HD + k * 32 + i),
                        make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]));
             }
           }
         }
         tc_fence_before_sync();
-        if (!whole && row < row_n)
-          __stcg(reinterpret_cast<float2*>(part + (size_t)kTileRows * HD + 2 * row), make_float2(mf - kLift, l));
       }
-      if (!whole) {
-        const int b0 = (int)(item_at / per), b1 = (int)((item_at + it.stages - 1) / per);
+      if (!direct) {
+        if (lrow < row_n)  // a half without work has seen nothing
+          __stcg(reinterpret_cast<float2*>(mine + (size_t)kTileRows * HD + 2 * row), make_float2(mf - kLift, l));
+        const int b0 = (int)(item_at / per), b1 = (int)((item_at + at.stages - 1) / per);
         __threadfence();
         named_sync(1, kSoftThreads);
-        if (tid == 0) {
-          const int old = atomicAdd(a.count + b0, 1);
-          s_last = old == b1 - b0;
-          if (old == b1 - b0) atomicExch(a.count + b0, 0);
-          __threadfence();
+        if (!whole) {
+          if (tid == 0) {
+            const int old = atomicAdd(a.count + b0, 1);
+            s_last = old == b1 - b0;
+            if (old == b1 - b0) atomicExch(a.count + b0, 0);
+            __threadfence();
+          }
+          named_sync(1, kSoftThreads);
         }
-        named_sync(1, kSoftThreads);
-        if (s_last) {
-          for (int i = tid; i < row_n * (HD / 4); i += kSoftThreads) {
-            const int rr = i / (HD / 4), d = (i % (HD / 4)) * 4;
-            float mm = -kInf, ll = 0.f;
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (whole || s_last) {
+          // a warp sums a row at a time, four rows and two parts in flight
+          const int sides = split ? 2 : 1, parts = (b1 - b0 + 1) * sides;
+          constexpr int kAcross = HD / 4, kStep = kSoftThreads / kAcross;
+          const int d = tid % kAcross * 4;
+          auto slot = [&](int k) { return a.part + (size_t)(2 * (b0 + k / sides) + (k / sides == 0)) * kTileRows * (HD + 2); };
+          for (int r0 = tid / kAcross; r0 < row_n; r0 += 4 * kStep) {
+            float mm[4], ll[4];
+            float4 y[4];
+#pragma unroll
+            for (int q = 0; q < 4; q++) mm[q] = -kInf, ll[q] = 0.f, y[q] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-            for (int k = b0; k <= b1; k++) {
-              const float* pk = a.part + (size_t)(2 * k + (k == b0)) * kTileRows * (HD + 2);
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(pk + (size_t)kTileRows * HD + 2 * rr));
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(pk + (size_t)rr * HD + d));
-              const float now = fmaxf(mm, ml.x);
-              const float fo = mm == -kInf ? 0.f : exp2_fast(mm - now), fn = ml.x == -kInf ? 0.f : exp2_fast(ml.x - now);
-              const float gn = ml.y == ml.y ? fn : 1.f, go = ll == ll ? fo : 1.f;
-              mm = now;
-              ll = ll * go + ml.y * gn;
-              y.x = y.x * go + v.x * gn, y.y = y.y * go + v.y * gn, y.z = y.z * go + v.z * gn, y.w = y.w * go + v.w * gn;
+            for (int k = 0; k < parts; k++) {
+              const float* p = slot(k);
+              float2 ml[4];
+              float4 v[4];
+#pragma unroll
+              for (int q = 0; q < 4; q++) {
+                const int rr = min(r0 + q * kStep, row_n - 1) + (k % sides) * kHalf;
+                ml[q] = __ldcg(reinterpret_cast<const float2*>(p + (size_t)kTileRows * HD + 2 * rr));
+                v[q] = __ldcg(reinterpret_cast<const float4*>(p + (size_t)rr * HD + d));
+              }
+#pragma unroll
+              for (int q = 0; q < 4; q++) {
+                const float now = fmaxf(mm[q], ml[q].x);
+                const float f = ml[q].y != ml[q].y ? 1.f : ml[q].x == -kInf ? 0.f : exp2_fast(ml[q].x - now);
+                const float g = ll[q] != ll[q] ? 1.f : mm[q] == -kInf ? 0.f : exp2_fast(mm[q] - now);
+                mm[q] = now;
+                ll[q] *= g;
+                y[q].x *= g, y[q].y *= g, y[q].z *= g, y[q].w *= g;
+                if (f != 0.f) {  // what a half without work did not write is not used
+                  ll[q] = fmaf(ml[q].y, f, ll[q]);
+                  y[q].x = fmaf(v[q].x, f, y[q].x), y[q].y = fmaf(v[q].y, f, y[q].y);
+                  y[q].z = fmaf(v[q].z, f, y[q].z), y[q].w = fmaf(v[q].w, f, y[q].w);
+                }
+              }
             }
-            const float inv = ll == 0.f ? 0.f : 1.f / ll;
-            const long long qr = (long long)it.tile * kTileRows + rr;
-            uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)((it.r0 + qr / a.group) * a.out_stride) +
-                          (size_t)(it.head * a.group + qr % a.group) * HD + d;
-            o[0] = f32_to_bf16_rn(y.x * inv);
-            o[1] = f32_to_bf16_rn(y.y * inv);
-            o[2] = f32_to_bf16_rn(y.z * inv);
-            o[3] = f32_to_bf16_rn(y.w * inv);
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+              const int rr = r0 + q * kStep;
+              if (rr >= row_n) continue;
+              const float inv = ll[q] == 0.f ? 0.f : 1.f / ll[q];
+              const long long qr = (long long)at.tile * kTileRows + rr;
+              uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)((at.r0 + qr / a.group) * a.out_stride) +
+                            (size_t)(at.head * a.group + qr % a.group) * HD + d;
+              const uint32_t lo = f32_to_bf16_rn(y[q].x * inv) | ((uint32_t)f32_to_bf16_rn(y[q].y * inv) << 16);
+              const uint32_t hi = f32_to_bf16_rn(y[q].z * inv) | ((uint32_t)f32_to_bf16_rn(y[q].w * inv) << 16);
+              if (a.vec_out) {
+                *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
+              } else {
+                o[0] = (uint16_t)lo, o[1] = (uint16_t)(lo >> 16), o[2] = (uint16_t)hi, o[3] = (uint16_t)(hi >> 16);
+              }
+            }
           }
         }
         named_sync(1, kSoftThreads);
-      }
-      if (stage == it.stages) {
-        stage = 0;
-        if (w < w1) next_item();
       }
     }
   }
