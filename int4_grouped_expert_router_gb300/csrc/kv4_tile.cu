@@ -49,7 +49,7 @@ constexpr float kLift = 9.f;
 constexpr float kInf = __builtin_huge_valf();
 // What an item costs beside its stages, in stages: it counts in the shares, ahead of the item's first stage.
 #ifndef COLI_KV4_TILE_COST
-#define COLI_KV4_TILE_COST 2
+#define COLI_KV4_TILE_COST 4
 #endif
 constexpr int kItemCost = COLI_KV4_TILE_COST;
 
@@ -550,8 +550,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
     const uint32_t v_base0 = smem_u32(s_v) + (cw / 4) * (HD * 128) + r * 128 + cc * 4;
     const uint8_t* unit = s_raw + cw * T::kUnit;
     float kmul = 0.f, vmul = 0.f;  // keys and values are multiplied by them; they only shrink within a segment
+    float kinv = 1.f, vinv = 0.f;  // 1 / kmul, 1 / vmul
     for (uint32_t n = 0; more(); n++) {
-      if (n == 0 || stage == 0) kmul = vmul = 0.f;
+      if (n == 0 || stage == 0) kmul = vmul = vinv = 0.f, kinv = 1.f;
       const int left = it.len - (it.first + stage) * kTileTok - cw * 16;  // tokens of this unit that exist
       wait(&raw_full, n & 1);
       // codes of tokens r, r + 8 (keys) and of token pairs c, c + 4 (values), with their scales and offsets
@@ -594,15 +595,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
           kbig = fmaxf(kbig, s_big[0][i]);
           vbig = fmaxf(vbig, s_big[1][i]);
         }
-        if (too_big(kbig, kmul)) kmul = below_2_14(kbig);
-        if (too_big(vbig, vmul)) vmul = below_2_14(vbig);
+        if (too_big(kbig, kmul)) kmul = below_2_14(kbig), kinv = 1.f / kmul;
+        if (too_big(vbig, vmul)) vmul = below_2_14(vbig), vinv = 1.f / vmul;
       }
       // ---- keys: odd tokens store the words of a pair in the other order: eight lanes then cover all banks ----
       wait(&k_empty[n & 1], ((n >> 1) & 1) ^ 1);
       if (cw == 0 && lane == 0) {  // the softmax of four stages ago is long done
-        s_par[n & 3][0] = kmul == 0.f ? 1.f : 1.f / kmul;
+        s_par[n & 3][0] = kinv;
         s_par[n & 3][1] = vmul;
-        s_par[n & 3][2] = vmul == 0.f ? 0.f : 1.f / vmul;
+        s_par[n & 3][2] = vinv;
         mbar_arrive(&par_full[n & 3]);
       }
       const uint32_t k_base = k_base0 + (n & 1) * T::kK;
