@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libcoli_moe.so")
 SOURCES = ["api.cu", "router.cu", "experts.cu", "decode.cu", "prefill.cu", "ep.cu", "ans.cu",
-           "kv4.cu", "kv4_attn.cu", "kv4_tile.cu", "norm.cu"]
+           "kv4.cu", "kv4_attn.cu", "kv4_attn_f32.cu", "kv4_tile.cu", "norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I" + INCLUDE]
