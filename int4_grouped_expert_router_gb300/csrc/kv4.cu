@@ -66,23 +66,42 @@ struct Place {
   bool there;  // and has a place: a position that is not negative, a page of the cache
 };
 
-// The places of rows row0, row0 + 1, ..: lane l finds that of row0 + l, l < n.
+// The places of rows row0, row0 + 1, ..: lane l finds that of row0 + l, l < n (n at most kMostRows).
+constexpr int kMostRows = 4;
 __device__ __forceinline__ Place kv4_places(const RowArgs& a, int row0, int n) {
   const int lane = threadIdx.x & 31, row = row0 + lane;
+  const bool mine = lane < n && row < a.p.T;
   Place at{0, 0, false, false};
-  int b = warp_seq_of(a.p, row0);
-  if (lane >= n || row >= a.p.T) return at;
-  if (a.p.q_start) {
-    while (b + 1 < a.p.B && __ldcg(a.p.q_start + b + 1) <= row) b++;  // a few steps: rows are neighbours
+  int b = row, r0 = row, r1 = row + 1, len = 0;
+  if (!a.p.q_start) {
+    if (mine) len = __ldcg(a.p.lens + b);
+  } else if (a.p.B < 32) {
+    // the whole plan in the warp's registers: one round trip
+    const int start = lane <= a.p.B ? __ldcg(a.p.q_start + lane) : 0;
+    const int length = lane < a.p.B ? __ldcg(a.p.lens + lane) : 0;
+#pragma unroll
+    for (int l = 0; l < kMostRows; l++) {
+      const unsigned le = __ballot_sync(0xffffffffu, lane < a.p.B && start <= row0 + l);
+      const int at_l = max(0, __popc(le) - 1);
+      const int from = __shfl_sync(0xffffffffu, start, at_l), to = __shfl_sync(0xffffffffu, start, at_l + 1);
+      const int have = __shfl_sync(0xffffffffu, length, at_l);
+      if (lane == l) b = at_l, r0 = from, r1 = to, len = have;
+    }
   } else {
-    b = row;
+    b = warp_seq_of(a.p, row0);
+    if (mine) {
+      while (b + 1 < a.p.B && __ldcg(a.p.q_start + b + 1) <= row) b++;  // a few steps: rows are neighbours
+      r0 = __ldcg(a.p.q_start + b);
+      r1 = __ldcg(a.p.q_start + b + 1);
+      len = __ldcg(a.p.lens + b);
+    }
   }
-  int r0, r1;
-  kv4_rows(a.p, b, r0, r1, a.err);
-  at.owned = row >= r0 && row < r1;
-  if (!at.owned) return at;
-  const int pos = kv4_len(a.p, a.c.page_log2, b, a.err) - (r1 - row);
-  if (pos < 0) return at;
+  // a range or a length that does not fit is reported by kv4_check_plan
+  at.owned = mine && r0 >= 0 && r1 <= a.p.T && row >= r0 && row < r1;
+  const long long most = (long long)a.p.table_stride << a.c.page_log2;
+  len = len < 0 ? 0 : len > most ? (int)most : len;
+  const int pos = len - (r1 - row);
+  if (!at.owned || pos < 0) return at;
   at.page = __ldcg(a.p.table + (size_t)b * a.p.table_stride + (pos >> a.c.page_log2));
   at.off = pos & ((1 << a.c.page_log2) - 1);
   at.there = at.page >= 0 && at.page < a.c.pages;
@@ -387,7 +406,7 @@ int launch_rows(coli_ctx* ctx, const char* who, const Kv4View& c, const Kv4Plan&
   // several slots a warp where that still gives every SM's schedulers a few warps
   const bool bf16 = dtype == COLI_DTYPE_BF16;
   const int chunks = (c.heads * c.hd + kChunk - 1) / kChunk;
-  const int slots = (long long)p.T * chunks >= (long long)most_slots(bf16) * 16 * ctx->num_sms ? most_slots(bf16) : 1;
+  const int slots = (long long)p.T * chunks >= (long long)most_slots(bf16) * 8 * ctx->num_sms ? most_slots(bf16) : 1;
   a.across = 0;
   while ((2 << a.across) <= slots && (1 << a.across) < chunks) a.across++;
   a.groups = (chunks + (1 << a.across) - 1) >> a.across;

@@ -90,6 +90,11 @@ struct Cfg {
   // Values enter the product dequantised where several tiles of rows share the work of it (bf16: 11 bits); otherwise as
   // codes, with a group's scale on the weight.
   static constexpr bool kDeq = !F32 && NT > 1;
+  // Key codes enter as they lie (0..15) for bf16 queries; centred for f32 ones, whose scores would lose two bits to the
+  // larger sums.
+  static constexpr bool kRawK = !F32;
+  static constexpr float kOdd = kRawK ? 0.0625f : 1.f;           // queries of codes at bit 4, which count sixteenfold
+  static constexpr float kUnitK = kRawK ? 16777216.f : 1.f;      // a code is this many times what enters
   // Value codes enter as they lie (0..15), which needs the sums cut short: the instruction cuts its accumulator off
   // instead of rounding it, and codes that are not centred make the sum large beside the result.
   static constexpr bool kRawV = !F32 && NT == 1;
@@ -504,10 +509,10 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
         sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
 #pragma unroll
-        for (int e = 0; e < 2; e++) sumq[nt][e][g] = 5.9604645e-8f * __shfl_sync(0xffffffffu, sum[g], (2 * cc + e) * 4);
+        for (int e = 0; e < 2; e++) sumq[nt][e][g] = (1.f / C::kUnitK) * __shfl_sync(0xffffffffu, sum[g], (2 * cc + e) * 4);
       }
-      // scores come in units of 2^-24 (expand_raw); not 0: minus infinity stays it
-      const float f = fmaxf(fabsf(a.scale) * 1.4426950408889634f * inv * 16777216.f, 1e-37f);
+      // not 0: minus infinity stays it
+      const float f = fmaxf(fabsf(a.scale) * 1.4426950408889634f * inv * C::kUnitK, 1e-37f);
 #pragma unroll
       for (int e = 0; e < 2; e++) {
         fac[nt][e] = __shfl_sync(0xffffffffu, f, (2 * cc + e) * 4);
@@ -522,8 +527,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         for (int h = 0; h < 2; h++) {
           if ((2 * i + h) % kStageUnits != warp) continue;
           const int at = (nt * (HD / 16) + 2 * i + h) * 32 + lane;
-          // codes at bit 4 count sixteenfold (expand_raw)
-          const float v1 = v[i][2 * h + 1] * 0.0625f, v5 = v[i][2 * h + 5] * 0.0625f;
+          const float v1 = v[i][2 * h + 1] * C::kOdd, v5 = v[i][2 * h + 5] * C::kOdd;
           const uint32_t b0 = pack_half2(v[i][2 * h], v[i][2 * h + 4]), b1 = pack_half2(v1, v5);
           s_q[at] = make_uint2(b0, b1);
           if constexpr (F32) {
@@ -590,8 +594,13 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
 #pragma unroll
           for (int i = g * C::kWpg; i < (g + 1) * C::kWpg; i++) {
             uint32_t a0[4], a1[4];
-            expand_raw(kw[0][i], a0);
-            expand_raw(kw[1][i], a1);
+            if constexpr (C::kRawK) {
+              expand_raw(kw[0][i], a0);
+              expand_raw(kw[1][i], a1);
+            } else {
+              expand(kw[0][i], a0);
+              expand(kw[1][i], a1);
+            }
 #pragma unroll
             for (int h = 0; h < 2; h++)
 #pragma unroll
@@ -608,7 +617,11 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
               }
           }
           const float ks[2] = {lo_bf16(kp[0][g]), lo_bf16(kp[1][g])};
-          const float ko[2] = {fmaf(-8.f, ks[0], hi_bf16(kp[0][g])), fmaf(-8.f, ks[1], hi_bf16(kp[1][g]))};  // of code 0
+          float ko[2] = {hi_bf16(kp[0][g]), hi_bf16(kp[1][g])};
+          if constexpr (C::kRawK) {  // of code 0
+            ko[0] = fmaf(-8.f, ks[0], ko[0]);
+            ko[1] = fmaf(-8.f, ks[1], ko[1]);
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; nt++)
 #pragma unroll
