@@ -936,9 +936,10 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
       // CTAs sums the run into its first slot, the last run to arrive sums the runs. Every load of a level is
       // independent of the others.
       const int c0 = (int)(item_at / per), c1 = (int)((item_at + it.stages - 1) / per), parts = c1 - c0 + 1;
-      const int me = blockIdx.x, lead = parts > kGroup ? c0 + (me - c0) / kGroup * kGroup : c0;
-      const int runs = parts > kGroup ? (parts + kGroup - 1) / kGroup : 1;
-      const int run = min(kGroup, c1 - lead + 1);  // parts of this CTA's run
+      const bool two = parts > 2 * kGroup;  // a second level costs about as much as one more round of loads
+      const int me = blockIdx.x, lead = two ? c0 + (me - c0) / kGroup * kGroup : c0;
+      const int runs = two ? (parts + kGroup - 1) / kGroup : 1;
+      const int run = two ? min(kGroup, c1 - lead + 1) : parts;  // parts of this CTA's run
       constexpr int kItems = (C::kRows * (HD / 4) + kConsumers - 1) / kConsumers;
       auto slot_of = [&](int k) { return a.part + (size_t)(2 * k + (k == c0)) * C::kRows * (HD + 2); };
       auto last_of = [&](int* count, int n) {  // this CTA's parts are written; true in the last of n to say so
