@@ -61,9 +61,10 @@ __device__ __forceinline__ int warp_seq_of(const Kv4Plan& p, int row) {
 
 // Where a row lives.
 struct Place {
-  int page, off;
-  bool owned;  // the row belongs to a sequence
-  bool there;  // and has a place: a position that is not negative, a page of the cache
+  uint64_t at;  // offset in the cache of the unit of head 0
+  int t;        // token of the unit
+  bool owned;   // the row belongs to a sequence
+  bool there;   // and has a place: a position that is not negative, a page of the cache
 };
 
 // The places of rows row0, row0 + 1, ..: lane l finds that of row0 + l, l < n (n at most kMostRows).
@@ -102,17 +103,18 @@ __device__ __forceinline__ Place kv4_places(const RowArgs& a, int row0, int n) {
   len = len < 0 ? 0 : len > most ? (int)most : len;
   const int pos = len - (r1 - row);
   if (!at.owned || pos < 0) return at;
-  at.page = __ldcg(a.p.table + (size_t)b * a.p.table_stride + (pos >> a.c.page_log2));
-  at.off = pos & ((1 << a.c.page_log2) - 1);
-  at.there = at.page >= 0 && at.page < a.c.pages;
+  const int page = __ldcg(a.p.table + (size_t)b * a.p.table_stride + (pos >> a.c.page_log2));
+  at.there = page >= 0 && page < a.c.pages;
+  if (at.there) at.at = kv4_unit(a.c, page, 0, pos & ((1 << a.c.page_log2) - 1)) - a.c.base;
+  at.t = pos & (kKvUnit - 1);
   if (!at.there) set_error(a.err, COLI_E_RANGE);
   return at;
 }
 
 // Lane l's place, in every lane.
 __device__ __forceinline__ Place place_of(const Place& at, int l) {
-  const int flags = __shfl_sync(0xffffffffu, (int)at.owned | (int)at.there << 1, l);
-  return Place{__shfl_sync(0xffffffffu, at.page, l), __shfl_sync(0xffffffffu, at.off, l), (flags & 1) != 0, (flags & 2) != 0};
+  const int rest = __shfl_sync(0xffffffffu, (int)at.owned | (int)at.there << 1 | at.t << 2, l);
+  return Place{__shfl_sync(0xffffffffu, at.at, l), rest >> 2, (rest & 1) != 0, (rest & 2) != 0};
 }
 
 __device__ __forceinline__ float max_nan(float x, float y) {
@@ -306,8 +308,8 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(RowArgs a) {
     const Place to = place_of(places, n >> a.across);
     if (!to.there || w.chunk(n) * kChunk >= a.c.heads * HD) continue;  // uniform
     const Spot<HD> s(w.chunk(n), a.c.heads);
-    uint8_t* at = const_cast<uint8_t*>(kv4_unit(a.c, to.page, 0, to.off));
-    const int t = to.off & 15;
+    uint8_t* at = a.c.base + to.at;
+    const int t = to.t;
     uint32_t pk, pv;
     const uint32_t nk = quantise<BF16, kGl>(xk[n], pk, s.in, a.err), nv = quantise<BF16, kGl>(xv[n], pv, s.in, a.err);
     // A token's half of a value word holds two channels below 16 of a run of 32 and the two 16 above: bytes of two
@@ -354,14 +356,16 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(RowArgs a) {
   const Place places = kv4_places(a, w.row0, w.rows);
   const uint32_t head_bytes = (uint32_t)(1 << (a.c.page_log2 - 4)) * kv4_unit_bytes(HD, NG);
   uint32_t nk[kSlots], nv[kSlots], pk[kSlots], pv[kSlots];
+  bool owned[kSlots];
 #pragma unroll
   for (int n = 0; n < kSlots; n++) {
     const Place from = place_of(places, n >> a.across);
+    owned[n] = from.owned;
     const Spot<HD> s(w.chunk(n), a.c.heads);
     nk[n] = nv[n] = pk[n] = pv[n] = 0;
     if (!s.in || !from.there) continue;
-    const uint8_t* at = kv4_unit(a.c, from.page, 0, from.off);
-    const int t = from.off & 15;
+    const uint8_t* at = a.c.base + from.at;
+    const int t = from.t;
     const int i = s.u >> 2, c = s.u & 3, r = 4 * (c & 1) + (c & 2), g = s.u / kGl;
     const uint8_t* unit = at + s.head * head_bytes;
     const uint8_t* v = unit + kv4_v_at(HD, NG) + 2 * (t & 1);
@@ -374,12 +378,11 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(RowArgs a) {
 #pragma unroll
   for (int n = 0; n < kSlots; n++) {
     const Spot<HD> s(w.chunk(n), a.c.heads);
-    const bool owned = place_of(places, n >> a.across).owned;
     const long long row = w.row(n);
     const bool upper = s.u & 2;  // as in the append
     const uint32_t other = __shfl_xor_sync(0xffffffffu, __byte_perm(nv[n], 0, upper ? 0x4420 : 0x4431), 2);
     const uint32_t mine = __byte_perm(nv[n], other, upper ? 0x3154 : 0x5420);
-    if (!s.in || !owned) continue;
+    if (!s.in || !owned[n]) continue;
     float x[8];
     values(nk[n], pk[n], x);
     store8<BF16>(a.k, row * a.k_stride + s.head * HD + 8 * s.u, a.vec, x);

@@ -8,6 +8,8 @@
 // 16-byte vectors of memory even where a row does not start at one (an odd D): the arrays share their
 // offset from such a boundary, so the row is cut at the boundaries of memory and the first and last
 // vector are taken element by element.
+#include <cuda_bf16.h>
+
 #include <type_traits>
 
 #include "norm.h"
@@ -83,7 +85,10 @@ __device__ __forceinline__ void store_vec(void* p, size_t row, int e0, int D, bo
     if constexpr (BF16 && V == 8) {
       uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; i++) w[i] = f32_to_bf16_rn(v[2 * i]) | ((uint32_t)f32_to_bf16_rn(v[2 * i + 1]) << 16);
+      for (int i = 0; i < 4; i++) {
+        const __nv_bfloat162 two = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&two);
+      }
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + row + e0) = make_uint4(w[0], w[1], w[2], w[3]);
       return;
     } else if constexpr (!BF16 && V == 4) {
