@@ -414,9 +414,14 @@ COLI_API int coli_kv4_read(coli_ctx *ctx, const coli_kv4_cache *cache, void *k, 
  * q, out: [T x q_heads x head_dim] in dtype, rows q_stride / out_stride elements apart; q_heads a
  * multiple of heads, at most COLI_MAX_KV_GROUP times it; scale finite; out must not overlap q.
  * Scores, the softmax's maximum and sum, and the output are held in binary32 (bf16 queries: weights
- * enter the product with V in 11 bits; f32: queries and weights in 22; what weighs less than 2^-32 of a
- * row's heaviest value may count as nothing). Results do not change from run to run. A non-finite query sets COLI_E_NONFINITE and gives NaN in its row.
- * Profiled as COLI_KERNEL_ATTENTION.
+ * and, for many rows, keys and values in 11 bits; f32: queries and weights in 22; what weighs less than
+ * 2^-29 of a row's heaviest value may count as nothing). Results do not change from run to run. A non-finite
+ * query sets COLI_E_NONFINITE and gives NaN in its row; a stored NaN that a row sees gives NaN there.
+ * Kernel forms, chosen on the host: up to 16 query rows per sequence and key/value head on average, f32, or
+ * heads of 256 channels: a streaming form that reads the cache once per 16 rows; otherwise 256-row tiles on the
+ * tensor cores. Each splits long sequences over the device. The first call of a shape sizes the workspace (it
+ * may allocate and wait for the stream): run one before any stream capture. A wait inside a kernel is bounded
+ * (2 s), after which the call sets COLI_E_TIMEOUT and its output is void. Profiled as COLI_KERNEL_ATTENTION.
  */
 COLI_API int coli_kv4_attention(coli_ctx *ctx, const coli_kv4_cache *cache, const void *q, long long q_stride,
                                 int dtype, int q_heads, int T, const int32_t *q_start, const int32_t *lens, int B,

@@ -1,28 +1,36 @@
-// Attention over the 4-bit key/value cache (layout: kv4.h), for decode steps, drafts and short prompts.
+// Attention over the 4-bit key/value cache (layout: kv4.h), for decode steps and the few rows of drafts.
 //
 // For a query row q at position p of its sequence and the visible positions t,
 //   x_t = scale sum_g [ s_tg q_g . (n_tg - 8) + o_tg sum(q_g) ],   out = sum_t a_t V_t / sum_t a_t,
 //   a_t = exp(x_t - max x),   sum_t a_t V_t = sum_t (a_t s_tg) (n_tg - 8) + sum_t a_t o_tg,
-// one pass over the tokens with a running maximum and sum. The codes enter the matrix instructions as
-// the small integers n - 8 that they are (exact in 16 bits), so nothing is dequantised: a group's
-// scale and offset are applied to the score of its token, and to the weight a_t before V.
+// one pass over the tokens with a running maximum and sum. The codes enter the matrix instructions as the small
+// integers that they are (exact in 16 bits): a group's scale and offset are applied to the score of its token, and to
+// the weight a_t before V. Queries enter in 16 bits after a power of two has brought a row's largest to 2^14 (bf16
+// ones then are exact down to 2^-29 of it); f32 queries and weights enter as a sum of two 16-bit values.
 //
-// What bounds it: the cache's bytes, read once (a key/value head's codes serve all of its query heads).
+// What bounds it: the cache's bytes, read once (a key/value head's codes serve all of its query heads), and beside
+// them the instructions that unpack codes and weigh tokens, about 330 per 16 tokens of a head (hd = 128, one group):
+// with every copy left out the kernel takes as long, with the arithmetic left out 0.6 of its time.
 //
-// Work split. An item is (sequence, key/value head, tile of 8 NT query rows); its tokens are cut into
-// stages of 64, and all items' stages, end to end, are dealt out evenly and contiguously to a grid that
-// fills the device: whatever the lengths, every CTA streams the same number of bytes. An item that
-// spans CTAs leaves partial (maximum, sum, output) triples in the workspace, and the CTA that arrives
-// last adds them up in CTA order, so that results do not depend on who is last.
+// Work split. An item is (sequence, key/value head, tile of 8 NT query rows); its tokens are cut into stages of 64,
+// and all items' stages, end to end, are dealt out evenly and contiguously to a grid that fills the device, each item
+// counting kItemCost stages more: whatever the lengths, every CTA has the same work. An item that spans CTAs leaves
+// partial (maximum, sum, output) triples in the workspace, and whoever arrives last adds them up in CTA order, so that
+// results do not depend on who is last.
 //
-// In a CTA a producer warp fills a ring of stages with bulk copies, a run of units of a page each (64
-// tokens are 8.7 KB at hd = 128, gs = 128: codes and scales of keys and values together), and four
-// consumer warps take one unit (16 tokens) of each stage, with their own running maximum and sum; they
-// are joined in shared memory when the item ends.
+// In a CTA a producer warp fills a ring of stages with bulk copies, a run of units of a page each (64 tokens are
+// 8.7 KB at hd = 128, gs = 128: codes and scales of keys and values together), and four consumer warps take one unit
+// (16 tokens) of each stage, with their own running maximum and sum; they are joined in shared memory when the item
+// ends. Three CTAs share an SM: one joins while the others compute (one CTA of twelve warps took 1.4 times as long on
+// a batch of 64).
 //
-// Consumer, per unit: S^T = K q^T with m16n8k16 (rows = 16 tokens, columns = 8 query rows: group sizes
-// up to 8 fill the instruction, where queries as rows would leave half of it empty), the softmax on the
-// accumulators, the weights transposed in registers (movmatrix), O^T += V^T a (rows = 16 channels).
+// Consumer, per unit: S^T = K q^T with m16n8k16 (rows = 16 tokens, columns = 8 query rows: group sizes up to 8 fill
+// the instruction, where queries as rows would leave half of it empty), the softmax on the accumulators, the weights
+// transposed in registers (movmatrix), O^T += V^T a (rows = 16 channels).
+//
+// Measured (bf16, hd 128, a copy's rate being 6782 GB/s): 64 requests of up to 8192 tokens, 8 heads of 8, gs 64:
+// 83 us, 3.7 TB/s; 131071 tokens of one request, gs 128: 42 us, 3.4 TB/s; a request of 1003 tokens: 10 us, of which
+// the launch, the dealing out, the queries and the joining of 16 parts are all but one.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -51,6 +59,7 @@ struct AttnArgs {
   int* count;     // arrivals: 2 per CTA for the run of parts whose sum its slot takes, then 1 per CTA for the runs of an item
   int* err;
   uint64_t wait_ns;
+  bool withhold;  // test hook: the call's first copy is withheld, and the waits on it give up
 };
 
 // One translation unit per type of the activations (kv4_attn.cu, kv4_attn_f32.cu): they compile side by side.
@@ -382,6 +391,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
     int slot = 0;
     uint32_t phase = 1;
     bool lost = false;
+    int fills = 0;  // of this lane's slot (lane < kStages)
     while (!lost) {
       if (stage < 0) w -= stage, stage = 0;
       if (w >= w1) break;
@@ -406,7 +416,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         mine -= C::kStages;
         my_phase ^= 1;
       }
-      bool done = lane >= n;
+      const bool held = a.withhold && w == kItemCost && lane == 0;
+      bool done = lane >= n || held;
       const uint64_t t0 = globaltimer_ns();
       while (!done) {
         if (mbar_test_wait(&s_empty[mine], my_phase)) {
@@ -422,6 +433,9 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
           lost = done = true;  // what was issued is still awaited by the consumers
         }
       }
+      // the slots of this round that were filled, from `slot` on: this lane's is `lane - slot` from there
+      const unsigned filled = __ballot_sync(0xffffffffu, lane < n && !lost && !held);
+      if (lane < C::kStages && (filled >> ((lane - slot + C::kStages) % C::kStages) & 1)) fills++;
       lost = __any_sync(0xffffffffu, lost);
       slot += n;
       if (slot >= C::kStages) {
@@ -435,6 +449,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         if (w < w1) next_item();
       }
     }
+    // no copy is in flight when the CTA ends, even if the consumers gave one up
+    if (lane < C::kStages && fills > 0) mbar_wait(&s_full[lane], (fills - 1) & 1);
     return;
   }
 

@@ -1,26 +1,36 @@
 // Attention over the 4-bit key/value cache (layout: kv4.h) for many query rows of a sequence: prompts and
 // chunks of them, bf16, on the fifth-generation tensor cores.
 //
-// The same formula as kv4_attn.cu, arranged for a bound of arithmetic instead of bytes. An item is a
-// (sequence, tile of 256 query rows, key/value head): a row is a (token, query head) pair, so the heads of a
-// group share the keys and values of their tile. Its visible tokens are cut into stages of 128; all items'
-// stages, end to end, are dealt out evenly and contiguously to one CTA per SM, and an item that spans CTAs is
+// The same formula as kv4_attn.h, arranged for a bound of arithmetic instead of bytes. An item is a (sequence, tile of
+// 256 query rows, key/value head): a row is a (token, query head) pair, so the heads of a group share the keys and
+// values of their tile. Its visible tokens are cut into stages of 128; all items' stages, end to end, are dealt out
+// evenly and contiguously to one CTA per SM (an item counting kItemCost stages more), and an item that spans CTAs is
 // joined by the CTA that arrives last, in CTA order.
 //
 // One CTA, 18 warps:
-//   producer      bulk copies of the stage's packed units into a ring of two
-//   8 converters  codes to 16-bit values o + s (n - 8) in the 128-byte-swizzled operand layout: K with a token
-//                 per row, V^T with a channel per row (the packed value words hold two neighbouring tokens, which
-//                 is the order that operand wants). Rounded once, to 11 bits, after a power of two has brought the
-//                 stage's largest key (value) below 2^14, so that no size of the keys and values is lost.
+//   producer      bulk copies of the stage's packed units
+//   8 converters  codes to 16-bit values o + s (n - 8) in the 128-byte-swizzled operand layout: K with a token per row,
+//                 V^T with a channel per row (the packed value words hold two neighbouring tokens, which is the order
+//                 that operand wants). Rounded once, to 11 bits, after a power of two has brought the largest key
+//                 (value) so far below 2^14, so that no size of the keys and values is lost. Eight bits (bf16) would
+//                 have needed no such factor, but cost the scores an error as large as the queries' own rounding.
 //   MMA           one thread: S_x = Q_x K^T, O_x += P_x V for the two halves x of 128 rows
 //   2 x 4 softmax a thread per row: running maximum (it moves only when passed by kSlack), weights
 //                 p = 2^(y - m + 9) in 16 bits, written over S in tensor memory as the next product's operand
-// While one half's softmax runs, the tensor core works on the other half. Tensor memory is full: S (128
-// columns) and O (hd columns) of both halves.
+// While one half's softmax runs, the tensor core works on the other half. Tensor memory is full: S (128 columns) and O
+// (hd columns) of both halves. A tile of at most 128 rows would leave one half idle: both then hold its queries, take
+// alternate stages and are joined like the parts of an item.
 //
-// K's channels lie in the order 0 4 1 5 2 6 3 7 within every eight, as the codes unpack, and Q's with them; V^T's
-// rows, the output's columns, in the order 0 2 .. 14 1 3 .. 15 within every sixteen, which the store undoes.
+// K's channels lie in the order 0 4 1 5 2 6 3 7 within every eight, as the codes unpack, and Q's with them; V^T's rows,
+// the output's columns, in the order 0 2 .. 14 1 3 .. 15 within every sixteen, which the store undoes.
+//
+// Measured: 2 x 2048 tokens over 10007, 32 heads on 8, hd 128, gs 64: 481 us, 925 TFLOP/s (0.48 of a cuBLAS bf16
+// product's rate); tensor pipe active 40 %. No single part binds: without the weights' exponentials and stores 399 us,
+// without the converters' stores 486 us, without one of the two products about 470 us; a stage takes 2.0 us, about
+// what the softmax of a half and the converters each need with the issue slots they share. What it cost to find: loops
+// unrolled beyond the instruction cache took 1068 us, matrix instructions issued with operands in plain registers (110
+// cycles each instead of 45) 589 us. Measured and dropped: the row's scores all in registers (672 us), two threads per
+// row (591 us), converters split into key and value warps (544 us), bulk register moves between warpgroups (no change).
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -78,6 +88,7 @@ struct TileArgs {
   int* count;
   int* err;
   uint64_t wait_ns;
+  bool withhold;  // test hook: the call's first copy is withheld, and the waits on it give up
 };
 
 struct Item {
@@ -411,6 +422,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
     // ------------------------------------ producer ------------------------------------
     const int page_tok = 1 << a.c.page_log2;
     int cached_b = -1, cached_from = 0, pages = 0;
+    uint32_t fills = 0;
     for (uint32_t n = 0; more(); n++) {
       const int tok = (it.first + stage) * kTileTok;
       const int units = min(kTileUnits, max(0, (it.len - tok + kKvUnit - 1) / kKvUnit));
@@ -423,11 +435,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         pages = page + lane < a.p.table_stride ? __ldcg(a.p.table + (size_t)it.b * a.p.table_stride + page + lane) : 0;
       }
       wait(&raw_empty, (n & 1) ^ 1);
-      if (!alive) break;  // what was issued is still awaited by the converters
-      if (lane == 0) mbar_arrive_expect_tx(&raw_full, units * T::kUnit);
+      if (__any_sync(0xffffffffu, !alive)) break;
+      const bool held = a.withhold && w == kItemCost;
+      if (lane == 0 && !held) mbar_arrive_expect_tx(&raw_full, units * T::kUnit);
+      fills += !held;
       __syncwarp();
       int pg = __shfl_sync(0xffffffffu, pages, (page - cached_from + lane) & 31);
-      if (lane < copies) {
+      if (lane < copies && !held) {
         if (pg < 0 || pg >= a.c.pages) {
           set_error(a.err, COLI_E_RANGE);
           pg = 0;  // some page of the cache in its place
@@ -443,6 +457,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         if (w < w1) next_item();
       }
     }
+    if (fills > 0) mbar_wait(&raw_full, (fills - 1) & 1);  // no copy is in flight when the CTA ends
   } else if (warp == kWarpMma) {
     // -------------------------------------- MMA --------------------------------------
     // One elected lane issues. Its operands are the same in the whole warp, and made so visibly (shuffles): they
@@ -537,9 +552,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
           if (w < w1) next_item();
         }
       }
-      // the last arrivals on these barriers come before the CTA's memory goes
-      wait(&k_empty[(n - 1) & 1], ((n - 1) >> 1) & 1);
-      wait(&v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1);
+      // the last arrivals on these barriers come before the CTA's memory goes, whatever has been given up
+      mbar_wait(&k_empty[(n - 1) & 1], ((n - 1) >> 1) & 1);
+      mbar_wait(&v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1);
     }
     __syncwarp();
   } else if (warp >= kWarpConv) {
@@ -990,6 +1005,8 @@ int launch_kv4_tiles(coli_ctx* ctx, const Kv4View& c, const Kv4Plan& p, const vo
   a.count = ctx->d_kv_count;
   a.err = ctx->d_status;
   a.wait_ns = ctx->wait_ns ? ctx->wait_ns : kWaitLimitNs;
+  a.withhold = ctx->test_withhold > 0;
+  if (a.withhold) ctx->test_withhold--;
   if (c.hd == 64) return c.ng == 1 ? launch_one<64, 1>(ctx, a) : launch_one<64, 2>(ctx, a);
   return c.ng == 1 ? launch_one<128, 1>(ctx, a) : c.ng == 2 ? launch_one<128, 2>(ctx, a) : launch_one<128, 4>(ctx, a);
 }

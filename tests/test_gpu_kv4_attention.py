@@ -228,3 +228,18 @@ def test_refusals(ctx):
         assert call(**wrong) == B.COLI_E_INVAL, wrong
         assert B.coli_last_error(ctx).startswith("kv4_attention")
     assert B.coli_check_error(ctx) == 0
+
+
+@pytest.mark.parametrize("rows", [[1, 1], [40, 100]])
+def test_a_wait_that_gives_up_is_reported_and_leaves_the_context_usable(rows):
+    """The first copy of a call is withheld: the waits on it give up (limit 20 ms), the call ends with an error, and the next
+    call on the same context is right again."""
+    c = Ctx.with_env(COLI_TEST_WAIT_NS=20_000_000, COLI_TEST_WITHHOLD=1)
+    try:
+        b = Batch(c.ctx, [3000, 1500], 2, 128, 64, 64, "bf16")
+        _, q_t = b.queries(rows, 8)
+        b.attend(q_t, rows)
+        assert B.coli_check_error(c.ctx) == B.COLI_E_TIMEOUT
+        check(b, rows, 8)
+    finally:
+        B.coli_destroy(c.ctx)
