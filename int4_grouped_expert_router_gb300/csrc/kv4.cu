@@ -1,9 +1,8 @@
 // Writing tokens into the 4-bit key/value cache and reading them back (layout: kv4.h).
 //
-// Both are bound by memory: the plain rows dominate. A warp takes up to four slots, a slot being 256 channels of a
-// row (eight neighbouring channels per lane): four rows of up to 256 channels, two of up to 512, or 1024 channels
-// of one; one slot where there are too few to fill the device. All its loads are issued together, and the places
-// of its rows are found by as many lanes at once. Codes are written as the layout gives them to a token: a whole
+// Both are bound by memory: the plain rows dominate. A warp takes 256 channels (eight neighbouring ones per
+// lane) of up to four rows; of one row where there are too few to fill the device. All its loads are issued together,
+// and the places of its rows are found by as many lanes at once. Codes are written as the layout gives them to a token: a whole
 // word of keys, and of values the halves of two words. A group of gs channels is gs / 8 neighbouring lanes for keys
 // and values alike. The two lanes whose channels share the value words of a token are two apart.
 //
@@ -34,8 +33,7 @@ struct RowArgs {
   void* v;
   long long k_stride, v_stride;
   bool vec;    // rows start at a 16-byte boundary
-  int groups;  // warps across a row
-  int across;  // log2 of the slots that lie across a row; the others are further rows
+  int groups;  // chunks (and warps) across a row
   int* err;
 };
 
@@ -127,6 +125,16 @@ __device__ __forceinline__ float max_nan(float x, float y) {
   return r;
 }
 
+// Two binary32 values as one 64-bit register pair, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  return (uint64_t)__float_as_uint(x) | (uint64_t)__float_as_uint(y) << 32;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+
 // A lane's eight channels as they lie in memory, and as binary32.
 template <bool BF16>
 struct Eight {
@@ -162,14 +170,9 @@ __device__ __forceinline__ Eight<BF16> load8(const void* p, long long at, bool v
 }
 
 template <bool BF16>
-__device__ __forceinline__ void store8(void* p, long long at, bool vec, const float (&x)[8]) {
+__device__ __forceinline__ void store8(void* p, long long at, bool vec, const Eight<BF16>& x) {
   if constexpr (BF16) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
+    const auto& w = x.w;
     uint16_t* d = static_cast<uint16_t*>(p) + at;
     if (vec)
       *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -179,8 +182,8 @@ __device__ __forceinline__ void store8(void* p, long long at, bool vec, const fl
   } else {
     float* d = static_cast<float*>(p) + at;
     if (vec) {
-      *reinterpret_cast<float4*>(d) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4*>(d + 4) = make_float4(x[4], x[5], x[6], x[7]);
+      *reinterpret_cast<uint4*>(d) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+      *reinterpret_cast<uint4*>(d + 4) = make_uint4(x.w[4], x.w[5], x.w[6], x.w[7]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; j++) d[j] = x[j];
@@ -248,17 +251,37 @@ __device__ __forceinline__ uint32_t quantise(const Eight<BF16>& x, uint32_t& par
     set_error(err, COLI_E_NONFINITE);
   }
   par = sb | (ob << 16);
-  // The quotient is clamped before it is rounded (the bounds are whole numbers). Adding 1.5 2^23 + 8 rounds it to the
-  // nearest integer, ties to even, and leaves its bits as 0x4b400000 + code; sixteenfold sums of those collect the
-  // codes, and the constant's share comes off at the end.
-  constexpr uint32_t kOnes = 0x11111111u;
-  uint32_t n = 0;
+  // Adding 1.5 2^23 + 8 rounds the quotient to the nearest integer, ties to even, and leaves its bits as
+  // 0x4b400000 + code, the code not yet clamped.
+  if constexpr (BF16) {
+    // A group that spans an ulp of its largest has codes within a few tens of 0..15 however o was rounded: they are
+    // clamped two at a time in 16 bits, codes i and i + 4, as their places in the word are 16 bits apart. (The products
+    // stay single: the compiler joins a product of pairs with the sum that follows, and its rounding would be lost.)
+    const uint64_t neg_o = pack2(-o, -o), round = pack2(12582920.f, 12582920.f);
+    uint32_t c[8];
 #pragma unroll
-  for (int i = 7; i >= 0; i--) {
-    const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], o), inv), -8.f), 7.f);
-    n = n * 16u + __float_as_uint(__fadd_rn(q, 12582920.f));
+    for (int i = 0; i < 4; i++) {
+      const uint64_t d = add2(pack2(x[2 * i], x[2 * i + 1]), neg_o);
+      const float q0 = __fmul_rn(__uint_as_float((uint32_t)d), inv), q1 = __fmul_rn(__uint_as_float((uint32_t)(d >> 32)), inv);
+      const uint64_t n = add2(pack2(q0, q1), round);
+      c[2 * i] = (uint32_t)n, c[2 * i + 1] = (uint32_t)(n >> 32);
+    }
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 3; i >= 0; i--) n = n * 16u + __vimin_s16x2_relu(__byte_perm(c[i], c[i + 4], 0x5410), 0x000f000fu);
+    return n;
+  } else {
+    // The quotient is clamped before it is rounded (the bounds are whole numbers); sixteenfold sums collect the codes,
+    // and the constant's share comes off at the end.
+    constexpr uint32_t kOnes = 0x11111111u;
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 7; i >= 0; i--) {
+      const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], o), inv), -8.f), 7.f);
+      n = n * 16u + __float_as_uint(__fadd_rn(q, 12582920.f));
+    }
+    return n - 0x4b400000u * kOnes;
   }
-  return n - 0x4b400000u * kOnes;
 }
 
 // A lane's place in its chunk: head and the lane's number u within it.
@@ -274,17 +297,15 @@ struct Spot {
   }
 };
 
-// A warp's slots.
+// A warp's slots: one chunk of kSlots rows.
+template <int kSlots>
 struct Share {
-  int row0, rows, chunk0, across;
-  __device__ __forceinline__ Share(const RowArgs& a, int slots) : across(a.across) {
+  int row0, chunk;
+  __device__ __forceinline__ Share(const RowArgs& a) {
     const int item = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    rows = slots >> a.across;
-    row0 = item / a.groups * rows;
-    chunk0 = (item % a.groups) << a.across;
+    row0 = item / a.groups * kSlots;
+    chunk = item % a.groups;
   }
-  __device__ __forceinline__ int row(int n) const { return row0 + (n >> across); }
-  __device__ __forceinline__ int chunk(int n) const { return chunk0 + (n & ((1 << across) - 1)); }
 };
 
 template <bool BF16, int HD, int NG, int kSlots>
@@ -293,60 +314,94 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(RowArgs a) {
   griddep_launch_dependents();
   griddep_wait();
   kv4_check_plan(a);
-  const Share w(a, kSlots);
+  const Share<kSlots> w(a);
   if (w.row0 >= a.p.T) return;  // uniform in the warp
+  const Spot<HD> s(w.chunk, a.c.heads);
   Eight<BF16> xk[kSlots] = {}, xv[kSlots] = {};
 #pragma unroll
   for (int n = 0; n < kSlots; n++) {
-    const Spot<HD> s(w.chunk(n), a.c.heads);
-    const long long row = w.row(n);
+    const long long row = w.row0 + n;
     if (row < a.p.T && s.in) {
       xk[n] = load8<BF16>(a.k, row * a.k_stride + s.head * HD + 8 * s.u, a.vec);
       xv[n] = load8<BF16>(a.v, row * a.v_stride + s.head * HD + 8 * s.u, a.vec);
     }
   }
-  const Place places = kv4_places(a, w.row0, w.rows);
-  const uint32_t head_bytes = (uint32_t)(1 << (a.c.page_log2 - 4)) * kv4_unit_bytes(HD, NG);
+  const Place places = kv4_places(a, w.row0, kSlots);
+  const uint32_t head_at = s.head * ((uint32_t)(1 << (a.c.page_log2 - 4)) * kv4_unit_bytes(HD, NG));
+  const int i = s.u >> 2, c = s.u & 3, upper = c >> 1, r = 4 * (c & 1) + 2 * upper;
+  Place to[kSlots];
+  uint32_t two[kSlots];
 #pragma unroll
   for (int n = 0; n < kSlots; n++) {
-    const Place to = place_of(places, n >> a.across);
-    if (!to.there || w.chunk(n) * kChunk >= a.c.heads * HD) continue;  // uniform
-    const Spot<HD> s(w.chunk(n), a.c.heads);
-    uint8_t* at = a.c.base + to.at;
-    const int t = to.t;
+    to[n] = place_of(places, n);
+    if (!to[n].there) continue;  // uniform
     uint32_t pk, pv;
     const uint32_t nk = quantise<BF16, kGl>(xk[n], pk, s.in, a.err), nv = quantise<BF16, kGl>(xv[n], pv, s.in, a.err);
     // A token's half of a value word holds two channels below 16 of a run of 32 and the two 16 above: bytes of two
     // lanes, each of which puts two of the four words together.
-    const int i = s.u >> 2, c = s.u & 3, upper = c >> 1;
     const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? nv & 0xffffu : nv >> 16, 2);
-    const uint32_t two = upper ? __byte_perm(nv, other, 0x3524) : __byte_perm(nv, other, 0x5140);
+    two[n] = upper ? __byte_perm(nv, other, 0x3524) : __byte_perm(nv, other, 0x5140);
     if (!s.in) continue;
-    uint8_t* unit = at + s.head * head_bytes;
+    const int t = to[n].t;
+    uint8_t* unit = a.c.base + to[n].at + head_at;
     *reinterpret_cast<uint32_t*>(unit + kv4_k_word(HD, t, i, c)) = nk;
-    uint8_t* v = unit + kv4_v_at(HD, NG) + 2 * (t & 1);
-    const int r = 4 * (c & 1) + 2 * upper;
-    *reinterpret_cast<uint16_t*>(v + kv4_v_word(HD, t >> 1, r, i)) = (uint16_t)two;
-    *reinterpret_cast<uint16_t*>(v + kv4_v_word(HD, t >> 1, r + 1, i)) = (uint16_t)(two >> 16);
     if (s.u % kGl == 0) {
       const int g = s.u / kGl;
       *reinterpret_cast<uint32_t*>(unit + kv4_kscale_at(HD) + (t * NG + g) * 4) = pk;
       *reinterpret_cast<uint32_t*>(unit + kv4_vscale_at(HD, NG) + (t * NG + g) * 4) = pv;
     }
   }
+  if (!s.in) return;
+  // the value words: whole where the other token is the next row
+  bool done = false;
+#pragma unroll
+  for (int n = 0; n < kSlots; n++) {
+    if (done || !to[n].there) {
+      done = false;
+      continue;
+    }
+    const int t = to[n].t;
+    uint8_t* v = a.c.base + to[n].at + head_at + kv4_v_at(HD, NG);
+    uint8_t *v0 = v + kv4_v_word(HD, t >> 1, r, i), *v1 = v + kv4_v_word(HD, t >> 1, r + 1, i);
+    if (n + 1 < kSlots && (t & 1) == 0 && to[n + 1].there && to[n + 1].at == to[n].at && to[n + 1].t == t + 1) {
+      *reinterpret_cast<uint32_t*>(v0) = __byte_perm(two[n], two[n + 1], 0x5410);
+      *reinterpret_cast<uint32_t*>(v1) = __byte_perm(two[n], two[n + 1], 0x7632);
+      done = true;
+    } else {
+      reinterpret_cast<uint16_t*>(v0)[t & 1] = (uint16_t)two[n];
+      reinterpret_cast<uint16_t*>(v1)[t & 1] = (uint16_t)(two[n] >> 16);
+    }
+  }
 }
 
-// o + s (n - 8) of a word's eight codes: the product is exact, so one rounding.
-__device__ __forceinline__ void values(uint32_t w, uint32_t par, float (&x)[8]) {
-  const float s = __uint_as_float(par << 16), o = __uint_as_float(par & 0xffff0000u);
-  const __half2 bias = __floats2half2_rn(1032.f, 1032.f);
+// o + s (n - 8) of a word's eight codes, rounded once: the product is exact in binary32, and bf16 takes one multiply-add
+// of its own type, for two channels.
+template <bool BF16>
+__device__ __forceinline__ Eight<BF16> values(uint32_t w, uint32_t par) {
+  Eight<BF16> x;
+  if constexpr (BF16) {
+    const __nv_bfloat162 s = as_bf162(__byte_perm(par, 0, 0x1010)), o = as_bf162(__byte_perm(par, 0, 0x3232));
+    const __nv_bfloat162 bias = __floats2bfloat162_rn(-136.f, -136.f);
+    uint32_t v[4];
 #pragma unroll
-  for (int m = 0; m < 4; m++) {
-    const uint32_t t = ((w >> (4 * m)) & 0x000f000fu) | 0x64006400u;  // 1024 + n in 16 bits
-    const __half2 n = __hsub2(*reinterpret_cast<const __half2*>(&t), bias);
-    x[m] = fmaf(s, __low2float(n), o);
-    x[m + 4] = fmaf(s, __high2float(n), o);
+    for (int m = 0; m < 4; m++) {  // channels m and m + 4
+      const uint32_t t = ((w >> (4 * m)) & 0x000f000fu) | 0x43004300u;  // 128 + n in bf16
+      v[m] = bits(__hfma2(__hadd2(as_bf162(t), bias), s, o));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) x.w[i] = __byte_perm(v[2 * i & 3], v[(2 * i & 3) + 1], i < 2 ? 0x5410 : 0x7632);
+  } else {
+    const float s = __uint_as_float(par << 16), o = __uint_as_float(par & 0xffff0000u);
+    const __half2 bias = __floats2half2_rn(1032.f, 1032.f);
+#pragma unroll
+    for (int m = 0; m < 4; m++) {
+      const uint32_t t = ((w >> (4 * m)) & 0x000f000fu) | 0x64006400u;  // 1024 + n in 16 bits
+      const __half2 n = __hsub2(*reinterpret_cast<const __half2*>(&t), bias);
+      x.w[m] = __float_as_uint(fmaf(s, __low2float(n), o));
+      x.w[m + 4] = __float_as_uint(fmaf(s, __high2float(n), o));
+    }
   }
+  return x;
 }
 
 template <bool BF16, int HD, int NG, int kSlots>
@@ -355,43 +410,39 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(RowArgs a) {
   griddep_launch_dependents();
   griddep_wait();
   kv4_check_plan(a);
-  const Share w(a, kSlots);
+  const Share<kSlots> w(a);
   if (w.row0 >= a.p.T) return;
-  const Place places = kv4_places(a, w.row0, w.rows);
-  const uint32_t head_bytes = (uint32_t)(1 << (a.c.page_log2 - 4)) * kv4_unit_bytes(HD, NG);
+  const Spot<HD> s(w.chunk, a.c.heads);
+  const Place places = kv4_places(a, w.row0, kSlots);
+  const uint32_t head_at = s.head * ((uint32_t)(1 << (a.c.page_log2 - 4)) * kv4_unit_bytes(HD, NG));
+  const int i = s.u >> 2, c = s.u & 3, r = 4 * (c & 1) + (c & 2), g = s.u / kGl;
   uint32_t nk[kSlots], nv[kSlots], pk[kSlots], pv[kSlots];
   bool owned[kSlots];
+  // through the first-level cache: the rows of a warp, and of its neighbours, are tokens that share sectors
 #pragma unroll
   for (int n = 0; n < kSlots; n++) {
-    const Place from = place_of(places, n >> a.across);
+    const Place from = place_of(places, n);
     owned[n] = from.owned;
-    const Spot<HD> s(w.chunk(n), a.c.heads);
     nk[n] = nv[n] = pk[n] = pv[n] = 0;
     if (!s.in || !from.there) continue;
-    const uint8_t* at = a.c.base + from.at;
     const int t = from.t;
-    const int i = s.u >> 2, c = s.u & 3, r = 4 * (c & 1) + (c & 2), g = s.u / kGl;
-    const uint8_t* unit = at + s.head * head_bytes;
+    const uint8_t* unit = a.c.base + from.at + head_at;
     const uint8_t* v = unit + kv4_v_at(HD, NG) + 2 * (t & 1);
-    nk[n] = __ldcg(reinterpret_cast<const uint32_t*>(unit + kv4_k_word(HD, t, i, c)));
-    nv[n] = __ldcg(reinterpret_cast<const unsigned short*>(v + kv4_v_word(HD, t >> 1, r, i))) |
-            ((uint32_t)__ldcg(reinterpret_cast<const unsigned short*>(v + kv4_v_word(HD, t >> 1, r + 1, i))) << 16);
-    pk[n] = __ldcg(reinterpret_cast<const uint32_t*>(unit + kv4_kscale_at(HD) + (t * NG + g) * 4));
-    pv[n] = __ldcg(reinterpret_cast<const uint32_t*>(unit + kv4_vscale_at(HD, NG) + (t * NG + g) * 4));
+    nk[n] = *reinterpret_cast<const uint32_t*>(unit + kv4_k_word(HD, t, i, c));
+    nv[n] = *reinterpret_cast<const unsigned short*>(v + kv4_v_word(HD, t >> 1, r, i)) |
+            ((uint32_t)*reinterpret_cast<const unsigned short*>(v + kv4_v_word(HD, t >> 1, r + 1, i)) << 16);
+    pk[n] = *reinterpret_cast<const uint32_t*>(unit + kv4_kscale_at(HD) + (t * NG + g) * 4);
+    pv[n] = *reinterpret_cast<const uint32_t*>(unit + kv4_vscale_at(HD, NG) + (t * NG + g) * 4);
   }
+  const bool upper = s.u & 2;  // as in the append
 #pragma unroll
   for (int n = 0; n < kSlots; n++) {
-    const Spot<HD> s(w.chunk(n), a.c.heads);
-    const long long row = w.row(n);
-    const bool upper = s.u & 2;  // as in the append
+    const long long row = w.row0 + n;
     const uint32_t other = __shfl_xor_sync(0xffffffffu, __byte_perm(nv[n], 0, upper ? 0x4420 : 0x4431), 2);
     const uint32_t mine = __byte_perm(nv[n], other, upper ? 0x3154 : 0x5420);
     if (!s.in || !owned[n]) continue;
-    float x[8];
-    values(nk[n], pk[n], x);
-    store8<BF16>(a.k, row * a.k_stride + s.head * HD + 8 * s.u, a.vec, x);
-    values(mine, pv[n], x);
-    store8<BF16>(a.v, row * a.v_stride + s.head * HD + 8 * s.u, a.vec, x);
+    store8<BF16>(a.k, row * a.k_stride + s.head * HD + 8 * s.u, a.vec, values<BF16>(nk[n], pk[n]));
+    store8<BF16>(a.v, row * a.v_stride + s.head * HD + 8 * s.u, a.vec, values<BF16>(mine, pv[n]));
   }
 }
 
@@ -414,12 +465,9 @@ int launch_rows(coli_ctx* ctx, const char* who, const Kv4View& c, const Kv4Plan&
   const bool bf16 = dtype == COLI_DTYPE_BF16;
   const int chunks = (c.heads * c.hd + kChunk - 1) / kChunk;
   const int slots = (long long)p.T * chunks >= (long long)most_slots(bf16) * 8 * ctx->num_sms ? most_slots(bf16) : 1;
-  a.across = 0;
-  while ((2 << a.across) <= slots && (1 << a.across) < chunks) a.across++;
-  a.groups = (chunks + (1 << a.across) - 1) >> a.across;
+  a.groups = chunks;
   a.err = ctx->d_status;
-  const int rows = slots >> a.across;
-  const long long grid = (((long long)p.T + rows - 1) / rows * a.groups + kWarps - 1) / kWarps;
+  const long long grid = (((long long)p.T + slots - 1) / slots * chunks + kWarps - 1) / kWarps;
   if (grid * kWarps > 0x7fffffffll) return fail(ctx, COLI_E_INVAL, std::string(who) + ": too many rows for one call");
   ProfScope prof(ctx, COLI_KERNEL_CACHE);
   auto kern = bf16 ? (slots > 1 ? kernel_of<READ, true, most_slots(true)>(c.hd, c.ng) : kernel_of<READ, true, 1>(c.hd, c.ng))
