@@ -19,7 +19,7 @@ namespace coli {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 2;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 256;  // channels of a warp's pass
 // Passes of a warp whose loads are in flight together, where there are enough rows (registers: twice as many for bf16).
@@ -194,10 +194,33 @@ __device__ __forceinline__ void store8(void* p, long long at, bool vec, const Ei
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
 __device__ __forceinline__ uint32_t bits(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 
-// Least and largest of a group's channels (GL neighbouring lanes); not a number if one of them is not. bf16
-// values are compared two at a time and travel as one register, the largest and the negated least.
-template <bool BF16, int GL>
-__device__ __forceinline__ void group_range(const Eight<BF16>& x, float& lo, float& hi) {
+// The largest of a few channels and of their negatives; not a number if one of them is not. bf16 values are compared
+// two at a time and travel as one register (largest, -least).
+template <bool BF16>
+struct Range {
+  uint32_t m[BF16 ? 1 : 2];
+
+  __device__ __forceinline__ void join(const Range& x) {
+    if constexpr (BF16) {
+      m[0] = bits(__hmax2_nan(as_bf162(m[0]), as_bf162(x.m[0])));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; i++) m[i] = __float_as_uint(max_nan(__uint_as_float(m[i]), __uint_as_float(x.m[i])));
+    }
+  }
+  __device__ __forceinline__ Range across(int mask) const {  // that of lane ^ mask
+    Range x;
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); i++) x.m[i] = __shfl_xor_sync(0xffffffffu, m[i], mask);
+    return x;
+  }
+  __device__ __forceinline__ float hi() const { return __uint_as_float(BF16 ? m[0] << 16 : m[0]); }
+  __device__ __forceinline__ float lo() const { return -__uint_as_float(BF16 ? m[0] & 0xffff0000u : m[BF16 ? 0 : 1]); }
+};
+
+template <bool BF16>
+__device__ __forceinline__ Range<BF16> range_of(const Eight<BF16>& x) {
+  Range<BF16> r;
   if constexpr (BF16) {
     __nv_bfloat162 most = as_bf162(x.w[0]), least = most;
 #pragma unroll
@@ -205,52 +228,49 @@ __device__ __forceinline__ void group_range(const Eight<BF16>& x, float& lo, flo
       most = __hmax2_nan(most, as_bf162(x.w[i]));
       least = __hmin2_nan(least, as_bf162(x.w[i]));
     }
-    // (largest, -least) of the even channels, and of the odd ones
+    // of the even channels, and of the odd ones
     const uint32_t neg = bits(least) ^ 0x80008000u;
-    __nv_bfloat162 m = __hmax2_nan(as_bf162(__byte_perm(bits(most), neg, 0x5410)), as_bf162(__byte_perm(bits(most), neg, 0x7632)));
-#pragma unroll
-    for (int s = 1; s < GL; s <<= 1) m = __hmax2_nan(m, as_bf162(__shfl_xor_sync(0xffffffffu, bits(m), s)));
-    hi = __low2float(m);
-    lo = -__high2float(m);
+    r.m[0] = __byte_perm(bits(most), neg, 0x5410);
+    r.join({{__byte_perm(bits(most), neg, 0x7632)}});
   } else {
-    hi = x[0], lo = -x[0];
+    float hi = x[0], lo = -x[0];
 #pragma unroll
     for (int i = 1; i < 8; i++) {
       hi = max_nan(hi, x[i]);
       lo = max_nan(lo, -x[i]);
     }
-#pragma unroll
-    for (int s = 1; s < GL; s <<= 1) {
-      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, s));
-      lo = max_nan(lo, __shfl_xor_sync(0xffffffffu, lo, s));
-    }
-    lo = -lo;
+    r.m[0] = __float_as_uint(hi), r.m[1] = __float_as_uint(lo);
   }
+  return r;
 }
 
 __device__ __forceinline__ uint32_t bf16_bits(float x) {  // of a number that is one
   return __bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
 
-// Codes of this lane's eight channels, 4 bits each in order; the group's scale | offset << 16.
-template <bool BF16, int GL>
-__device__ __forceinline__ uint32_t quantise(const Eight<BF16>& x, uint32_t& par, bool report, int* err) {
-  float lo, hi;
-  group_range<BF16, GL>(x, lo, hi);
-  const float span = __fsub_rn(hi, lo);
+// A group's scale | offset << 16, and 1 / scale, from its range.
+template <bool BF16>
+__device__ __forceinline__ uint32_t parameters(const Range<BF16>& x, float& inv, bool report, int* err) {
+  const float lo = x.lo(), span = __fsub_rn(x.hi(), lo);
   uint32_t sb = 0, ob = 0x7fc0u;
-  float inv = 0.f, o = 0.f;
+  inv = 0.f;
   if (span < kInf) {
     sb = bf16_bits(__fmul_rn(span, 1.0f / 15.0f));
     if (sb < 0x0080u) sb = 0;  // below the smallest normal number
     const float s = __uint_as_float(sb << 16);
     ob = bf16_bits(__fadd_rn(lo, __fmul_rn(8.0f, s)));
-    o = __uint_as_float(ob << 16);
     inv = sb ? __frcp_rn(s) : 0.f;
   } else if (report) {
     set_error(err, COLI_E_NONFINITE);
   }
-  par = sb | (ob << 16);
+  return sb | (ob << 16);
+}
+
+// Codes of eight channels, 4 bits each in order.
+template <bool BF16>
+__device__ __forceinline__ uint32_t codes(const Eight<BF16>& x, uint32_t par, float inv) {
+  // a group that is not finite has no offset to take off
+  const float o = (par & 0x7fff0000u) > 0x7f800000u ? 0.f : __uint_as_float(par & 0xffff0000u);
   // Adding 1.5 2^23 + 8 rounds the quotient to the nearest integer, ties to even, and leaves its bits as
   // 0x4b400000 + code, the code not yet clamped.
   if constexpr (BF16) {
@@ -282,6 +302,27 @@ __device__ __forceinline__ uint32_t quantise(const Eight<BF16>& x, uint32_t& par
     }
     return n - 0x4b400000u * kOnes;
   }
+}
+
+// Keys and values of a row, in groups of GL neighbouring lanes: even lanes find the keys' scale and offset, odd lanes the
+// values', and they exchange them. Returns the lane's own parameters.
+template <bool BF16, int GL>
+__device__ __forceinline__ uint32_t quantise(const Eight<BF16>& xk, const Eight<BF16>& xv, uint32_t& nk, uint32_t& nv, bool report,
+                                             int* err) {
+  static_assert(GL >= 2, "a group has lanes of both kinds");
+  const bool odd = threadIdx.x & 1;
+  const Range<BF16> k = range_of(xk), v = range_of(xv);
+  Range<BF16> mine = odd ? v : k;
+  mine.join((odd ? k : v).across(1));
+#pragma unroll
+  for (int s = 2; s < GL; s <<= 1) mine.join(mine.across(s));
+  float inv;
+  const uint32_t par = parameters(mine, inv, report, err);
+  const uint32_t par2 = __shfl_xor_sync(0xffffffffu, par, 1);
+  const float inv2 = __shfl_xor_sync(0xffffffffu, inv, 1);
+  nk = codes(xk, odd ? par2 : par, odd ? inv2 : inv);
+  nv = codes(xv, odd ? par : par2, odd ? inv : inv2);
+  return par;
 }
 
 // A lane's place in its chunk: head and the lane's number u within it.
@@ -335,8 +376,8 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(RowArgs a) {
   for (int n = 0; n < kSlots; n++) {
     to[n] = place_of(places, n);
     if (!to[n].there) continue;  // uniform
-    uint32_t pk, pv;
-    const uint32_t nk = quantise<BF16, kGl>(xk[n], pk, s.in, a.err), nv = quantise<BF16, kGl>(xv[n], pv, s.in, a.err);
+    uint32_t nk, nv;
+    const uint32_t par = quantise<BF16, kGl>(xk[n], xv[n], nk, nv, s.in, a.err);
     // A token's half of a value word holds two channels below 16 of a run of 32 and the two 16 above: bytes of two
     // lanes, each of which puts two of the four words together.
     const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? nv & 0xffffu : nv >> 16, 2);
@@ -345,11 +386,8 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(RowArgs a) {
     const int t = to[n].t;
     uint8_t* unit = a.c.base + to[n].at + head_at;
     *reinterpret_cast<uint32_t*>(unit + kv4_k_word(HD, t, i, c)) = nk;
-    if (s.u % kGl == 0) {
-      const int g = s.u / kGl;
-      *reinterpret_cast<uint32_t*>(unit + kv4_kscale_at(HD) + (t * NG + g) * 4) = pk;
-      *reinterpret_cast<uint32_t*>(unit + kv4_vscale_at(HD, NG) + (t * NG + g) * 4) = pv;
-    }
+    if (s.u % kGl < 2)
+      *reinterpret_cast<uint32_t*>(unit + (s.u & 1 ? kv4_vscale_at(HD, NG) : kv4_kscale_at(HD)) + (t * NG + s.u / kGl) * 4) = par;
   }
   if (!s.in) return;
   // the value words: whole where the other token is the next row
