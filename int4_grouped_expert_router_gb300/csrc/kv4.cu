@@ -1,14 +1,18 @@
 // Writing tokens into the 4-bit key/value cache and reading them back (layout: kv4.h).
 //
-// Both are bound by memory: the plain rows dominate. A warp takes 256 channels (eight neighbouring ones per
-// lane) of up to four rows; of one row where there are too few to fill the device. All its loads are issued together,
-// and the places of its rows are found by as many lanes at once. Codes are written as the layout gives them to a token: a whole
-// word of keys, and of values the halves of two words. A group of gs channels is gs / 8 neighbouring lanes for keys
-// and values alike. The two lanes whose channels share the value words of a token are two apart.
+// Both are bound by memory: the plain rows dominate. A warp takes 256 channels (eight neighbouring ones per lane) of up
+// to four rows; of one row where there are too few to fill the device. All its loads are issued together, and the places
+// of its rows are found by as many lanes at once. Codes are written as the layout gives them to a token: a whole word of
+// keys, and of values the halves of two words. A token's halves lie eight sectors apart per head, so that a warp's rows
+// are better neighbours in time than in channels (four rows of 256 channels 23.9 us, one row of 1024 27.9 us): two tokens
+// of a pair store whole words, and the read finds the sectors of its other rows in the first-level cache. A group of gs
+// channels is gs / 8 neighbouring lanes for keys and values alike. The two lanes whose channels share the value words of
+// a token are two apart.
 //
-// Measured: 9198 ragged rows of 8 heads of 128 (bf16, gs 32) written and read back in 28 us (71 MB, 2.5 TB/s), a history
-// of 36K rows of 4 heads of 64 read in 13.7 us (3.5 TB/s). Both are then bound by instructions (the ALU pipe 57 %
-// active in the write, 63 % in the read), most of them the range, rounding and clamping of each channel.
+// Measured: 9198 ragged rows of 8 heads of 128 (bf16, gs 32) written and read back in 23.0 us (71 MB, 3.1 TB/s), a history
+// of 36K rows of 4 heads of 64 read in 12.0 us (4.1 TB/s). Instructions and the chain plan, page, row bind them: the write
+// fills 64 % of the issue slots and half of the ALU pipe, most of it the range, rounding and clamping of each channel, the
+// read 58 %. CTAs of four warps took 3 % longer, of one or eight warps 10 %; eight rows a warp 10 to 20 %.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

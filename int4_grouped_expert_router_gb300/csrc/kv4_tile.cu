@@ -30,7 +30,8 @@
 // what the softmax of a half and the converters each need with the issue slots they share. What it cost to find: loops
 // unrolled beyond the instruction cache took 1068 us, matrix instructions issued with operands in plain registers (110
 // cycles each instead of 45) 589 us. Measured and dropped: the row's scores all in registers (672 us), two threads per
-// row (591 us), converters split into key and value warps (544 us), bulk register moves between warpgroups (no change).
+// row (591 us), converters split into key and value warps (544 us), bulk register moves between warpgroups (no change),
+// maximum and exponentials in one pass over the scores (523 us), the next stage fetched into L2 ahead (no change).
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -69,7 +70,8 @@ struct Tile {
   static constexpr uint32_t kRaw = kTileUnits * kUnit;
   static constexpr uint32_t kQ = kHalf * HD * 2;     // one half's queries
   static constexpr uint32_t kK = kTileTok * HD * 2;  // keys, and values, of a stage
-  static constexpr uint32_t kSmem = 1024 + 2 * kQ + 2 * kK + 2 * kK + kRaw;
+  static constexpr uint32_t kScales = kTileUnits * 2 * kKvUnit * NG * 4;  // a stage's scales and offsets in 16 bits
+  static constexpr uint32_t kSmem = 1024 + 2 * kQ + 2 * kK + 2 * kK + kRaw + kScales;
   static constexpr int kWords = HD / 32, kWpg = kWords / NG;
 };
 
@@ -257,6 +259,16 @@ __device__ __forceinline__ void sts32(uint32_t at, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
+template <int N>
+__device__ __forceinline__ void sts_words(uint32_t at, const uint32_t (&w)[N]) {
+  if constexpr (N == 4)
+    sts128(at, w);
+  else if constexpr (N == 2)
+    asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(w[0]), "r"(w[1]) : "memory");
+  else
+    sts32(at, w[0]);
+}
+
 // 2^(13 - floor(log2 x)), within what binary32 has: x times it lies in [2^13, 2^14).
 __device__ __forceinline__ float below_2_14(float x) {
   const int ex = min(253, max(1, 127 + 13 + 127 - (int)(__float_as_uint(x) >> 23)));
@@ -273,6 +285,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
   uint8_t* s_k = s_q + 2 * T::kQ;         // [2 stages][HD / 64][128 tokens][128 bytes]
   uint8_t* s_v = s_k + 2 * T::kK;         // [2 stages][2][HD channels][128 bytes = 64 tokens]
   uint8_t* s_raw = s_v + 2 * T::kK;       // [kTileUnits] packed units
+  uint8_t* s_scale = s_raw + T::kRaw;     // [kTileUnits][keys, values][16 tokens][NG] scale | offset << 16
   __shared__ __align__(8) uint64_t raw_full, raw_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], par_full[4],
       q_full[2], s_full[2], p_full[2], o_full[2];
   __shared__ float s_par[4][3];           // per stage: 1 / key factor, value factor (0: none yet), 1 / value factor
@@ -564,42 +577,39 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
     const uint32_t k_base0 = smem_u32(s_k) + (cw * 16 + r) * 128;
     const uint32_t v_base0 = smem_u32(s_v) + (cw / 4) * (HD * 128) + r * 128 + cc * 4;
     const uint8_t* unit = s_raw + cw * T::kUnit;
+    const uint8_t* scales_at = s_scale + cw * (2 * kKvUnit * NG * 4);
+    const uint32_t scales = smem_u32(scales_at);
     float kmul = 0.f, vmul = 0.f;  // keys and values are multiplied by them; they only shrink within a segment
     float kinv = 1.f, vinv = 0.f;  // 1 / kmul, 1 / vmul
     for (uint32_t n = 0; more(); n++) {
       if (n == 0 || stage == 0) kmul = vmul = vinv = 0.f, kinv = 1.f;
       const int left = it.len - (it.first + stage) * kTileTok - cw * 16;  // tokens of this unit that exist
       wait(&raw_full, n & 1);
-      // codes of tokens r, r + 8 (keys) and of token pairs c, c + 4 (values), with their scales and offsets
-      uint32_t kw[2][T::kWords], vw[2][T::kWords], kp[2][NG], vp[2][NG], p0[2][NG], p1[2][NG];
+      // codes of tokens r, r + 8 (keys) and of token pairs c, c + 4 (values); scales and offsets of one token, keys' in
+      // lanes 0..15, values' in lanes 16..31: made ready once, and shared through s_scale
+      uint32_t kw[2][T::kWords], vw[2][T::kWords], sc[NG];
 #pragma unroll
       for (int h = 0; h < 2; h++) {
         lds_words(unit + h * 32 * T::kWords * 4 + lane * T::kWords * 4, kw[h]);
         lds_words(unit + kv4_v_at(HD, NG) + h * 4 * HD + lane * T::kWords * 4, vw[h]);
-        lds_words(unit + kv4_kscale_at(HD) + (r + 8 * h) * NG * 4, kp[h]);
-        lds_words(unit + kv4_vscale_at(HD, NG) + (r + 8 * h) * NG * 4, vp[h]);
-        lds_words(unit + kv4_vscale_at(HD, NG) + (2 * cc + 8 * h) * NG * 4, p0[h]);
-        lds_words(unit + kv4_vscale_at(HD, NG) + (2 * cc + 8 * h + 1) * NG * 4, p1[h]);
       }
+      lds_words(unit + (lane < 16 ? kv4_kscale_at(HD) : kv4_vscale_at(HD, NG)) + (lane & 15) * NG * 4, sc);
       __syncwarp();
       if (lane == 0) mbar_arrive(&raw_empty);
-      float kbig = 0.f, vbig = 0.f;  // the largest |o| + 8 s of this lane's tokens
-      bool broken[2];                // a value that is not finite is shown by its key: rows that do not see it have weight 0
+      const bool live = (lane & 15) < left;
+      float big = 0.f;      // the largest |o| + 8 s of the token
+      bool broken = false;  // a value that is not finite is shown by its key: rows that do not see it have weight 0
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
-        broken[h] = false;
-        const bool live = r + 8 * h < left;
-#pragma unroll
-        for (int g = 0; g < NG; g++) {
-          broken[h] = broken[h] || hi_bf16(vp[h][g]) != hi_bf16(vp[h][g]);
-          kbig = fmaxf(kbig, live ? fmaf(8.f, lo_bf16(kp[h][g]), fabsf(hi_bf16(kp[h][g]))) : 0.f);
-          vbig = fmaxf(vbig, live ? fmaf(8.f, lo_bf16(vp[h][g]), fabsf(hi_bf16(vp[h][g]))) : 0.f);
-        }
+      for (int g = 0; g < NG; g++) {
+        broken = broken || (sc[g] & 0x7fff0000u) > 0x7f800000u;
+        big = fmaxf(big, fmaf(8.f, lo_bf16(sc[g]), fabsf(hi_bf16(sc[g]))));
       }
+      if (!live) big = 0.f;
+      broken = __shfl_sync(0xffffffffu, broken, lane | 16);
       auto too_big = [](float x, float mul) { return mul == 0.f ? x > 0.f : x * mul >= 16384.f; };
-      if (named_sync_or(2, kConvWarps * 32, too_big(kbig, kmul) || too_big(vbig, vmul))) {
-        kbig = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(kbig)));
-        vbig = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vbig)));
+      if (named_sync_or(2, kConvWarps * 32, too_big(big, lane < 16 ? kmul : vmul))) {
+        float kbig = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 16 ? __float_as_uint(big) : 0u));
+        float vbig = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 16 ? 0u : __float_as_uint(big)));
         if (lane == 0) {
           s_big[0][cw] = kbig;
           s_big[1][cw] = vbig;
@@ -613,6 +623,21 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         if (too_big(kbig, kmul)) kmul = below_2_14(kbig), kinv = 1.f / kmul;
         if (too_big(vbig, vmul)) vmul = below_2_14(vbig), vinv = 1.f / vmul;
       }
+      {
+        const float mul = lane < 16 ? kmul : vmul;
+#pragma unroll
+        for (int g = 0; g < NG; g++) {
+          float o = hi_bf16(sc[g]) * mul;
+          if (lane < 16)
+            o = broken ? __uint_as_float(0x7fc00000u) : o;
+          else
+            o = o == o ? o : 0.f;
+          const uint32_t ready = bits(__floats2half2_rn(lo_bf16(sc[g]) * mul, o));
+          sc[g] = live && (lane < 16 || vmul != 0.f) ? ready : 0u;
+        }
+        sts_words(scales + lane * NG * 4, sc);
+        __syncwarp();
+      }
       // ---- keys: odd tokens store the words of a pair in the other order: eight lanes then cover all banks ----
       wait(&k_empty[n & 1], ((n >> 1) & 1) ^ 1);
       if (cw == 0 && lane == 0) {  // the softmax of four stages ago is long done
@@ -625,13 +650,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
       const int odd = r & 1;
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        const bool live = r + 8 * h < left;
         __half2 s[NG], o[NG];
+        lds_words(scales_at + (r + 8 * h) * NG * 4, sc);
 #pragma unroll
-        for (int g = 0; g < NG; g++) {
-          s[g] = __float2half2_rn(live ? lo_bf16(kp[h][g]) * kmul : 0.f);
-          o[g] = __float2half2_rn(!live ? 0.f : broken[h] ? __uint_as_float(0x7fc00000u) : hi_bf16(kp[h][g]) * kmul);
-        }
+        for (int g = 0; g < NG; g++) s[g] = as_half2(__byte_perm(sc[g], 0, 0x1010)), o[g] = as_half2(__byte_perm(sc[g], 0, 0x3232));
 #pragma unroll
         for (int i = 0; i < T::kWords; i++) {
           const int j = i ^ 1;
@@ -648,15 +670,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
       const uint32_t v_base = v_base0 + (n & 1) * T::kK;
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        const int t = 2 * cc + 8 * h;
-        const bool live0 = t < left && vmul != 0.f, live1 = t + 1 < left && vmul != 0.f;
         __half2 s[NG], o[NG];
+        uint32_t sc1[NG];
+        lds_words(scales_at + (16 + 2 * cc + 8 * h) * NG * 4, sc);
+        lds_words(scales_at + (16 + 2 * cc + 8 * h + 1) * NG * 4, sc1);
 #pragma unroll
-        for (int g = 0; g < NG; g++) {
-          const float o0 = hi_bf16(p0[h][g]), o1 = hi_bf16(p1[h][g]);
-          s[g] = __floats2half2_rn(live0 ? lo_bf16(p0[h][g]) * vmul : 0.f, live1 ? lo_bf16(p1[h][g]) * vmul : 0.f);
-          o[g] = __floats2half2_rn(live0 && o0 == o0 ? o0 * vmul : 0.f, live1 && o1 == o1 ? o1 * vmul : 0.f);
-        }
+        for (int g = 0; g < NG; g++)
+          s[g] = as_half2(__byte_perm(sc[g], sc1[g], 0x5410)), o[g] = as_half2(__byte_perm(sc[g], sc1[g], 0x7632));
         const uint32_t at = v_base + ((((cw % 4) * 2 + h) ^ r) << 4);  // the chunk of eight tokens
 #pragma unroll
         for (int i = 0; i < T::kWords; i++) {
@@ -690,6 +710,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
       const bool split = row_n <= kHalf;
       if (split && x == 1 && n_here == 1) return;
       const int lrow = split ? row & (kHalf - 1) : row;
+      if ((lrow & ~31) >= row_n) {  // a warp without rows: whatever its queries hold, nothing reads their results
+        if (lane == 0) mbar_arrive(&q_full[x]);
+        return;
+      }
       const long long q_row = (long long)it.tile * kTileRows + min(lrow, row_n - 1);
       const size_t at = (size_t)((it.r0 + q_row / a.group) * a.q_stride) + (size_t)(it.head * a.group + q_row % a.group) * HD;
       const unsigned short* src = static_cast<const unsigned short*>(a.q) + at;
@@ -747,8 +771,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
       const int lrow = split ? row & (kHalf - 1) : row;
       const long long q_row = (long long)at.tile * kTileRows + min(lrow, row_n - 1);  // rows past the end repeat the last
       const int pos = at.len - at.m + (int)(q_row / a.group);
+      const bool rows = (lrow & ~31) < row_n;  // a warp without rows only keeps the products' pace
       float mf = -kInf, l = 0.f, vmul = 0.f, unscale = 0.f;
-      if (active) {
+      if (active && !rows) {
+        for (int j = split ? x : 0; j < n_here; j += split ? 2 : 1, ns++) {
+          wait(&s_full[x], ns & 1);
+          if (lane == 0) mbar_arrive(&p_full[x]);
+        }
+      } else if (active) {
         const int step = split ? 2 : 1, j0 = split ? x : 0;
         for (int j = j0; j < n_here; j += step, ns++) {
           const int t0 = (at.first + stage + j) * kTileTok;
@@ -851,6 +881,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         wait(&o_full[x], nseg & 1);
         nseg++;
         tc_fence_after_sync();
+      }
+      if (active && rows) {
         const float inv = direct ? (l == 0.f ? 0.f : unscale / l) : unscale;
         const size_t out_row = (size_t)((at.r0 + q_row / a.group) * a.out_stride) + (size_t)(at.head * a.group + q_row % a.group) * HD;
 #pragma unroll 1
