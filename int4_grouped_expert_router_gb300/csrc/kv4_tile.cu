@@ -60,7 +60,7 @@ constexpr float kLift = 9.f;
 constexpr float kInf = __builtin_huge_valf();
 // What an item costs beside its stages, in stages: it counts in the shares, ahead of the item's first stage.
 #ifndef COLI_KV4_TILE_COST
-#define COLI_KV4_TILE_COST 4
+#define COLI_KV4_TILE_COST 6
 #endif
 constexpr int kItemCost = COLI_KV4_TILE_COST;
 
