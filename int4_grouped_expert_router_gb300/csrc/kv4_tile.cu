@@ -714,46 +714,53 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         if (lane == 0) mbar_arrive(&q_full[x]);
         return;
       }
+      // Lanes lie along a row, HD / 8 of them: a thread fetching its own row would touch 32 lines with every load.
+      constexpr int kAcross = HD / 8, kAtOnce = 32 / kAcross;  // lanes of a row, rows of a load
       const long long q_row = (long long)it.tile * kTileRows + min(lrow, row_n - 1);
-      const size_t at = (size_t)((it.r0 + q_row / a.group) * a.q_stride) + (size_t)(it.head * a.group + q_row % a.group) * HD;
-      const unsigned short* src = static_cast<const unsigned short*>(a.q) + at;
-      uint4 v[HD / 8];  // all in flight
+      const long long mine = (it.r0 + q_row / a.group) * a.q_stride + (it.head * a.group + q_row % a.group) * HD;
+      const int ch = lane % kAcross, sub = lane / kAcross;
+      uint4 v[kAcross];  // all in flight
 #pragma unroll
-      for (int ch = 0; ch < HD / 8; ch++) {
+      for (int i = 0; i < kAcross; i++) {
+        const unsigned short* src = static_cast<const unsigned short*>(a.q) + __shfl_sync(0xffffffffu, mine, i * kAtOnce + sub) + 8 * ch;
         if (a.vec) {
-          v[ch] = __ldcg(reinterpret_cast<const uint4*>(src) + ch);
+          v[i] = __ldcg(reinterpret_cast<const uint4*>(src));
         } else {
           uint32_t e[4];
 #pragma unroll
-          for (int i = 0; i < 4; i++) e[i] = __ldcg(src + 8 * ch + 2 * i) | ((uint32_t)__ldcg(src + 8 * ch + 2 * i + 1) << 16);
-          v[ch] = make_uint4(e[0], e[1], e[2], e[3]);
+          for (int j = 0; j < 4; j++) e[j] = __ldcg(src + 2 * j) | ((uint32_t)__ldcg(src + 2 * j + 1) << 16);
+          v[i] = make_uint4(e[0], e[1], e[2], e[3]);
         }
       }
-      uint32_t amax = 0;
+      const uint32_t dst = smem_u32(s_q) + x * T::kQ + (ch / 8) * (kHalf * 128);
+      const int first_row = row & (kHalf - 1) & ~31;
+      float inv = 1.f;  // of this thread's row
+      bool broken = false;
 #pragma unroll
-      for (int ch = 0; ch < HD / 8; ch++) {
-        const uint32_t qw[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
+      for (int i = 0; i < kAcross; i++) {
+        const uint32_t qw[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t amax = 0;
 #pragma unroll
-        for (int i = 0; i < 4; i++) amax = max(amax, max(qw[i] & 0x7fffu, qw[i] >> 16 & 0x7fffu));
-      }
-      if (amax >= 0x7f80u && lrow < row_n) set_error(a.err, COLI_E_NONFINITE);
-      const int ex = min(253, max(1, 127 + 14 + 127 - (int)(amax >> 7)));
-      float mult = amax == 0 ? 1.f : __uint_as_float((uint32_t)ex << 23);
-      const float inv = amax == 0 ? 1.f : __uint_as_float((uint32_t)(254 - ex) << 23);
-      if (a.scale < 0.f) mult = -mult;
-      if (amax >= 0x7f80u) mult = __uint_as_float(0x7fc00000u);
-      const uint32_t dst = smem_u32(s_q) + x * T::kQ + (row & (kHalf - 1)) * 128;
+        for (int j = 0; j < 4; j++) amax = max(amax, max(qw[j] & 0x7fffu, qw[j] >> 16 & 0x7fffu));
 #pragma unroll
-      for (int ch = 0; ch < HD / 8; ch++) {
-        const uint32_t qw[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
+        for (int o = 1; o < kAcross; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const int ex = min(253, max(1, 127 + 14 + 127 - (int)(amax >> 7)));
+        float mult = amax == 0 ? 1.f : __uint_as_float((uint32_t)ex << 23);
+        const float of = __shfl_sync(0xffffffffu, amax == 0 ? 1.f : __uint_as_float((uint32_t)(254 - ex) << 23), lane % kAtOnce * kAcross);
+        if (lane / kAtOnce == i) inv = of;
+        if (a.scale < 0.f) mult = -mult;
+        if (amax >= 0x7f80u) mult = __uint_as_float(0x7fc00000u);
+        broken = broken || amax >= 0x7f80u;  // rows past the end repeat the last
         float f[8];
 #pragma unroll
         for (int j = 0; j < 4; j++) f[2 * j] = lo_bf16(qw[j]) * mult, f[2 * j + 1] = hi_bf16(qw[j]) * mult;
         uint32_t o[4];
 #pragma unroll
         for (int j = 0; j < 4; j++) o[j] = bits(__floats2half2_rn(f[j], f[j + 4]));
-        sts128(dst + (ch / 8) * (kHalf * 128) + (((ch % 8) ^ (row & 7)) << 4), o);
+        const int at = first_row + i * kAtOnce + sub;
+        sts128(dst + at * 128 + (((ch % 8) ^ (at & 7)) << 4), o);
       }
+      if (broken) set_error(a.err, COLI_E_NONFINITE);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[x]);
