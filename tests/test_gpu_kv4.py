@@ -56,6 +56,26 @@ def test_tokens_written_one_by_one_equal_those_written_at_once(ctx):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,hd,gs", [(8, 64, 32), (4, 128, 64), (2, 256, 128)])
+def test_many_rows_at_once_equal_those_written_in_pieces(ctx, heads, hd, gs, dtype):
+    """Thousands of rows, which a warp takes several at a time (tokens that share words among them), against pieces of a
+    few hundred, most of them from an odd token on."""
+    lens = [1501, 3, 700, 0, 513]
+    b = Batch(ctx, lens, heads, hd, gs, 32, dtype)
+    c = Batch(ctx, lens, heads, hd, gs, 32, dtype, write=False)
+    for i, n in enumerate(lens):
+        for at in range(0, n, 301):
+            to = min(n, at + 301)
+            rows = slice(int(c.start[i]) + at, int(c.start[i]) + to)
+            B.coli_kv4_append(ctx, c.cache, c.k_t[rows], c.v_t[rows], torch.tensor([to], dtype=torch.int32).cuda(),
+                              c.table[i:i + 1], torch.tensor([0, to - at], dtype=torch.int32).cuda())
+    assert torch.equal(b.cache.data, c.cache.data)
+    k, v = read_all(b)
+    assert B.coli_check_error(ctx) == 0
+    assert np.array_equal(k, rounded(b.K, dtype)) and np.array_equal(v, rounded(b.V, dtype))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_slices_of_a_fused_projection_at_any_alignment(ctx, dtype):
     """k and v as slices of wider rows that start off any vector boundary; the read-back goes into such slices too."""
     heads, hd, T = 2, 128, 21

@@ -59,6 +59,13 @@ def test_prompts_drafts_and_rows_that_see_nothing(ctx, lens, rows, dtype):
             assert bool((out[int(b.q_start[i]) + j] == 0).all())
 
 
+@pytest.mark.parametrize("hd,gs", [(64, 64), (128, 32)])
+@pytest.mark.parametrize("rows", [[31, 32, 33], [63, 64, 65, 1], [97, 127, 128, 129], [161, 255, 256, 257]])
+def test_tiles_that_end_around_a_warp(ctx, hd, gs, rows):
+    """Query rows per head one below, at and one above what fills a warp, a half and a tile of the tensor-core form."""
+    check(Batch(ctx, [300 - 7 * i for i in range(len(rows))], 1, hd, gs, 16, "bf16"), rows, 1)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 100, 5000])
 @pytest.mark.parametrize("rows", [1, 6, 150])
