@@ -221,6 +221,10 @@ COLI_API int coli_expert_table_set(coli_ctx *ctx, int e, uint64_t gate, uint64_t
  * and y is rounded to bf16 once at the end). idx, w, n_sel: as produced by coli_router_select,
  * device pointers. Slots with idx < 0 beyond n_sel are ignored. D and I come from the table.
  * Every weight byte of an expert is read once per call however many of the S tokens chose it.
+ * Straight after a router call on the same x_rows the kernels may read x before the router has ended
+ * (coli_expert_group_issue too, until the round's take): no other context, and no kernel of the
+ * caller's that releases its dependents before it ends, may write x between the two calls. After
+ * anything else they wait for all earlier work on the stream.
  * Kernel forms, chosen on the host:
  *   - S == 1, every expert of the table streamable (D a multiple of 1024 and at most 6144, I a
  *     multiple of 16, every group size 0 or a multiple of 32): one persistent streaming kernel that

@@ -40,6 +40,34 @@ bool injected(coli_ctx* ctx) {
   return false;
 }
 
+// The capture that the context's stream is in (0: none). False if it cannot be told.
+static bool capture_of(coli_ctx* ctx, unsigned long long& id) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  id = 0;
+  if (cudaStreamGetCaptureInfo(ctx->stream, &status, &id) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return false;
+  }
+  if (status != cudaStreamCaptureStatusActive) id = 0;
+  return true;
+}
+
+// After a router launch: every CTA of the router waits for the work before it, x among it, and only then lets the next
+// kernel start (its many-token form never does so early), so x is complete when that kernel starts. Other kernels make no
+// such promise: the norms, the cache read and the attention let their successor start at once and store to it later.
+static void settle_x(coli_ctx* ctx, const void* x) {
+  ctx->settled_x = capture_of(ctx, ctx->settled_capture) ? x : nullptr;
+  ctx->settled_stream = ctx->stream;
+}
+
+// Before every compute call that may write where a later call reads x.
+static void unsettle_x(coli_ctx* ctx) { ctx->settled_x = nullptr; }
+
+bool x_settled(coli_ctx* ctx, const void* x) {
+  unsigned long long id;
+  return ctx->settled_x == x && ctx->settled_stream == ctx->stream && capture_of(ctx, id) && id == ctx->settled_capture;
+}
+
 int ensure_workspace(coli_ctx* ctx, size_t bytes) {
   bytes = align_up(bytes < 256 ? 256 : bytes, 256);
   if (bytes <= ctx->ws.bytes) return COLI_OK;
@@ -300,6 +328,7 @@ void coli_destroy(coli_ctx* ctx) {
 int coli_set_stream(coli_ctx* ctx, void* cuda_stream) {
   if (!ctx) return COLI_E_INVAL;
   ctx->stream = static_cast<cudaStream_t>(cuda_stream);
+  unsettle_x(ctx);
   return COLI_OK;
 }
 
@@ -554,8 +583,12 @@ int coli_router_select(coli_ctx* ctx, const void* x, int x_dtype, int S, int D, 
     return fail(ctx, COLI_E_INVAL, "router: size out of range");
   if (injected(ctx)) return COLI_E_INJECTED;
   cudaSetDevice(ctx->device);
+  unsettle_x(ctx);
   int rc = launch_router(ctx, x, x_dtype, S, D, Wr, bias, E, K, topp, norm_topk, routed_scale, -1, idx, w, n_sel);
-  if (rc == COLI_OK) ctx->compute_calls++;
+  if (rc == COLI_OK) {
+    ctx->compute_calls++;
+    settle_x(ctx, x);
+  }
   return rc;
 }
 
@@ -570,8 +603,12 @@ int coli_router_select_shared(coli_ctx* ctx, const void* x, int x_dtype, int S, 
     return fail(ctx, COLI_E_INVAL, "router_shared: size or shared id out of range");
   if (injected(ctx)) return COLI_E_INJECTED;
   cudaSetDevice(ctx->device);
+  unsettle_x(ctx);
   int rc = launch_router(ctx, x, x_dtype, S, D, Wr, bias, E, K, topp, norm_topk, routed_scale, shared, idx, w, n_sel);
-  if (rc == COLI_OK) ctx->compute_calls++;
+  if (rc == COLI_OK) {
+    ctx->compute_calls++;
+    settle_x(ctx, x);
+  }
   return rc;
 }
 
@@ -586,9 +623,13 @@ int coli_router_select_noalloc(coli_ctx* ctx, const void* x, int x_dtype, int S,
     return fail(ctx, COLI_E_INVAL, "router_noalloc: size out of range");
   if (injected(ctx)) return COLI_E_INJECTED;
   cudaSetDevice(ctx->device);
+  unsettle_x(ctx);
   int rc = launch_router_noalloc(ctx, x, x_dtype, S, D, Wr, bias, E, K, topp, norm_topk, routed_scale, -1, idx, w,
                                   n_sel);
-  if (rc == COLI_OK) ctx->compute_calls++;
+  if (rc == COLI_OK) {
+    ctx->compute_calls++;
+    settle_x(ctx, x);
+  }
   return rc;
 }
 
@@ -604,6 +645,7 @@ int coli_expert_group(coli_ctx* ctx, const void* x_rows, int x_dtype, int S, con
   if (injected(ctx)) return COLI_E_INJECTED;
   cudaSetDevice(ctx->device);
   int rc = launch_expert_group(ctx, x_rows, x_dtype, S, idx, w, n_sel, K, resid, y, x_dtype);
+  unsettle_x(ctx);  // y may be x
   if (rc == COLI_OK) ctx->compute_calls++;
   return rc;
 }
@@ -617,6 +659,7 @@ int coli_w4_linear(coli_ctx* ctx, uint64_t W, const void* x, int x_dtype, int S,
   if (injected(ctx)) return COLI_E_INJECTED;
   cudaSetDevice(ctx->device);
   const HostTensor& t = ctx->tensors[W - 1];
+  unsettle_x(ctx);
   // one token through a tensor whose rows and scales can be streamed in 16-row units: the streaming kernel
   int rc = S == 1 && ctx->stream_ffn && stream_linear_ok(t) ? launch_stream_linear(ctx, t, x, x_dtype, resid, y)
                                                            : launch_linear(ctx, t.desc, t.d_solo, x, x_dtype, S, resid, y);
@@ -685,6 +728,7 @@ int coli_ans_decode(coli_ctx* ctx, uint64_t h, uint8_t* out) {
   if (!out) return fail(ctx, COLI_E_INVAL, "ans_decode: NULL pointer");
   if (injected(ctx)) return COLI_E_INJECTED;
   cudaSetDevice(ctx->device);
+  unsettle_x(ctx);
   int rc = launch_ans_decode(ctx, st->d_blob, st->blocks, out);
   if (rc == COLI_OK) ctx->compute_calls++;
   return rc;
@@ -701,6 +745,7 @@ int coli_ans_w4_linear(coli_ctx* ctx, uint64_t h, const float* scales, int O, in
     return fail(ctx, COLI_E_INVAL, "ans_w4_linear: shape does not match the stream (O rows of I/2 bytes, I even, 256 <= I <= 16384)");
   if (injected(ctx)) return COLI_E_INJECTED;
   cudaSetDevice(ctx->device);
+  unsettle_x(ctx);
   int rc = launch_ans_gemv(ctx, *st, scales, O, I, gs, x, x_dtype, resid, y);
   if (rc == COLI_OK) ctx->compute_calls++;
   return rc;
@@ -740,6 +785,7 @@ int coli_partials_reduce(coli_ctx* ctx, const float* parts, int n, int S, int D,
     return fail(ctx, COLI_E_INVAL, "partials_reduce: size out of range");
   if (injected(ctx)) return COLI_E_INJECTED;
   cudaSetDevice(ctx->device);
+  unsettle_x(ctx);
   int rc = launch_partials_reduce(ctx, parts, n, S, D, resid, dtype, y);
   if (rc == COLI_OK) ctx->compute_calls++;
   return rc;
@@ -778,6 +824,7 @@ int coli_expert_group_take(coli_ctx* ctx, const void* resid, void* y) {
   if (ctx->n_issued == 0) return fail(ctx, COLI_E_INVAL, "take: nothing issued");
   if (injected(ctx)) return COLI_E_INJECTED;
   cudaSetDevice(ctx->device);
+  unsettle_x(ctx);
   int rc = launch_take(ctx, ctx->round_S, ctx->round_D, ctx->n_issued, resid, ctx->round_dtype, y);
   if (rc != COLI_OK) return rc;
   ctx->compute_calls++;
@@ -833,6 +880,7 @@ int coli_kv4_append(coli_ctx* ctx, const coli_kv4_cache* cache, const void* k, l
   if (k_stride < row || v_stride < row) return fail(ctx, COLI_E_INVAL, "kv4_append: row stride below heads * head_dim");
   if (injected(ctx)) return COLI_E_INJECTED;
   cudaSetDevice(ctx->device);
+  unsettle_x(ctx);
   rc = launch_kv4_append(ctx, kv4_view(cache), Kv4Plan{q_start, lens, table, T, B, table_stride}, k, k_stride, v, v_stride,
                          dtype);
   if (rc == COLI_OK) ctx->compute_calls++;
@@ -849,6 +897,7 @@ int coli_kv4_read(coli_ctx* ctx, const coli_kv4_cache* cache, void* k, long long
   if (k_stride < row || v_stride < row) return fail(ctx, COLI_E_INVAL, "kv4_read: row stride below heads * head_dim");
   if (injected(ctx)) return COLI_E_INJECTED;
   cudaSetDevice(ctx->device);
+  unsettle_x(ctx);
   rc = launch_kv4_read(ctx, kv4_view(cache), Kv4Plan{q_start, lens, table, T, B, table_stride}, k, k_stride, v, v_stride,
                        dtype);
   if (rc == COLI_OK) ctx->compute_calls++;
@@ -870,6 +919,7 @@ int coli_kv4_attention(coli_ctx* ctx, const coli_kv4_cache* cache, const void* q
   if (window < 0) return fail(ctx, COLI_E_INVAL, "kv4_attention: window must not be negative");
   if (injected(ctx)) return COLI_E_INJECTED;
   cudaSetDevice(ctx->device);
+  unsettle_x(ctx);
   rc = launch_kv4_attention(ctx, kv4_view(cache), Kv4Plan{q_start, lens, table, T, B, table_stride}, q, q_stride, dtype,
                             q_heads, scale, window, out, out_stride);
   if (rc == COLI_OK) ctx->compute_calls++;
@@ -900,6 +950,7 @@ int coli_norm_residual(coli_ctx* ctx, const void* block, const void* resid, cons
   if (injected(ctx)) return COLI_E_INJECTED;
   cudaSetDevice(ctx->device);
   NormArgs a{block, resid, gate, gate && gate_rows > 1, gate_sigmoid != 0, alpha, w_post, w_pre, eps, dtype, S, D, h_out, x_out};
+  unsettle_x(ctx);
   int rc = launch_norm_residual(ctx, a);
   if (rc == COLI_OK) ctx->compute_calls++;
   return rc;

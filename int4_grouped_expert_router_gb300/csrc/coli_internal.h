@@ -138,6 +138,12 @@ struct coli_ctx {
   void* d_router = nullptr;
   int router_rows = 0, router_parts = 0;
   int test_withhold_router = 0;
+  // The expert kernels read x ahead of their wait on the preceding kernel where the router is known to have
+  // finished that wait with x complete (x_settled): the x, the stream and the capture (0: none) of a router call
+  // after which this context has launched nothing that could write to x.
+  const void* settled_x = nullptr;
+  cudaStream_t settled_stream = nullptr;
+  unsigned long long settled_capture = 0;
   int* d_kv_count = nullptr;  // coli::kKvCounters arrival counters of the cache attention, zero between calls
   coli::Workspace ws;
   // resident issue/take: f32 partial sums [COLI_MAX_ISSUES][S x D] of the current round's issues
@@ -165,6 +171,8 @@ int fail(coli_ctx* ctx, int code, const std::string& msg);
 int cuda_fail(coli_ctx* ctx, cudaError_t e, const char* what);
 bool injected(coli_ctx* ctx);  // COLI_FAIL_AFTER: true if this compute call must fail
 int ensure_workspace(coli_ctx* ctx, size_t bytes);
+// Whether a kernel launched now, programmatically serialised, may read x before its griddepcontrol.wait.
+bool x_settled(coli_ctx* ctx, const void* x);
 int ensure_slots(coli_ctx* ctx, size_t bytes);
 
 constexpr size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }

@@ -85,6 +85,7 @@ struct StreamParams {
   unsigned long long wait_ns;
   int withhold;              // test hook: the CTA owning unit 0 withholds the copy of its first gate stage
   int x_bulk;                // x is 16-byte aligned: each CTA copies it whole into shared memory
+  bool x_settled;            // x may be read before griddepcontrol.wait
 };
 
 // Limbs of 16 values of h held by lanes 0..15 (lanes 16..31 hold 0); every lane returns the same
@@ -173,9 +174,13 @@ __global__ void __launch_bounds__(MAXT, 1) stream_ffn_kernel(const StreamParams 
     mbar_init(&cs.xfull, 1);
     mbar_init(&cs.xfree, NW);
     mbar_fence_init();
-    // x (the router's input, complete before this grid started) into gate/up stage 0 with one bulk
-    // copy: every CTA needs all of it, and 152 CTAs of per-thread loads of the same 24 KiB queue for
-    // microseconds behind each other in L2, where one bulk request per CTA does not
+  }
+  // Straight after the router, x (its input) was complete before this grid started; after any other kernel it may still
+  // be on its way.
+  if (!P.x_settled) griddep_wait();
+  if (tid == 0) {
+    // x into gate/up stage 0 with one bulk copy: every CTA needs all of it, and 152 CTAs of per-thread loads of the same
+    // 24 KiB queue for microseconds behind each other in L2, where one bulk request per CTA does not
     if (P.x_bulk) {
       const uint32_t xbytes = (uint32_t)D * (P.x_dtype == COLI_DTYPE_F32 ? 4u : 2u);
       mbar_arrive_expect_tx(&cs.xfull, xbytes);
@@ -829,6 +834,7 @@ int launch_stream_ffn(coli_ctx* ctx, const void* x, int x_dtype, const int32_t* 
   P.wait_ns = ctx->wait_ns;
   P.withhold = ctx->test_withhold > 0;  // one-shot: only the next launch withholds
   P.x_bulk = (reinterpret_cast<uintptr_t>(x) & 15) == 0;
+  P.x_settled = x_settled(ctx, x);
   if (ctx->test_withhold > 0) ctx->test_withhold--;
   {
     ProfScope prof(ctx, COLI_KERNEL_GATEUP);

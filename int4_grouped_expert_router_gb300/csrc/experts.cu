@@ -85,6 +85,7 @@ struct GroupParams {
   int h_dtype;     // dtype of h (f32; the dense projection passes its activations here)
   float* yr;       // [routes x D] (S > 1)
   int* plan;       // pre[0..S] (written by CTA 0 of the gate/up kernel)
+  bool x_settled;  // x may be read before griddepcontrol.wait (gate/up kernel)
   int* err;
 };
 
@@ -507,7 +508,9 @@ __device__ __forceinline__ void gateup_body(const GroupParams& P, const FusedPar
       for (int s = 0; s < kFDStages; s++) mbar_init(&sm.dbars[warp][s], 1);
     mbar_fence_init();
   }
-  // prologue overlapping the router's tail: activation limbs of token 0
+  // prologue overlapping the router's tail: activation limbs of token 0. Straight after the router, x (its input) was
+  // complete before this grid started; after any other kernel it may still be on its way.
+  if (!P.x_settled) griddep_wait();
   Limbs L;
   int cur_tok = 0;
   {
@@ -1203,6 +1206,7 @@ int launch_expert_group(coli_ctx* ctx, const void* x, int x_dtype, int S, const 
   P.h_dtype = COLI_DTYPE_F32;
   P.yr = reinterpret_cast<float*>(ctx->ws.base + h_bytes);
   P.plan = reinterpret_cast<int*>(ctx->ws.base + h_bytes + yr_bytes + yp_bytes);
+  P.x_settled = x_settled(ctx, x);
   P.err = ctx->d_status;
 
   if (fused) {
