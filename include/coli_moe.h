@@ -98,7 +98,10 @@ COLI_API int coli_last_code(coli_ctx *ctx);
 COLI_API int coli_check_error(coli_ctx *ctx);
 
 /* Pre-size the workspace for calls up to these sizes so that no later compute call allocates.
- * Without it, a compute call that needs more workspace than the last one allocates (once). */
+ * Without it, a compute call that needs more workspace than the last one allocates (once) and frees
+ * the old one, whose address a graph captured before still holds: reserve before capturing. The sizes
+ * are those of the router and expert calls; coli_kv4_attention has memory of its own, of one size (two
+ * partial results of 256 rows per SM, 40 MB), which this call also allocates. */
 COLI_API int coli_reserve(coli_ctx *ctx, int max_S, int max_E, int max_K, int max_D, int max_I);
 
 /* Per-kernel timing: when on, every kernel launch of this context is bracketed by two CUDA events
@@ -423,9 +426,10 @@ COLI_API int coli_kv4_read(coli_ctx *ctx, const coli_kv4_cache *cache, void *k, 
  * query sets COLI_E_NONFINITE and gives NaN in its row; a stored NaN that a row sees gives NaN there.
  * Kernel forms, chosen on the host: up to 16 query rows per sequence and key/value head on average, f32, or
  * heads of 256 channels: a streaming form that reads the cache once per 16 rows; otherwise 256-row tiles on the
- * tensor cores. Each splits long sequences over the device. The first call of a shape sizes the workspace (it
- * may allocate and wait for the stream): run one before any stream capture. A wait inside a kernel is bounded
- * (2 s), after which the call sets COLI_E_TIMEOUT and its output is void. Profiled as COLI_KERNEL_ATTENTION.
+ * tensor cores. Each splits long sequences over the device. A context's first call allocates the memory for the
+ * parts, unless coli_reserve has: run one, of any shape, before any stream capture. That memory never moves, so
+ * captured calls stay valid whatever is called later. A wait inside a kernel is bounded (2 s), after which the call
+ * sets COLI_E_TIMEOUT and its output is void. Profiled as COLI_KERNEL_ATTENTION.
  */
 COLI_API int coli_kv4_attention(coli_ctx *ctx, const coli_kv4_cache *cache, const void *q, long long q_stride,
                                 int dtype, int q_heads, int T, const int32_t *q_start, const int32_t *lens, int B,

@@ -106,6 +106,16 @@ int ensure_slots(coli_ctx* ctx, size_t bytes) {
   return COLI_OK;
 }
 
+// The cache attention's partial results: allocated by its first call or coli_reserve, and never moved.
+int ensure_kv_part(coli_ctx* ctx) {
+  if (ctx->d_kv_part) return COLI_OK;
+  void* p = nullptr;
+  cudaError_t e = cudaMalloc(&p, (size_t)ctx->num_sms * kKvPartFloats * sizeof(float));
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "attention partials cudaMalloc");
+  ctx->d_kv_part = static_cast<float*>(p);
+  return COLI_OK;
+}
+
 static cudaEvent_t prof_event(coli_ctx* ctx) {
   if (!ctx->prof_free.empty()) {
     cudaEvent_t e = ctx->prof_free.back();
@@ -314,6 +324,7 @@ void coli_destroy(coli_ctx* ctx) {
   if (ctx->d_status) cudaFree(ctx->d_status);
   if (ctx->d_router) cudaFree(ctx->d_router);
   if (ctx->d_kv_count) cudaFree(ctx->d_kv_count);
+  if (ctx->d_kv_part) cudaFree(ctx->d_kv_part);
   if (ctx->ws.base) cudaFree(ctx->ws.base);
   if (ctx->slots) cudaFree(ctx->slots);
   for (auto& r : ctx->prof_pending) {
@@ -408,6 +419,7 @@ int coli_reserve(coli_ctx* ctx, int max_S, int max_E, int max_K, int max_D, int 
   const size_t slots = (size_t)COLI_MAX_ISSUES * max_S * max_D * sizeof(float);
   cudaSetDevice(ctx->device);
   int rc = ensure_slots(ctx, slots);
+  if (rc == COLI_OK) rc = ensure_kv_part(ctx);
   if (rc != COLI_OK) return rc;
   return ensure_workspace(ctx, router > experts ? router : experts);
 }

@@ -34,6 +34,9 @@ constexpr size_t kRouterScratchBytes = 256 + (size_t)15 * 1024 * 8;
 
 // Arrival counters of split work in the cache attention (one per CTA of its grid), zero between calls.
 constexpr int kKvCounters = 4096;
+// Partial results of the cache attention, in floats per SM: two for the tensor-core form's CTA of 256 rows of 128 channels
+// and a (maximum, sum) pair, and more than any CTAs of the streaming form leave.
+constexpr size_t kKvPartFloats = (size_t)2 * 256 * (128 + 2);
 
 // Device status words of a context: [0] error code, [1] unused, [2..] the opt-in fused decode
 // kernel's synchronisation words (grid barrier at [2], [3]; row-range counters from
@@ -145,6 +148,7 @@ struct coli_ctx {
   cudaStream_t settled_stream = nullptr;
   unsigned long long settled_capture = 0;
   int* d_kv_count = nullptr;  // coli::kKvCounters arrival counters of the cache attention, zero between calls
+  float* d_kv_part = nullptr;  // num_sms x kKvPartFloats: one size for every call, so that captured calls keep their address
   coli::Workspace ws;
   // resident issue/take: f32 partial sums [COLI_MAX_ISSUES][S x D] of the current round's issues
   float* slots = nullptr;
@@ -174,6 +178,7 @@ int ensure_workspace(coli_ctx* ctx, size_t bytes);
 // Whether a kernel launched now, programmatically serialised, may read x before its griddepcontrol.wait.
 bool x_settled(coli_ctx* ctx, const void* x);
 int ensure_slots(coli_ctx* ctx, size_t bytes);
+int ensure_kv_part(coli_ctx* ctx);
 
 constexpr size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 

@@ -15,7 +15,7 @@
 // Work split. An item is (sequence, key/value head, tile of 8 NT query rows); its tokens are cut into stages of 64,
 // and all items' stages, end to end, are dealt out evenly and contiguously to a grid that fills the device, each item
 // counting kItemCost stages more: whatever the lengths, every CTA has the same work. An item that spans CTAs leaves
-// partial (maximum, sum, output) triples in the workspace, and whoever arrives last adds them up in CTA order, so that
+// partial (maximum, sum, output) triples in the context's memory, and whoever arrives last adds them up in CTA order, so that
 // results do not depend on who is last.
 //
 // In a CTA a producer warp fills a ring of stages with bulk copies, a run of units of a page each (64 tokens are
@@ -1050,9 +1050,10 @@ int launch_one(coli_ctx* ctx, AttnArgs& a, long long most_stages) {
   int grid = ctx->num_sms * C::kCtas;
   if (most_stages < grid) grid = (int)most_stages;
   if (grid > kKvCounters / 3) grid = kKvCounters / 3;
-  int rc = ensure_workspace(ctx, (size_t)2 * grid * C::kRows * (HD + 2) * sizeof(float));
+  static_assert((size_t)2 * C::kCtas * C::kRows * (HD + 2) <= kKvPartFloats, "an SM's CTAs leave more than there is room for");
+  int rc = ensure_kv_part(ctx);
   if (rc != COLI_OK) return rc;
-  a.part = reinterpret_cast<float*>(ctx->ws.base);
+  a.part = ctx->d_kv_part;
   auto kern = kv4_attn_kernel<HD, NG, NT, F32>;
   static std::atomic<uint64_t> ready{0};  // devices (below 64) on which this instance has its attribute
   const uint64_t bit = ctx->device < 64 ? 1ull << ctx->device : 0;

@@ -1020,9 +1020,10 @@ template <int HD, int NG>
 int launch_one(coli_ctx* ctx, TileArgs& a) {
   using T = Tile<HD, NG>;
   const int grid = ctx->num_sms < kKvCounters ? ctx->num_sms : kKvCounters;
-  int rc = ensure_workspace(ctx, (size_t)2 * grid * kTileRows * (HD + 2) * sizeof(float));
+  static_assert((size_t)2 * kTileRows * (HD + 2) <= kKvPartFloats, "a CTA leaves more than there is room for");
+  int rc = ensure_kv_part(ctx);
   if (rc != COLI_OK) return rc;
-  a.part = reinterpret_cast<float*>(ctx->ws.base);
+  a.part = ctx->d_kv_part;
   auto kern = kv4_tile_kernel<HD, NG>;
   static std::atomic<uint64_t> ready{0};  // devices (below 64) on which this instance has its attribute
   const uint64_t bit = ctx->device < 64 ? 1ull << ctx->device : 0;
