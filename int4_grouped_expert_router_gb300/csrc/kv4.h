@@ -91,6 +91,10 @@ __device__ __forceinline__ void kv4_rows(const Kv4Plan& p, int b, int& r0, int& 
   }
 }
 
+// The first position that a row at position pos sees (pos may be negative: such a row sees nothing). Any window goes: no
+// difference is formed that could pass 32 bits.
+__device__ __forceinline__ int kv4_from(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
+
 // The length of sequence b, clamped to what its table can name.
 __device__ __forceinline__ int kv4_len(const Kv4Plan& p, int page_log2, int b, int* err) {
   const int len = __ldcg(p.lens + b);

@@ -134,8 +134,7 @@ __device__ __forceinline__ void load_seq(const Kv4View& c, const Kv4Plan& p, int
   it.m = r1 - it.r0;
   it.len = kv4_len(p, c.page_log2, it.b, err);
   // the first row's window starts the sequence's visible part
-  const int lo = window > 0 ? max(0, it.len - it.m - window + 1) : 0;
-  it.first = lo / kStageTok;
+  it.first = kv4_from(it.len - it.m, window) / kStageTok;
   it.stages = max(1, (it.len + kStageTok - 1) / kStageTok - it.first);
 }
 
@@ -579,8 +578,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
     float* stash = s_join + warp * C::kRows * C::kPad + 2 * r;
     const int pos_min = it.len - it.m + tile_row / a.group;  // first row's position
     const int pos_max = it.len - it.m + (tile_row + row_n - 1) / a.group;
-    const int lo_max = a.window > 0 ? pos_max - a.window + 1 : 0;
-    const int lo_min = a.window > 0 ? pos_min - a.window + 1 : 0;
+    const int lo_max = kv4_from(pos_max, a.window), lo_min = kv4_from(pos_min, a.window);
 
     // One unit; `masked`: some row does not see some token of it.
     auto process = [&](auto masked, uint32_t unit, int t0) {
@@ -667,7 +665,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
 #pragma unroll
           for (int j = 0; j < 4; j++) {
             const int t = t0 + r + 8 * (j >> 1);
-            if (t > pos[nt][j & 1] || (a.window > 0 && t <= pos[nt][j & 1] - a.window)) x[nt][j] = -kInf;
+            if (t > pos[nt][j & 1] || t < kv4_from(pos[nt][j & 1], a.window)) x[nt][j] = -kInf;
           }
       }
       // ---- running maximum: moves only when a score passes it by kSlack ----

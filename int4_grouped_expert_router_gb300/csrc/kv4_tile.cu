@@ -110,7 +110,7 @@ __device__ __forceinline__ void tile_span(const TileArgs& a, int m, int len, int
   const long long all = (long long)m * a.group;
   const long long last_row = row0 + kTileRows - 1 < all - 1 ? row0 + kTileRows - 1 : all - 1;
   const int last = len - m + (int)(last_row / a.group);
-  const int lo = a.window > 0 ? max(0, len - m + (int)(row0 / a.group) - a.window + 1) : 0;
+  const int lo = kv4_from(len - m + (int)(row0 / a.group), a.window);
   first = last < 0 ? 0 : lo / kTileTok;
   stages = last < 0 ? 1 : last / kTileTok - first + 1;
 }
@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
           unscale = s_par[par][2];
           // columns [c0, c1) are visible to this row; the others are struck out where they lie
           const int c1 = min(kTileTok, max(0, pos - t0 + 1));
-          const int c0 = a.window > 0 ? min(kTileTok, max(0, pos - a.window + 1 - t0)) : 0;
+          const int c0 = min(kTileTok, max(0, kv4_from(pos, a.window) - t0));
           uint32_t sv[32];
           if (__any_sync(0xffffffffu, c1 < kTileTok || c0 > 0)) {
 #pragma unroll 1
