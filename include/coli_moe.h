@@ -379,7 +379,7 @@ COLI_API int coli_ans_w4_linear(coli_ctx *ctx, uint64_t handle, const float *sca
  *     position lens[b] - m + i. NULL: one row per sequence, T == B. Rows outside every sequence's
  *     range are left alone. A row with a negative position (a sequence shorter than its rows)
  *     stores nothing and reads zeros.
- * A length that does not fit the table (lens < 0 or > table_stride * page_tokens), a page index
+ * A length that does not fit (lens < 0, > table_stride * page_tokens or > 2^31 - 256), a page index
  * outside the cache, or a row range outside 0..T sets COLI_E_RANGE; nothing outside the arrays is
  * touched, the length is clamped, rows of a bad page are not written and read as zeros, and an
  * attention over one has undefined (finite or NaN) values for that sequence.

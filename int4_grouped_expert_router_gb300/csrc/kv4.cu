@@ -105,7 +105,7 @@ __device__ __forceinline__ Place kv4_places(const RowArgs& a, int row0, int n) {
   }
   // a range or a length that does not fit is reported by kv4_check_plan
   at.owned = mine && r0 >= 0 && r1 <= a.p.T && row >= r0 && row < r1;
-  const long long most = (long long)a.p.table_stride << a.c.page_log2;
+  const long long most = kv4_most(a.p, a.c.page_log2);
   len = len < 0 ? 0 : len > most ? (int)most : len;
   const int pos = len - (r1 - row);
   if (!at.owned || pos < 0) return at;

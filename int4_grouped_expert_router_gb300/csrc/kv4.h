@@ -26,6 +26,7 @@
 namespace coli {
 
 constexpr int kKvUnit = 16;  // tokens of a unit
+constexpr long long kKvMaxLen = (1ll << 31) - 256;  // longest sequence: positions rounded up to a stage stay below 2^31
 
 __host__ __device__ constexpr uint32_t kv4_unit_bytes(int hd, int ng) { return (uint32_t)(16 * hd + 128 * ng); }
 // Offsets of a unit's parts.
@@ -95,10 +96,15 @@ __device__ __forceinline__ void kv4_rows(const Kv4Plan& p, int b, int& r0, int& 
 // difference is formed that could pass 32 bits.
 __device__ __forceinline__ int kv4_from(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
 
+// The most tokens that a sequence can have.
+__device__ __forceinline__ long long kv4_most(const Kv4Plan& p, int page_log2) {
+  return min((long long)p.table_stride << page_log2, kKvMaxLen);
+}
+
 // The length of sequence b, clamped to what its table can name.
 __device__ __forceinline__ int kv4_len(const Kv4Plan& p, int page_log2, int b, int* err) {
   const int len = __ldcg(p.lens + b);
-  const long long most = (long long)p.table_stride << page_log2;
+  const long long most = kv4_most(p, page_log2);
   if (len < 0 || len > most) {
     set_error(err, COLI_E_RANGE);
     return len < 0 ? 0 : (int)most;

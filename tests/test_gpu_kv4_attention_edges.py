@@ -37,3 +37,35 @@ def test_a_window_as_large_as_an_int_is_none(ctx, rows, dtype, hd, window):
     assert B.coli_check_error(ctx) == 0
     assert torch.equal(out, b.attend(q_t, rows))
     within(b, out, *b.expect(q, rows))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_longest_sequence(ctx, dtype):
+    """Two thousand million tokens, of which the last 600 are written and the windows see some; one more is an error."""
+    n, page, heads, hd, gs = (1 << 31) - 256, 256, 2, 64, 32
+    b = Batch(ctx, [600], heads, hd, gs, page, dtype, write=False)
+    first = (n - 600) // page
+    table = torch.full((1, (1 << 31) // page), -1, dtype=torch.int32, device="cuda")
+    table[0, first:first + 4] = torch.tensor([2, 0, 3, 1], dtype=torch.int32)
+    b.cache = B.coli_kv4_cache(4, page, heads, hd, gs)
+    b.cache.data.fill_(255)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    B.coli_kv4_append(ctx, b.cache, b.k_t, b.v_t, lens, table, b.start_t)
+    for rows, q_heads in (([1], 4), ([1], 24), ([70], 8)):
+        q, q_t = b.queries(rows, q_heads)
+        start = torch.from_numpy(b.q_start).cuda()
+        out = torch.empty_like(q_t)
+        B.coli_kv4_attention(ctx, b.cache, q_t, lens, table, out, q_start=start, window=300)
+        assert B.coli_check_error(ctx) == 0
+        within(b, out, *b.expect(q, rows, window=300))
+        again = torch.empty_like(q_t)
+        B.coli_kv4_attention(ctx, b.cache, q_t, lens + 1, table, again, q_start=start, window=300)
+        assert B.coli_check_error(ctx) == B.COLI_E_RANGE
+        assert torch.equal(out, again)  # of the clamped length
+    k, v = torch.empty_like(b.k_t), torch.empty_like(b.v_t)
+    B.coli_kv4_read(ctx, b.cache, k, v, lens, table, b.start_t)
+    assert B.coli_check_error(ctx) == 0
+    assert torch.equal(k.double().cpu(), torch.from_numpy(b.K).to(k.dtype).double())
+    assert torch.equal(v.double().cpu(), torch.from_numpy(b.V).to(v.dtype).double())
+    B.coli_kv4_read(ctx, b.cache, k, v, lens + 255, table, b.start_t)
+    assert B.coli_check_error(ctx) == B.COLI_E_RANGE
