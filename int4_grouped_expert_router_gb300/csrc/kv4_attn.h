@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
     }
     // value scales (dequantised: values) are multiplied by vmul, a power of two that keeps them below kTop; it only
     // shrinks, and the outputs with it.
-    float vmul = __uint_as_float(253u << 23), eight = 0.f;  // eight: 8 / vmul
+    float vmul = __uint_as_float(253u << 23), eight = 8.f / vmul;
     bool stashed = false;                                  // part of the sums lies in the join buffer
     float* stash = s_join + warp * C::kRows * C::kPad + 2 * r;
     const int pos_min = it.len - it.m + tile_row / a.group;  // first row's position

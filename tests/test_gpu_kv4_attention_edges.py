@@ -69,3 +69,15 @@ def test_the_longest_sequence(ctx, dtype):
     assert torch.equal(v.double().cpu(), torch.from_numpy(b.V).to(v.dtype).double())
     B.coli_kv4_read(ctx, b.cache, k, v, lens + 255, table, b.start_t)
     assert B.coli_check_error(ctx) == B.COLI_E_RANGE
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,q_heads", FORMS)
+@pytest.mark.parametrize("v_scale", [1e-36, 2e-35])
+def test_values_near_the_ends_of_binary32(ctx, v_scale, rows, q_heads, dtype):
+    """Outputs of 1e-36 are normal numbers."""
+    b = Batch(ctx, [77, 300], 2, 128, 64, 32, dtype, v_scale=v_scale)
+    q, q_t = b.queries(rows, q_heads)
+    out = b.attend(q_t, rows)
+    assert B.coli_check_error(ctx) == 0
+    within(b, out, *b.expect(q, rows))
