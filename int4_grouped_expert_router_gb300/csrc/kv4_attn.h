@@ -883,9 +883,11 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
     }
 
     // ---- join the four warps ----
-    // exact: powers of two; the channels whose codes lie at bit 4 count sixteenfold
-    const float unscale = (C::kDeq ? 1.f / kTopScale : C::kRawV ? 16777216.f : 1.f) / vmul;
-    const float unscale1 = C::kRawV ? unscale * 0.0625f : unscale;
+    // exact: powers of two, one after the other (their product may not be a number); the channels whose codes lie at bit 4
+    // count sixteenfold
+    constexpr float kUnscale = C::kDeq ? 1.f / kTopScale : C::kRawV ? 16777216.f : 1.f;
+    constexpr float kUnscale1 = C::kRawV ? kUnscale * 0.0625f : kUnscale;
+    const float vinv = 1.f / vmul;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
@@ -909,7 +911,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
           const float add = C::kDeq ? 0.f : bias[nt][e][(i / 2) / C::kWpg];
           float2* at = reinterpret_cast<float2*>(dst + 16 * i);
           const float2 had = C::kRawV && stashed ? *at : make_float2(0.f, 0.f);
-          *at = make_float2(fmaf(had.x + o[nt][i][e], unscale, add), fmaf(had.y + o[nt][i][2 + e], unscale1, add));
+          *at = make_float2(fmaf((had.x + o[nt][i][e]) * kUnscale, vinv, add), fmaf((had.y + o[nt][i][2 + e]) * kUnscale1, vinv, add));
         }
       }
     named_sync(1, kConsumers);

@@ -59,7 +59,7 @@ constexpr int kSeqChunk = 512;                     // sequences whose stage coun
 // Weights are 2^(y - m + kLift); the maximum m moves when a score passes it by kSlack (log2). 16 bits hold
 // 2^(kLift + kSlack), and a move costs a pass over the output.
 constexpr float kSlack = 6.f;
-constexpr float kLift = 9.f;
+constexpr float kLift = 9.f, kUnlift = 1.f / 512.f;
 constexpr float kInf = __builtin_huge_valf();
 // What an item costs beside its stages, in stages: it counts in the shares, ahead of the item's first stage.
 #ifndef COLI_KV4_TILE_COST
@@ -893,7 +893,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         tc_fence_after_sync();
       }
       if (active && rows) {
-        const float inv = direct ? (l == 0.f ? 0.f : unscale / l) : unscale;
+        // unscale comes second: beside very small or very large values its product with the other factor may not be a
+        // normal number
+        const float inv = direct ? (l == 0.f ? 0.f : 1.f / l) : kUnlift;
         const size_t out_row = (size_t)((at.r0 + q_row / a.group) * a.out_stride) + (size_t)(at.head * a.group + q_row % a.group) * HD;
 #pragma unroll 1
         for (int k = 0; k < HD / 32; k++) {
@@ -904,7 +906,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
 #pragma unroll
             for (int h = 0; h < 2; h++)
 #pragma unroll
-              for (int i = 0; i < 16; i++) y[16 * h + 2 * (i % 8) + i / 8] = __uint_as_float(sv[16 * h + i]) * inv;
+              for (int i = 0; i < 16; i++) y[16 * h + 2 * (i % 8) + i / 8] = __uint_as_float(sv[16 * h + i]) * inv * unscale;
             if (l != l) {
 #pragma unroll
               for (int i = 0; i < 32; i++) y[i] = l;
@@ -936,7 +938,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
       }
       if (!direct) {
         if (lrow < row_n)  // a half without work has seen nothing
-          __stcg(reinterpret_cast<float2*>(mine + (size_t)kTileRows * HD + 2 * row), make_float2(mf - kLift, l));
+          __stcg(reinterpret_cast<float2*>(mine + (size_t)kTileRows * HD + 2 * row), make_float2(mf, l * kUnlift));
         const int b0 = (int)(item_at / per), b1 = (int)((item_at + at.stages - 1) / per);
         __threadfence();
         named_sync(1, kSoftThreads);

@@ -81,3 +81,29 @@ def test_values_near_the_ends_of_binary32(ctx, v_scale, rows, q_heads, dtype):
     out = b.attend(q_t, rows)
     assert B.coli_check_error(ctx) == 0
     within(b, out, *b.expect(q, rows))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,q_heads", FORMS)
+def test_sums_of_values_near_the_upper_end(ctx, rows, q_heads, dtype):
+    """Values of 1e35: a sum of 300 weights times them is finite, and so has to be every step on its way."""
+    b = Batch(ctx, [77, 300], 2, 128, 64, 32, dtype, v_scale=1e35)
+    q, q_t = b.queries(rows, q_heads)
+    out = b.attend(q_t, rows)
+    assert B.coli_check_error(ctx) == 0
+    within(b, out, *b.expect(q, rows))
+
+
+@pytest.mark.parametrize("v_scale", [1e-36, 1e35])
+def test_sums_that_one_cta_finishes(ctx, v_scale):
+    """More items than CTAs, so that many are finished where they are computed: 160 prompts of 140 rows over 900 tokens that
+    weigh about the same, values around three times their spread."""
+    b = Batch(ctx, [900] * 160, 1, 64, 64, 64, "bf16", k_scale=0.1, write=False)
+    b.v = (v_scale * (3 + b.v)).astype(np.float32)
+    B.coli_kv4_append(ctx, b.cache, b.k_t.float(), torch.from_numpy(b.v).cuda(), b.lens_t, b.table, b.start_t)
+    b.V = O.stored(b.v, 64)
+    rows = [140] * 160
+    q, q_t = b.queries(rows, 1)
+    out = b.attend(q_t, rows)
+    assert B.coli_check_error(ctx) == 0
+    within(b, out, *b.expect(q, rows))
