@@ -76,6 +76,9 @@ __device__ __forceinline__ const uint8_t* kv4_unit(const Kv4View& c, int page, i
   return c.base + unit * kv4_unit_bytes(c.hd, c.ng);
 }
 
+// Whether a group's scale | offset << 16 is of values that are not finite: NaN, or an offset that has rounded to infinity.
+__device__ __forceinline__ bool kv4_broken(uint32_t par) { return (par & 0x7f800000u) == 0x7f800000u; }
+
 // The rows [r0, r1) of sequence b, made safe: an order or a range that does not fit gives an empty range
 // and the error.
 __device__ __forceinline__ void kv4_rows(const Kv4Plan& p, int b, int& r0, int& r1, int* err) {

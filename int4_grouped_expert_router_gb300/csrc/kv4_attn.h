@@ -652,7 +652,12 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         for (int h = 0; h < 2; h++) {
           bool broken = false;
 #pragma unroll
-          for (int g = 0; g < NG; g++) broken = broken || (vp[h][g] & 0x7fff0000u) > 0x7f800000u;
+          for (int g = 0; g < NG; g++) {
+            if (kv4_broken(vp[h][g])) {
+              broken = true;
+              vp[h][g] = 0;
+            }
+          }
           if (broken) {
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) x[nt][2 * h] = x[nt][2 * h + 1] = __uint_as_float(0x7fc00000u);
@@ -801,7 +806,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
             for (int g = 0; g < NG; g++) {
               const float o0 = hi_bf16(p0[g]), o1 = hi_bf16(p1[g]);
               s[h][g] = __floats2half2_rn(live0 ? lo_bf16(p0[g]) * vmul : 0.f, live1 ? lo_bf16(p1[g]) * vmul : 0.f);
-              off[h][g] = __floats2half2_rn(live0 && o0 == o0 ? o0 * vmul : 0.f, live1 && o1 == o1 ? o1 * vmul : 0.f);
+              off[h][g] = __floats2half2_rn(live0 && fabsf(o0) < kInf ? o0 * vmul : 0.f, live1 && fabsf(o1) < kInf ? o1 * vmul : 0.f);
             }
           }
         }

@@ -604,8 +604,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
       bool broken = false;  // a value that is not finite is shown by its key: rows that do not see it have weight 0
 #pragma unroll
       for (int g = 0; g < NG; g++) {
-        broken = broken || (sc[g] & 0x7fff0000u) > 0x7f800000u;
-        big = fmaxf(big, fmaf(8.f, lo_bf16(sc[g]), fabsf(hi_bf16(sc[g]))));
+        const bool bad = kv4_broken(sc[g]);
+        broken = broken || bad;
+        big = fmaxf(big, bad ? 0.f : fmaf(8.f, lo_bf16(sc[g]), fabsf(hi_bf16(sc[g]))));
       }
       if (!live) big = 0.f;
       broken = __shfl_sync(0xffffffffu, broken, lane | 16);
@@ -632,9 +633,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         for (int g = 0; g < NG; g++) {
           float o = hi_bf16(sc[g]) * mul;
           if (lane < 16)
-            o = broken ? __uint_as_float(0x7fc00000u) : o;
+            o = broken || kv4_broken(sc[g]) ? __uint_as_float(0x7fc00000u) : o;
           else
-            o = o == o ? o : 0.f;
+            o = fabsf(o) < kInf ? o : 0.f;
           const uint32_t ready = bits(__floats2half2_rn(lo_bf16(sc[g]) * mul, o));
           sc[g] = live && (lane < 16 || vmul != 0.f) ? ready : 0u;
         }

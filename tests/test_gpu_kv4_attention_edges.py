@@ -107,3 +107,37 @@ def test_sums_that_one_cta_finishes(ctx, v_scale):
     out = b.attend(q_t, rows)
     assert B.coli_check_error(ctx) == 0
     within(b, out, *b.expect(q, rows))
+
+
+def spoil(b, where, tokens, channels, value):
+    """Write the batch's tokens again with `value` in some channels of the first head of one token of a sequence or more
+    (through binary32, which holds every value); the oracle's keys or values follow."""
+    k, v = torch.from_numpy(b.k.copy()), torch.from_numpy(b.v.copy())
+    for t in tokens:
+        (k if where == "keys" else v)[t, 0, channels] = value
+    B.coli_kv4_append(b.ctx, b.cache, k.cuda(), v.cuda(), b.lens_t, b.table, b.start_t)
+    b.K, b.V = O.stored(k.numpy(), b.gs), O.stored(v.numpy(), b.gs)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("where", ["keys", "values"])
+@pytest.mark.parametrize("value", [3.4e38, -3.4e38])
+@pytest.mark.parametrize("rows,q_heads,window", [([5], 2, 0), ([8], 4, 0), ([60], 4, 0), ([1], 4, 45), ([1], 24, 45), ([60], 4, 40)])
+def test_what_is_infinite_in_masked_places_is_not_seen(ctx, rows, q_heads, window, value, where, dtype):
+    """A whole group of 3.4e38 is finite, but its offset rounds to infinity. Rows before the token, and rows whose window has
+    left it, are as without it."""
+    b = Batch(ctx, [200], 2, 128, 32, 32, dtype)
+    m = rows[0]
+    token = 200 - m // 2 if m > 1 else 150
+    spoil(b, where, [token], slice(32, 64), value)
+    B.coli_check_error(ctx)
+    q, q_t = b.queries(rows, q_heads)
+    out = b.attend(q_t, rows, window=window)
+    ref, mag, size = b.expect(q, rows, window=window)
+    assert not np.isfinite(O.stored(np.full((1, 32), value, np.float32), 32)).any()
+    p = 200 - m + np.arange(m)
+    clear = (p < token) | ((p - window >= token) if window else False)
+    assert clear.any()
+    V = np.where(np.isfinite(b.V), b.V, 0)
+    tol = bound(ref, mag, size, dtype, 200, np.abs(V).max())
+    assert_within(out[torch.from_numpy(clear).cuda()], ref[clear], tol[clear])
