@@ -423,7 +423,8 @@ COLI_API int coli_kv4_read(coli_ctx *ctx, const coli_kv4_cache *cache, void *k, 
  * Scores, the softmax's maximum and sum, and the output are held in binary32 (bf16 queries: weights
  * and, for many rows, keys and values in 11 bits; f32: queries and weights in 22; what weighs less than
  * 2^-29 of a row's heaviest value may count as nothing). Results do not change from run to run. A non-finite
- * query sets COLI_E_NONFINITE and gives NaN in its row; a stored NaN that a row sees gives NaN there.
+ * query sets COLI_E_NONFINITE and gives NaN in its row. What is stored and not finite touches no row that does not see
+ * it: in a row that does, a value gives NaN (or an infinity) in the channels of its group, a key in the whole row.
  * Kernel forms, chosen on the host: up to 16 query rows per sequence and key/value head on average, f32, or
  * heads of 256 channels: a streaming form that reads the cache once per 16 rows; otherwise 256-row tiles on the
  * tensor cores. Each splits long sequences over the device. A context's first call allocates the memory for the

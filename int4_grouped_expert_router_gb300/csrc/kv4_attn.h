@@ -575,6 +575,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
     // shrinks, and the outputs with it.
     float vmul = __uint_as_float(253u << 23), eight = 8.f / vmul;
     bool stashed = false;                                  // part of the sums lies in the join buffer
+    uint32_t nan_groups = 0;                               // dequantised: by row and group, a value seen is not finite
     float* stash = s_join + warp * C::kRows * C::kPad + 2 * r;
     const int pos_min = it.len - it.m + tile_row / a.group;  // first row's position
     const int pos_max = it.len - it.m + (tile_row + row_n - 1) / a.group;
@@ -645,25 +646,6 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
               x[nt][j] = fmaf(ks[j >> 1], acc[0][nt][j] + acc[1][nt][j], fmaf(ko[j >> 1], sumq[nt][j & 1][g], x[nt][j]));
         }
       }
-      if constexpr (C::kDeq) {
-        // a value that is not finite is kept out of the product and shown by its token's score: rows that do not see
-        // the token have weight 0
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-          bool broken = false;
-#pragma unroll
-          for (int g = 0; g < NG; g++) {
-            if (kv4_broken(vp[h][g])) {
-              broken = true;
-              vp[h][g] = 0;
-            }
-          }
-          if (broken) {
-#pragma unroll
-            for (int nt = 0; nt < NT; nt++) x[nt][2 * h] = x[nt][2 * h + 1] = __uint_as_float(0x7fc00000u);
-          }
-        }
-      }
       if constexpr (kMasked) {
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
@@ -672,6 +654,21 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
             const int t = t0 + r + 8 * (j >> 1);
             if (t > pos[nt][j & 1] || t < kv4_from(pos[nt][j & 1], a.window)) x[nt][j] = -kInf;
           }
+      }
+      if constexpr (C::kDeq) {
+        // values that are not finite are kept out of the product, and noted in the rows that see them
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+          for (int g = 0; g < NG; g++)
+            if (kv4_broken(vp[h][g])) {
+              vp[h][g] = 0;
+#pragma unroll
+              for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < 2; e++)
+                  if (!kMasked || x[nt][2 * h + e] != -kInf) nan_groups |= 1u << ((nt * 2 + e) * NG + g);
+            }
       }
       // ---- running maximum: moves only when a score passes it by kSlack ----
       float y[NT][4], most = -kInf;
@@ -893,6 +890,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
     constexpr float kUnscale = C::kDeq ? 1.f / kTopScale : C::kRawV ? 16777216.f : 1.f;
     constexpr float kUnscale1 = C::kRawV ? kUnscale * 0.0625f : kUnscale;
     const float vinv = 1.f / vmul;
+    if constexpr (C::kDeq)
+      for (int s = 4; s < 32; s <<= 1) nan_groups |= __shfl_xor_sync(0xffffffffu, nan_groups, s);
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
@@ -913,7 +912,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         float* dst = s_join + (warp * C::kRows + row) * C::kPad + 2 * r;
 #pragma unroll
         for (int i = 0; i < C::kMt; i++) {
-          const float add = C::kDeq ? 0.f : bias[nt][e][(i / 2) / C::kWpg];
+          const int g = (i / 2) / C::kWpg;
+          const float add = !C::kDeq ? bias[nt][e][g] : nan_groups >> ((nt * 2 + e) * NG + g) & 1 ? __uint_as_float(0x7fc00000u) : 0.f;
           float2* at = reinterpret_cast<float2*>(dst + 16 * i);
           const float2 had = C::kRawV && stashed ? *at : make_float2(0.f, 0.f);
           *at = make_float2(fmaf((had.x + o[nt][i][e]) * kUnscale, vinv, add), fmaf((had.y + o[nt][i][2 + e]) * kUnscale1, vinv, add));

@@ -291,8 +291,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
   uint8_t* s_scale = s_raw + T::kRaw;     // [kTileUnits][keys, values][16 tokens][NG] scale | offset << 16
   __shared__ __align__(8) uint64_t raw_full, raw_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], par_full[4],
       q_full[2], s_full[2], p_full[2], o_full[2];
-  __shared__ float s_par[4][3];           // per stage: 1 / key factor, value factor (0: none yet), 1 / value factor
+  // per stage: 1 / key factor, value factor (0: none yet; below 0: s_nan names tokens of the stage), 1 / value factor
+  __shared__ float s_par[4][3];
   __shared__ float s_big[2][kConvWarps];  // largest key and value of each unit, when a factor has to move
+  __shared__ uint32_t s_nan[4][kConvWarps][NG];  // per stage, unit and group: tokens whose values are not finite
+  __shared__ uint8_t s_nan_row[kSoftThreads];    // of a row's segment: groups of which it has seen such values
   __shared__ uint32_t s_tmem;
   __shared__ long long s_w[kSeqChunk];
   __shared__ long long s_at;
@@ -601,7 +604,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
       if (lane == 0) mbar_arrive(&raw_empty);
       const bool live = (lane & 15) < left;
       float big = 0.f;      // the largest |o| + 8 s of the token
-      bool broken = false;  // a value that is not finite is shown by its key: rows that do not see it have weight 0
+      bool broken = false;  // a value is not finite: kept out of the products, and noted for the rows that see it
 #pragma unroll
       for (int g = 0; g < NG; g++) {
         const bool bad = kv4_broken(sc[g]);
@@ -609,23 +612,36 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         big = fmaxf(big, bad ? 0.f : fmaf(8.f, lo_bf16(sc[g]), fabsf(hi_bf16(sc[g]))));
       }
       if (!live) big = 0.f;
-      broken = __shfl_sync(0xffffffffu, broken, lane | 16);
+      broken = broken && live && lane >= 16;
       auto too_big = [](float x, float mul) { return mul == 0.f ? x > 0.f : x * mul >= 16384.f; };
-      if (named_sync_or(2, kConvWarps * 32, too_big(big, lane < 16 ? kmul : vmul))) {
+      if (named_sync_or(2, kConvWarps * 32, too_big(big, lane < 16 ? kmul : vmul) || broken)) {
         float kbig = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 16 ? __float_as_uint(big) : 0u));
         float vbig = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 16 ? 0u : __float_as_uint(big)));
         if (lane == 0) {
           s_big[0][cw] = kbig;
           s_big[1][cw] = vbig;
         }
-        named_sync(2, kConvWarps * 32);
+        const bool noted = named_sync_or(2, kConvWarps * 32, broken);  // the same in all converters
 #pragma unroll
         for (int i = 0; i < kConvWarps; i++) {
           kbig = fmaxf(kbig, s_big[0][i]);
           vbig = fmaxf(vbig, s_big[1][i]);
         }
+        if (noted) {
+          wait(&k_empty[n & 1], ((n >> 1) & 1) ^ 1);  // the softmax of four stages ago is long done
+#pragma unroll
+          for (int g = 0; g < NG; g++) {
+            const unsigned tokens = __ballot_sync(0xffffffffu, live && lane >= 16 && kv4_broken(sc[g])) >> 16;
+            if (lane == 0) s_nan[n & 3][cw][g] = tokens;
+          }
+          named_sync(2, kConvWarps * 32);
+        }
         if (too_big(kbig, kmul)) kmul = below_2_14(kbig), kinv = 1.f / kmul;
         if (too_big(vbig, vmul)) vmul = below_2_14(vbig), vinv = 1.f / vmul;
+        if (noted) {
+          if (vmul == 0.f) vmul = __uint_as_float(253u << 23), vinv = 1.f / vmul;
+          vinv = -vinv;  // until it is passed on
+        }
       }
       {
         const float mul = lane < 16 ? kmul : vmul;
@@ -633,7 +649,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         for (int g = 0; g < NG; g++) {
           float o = hi_bf16(sc[g]) * mul;
           if (lane < 16)
-            o = broken || kv4_broken(sc[g]) ? __uint_as_float(0x7fc00000u) : o;
+            o = kv4_broken(sc[g]) ? __uint_as_float(0x7fc00000u) : o;
           else
             o = fabsf(o) < kInf ? o : 0.f;
           const uint32_t ready = bits(__floats2half2_rn(lo_bf16(sc[g]) * mul, o));
@@ -646,10 +662,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
       wait(&k_empty[n & 1], ((n >> 1) & 1) ^ 1);
       if (cw == 0 && lane == 0) {  // the softmax of four stages ago is long done
         s_par[n & 3][0] = kinv;
-        s_par[n & 3][1] = vmul;
-        s_par[n & 3][2] = vinv;
+        s_par[n & 3][1] = copysignf(vmul, vinv);
+        s_par[n & 3][2] = fabsf(vinv);
         mbar_arrive(&par_full[n & 3]);
       }
+      vinv = fabsf(vinv);
       const uint32_t k_base = k_base0 + (n & 1) * T::kK;
       const int odd = r & 1;
 #pragma unroll
@@ -784,6 +801,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
       const int pos = at.len - at.m + (int)(q_row / a.group);
       const bool rows = (lrow & ~31) < row_n;  // a warp without rows only keeps the products' pace
       float mf = -kInf, l = 0.f, vmul = 0.f, unscale = 0.f;
+      s_nan_row[tid] = 0;
       if (active && !rows) {
         for (int j = split ? x : 0; j < n_here; j += split ? 2 : 1, ns++) {
           wait(&s_full[x], ns & 1);
@@ -800,7 +818,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
           const uint32_t par = (n + j) & 3;
           wait(&par_full[par], ((n + j) >> 2) & 1);
           // kept above 0, so that struck-out scores (minus infinity) stay so
-          const float fac = fmaxf(fac0 * s_par[par][0], 1e-37f), vnow = s_par[par][1];
+          const float fac = fmaxf(fac0 * s_par[par][0], 1e-37f);
+          float vnow = s_par[par][1];
           unscale = s_par[par][2];
           // columns [c0, c1) are visible to this row; the others are struck out where they lie
           const int c1 = min(kTileTok, max(0, pos - t0 + 1));
@@ -830,6 +849,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
           const float top = mx == -kInf ? -kInf : fac * mx;
           const bool grow = top > mf + kSlack;
           if (__any_sync(0xffffffffu, grow) || vnow != vmul) {
+            if (vnow < 0.f) {
+              vnow = -vnow;
+              uint32_t nan_groups = 0;
+#pragma unroll 1
+              for (int u = 0; u < kTileUnits; u++) {
+                // the unit's tokens [c0, c1)
+                const uint32_t sees = ((1u << min(16, max(0, c1 - 16 * u))) - 1) & ~((1u << min(16, max(0, c0 - 16 * u))) - 1);
+#pragma unroll
+                for (int g = 0; g < NG; g++) nan_groups |= (s_nan[par][u][g] & sees) != 0 ? 1u << g : 0u;
+              }
+              s_nan_row[tid] |= (uint8_t)nan_groups;
+            }
             const float shrink = vmul == 0.f ? 1.f : vnow / vmul;
             vmul = vnow;
             const float now = grow ? top : mf;
@@ -908,9 +939,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
             for (int h = 0; h < 2; h++)
 #pragma unroll
               for (int i = 0; i < 16; i++) y[16 * h + 2 * (i % 8) + i / 8] = __uint_as_float(sv[16 * h + i]) * inv * unscale;
-            if (l != l) {
+            if (l != l || (s_nan_row[tid] >> (k / T::kWpg) & 1)) {
 #pragma unroll
-              for (int i = 0; i < 32; i++) y[i] = l;
+              for (int i = 0; i < 32; i++) y[i] = __uint_as_float(0x7fc00000u);
             }
             if (direct) {
               uint16_t* o = static_cast<uint16_t*>(a.out) + out_row + k * 32;
@@ -977,7 +1008,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
 #pragma unroll
               for (int q = 0; q < 4; q++) {
                 const float now = fmaxf(mm[q], ml[q].x);
-                const float f = ml[q].y != ml[q].y ? 1.f : ml[q].x == -kInf ? 0.f : exp2_fast(ml[q].x - now);
+                // never 0 for what has seen something, so that a value that is not a number stays one
+                const float f = ml[q].y != ml[q].y ? 1.f : ml[q].x == -kInf ? 0.f : fmaxf(exp2_fast(ml[q].x - now), 0x1p-126f);
                 const float g = ll[q] != ll[q] ? 1.f : mm[q] == -kInf ? 0.f : exp2_fast(mm[q] - now);
                 mm[q] = now;
                 ll[q] *= g;

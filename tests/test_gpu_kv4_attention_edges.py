@@ -141,3 +141,44 @@ def test_what_is_infinite_in_masked_places_is_not_seen(ctx, rows, q_heads, windo
     V = np.where(np.isfinite(b.V), b.V, 0)
     tol = bound(ref, mag, size, dtype, 200, np.abs(V).max())
     assert_within(out[torch.from_numpy(clear).cuda()], ref[clear], tol[clear])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,rows,q_heads", [([77, 300], [1, 1], 8), ([77, 300], [1, 1], 24), ([120, 300], [70, 90], 8),
+                                               ([6000, 900], [1, 1], 8), ([6000, 900], [1, 1], 24), ([6000, 900], [20, 40], 8)])
+def test_a_value_that_is_not_a_number_spoils_its_group_alone(ctx, lens, rows, q_heads, dtype):
+    """The channels of the group, of the heads that share the key/value head, in the rows that see the token, however many
+    rows there are and however the tokens are split."""
+    b = Batch(ctx, lens, 2, 128, 32, 32, dtype)
+    # before every row of sequence 0, and between the rows of sequence 1 (or before its only row)
+    spoil(b, "values", [3], slice(40, 41), float("nan"))
+    spoil(b, "values", [3, lens[0] + lens[1] - 1 - rows[1] // 2], slice(40, 41), float("nan"))
+    assert B.coli_check_error(ctx) == B.COLI_E_NONFINITE
+    q, q_t = b.queries(rows, q_heads)
+    out = b.attend(q_t, rows).float().cpu().numpy().astype(np.float64)
+    assert B.coli_check_error(ctx) == 0
+    ref, mag, size = b.expect(q, rows)
+    bad = np.isnan(ref)
+    assert bad[:, :q_heads // 2, 32:64].any() and not bad[:, q_heads // 2:].any() and not bad[..., 64:].any()
+    assert np.array_equal(np.isnan(out), bad)
+    tol = bound(ref, mag, size, dtype, max(lens), np.nanmax(np.abs(b.V)))
+    assert (np.abs(out - ref)[~bad] <= tol[~bad]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,rows,q_heads", [([77, 300], [1, 1], 8), ([77, 300], [1, 1], 24), ([120, 300], [70, 90], 8),
+                                               ([6000, 900], [20, 40], 8)])
+def test_a_key_that_is_not_a_number_spoils_its_heads_rows(ctx, lens, rows, q_heads, dtype):
+    b = Batch(ctx, lens, 2, 128, 32, 32, dtype)
+    spoil(b, "keys", [3, lens[0] + lens[1] - 1 - rows[1] // 2], slice(40, 41), float("nan"))
+    assert B.coli_check_error(ctx) == B.COLI_E_NONFINITE
+    q, q_t = b.queries(rows, q_heads)
+    out = b.attend(q_t, rows).float().cpu().numpy().astype(np.float64)
+    assert B.coli_check_error(ctx) == 0
+    with np.errstate(invalid="ignore"):
+        ref, mag, size = b.expect(q, rows)
+    bad = np.isnan(ref)
+    assert bad[:rows[0], :q_heads // 2].all() and not bad[:, q_heads // 2:].any()
+    assert np.array_equal(np.isnan(out), bad)
+    tol = bound(ref, mag, size, dtype, max(lens), np.abs(b.V).max())
+    assert (np.abs(out - ref)[~bad] <= tol[~bad]).all()
