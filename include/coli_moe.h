@@ -383,7 +383,8 @@ COLI_API int coli_ans_w4_linear(coli_ctx *ctx, uint64_t handle, const float *sca
  * outside the cache, or a row range outside 0..T sets COLI_E_RANGE; nothing outside the arrays is
  * touched, the length is clamped, rows of a bad page are not written and read as zeros, and an
  * attention over one has undefined (finite or NaN) values for that sequence.
- * Sequences may share pages that no call in flight writes.
+ * Sequences may share pages that no call in flight writes. Pages whose tokens come before the window of
+ * every row of the call (coli_kv4_attention with a window) may be given back: their entries may hold anything.
  */
 typedef struct coli_kv4_cache {
   void *base;          /* device pointer, 16-byte aligned, coli_kv4_bytes() bytes */

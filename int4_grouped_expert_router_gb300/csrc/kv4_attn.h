@@ -406,8 +406,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         const int at = tok + k * per_copy * kKvUnit;
         int pg = __ldcg(a.p.table + (size_t)it.b * a.p.table_stride + (at >> a.c.page_log2));
         if (pg < 0 || pg >= a.c.pages) {
-          set_error(a.err, COLI_E_RANGE);
-          pg = 0;  // some page of the cache in its place
+          if (at + per_copy * kKvUnit > kv4_from(it.len - it.m, a.window)) set_error(a.err, COLI_E_RANGE);
+          pg = 0;  // some page of the cache in its place; no row sees a page that its window has left
         }
         src[k] = a.c.base + pg * page_bytes + (uint32_t)(it.head * (page_tok / kKvUnit) + (at & (page_tok - 1)) / kKvUnit) * C::kUnit;
       }
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
       for (int h = 0; h < 2; h++) {
         lds_words(unit + kv4_kscale_at(HD) + (r + 8 * h) * NG * 4, kp[h]);
         lds_words(unit + kv4_vscale_at(HD, NG) + (r + 8 * h) * NG * 4, vp[h]);
-        if (kMasked && t0 + r + 8 * h >= it.len) {  // tokens past the sequence hold anything
+        if (kMasked && (t0 + r + 8 * h >= it.len || t0 + r + 8 * h < lo_min)) {  // tokens that no row sees hold anything
 #pragma unroll
           for (int g = 0; g < NG; g++) vp[h][g] = 0;
         }
@@ -798,7 +798,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
             const uint32_t at = unit + kv4_vscale_at(HD, NG) + (2 * cc + 8 * h) * NG * 4;
             lds_words(at, p0);
             lds_words(at + NG * 4, p1);
-            const bool live0 = !kMasked || t0 + 2 * cc + 8 * h < it.len, live1 = !kMasked || t0 + 2 * cc + 8 * h + 1 < it.len;
+            const int t = t0 + 2 * cc + 8 * h;
+            const bool live0 = !kMasked || (t < it.len && t >= lo_min), live1 = !kMasked || (t + 1 < it.len && t + 1 >= lo_min);
 #pragma unroll
             for (int g = 0; g < NG; g++) {
               const float o0 = hi_bf16(p0[g]), o1 = hi_bf16(p1[g]);

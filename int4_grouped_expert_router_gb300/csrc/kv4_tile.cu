@@ -100,17 +100,18 @@ struct Item {
   int b, tile, head;
   int r0, m, len;
   int first, stages;  // first stage of kTileTok tokens, number of stages (at least 1)
+  int lo;             // first token that a row of the tile sees
 };
 
 __device__ __forceinline__ int tiles_of(int m, int group) { return (int)(((long long)m * group + kTileRows - 1) / kTileRows); }
 
 // Stages of tile k of a sequence: from the window of its first row to the position of its last.
-__device__ __forceinline__ void tile_span(const TileArgs& a, int m, int len, int k, int& first, int& stages) {
+__device__ __forceinline__ void tile_span(const TileArgs& a, int m, int len, int k, int& first, int& stages, int& lo) {
   const long long row0 = (long long)k * kTileRows;
   const long long all = (long long)m * a.group;
   const long long last_row = row0 + kTileRows - 1 < all - 1 ? row0 + kTileRows - 1 : all - 1;
   const int last = len - m + (int)(last_row / a.group);
-  const int lo = kv4_from(len - m + (int)(row0 / a.group), a.window);
+  lo = kv4_from(len - m + (int)(row0 / a.group), a.window);
   first = last < 0 ? 0 : lo / kTileTok;
   stages = last < 0 ? 1 : last / kTileTok - first + 1;
 }
@@ -129,8 +130,8 @@ __device__ __forceinline__ long long seq_stages(const TileArgs& a, int b) {
   load_seq(a, it);
   long long sum = 0;
   for (int k = threadIdx.x & 31, n = tiles_of(it.m, a.group); k < n; k += 32) {
-    int first, stages;
-    tile_span(a, it.m, it.len, k, first, stages);
+    int first, stages, lo;
+    tile_span(a, it.m, it.len, k, first, stages, lo);
     sum += stages + kItemCost;
   }
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -382,8 +383,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
     long long at = s_at;
     const int n = tiles_of(it.m, a.group);
     for (int k0 = 0; k0 < n; k0 += 32) {
-      int first, stages = 0;
-      if (k0 + lane < n) tile_span(a, it.m, it.len, k0 + lane, first, stages);
+      int first, stages = 0, lo;
+      if (k0 + lane < n) tile_span(a, it.m, it.len, k0 + lane, first, stages, lo);
       const long long mine = k0 + lane < n ? (long long)(stages + kItemCost) * heads : 0;
       long long inc = mine;
       for (int o = 1; o < 32; o <<= 1) {
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
   const uint32_t tmem = s_tmem;
 
   it.tile = s_start_tile;
-  tile_span(a, it.m, it.len, it.tile, it.first, it.stages);
+  tile_span(a, it.m, it.len, it.tile, it.first, it.stages, it.lo);
   const long long local = w0 - s_at;
   it.head = (int)(local / (it.stages + kItemCost));
   // below 0: in the item's cost. w counts stages and costs.
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         load_seq(a, it);
       } while (it.m == 0 && it.b + 1 < a.p.B);
     }
-    tile_span(a, it.m, it.len, it.tile, it.first, it.stages);
+    tile_span(a, it.m, it.len, it.tile, it.first, it.stages, it.lo);
   };
   auto rows_here = [&]() { return (int)min((long long)kTileRows, (long long)it.m * a.group - (long long)it.tile * kTileRows); };
   bool alive = true;
@@ -462,8 +463,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
       int pg = __shfl_sync(0xffffffffu, pages, (page - cached_from + lane) & 31);
       if (lane < copies && !held) {
         if (pg < 0 || pg >= a.c.pages) {
-          set_error(a.err, COLI_E_RANGE);
-          pg = 0;  // some page of the cache in its place
+          if (tok + (lane + 1) * per_copy * kKvUnit > it.lo) set_error(a.err, COLI_E_RANGE);
+          pg = 0;  // some page of the cache in its place; no row sees a page that its window has left
         }
         const int take = min(per_copy, units - lane * per_copy);
         const uint8_t* src = a.c.base + (((size_t)pg * heads + it.head) * (size_t)(page_tok / kKvUnit) +
@@ -602,7 +603,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
       lds_words(unit + (lane < 16 ? kv4_kscale_at(HD) : kv4_vscale_at(HD, NG)) + (lane & 15) * NG * 4, sc);
       __syncwarp();
       if (lane == 0) mbar_arrive(&raw_empty);
-      const bool live = (lane & 15) < left;
+      // tokens that no row of the tile sees hold anything
+      const bool live = (lane & 15) < left && (lane & 15) >= it.lo - (it.first + stage) * kTileTok - cw * 16;
       float big = 0.f;      // the largest |o| + 8 s of the token
       bool broken = false;  // a value is not finite: kept out of the products, and noted for the rows that see it
 #pragma unroll

@@ -182,3 +182,23 @@ def test_a_key_that_is_not_a_number_spoils_its_heads_rows(ctx, lens, rows, q_hea
     assert np.array_equal(np.isnan(out), bad)
     tol = bound(ref, mag, size, dtype, max(lens), np.abs(b.V).max())
     assert (np.abs(out - ref)[~bad] <= tol[~bad]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,q_heads", [([1, 1], 8), ([1, 1], 24), ([7, 3], 4), ([70, 90], 8), ([140, 20], 4)])
+@pytest.mark.parametrize("page,window", [(16, 50), (64, 1), (16, 17), (32, 200)])
+def test_pages_that_the_window_has_left_may_be_gone(ctx, page, window, rows, q_heads, dtype):
+    """A server that gives back pages older than any row's window marks them as it likes."""
+    b = Batch(ctx, [900, 333], 2, 128, 64, page, dtype)
+    q, q_t = b.queries(rows, q_heads)
+    with_all = b.attend(q_t, rows, window=window)
+    gone = 0
+    for i, (n, m) in enumerate(zip(b.lens, rows)):
+        left = max(0, n - m - window + 1) // page  # whole pages before the first row's window
+        b.table[i, :left] = torch.tensor([-1, b.cache.pages, -(1 << 31), (1 << 31) - 1], dtype=torch.int32).repeat(left)[:left].cuda()
+        gone += left
+    assert gone > 0
+    out = b.attend(q_t, rows, window=window)
+    assert B.coli_check_error(ctx) == 0
+    assert torch.equal(out, with_all)
+    within(b, out, *b.expect(q, rows, window=window))
