@@ -870,6 +870,28 @@ static int kv4_check(coli_ctx* ctx, const char* who, const coli_kv4_cache* cache
   return COLI_OK;
 }
 
+// Whether T rows of `row` bytes from a on, sa bytes apart, share a byte with T such rows from b on, sb apart (strides of at
+// least a row).
+static bool rows_overlap(uintptr_t a, long long sa, uintptr_t b, long long sb, long long row, int T) {
+  const long long d = (long long)(b - a);  // row j of b lies d + j sb - i sa after row i of a
+  if (d >= (T - 1) * sa + row || -d >= (T - 1) * sb + row) return false;
+  auto meet = [&](long long i, long long j) {
+    const long long off = d + j * sb - i * sa;
+    return i >= 0 && i < T && j >= 0 && j < T && off < row && -off < row;
+  };
+  if (sa == sb) {  // slices of one array: only i - j counts
+    const long long k = d / sa;
+    for (long long i = k - 1; i <= k + 1; i++)
+      if (i < 0 ? meet(0, -i) : meet(i, 0)) return true;
+    return false;
+  }
+  for (long long i = 0; i < T; i++) {
+    const long long j = (i * sa - d) / sb;
+    if (meet(i, j - 1) || meet(i, j) || meet(i, j + 1)) return true;
+  }
+  return false;
+}
+
 static Kv4View kv4_view(const coli_kv4_cache* c) {
   Kv4View v;
   v.base = static_cast<uint8_t*>(c->base);
@@ -927,6 +949,9 @@ int coli_kv4_attention(coli_ctx* ctx, const coli_kv4_cache* cache, const void* q
   const long long row = (long long)q_heads * cache->head_dim;
   if (q_stride < row || out_stride < row)
     return fail(ctx, COLI_E_INVAL, "kv4_attention: row stride below q_heads * head_dim");
+  const long long elem = dtype == COLI_DTYPE_F32 ? 4 : 2;
+  if (rows_overlap((uintptr_t)q, q_stride * elem, (uintptr_t)out, out_stride * elem, row * elem, T))
+    return fail(ctx, COLI_E_INVAL, "kv4_attention: out overlaps q");
   if (!(scale == scale) || scale - scale != 0.f) return fail(ctx, COLI_E_INVAL, "kv4_attention: scale must be finite");
   if (window < 0) return fail(ctx, COLI_E_INVAL, "kv4_attention: window must not be negative");
   if (injected(ctx)) return COLI_E_INJECTED;

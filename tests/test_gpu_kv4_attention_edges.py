@@ -202,3 +202,34 @@ def test_pages_that_the_window_has_left_may_be_gone(ctx, page, window, rows, q_h
     assert B.coli_check_error(ctx) == 0
     assert torch.equal(out, with_all)
     within(b, out, *b.expect(q, rows, window=window))
+
+
+@pytest.mark.parametrize("T", [1, 3])
+def test_out_over_q_is_refused_and_slices_beside_it_are_not(ctx, T):
+    b = Batch(ctx, [50, 90, 7][:T], 2, 128, 64, 16, "bf16")
+    _, q = b.queries([1] * T, 4)
+    row = 4 * 128
+    want = b.attend(q, [1] * T)
+    buf = torch.zeros(8 * T * row, dtype=q.dtype, device="cuda")
+
+    def rows(at, stride):
+        return buf.as_strided((T, 4, 128), (stride, 128, 1), at)
+
+    base = 4 * row
+    # places of out: on q, a little before and after it, on its last row, between its rows but too near
+    for stride, at, out_stride in ((row, base, row), (row, base + 1, row), (row, base - 1, row), (row, base + T * row - 1, row),
+                                   (row, base - T * row + 1, row), (2 * row + 1, base + row - 1, 2 * row + 1),
+                                   (2 * row, base + row // 2, row + 3)):
+        if T == 1 and abs(at - base) >= row:
+            continue
+        with pytest.raises(B.ColiError) as e:
+            B.coli_kv4_attention(ctx, b.cache, rows(base, stride), b.lens_t, b.table, rows(at, out_stride))
+        assert e.value.code == B.COLI_E_INVAL and "overlaps" in B.coli_last_error(ctx)
+    for stride, at, out_stride in ((row, base + T * row, row), (row, base - T * row, row), (2 * row, base + row, 2 * row),
+                                   (2 * row, base - row, 2 * row), (2 * row + 1, base + row, 2 * row + 1), (2 * row, 0, row)):
+        buf.zero_()
+        q2, out = rows(base, stride), rows(at, out_stride)
+        q2.copy_(q)
+        B.coli_kv4_attention(ctx, b.cache, q2, b.lens_t, b.table, out)
+        assert torch.equal(out, want) and torch.equal(q2, q)
+    assert B.coli_check_error(ctx) == 0
