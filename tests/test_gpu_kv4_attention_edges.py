@@ -7,7 +7,7 @@ import torch
 import oracle.kv4 as O
 from int4_grouped_expert_router_gb300 import binding as B
 from gpu_util import Ctx
-from kv4_util import Batch, assert_within, bound
+from kv4_util import Batch, as_dtype, assert_within, bound, rng
 
 pytestmark = pytest.mark.gpu
 
@@ -233,3 +233,25 @@ def test_out_over_q_is_refused_and_slices_beside_it_are_not(ctx, T):
         B.coli_kv4_attention(ctx, b.cache, q2, b.lens_t, b.table, out)
         assert torch.equal(out, want) and torch.equal(q2, q)
     assert B.coli_check_error(ctx) == 0
+
+
+def test_queries_count_down_to_two_to_the_minus_27_of_their_largest(ctx):
+    """bf16 queries are held in 16 bits at a common power of two per row. A channel of 1 beside channels of about 2^-27 that
+    meet keys of 2^27, while the 1 meets keys of 0: every bit of the small ones is in the scores."""
+    r = rng("spread")
+    n, hd, gs = 60, 128, 32
+    b = Batch(ctx, [n], 1, hd, gs, 16, "bf16", write=False)
+    k = 2.0 ** 27 * r.normal(size=(n, 1, hd))
+    k[..., :gs] = 0
+    b.k, b.k_t = as_dtype(k, "bf16")
+    B.coli_kv4_append(ctx, b.cache, b.k_t, b.v_t, b.lens_t, b.table, b.start_t)
+    b.K = O.stored(b.k, gs)
+    for m, heads in ((1, 8), (1, 16), (30, 8)):
+        q = r.choice([-1.0, 1.0], size=(m, heads, hd)) * r.integers(128, 256, size=(m, heads, hd)) * 2.0 ** -34
+        q[..., 0] = 1
+        b.queries([m], heads)  # the rows' place
+        q, q_t = as_dtype(q, "bf16")
+        assert np.array_equal(q[..., 1:] * 2.0 ** 34, np.rint(q[..., 1:] * 2.0 ** 34))
+        out = b.attend(q_t, [m], scale=0.25)
+        assert B.coli_check_error(ctx) == 0
+        within(b, out, *b.expect(q, [m], scale=0.25))
