@@ -32,7 +32,8 @@ constexpr int kPanelCols = 16;
 // logits of at most 15 tokens x 1024 (column part, expert) pairs.
 constexpr size_t kRouterScratchBytes = 256 + (size_t)15 * 1024 * 8;
 
-// Arrival counters of split work in the cache attention (one per CTA of its grid), zero between calls.
+// Arrival counters of split work in the cache attention (the streaming form uses three per CTA of its grid, the tensor-core
+// form one), zero between calls.
 constexpr int kKvCounters = 4096;
 // Partial results of the cache attention, in floats per SM: two for the tensor-core form's CTA of 256 rows of 128 channels
 // and a (maximum, sum) pair, and more than any CTAs of the streaming form leave.

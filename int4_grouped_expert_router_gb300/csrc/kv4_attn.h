@@ -6,7 +6,8 @@
 // one pass over the tokens with a running maximum and sum. The codes enter the matrix instructions as the small
 // integers that they are (exact in 16 bits): a group's scale and offset are applied to the score of its token, and to
 // the weight a_t before V. Queries enter in 16 bits after a power of two has brought a row's largest to 2^14 (bf16
-// ones then are exact down to 2^-29 of it); f32 queries and weights enter as a sum of two 16-bit values.
+// ones then are exact down to 2^-27 of it: half of them also take a factor 1/16); f32 queries and weights enter as a sum
+// of two 16-bit values.
 //
 // What bounds it: the cache's bytes, read once (a key/value head's codes serve all of its query heads), and beside
 // them the instructions that unpack codes and weigh tokens, about 330 per 16 tokens of a head (hd = 128, one group):
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
     const int row_n = min(C::kRows, rows_all - tile_row);
 
     // queries: fragments of 16-bit integers-friendly values (each row scaled by a power of two so that its
-    // largest element lies in [2^14, 2^15): bf16 elements down to 2^-29 of it stay exact), their sums per
+    // largest element lies in [2^14, 2^15): bf16 elements down to 2^-27 of it stay exact, kOdd counted), their sums per
     // group, and the factor that takes a row's scores to log2 units.
     float fac[NT][2], sumq[NT][2][NG];
     int pos[NT][2];
