@@ -225,6 +225,12 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   return r;
 }
 
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
 __device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
@@ -604,26 +610,34 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&raw_empty);
       // tokens that no row of the tile sees hold anything
-      const bool live = (lane & 15) < left && (lane & 15) >= it.lo - (it.first + stage) * kTileTok - cw * 16;
-      float big = 0.f;      // the largest |o| + 8 s of the token
-      bool broken = false;  // a value is not finite: kept out of the products, and noted for the rows that see it
+      const int before = max(0, it.lo - (it.first + stage) * kTileTok - cw * 16);
+      const bool live = (uint32_t)((lane & 15) - before) < (uint32_t)max(0, left - before);
+      float big = 0.f;  // the largest |o| + 8 s of the token; not a number, or infinite, if a key or value is not finite
 #pragma unroll
-      for (int g = 0; g < NG; g++) {
-        const bool bad = kv4_broken(sc[g]);
-        broken = broken || bad;
-        big = fmaxf(big, bad ? 0.f : fmaf(8.f, lo_bf16(sc[g]), fabsf(hi_bf16(sc[g]))));
-      }
+      for (int g = 0; g < NG; g++) big = max_nan(big, fmaf(8.f, lo_bf16(sc[g]), fabsf(hi_bf16(sc[g]))));
       if (!live) big = 0.f;
-      broken = broken && live && lane >= 16;
-      auto too_big = [](float x, float mul) { return mul == 0.f ? x > 0.f : x * mul >= 16384.f; };
-      if (named_sync_or(2, kConvWarps * 32, too_big(big, lane < 16 ? kmul : vmul) || broken)) {
+      auto too_big = [](float x, float mul) { return mul == 0.f ? !(x <= 0.f) : !(x * mul < 16384.f); };
+      if (named_sync_or(2, kConvWarps * 32, too_big(big, lane < 16 ? kmul : vmul))) {
+        // What is not finite stays out of the factors. A key becomes NaN, as its scores then do; a value becomes 0, and is
+        // noted for the rows that see it.
+        uint32_t broken = 0;
+        big = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; g++) {
+          if (kv4_broken(sc[g])) {
+            broken |= live && lane >= 16 ? 1u << g : 0u;
+            sc[g] = lane < 16 ? 0x7fc00000u : 0u;
+          } else if (live) {
+            big = fmaxf(big, fmaf(8.f, lo_bf16(sc[g]), fabsf(hi_bf16(sc[g]))));
+          }
+        }
         float kbig = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 16 ? __float_as_uint(big) : 0u));
         float vbig = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 16 ? 0u : __float_as_uint(big)));
         if (lane == 0) {
           s_big[0][cw] = kbig;
           s_big[1][cw] = vbig;
         }
-        const bool noted = named_sync_or(2, kConvWarps * 32, broken);  // the same in all converters
+        const bool noted = named_sync_or(2, kConvWarps * 32, broken != 0);  // the same in all converters
 #pragma unroll
         for (int i = 0; i < kConvWarps; i++) {
           kbig = fmaxf(kbig, s_big[0][i]);
@@ -633,7 +647,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
           wait(&k_empty[n & 1], ((n >> 1) & 1) ^ 1);  // the softmax of four stages ago is long done
 #pragma unroll
           for (int g = 0; g < NG; g++) {
-            const unsigned tokens = __ballot_sync(0xffffffffu, live && lane >= 16 && kv4_broken(sc[g])) >> 16;
+            const unsigned tokens = __ballot_sync(0xffffffffu, broken >> g & 1) >> 16;
             if (lane == 0) s_nan[n & 3][cw][g] = tokens;
           }
           named_sync(2, kConvWarps * 32);
@@ -649,12 +663,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(TileArgs a) {
         const float mul = lane < 16 ? kmul : vmul;
 #pragma unroll
         for (int g = 0; g < NG; g++) {
-          float o = hi_bf16(sc[g]) * mul;
-          if (lane < 16)
-            o = kv4_broken(sc[g]) ? __uint_as_float(0x7fc00000u) : o;
-          else
-            o = fabsf(o) < kInf ? o : 0.f;
-          const uint32_t ready = bits(__floats2half2_rn(lo_bf16(sc[g]) * mul, o));
+          const uint32_t ready = bits(__floats2half2_rn(lo_bf16(sc[g]) * mul, hi_bf16(sc[g]) * mul));
           sc[g] = live && (lane < 16 || vmul != 0.f) ? ready : 0u;
         }
         sts_words(scales + lane * NG * 4, sc);
