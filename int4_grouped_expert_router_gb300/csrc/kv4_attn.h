@@ -107,11 +107,14 @@ struct Cfg {
   static constexpr bool kRawK = !F32;
   static constexpr float kOdd = kRawK ? 0.0625f : 1.f;           // queries of codes at bit 4, which count sixteenfold
   static constexpr float kUnitK = kRawK ? 16777216.f : 1.f;      // a code is this many times what enters
-  // Value codes enter as they lie (0..15), which needs the sums cut short: the instruction cuts its accumulator off
-  // instead of rounding it, and codes that are not centred make the sum large beside the result.
+  // Value codes enter as they are (0..15). The instruction cuts its accumulator off instead of rounding it, and codes
+  // that are not centred make the sum large beside the result, so that what is cut shows there, always downward: hence
+  // codes at bit 4, and sums that leave the accumulator after kSumUnits. Balanced values then cancel to 2^-22 of eight
+  // steps (2^-18.5 with codes as they lie and 64 units, where 131071 tokens came out 0.07 % too low; that took 80 us for
+  // the batch of 64, this 84, centred codes 86).
   static constexpr bool kRawV = !F32 && NT == 1;
   static constexpr float kTop = kDeq ? 16384.f : kTopScale;  // dequantised values and weights are rounded apart
-  static constexpr int kSumUnits = 64;  // units after which a sum moves to shared memory
+  static constexpr int kSumUnits = 16;  // units after which a sum moves to shared memory
   static constexpr int kCtas = HD == 256 ? (NT == 1 ? 2 : 1) : NT == 1 ? 3 : 2;  // resident per SM (registers)
   static constexpr uint32_t kJoin = kStageUnits * kRows * (kPad + 2) * 4;
   static constexpr uint32_t kQ = NT * (HD / 16) * 32 * 8 * (F32 ? 2 : 1);
@@ -164,13 +167,23 @@ __device__ __forceinline__ void expand(uint32_t w, uint32_t (&a)[4]) {
 }
 
 // The same pairs as they lie, one logic operation each: a nibble at the end of a 16-bit float's mantissa is the
-// subnormal number n 2^-24, at bit 4 n 2^-20, and the matrix instruction takes subnormal operands at full precision.
+// subnormal number n 2^-24, at bit 4 n 2^-20, which the matrix instruction takes as they are. Its sum, however, is cut off
+// some 24 bits below the operands' smallest normal number times the other factor, whatever leading zeros a subnormal one
+// has: at the mantissa's end 18 to 19 bits of the sum are left.
 __device__ __forceinline__ void expand_raw(uint32_t w, uint32_t (&a)[4]) {
   const uint32_t w8 = w >> 8;
   a[0] = w & 0x000f000fu;
   a[1] = w & 0x00f000f0u;
   a[2] = w8 & 0x000f000fu;
   a[3] = w8 & 0x00f000f0u;
+}
+
+// The same pairs as n 2^-20, all at bit 4: so the sum keeps 22 bits.
+__device__ __forceinline__ void expand_raw4(uint32_t w, uint32_t (&a)[4]) {
+  a[0] = (w << 4) & 0x00f000f0u;
+  a[1] = w & 0x00f000f0u;
+  a[2] = (w >> 4) & 0x00f000f0u;
+  a[3] = (w >> 8) & 0x00f000f0u;
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -814,8 +827,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
           const int g = i / C::kWpg;
           uint32_t a0[4], a1[4];
           if constexpr (C::kRawV) {
-            expand_raw(vw[0][i], a0);
-            expand_raw(vw[1][i], a1);
+            expand_raw4(vw[0][i], a0);
+            expand_raw4(vw[1][i], a1);
           } else {
             expand(vw[0][i], a0);
             expand(vw[1][i], a1);
@@ -887,10 +900,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
     }
 
     // ---- join the four warps ----
-    // exact: powers of two, one after the other (their product may not be a number); the channels whose codes lie at bit 4
-    // count sixteenfold
-    constexpr float kUnscale = C::kDeq ? 1.f / kTopScale : C::kRawV ? 16777216.f : 1.f;
-    constexpr float kUnscale1 = C::kRawV ? kUnscale * 0.0625f : kUnscale;
+    // exact: powers of two, one after the other (their product may not be a number)
+    constexpr float kUnscale = C::kDeq ? 1.f / kTopScale : C::kRawV ? 1048576.f : 1.f;
     const float vinv = 1.f / vmul;
     if constexpr (C::kDeq)
       for (int s = 4; s < 32; s <<= 1) nan_groups |= __shfl_xor_sync(0xffffffffu, nan_groups, s);
@@ -918,7 +929,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
           const float add = !C::kDeq ? bias[nt][e][g] : nan_groups >> ((nt * 2 + e) * NG + g) & 1 ? __uint_as_float(0x7fc00000u) : 0.f;
           float2* at = reinterpret_cast<float2*>(dst + 16 * i);
           const float2 had = C::kRawV && stashed ? *at : make_float2(0.f, 0.f);
-          *at = make_float2(fmaf((had.x + o[nt][i][e]) * kUnscale, vinv, add), fmaf((had.y + o[nt][i][2 + e]) * kUnscale1, vinv, add));
+          *at = make_float2(fmaf((had.x + o[nt][i][e]) * kUnscale, vinv, add), fmaf((had.y + o[nt][i][2 + e]) * kUnscale, vinv, add));
         }
       }
     named_sync(1, kConsumers);

@@ -81,3 +81,31 @@ def test_more_than_64_stages_of_an_item_in_a_cta(ctx, dtype, hd, gs, q_heads):
     parts = [O.attention(q[i:i + 1], b.K[:m], b.V[:m], [m - 1], hd ** -0.5) for i, m in enumerate(lens)]
     ref, mag, size = (np.concatenate(x) for x in zip(*parts))
     assert_within(out, ref, bound(ref, mag, size, dtype, n, np.abs(b.V).max()))
+
+
+@pytest.mark.parametrize("hd,gs", [(64, 64), (128, 32)])
+@pytest.mark.parametrize("q_heads", [1, 8, 16])
+def test_values_that_cancel_leave_what_32_bits_leave(ctx, hd, gs, q_heads):
+    """Every second token has its neighbour's key and the negative of its value, all of them eighths, so that a bf16 call's
+    rounded weights cancel too and the output is 0 (its own rounding then hides nothing). A sum of products whose terms are
+    all of one sign, at most 8 s = 1 times the sum of the weights, loses less than 2^-23 of itself with each step that is
+    cut off: 2^-19.9 over 16 steps as it grows, and once more as much below for the terms and the sums after."""
+    n, B_, s = 30000, 160, 0.125
+    r = rng("balanced", hd, gs)
+    codes = r.integers(1, 16, (n // 2, 1, hd))
+    codes = np.stack([codes, 16 - codes], 1).reshape(n, 1, hd)
+    codes[..., ::gs], codes[..., 1::gs] = 0, 15  # of each group, so that its scale is s and its offset 0
+    b = Batch(ctx, [n], 1, hd, gs, 64, "bf16", write=False)
+    _, k_t = as_dtype(np.repeat(r.normal(size=(n // 2, 1, hd)), 2, 0), "bf16")
+    v, v_t = as_dtype(s * (codes - 8), "bf16")
+    assert np.array_equal(O.stored(v, gs), v)
+    B.coli_kv4_append(ctx, b.cache, k_t, v_t, b.lens_t, b.table, b.start_t)
+    _, q_t = as_dtype(1.2 * r.normal(size=(B_, q_heads, hd)), "bf16")
+    out = torch.empty_like(q_t)
+    B.coli_kv4_attention(ctx, b.cache, q_t, torch.tensor([n - 2 * i for i in range(B_)], dtype=torch.int32).cuda(),
+                         b.table.repeat(B_, 1), out)
+    assert B.coli_check_error(ctx) == 0
+    out = out.float().cpu().numpy()
+    fixed = np.arange(hd) % gs < 2
+    assert np.abs(out[..., fixed] - v[0, 0, fixed]).max() <= 2.0 ** -9
+    assert np.abs(out[..., ~fixed]).max() <= 2.0 ** -18.9
