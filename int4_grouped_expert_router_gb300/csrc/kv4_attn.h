@@ -227,6 +227,12 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   return r;
 }
 
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
 __device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
@@ -665,24 +671,10 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
           for (int j = 0; j < 4; j++) {
-            const int t = t0 + r + 8 * (j >> 1);
-            if (t > pos[nt][j & 1] || t < kv4_from(pos[nt][j & 1], a.window)) x[nt][j] = -kInf;
+            // (the difference may wrap for a negative position, which sees nothing anyhow)
+            const int t = t0 + r + 8 * (j >> 1), p = pos[nt][j & 1];
+            if (t > p || (a.window > 0 && t <= (int)((uint32_t)p - (uint32_t)a.window))) x[nt][j] = -kInf;
           }
-      }
-      if constexpr (C::kDeq) {
-        // values that are not finite are kept out of the product, and noted in the rows that see them
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-#pragma unroll
-          for (int g = 0; g < NG; g++)
-            if (kv4_broken(vp[h][g])) {
-              vp[h][g] = 0;
-#pragma unroll
-              for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                for (int e = 0; e < 2; e++)
-                  if (!kMasked || x[nt][2 * h + e] != -kInf) nan_groups |= 1u << ((nt * 2 + e) * NG + g);
-            }
       }
       // ---- running maximum: moves only when a score passes it by kSlack ----
       float y[NT][4], most = -kInf;
@@ -692,13 +684,34 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
         for (int j = 0; j < 4; j++) y[nt][j] = fmaf(fac[nt][j & 1], x[nt][j], -mf[nt][j & 1]);
         most = max3(max3(most, y[nt][0], y[nt][1]), y[nt][2], y[nt][3]);
       }
-      float top = 0.f;  // largest value scale (dequantised: bound of the values) of the unit
+      // largest value scale (dequantised: bound of the values, not a number or infinite if one is not finite) of the unit
+      float top = 0.f;
 #pragma unroll
       for (int h = 0; h < 2; h++)
 #pragma unroll
         for (int g = 0; g < NG; g++)
-          top = fmaxf(top, C::kDeq ? fmaf(8.f, lo_bf16(vp[h][g]), fabsf(hi_bf16(vp[h][g]))) : lo_bf16(vp[h][g]));
-      if (__any_sync(0xffffffffu, most > kSlack || top * vmul >= C::kTop)) {
+          top = C::kDeq ? max_nan(top, fmaf(8.f, lo_bf16(vp[h][g]), fabsf(hi_bf16(vp[h][g])))) : fmaxf(top, lo_bf16(vp[h][g]));
+      if (__any_sync(0xffffffffu, most > kSlack || !(top * vmul < C::kTop))) {
+        if (C::kDeq && !(top < kInf)) {
+          // what is not finite stays out of the factor and the product, and is noted in the rows that see it
+          top = 0.f;
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            uint32_t bad = 0;
+#pragma unroll
+            for (int g = 0; g < NG; g++) {
+              if (kv4_broken(vp[h][g]))
+                bad |= 1u << g;
+              else
+                top = fmaxf(top, fmaf(8.f, lo_bf16(vp[h][g]), fabsf(hi_bf16(vp[h][g]))));
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+              for (int e = 0; e < 2; e++)
+                if (!kMasked || x[nt][2 * h + e] != -kInf) nan_groups |= bad << ((nt * 2 + e) * NG);
+          }
+        }
         const float seen = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
         float shrink = 1.f;
         if (seen * vmul >= C::kTop) {
@@ -900,9 +913,9 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<HD, NG, NT, F32>::kCtas) kv4
     }
 
     // ---- join the four warps ----
-    // exact: powers of two, one after the other (their product may not be a number)
-    constexpr float kUnscale = C::kDeq ? 1.f / kTopScale : C::kRawV ? 1048576.f : 1.f;
-    const float vinv = 1.f / vmul;
+    // exact: powers of two, one after the other for values as codes (their product may not be a number)
+    constexpr float kUnscale = C::kRawV ? 1048576.f : 1.f;
+    const float vinv = (C::kDeq ? 1.f / kTopScale : 1.f) / vmul;
     if constexpr (C::kDeq)
       for (int s = 4; s < 32; s <<= 1) nan_groups |= __shfl_xor_sync(0xffffffffu, nan_groups, s);
 #pragma unroll
