@@ -30,7 +30,8 @@
  *  - Test hook: if the environment variable COLI_FAIL_AFTER=N is set when a context is created,
  *    every compute call after the first N successful ones returns COLI_E_INJECTED without
  *    launching anything ([fixes] 3). Uploads, frees, table updates and queries are never gated.
- *  - A context is used by one host thread at a time.
+ *  - A context is used by one host thread at a time. Its calls share scratch memory: where they go to
+ *    several streams, the streams are ordered.
  */
 #ifndef COLI_MOE_H
 #define COLI_MOE_H
@@ -421,17 +422,21 @@ COLI_API int coli_kv4_read(coli_ctx *ctx, const coli_kv4_cache *cache, void *k, 
  * (t > p - window), of key/value head h / (q_heads / heads). A row that sees nothing gives zeros.
  * q, out: [T x q_heads x head_dim] in dtype, rows q_stride / out_stride elements apart; q_heads a
  * multiple of heads, at most COLI_MAX_KV_GROUP times it; scale finite; out must not overlap q.
- * Scores, the softmax's maximum and sum, and the output are held in binary32 (bf16 queries: weights
- * and, for many rows, keys and values in 11 bits; f32: queries and weights in 22; what weighs less than
- * 2^-29 of a row's heaviest value may count as nothing). Results do not change from run to run. A non-finite
- * query sets COLI_E_NONFINITE and gives NaN in its row. What is stored and not finite touches no row that does not see
- * it: in a row that does, a value gives NaN (or an infinity) in the channels of its group, a key in the whole row.
+ * Scores, the softmax's maximum and sum, and the output are held in binary32 (bf16 queries: weights and, from 9
+ * rows on, values in 11 bits, in the tensor-core form keys too, and the matrix instructions keep 18 bits or more of a
+ * sum of products; f32: queries and weights in 22; what weighs less than 2^-29 of a row's heaviest value may count as
+ * nothing). Sums of weights times values have to fit binary32: with values above about 1e30 they may not. Results do
+ * not change from run to run. A non-finite query sets COLI_E_NONFINITE and gives NaN in its row. What is stored and not
+ * finite touches no row that does not see it: in a row that does, a value gives NaN (or an infinity) in the channels of
+ * its group, a key in the whole row.
  * Kernel forms, chosen on the host: up to 16 query rows per sequence and key/value head on average, f32, or
  * heads of 256 channels: a streaming form that reads the cache once per 16 rows; otherwise 256-row tiles on the
- * tensor cores. Each splits long sequences over the device. A context's first call allocates the memory for the
- * parts, unless coli_reserve has: run one, of any shape, before any stream capture. That memory never moves, so
- * captured calls stay valid whatever is called later. A wait inside a kernel is bounded (2 s), after which the call
- * sets COLI_E_TIMEOUT and its output is void. Profiled as COLI_KERNEL_ATTENTION.
+ * tensor cores. The average is over the call: a prompt's chunk among decoding sequences takes them all to the
+ * tiles, so give prompts and decoding sequences calls of their own. Each form splits long sequences over the device.
+ * A context's first call allocates the memory for the parts, unless coli_reserve has: run one, of any shape, before
+ * any stream capture. That memory never moves, so captured calls stay valid whatever is called later. A wait inside a
+ * kernel is bounded (2 s), after which the call sets COLI_E_TIMEOUT and its output is void. Profiled as
+ * COLI_KERNEL_ATTENTION.
  */
 COLI_API int coli_kv4_attention(coli_ctx *ctx, const coli_kv4_cache *cache, const void *q, long long q_stride,
                                 int dtype, int q_heads, int T, const int32_t *q_start, const int32_t *lens, int B,

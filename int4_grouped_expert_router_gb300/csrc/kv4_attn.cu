@@ -4,9 +4,11 @@
 namespace coli {
 
 // Query rows per sequence and key/value head, on average, from which the tensor-core tiles of kv4_tile.cu take over: up
-// to 16 rows one pass of kv4_attn.h serves them all; from 17 on it reads and unpacks the cache again for every 16 (eight
-// requests of up to 20011 tokens with 30 rows each: 112 us there, 86 us with tiles; 8192 rows over 10007 tokens: 4.9 ms
-// and 0.46 ms). Tiles are made for bf16 and heads of at most 128 channels (tensor memory holds two 128-row outputs).
+// to 16 rows one pass of kv4_attn.h serves them all; from 17 on it reads and unpacks the cache again for every 16. Eight
+// requests with 30 rows each: up to 300 tokens 20 us there and 21 us with tiles, 1000 tokens 27 and 27, 3000 tokens 40 and
+// 38, 20011 tokens 113 and 87; 8192 rows over 10007 tokens 4.9 ms and 0.46 ms. The average hides a mix: a prompt chunk of
+// 512 rows among 64 decoding requests of 4000 tokens takes the tiles for all of them, 357 us where the two kinds called
+// apart take 81 and 79. Tiles are made for bf16 and heads of at most 128 channels (tensor memory holds two 128-row outputs).
 constexpr int kTileFrom = 17;
 
 int launch_attn_bf16(coli_ctx* ctx, AttnArgs& a) { return launch_shape<false>(ctx, a); }

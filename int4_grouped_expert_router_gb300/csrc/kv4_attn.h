@@ -10,7 +10,7 @@
 // of two 16-bit values.
 //
 // What bounds it: the cache's bytes, read once (a key/value head's codes serve all of its query heads), and beside
-// them the instructions that unpack codes and weigh tokens, about 330 per 16 tokens of a head (hd = 128, one group):
+// them the instructions that unpack codes and weigh tokens, about 340 per 16 tokens of a head (hd = 128, one group):
 // with every copy left out the kernel takes as long, with the arithmetic left out 0.6 of its time.
 //
 // Work split. An item is (sequence, key/value head, tile of 8 NT query rows); its tokens are cut into stages of 64,
@@ -32,7 +32,7 @@
 // transposed in registers (movmatrix), O^T += V^T a (rows = 16 channels).
 //
 // Measured (bf16, hd 128, a copy's rate being 6782 GB/s): 64 requests of up to 8192 tokens, 8 heads of 8, gs 64:
-// 83 us, 3.7 TB/s; 131071 tokens of one request, gs 128: 42 us, 3.4 TB/s; a request of 1003 tokens: 10 us, of which
+// 84 us, 3.6 TB/s; 131071 tokens of one request, gs 128: 44 us, 3.3 TB/s; a request of 1003 tokens: 10 us, of which
 // the launch, the dealing out, the queries and the joining of 16 parts are all but one.
 #pragma once
 

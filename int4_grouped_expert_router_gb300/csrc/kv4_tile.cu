@@ -24,11 +24,11 @@
 // K's channels lie in the order 0 4 1 5 2 6 3 7 within every eight, as the codes unpack, and Q's with them; V^T's rows,
 // the output's columns, in the order 0 2 .. 14 1 3 .. 15 within every sixteen, which the store undoes.
 //
-// Measured: 2 x 2048 tokens over 10007, 32 heads on 8, hd 128, gs 64: 457 us, 975 TFLOP/s (0.51 of a cuBLAS bf16
+// Measured: 2 x 2048 tokens over 10007, 32 heads on 8, hd 128, gs 64: 459 us, 971 TFLOP/s (0.51 of a cuBLAS bf16
 // product's rate). The converters set the pace: a stage takes them 1.8 to 1.9 us, with one softmax warp at work as with
 // eight, half of it the dequantising, the rest the agreement on factors, waits and stores. A lane makes the scale and
 // offset of one token ready for its warp (470 us; every lane for all tokens that it touches: 487 us). Eight requests of
-// up to 20011 tokens with 30 rows a head: 86 us, of which 25 us do not depend on the lengths (start, queries, joining).
+// up to 20011 tokens with 30 rows a head: 87 us, of which 25 us do not depend on the lengths (start, queries, joining).
 // What it cost to find: loops unrolled beyond the instruction cache took 1068 us, matrix instructions issued with
 // operands in plain registers (110 cycles each instead of 45) 589 us; a thread fetching its own row of queries cost 6 us.
 // Measured and dropped, against 482 us then: the row's scores all in registers (672 us), two threads per row (591 us),

@@ -2,7 +2,8 @@
 
     python -m int4_grouped_expert_router_gb300.run_decoder [--workload tiny] [--batch B] [--prompt N] [--steps N]
 
-The whole layer on the device, with nothing but library calls between the residual stream going in and coming out:
+The layer on the device, with nothing but library calls between the residual stream going in and coming out. It has no
+positions: the library has no rotary step, which a model's q and k get between the projection and the append.
 
     n      = rmsnorm(h, w_in)                                    coli_norm_residual (no block)
     q,k,v  = Wqkv n                                              coli_w4_linear
@@ -13,8 +14,8 @@ The whole layer on the device, with nothing but library calls between the residu
     y      = routed int4 experts of n                            coli_router_select, coli_expert_group
     h, n   = h + rmsnorm(y, w_post2), rmsnorm(h, w_next)         coli_norm_residual
 
-(positions: a rotary step on q and k would go between the projection and the append). Prints the mean event-timed
-microseconds of the prompt pass and of a decode step, after the device error word has come back clean.
+Prints the event-timed microseconds of the prompt pass and of a decode step (the median), after the device error word has
+come back clean.
 """
 from __future__ import annotations
 
