@@ -74,6 +74,11 @@ extern "C" {
 #define COLI_MAX_KV_SEQS 65536      /* B (sequences) of the cache calls */
 #define COLI_MAX_KV_HEADS 256       /* key/value heads of a cache */
 #define COLI_MAX_KV_GROUP 64        /* query heads per key/value head */
+#define COLI_MAX_DENSE_ROWS 1048576 /* O of coli_dense_upload (I: COLI_MAX_DIM) */
+#define COLI_MAX_VOCAB 16777216     /* V of coli_logprobs */
+#define COLI_MAX_TOP 32             /* alternatives per row of coli_logprobs */
+#define COLI_MAX_ROTARY_DIM 1024    /* head_dim of coli_rotary */
+#define COLI_MAX_ROTARY_HEADS 16384 /* q_heads, k_heads of coli_rotary */
 
 typedef struct coli_ctx coli_ctx;
 
@@ -107,8 +112,8 @@ COLI_API int coli_reserve(coli_ctx *ctx, int max_S, int max_E, int max_K, int ma
 
 /* Per-kernel timing: when on, every kernel launch of this context is bracketed by two CUDA events
  * recorded on the context's stream (off by default). Kinds: COLI_KERNEL_ROUTER, _GATEUP, _DOWN,
- * _COMBINE, _LINEAR, _CACHE, _ATTENTION, _NORM. coli_profile_read synchronises the stream and returns, for one kind, the summed event
- * time in milliseconds and the number of launches since the previous read of that kind. */
+ * _COMBINE, _LINEAR, _CACHE, _ATTENTION, _NORM, _ROTARY, _LOGPROBS. coli_profile_read synchronises the stream and returns, for one
+ * kind, the summed event time in milliseconds and the number of launches since the previous read of that kind. */
 #define COLI_KERNEL_ROUTER 0
 #define COLI_KERNEL_GATEUP 1
 #define COLI_KERNEL_DOWN 2
@@ -117,6 +122,8 @@ COLI_API int coli_reserve(coli_ctx *ctx, int max_S, int max_E, int max_K, int ma
 #define COLI_KERNEL_CACHE 5
 #define COLI_KERNEL_ATTENTION 6
 #define COLI_KERNEL_NORM 7
+#define COLI_KERNEL_ROTARY 8
+#define COLI_KERNEL_LOGPROBS 9
 COLI_API int coli_profile_enable(coli_ctx *ctx, int on);
 COLI_API int coli_profile_read(coli_ctx *ctx, int kind, double *total_ms, long long *launches);
 
@@ -460,6 +467,107 @@ COLI_API int coli_kv4_attention(coli_ctx *ctx, const coli_kv4_cache *cache, cons
 COLI_API int coli_norm_residual(coli_ctx *ctx, const void *block, const void *resid, const void *gate, int gate_rows,
                                 int gate_sigmoid, float alpha, const float *w_post, const float *w_pre, float eps,
                                 int dtype, int S, int D, void *h_out, void *x_out);
+
+/*
+ * Rotary positions: the pairs of channels of q and k turned by an angle that grows with the row's position p,
+ *   (a, b) -> scale * (a cos(p f_i) - b sin(p f_i),  b cos(p f_i) + a sin(p f_i)),   pair i of rot_dim / 2,
+ * pair i being the channels (i, i + rot_dim / 2) of a head, or (2 i, 2 i + 1) if interleaved. Channels from rot_dim on are
+ * copied as they are. Goes between a projection and coli_kv4_append.
+ *
+ * The frequencies are a table freqs [rot_dim / 2] in turns per position, as 64-bit fractions of a turn (f_i / 2 pi * 2^64,
+ * modulo 2^64): the turn that a position makes is a whole-number product, exact at any position.
+ *
+ * coli_rotary_freqs: host only. Writes the table for f_i = base^(-2 i / rot_dim) and one of these scalings for long contexts:
+ *   COLI_ROTARY_PLAIN   f_i
+ *   COLI_ROTARY_LINEAR  f_i / factor
+ *   COLI_ROTARY_BASE    f_i of the base  base * factor^(rot_dim / (rot_dim - 2))   (rot_dim 2: f_0 = 1)
+ *   COLI_ROTARY_PARTS   f_i (g + (1 - g) / factor),  g = (r_i - low) / (high - low) within 0..1,  r_i = original_len f_i / (2 pi)
+ *                       the turns that the pair makes over the original length: fast pairs stay, slow ones are stretched
+ * COLI_E_INVAL for rot_dim odd or outside 2..COLI_MAX_ROTARY_DIM, base <= 1, factor < 1 (not looked at for PLAIN; low, high,
+ * original_len for PARTS alone: 0 <= low < high, original_len > 0), an unknown scaling, or values that are not finite.
+ */
+#define COLI_ROTARY_PLAIN 0
+#define COLI_ROTARY_LINEAR 1
+#define COLI_ROTARY_BASE 2
+#define COLI_ROTARY_PARTS 3
+COLI_API int coli_rotary_freqs(int rot_dim, double base, int scaling, double factor, double original_len, double low,
+                               double high, uint64_t *freqs);
+
+/*
+ * q, q_out: [T x q_heads x head_dim], k, k_out: [T x k_heads x head_dim] in dtype; the channels and heads of a row contiguous,
+ * rows a stride apart (elements; slices of a fused projection's output serve as they are). Either of q and k may be NULL, with
+ * its output and 0 heads. An output may be its input (same address and stride): in place; no other overlap. freqs: device.
+ * Where a row is:
+ *   positions [T] (device int32): any value, negative ones too, which turn backwards -- so the call with all positions negated
+ *     undoes a turn of scale 1, and is the gradient of the call. q_start and lens are then NULL and B 0;
+ *   positions NULL: the plan of the cache calls. Row i of the m rows of sequence b is at lens[b] - m + i. Rows outside every
+ *     sequence's range are left alone, rows with a negative position are copied as they are. A length below 0 or a row range
+ *     outside 0..T sets COLI_E_RANGE.
+ * The turn is found in 32 bits of a turn, its sine and cosine in binary32, and the result is rounded to dtype once.
+ * 2 <= rot_dim <= head_dim, rot_dim even, scale finite. 1 <= T <= COLI_MAX_KV_ROWS. Profiled as COLI_KERNEL_ROTARY.
+ */
+COLI_API int coli_rotary(coli_ctx *ctx, const void *q, long long q_stride, void *q_out, long long q_out_stride, int q_heads,
+                         const void *k, long long k_stride, void *k_out, long long k_out_stride, int k_heads, int dtype,
+                         int head_dim, int rot_dim, int interleaved, const uint64_t *freqs, float scale, int T,
+                         const int32_t *positions, const int32_t *q_start, const int32_t *lens, int B);
+
+/*
+ * Products with weights that are not quantised (an output head, projections kept in 16 bits, dense blocks):
+ *   y[t, o] = resid[t, o] + act(sum_i W[o, i] x[t, i] + bias[o]) * mul[t, o]
+ * each of bias, act, mul and resid optional.
+ *
+ * coli_dense_upload: W [O x I] row-major bfloat16, host or device memory (16-bit aligned); the library keeps a copy of its own
+ * in its own layout. Returns a handle, 0 on failure (reason in coli_last_error). The handles are a kind of their own: other
+ * calls do not take them. O <= COLI_MAX_DENSE_ROWS, I <= COLI_MAX_DIM, any value from 1 on. Neither this call nor
+ * coli_dense_free may be made while the stream is being captured; coli_dense_free waits for the stream.
+ */
+COLI_API uint64_t coli_dense_upload(coli_ctx *ctx, const uint16_t *W, int O, int I);
+COLI_API int coli_dense_shape(coli_ctx *ctx, uint64_t handle, int *O, int *I);
+COLI_API int coli_dense_free(coli_ctx *ctx, uint64_t handle);
+
+/*
+ * x [S x I] in x_dtype; y, mul, resid [S x O] in y_dtype (any pairing of the two); rows a stride apart (elements). bias [O] f32.
+ * bias, mul, resid: NULL for none. act:
+ *   COLI_ACT_NONE       z
+ *   COLI_ACT_SILU       z / (1 + exp(-z))
+ *   COLI_ACT_GELU       z/2 (1 + erf(z / sqrt 2))
+ *   COLI_ACT_GELU_TANH  z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))
+ *   COLI_ACT_RELU       max(z, 0)
+ *   COLI_ACT_RELU2      max(z, 0)^2
+ * y may be mul or resid (same address and stride); no other overlap of y with an input. 1 <= S <= COLI_MAX_TOKENS.
+ * Products of bfloat16 values are exact, binary32 activations enter as three bfloat16 parts that add up to them, and sums are
+ * held in binary32; y is rounded once. Results do not change from run to run. A product that is not finite sets
+ * COLI_E_NONFINITE, and spoils its row of x (its row of W) alone. Binary32 activations, and rows of x that do not start at
+ * 16-byte boundaries, are first laid out in the workspace (coli_reserve). Profiled as COLI_KERNEL_LINEAR.
+ */
+#define COLI_ACT_NONE 0
+#define COLI_ACT_SILU 1
+#define COLI_ACT_GELU 2
+#define COLI_ACT_GELU_TANH 3
+#define COLI_ACT_RELU 4
+#define COLI_ACT_RELU2 5
+COLI_API int coli_dense_linear(coli_ctx *ctx, uint64_t W, const void *x, long long x_stride, int x_dtype, int S,
+                               const float *bias, int act, const void *mul, long long mul_stride, const void *resid,
+                               long long resid_stride, void *y, long long y_stride, int y_dtype);
+
+/*
+ * Log probabilities: for each of S rows of logits x [S x V] (rows `stride` elements apart, dtype f32 or bf16),
+ *   z = scale x,  log p_v = z_v - log(sum_u exp(z_u)).
+ * Outputs, each NULL if not wanted (one at least is):
+ *   logp [S x n] f32: log p of the given tokens [S x n] (int32); a negative token stands for none and gives 0, one >= V sets
+ *     COLI_E_RANGE and gives NaN. tokens and logp come together, 1 <= n <= V of any size.
+ *   entropy [S] f32: -sum p log p.
+ *   top_id, top_logp [S x k]: the k entries with the largest logits in descending order and their log p, equal ones by index;
+ *     k <= COLI_MAX_TOP, both or neither. Entries of -infinity (forbidden tokens) are no alternatives: slots that are left over
+ *     have id -1 and log p -infinity.
+ * Entries of -infinity have probability 0. A row that has nothing else gives log p = -infinity and entropy 0. A NaN or
+ * +infinity sets COLI_E_NONFINITE; its row is NaN, its ids -1. Sums and logarithms are held in binary32, relative to the largest
+ * entry. scale > 0 (the inverse temperature), at most 1e30. 1 <= S <= COLI_MAX_TOKENS, V <= COLI_MAX_VOCAB, n <= COLI_MAX_VOCAB.
+ * Results do not change from run to run. Profiled as COLI_KERNEL_LOGPROBS.
+ */
+COLI_API int coli_logprobs(coli_ctx *ctx, const void *logits, long long stride, int dtype, int S, int V, float scale,
+                           const int32_t *tokens, int n, float *logp, float *entropy, int k, int32_t *top_id,
+                           float *top_logp);
 
 #ifdef __cplusplus
 }

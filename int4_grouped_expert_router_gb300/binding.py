@@ -44,10 +44,14 @@ COLI_DTYPE_BF16 = _C["COLI_DTYPE_BF16"]
 COLI_MAX_EXPERTS = _C["COLI_MAX_EXPERTS"]
 COLI_MAX_K = _C["COLI_MAX_K"]
 COLI_MAX_ISSUES = _C["COLI_MAX_ISSUES"]
+ROTARY_SCALINGS = {name: _C["COLI_ROTARY_" + name.upper()] for name in ("plain", "linear", "base", "parts")}
+ROTARY_SCALINGS["none"] = ROTARY_SCALINGS["plain"]
+ACTIVATIONS = {name: _C["COLI_ACT_" + name.upper()] for name in ("none", "silu", "gelu", "gelu_tanh", "relu", "relu2")}
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_D = ctypes.c_double
 _L = ctypes.c_longlong
 _U64 = ctypes.c_uint64
 
@@ -84,6 +88,13 @@ SIGNATURES = {
     "coli_kv4_read": (_I, [_P, _P, _P, _L, _P, _L, _I, _I, _P, _P, _I, _P, _I]),
     "coli_kv4_attention": (_I, [_P, _P, _P, _L, _I, _I, _I, _P, _P, _I, _P, _I, _F, _I, _P, _L]),
     "coli_norm_residual": (_I, [_P, _P, _P, _P, _I, _I, _F, _P, _P, _F, _I, _I, _I, _P, _P]),
+    "coli_rotary_freqs": (_I, [_I, _D, _I, _D, _D, _D, _D, _P]),
+    "coli_rotary": (_I, [_P, _P, _L, _P, _L, _I, _P, _L, _P, _L, _I, _I, _I, _I, _I, _P, _F, _I, _P, _P, _P, _I]),
+    "coli_dense_upload": (_U64, [_P, _P, _I, _I]),
+    "coli_dense_shape": (_I, [_P, _U64, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]),
+    "coli_dense_free": (_I, [_P, _U64]),
+    "coli_dense_linear": (_I, [_P, _U64, _P, _L, _I, _I, _P, _I, _P, _L, _P, _L, _P, _L, _I]),
+    "coli_logprobs": (_I, [_P, _P, _L, _I, _I, _I, _F, _P, _I, _P, _P, _I, _P, _P]),
     "coli_profile_enable": (_I, [_P, _I]),
     "coli_profile_read": (_I, [_P, _I, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_longlong)]),
 }
@@ -96,6 +107,8 @@ COLI_KERNEL_LINEAR = _C["COLI_KERNEL_LINEAR"]
 COLI_KERNEL_CACHE = _C["COLI_KERNEL_CACHE"]
 COLI_KERNEL_ATTENTION = _C["COLI_KERNEL_ATTENTION"]
 COLI_KERNEL_NORM = _C["COLI_KERNEL_NORM"]
+COLI_KERNEL_ROTARY = _C["COLI_KERNEL_ROTARY"]
+COLI_KERNEL_LOGPROBS = _C["COLI_KERNEL_LOGPROBS"]
 
 
 class ColiError(RuntimeError):
@@ -518,6 +531,130 @@ def coli_norm_residual(ctx, block, resid, gate, alpha, w_post, w_pre, eps, h, x,
     rc = (_lib or library()).coli_norm_residual(ctx, at[0], at[1], at[4], rows, gate_sigmoid, alpha, at[5], at[6], eps,
                                                 act_dtype(first), S, D, at[2], at[3])
     return rc if rc == COLI_OK else _check(ctx, rc, "coli_norm_residual")
+
+
+def coli_rotary_freqs(rot_dim, base=10000.0, scaling="none", factor=1.0, original_len=0, low=1.0, high=32.0, device="cuda"):
+    """The table of a rotary step's frequencies (int64 [rot_dim / 2], 64-bit fractions of a turn); scaling: "none", "linear",
+    "base" or "parts"."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"rotary_freqs: scaling must be one of {sorted(ROTARY_SCALINGS)}")
+    table = torch.empty(max(1, rot_dim // 2), dtype=torch.int64)
+    rc = library().coli_rotary_freqs(rot_dim, base, ROTARY_SCALINGS[scaling], factor, original_len, low, high, _ptr(table))
+    if rc != COLI_OK:
+        raise ColiError(rc, "coli_rotary_freqs: a size or factor out of range")
+    return table.to(device)
+
+
+def coli_rotary(ctx, q, k, freqs, q_out, k_out, lens=None, q_start=None, positions=None, interleaved=False, scale=1.0):
+    """q_out, k_out = q, k [T x heads x head_dim] with the first 2 * freqs.numel() channels of each head turned by the row's
+    position: `positions` [T], or that of the plan lens [B], q_start [B + 1]. q_out may be q, k_out k; q or k may be None."""
+    first = q if q is not None else k
+    if first is None or first.dim() != 3:
+        raise ValueError("rotary: q or k must be given, [T x heads x head_dim]")
+    T, hd, dtype = first.shape[0], first.shape[2], first.dtype
+    at = []
+    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None or out is None:
+            if x is not None or out is not None:
+                raise ValueError(f"rotary: {name} and {name}_out come together")
+            at += [None, 0, None, 0, 0]
+        elif x.dtype != dtype or out.dtype != dtype or x.dim() != 3:
+            raise ValueError("rotary: q, k and their outputs must be [T x heads x head_dim] of one dtype")
+        else:
+            heads = x.shape[1]
+            at += [x.data_ptr(), _rows3(x, T, heads, hd, name), out.data_ptr(), _rows3(out, T, heads, hd, name + "_out"), heads]
+    if freqs.dtype != torch.int64 or not freqs.is_cuda or not freqs.is_contiguous():
+        raise ValueError("rotary: freqs must be a contiguous int64 CUDA tensor (coli_rotary_freqs)")
+    for t, size, name in ((positions, T, "positions"), (lens, None, "lens"), (q_start, None, "q_start")):
+        if t is not None and (t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or size not in (None, t.numel())):
+            raise ValueError(f"rotary: {name} must be a contiguous int32 CUDA tensor" + (f" of {size} entries" if size else ""))
+    B = 0 if lens is None else lens.numel()
+    if q_start is not None and q_start.numel() != B + 1:
+        raise ValueError("rotary: q_start must have B + 1 entries")
+    rc = (_lib or library()).coli_rotary(ctx, *at, act_dtype(first), hd, 2 * freqs.numel(), interleaved, freqs.data_ptr(), scale, T,
+                                         *(None if t is None else t.data_ptr() for t in (positions, q_start, lens)), B)
+    return rc if rc == COLI_OK else _check(ctx, rc, "coli_rotary")
+
+
+def coli_dense_upload(ctx, W):
+    """Upload a weight W [O x I] (bfloat16, host or device); returns the handle (raises on failure)."""
+    if W.dim() != 2 or W.dtype != torch.bfloat16 or not W.is_contiguous():
+        raise ValueError("dense_upload: W must be a contiguous [O x I] bfloat16 tensor")
+    h = library().coli_dense_upload(ctx, _ptr(W), *W.shape)
+    if h == 0:
+        raise ColiError(library().coli_last_code(ctx), f"coli_dense_upload: {coli_last_error(ctx)}")
+    return h
+
+
+def coli_dense_shape(ctx, handle):
+    """(O, I) of an uploaded weight."""
+    O, I = ctypes.c_int(), ctypes.c_int()
+    _check(ctx, library().coli_dense_shape(ctx, handle, ctypes.byref(O), ctypes.byref(I)), "coli_dense_shape")
+    return O.value, I.value
+
+
+def coli_dense_free(ctx, handle):
+    return _check(ctx, library().coli_dense_free(ctx, handle), "coli_dense_free")
+
+
+def _rows2(t, shape, name):
+    """The row stride of a CUDA tensor [S x n] whose rows may be apart."""
+    if not t.is_cuda or t.shape != shape:
+        raise ValueError(f"{name} must be a CUDA tensor {list(shape)}")
+    row, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return shape[1] if shape[0] == 1 else row
+
+
+def coli_dense_linear(ctx, W, x, y, bias=None, act="none", mul=None, resid=None):
+    """y = resid + act(W x + bias) * mul for every row of x ([S x I] -> [S x O]); W a coli_dense_upload handle, mul and resid
+    [S x O] in y's dtype, bias [O] float32, act one of ACTIVATIONS. y may be mul or resid."""
+    if act not in ACTIVATIONS:
+        raise ValueError(f"dense_linear: act must be one of {sorted(ACTIVATIONS)}")
+    O, I = coli_dense_shape(ctx, W)
+    if x.dim() != 2:
+        raise ValueError("dense_linear: x must be [S x I]")
+    S = x.shape[0]
+    xs, out = _rows2(x, (S, I), "x"), torch.Size((S, O))
+    at = []
+    for t, name in ((mul, "mul"), (resid, "resid"), (y, "y")):
+        if t is None:
+            at += [None, 0]
+        elif t.dtype != y.dtype:
+            raise ValueError("dense_linear: mul, resid and y must have one dtype")
+        else:
+            at += [t.data_ptr(), _rows2(t, out, name)]
+    if bias is not None and (bias.dtype != torch.float32 or not bias.is_cuda or not bias.is_contiguous() or bias.numel() != O):
+        raise ValueError("dense_linear: bias must be a contiguous float32 CUDA tensor [O]")
+    rc = (_lib or library()).coli_dense_linear(ctx, W, x.data_ptr(), xs, act_dtype(x), S, None if bias is None else bias.data_ptr(),
+                                               ACTIVATIONS[act], *at, act_dtype(y))
+    return rc if rc == COLI_OK else _check(ctx, rc, "coli_dense_linear")
+
+
+def coli_logprobs(ctx, logits, scale=1.0, tokens=None, logp=None, entropy=None, top_id=None, top_logp=None):
+    """Log probabilities of scale * logits [S x V]: logp of tokens (both [S x n] or [S]), entropy [S], the largest entries top_id
+    (int32) and top_logp [S x k]. Outputs are float32 CUDA tensors; those left out are not computed."""
+    if logits.dim() != 2:
+        raise ValueError("logprobs: logits must be [S x V]")
+    S, V = logits.shape
+    stride = _rows2(logits, logits.shape, "logits")
+    at = []
+    for t, dt, name in ((tokens, torch.int32, "tokens"), (logp, torch.float32, "logp"), (entropy, torch.float32, "entropy"),
+                        (top_id, torch.int32, "top_id"), (top_logp, torch.float32, "top_logp")):
+        if t is None:
+            at.append(None)
+        elif t.dtype != dt or not t.is_cuda or not t.is_contiguous() or t.shape[0] != S or (t is entropy and t.numel() != S):
+            raise ValueError(f"logprobs: {name} must be a contiguous {dt} CUDA tensor with a row for each of logits")
+        else:
+            at.append(t.data_ptr())
+    n = 0 if tokens is None else tokens.numel() // max(1, S)
+    k = 0 if top_id is None else top_id.numel() // max(1, S)
+    if (logp is not None and logp.numel() != n * S) or (top_logp is not None and top_logp.numel() != k * S):
+        raise ValueError("logprobs: logp must have the shape of tokens, top_logp that of top_id")
+    rc = (_lib or library()).coli_logprobs(ctx, logits.data_ptr(), stride, act_dtype(logits), S, V, scale, at[0], n, at[1], at[2], k,
+                                           at[3], at[4])
+    return rc if rc == COLI_OK else _check(ctx, rc, "coli_logprobs")
 
 
 def coli_profile_enable(ctx, on):

@@ -8,9 +8,12 @@
 
 #include "coli_internal.h"
 #include "ans.h"
+#include "dense.h"
 #include "ep.h"
 #include "kv4.h"
+#include "logprobs.h"
 #include "norm.h"
+#include "rotary.h"
 
 namespace coli {
 
@@ -290,6 +293,8 @@ int coli_init(coli_ctx** out, int device, void* cuda_stream) {
   if ((e = cudaMalloc(&p, kKvCounters * sizeof(int))) != cudaSuccess) goto fail;
   ctx->d_kv_count = static_cast<int*>(p);
   if ((e = cudaMemset(ctx->d_kv_count, 0, kKvCounters * sizeof(int))) != cudaSuccess) goto fail;
+  if ((e = cudaMalloc(&ctx->d_logprob, logprob_bytes(ctx->num_sms))) != cudaSuccess) goto fail;
+  if ((e = cudaMemset(ctx->d_logprob, 0, logprob_bytes(ctx->num_sms))) != cudaSuccess) goto fail;
   if ((e = cudaMalloc(&ctx->d_router, kRouterScratchBytes)) != cudaSuccess) goto fail;
   if ((e = cudaMemset(ctx->d_router, 0, kRouterScratchBytes)) != cudaSuccess) goto fail;
   {
@@ -318,7 +323,10 @@ void coli_destroy(coli_ctx* ctx) {
     if (t.panel) cudaFree(t.panel);
     if (t.sT) cudaFree(t.sT);
   }
+  for (auto& t : ctx->dense)
+    if (t.w) cudaFree(t.w);
   if (ctx->d_solo_route) cudaFree(ctx->d_solo_route);
+  if (ctx->d_logprob) cudaFree(ctx->d_logprob);
   ans_release_all(ctx);
   if (ctx->d_table) cudaFree(ctx->d_table);
   if (ctx->d_status) cudaFree(ctx->d_status);
@@ -361,9 +369,9 @@ int coli_check_error(coli_ctx* ctx) {
     e = cudaMemset(ctx->d_status, 0, code == COLI_E_TIMEOUT ? kStatusBytes : sizeof(int));
     if (e != cudaSuccess) return cuda_fail(ctx, e, "coli_check_error: clear error word");
     ctx->last_error = code == COLI_E_ROUTE ? "device: expert index out of range or unset table entry"
-                      : code == COLI_E_NONFINITE ? "device: non-finite activation, router score or cache entry"
+                      : code == COLI_E_NONFINITE ? "device: non-finite activation, router score, logit or cache entry"
                       : code == COLI_E_TIMEOUT   ? "device: a bounded wait inside a kernel gave up"
-                      : code == COLI_E_RANGE     ? "device: a cache length, page index or row range outside its array"
+                      : code == COLI_E_RANGE     ? "device: a length, page index, token or row range outside its array"
                                                  : "device error";
   }
   return code;
@@ -376,7 +384,7 @@ int coli_profile_enable(coli_ctx* ctx, int on) {
 }
 
 int coli_profile_read(coli_ctx* ctx, int kind, double* total_ms, long long* launches) {
-  if (!ctx || kind < 0 || kind > COLI_KERNEL_NORM || !total_ms || !launches) return COLI_E_INVAL;
+  if (!ctx || kind < 0 || kind > COLI_KERNEL_LOGPROBS || !total_ms || !launches) return COLI_E_INVAL;
   cudaSetDevice(ctx->device);
   cudaError_t e = cudaStreamSynchronize(ctx->stream);
   if (e != cudaSuccess) return cuda_fail(ctx, e, "coli_profile_read: stream sync");
@@ -870,14 +878,14 @@ static int kv4_check(coli_ctx* ctx, const char* who, const coli_kv4_cache* cache
   return COLI_OK;
 }
 
-// Whether T rows of `row` bytes from a on, sa bytes apart, share a byte with T such rows from b on, sb apart (strides of at
-// least a row).
-static bool rows_overlap(uintptr_t a, long long sa, uintptr_t b, long long sb, long long row, int T) {
+// Whether T rows of row_a bytes from a on, sa bytes apart, share a byte with T rows of row_b bytes from b on, sb apart (strides
+// of at least a row).
+static bool rows_overlap(uintptr_t a, long long sa, long long row_a, uintptr_t b, long long sb, long long row_b, int T) {
   const long long d = (long long)(b - a);  // row j of b lies d + j sb - i sa after row i of a
-  if (d >= (T - 1) * sa + row || -d >= (T - 1) * sb + row) return false;
+  if (d >= (T - 1) * sa + row_a || -d >= (T - 1) * sb + row_b) return false;
   auto meet = [&](long long i, long long j) {
     const long long off = d + j * sb - i * sa;
-    return i >= 0 && i < T && j >= 0 && j < T && off < row && -off < row;
+    return i >= 0 && i < T && j >= 0 && j < T && off < row_a && -off < row_b;
   };
   if (sa == sb) {  // slices of one array: only i - j counts
     const long long k = d / sa;
@@ -950,7 +958,7 @@ int coli_kv4_attention(coli_ctx* ctx, const coli_kv4_cache* cache, const void* q
   if (q_stride < row || out_stride < row)
     return fail(ctx, COLI_E_INVAL, "kv4_attention: row stride below q_heads * head_dim");
   const long long elem = dtype == COLI_DTYPE_F32 ? 4 : 2;
-  if (rows_overlap((uintptr_t)q, q_stride * elem, (uintptr_t)out, out_stride * elem, row * elem, T))
+  if (rows_overlap((uintptr_t)q, q_stride * elem, row * elem, (uintptr_t)out, out_stride * elem, row * elem, T))
     return fail(ctx, COLI_E_INVAL, "kv4_attention: out overlaps q");
   if (!(scale == scale) || scale - scale != 0.f) return fail(ctx, COLI_E_INVAL, "kv4_attention: scale must be finite");
   if (window < 0) return fail(ctx, COLI_E_INVAL, "kv4_attention: window must not be negative");
@@ -989,6 +997,215 @@ int coli_norm_residual(coli_ctx* ctx, const void* block, const void* resid, cons
   NormArgs a{block, resid, gate, gate && gate_rows > 1, gate_sigmoid != 0, alpha, w_post, w_pre, eps, dtype, S, D, h_out, x_out};
   unsettle_x(ctx);
   int rc = launch_norm_residual(ctx, a);
+  if (rc == COLI_OK) ctx->compute_calls++;
+  return rc;
+}
+
+int coli_rotary_freqs(int rot_dim, double base, int scaling, double factor, double original_len, double low, double high,
+                      uint64_t* freqs) {
+  return rotary_freqs(rot_dim, base, scaling, factor, original_len, low, high, freqs);
+}
+
+int coli_rotary(coli_ctx* ctx, const void* q, long long q_stride, void* q_out, long long q_out_stride, int q_heads,
+                const void* k, long long k_stride, void* k_out, long long k_out_stride, int k_heads, int dtype, int head_dim,
+                int rot_dim, int interleaved, const uint64_t* freqs, float scale, int T, const int32_t* positions,
+                const int32_t* q_start, const int32_t* lens, int B) {
+  if (!ctx) return COLI_E_INVAL;
+  if ((!q && !k) || !freqs) return fail(ctx, COLI_E_INVAL, "rotary: NULL pointer");
+  if (dtype != COLI_DTYPE_F32 && dtype != COLI_DTYPE_BF16) return fail(ctx, COLI_E_INVAL, "rotary: dtype");
+  if (head_dim < 2 || head_dim > COLI_MAX_ROTARY_DIM || rot_dim < 2 || rot_dim > head_dim || rot_dim % 2 != 0)
+    return fail(ctx, COLI_E_INVAL, "rotary: rot_dim must be even, from 2 to head_dim, head_dim at most COLI_MAX_ROTARY_DIM");
+  if (T < 1 || T > COLI_MAX_KV_ROWS) return fail(ctx, COLI_E_INVAL, "rotary: T out of range");
+  if (!(scale == scale) || scale - scale != 0.f) return fail(ctx, COLI_E_INVAL, "rotary: scale must be finite");
+  const uintptr_t elem = dtype == COLI_DTYPE_F32 ? 4 : 2;
+  RotaryArgs a{};
+  a.side[0] = RotarySide{q, q_out, q_stride, q_out_stride, q_heads};
+  a.side[1] = RotarySide{k, k_out, k_stride, k_out_stride, k_heads};
+  for (RotarySide& s : a.side) {
+    if ((s.in != nullptr) != (s.out != nullptr) || (s.in != nullptr) != (s.heads != 0))
+      return fail(ctx, COLI_E_INVAL, "rotary: an input comes with its output and its heads");
+    if (!s.in) continue;
+    if (s.heads < 1 || s.heads > COLI_MAX_ROTARY_HEADS) return fail(ctx, COLI_E_INVAL, "rotary: heads out of range");
+    if (((uintptr_t)s.in | (uintptr_t)s.out) % elem != 0) return fail(ctx, COLI_E_INVAL, "rotary: array not aligned to its dtype");
+    const long long row = (long long)s.heads * head_dim;
+    if (T == 1) s.in_stride = s.out_stride = row;  // of one row it says nothing
+    if (s.in_stride < row || s.out_stride < row) return fail(ctx, COLI_E_INVAL, "rotary: row stride below heads * head_dim");
+  }
+  auto overlap = [&](const RotarySide& out, const RotarySide& other, bool other_in) {
+    if (!out.in || !other.in) return false;
+    const long long e = (long long)elem;
+    return rows_overlap((uintptr_t)out.out, out.out_stride * e, (long long)out.heads * head_dim * e,
+                        (uintptr_t)(other_in ? other.in : other.out), (other_in ? other.in_stride : other.out_stride) * e,
+                        (long long)other.heads * head_dim * e, T);
+  };
+  for (int i = 0; i < 2; i++) {
+    const RotarySide &s = a.side[i], &o = a.side[1 - i];
+    const bool in_place = s.in == s.out && s.in_stride == s.out_stride;
+    if ((!in_place && overlap(s, s, true)) || overlap(s, o, true) || (i == 0 && overlap(s, o, false)))
+      return fail(ctx, COLI_E_INVAL, "rotary: an output overlaps another array");
+  }
+  if (positions) {
+    if (q_start || lens || B != 0) return fail(ctx, COLI_E_INVAL, "rotary: positions or a plan, not both");
+  } else {
+    if (!lens || B < 1 || B > COLI_MAX_KV_SEQS) return fail(ctx, COLI_E_INVAL, "rotary: without positions, lens and 1 to COLI_MAX_KV_SEQS sequences");
+    if (!q_start && T != B) return fail(ctx, COLI_E_INVAL, "rotary: without q_start there is one row per sequence (T == B)");
+  }
+  if (injected(ctx)) return COLI_E_INJECTED;
+  cudaSetDevice(ctx->device);
+  a.hd = head_dim;
+  a.rot = rot_dim;
+  a.freqs = freqs;
+  a.scale = scale;
+  a.T = T;
+  a.positions = positions;
+  a.q_start = q_start;
+  a.lens = lens;
+  a.B = B;
+  unsettle_x(ctx);
+  int rc = launch_rotary(ctx, a, dtype, interleaved != 0);
+  if (rc == COLI_OK) ctx->compute_calls++;
+  return rc;
+}
+
+uint64_t coli_dense_upload(coli_ctx* ctx, const uint16_t* W, int O, int I) {
+  if (!ctx) return 0;
+  if (!W || (uintptr_t)W % 2 != 0 || O < 1 || O > COLI_MAX_DENSE_ROWS || I < 1 || I > COLI_MAX_DIM) {
+    fail(ctx, COLI_E_INVAL, "dense_upload: NULL or unaligned pointer, or shape out of range");
+    return 0;
+  }
+  cudaSetDevice(ctx->device);
+  // through a piece of device memory of whole row blocks, so that host and device sources are read alike
+  const size_t row = (size_t)I * 2;
+  const long long blocks = std::max<long long>(1, (long long)((64u << 20) / (row * kDenseRows)));
+  const int piece = (int)std::min<long long>(blocks * kDenseRows, O);
+  void *pw = nullptr, *tmp = nullptr;
+  cudaError_t e = cudaMalloc(&pw, dense_bytes(O, I));
+  if (e == cudaSuccess) e = cudaMalloc(&tmp, row * piece);
+  for (int at = 0; at < O && e == cudaSuccess; at += piece) {
+    const int rows = std::min(piece, O - at);
+    e = cudaMemcpyAsync(tmp, W + (size_t)at * I, row * rows, cudaMemcpyDefault, ctx->stream);
+    if (e == cudaSuccess) e = launch_dense_pack(ctx->stream, static_cast<uint16_t*>(tmp), rows, at, O, I, static_cast<uint8_t*>(pw));
+  }
+  const cudaError_t sync = cudaStreamSynchronize(ctx->stream);
+  if (e == cudaSuccess) e = sync;
+  if (tmp) cudaFree(tmp);
+  if (e != cudaSuccess) {
+    if (pw) cudaFree(pw);
+    cuda_fail(ctx, e, "dense_upload");
+    return 0;
+  }
+  DenseTensor t;
+  t.w = static_cast<uint8_t*>(pw);
+  t.O = O;
+  t.I = I;
+  ctx->dense.push_back(t);
+  return (uint64_t)ctx->dense.size();
+}
+
+static DenseTensor* dense_tensor(coli_ctx* ctx, uint64_t h) {
+  return h >= 1 && h <= ctx->dense.size() && ctx->dense[h - 1].w ? &ctx->dense[h - 1] : nullptr;
+}
+
+int coli_dense_shape(coli_ctx* ctx, uint64_t handle, int* O, int* I) {
+  if (!ctx) return COLI_E_INVAL;
+  const DenseTensor* t = dense_tensor(ctx, handle);
+  if (!t) return fail(ctx, COLI_E_INVAL, "dense_shape: unknown handle");
+  if (O) *O = t->O;
+  if (I) *I = t->I;
+  return COLI_OK;
+}
+
+int coli_dense_free(coli_ctx* ctx, uint64_t handle) {
+  if (!ctx) return COLI_E_INVAL;
+  DenseTensor* t = dense_tensor(ctx, handle);
+  if (!t) return fail(ctx, COLI_E_INVAL, "dense_free: unknown handle");
+  cudaSetDevice(ctx->device);
+  cudaError_t e = cudaStreamSynchronize(ctx->stream);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "dense_free: stream sync");
+  cudaFree(t->w);
+  *t = DenseTensor{};
+  return COLI_OK;
+}
+
+int coli_dense_linear(coli_ctx* ctx, uint64_t W, const void* x, long long x_stride, int x_dtype, int S, const float* bias,
+                      int act, const void* mul, long long mul_stride, const void* resid, long long resid_stride, void* y,
+                      long long y_stride, int y_dtype) {
+  if (!ctx) return COLI_E_INVAL;
+  if (!x || !y) return fail(ctx, COLI_E_INVAL, "dense_linear: NULL pointer");
+  const DenseTensor* t = dense_tensor(ctx, W);
+  if (!t) return fail(ctx, COLI_E_INVAL, "dense_linear: unknown handle");
+  for (int dtype : {x_dtype, y_dtype})
+    if (dtype != COLI_DTYPE_F32 && dtype != COLI_DTYPE_BF16) return fail(ctx, COLI_E_INVAL, "dense_linear: dtype");
+  if (S < 1 || S > COLI_MAX_TOKENS) return fail(ctx, COLI_E_INVAL, "dense_linear: S out of range");
+  if (act < COLI_ACT_NONE || act > COLI_ACT_RELU2) return fail(ctx, COLI_E_INVAL, "dense_linear: unknown activation");
+  const long long ex = x_dtype == COLI_DTYPE_F32 ? 4 : 2, ey = y_dtype == COLI_DTYPE_F32 ? 4 : 2;
+  if (S == 1) x_stride = t->I, mul_stride = resid_stride = y_stride = t->O;  // of one row they say nothing
+  if (x_stride < t->I || y_stride < t->O || (mul && mul_stride < t->O) || (resid && resid_stride < t->O))
+    return fail(ctx, COLI_E_INVAL, "dense_linear: row stride below the row");
+  if ((uintptr_t)x % ex != 0 || ((uintptr_t)y | (uintptr_t)mul | (uintptr_t)resid) % ey != 0 || (uintptr_t)bias % 4 != 0)
+    return fail(ctx, COLI_E_INVAL, "dense_linear: array not aligned to its dtype");
+  auto overlaps = [&](const void* p, long long stride, long long row) {
+    return p && rows_overlap((uintptr_t)p, stride, row, (uintptr_t)y, y_stride * ey, t->O * ey, S);
+  };
+  if (overlaps(x, x_stride * ex, t->I * ex) || (!(mul == y && mul_stride == y_stride) && overlaps(mul, mul_stride * ey, t->O * ey)) ||
+      (!(resid == y && resid_stride == y_stride) && overlaps(resid, resid_stride * ey, t->O * ey)))
+    return fail(ctx, COLI_E_INVAL, "dense_linear: y overlaps an input");
+  if (injected(ctx)) return COLI_E_INJECTED;
+  cudaSetDevice(ctx->device);
+  DenseArgs a{};
+  a.w = t->w;
+  a.O = t->O;
+  a.I = t->I;
+  a.x = x;
+  a.x_stride = x_stride;
+  a.S = S;
+  a.bias = bias;
+  a.act = act;
+  a.mul = mul;
+  a.resid = resid;
+  a.y = y;
+  a.mul_stride = mul_stride;
+  a.resid_stride = resid_stride;
+  a.y_stride = y_stride;
+  unsettle_x(ctx);
+  int rc = launch_dense(ctx, a, x_dtype, y_dtype);
+  if (rc == COLI_OK) ctx->compute_calls++;
+  return rc;
+}
+
+int coli_logprobs(coli_ctx* ctx, const void* logits, long long stride, int dtype, int S, int V, float scale,
+                  const int32_t* tokens, int n, float* logp, float* entropy, int k, int32_t* top_id, float* top_logp) {
+  if (!ctx) return COLI_E_INVAL;
+  if (!logits || (!logp && !entropy && !top_id)) return fail(ctx, COLI_E_INVAL, "logprobs: NULL pointer, or no output");
+  if (dtype != COLI_DTYPE_F32 && dtype != COLI_DTYPE_BF16) return fail(ctx, COLI_E_INVAL, "logprobs: dtype");
+  if (S < 1 || S > COLI_MAX_TOKENS || V < 1 || V > COLI_MAX_VOCAB) return fail(ctx, COLI_E_INVAL, "logprobs: size out of range");
+  if ((tokens != nullptr) != (logp != nullptr) || (logp ? n < 1 || n > COLI_MAX_VOCAB : n != 0))
+    return fail(ctx, COLI_E_INVAL, "logprobs: tokens and logp come together, with their number n");
+  if ((top_id != nullptr) != (top_logp != nullptr) || (top_id ? k < 1 || k > COLI_MAX_TOP : k != 0))
+    return fail(ctx, COLI_E_INVAL, "logprobs: top_id and top_logp come together, with their number k");
+  if (!(scale > 0.f) || !(scale <= 1e30f)) return fail(ctx, COLI_E_INVAL, "logprobs: scale must be above 0 and at most 1e30");
+  if (S == 1) stride = V;  // of one row it says nothing
+  if (stride < V) return fail(ctx, COLI_E_INVAL, "logprobs: row stride below V");
+  if ((uintptr_t)logits % (dtype == COLI_DTYPE_F32 ? 4 : 2) != 0 ||
+      ((uintptr_t)tokens | (uintptr_t)logp | (uintptr_t)entropy | (uintptr_t)top_id | (uintptr_t)top_logp) % 4 != 0)
+    return fail(ctx, COLI_E_INVAL, "logprobs: array not aligned to its dtype");
+  if (injected(ctx)) return COLI_E_INJECTED;
+  cudaSetDevice(ctx->device);
+  LogprobArgs a{};
+  a.x = logits;
+  a.stride = stride;
+  a.S = S;
+  a.V = V;
+  a.scale = scale;
+  a.tokens = tokens;
+  a.n = n;
+  a.logp = logp;
+  a.entropy = entropy;
+  a.k = k;
+  a.top_id = top_id;
+  a.top_logp = top_logp;
+  unsettle_x(ctx);
+  int rc = launch_logprobs(ctx, a, dtype);
   if (rc == COLI_OK) ctx->compute_calls++;
   return rc;
 }

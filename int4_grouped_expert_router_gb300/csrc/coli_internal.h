@@ -99,6 +99,12 @@ struct HostTensor {
   float* sT = nullptr;           // transposed chunk-group scales (desc.sT)
 };
 
+// One uploaded 16-bit weight (coli_dense_upload): layout in dense.h.
+struct DenseTensor {
+  uint8_t* w = nullptr;
+  int O = 0, I = 0;
+};
+
 struct Workspace {
   char* base = nullptr;
   size_t bytes = 0;
@@ -150,6 +156,8 @@ struct coli_ctx {
   unsigned long long settled_capture = 0;
   int* d_kv_count = nullptr;  // coli::kKvCounters arrival counters of the cache attention, zero between calls
   float* d_kv_part = nullptr;  // num_sms x kKvPartFloats: one size for every call, so that captured calls keep their address
+  std::vector<coli::DenseTensor> dense;  // handle = index + 1; w NULL: freed
+  void* d_logprob = nullptr;  // what CTAs that share a row of logits leave for the one that ends it (logprobs.h), zero at first
   coli::Workspace ws;
   // resident issue/take: f32 partial sums [COLI_MAX_ISSUES][S x D] of the current round's issues
   float* slots = nullptr;
@@ -166,8 +174,8 @@ struct coli_ctx {
   };
   std::vector<ProfRec> prof_pending;
   std::vector<cudaEvent_t> prof_free;
-  double prof_ms[COLI_KERNEL_NORM + 1] = {};
-  long long prof_n[COLI_KERNEL_NORM + 1] = {};
+  double prof_ms[COLI_KERNEL_LOGPROBS + 1] = {};
+  long long prof_n[COLI_KERNEL_LOGPROBS + 1] = {};
 };
 
 namespace coli {

@@ -50,21 +50,6 @@ __device__ __forceinline__ void kv4_check_plan(const RowArgs& a) {
   }
 }
 
-// The last sequence b with q_start[b] <= row, found by a whole warp, 32 entries at a time. Whatever
-// q_start holds, the result is a sequence; kv4_place checks that it owns the row.
-__device__ __forceinline__ int warp_seq_of(const Kv4Plan& p, int row) {
-  if (!p.q_start) return row;
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = p.B;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-    const unsigned le = __ballot_sync(0xffffffffu, at < hi && __ldcg(p.q_start + at) <= row);
-    lo += max(0, __popc(le) - 1) * step;
-    hi = min(hi, lo + step);
-  }
-  return lo;
-}
-
 // Where a row lives.
 struct Place {
   uint64_t at;  // offset in the cache of the unit of head 0
@@ -95,7 +80,7 @@ __device__ __forceinline__ Place kv4_places(const RowArgs& a, int row0, int n) {
       if (lane == l) b = at_l, r0 = from, r1 = to, len = have;
     }
   } else {
-    b = warp_seq_of(a.p, row0);
+    b = kv4_seq_of(a.p.q_start, a.p.B, row0);
     if (mine) {
       while (b + 1 < a.p.B && __ldcg(a.p.q_start + b + 1) <= row) b++;  // a few steps: rows are neighbours
       r0 = __ldcg(a.p.q_start + b);

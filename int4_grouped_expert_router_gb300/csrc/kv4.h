@@ -95,6 +95,20 @@ __device__ __forceinline__ void kv4_rows(const Kv4Plan& p, int b, int& r0, int& 
   }
 }
 
+// The last sequence b with q_start[b] <= row, found by a whole warp, 32 entries at a time. Whatever q_start (not NULL) holds,
+// the result is a sequence of 0..B-1; the caller checks that it owns the row.
+__device__ __forceinline__ int kv4_seq_of(const int32_t* q_start, int B, int row) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, at < hi && __ldcg(q_start + at) <= row);
+    lo += max(0, __popc(le) - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
 // The first position that a row at position pos sees (pos may be negative: such a row sees nothing). Any window goes: no
 // difference is formed that could pass 32 bits.
 __device__ __forceinline__ int kv4_from(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }

@@ -1,0 +1,275 @@
+// Rotary positions: pairs of channels of q and k turned by position * frequency, and the table of frequencies.
+//
+// The angle. A frequency is a 64-bit fraction F of a turn per position, so position * F modulo 2^64 is the exact place in the
+// turn: two multiplications of whole numbers, whatever the position, where binary32 would have lost the fraction from a few
+// thousand turns on. Its upper 32 bits, read as a signed part of a half turn, go to sincospif.
+//
+// Bound by memory: q and k are read and written once. The sines and cosines of a row are shared by all of its heads, so a CTA
+// takes whole rows and makes their table in shared memory while its first loads are on their way.
+#include <cuda_bf16.h>
+
+#include <cmath>
+#include <type_traits>
+
+#include "kv4.h"
+#include "pipe.h"
+#include "rotary.h"
+
+namespace coli {
+
+// f / (2 pi) * 2^64 of a frequency in radians, rounded; two doubles hold the quotient, since one would leave an error that
+// 2^31 positions turn into 2^-22 of a turn.
+static uint64_t turns_of(double f) {
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;  // 1 / (2 pi)
+  const double hi = f * kHi;
+  const double lo = std::fma(f, kHi, -hi) + f * kLo;
+  const double whole = std::floor(hi);
+  return (uint64_t)std::ldexp(hi - whole, 64) + (uint64_t)(int64_t)std::llrint(std::ldexp(lo, 64));
+}
+
+int rotary_freqs(int rot, double base, int scaling, double factor, double original, double low, double high, uint64_t* out) {
+  if (!out || rot < 2 || rot > COLI_MAX_ROTARY_DIM || rot % 2 != 0 || !std::isfinite(base) || !(base > 1.0)) return COLI_E_INVAL;
+  if (scaling < COLI_ROTARY_PLAIN || scaling > COLI_ROTARY_PARTS) return COLI_E_INVAL;
+  if (scaling != COLI_ROTARY_PLAIN && (!std::isfinite(factor) || !(factor >= 1.0))) return COLI_E_INVAL;
+  if (scaling == COLI_ROTARY_PARTS && (!std::isfinite(original) || !(original > 0.0) || !std::isfinite(high) || !(low >= 0.0) || !(low < high)))
+    return COLI_E_INVAL;
+  if (scaling == COLI_ROTARY_BASE && rot > 2) {
+    base *= std::pow(factor, (double)rot / (rot - 2));
+    if (!std::isfinite(base)) return COLI_E_INVAL;
+  }
+  for (int i = 0; i < rot / 2; i++) {
+    double f = std::pow(base, -2.0 * i / rot);
+    if (scaling == COLI_ROTARY_LINEAR) f /= factor;
+    if (scaling == COLI_ROTARY_PARTS) {
+      double g = (original * f * 0.15915494309189535 - low) / (high - low);
+      g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
+      f *= g + (1.0 - g) / factor;
+    }
+    out[i] = turns_of(f);
+  }
+  return COLI_OK;
+}
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMostRows = 16;  // rows of a CTA
+
+template <int V>
+struct Vec;  // V bf16 or f32 elements as they lie in memory
+template <> struct Vec<16> { using T = uint4; };
+template <> struct Vec<8> { using T = uint2; };
+template <> struct Vec<4> { using T = uint32_t; };
+template <> struct Vec<2> { using T = uint16_t; };
+
+template <typename T>
+__device__ __forceinline__ T load_cg(const void* p) {
+  if constexpr (sizeof(T) == 2)
+    return __ldcg(static_cast<const unsigned short*>(p));
+  else if constexpr (sizeof(T) == 4)
+    return __ldcg(static_cast<const unsigned int*>(p));
+  else
+    return __ldcg(static_cast<const T*>(p));
+}
+
+template <bool BF16, int V, typename R>
+__device__ __forceinline__ void unpack(const R& raw, float (&v)[V]) {
+  if constexpr (BF16 && V == 1) {
+    v[0] = __uint_as_float((uint32_t)raw << 16);
+  } else {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
+#pragma unroll
+    for (int i = 0; i < (BF16 ? V / 2 : V); i++) {
+      if constexpr (BF16)
+        v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      else
+        v[i] = __uint_as_float(w[i]);
+    }
+  }
+}
+
+template <bool BF16, int V, typename R>
+__device__ __forceinline__ R pack(const float (&v)[V]) {
+  R raw;
+  if constexpr (BF16 && V == 1) {
+    raw = f32_to_bf16_rn(v[0]);
+  } else {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&raw);
+#pragma unroll
+    for (int i = 0; i < (BF16 ? V / 2 : V); i++) {
+      if constexpr (BF16) {
+        const __nv_bfloat162 two = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&two);
+      } else {
+        w[i] = __float_as_uint(v[i]);
+      }
+    }
+  }
+  return raw;
+}
+
+// Vectors of V elements. A task is two of them (two halves' worth of V pairs, or 2 V neighbouring channels), or, behind the
+// turned part, one that is copied.
+template <bool BF16, int V, bool HALF>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a, int rows) {
+  constexpr int E = BF16 ? 2 : 4, U = V == 1 ? 4 : 2;
+  using R = typename Vec<V * E>::T;
+  extern __shared__ float2 s_turn[];  // [rows][rot / 2] cosine, sine
+  __shared__ long long s_pos[kMostRows];
+  constexpr long long kGone = 1ll << 40, kCopied = 1ll << 41;  // not of any sequence; before its sequence's first position
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x, lane = tid & 31, half = a.rot / 2;
+  const int row0 = blockIdx.x * rows;
+  const int here = min(rows, a.T - row0);
+  const int turned = half / V, copied = (a.hd - a.rot) / V, per_head = turned + copied;
+  const int per_row = per_head * (a.side[0].heads + a.side[1].heads);
+  const int tasks = per_row * here;
+
+  // A task's place: where its vectors are read and written, and which pairs they hold.
+  struct Task {
+    const char* in;
+    char* out;
+    int row, pair;  // pair < 0: a copy
+  };
+  auto task_of = [&](int i) {
+    Task t;
+    t.row = i / per_row;
+    i -= t.row * per_row;
+    int head = i / per_head;
+    const int v = i - head * per_head;
+    const bool k = head >= a.side[0].heads;
+    if (k) head -= a.side[0].heads;
+    const RotarySide& s = a.side[k];
+    const int channel = head * a.hd + (v < turned ? (HALF ? v * V : v * 2 * V) : a.rot + (v - turned) * V);
+    t.pair = v < turned ? v * V : -1;
+    t.in = static_cast<const char*>(s.in) + ((row0 + t.row) * s.in_stride + channel) * E;
+    t.out = static_cast<char*>(s.out) + ((row0 + t.row) * s.out_stride + channel) * E;
+    return t;
+  };
+  const int apart = (HALF ? half : V) * E;  // bytes between a task's vectors
+
+  bool made = false;
+  for (int first = 0; first < tasks; first += kThreads * U) {
+    Task t[U];
+    R x[U][2];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int i = first + u * kThreads + tid;
+      t[u].row = -1;
+      if (i < tasks) {
+        t[u] = task_of(i);
+        x[u][0] = load_cg<R>(t[u].in);
+        if (t[u].pair >= 0) x[u][1] = load_cg<R>(t[u].in + apart);
+      }
+    }
+    if (!made) {
+      made = true;
+      if (a.positions) {
+        if (tid < here) s_pos[tid] = __ldcg(a.positions + row0 + tid);
+      } else if (!a.q_start) {
+        if (tid < here) {
+          const int len = __ldcg(a.lens + row0 + tid);
+          if (len < 0) set_error(a.err, COLI_E_RANGE);
+          s_pos[tid] = len > 0 ? len - 1 : kCopied;
+        }
+      } else {
+        for (int r = tid >> 5; r < here; r += kThreads / 32) {
+          const int row = row0 + r, b = kv4_seq_of(a.q_start, a.B, row);
+          if (lane == 0) {
+            const int r0 = __ldcg(a.q_start + b), r1 = __ldcg(a.q_start + b + 1), len = __ldcg(a.lens + b);
+            const bool owned = r0 >= 0 && r1 <= a.T && row >= r0 && row < r1;
+            const long long pos = (long long)max(len, 0) - (r1 - row);
+            s_pos[r] = !owned ? kGone : pos < 0 ? kCopied : pos;
+          }
+        }
+        // ranges and lengths that do not fit are reported whether or not a row falls in them
+        for (int b = blockIdx.x * kThreads + tid; b < a.B; b += gridDim.x * kThreads) {
+          const int r0 = __ldcg(a.q_start + b), r1 = __ldcg(a.q_start + b + 1);
+          if (r0 < 0 || r1 < r0 || r1 > a.T || __ldcg(a.lens + b) < 0) set_error(a.err, COLI_E_RANGE);
+        }
+      }
+      __syncthreads();
+      for (int i = tid; i < here * half; i += kThreads) {
+        const int r = i / half;
+        const long long pos = s_pos[r];
+        if (pos < kGone) {
+          const uint32_t turn = (uint32_t)(((uint64_t)pos * __ldcg(reinterpret_cast<const unsigned long long*>(a.freqs) + (i - r * half))) >> 32);
+          float sine, cosine;
+          sincospif((float)(int)turn * 4.656612873077393e-10f, &sine, &cosine);  // 2^-31
+          s_turn[i] = make_float2(cosine * a.scale, sine * a.scale);
+        }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      if (t[u].row < 0) continue;
+      const long long pos = s_pos[t[u].row];
+      if (pos == kGone) continue;
+      if (pos != kCopied && t[u].pair >= 0) {
+        const float2* turn = s_turn + t[u].row * half + t[u].pair;
+        float v[2][V];
+        unpack<BF16, V>(x[u][0], v[0]);
+        unpack<BF16, V>(x[u][1], v[1]);
+        auto rotate = [&](float& p, float& q, float2 cs) {
+          const float c = fmaf(p, cs.x, -q * cs.y), d = fmaf(q, cs.x, p * cs.y);
+          p = c, q = d;
+        };
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+          if constexpr (HALF || V == 1)
+            rotate(v[0][i], v[1][i], turn[i]);
+          else
+            rotate(v[2 * i / V][2 * i % V], v[2 * i / V][2 * i % V + 1], turn[i]);
+        }
+        x[u][0] = pack<BF16, V, R>(v[0]);
+        x[u][1] = pack<BF16, V, R>(v[1]);
+      }
+      *reinterpret_cast<R*>(t[u].out) = x[u][0];
+      if (t[u].pair >= 0) *reinterpret_cast<R*>(t[u].out + apart) = x[u][1];
+    }
+  }
+}
+
+template <bool BF16, int V, bool HALF>
+cudaError_t launch_one(coli_ctx* ctx, const RotaryArgs& a) {
+  const int per_row = ((a.rot / 2 + a.hd - a.rot) / V) * (a.side[0].heads + a.side[1].heads);
+  const int rows = per_row >= kThreads ? 1 : min(kMostRows, kThreads / per_row);
+  const size_t smem = (size_t)rows * (a.rot / 2) * sizeof(float2);  // at most kThreads * V pairs: 16 KB
+  return launch_k(rotary_kernel<BF16, V, HALF>, (a.T + rows - 1) / rows, kThreads, smem, ctx->stream, true, false, a, rows);
+}
+
+}  // namespace
+
+int launch_rotary(coli_ctx* ctx, const RotaryArgs& args, int dtype, bool interleaved) {
+  RotaryArgs a = args;
+  a.err = ctx->d_status;
+  const int elem = dtype == COLI_DTYPE_BF16 ? 2 : 4;
+  // the widest vectors that every row, head, half and copied part is a whole number of
+  long long whole = (long long)a.hd | (interleaved ? a.rot : a.rot / 2) | (a.hd - a.rot);
+  uintptr_t at = 0;
+  for (const RotarySide& s : a.side)
+    if (s.in) {
+      at |= (uintptr_t)s.in | (uintptr_t)s.out;
+      if (a.T > 1) whole |= s.in_stride | s.out_stride;
+    }
+  if (interleaved) whole |= a.rot / 2;  // a task is two neighbouring vectors
+  at |= (uintptr_t)(whole * elem);
+  ProfScope prof(ctx, COLI_KERNEL_ROTARY);
+  cudaError_t e;
+  auto pick = [&](auto bf16, auto v16, auto v8) {
+    constexpr bool kBf16 = decltype(bf16)::value;
+    if (at % 16 == 0) return interleaved ? launch_one<kBf16, decltype(v16)::value, false>(ctx, a) : launch_one<kBf16, decltype(v16)::value, true>(ctx, a);
+    if (at % 8 == 0) return interleaved ? launch_one<kBf16, decltype(v8)::value, false>(ctx, a) : launch_one<kBf16, decltype(v8)::value, true>(ctx, a);
+    return interleaved ? launch_one<kBf16, 1, false>(ctx, a) : launch_one<kBf16, 1, true>(ctx, a);
+  };
+  if (dtype == COLI_DTYPE_BF16)
+    e = pick(std::true_type{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
+  else
+    e = pick(std::false_type{}, std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "rotary launch");
+  return COLI_OK;
+}
+
+}  // namespace coli
