@@ -109,13 +109,14 @@ int ensure_slots(coli_ctx* ctx, size_t bytes) {
   return COLI_OK;
 }
 
-// The cache attention's partial results: allocated by its first call or coli_reserve, and never moved.
-int ensure_kv_part(coli_ctx* ctx) {
-  if (ctx->d_kv_part) return COLI_OK;
+// Partial results of split work: allocated by the first call that may split (cache attention, 16-bit products) or
+// coli_reserve, and never moved.
+int ensure_part(coli_ctx* ctx) {
+  if (ctx->d_part) return COLI_OK;
   void* p = nullptr;
-  cudaError_t e = cudaMalloc(&p, (size_t)ctx->num_sms * kKvPartFloats * sizeof(float));
-  if (e != cudaSuccess) return cuda_fail(ctx, e, "attention partials cudaMalloc");
-  ctx->d_kv_part = static_cast<float*>(p);
+  cudaError_t e = cudaMalloc(&p, (size_t)ctx->num_sms * kPartFloats * sizeof(float));
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "partial results cudaMalloc");
+  ctx->d_part = static_cast<float*>(p);
   return COLI_OK;
 }
 
@@ -226,17 +227,22 @@ static int make_desc(coli_ctx* ctx, HostTensor& t) {
   return COLI_OK;
 }
 
-int encode_bf16_rows_map(coli_ctx* ctx, CUtensorMap* map, void* base, long long rows, int cols) {
+int encode_rows_map(coli_ctx* ctx, CUtensorMap* map, void* base, long long rows, int cols, long long stride, int box_cols,
+                    int box_rows) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return fail(ctx, COLI_E_CUDA, "cuTensorMapEncodeTiled unavailable");
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-  cuuint32_t box[2] = {64, 16};
+  cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+  cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   cuuint32_t es[2] = {1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(ctx, COLI_E_CUDA, "activation tensor map encoding failed");
   return COLI_OK;
+}
+
+int encode_bf16_rows_map(coli_ctx* ctx, CUtensorMap* map, void* base, long long rows, int cols) {
+  return encode_rows_map(ctx, map, base, rows, cols, cols, 64, 16);
 }
 
 }  // namespace coli
@@ -293,6 +299,9 @@ int coli_init(coli_ctx** out, int device, void* cuda_stream) {
   if ((e = cudaMalloc(&p, kKvCounters * sizeof(int))) != cudaSuccess) goto fail;
   ctx->d_kv_count = static_cast<int*>(p);
   if ((e = cudaMemset(ctx->d_kv_count, 0, kKvCounters * sizeof(int))) != cudaSuccess) goto fail;
+  if ((e = cudaMalloc(&p, ctx->num_sms * sizeof(int))) != cudaSuccess) goto fail;
+  ctx->d_dense_count = static_cast<int*>(p);
+  if ((e = cudaMemset(ctx->d_dense_count, 0, ctx->num_sms * sizeof(int))) != cudaSuccess) goto fail;
   if ((e = cudaMalloc(&ctx->d_logprob, logprob_bytes(ctx->num_sms))) != cudaSuccess) goto fail;
   if ((e = cudaMemset(ctx->d_logprob, 0, logprob_bytes(ctx->num_sms))) != cudaSuccess) goto fail;
   if ((e = cudaMalloc(&ctx->d_router, kRouterScratchBytes)) != cudaSuccess) goto fail;
@@ -326,13 +335,14 @@ void coli_destroy(coli_ctx* ctx) {
   for (auto& t : ctx->dense)
     if (t.w) cudaFree(t.w);
   if (ctx->d_solo_route) cudaFree(ctx->d_solo_route);
+  if (ctx->d_dense_count) cudaFree(ctx->d_dense_count);
   if (ctx->d_logprob) cudaFree(ctx->d_logprob);
   ans_release_all(ctx);
   if (ctx->d_table) cudaFree(ctx->d_table);
   if (ctx->d_status) cudaFree(ctx->d_status);
   if (ctx->d_router) cudaFree(ctx->d_router);
   if (ctx->d_kv_count) cudaFree(ctx->d_kv_count);
-  if (ctx->d_kv_part) cudaFree(ctx->d_kv_part);
+  if (ctx->d_part) cudaFree(ctx->d_part);
   if (ctx->ws.base) cudaFree(ctx->ws.base);
   if (ctx->slots) cudaFree(ctx->slots);
   for (auto& r : ctx->prof_pending) {
@@ -424,10 +434,13 @@ int coli_reserve(coli_ctx* ctx, int max_S, int max_E, int max_K, int max_D, int 
   // one-launch S == 1 FFN: a partial row of y per CTA
   const size_t stream = (size_t)ctx->num_sms * max_D * sizeof(float);
   if (stream > experts) experts = stream;
+  // 16-bit products: activations as up to three planes of 16-bit rows
+  const size_t planes = dense_x_bytes(max_S, std::max(max_D, max_I), 3);
+  if (planes > experts) experts = planes;
   const size_t slots = (size_t)COLI_MAX_ISSUES * max_S * max_D * sizeof(float);
   cudaSetDevice(ctx->device);
   int rc = ensure_slots(ctx, slots);
-  if (rc == COLI_OK) rc = ensure_kv_part(ctx);
+  if (rc == COLI_OK) rc = ensure_part(ctx);
   if (rc != COLI_OK) return rc;
   return ensure_workspace(ctx, router > experts ? router : experts);
 }
@@ -1084,7 +1097,7 @@ uint64_t coli_dense_upload(coli_ctx* ctx, const uint16_t* W, int O, int I) {
   for (int at = 0; at < O && e == cudaSuccess; at += piece) {
     const int rows = std::min(piece, O - at);
     e = cudaMemcpyAsync(tmp, W + (size_t)at * I, row * rows, cudaMemcpyDefault, ctx->stream);
-    if (e == cudaSuccess) e = launch_dense_pack(ctx->stream, static_cast<uint16_t*>(tmp), rows, at, O, I, static_cast<uint8_t*>(pw));
+    if (e == cudaSuccess) e = launch_dense_pack(ctx->stream, static_cast<uint16_t*>(tmp), rows, at, I, static_cast<uint8_t*>(pw));
   }
   const cudaError_t sync = cudaStreamSynchronize(ctx->stream);
   if (e == cudaSuccess) e = sync;

@@ -35,9 +35,10 @@ constexpr size_t kRouterScratchBytes = 256 + (size_t)15 * 1024 * 8;
 // Arrival counters of split work in the cache attention (the streaming form uses three per CTA of its grid, the tensor-core
 // form one), zero between calls.
 constexpr int kKvCounters = 4096;
-// Partial results of the cache attention, in floats per SM: two for the tensor-core form's CTA of 256 rows of 128 channels
-// and a (maximum, sum) pair, and more than any CTAs of the streaming form leave.
-constexpr size_t kKvPartFloats = (size_t)2 * 256 * (128 + 2);
+// Partial results of work that is split over CTAs, in floats per SM: of the cache attention two for the tensor-core form's CTA
+// of 256 rows of 128 channels and a (maximum, sum) pair, and more than any CTAs of the streaming form leave; of the 16-bit
+// products two tiles of 128 rows x 256 tokens.
+constexpr size_t kPartFloats = (size_t)2 * 256 * (128 + 2);
 
 // Device status words of a context: [0] error code, [1] unused, [2..] the opt-in fused decode
 // kernel's synchronisation words (grid barrier at [2], [3]; row-range counters from
@@ -155,7 +156,8 @@ struct coli_ctx {
   cudaStream_t settled_stream = nullptr;
   unsigned long long settled_capture = 0;
   int* d_kv_count = nullptr;  // coli::kKvCounters arrival counters of the cache attention, zero between calls
-  float* d_kv_part = nullptr;  // num_sms x kKvPartFloats: one size for every call, so that captured calls keep their address
+  int* d_dense_count = nullptr;  // num_sms arrival counters of the 16-bit products, zero between calls
+  float* d_part = nullptr;  // num_sms x kPartFloats: one size for every call, so that captured calls keep their address
   std::vector<coli::DenseTensor> dense;  // handle = index + 1; w NULL: freed
   void* d_logprob = nullptr;  // what CTAs that share a row of logits leave for the one that ends it (logprobs.h), zero at first
   coli::Workspace ws;
@@ -187,7 +189,7 @@ int ensure_workspace(coli_ctx* ctx, size_t bytes);
 // Whether a kernel launched now, programmatically serialised, may read x before its griddepcontrol.wait.
 bool x_settled(coli_ctx* ctx, const void* x);
 int ensure_slots(coli_ctx* ctx, size_t bytes);
-int ensure_kv_part(coli_ctx* ctx);
+int ensure_part(coli_ctx* ctx);
 
 constexpr size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -212,6 +214,9 @@ int launch_prefill(coli_ctx* ctx, const void* x, int S, const int32_t* idx, cons
 // TMA map over a row-major bf16 matrix [rows x cols] read in 16-row x 64-column boxes with the
 // 128-byte swizzle (cols a multiple of 8).
 int encode_bf16_rows_map(coli_ctx* ctx, CUtensorMap* map, void* base, long long rows, int cols);
+// The same with rows `stride` elements apart (a multiple of 8, base 16-byte aligned), in boxes of box_rows x box_cols.
+int encode_rows_map(coli_ctx* ctx, CUtensorMap* map, void* base, long long rows, int cols, long long stride, int box_cols,
+                    int box_rows);
 
 int launch_router_noalloc(coli_ctx* ctx, const void* x, int x_dtype, int S, int D, const float* Wr,
                           const float* bias, int E, int K, float topp, int norm_topk, float routed_scale, int shared,

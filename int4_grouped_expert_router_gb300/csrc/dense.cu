@@ -1,20 +1,65 @@
-// y = resid + act(W x + bias) * mul with 16-bit weights (layout: dense.h).
+// y = resid + act(W x + bias) * mul with 16-bit weights (layout: dense.h), on the fifth-generation tensor cores.
+//
+// D = W X^T: the rows of W are the instruction's M (128), the tokens its N (16 to 256, the smallest that covers S, or 256).
+// Units of work are (128 rows x N tokens) tiles times column tiles of 64, dealt out evenly and contiguously to one CTA per SM,
+// so that one token keeps every SM streaming a contiguous run of W, and many tokens leave no part of a wave idle. A tile that
+// several CTAs share is joined by the one that arrives last, in CTA order, so results do not depend on who that is.
+//
+// One CTA, 12 warps: a producer (W by bulk copies, x by tiled ones, a ring of stages), a thread that issues the products, and
+// eight warps for what follows (bias, activation, factor, residual), which take a tile from tensor memory while the next one
+// is being formed in the other half of it. The ring is filled with weights before the work ahead in the stream is waited for.
+//
+// Sums. The tensor core cuts a sum off where binary32 would round it, always towards zero, and 6144 products leave 2^-17 that
+// way. Where y is binary32 a chunk of kChunk column tiles is formed at a time and the chunks are added in registers.
+// Binary32 activations enter as parts of 8 bits by truncation, x = h + m + l exactly (two parts, 16 bits, where y is
+// rounded to 8), each multiplied with the same staged tile of W.
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
 #include "dense.h"
 #include "pipe.h"
+#include "tc.h"
 
 namespace coli {
 
 namespace {
 
 constexpr float kInf = __builtin_huge_valf();
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8, kWarpEpi = 4;  // warps 0 and 1: producer, products; a quarter of the lanes goes by warp % 4
+constexpr int kChunk = 4;                   // column tiles
 
-__device__ __forceinline__ const uint16_t* dense_at(const uint8_t* w, int col_tiles, int o, int i) {
-  const uint8_t* tile = w + ((size_t)(o / kDenseRows) * col_tiles + i / kDenseCols) * kDenseTile;
+// P parts of x for a staged tile of W; kExact: y is binary32.
+template <int N, int P, bool EXACT>
+struct Shape {
+  static constexpr uint32_t kX = P * N * 128;
+  static constexpr uint32_t kStage = kDenseTile + kX;
+  static constexpr int kStages = std::min<uint32_t>(12, 224 * 1024 / kStage);
+  static constexpr uint32_t kSmem = 1024 + kStages * kStage;
+  static constexpr int kTmem = 2 * N;  // two accumulators; a power of two from 32 on
+  static constexpr int kGroups = N / 16;                    // of 16 tokens
+  static constexpr int kMine = (kGroups + 1) / 2;           // of a warp
+};
+
+struct TileArgs {
+  DenseArgs d;
+  int kt;       // column tiles
+  int nt;       // tiles of tokens
+  long long total;
+  bool stream;  // W is read once
+  float* part;  // per CTA two of [N][128]
+  int* count;   // per CTA, zero between calls
+  uint64_t wait_ns;
+  bool withhold;  // test hook: the call's first copy is withheld, and the waits on it give up
+};
+
+__device__ __forceinline__ uint8_t* dense_at(uint8_t* w, int col_tiles, int o, int i) {
   const int r = o % kDenseRows, chunk = i % kDenseCols / 8;
-  return reinterpret_cast<const uint16_t*>(tile + r * 128 + ((chunk ^ (r & 7)) << 4)) + i % 8;
+  return w + ((size_t)(o / kDenseRows) * col_tiles + i / kDenseCols) * kDenseTile + r * 128 + ((chunk ^ (r & 7)) << 4);
 }
 
-__global__ void dense_pack_kernel(const uint16_t* src, int rows, int row0, int O, int I, int col_tiles, uint8_t* w) {
+__global__ void dense_pack_kernel(const uint16_t* src, int rows, int row0, int I, int col_tiles, uint8_t* w) {
   const long long chunks = (long long)((rows + kDenseRows - 1) / kDenseRows) * kDenseRows * col_tiles * 8;
   for (long long n = (long long)blockIdx.x * blockDim.x + threadIdx.x; n < chunks; n += (long long)gridDim.x * blockDim.x) {
     const int r = (int)(n / (col_tiles * 8)), i0 = (int)(n % (col_tiles * 8)) * 8;
@@ -22,57 +67,448 @@ __global__ void dense_pack_kernel(const uint16_t* src, int rows, int row0, int O
     if (r < rows)
       for (int i = 0; i < 8; i++)
         if (i0 + i < I) v[i / 2] |= (uint32_t)src[(size_t)r * I + i0 + i] << (16 * (i & 1));
-    *reinterpret_cast<uint4*>(const_cast<uint16_t*>(dense_at(w, col_tiles, row0 + r, i0))) = make_uint4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<uint4*>(dense_at(w, col_tiles, row0 + r, i0)) = make_uint4(v[0], v[1], v[2], v[3]);
   }
 }
 
-__device__ __forceinline__ float dense_act(float z, int act) {
-  switch (act) {
-    case COLI_ACT_SILU: return z / (1.f + expf(-z));
-    case COLI_ACT_GELU: return 0.5f * z * erfcf(z * -0.70710678118654752f);
-    case COLI_ACT_GELU_TANH: return z / (1.f + expf(-1.5957691216057308f * fmaf(0.044715f * z * z, z, z)));
-    case COLI_ACT_RELU: return fmaxf(z, 0.f);
-    case COLI_ACT_RELU2: return fmaxf(z, 0.f) * fmaxf(z, 0.f);
-  }
-  return z;
-}
-
-__global__ void dense_kernel(DenseArgs a, int x_dtype, int y_dtype, int col_tiles) {
+// x as planes of bf16 rows that start at 16-byte boundaries: itself, or its parts of 8 bits.
+template <bool BF16, int P>
+__global__ void dense_x_kernel(const void* x, long long stride, int S, int I, uint8_t* to) {
   griddep_launch_dependents();
   griddep_wait();
-  const long long cells = (long long)a.S * a.O;
-  for (long long n = (long long)blockIdx.x * blockDim.x + threadIdx.x; n < cells; n += (long long)gridDim.x * blockDim.x) {
-    const int t = (int)(n / a.O), o = (int)(n % a.O);
-    float z = 0.f;
-    for (int i = 0; i < a.I; i++) z = fmaf(bf16_to_f32(*dense_at(a.w, col_tiles, o, i)), load_act(a.x, x_dtype, (size_t)t * a.x_stride + i), z);
-    if (!(fabsf(z) < kInf)) set_error(a.err, COLI_E_NONFINITE);
-    if (a.bias) z += __ldcg(a.bias + o);
-    z = dense_act(z, a.act);
-    if (a.mul) z *= load_act(a.mul, y_dtype, (size_t)t * a.mul_stride + o);
-    if (a.resid) z += load_act(a.resid, y_dtype, (size_t)t * a.resid_stride + o);
-    const size_t to = (size_t)t * a.y_stride + o;
-    if (y_dtype == COLI_DTYPE_F32)
-      static_cast<float*>(a.y)[to] = z;
-    else
-      static_cast<uint16_t*>(a.y)[to] = f32_to_bf16_rn(z);
+  const int chunks = (I + 7) / 8;
+  const long long n_all = (long long)S * chunks;
+  for (long long n = (long long)blockIdx.x * blockDim.x + threadIdx.x; n < n_all; n += (long long)gridDim.x * blockDim.x) {
+    const int s = (int)(n / chunks), i0 = (int)(n - (long long)s * chunks) * 8;
+    uint32_t v[P][4] = {};
+    const size_t at = (size_t)s * stride + i0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      if (i0 + i >= I) break;
+      const int shift = 16 * (i & 1);
+      if constexpr (BF16) {
+        v[0][i / 2] |= (uint32_t)__ldcg(static_cast<const unsigned short*>(x) + at + i) << shift;
+      } else {
+        float rest = __ldcg(static_cast<const float*>(x) + at + i);
+#pragma unroll
+        for (int p = 0; p < P; p++) {
+          const uint32_t u = __float_as_uint(rest);
+          // what is not finite stays what it is, in the first part alone
+          const bool finite = (u & 0x7f800000u) != 0x7f800000u;
+          const uint32_t top = finite ? u & 0xffff0000u : (u & 0x7fffffu) ? 0x7fc00000u : u;
+          v[p][i / 2] |= (top >> 16) << shift;
+          rest = finite ? rest - __uint_as_float(top) : 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < P; p++)
+      *reinterpret_cast<uint4*>(to + ((size_t)p * n_all + n) * 16) = make_uint4(v[p][0], v[p][1], v[p][2], v[p][3]);
   }
+}
+
+__device__ __forceinline__ void dense_act(float (&z)[16], int act) {
+  switch (act) {
+    case COLI_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < 16; i++) z[i] = z[i] / (1.f + expf(-z[i]));
+      break;
+    case COLI_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < 16; i++) z[i] = 0.5f * z[i] * erfcf(z[i] * -0.70710678118654752f);
+      break;
+    case COLI_ACT_GELU_TANH:
+#pragma unroll
+      for (int i = 0; i < 16; i++) z[i] = z[i] / (1.f + expf(-1.5957691216057308f * fmaf(0.044715f * z[i] * z[i], z[i], z[i])));
+      break;
+    case COLI_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < 16; i++) z[i] = z[i] < 0.f ? 0.f : z[i];
+      break;
+    case COLI_ACT_RELU2:
+#pragma unroll
+      for (int i = 0; i < 16; i++) z[i] = z[i] < 0.f ? 0.f : z[i] * z[i];
+      break;
+  }
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t at, const float (&v)[16]) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; i++) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int N, int P, bool EXACT>
+__global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constant__ CUtensorMap x_map, TileArgs a) {
+  using H = Shape<N, P, EXACT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);  // [kStages][W tile | P tiles of x]
+  __shared__ __align__(8) uint64_t full[H::kStages], empty[H::kStages], acc_full[2], acc_empty[2];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < H::kStages; i++) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; i++) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kEpiWarps);
+    }
+    mbar_fence_init();
+  }
+  if (warp == 1) tmem_alloc(&s_tmem, H::kTmem);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = s_tmem;
+
+  const long long w0 = a.total * blockIdx.x / gridDim.x, w1 = a.total * (blockIdx.x + 1) / gridDim.x;
+  const int tile0 = (int)(w0 / a.kt), k0 = (int)(w0 - (long long)tile0 * a.kt);
+  bool alive = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (alive && !mbar_wait_suspend(bar, parity, a.wait_ns)) {
+      set_error(a.d.err, COLI_E_TIMEOUT);
+      alive = false;  // void from here on, but nothing hangs
+    }
+  };
+
+  if (warp == 0) {
+    // ------------------------------------ producer ------------------------------------
+    if (elect_one()) {
+      const uint64_t once = l2_evict_first_policy();
+      const uint32_t units = (uint32_t)(w1 - w0);
+      const uint8_t* w_at = a.d.w + ((size_t)(tile0 / a.nt) * a.kt + k0) * kDenseTile;  // of the next copy of W
+      int w_k = k0, w_n = tile0 % a.nt;
+      auto copy_w = [&](uint32_t n) {
+        const uint32_t s = n % H::kStages;
+        const bool held = a.withhold && n == 0 && blockIdx.x == 0;
+        if (!held) {
+          mbar_arrive_expect_tx(&full[s], H::kStage);
+          if (a.stream)
+            bulk_g2s_stream(smem + s * H::kStage, w_at, kDenseTile, &full[s], once);
+          else
+            bulk_g2s(smem + s * H::kStage, w_at, kDenseTile, &full[s]);
+        }
+        w_at += kDenseTile;
+        if (++w_k == a.kt) {
+          w_k = 0;
+          if (++w_n == a.nt)
+            w_n = 0;
+          else
+            w_at -= (size_t)a.kt * kDenseTile;  // the same rows for the next tokens
+        }
+      };
+      int x_k = k0, x_n = tile0 % a.nt;
+      auto copy_x = [&](uint32_t n) {
+        const uint32_t s = n % H::kStages;
+        const bool held = a.withhold && n == 0 && blockIdx.x == 0;
+        if (!held)
+#pragma unroll
+          for (int p = 0; p < P; p++)
+            tma_load_2d(smem + s * H::kStage + kDenseTile + p * N * 128, &x_map, x_k * kDenseCols, p * a.d.S + x_n * N, &full[s]);
+        if (++x_k == a.kt) {
+          x_k = 0;
+          if (++x_n == a.nt) x_n = 0;
+        }
+      };
+      const uint32_t ahead = units < (uint32_t)H::kStages ? units : (uint32_t)H::kStages;
+      for (uint32_t n = 0; n < ahead; n++) copy_w(n);  // weights do not depend on the work before this call
+      griddep_wait();
+      for (uint32_t n = 0; n < ahead; n++) copy_x(n);
+      uint32_t n = ahead;
+      for (; n < units && alive; n++) {
+        wait(&empty[n % H::kStages], (n / H::kStages + 1) & 1);
+        if (!alive) break;
+        copy_w(n);
+        copy_x(n);
+      }
+      // no copy or product is in flight when the CTA ends, whatever has been given up
+      for (uint32_t i = n > (uint32_t)H::kStages ? n - H::kStages : 0; i < n; i++) {
+        if (!(a.withhold && i == 0 && blockIdx.x == 0)) mbar_wait(&full[i % H::kStages], (i / H::kStages) & 1, a.wait_ns);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------ products ------------------------------------
+    // operands in uniform registers
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t w_desc = uniform(sw128_kmajor_desc(smem)), x_desc = uniform(sw128_kmajor_desc(smem + kDenseTile));
+    if (elect_one()) {
+      constexpr uint32_t kId = bf16_f32_idesc(kDenseRows, N);
+      uint32_t s = 0, phase = 0, chunk = 0;
+      int k = k0;
+      long long w = w0;
+      while (w < w1) {
+        const int seg = (int)min((long long)(a.kt - k), w1 - w);
+        for (int done = 0; done < seg;) {
+          const int here = EXACT ? min(kChunk, seg - done) : seg;
+          wait(&acc_empty[chunk & 1], ((chunk >> 1) + 1) & 1);
+          tc_fence_after_sync();
+          const uint32_t acc = tm + (chunk & 1) * N;
+          for (int i = 0; i < here; i++) {
+            wait(&full[s], phase);
+            tc_fence_after_sync();
+            const uint32_t at = s * (H::kStage >> 4);  // a descriptor's address field counts 16 bytes
+#pragma unroll
+            for (int p = P - 1; p >= 0; p--)  // the small parts first
+#pragma unroll
+              for (int kk = 0; kk < 4; kk++)
+                tc_mma_bf16(acc, w_desc + at + kk * 2, x_desc + at + p * (N * 8) + kk * 2, kId, i > 0 || p < P - 1 || kk > 0);
+            tc_commit(&empty[s]);
+            if (++s == (uint32_t)H::kStages) s = 0, phase ^= 1;
+          }
+          tc_commit(&acc_full[chunk & 1]);
+          chunk++;
+          done += here;
+        }
+        w += seg;
+        k = 0;
+      }
+      // the last arrivals on these barriers come before the CTA's memory goes
+      const uint32_t units = (uint32_t)(w1 - w0);
+      for (uint32_t i = units > (uint32_t)H::kStages ? units - H::kStages : 0; i < units; i++)
+        mbar_wait(&empty[i % H::kStages], (i / H::kStages) & 1, a.wait_ns);
+    }
+    __syncwarp();
+  } else if (warp >= kWarpEpi) {
+    // ------------------------------------- what follows -------------------------------------
+    griddep_wait();
+    const int half = (warp - kWarpEpi) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t tm = tmem + ((uint32_t)(warp & 3) << 21);  // lanes 32 (warp % 4) on
+    bool broken = false;
+    // 16 tokens of group g of a tile, from their sums on
+    auto finish = [&](float (&z)[16], int tile, int g) {
+      const int o = tile / a.nt * kDenseRows + row, t0 = tile % a.nt * N + g * 16;
+      if (o >= a.d.O || t0 >= a.d.S) return;
+      const int n = min(16, a.d.S - t0);
+      float f[16], q[16];
+      auto load = [&](const void* p, long long stride, float (&v)[16]) {
+        const size_t at = (size_t)t0 * stride + o;
+#pragma unroll
+        for (int i = 0; i < 16; i++)
+          if (i < n)
+            v[i] = EXACT ? __ldcg(static_cast<const float*>(p) + at + i * stride)
+                         : bf16_to_f32(__ldcg(static_cast<const unsigned short*>(p) + at + i * stride));
+      };
+      if (a.d.mul) load(a.d.mul, a.d.mul_stride, f);
+      if (a.d.resid) load(a.d.resid, a.d.resid_stride, q);
+      const float b = a.d.bias ? __ldcg(a.d.bias + o) : 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; i++) {
+        broken |= i < n && !(fabsf(z[i]) < kInf);
+        if (a.d.bias) z[i] += b;
+      }
+      dense_act(z, a.d.act);
+      if (a.d.mul)
+#pragma unroll
+        for (int i = 0; i < 16; i++) z[i] *= f[i];
+      if (a.d.resid)
+#pragma unroll
+        for (int i = 0; i < 16; i++) z[i] += q[i];
+      const size_t at = (size_t)t0 * a.d.y_stride + o;
+#pragma unroll
+      for (int i = 0; i < 16; i++)
+        if (i < n) {
+          if constexpr (EXACT)
+            static_cast<float*>(a.d.y)[at + i * a.d.y_stride] = z[i];
+          else
+            static_cast<uint16_t*>(a.d.y)[at + i * a.d.y_stride] = f32_to_bf16_rn(z[i]);
+        }
+    };
+    uint32_t chunk = 0;
+    int k = k0, tile = tile0;
+    long long w = w0;
+    while (w < w1) {
+      const int seg = (int)min((long long)(a.kt - k), w1 - w);
+      const bool whole = seg == a.kt;
+      // a tile's beginning goes to the CTA's second part, a continuation to its first
+      float* mine = a.part + ((size_t)2 * blockIdx.x + (k == 0)) * N * kDenseRows + row;
+      auto store = [&](const float (&z)[16], int g) {
+#pragma unroll
+        for (int i = 0; i < 16; i++) mine[(g * 16 + i) * kDenseRows] = z[i];
+      };
+      if constexpr (EXACT) {
+        float sum[H::kMine][16] = {};
+#pragma unroll 1
+        for (int done = 0; done < seg; done += kChunk) {
+          wait(&acc_full[chunk & 1], (chunk >> 1) & 1);
+          __syncwarp();
+          tc_fence_after_sync();
+          const uint32_t acc = tm + (chunk & 1) * N;
+          const bool last = done + kChunk >= seg;
+          if (last && done == 0) break;  // one chunk: it is where it is read from below
+#pragma unroll
+          for (int m = 0; m < H::kMine; m++) {
+            const int g = 2 * m + half;
+            if (g >= H::kGroups) break;
+            float v[16];
+            tmem_ld16(acc + g * 16, v);
+#pragma unroll
+            for (int i = 0; i < 16; i++) sum[m][i] += v[i];
+            if (last) tmem_st16(acc + g * 16, sum[m]);
+          }
+          if (last) break;
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[chunk & 1]);
+          chunk++;
+        }
+        tmem_wait_st();
+      } else {
+        wait(&acc_full[chunk & 1], (chunk >> 1) & 1);
+        __syncwarp();
+        tc_fence_after_sync();
+      }
+#pragma unroll 1
+      for (int g = half; g < H::kGroups; g += 2) {
+        float v[16];
+        tmem_ld16(tm + (chunk & 1) * N + g * 16, v);
+        if (whole)
+          finish(v, tile, g);
+        else
+          store(v, g);
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[chunk & 1]);
+      chunk++;
+      if (!whole) {
+        // the CTAs of this tile: from the one that begins it to the one that ends it
+        const long long u0 = (long long)tile * a.kt, u1 = u0 + a.kt - 1;
+        const int first = (int)(((u0 + 1) * gridDim.x - 1) / a.total), last = (int)(((u1 + 1) * gridDim.x - 1) / a.total);
+        __threadfence();
+        named_sync(1, kEpiWarps * 32);
+        if (tid == kWarpEpi * 32) {
+          s_last = atomicAdd(a.count + first, 1) == last - first;
+          if (s_last) a.count[first] = 0;
+        }
+        named_sync(1, kEpiWarps * 32);
+        if (s_last) {
+          __threadfence();
+#pragma unroll 1
+          for (int g = half; g < H::kGroups; g += 2) {
+            float z[16];
+            const float* p = a.part + ((size_t)2 * first + 1) * N * kDenseRows + g * 16 * kDenseRows + row;
+#pragma unroll
+            for (int i = 0; i < 16; i++) z[i] = __ldcg(p + i * kDenseRows);
+            p += (size_t)N * kDenseRows;  // the first part of the CTA after
+#pragma unroll 2
+            for (int c = first + 1; c <= last; c++, p += (size_t)2 * N * kDenseRows)
+#pragma unroll
+              for (int i = 0; i < 16; i++) z[i] += __ldcg(p + i * kDenseRows);
+            finish(z, tile, g);
+          }
+        }
+        named_sync(1, kEpiWarps * 32);  // s_last is read before it is written again
+      }
+      w += seg;
+      k = 0;
+      tile++;
+    }
+    if (broken) set_error(a.d.err, COLI_E_NONFINITE);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 1) tmem_dealloc(tmem, H::kTmem);
+}
+
+template <int N, int P, bool EXACT>
+int launch_one(coli_ctx* ctx, TileArgs& a, const CUtensorMap& map) {
+  using H = Shape<N, P, EXACT>;
+  static_assert((size_t)2 * N * kDenseRows <= kPartFloats, "a CTA leaves more than there is room for");
+  a.kt = (a.d.I + kDenseCols - 1) / kDenseCols;
+  a.nt = (a.d.S + N - 1) / N;
+  a.total = (long long)((a.d.O + kDenseRows - 1) / kDenseRows) * a.nt * a.kt;
+  a.stream = a.nt == 1;
+  auto kern = dense_kernel<N, P, EXACT>;
+  static std::atomic<uint64_t> ready{0};  // devices (below 64) on which this instance has its attribute
+  const uint64_t bit = ctx->device < 64 ? 1ull << ctx->device : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, H::kSmem);
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "dense_linear attribute");
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const int grid = (int)std::min<long long>(ctx->num_sms, a.total);
+  cudaError_t e = launch_k(kern, grid, kThreads, H::kSmem, ctx->stream, true, false, map, a);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "dense_linear launch");
+  return COLI_OK;
+}
+
+template <bool BF16, int P>
+cudaError_t lay_out(coli_ctx* ctx, const DenseArgs& a, uint8_t* to) {
+  const long long chunks = (long long)a.S * ((a.I + 7) / 8);
+  const int grid = (int)std::min<long long>((chunks + 127) / 128, (long long)ctx->num_sms * 16);
+  return launch_k(dense_x_kernel<BF16, P>, grid, 128, 0, ctx->stream, true, false, a.x, a.x_stride, a.S, a.I, to);
 }
 
 }  // namespace
 
-cudaError_t launch_dense_pack(cudaStream_t stream, const uint16_t* src, int rows, int row0, int O, int I, uint8_t* w) {
-  dense_pack_kernel<<<1216, 256, 0, stream>>>(src, rows, row0, O, I, (I + kDenseCols - 1) / kDenseCols, w);
+cudaError_t launch_dense_pack(cudaStream_t stream, const uint16_t* src, int rows, int row0, int I, uint8_t* w) {
+  dense_pack_kernel<<<1216, 256, 0, stream>>>(src, rows, row0, I, (I + kDenseCols - 1) / kDenseCols, w);
   return cudaGetLastError();
 }
 
 int launch_dense(coli_ctx* ctx, const DenseArgs& args, int x_dtype, int y_dtype) {
-  DenseArgs a = args;
-  a.err = ctx->d_status;
+  TileArgs a{};
+  a.d = args;
+  a.d.err = ctx->d_status;
+  a.wait_ns = ctx->wait_ns ? ctx->wait_ns : kWaitLimitNs;
+  a.withhold = ctx->test_withhold > 0;
+  int rc = ensure_part(ctx);
+  if (rc != COLI_OK) return rc;
+  a.part = ctx->d_part;
+  a.count = ctx->d_dense_count;
+  const bool exact = y_dtype == COLI_DTYPE_F32;
+  const int parts = x_dtype == COLI_DTYPE_BF16 ? 1 : exact ? 3 : 2;
+  // rows of x by tiled copies where they lie, or from planes laid out in the workspace
+  const long long row = a.d.S == 1 ? (a.d.I + 7) / 8 * 8 : a.d.x_stride;
+  const bool direct = parts == 1 && (uintptr_t)a.d.x % 16 == 0 && row % 8 == 0;
+  if (!direct) {
+    rc = ensure_workspace(ctx, dense_x_bytes(a.d.S, a.d.I, parts));
+    if (rc != COLI_OK) return rc;
+  }
+  const int S = a.d.S;
+  const bool wide = parts == 1;  // a tile of 256 tokens leaves room for stages
+  const int N = S <= 16 ? 16 : S <= 32 ? 32 : S <= 64 ? 64 : S <= 128 || !wide ? 128 : 256;
+  CUtensorMap map;
+  if (direct)
+    rc = encode_rows_map(ctx, &map, const_cast<void*>(a.d.x), S, a.d.I, row, kDenseCols, N);
+  else
+    rc = encode_rows_map(ctx, &map, ctx->ws.base, (long long)parts * S, a.d.I, (a.d.I + 7) / 8 * 8, kDenseCols, N);
+  if (rc != COLI_OK) return rc;
+  if (a.withhold) ctx->test_withhold--;
   ProfScope prof(ctx, COLI_KERNEL_LINEAR);
-  const cudaError_t e = launch_k(dense_kernel, ctx->num_sms * 8, 256, 0, ctx->stream, true, false, a, x_dtype, y_dtype,
-                                 (a.I + kDenseCols - 1) / kDenseCols);
-  if (e != cudaSuccess) return cuda_fail(ctx, e, "dense_linear launch");
-  return COLI_OK;
+  if (!direct) {
+    uint8_t* to = reinterpret_cast<uint8_t*>(ctx->ws.base);
+    const cudaError_t e = parts == 1 ? lay_out<true, 1>(ctx, a.d, to) : parts == 2 ? lay_out<false, 2>(ctx, a.d, to) : lay_out<false, 3>(ctx, a.d, to);
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "dense_linear layout launch");
+  }
+  auto tokens = [&](auto p, auto y32) {
+    constexpr int P = decltype(p)::value;
+    constexpr bool E = decltype(y32)::value;
+    switch (N) {
+      case 16: return launch_one<16, P, E>(ctx, a, map);
+      case 32: return launch_one<32, P, E>(ctx, a, map);
+      case 64: return launch_one<64, P, E>(ctx, a, map);
+      case 128: return launch_one<128, P, E>(ctx, a, map);
+    }
+    if constexpr (P == 1) return launch_one<256, P, E>(ctx, a, map);
+    return COLI_E_INVAL;
+  };
+  if (parts == 3) return tokens(std::integral_constant<int, 3>{}, std::true_type{});
+  if (parts == 2) return tokens(std::integral_constant<int, 2>{}, std::false_type{});
+  if (exact) return tokens(std::integral_constant<int, 1>{}, std::true_type{});
+  return tokens(std::integral_constant<int, 1>{}, std::false_type{});
 }
 
 }  // namespace coli

@@ -31,8 +31,11 @@ struct DenseArgs {
   int* err;
 };
 
+// Workspace of a call that lays its activations out first: `parts` planes of S rows, each padded to 16 bytes.
+inline size_t dense_x_bytes(long long S, int I, int parts) { return (size_t)S * ((size_t)(I + 7) / 8 * 16) * parts; }
+
 // rows [row0, row0 + rows) of W [. x I], row-major at `src`, into the layout; row0 a multiple of kDenseRows.
-cudaError_t launch_dense_pack(cudaStream_t stream, const uint16_t* src, int rows, int row0, int O, int I, uint8_t* w);
+cudaError_t launch_dense_pack(cudaStream_t stream, const uint16_t* src, int rows, int row0, int I, uint8_t* w);
 int launch_dense(coli_ctx* ctx, const DenseArgs& a, int x_dtype, int y_dtype);
 
 }  // namespace coli

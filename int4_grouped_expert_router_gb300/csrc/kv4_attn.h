@@ -1081,10 +1081,10 @@ int launch_one(coli_ctx* ctx, AttnArgs& a, long long most_stages) {
   int grid = ctx->num_sms * C::kCtas;
   if (most_stages < grid) grid = (int)most_stages;
   if (grid > kKvCounters / 3) grid = kKvCounters / 3;
-  static_assert((size_t)2 * C::kCtas * C::kRows * (HD + 2) <= kKvPartFloats, "an SM's CTAs leave more than there is room for");
-  int rc = ensure_kv_part(ctx);
+  static_assert((size_t)2 * C::kCtas * C::kRows * (HD + 2) <= kPartFloats, "an SM's CTAs leave more than there is room for");
+  int rc = ensure_part(ctx);
   if (rc != COLI_OK) return rc;
-  a.part = ctx->d_kv_part;
+  a.part = ctx->d_part;
   auto kern = kv4_attn_kernel<HD, NG, NT, F32>;
   static std::atomic<uint64_t> ready{0};  // devices (below 64) on which this instance has its attribute
   const uint64_t bit = ctx->device < 64 ? 1ull << ctx->device : 0;

@@ -147,17 +147,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
-// One lane of a converged warp, the same in every call.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
-  return p != 0;
-}
-
-__device__ __forceinline__ uint64_t uniform(uint64_t v) {
-  return (uint64_t)__shfl_sync(0xffffffffu, (uint32_t)v, 0) | (uint64_t)__shfl_sync(0xffffffffu, (uint32_t)(v >> 32), 0) << 32;
-}
-
 // f16 A and B (K-major), f32 accumulator.
 __host__ __device__ constexpr uint32_t f16_f32_idesc(uint32_t M, uint32_t N) {
   return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
@@ -1066,10 +1055,10 @@ template <int HD, int NG>
 int launch_one(coli_ctx* ctx, TileArgs& a) {
   using T = Tile<HD, NG>;
   const int grid = ctx->num_sms < kKvCounters ? ctx->num_sms : kKvCounters;
-  static_assert((size_t)2 * kTileRows * (HD + 2) <= kKvPartFloats, "a CTA leaves more than there is room for");
-  int rc = ensure_kv_part(ctx);
+  static_assert((size_t)2 * kTileRows * (HD + 2) <= kPartFloats, "a CTA leaves more than there is room for");
+  int rc = ensure_part(ctx);
   if (rc != COLI_OK) return rc;
-  a.part = ctx->d_kv_part;
+  a.part = ctx->d_part;
   auto kern = kv4_tile_kernel<HD, NG>;
   static std::atomic<uint64_t> ready{0};  // devices (below 64) on which this instance has its attribute
   const uint64_t bit = ctx->device < 64 ? 1ull << ctx->device : 0;

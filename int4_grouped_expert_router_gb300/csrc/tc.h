@@ -54,6 +54,19 @@ __device__ __forceinline__ void tc_mma_bf16(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
+// One lane of a converged warp, the same in every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
+}
+
+// A value that is the same in the whole warp, made so visibly: it then lives in uniform registers, where the
+// instructions of the tensor core want their operands (about 45 cycles to issue one, 110 from plain registers).
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+  return (uint64_t)__shfl_sync(0xffffffffu, (uint32_t)v, 0) | (uint64_t)__shfl_sync(0xffffffffu, (uint32_t)(v >> 32), 0) << 32;
+}
+
 // Arrive on `bar` once every tcgen05 operation this thread issued before has completed.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
