@@ -5,8 +5,8 @@
 // so that one token keeps every SM streaming a contiguous run of W, and many tokens leave no part of a wave idle. A tile that
 // several CTAs share is joined by the one that arrives last, in CTA order, so results do not depend on who that is.
 //
-// One CTA, 12 warps: a producer (W by bulk copies, x by tiled ones, a ring of stages), a thread that issues the products, and
-// eight warps for what follows (bias, activation, factor, residual), which take a tile from tensor memory while the next one
+// One CTA, 20 warps: a producer (W by bulk copies, x by tiled ones, a ring of stages), a thread that issues the products, and
+// sixteen warps for what follows (bias, activation, factor, residual), which take a tile from tensor memory while the next one
 // is being formed in the other half of it. The ring is filled with weights before the work ahead in the stream is waited for.
 //
 // Sums. The tensor core cuts a sum off where binary32 would round it, always towards zero, and 6144 products leave 2^-17 that
@@ -26,9 +26,11 @@ namespace coli {
 namespace {
 
 constexpr float kInf = __builtin_huge_valf();
-constexpr int kThreads = 384;
-constexpr int kEpiWarps = 8, kWarpEpi = 4;  // warps 0 and 1: producer, products; a quarter of the lanes goes by warp % 4
-constexpr int kChunk = 4;                   // column tiles
+constexpr int kEpiWarps = 16, kWarpEpi = 4;  // warps 0 and 1: producer, products; a quarter of the lanes goes by warp % 4
+constexpr int kThreads = (kWarpEpi + kEpiWarps) * 32;
+constexpr int kChunk = 4;   // column tiles
+constexpr int kGroup = 8;   // tokens that a thread of the last warps takes at a time
+constexpr int kSets = kEpiWarps / 4;
 
 // P parts of x for a staged tile of W; kExact: y is binary32.
 template <int N, int P, bool EXACT>
@@ -38,8 +40,8 @@ struct Shape {
   static constexpr int kStages = std::min<uint32_t>(12, 224 * 1024 / kStage);
   static constexpr uint32_t kSmem = 1024 + kStages * kStage;
   static constexpr int kTmem = 2 * N;  // two accumulators; a power of two from 32 on
-  static constexpr int kGroups = N / 16;                    // of 16 tokens
-  static constexpr int kMine = (kGroups + 1) / 2;           // of a warp
+  static constexpr int kGroups = N / kGroup;
+  static constexpr int kMine = (kGroups + kSets - 1) / kSets;  // groups of a warp
 };
 
 struct TileArgs {
@@ -107,40 +109,49 @@ __global__ void dense_x_kernel(const void* x, long long stride, int S, int I, ui
   }
 }
 
-__device__ __forceinline__ void dense_act(float (&z)[16], int act) {
+__device__ __forceinline__ void dense_act(float (&z)[kGroup], int act) {
   switch (act) {
     case COLI_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < 16; i++) z[i] = z[i] / (1.f + expf(-z[i]));
+      for (int i = 0; i < kGroup; i++) z[i] = z[i] / (1.f + expf(-z[i]));
       break;
     case COLI_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < 16; i++) z[i] = 0.5f * z[i] * erfcf(z[i] * -0.70710678118654752f);
+      for (int i = 0; i < kGroup; i++) z[i] = 0.5f * z[i] * erfcf(z[i] * -0.70710678118654752f);
       break;
     case COLI_ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < 16; i++) z[i] = z[i] / (1.f + expf(-1.5957691216057308f * fmaf(0.044715f * z[i] * z[i], z[i], z[i])));
+      for (int i = 0; i < kGroup; i++) z[i] = z[i] / (1.f + expf(-1.5957691216057308f * fmaf(0.044715f * z[i] * z[i], z[i], z[i])));
       break;
     case COLI_ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < 16; i++) z[i] = z[i] < 0.f ? 0.f : z[i];
+      for (int i = 0; i < kGroup; i++) z[i] = z[i] < 0.f ? 0.f : z[i];
       break;
     case COLI_ACT_RELU2:
 #pragma unroll
-      for (int i = 0; i < 16; i++) z[i] = z[i] < 0.f ? 0.f : z[i] * z[i];
+      for (int i = 0; i < kGroup; i++) z[i] = z[i] < 0.f ? 0.f : z[i] * z[i];
       break;
   }
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t at, const float (&v)[16]) {
-  uint32_t r[16];
-#pragma unroll
-  for (int i = 0; i < 16; i++) r[i] = __float_as_uint(v[i]);
+// Eight consecutive columns of this thread's lane (see tmem_ld16).
+__device__ __forceinline__ void tmem_ld8(uint32_t at, float (&v)[8]) {
+  uint32_t r[8];
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
-      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(at)
       : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; i++) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t at, const float (&v)[8]) {
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) r[i] = __float_as_uint(v[i]);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(at)
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -282,46 +293,57 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   } else if (warp >= kWarpEpi) {
     // ------------------------------------- what follows -------------------------------------
     griddep_wait();
-    const int half = (warp - kWarpEpi) >> 2, row = (warp & 3) * 32 + lane;
+    const int set = (warp - kWarpEpi) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tm = tmem + ((uint32_t)(warp & 3) << 21);  // lanes 32 (warp % 4) on
     bool broken = false;
-    // 16 tokens of group g of a tile, from their sums on
-    auto finish = [&](float (&z)[16], int tile, int g) {
-      const int o = tile / a.nt * kDenseRows + row, t0 = tile % a.nt * N + g * 16;
-      if (o >= a.d.O || t0 >= a.d.S) return;
-      const int n = min(16, a.d.S - t0);
-      float f[16], q[16];
-      auto load = [&](const void* p, long long stride, float (&v)[16]) {
-        const size_t at = (size_t)t0 * stride + o;
+    // A tile's rows from this thread's, a group of tokens at a time. What is read beside the sums is asked for a group ahead.
+    struct Beside {
+      uint32_t f[kGroup], r[kGroup];
+    };
+    int o, t0;  // of the tile: this thread's row, the first token
+    auto ask = [&](Beside& v, int g) {
+      if (g >= H::kGroups || o >= a.d.O) return;
+      const int n = a.d.S - t0 - g * kGroup;
+      auto load = [&](const void* p, long long stride, uint32_t (&to)[kGroup]) {
+        const char* at = static_cast<const char*>(p) + ((size_t)(t0 + g * kGroup) * stride + o) * (EXACT ? 4 : 2);
+        const size_t step = (size_t)stride * (EXACT ? 4 : 2);
 #pragma unroll
-        for (int i = 0; i < 16; i++)
-          if (i < n)
-            v[i] = EXACT ? __ldcg(static_cast<const float*>(p) + at + i * stride)
-                         : bf16_to_f32(__ldcg(static_cast<const unsigned short*>(p) + at + i * stride));
+        for (int i = 0; i < kGroup; i++, at += step)
+          if (i < n) {
+            if constexpr (EXACT)
+              to[i] = __ldcg(reinterpret_cast<const unsigned int*>(at));
+            else
+              to[i] = __ldcg(reinterpret_cast<const unsigned short*>(at));
+          }
       };
-      if (a.d.mul) load(a.d.mul, a.d.mul_stride, f);
-      if (a.d.resid) load(a.d.resid, a.d.resid_stride, q);
-      const float b = a.d.bias ? __ldcg(a.d.bias + o) : 0.f;
+      if (a.d.mul) load(a.d.mul, a.d.mul_stride, v.f);
+      if (a.d.resid) load(a.d.resid, a.d.resid_stride, v.r);
+    };
+    auto value = [](uint32_t u) { return __uint_as_float(EXACT ? u : u << 16); };
+    auto finish = [&](float (&z)[kGroup], const Beside& v, int g, float bias) {
+      if (o >= a.d.O) return;
+      const int n = a.d.S - t0 - g * kGroup;
 #pragma unroll
-      for (int i = 0; i < 16; i++) {
+      for (int i = 0; i < kGroup; i++) {
         broken |= i < n && !(fabsf(z[i]) < kInf);
-        if (a.d.bias) z[i] += b;
+        z[i] += bias;
       }
       dense_act(z, a.d.act);
       if (a.d.mul)
 #pragma unroll
-        for (int i = 0; i < 16; i++) z[i] *= f[i];
+        for (int i = 0; i < kGroup; i++) z[i] *= value(v.f[i]);
       if (a.d.resid)
 #pragma unroll
-        for (int i = 0; i < 16; i++) z[i] += q[i];
-      const size_t at = (size_t)t0 * a.d.y_stride + o;
+        for (int i = 0; i < kGroup; i++) z[i] += value(v.r[i]);
+      char* at = static_cast<char*>(a.d.y) + ((size_t)(t0 + g * kGroup) * a.d.y_stride + o) * (EXACT ? 4 : 2);
+      const size_t step = (size_t)a.d.y_stride * (EXACT ? 4 : 2);
 #pragma unroll
-      for (int i = 0; i < 16; i++)
+      for (int i = 0; i < kGroup; i++, at += step)
         if (i < n) {
           if constexpr (EXACT)
-            static_cast<float*>(a.d.y)[at + i * a.d.y_stride] = z[i];
+            *reinterpret_cast<float*>(at) = z[i];
           else
-            static_cast<uint16_t*>(a.d.y)[at + i * a.d.y_stride] = f32_to_bf16_rn(z[i]);
+            *reinterpret_cast<uint16_t*>(at) = f32_to_bf16_rn(z[i]);
         }
     };
     uint32_t chunk = 0;
@@ -330,14 +352,12 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     while (w < w1) {
       const int seg = (int)min((long long)(a.kt - k), w1 - w);
       const bool whole = seg == a.kt;
-      // a tile's beginning goes to the CTA's second part, a continuation to its first
-      float* mine = a.part + ((size_t)2 * blockIdx.x + (k == 0)) * N * kDenseRows + row;
-      auto store = [&](const float (&z)[16], int g) {
-#pragma unroll
-        for (int i = 0; i < 16; i++) mine[(g * 16 + i) * kDenseRows] = z[i];
-      };
+      o = tile / a.nt * kDenseRows + row;
+      t0 = tile % a.nt * N;
+      const float bias = a.d.bias && o < a.d.O ? __ldcg(a.d.bias + o) : 0.f;
+      Beside next;
       if constexpr (EXACT) {
-        float sum[H::kMine][16] = {};
+        float sum[H::kMine][kGroup] = {};
 #pragma unroll 1
         for (int done = 0; done < seg; done += kChunk) {
           wait(&acc_full[chunk & 1], (chunk >> 1) & 1);
@@ -348,13 +368,13 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           if (last && done == 0) break;  // one chunk: it is where it is read from below
 #pragma unroll
           for (int m = 0; m < H::kMine; m++) {
-            const int g = 2 * m + half;
+            const int g = kSets * m + set;
             if (g >= H::kGroups) break;
-            float v[16];
-            tmem_ld16(acc + g * 16, v);
+            float v[kGroup];
+            tmem_ld8(acc + g * kGroup, v);
 #pragma unroll
-            for (int i = 0; i < 16; i++) sum[m][i] += v[i];
-            if (last) tmem_st16(acc + g * 16, sum[m]);
+            for (int i = 0; i < kGroup; i++) sum[m][i] += v[i];
+            if (last) tmem_st8(acc + g * kGroup, sum[m]);
           }
           if (last) break;
           tc_fence_before_sync();
@@ -362,26 +382,36 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           if (lane == 0) mbar_arrive(&acc_empty[chunk & 1]);
           chunk++;
         }
+        if (whole) ask(next, set);
         tmem_wait_st();
       } else {
+        if (whole) ask(next, set);
         wait(&acc_full[chunk & 1], (chunk >> 1) & 1);
         __syncwarp();
         tc_fence_after_sync();
       }
+      const uint32_t acc = tm + (chunk & 1) * N;
+      if (whole) {
 #pragma unroll 1
-      for (int g = half; g < H::kGroups; g += 2) {
-        float v[16];
-        tmem_ld16(tm + (chunk & 1) * N + g * 16, v);
-        if (whole)
-          finish(v, tile, g);
-        else
-          store(v, g);
-      }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[chunk & 1]);
-      chunk++;
-      if (!whole) {
+        for (int g = set; g < H::kGroups; g += kSets) {
+          float z[kGroup];
+          tmem_ld8(acc + g * kGroup, z);
+          const Beside now = next;
+          ask(next, g + kSets);
+          finish(z, now, g, bias);
+        }
+      } else {
+        // a tile's beginning goes to the CTA's second part, a continuation to its first; four tokens of a row together
+        constexpr size_t kPart = (size_t)(N / 4) * kDenseRows;
+        float4* parts = reinterpret_cast<float4*>(a.part) + row;
+        float4* mine = parts + ((size_t)2 * blockIdx.x + (k == 0)) * kPart;
+#pragma unroll 1
+        for (int g = set; g < H::kGroups; g += kSets) {
+          float z[kGroup];
+          tmem_ld8(acc + g * kGroup, z);
+#pragma unroll
+          for (int i = 0; i < 2; i++) __stcg(mine + (g * 2 + i) * kDenseRows, make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]));
+        }
         // the CTAs of this tile: from the one that begins it to the one that ends it
         const long long u0 = (long long)tile * a.kt, u1 = u0 + a.kt - 1;
         const int first = (int)(((u0 + 1) * gridDim.x - 1) / a.total), last = (int)(((u1 + 1) * gridDim.x - 1) / a.total);
@@ -394,22 +424,50 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         named_sync(1, kEpiWarps * 32);
         if (s_last) {
           __threadfence();
+          // in CTA order, its own sums from tensor memory; the first of the others' is asked for a group ahead, too
+          const int own = blockIdx.x, other = first == own ? first + 1 : first;
+          auto part_of = [&](int c, int g, int i) { return __ldcg(parts + ((size_t)2 * c + (c == first)) * kPart + (g * 2 + i) * kDenseRows); };
+          float4 p[2];
+          auto ask_part = [&](int g) {
+            if (g < H::kGroups)
+#pragma unroll
+              for (int i = 0; i < 2; i++) p[i] = part_of(other, g, i);
+          };
+          ask_part(set);
+          ask(next, set);
 #pragma unroll 1
-          for (int g = half; g < H::kGroups; g += 2) {
-            float z[16];
-            const float* p = a.part + ((size_t)2 * first + 1) * N * kDenseRows + g * 16 * kDenseRows + row;
+          for (int g = set; g < H::kGroups; g += kSets) {
+            float mine8[kGroup], z[kGroup];
+            tmem_ld8(acc + g * kGroup, mine8);
 #pragma unroll
-            for (int i = 0; i < 16; i++) z[i] = __ldcg(p + i * kDenseRows);
-            p += (size_t)N * kDenseRows;  // the first part of the CTA after
-#pragma unroll 2
-            for (int c = first + 1; c <= last; c++, p += (size_t)2 * N * kDenseRows)
+            for (int i = 0; i < 2; i++) z[4 * i] = p[i].x, z[4 * i + 1] = p[i].y, z[4 * i + 2] = p[i].z, z[4 * i + 3] = p[i].w;
+            if (first == own)
 #pragma unroll
-              for (int i = 0; i < 16; i++) z[i] += __ldcg(p + i * kDenseRows);
-            finish(z, tile, g);
+              for (int i = 0; i < kGroup; i++) z[i] += mine8[i];  // two terms: in either order the same
+            ask_part(g + kSets);
+            const Beside now = next;
+            ask(next, g + kSets);
+#pragma unroll 4
+            for (int c = other + 1; c <= last; c++) {
+              float4 v[2];
+              if (c != own)
+#pragma unroll
+                for (int i = 0; i < 2; i++) v[i] = part_of(c, g, i);
+              else
+#pragma unroll
+                for (int i = 0; i < 2; i++) v[i] = make_float4(mine8[4 * i], mine8[4 * i + 1], mine8[4 * i + 2], mine8[4 * i + 3]);
+#pragma unroll
+              for (int i = 0; i < 2; i++) z[4 * i] += v[i].x, z[4 * i + 1] += v[i].y, z[4 * i + 2] += v[i].z, z[4 * i + 3] += v[i].w;
+            }
+            finish(z, now, g, bias);
           }
         }
         named_sync(1, kEpiWarps * 32);  // s_last is read before it is written again
       }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[chunk & 1]);
+      chunk++;
       w += seg;
       k = 0;
       tile++;
