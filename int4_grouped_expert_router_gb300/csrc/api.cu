@@ -228,7 +228,7 @@ static int make_desc(coli_ctx* ctx, HostTensor& t) {
 }
 
 int encode_rows_map(coli_ctx* ctx, CUtensorMap* map, void* base, long long rows, int cols, long long stride, int box_cols,
-                    int box_rows) {
+                    int box_rows, bool swizzle) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return fail(ctx, COLI_E_CUDA, "cuTensorMapEncodeTiled unavailable");
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
@@ -236,13 +236,14 @@ int encode_rows_map(coli_ctx* ctx, CUtensorMap* map, void* base, long long rows,
   cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   cuuint32_t es[2] = {1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(ctx, COLI_E_CUDA, "activation tensor map encoding failed");
   return COLI_OK;
 }
 
 int encode_bf16_rows_map(coli_ctx* ctx, CUtensorMap* map, void* base, long long rows, int cols) {
-  return encode_rows_map(ctx, map, base, rows, cols, cols, 64, 16);
+  return encode_rows_map(ctx, map, base, rows, cols, cols, 64, 16, true);
 }
 
 }  // namespace coli
@@ -299,9 +300,9 @@ int coli_init(coli_ctx** out, int device, void* cuda_stream) {
   if ((e = cudaMalloc(&p, kKvCounters * sizeof(int))) != cudaSuccess) goto fail;
   ctx->d_kv_count = static_cast<int*>(p);
   if ((e = cudaMemset(ctx->d_kv_count, 0, kKvCounters * sizeof(int))) != cudaSuccess) goto fail;
-  if ((e = cudaMalloc(&p, ctx->num_sms * sizeof(int))) != cudaSuccess) goto fail;
+  if ((e = cudaMalloc(&p, ctx->num_sms * kDenseCounters * sizeof(int))) != cudaSuccess) goto fail;
   ctx->d_dense_count = static_cast<int*>(p);
-  if ((e = cudaMemset(ctx->d_dense_count, 0, ctx->num_sms * sizeof(int))) != cudaSuccess) goto fail;
+  if ((e = cudaMemset(ctx->d_dense_count, 0, ctx->num_sms * kDenseCounters * sizeof(int))) != cudaSuccess) goto fail;
   if ((e = cudaMalloc(&ctx->d_logprob, logprob_bytes(ctx->num_sms))) != cudaSuccess) goto fail;
   if ((e = cudaMemset(ctx->d_logprob, 0, logprob_bytes(ctx->num_sms))) != cudaSuccess) goto fail;
   if ((e = cudaMalloc(&ctx->d_router, kRouterScratchBytes)) != cudaSuccess) goto fail;
@@ -434,8 +435,8 @@ int coli_reserve(coli_ctx* ctx, int max_S, int max_E, int max_K, int max_D, int 
   // one-launch S == 1 FFN: a partial row of y per CTA
   const size_t stream = (size_t)ctx->num_sms * max_D * sizeof(float);
   if (stream > experts) experts = stream;
-  // 16-bit products: activations as up to three planes of 16-bit rows
-  const size_t planes = dense_x_bytes(max_S, std::max(max_D, max_I), 3);
+  // 16-bit products: activations as up to four planes of 16-bit rows
+  const size_t planes = dense_x_bytes(max_S, std::max(max_D, max_I), 4);
   if (planes > experts) experts = planes;
   const size_t slots = (size_t)COLI_MAX_ISSUES * max_S * max_D * sizeof(float);
   cudaSetDevice(ctx->device);
@@ -1111,6 +1112,11 @@ uint64_t coli_dense_upload(coli_ctx* ctx, const uint16_t* W, int O, int I) {
   t.w = static_cast<uint8_t*>(pw);
   t.O = O;
   t.I = I;
+  if (encode_rows_map(ctx, &t.map, pw, (long long)(dense_bytes(O, I) / (kDenseCols * 2)), kDenseCols, kDenseCols, kDenseCols, kDenseRows,
+                      false) != COLI_OK) {
+    cudaFree(pw);
+    return 0;
+  }
   ctx->dense.push_back(t);
   return (uint64_t)ctx->dense.size();
 }
@@ -1181,7 +1187,7 @@ int coli_dense_linear(coli_ctx* ctx, uint64_t W, const void* x, long long x_stri
   a.resid_stride = resid_stride;
   a.y_stride = y_stride;
   unsettle_x(ctx);
-  int rc = launch_dense(ctx, a, x_dtype, y_dtype);
+  int rc = launch_dense(ctx, a, t->map, x_dtype, y_dtype);
   if (rc == COLI_OK) ctx->compute_calls++;
   return rc;
 }

@@ -100,10 +100,14 @@ struct HostTensor {
   float* sT = nullptr;           // transposed chunk-group scales (desc.sT)
 };
 
+// Arrival counters of the 16-bit products, per CTA.
+constexpr int kDenseCounters = 4;
+
 // One uploaded 16-bit weight (coli_dense_upload): layout in dense.h.
 struct DenseTensor {
   uint8_t* w = nullptr;
   int O = 0, I = 0;
+  CUtensorMap map{};  // the tiles as rows of 64 columns, in boxes of a tile
 };
 
 struct Workspace {
@@ -156,7 +160,7 @@ struct coli_ctx {
   cudaStream_t settled_stream = nullptr;
   unsigned long long settled_capture = 0;
   int* d_kv_count = nullptr;  // coli::kKvCounters arrival counters of the cache attention, zero between calls
-  int* d_dense_count = nullptr;  // num_sms arrival counters of the 16-bit products, zero between calls
+  int* d_dense_count = nullptr;  // kDenseCounters per SM: arrival counters of the 16-bit products, zero between calls
   float* d_part = nullptr;  // num_sms x kPartFloats: one size for every call, so that captured calls keep their address
   std::vector<coli::DenseTensor> dense;  // handle = index + 1; w NULL: freed
   void* d_logprob = nullptr;  // what CTAs that share a row of logits leave for the one that ends it (logprobs.h), zero at first
@@ -214,9 +218,10 @@ int launch_prefill(coli_ctx* ctx, const void* x, int S, const int32_t* idx, cons
 // TMA map over a row-major bf16 matrix [rows x cols] read in 16-row x 64-column boxes with the
 // 128-byte swizzle (cols a multiple of 8).
 int encode_bf16_rows_map(coli_ctx* ctx, CUtensorMap* map, void* base, long long rows, int cols);
-// The same with rows `stride` elements apart (a multiple of 8, base 16-byte aligned), in boxes of box_rows x box_cols.
+// The same with rows `stride` elements apart (a multiple of 8, base 16-byte aligned), in boxes of box_rows x box_cols, with or
+// without the swizzle.
 int encode_rows_map(coli_ctx* ctx, CUtensorMap* map, void* base, long long rows, int cols, long long stride, int box_cols,
-                    int box_rows);
+                    int box_rows, bool swizzle);
 
 int launch_router_noalloc(coli_ctx* ctx, const void* x, int x_dtype, int S, int D, const float* Wr,
                           const float* bias, int E, int K, float topp, int norm_topk, float routed_scale, int shared,

@@ -15,6 +15,7 @@
 // rounded to 8), each multiplied with the same staged tile of W.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "dense.h"
@@ -31,15 +32,29 @@ constexpr int kThreads = (kWarpEpi + kEpiWarps) * 32;
 constexpr int kChunk = 4;   // column tiles
 constexpr int kGroup = 8;   // tokens that a thread of the last warps takes at a time
 constexpr int kSets = kEpiWarps / 4;
+constexpr int kQuad = 4;
+static_assert(kSets == kDenseCounters, "a counter for each set");
 
-// P parts of x for a staged tile of W; kExact: y is binary32.
-template <int N, int P, bool EXACT>
+// P parts of x for a staged tile of W, or kQuad: the parts of a token are four neighbouring rows of one tile (the last of them
+// 0), and their columns are added at the end. EXACT: y is binary32. PAIR: two CTAs of a cluster form 256 rows x N tokens with one
+// instruction (cta_group::2), each staging its 128 rows and half of the tokens.
+template <bool EXACT>
+constexpr int kPairTokens = EXACT ? 192 : 256;
+
+template <int N, int P, bool EXACT, bool PAIR>
 struct Shape {
-  static constexpr uint32_t kX = P * N * 128;
+  static constexpr int kCtas = PAIR ? 2 : 1;
+  static constexpr int kXRows = N / kCtas;
+  static constexpr int kPasses = P == kQuad ? 1 : P;
+  static constexpr int kTokens = P == kQuad ? N / kQuad : N;          // of a tile
+  static constexpr int kTake = P == kQuad ? kGroup / kQuad : kGroup;  // of a group
+  static constexpr uint32_t kX = kPasses * kXRows * 128;
   static constexpr uint32_t kStage = kDenseTile + kX;
   static constexpr int kStages = std::min<uint32_t>(12, 224 * 1024 / kStage);
   static constexpr uint32_t kSmem = 1024 + kStages * kStage;
-  static constexpr int kTmem = 2 * N;  // two accumulators; a power of two from 32 on
+  // Accumulators. Chunks of few products are formed faster than a round trip between the two sides takes.
+  static constexpr int kAccs = EXACT && N <= 128 ? 4 : 2;
+  static constexpr int kTmem = N == 192 ? 512 : kAccs * N;  // a power of two from 32 on
   static constexpr int kGroups = N / kGroup;
   static constexpr int kMine = (kGroups + kSets - 1) / kSets;  // groups of a warp
 };
@@ -47,10 +62,11 @@ struct Shape {
 struct TileArgs {
   DenseArgs d;
   int kt;       // column tiles
-  int nt;       // tiles of tokens
+  int rt;       // tiles of 128 rows, or 256 of a pair. A tile's number counts them first: the shares that have other tokens
+                // then walk through the same rows at the same time, and find them in L2
   long long total;
   bool stream;  // W is read once
-  float* part;  // per CTA two of [N][128]
+  float* part;  // per CTA two of [N / 4][128][4]
   int* count;   // per CTA, zero between calls
   uint64_t wait_ns;
   bool withhold;  // test hook: the call's first copy is withheld, and the waits on it give up
@@ -73,63 +89,81 @@ __global__ void dense_pack_kernel(const uint16_t* src, int rows, int row0, int I
   }
 }
 
-// x as planes of bf16 rows that start at 16-byte boundaries: itself, or its parts of 8 bits.
+// Eight elements of x from `at` on, of which those from `have` on are 0.
+__device__ __forceinline__ void dense_eight(const void* x, size_t at, int have, bool bf16, bool vec, float (&e)[8]) {
+  if (bf16) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) e[i] = i < have ? bf16_to_f32(__ldcg(static_cast<const unsigned short*>(x) + at + i)) : 0.f;
+  } else if (vec && have >= 8) {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const float4 q = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(x) + at) + i);
+      e[4 * i] = q.x, e[4 * i + 1] = q.y, e[4 * i + 2] = q.z, e[4 * i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++) e[i] = i < have ? __ldcg(static_cast<const float*>(x) + at + i) : 0.f;
+  }
+}
+
+// Them as P chunks of bf16: their parts of 8 bits. What is not finite stays what it is, in the first part alone.
+template <int P>
+__device__ __forceinline__ void dense_parts(float (&e)[8], uint32_t (&v)[P][4]) {
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+#pragma unroll
+    for (int p = 0; p < P; p++) {
+      const uint32_t u = __float_as_uint(e[i]);
+      const bool finite = (u & 0x7f800000u) != 0x7f800000u;
+      const uint32_t top = finite ? u & 0xffff0000u : (u & 0x7fffffu) ? 0x7fc00000u : u;
+      v[p][i / 2] = i & 1 ? v[p][i / 2] | top : top >> 16;
+      e[i] = finite ? e[i] - __uint_as_float(top) : 0.f;
+    }
+}
+
+// x as P planes of bf16 rows that start at 16-byte boundaries, or the parts of a row as kQuad rows of one plane.
 template <bool BF16, int P>
-__global__ void dense_x_kernel(const void* x, long long stride, int S, int I, uint8_t* to) {
+__global__ void dense_x_kernel(const void* x, long long stride, int S, int I, bool vec, uint8_t* to) {
   griddep_launch_dependents();
   griddep_wait();
   const int chunks = (I + 7) / 8;
   const long long n_all = (long long)S * chunks;
   for (long long n = (long long)blockIdx.x * blockDim.x + threadIdx.x; n < n_all; n += (long long)gridDim.x * blockDim.x) {
     const int s = (int)(n / chunks), i0 = (int)(n - (long long)s * chunks) * 8;
-    uint32_t v[P][4] = {};
-    const size_t at = (size_t)s * stride + i0;
+    float e[8];
+    uint32_t v[P][4];
+    dense_eight(x, (size_t)s * stride + i0, I - i0, BF16, vec, e);
+    dense_parts<P>(e, v);  // nothing is left for a fourth part
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      if (i0 + i >= I) break;
-      const int shift = 16 * (i & 1);
-      if constexpr (BF16) {
-        v[0][i / 2] |= (uint32_t)__ldcg(static_cast<const unsigned short*>(x) + at + i) << shift;
-      } else {
-        float rest = __ldcg(static_cast<const float*>(x) + at + i);
-#pragma unroll
-        for (int p = 0; p < P; p++) {
-          const uint32_t u = __float_as_uint(rest);
-          // what is not finite stays what it is, in the first part alone
-          const bool finite = (u & 0x7f800000u) != 0x7f800000u;
-          const uint32_t top = finite ? u & 0xffff0000u : (u & 0x7fffffu) ? 0x7fc00000u : u;
-          v[p][i / 2] |= (top >> 16) << shift;
-          rest = finite ? rest - __uint_as_float(top) : 0.f;
-        }
-      }
+    for (int p = 0; p < P; p++) {
+      const size_t at = P == kQuad ? n + (3ll * s + p) * chunks : p * n_all + n;
+      *reinterpret_cast<uint4*>(to + at * 16) = make_uint4(v[p][0], v[p][1], v[p][2], v[p][3]);
     }
-#pragma unroll
-    for (int p = 0; p < P; p++)
-      *reinterpret_cast<uint4*>(to + ((size_t)p * n_all + n) * 16) = make_uint4(v[p][0], v[p][1], v[p][2], v[p][3]);
   }
 }
 
-__device__ __forceinline__ void dense_act(float (&z)[kGroup], int act) {
+template <int N>
+__device__ __forceinline__ void dense_act(float (&z)[N], int act) {
   switch (act) {
     case COLI_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < kGroup; i++) z[i] = z[i] / (1.f + expf(-z[i]));
+      for (int i = 0; i < N; i++) z[i] = z[i] / (1.f + expf(-z[i]));
       break;
     case COLI_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < kGroup; i++) z[i] = 0.5f * z[i] * erfcf(z[i] * -0.70710678118654752f);
+      for (int i = 0; i < N; i++) z[i] = 0.5f * z[i] * erfcf(z[i] * -0.70710678118654752f);
       break;
     case COLI_ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < kGroup; i++) z[i] = z[i] / (1.f + expf(-1.5957691216057308f * fmaf(0.044715f * z[i] * z[i], z[i], z[i])));
+      for (int i = 0; i < N; i++) z[i] = z[i] / (1.f + expf(-1.5957691216057308f * fmaf(0.044715f * z[i] * z[i], z[i], z[i])));
       break;
     case COLI_ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < kGroup; i++) z[i] = z[i] < 0.f ? 0.f : z[i];
+      for (int i = 0; i < N; i++) z[i] = z[i] < 0.f ? 0.f : z[i];
       break;
     case COLI_ACT_RELU2:
 #pragma unroll
-      for (int i = 0; i < kGroup; i++) z[i] = z[i] < 0.f ? 0.f : z[i] * z[i];
+      for (int i = 0; i < N; i++) z[i] = z[i] < 0.f ? 0.f : z[i] * z[i];
       break;
   }
 }
@@ -155,34 +189,41 @@ __device__ __forceinline__ void tmem_st8(uint32_t at, const float (&v)[8]) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-template <int N, int P, bool EXACT>
-__global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constant__ CUtensorMap x_map, TileArgs a) {
-  using H = Shape<N, P, EXACT>;
+template <int N, int P, bool EXACT, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap w_map,
+                                                            TileArgs a) {
+  using H = Shape<N, P, EXACT, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);  // [kStages][W tile | P tiles of x]
-  __shared__ __align__(8) uint64_t full[H::kStages], empty[H::kStages], acc_full[2], acc_empty[2];
+  // Of a pair, `full` and `acc_empty` of the first CTA count for both.
+  __shared__ __align__(8) uint64_t full[H::kStages], empty[H::kStages], acc_full[H::kAccs], acc_empty[H::kAccs];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_last;
+  __shared__ int s_last[kSets];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = PAIR ? (int)cluster_ctarank() : 0;
+  const long long shares = gridDim.x / H::kCtas, share = blockIdx.x / H::kCtas;
   griddep_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < H::kStages; i++) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; i++) {
+    for (int i = 0; i < H::kAccs; i++) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], kEpiWarps);
+      mbar_init(&acc_empty[i], kEpiWarps * H::kCtas);
     }
     mbar_fence_init();
   }
-  if (warp == 1) tmem_alloc(&s_tmem, H::kTmem);
+  if (warp == 1) tmem_alloc_n<H::kCtas>(&s_tmem, H::kTmem);
   tc_fence_before_sync();
-  __syncthreads();
+  if constexpr (PAIR)
+    cluster_sync();
+  else
+    __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = s_tmem;
 
-  const long long w0 = a.total * blockIdx.x / gridDim.x, w1 = a.total * (blockIdx.x + 1) / gridDim.x;
+  const long long w0 = a.total * share / shares, w1 = a.total * (share + 1) / shares;
   const int tile0 = (int)(w0 / a.kt), k0 = (int)(w0 - (long long)tile0 * a.kt);
   bool alive = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -191,45 +232,63 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       alive = false;  // void from here on, but nothing hangs
     }
   };
+  const bool holds = a.withhold && share == 0;  // the first copy, in both CTAs of a pair
+  // the last arrivals on these barriers come before the CTA's memory goes, and with them the last reads of it
+  auto wait_for_products = [&]() {
+    const uint32_t units = (uint32_t)(w1 - w0);
+    for (uint32_t i = units > (uint32_t)H::kStages ? units - H::kStages : 0; i < units; i++)
+      mbar_wait(&empty[i % H::kStages], (i / H::kStages) & 1, a.wait_ns);
+  };
 
   if (warp == 0) {
     // ------------------------------------ producer ------------------------------------
     if (elect_one()) {
       const uint64_t once = l2_evict_first_policy();
       const uint32_t units = (uint32_t)(w1 - w0);
-      const uint8_t* w_at = a.d.w + ((size_t)(tile0 / a.nt) * a.kt + k0) * kDenseTile;  // of the next copy of W
-      int w_k = k0, w_n = tile0 % a.nt;
+      const uint32_t full0 = PAIR ? cluster_address(smem_u32(full), 0) : smem_u32(full);
+      struct At {
+        int k, n, rows;  // column tile, tile of tokens, 128 rows
+      };
+      auto advance = [&](At& at) {
+        if (++at.k < a.kt) return;
+        at.k = 0;
+        at.rows += H::kCtas;
+        if (at.rows < a.rt * H::kCtas) return;
+        at.rows = rank;
+        at.n++;
+      };
+      const At start{k0, tile0 / a.rt, tile0 % a.rt * H::kCtas + rank};
+      At w_at = start, x_at = start;
       auto copy_w = [&](uint32_t n) {
         const uint32_t s = n % H::kStages;
-        const bool held = a.withhold && n == 0 && blockIdx.x == 0;
-        if (!held) {
-          mbar_arrive_expect_tx(&full[s], H::kStage);
-          if (a.stream)
-            bulk_g2s_stream(smem + s * H::kStage, w_at, kDenseTile, &full[s], once);
-          else
-            bulk_g2s(smem + s * H::kStage, w_at, kDenseTile, &full[s]);
+        uint8_t* to = smem + s * H::kStage;
+        if (!(holds && n == 0)) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], H::kStage * H::kCtas);
+          if constexpr (PAIR) {
+            tma_load_2d_pair(to, &w_map, 0, (w_at.rows * a.kt + w_at.k) * kDenseRows, full0 + s * 8);
+          } else {
+            const uint8_t* from = a.d.w + ((size_t)w_at.rows * a.kt + w_at.k) * kDenseTile;
+            if (a.stream)
+              bulk_g2s_stream(to, from, kDenseTile, &full[s], once);
+            else
+              bulk_g2s(to, from, kDenseTile, &full[s]);
+          }
         }
-        w_at += kDenseTile;
-        if (++w_k == a.kt) {
-          w_k = 0;
-          if (++w_n == a.nt)
-            w_n = 0;
-          else
-            w_at -= (size_t)a.kt * kDenseTile;  // the same rows for the next tokens
-        }
+        advance(w_at);
       };
-      int x_k = k0, x_n = tile0 % a.nt;
       auto copy_x = [&](uint32_t n) {
         const uint32_t s = n % H::kStages;
-        const bool held = a.withhold && n == 0 && blockIdx.x == 0;
-        if (!held)
+        if (!(holds && n == 0))
 #pragma unroll
-          for (int p = 0; p < P; p++)
-            tma_load_2d(smem + s * H::kStage + kDenseTile + p * N * 128, &x_map, x_k * kDenseCols, p * a.d.S + x_n * N, &full[s]);
-        if (++x_k == a.kt) {
-          x_k = 0;
-          if (++x_n == a.nt) x_n = 0;
-        }
+          for (int p = 0; p < H::kPasses; p++) {
+            uint8_t* to = smem + s * H::kStage + kDenseTile + p * H::kXRows * 128;
+            const int y = p * a.d.S + x_at.n * N + rank * H::kXRows;
+            if constexpr (PAIR)
+              tma_load_2d_pair(to, &x_map, x_at.k * kDenseCols, y, full0 + s * 8);
+            else
+              tma_load_2d(to, &x_map, x_at.k * kDenseCols, y, &full[s]);
+          }
+        advance(x_at);
       };
       const uint32_t ahead = units < (uint32_t)H::kStages ? units : (uint32_t)H::kStages;
       for (uint32_t n = 0; n < ahead; n++) copy_w(n);  // weights do not depend on the work before this call
@@ -242,10 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         copy_w(n);
         copy_x(n);
       }
-      // no copy or product is in flight when the CTA ends, whatever has been given up
-      for (uint32_t i = n > (uint32_t)H::kStages ? n - H::kStages : 0; i < n; i++) {
-        if (!(a.withhold && i == 0 && blockIdx.x == 0)) mbar_wait(&full[i % H::kStages], (i / H::kStages) & 1, a.wait_ns);
-      }
+      // no copy is in flight when the CTA ends, whatever has been given up; of a pair the first CTA waits for both
+      if (rank == 0)
+        for (uint32_t i = n > (uint32_t)H::kStages ? n - H::kStages : 0; i < n; i++)
+          if (!(holds && i == 0)) mbar_wait(&full[i % H::kStages], (i / H::kStages) & 1, a.wait_ns);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -253,8 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     // operands in uniform registers
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t w_desc = uniform(sw128_kmajor_desc(smem)), x_desc = uniform(sw128_kmajor_desc(smem + kDenseTile));
-    if (elect_one()) {
-      constexpr uint32_t kId = bf16_f32_idesc(kDenseRows, N);
+    if (rank == 0 && elect_one()) {
+      constexpr uint32_t kId = bf16_f32_idesc(kDenseRows * H::kCtas, N);
       uint32_t s = 0, phase = 0, chunk = 0;
       int k = k0;
       long long w = w0;
@@ -262,32 +321,32 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         const int seg = (int)min((long long)(a.kt - k), w1 - w);
         for (int done = 0; done < seg;) {
           const int here = EXACT ? min(kChunk, seg - done) : seg;
-          wait(&acc_empty[chunk & 1], ((chunk >> 1) + 1) & 1);
+          wait(&acc_empty[chunk % H::kAccs], (chunk / H::kAccs + 1) & 1);
           tc_fence_after_sync();
-          const uint32_t acc = tm + (chunk & 1) * N;
+          const uint32_t acc = tm + chunk % H::kAccs * N;
           for (int i = 0; i < here; i++) {
             wait(&full[s], phase);
             tc_fence_after_sync();
             const uint32_t at = s * (H::kStage >> 4);  // a descriptor's address field counts 16 bytes
 #pragma unroll
-            for (int p = P - 1; p >= 0; p--)  // the small parts first
+            for (int p = H::kPasses - 1; p >= 0; p--)  // the small parts first
 #pragma unroll
               for (int kk = 0; kk < 4; kk++)
-                tc_mma_bf16(acc, w_desc + at + kk * 2, x_desc + at + p * (N * 8) + kk * 2, kId, i > 0 || p < P - 1 || kk > 0);
-            tc_commit(&empty[s]);
+                tc_mma_bf16_n<H::kCtas>(acc, w_desc + at + kk * 2, x_desc + at + p * (H::kXRows * 8) + kk * 2, kId,
+                                        i > 0 || p < H::kPasses - 1 || kk > 0);
+            tc_commit_n<H::kCtas>(&empty[s]);
             if (++s == (uint32_t)H::kStages) s = 0, phase ^= 1;
           }
-          tc_commit(&acc_full[chunk & 1]);
+          tc_commit_n<H::kCtas>(&acc_full[chunk % H::kAccs]);
           chunk++;
           done += here;
         }
         w += seg;
         k = 0;
       }
-      // the last arrivals on these barriers come before the CTA's memory goes
-      const uint32_t units = (uint32_t)(w1 - w0);
-      for (uint32_t i = units > (uint32_t)H::kStages ? units - H::kStages : 0; i < units; i++)
-        mbar_wait(&empty[i % H::kStages], (i / H::kStages) & 1, a.wait_ns);
+      wait_for_products();
+    } else if (PAIR && rank == 1 && elect_one()) {
+      wait_for_products();
     }
     __syncwarp();
   } else if (warp >= kWarpEpi) {
@@ -296,19 +355,27 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     const int set = (warp - kWarpEpi) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tm = tmem + ((uint32_t)(warp & 3) << 21);  // lanes 32 (warp % 4) on
     bool broken = false;
+    const uint32_t acc_empty0 = PAIR ? cluster_address(smem_u32(acc_empty), 0) : 0;
+    auto free_acc = [&](uint32_t i) {
+      if constexpr (PAIR)
+        mbar_arrive_cluster(acc_empty0 + i * 8);
+      else
+        mbar_arrive(&acc_empty[i]);
+    };
     // A tile's rows from this thread's, a group of tokens at a time. What is read beside the sums is asked for a group ahead.
+    constexpr int kTake = H::kTake;
     struct Beside {
-      uint32_t f[kGroup], r[kGroup];
+      uint32_t f[kTake], r[kTake];
     };
     int o, t0;  // of the tile: this thread's row, the first token
     auto ask = [&](Beside& v, int g) {
       if (g >= H::kGroups || o >= a.d.O) return;
-      const int n = a.d.S - t0 - g * kGroup;
-      auto load = [&](const void* p, long long stride, uint32_t (&to)[kGroup]) {
-        const char* at = static_cast<const char*>(p) + ((size_t)(t0 + g * kGroup) * stride + o) * (EXACT ? 4 : 2);
+      const int n = a.d.S - t0 - g * kTake;
+      auto load = [&](const void* p, long long stride, uint32_t (&to)[kTake]) {
+        const char* at = static_cast<const char*>(p) + ((size_t)(t0 + g * kTake) * stride + o) * (EXACT ? 4 : 2);
         const size_t step = (size_t)stride * (EXACT ? 4 : 2);
 #pragma unroll
-        for (int i = 0; i < kGroup; i++, at += step)
+        for (int i = 0; i < kTake; i++, at += step)
           if (i < n) {
             if constexpr (EXACT)
               to[i] = __ldcg(reinterpret_cast<const unsigned int*>(at));
@@ -320,25 +387,30 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       if (a.d.resid) load(a.d.resid, a.d.resid_stride, v.r);
     };
     auto value = [](uint32_t u) { return __uint_as_float(EXACT ? u : u << 16); };
-    auto finish = [&](float (&z)[kGroup], const Beside& v, int g, float bias) {
+    auto finish = [&](float (&sum)[kGroup], const Beside& v, int g, float bias) {
       if (o >= a.d.O) return;
-      const int n = a.d.S - t0 - g * kGroup;
+      const int n = a.d.S - t0 - g * kTake;
+      float z[kTake];
 #pragma unroll
-      for (int i = 0; i < kGroup; i++) {
+      for (int i = 0; i < kTake; i++) {
+        if constexpr (P == kQuad)
+          z[i] = (sum[4 * i + 2] + sum[4 * i + 1]) + sum[4 * i];
+        else
+          z[i] = sum[i];
         broken |= i < n && !(fabsf(z[i]) < kInf);
         z[i] += bias;
       }
       dense_act(z, a.d.act);
       if (a.d.mul)
 #pragma unroll
-        for (int i = 0; i < kGroup; i++) z[i] *= value(v.f[i]);
+        for (int i = 0; i < kTake; i++) z[i] *= value(v.f[i]);
       if (a.d.resid)
 #pragma unroll
-        for (int i = 0; i < kGroup; i++) z[i] += value(v.r[i]);
-      char* at = static_cast<char*>(a.d.y) + ((size_t)(t0 + g * kGroup) * a.d.y_stride + o) * (EXACT ? 4 : 2);
+        for (int i = 0; i < kTake; i++) z[i] += value(v.r[i]);
+      char* at = static_cast<char*>(a.d.y) + ((size_t)(t0 + g * kTake) * a.d.y_stride + o) * (EXACT ? 4 : 2);
       const size_t step = (size_t)a.d.y_stride * (EXACT ? 4 : 2);
 #pragma unroll
-      for (int i = 0; i < kGroup; i++, at += step)
+      for (int i = 0; i < kTake; i++, at += step)
         if (i < n) {
           if constexpr (EXACT)
             *reinterpret_cast<float*>(at) = z[i];
@@ -352,18 +424,18 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     while (w < w1) {
       const int seg = (int)min((long long)(a.kt - k), w1 - w);
       const bool whole = seg == a.kt;
-      o = tile / a.nt * kDenseRows + row;
-      t0 = tile % a.nt * N;
+      o = (tile % a.rt * H::kCtas + rank) * kDenseRows + row;
+      t0 = tile / a.rt * H::kTokens;
       const float bias = a.d.bias && o < a.d.O ? __ldcg(a.d.bias + o) : 0.f;
       Beside next;
       if constexpr (EXACT) {
         float sum[H::kMine][kGroup] = {};
 #pragma unroll 1
         for (int done = 0; done < seg; done += kChunk) {
-          wait(&acc_full[chunk & 1], (chunk >> 1) & 1);
+          wait(&acc_full[chunk % H::kAccs], chunk / H::kAccs & 1);
           __syncwarp();
           tc_fence_after_sync();
-          const uint32_t acc = tm + (chunk & 1) * N;
+          const uint32_t acc = tm + chunk % H::kAccs * N;
           const bool last = done + kChunk >= seg;
           if (last && done == 0) break;  // one chunk: it is where it is read from below
 #pragma unroll
@@ -379,18 +451,18 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           if (last) break;
           tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[chunk & 1]);
+          if (lane == 0) free_acc(chunk % H::kAccs);
           chunk++;
         }
-        if (whole) ask(next, set);
         tmem_wait_st();
+        if (whole) ask(next, set);
       } else {
         if (whole) ask(next, set);
-        wait(&acc_full[chunk & 1], (chunk >> 1) & 1);
+        wait(&acc_full[chunk % H::kAccs], chunk / H::kAccs & 1);
         __syncwarp();
         tc_fence_after_sync();
       }
-      const uint32_t acc = tm + (chunk & 1) * N;
+      const uint32_t acc = tm + chunk % H::kAccs * N;
       if (whole) {
 #pragma unroll 1
         for (int g = set; g < H::kGroups; g += kSets) {
@@ -412,21 +484,23 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
 #pragma unroll
           for (int i = 0; i < 2; i++) __stcg(mine + (g * 2 + i) * kDenseRows, make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]));
         }
-        // the CTAs of this tile: from the one that begins it to the one that ends it
+        // the shares of this tile: from the one that begins it to the one that ends it. The four warps of a set, which hold
+        // all rows of their tokens, join them on their own.
         const long long u0 = (long long)tile * a.kt, u1 = u0 + a.kt - 1;
-        const int first = (int)(((u0 + 1) * gridDim.x - 1) / a.total), last = (int)(((u1 + 1) * gridDim.x - 1) / a.total);
+        const int first = (int)(((u0 + 1) * shares - 1) / a.total), last = (int)(((u1 + 1) * shares - 1) / a.total);
         __threadfence();
-        named_sync(1, kEpiWarps * 32);
-        if (tid == kWarpEpi * 32) {
-          s_last = atomicAdd(a.count + first, 1) == last - first;
-          if (s_last) a.count[first] = 0;
+        named_sync(1 + set, 128);
+        if ((tid & 127) == 0) {
+          int* count = a.count + (first * H::kCtas + rank) * kSets + set;
+          s_last[set] = atomicAdd(count, 1) == last - first;
+          if (s_last[set]) *count = 0;
         }
-        named_sync(1, kEpiWarps * 32);
-        if (s_last) {
+        named_sync(1 + set, 128);
+        if (s_last[set]) {
           __threadfence();
           // in CTA order, its own sums from tensor memory; the first of the others' is asked for a group ahead, too
-          const int own = blockIdx.x, other = first == own ? first + 1 : first;
-          auto part_of = [&](int c, int g, int i) { return __ldcg(parts + ((size_t)2 * c + (c == first)) * kPart + (g * 2 + i) * kDenseRows); };
+          const int own = (int)share, other = first == own ? first + 1 : first;
+          auto part_of = [&](int c, int g, int i) { return __ldcg(parts + ((size_t)2 * (c * H::kCtas + rank) + (c == first)) * kPart + (g * 2 + i) * kDenseRows); };
           float4 p[2];
           auto ask_part = [&](int g) {
             if (g < H::kGroups)
@@ -462,11 +536,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
             finish(z, now, g, bias);
           }
         }
-        named_sync(1, kEpiWarps * 32);  // s_last is read before it is written again
+        named_sync(1 + set, 128);  // s_last is read before it is written again
       }
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[chunk & 1]);
+      if (lane == 0) free_acc(chunk % H::kAccs);
       chunk++;
       w += seg;
       k = 0;
@@ -475,20 +549,27 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     if (broken) set_error(a.d.err, COLI_E_NONFINITE);
   }
   tc_fence_before_sync();
-  __syncthreads();
+  if constexpr (PAIR)
+    cluster_sync();
+  else
+    __syncthreads();
   tc_fence_after_sync();
-  if (warp == 1) tmem_dealloc(tmem, H::kTmem);
+  if (warp == 1) tmem_dealloc_n<H::kCtas>(tmem, H::kTmem);
 }
 
-template <int N, int P, bool EXACT>
-int launch_one(coli_ctx* ctx, TileArgs& a, const CUtensorMap& map) {
-  using H = Shape<N, P, EXACT>;
+template <int N, int P, bool EXACT, bool PAIR>
+int launch_one(coli_ctx* ctx, TileArgs& a, const CUtensorMap& x_map, const CUtensorMap& w_map) {
+  using H = Shape<N, P, EXACT, PAIR>;
   static_assert((size_t)2 * N * kDenseRows <= kPartFloats, "a CTA leaves more than there is room for");
   a.kt = (a.d.I + kDenseCols - 1) / kDenseCols;
-  a.nt = (a.d.S + N - 1) / N;
-  a.total = (long long)((a.d.O + kDenseRows - 1) / kDenseRows) * a.nt * a.kt;
-  a.stream = a.nt == 1;
-  auto kern = dense_kernel<N, P, EXACT>;
+  const int rows = kDenseRows * H::kCtas, nt = (a.d.S + H::kTokens - 1) / H::kTokens;
+  a.rt = (a.d.O + rows - 1) / rows;
+  a.total = (long long)a.rt * nt * a.kt;
+  a.stream = nt == 1;
+  // Where the weight is larger than L2 and a few tiles of tokens read it, they do so in step: as many shares for each.
+  int shares = ctx->num_sms / H::kCtas;
+  if (nt > 1 && nt <= 8 && dense_bytes(a.d.O, a.d.I) > ((size_t)96 << 20)) shares = shares / nt * nt;
+  auto kern = dense_kernel<N, P, EXACT, PAIR>;
   static std::atomic<uint64_t> ready{0};  // devices (below 64) on which this instance has its attribute
   const uint64_t bit = ctx->device < 64 ? 1ull << ctx->device : 0;
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
@@ -496,17 +577,50 @@ int launch_one(coli_ctx* ctx, TileArgs& a, const CUtensorMap& map) {
     if (e != cudaSuccess) return cuda_fail(ctx, e, "dense_linear attribute");
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  const int grid = (int)std::min<long long>(ctx->num_sms, a.total);
-  cudaError_t e = launch_k(kern, grid, kThreads, H::kSmem, ctx->stream, true, false, map, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<long long>(shares, a.total) * H::kCtas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = H::kSmem;
+  cfg.stream = ctx->stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = H::kCtas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, x_map, w_map, a);
   if (e != cudaSuccess) return cuda_fail(ctx, e, "dense_linear launch");
   return COLI_OK;
 }
 
+// Tokens of a tile, kPair for pairs of CTAs: what takes the fewest cycles by what was measured on O, I of 768 to 50021 and S
+// to 2048. A column tile takes its bytes from L2 at 64 a cycle, or its products; a shared tile takes 30 N cycles and 17 N for
+// every share of it but one. (O = I = 6144, 256 tokens: 64 a tile 34.8 us, 128 32.5, pairs 35.1; O = 2048: 17.3, 21.7, 37.5;
+// 1024 tokens: 100.5, 73.0, 63.7 and 38.5, 29.8, 36.4.)
+constexpr int kPair = 256;
+int dense_tokens(int S, int O, int I, int parts, bool exact, int num_sms) {
+  if (S <= 16) return 16;
+  const double kt = (I + kDenseCols - 1) / kDenseCols;
+  int best = 32;
+  double least = 0;
+  for (int N : {32, 64, 128, kPair}) {
+    const int ctas = N == kPair ? 2 : 1, tokens = N < kPair ? N : exact ? kPairTokens<true> : kPairTokens<false>;
+    const double tiles = (double)((O + kDenseRows * ctas - 1) / (kDenseRows * ctas)) * ((S + tokens - 1) / tokens);
+    const double shares = std::min<double>(num_sms / ctas, tiles * kt);
+    const double unit = std::max((kDenseTile + parts * tokens / ctas * 128.0) / 64 + 16, parts * tokens * 2.0 + 80);
+    const double cycles = tiles * kt / shares * unit + tokens * (30 + 17 * std::max(1.0, std::ceil(shares / tiles)));
+    if (N == 32 || cycles < least) best = N, least = cycles;
+  }
+  return best;
+}
+
 template <bool BF16, int P>
-cudaError_t lay_out(coli_ctx* ctx, const DenseArgs& a, uint8_t* to) {
+cudaError_t lay_out(coli_ctx* ctx, const DenseArgs& a, bool vec, uint8_t* to) {
   const long long chunks = (long long)a.S * ((a.I + 7) / 8);
   const int grid = (int)std::min<long long>((chunks + 127) / 128, (long long)ctx->num_sms * 16);
-  return launch_k(dense_x_kernel<BF16, P>, grid, 128, 0, ctx->stream, true, false, a.x, a.x_stride, a.S, a.I, to);
+  return launch_k(dense_x_kernel<BF16, P>, grid, 128, 0, ctx->stream, true, false, a.x, a.x_stride, a.S, a.I, vec, to);
 }
 
 }  // namespace
@@ -516,7 +630,7 @@ cudaError_t launch_dense_pack(cudaStream_t stream, const uint16_t* src, int rows
   return cudaGetLastError();
 }
 
-int launch_dense(coli_ctx* ctx, const DenseArgs& args, int x_dtype, int y_dtype) {
+int launch_dense(coli_ctx* ctx, const DenseArgs& args, const CUtensorMap& w_map, int x_dtype, int y_dtype) {
   TileArgs a{};
   a.d = args;
   a.d.err = ctx->d_status;
@@ -527,42 +641,44 @@ int launch_dense(coli_ctx* ctx, const DenseArgs& args, int x_dtype, int y_dtype)
   a.part = ctx->d_part;
   a.count = ctx->d_dense_count;
   const bool exact = y_dtype == COLI_DTYPE_F32;
-  const int parts = x_dtype == COLI_DTYPE_BF16 ? 1 : exact ? 3 : 2;
+  const int parts = x_dtype == COLI_DTYPE_BF16 ? 1 : !exact ? 2 : a.d.S <= kQuad ? kQuad : 3;
   // rows of x by tiled copies where they lie, or from planes laid out in the workspace
   const long long row = a.d.S == 1 ? (a.d.I + 7) / 8 * 8 : a.d.x_stride;
   const bool direct = parts == 1 && (uintptr_t)a.d.x % 16 == 0 && row % 8 == 0;
-  if (!direct) {
-    rc = ensure_workspace(ctx, dense_x_bytes(a.d.S, a.d.I, parts));
-    if (rc != COLI_OK) return rc;
-  }
   const int S = a.d.S;
-  const bool wide = parts == 1;  // a tile of 256 tokens leaves room for stages
-  const int N = S <= 16 ? 16 : S <= 32 ? 32 : S <= 64 ? 64 : S <= 128 || !wide ? 128 : 256;
-  CUtensorMap map;
-  if (direct)
-    rc = encode_rows_map(ctx, &map, const_cast<void*>(a.d.x), S, a.d.I, row, kDenseCols, N);
-  else
-    rc = encode_rows_map(ctx, &map, ctx->ws.base, (long long)parts * S, a.d.I, (a.d.I + 7) / 8 * 8, kDenseCols, N);
+  const int N = dense_tokens(S, a.d.O, a.d.I, parts, exact, ctx->num_sms);
+  const int box = N < kPair ? N : (exact ? kPairTokens<true> : kPairTokens<false>) / 2;
+  CUtensorMap map{};
+  if (direct) {
+    rc = encode_rows_map(ctx, &map, const_cast<void*>(a.d.x), S, a.d.I, row, kDenseCols, box, true);
+  } else {
+    rc = ensure_workspace(ctx, dense_x_bytes(S, a.d.I, parts));
+    if (rc == COLI_OK) rc = encode_rows_map(ctx, &map, ctx->ws.base, (long long)parts * S, a.d.I, (a.d.I + 7) / 8 * 8, kDenseCols, box, true);
+  }
   if (rc != COLI_OK) return rc;
   if (a.withhold) ctx->test_withhold--;
   ProfScope prof(ctx, COLI_KERNEL_LINEAR);
   if (!direct) {
     uint8_t* to = reinterpret_cast<uint8_t*>(ctx->ws.base);
-    const cudaError_t e = parts == 1 ? lay_out<true, 1>(ctx, a.d, to) : parts == 2 ? lay_out<false, 2>(ctx, a.d, to) : lay_out<false, 3>(ctx, a.d, to);
+    const bool vec = (uintptr_t)a.d.x % 16 == 0 && row % 4 == 0;
+    const cudaError_t e = parts == 1   ? lay_out<true, 1>(ctx, a.d, false, to)
+                          : parts == 2 ? lay_out<false, 2>(ctx, a.d, vec, to)
+                          : parts == 3 ? lay_out<false, 3>(ctx, a.d, vec, to)
+                                       : lay_out<false, kQuad>(ctx, a.d, vec, to);
     if (e != cudaSuccess) return cuda_fail(ctx, e, "dense_linear layout launch");
   }
   auto tokens = [&](auto p, auto y32) {
     constexpr int P = decltype(p)::value;
     constexpr bool E = decltype(y32)::value;
     switch (N) {
-      case 16: return launch_one<16, P, E>(ctx, a, map);
-      case 32: return launch_one<32, P, E>(ctx, a, map);
-      case 64: return launch_one<64, P, E>(ctx, a, map);
-      case 128: return launch_one<128, P, E>(ctx, a, map);
+      case 16: return launch_one<16, P, E, false>(ctx, a, map, w_map);
+      case 32: return launch_one<32, P, E, false>(ctx, a, map, w_map);
+      case 64: return launch_one<64, P, E, false>(ctx, a, map, w_map);
+      case 128: return launch_one<128, P, E, false>(ctx, a, map, w_map);
     }
-    if constexpr (P == 1) return launch_one<256, P, E>(ctx, a, map);
-    return COLI_E_INVAL;
+    return launch_one<kPairTokens<E>, P, E, true>(ctx, a, map, w_map);
   };
+  if (parts == kQuad) return launch_one<16, kQuad, true, false>(ctx, a, map, w_map);
   if (parts == 3) return tokens(std::integral_constant<int, 3>{}, std::true_type{});
   if (parts == 2) return tokens(std::integral_constant<int, 2>{}, std::false_type{});
   if (exact) return tokens(std::integral_constant<int, 1>{}, std::true_type{});

@@ -31,11 +31,12 @@ struct DenseArgs {
   int* err;
 };
 
-// Workspace of a call that lays its activations out first: `parts` planes of S rows, each padded to 16 bytes.
+// Workspace of a call that lays its activations out first: `parts` planes (up to 4) of S rows, each padded to 16 bytes.
 inline size_t dense_x_bytes(long long S, int I, int parts) { return (size_t)S * ((size_t)(I + 7) / 8 * 16) * parts; }
 
 // rows [row0, row0 + rows) of W [. x I], row-major at `src`, into the layout; row0 a multiple of kDenseRows.
 cudaError_t launch_dense_pack(cudaStream_t stream, const uint16_t* src, int rows, int row0, int I, uint8_t* w);
-int launch_dense(coli_ctx* ctx, const DenseArgs& a, int x_dtype, int y_dtype);
+// w_map: the weight's tiles as rows of 64, in boxes of a tile.
+int launch_dense(coli_ctx* ctx, const DenseArgs& a, const CUtensorMap& w_map, int x_dtype, int y_dtype);
 
 }  // namespace coli

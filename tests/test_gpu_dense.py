@@ -281,3 +281,82 @@ def test_refusals(ctx):
     with pytest.raises(B.ColiError):
         B.coli_dense_free(ctx, h)
     assert B.coli_check_error(ctx) == 0
+
+
+@pytest.mark.parametrize("x_dtype,y", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("S,I,O_", [(60, 1030, 4001), (300, 320, 6100), (600, 700, 4000), (2100, 1030, 5001), (700, 2050, 12001),
+                                    (260, 6144, 9001)])
+def test_every_tile_of_tokens(ctx, S, I, O_, x_dtype, y):
+    """Sizes at which tiles of 32, 64, 128 tokens and pairs of CTAs are chosen, shared by CTAs or not, and a weight larger than
+    L2 that two tiles of tokens read in step. In norm: see close(); a bf16 result rounds to 2^-9 on average."""
+    g = torch.Generator(device="cuda").manual_seed(S)
+    W = (0.05 * torch.randn(O_, I, device="cuda", generator=g)).bfloat16()
+    x = torch.randn(S, I, device="cuda", generator=g).to(DT[x_dtype])
+    bias, resid = torch.randn(O_, device="cuda", generator=g), torch.randn(S, O_, device="cuda", generator=g).to(DT[y])
+    guard = torch.full((S + 2, O_), 7.0, dtype=DT[y], device="cuda")
+    h = B.coli_dense_upload(ctx, W)
+    B.coli_dense_linear(ctx, h, x, guard[1:-1], bias=bias, act="relu", resid=resid)
+    assert B.coli_check_error(ctx) == 0
+    want = torch.relu(x.double() @ W.double().t() + bias.double()) + resid.double()
+    off = guard[1:-1].double() - want
+    assert off.norm() <= (4e-6 if y == "f32" else 2.0 ** -8) * want.norm()
+    size = x.double().abs() @ W.double().abs().t() + bias.abs().double()
+    steps = I / 16 * (3 if x_dtype == "f32" else 1) + 64
+    assert ((off.abs() - size * steps * 2.0 ** -23 - want.abs() * (2.0 ** -8 if y == "bf16" else 2.0 ** -23)) <= 0).all()
+    assert (guard[0] == 7).all() and (guard[-1] == 7).all()
+    again = torch.empty_like(guard[1:-1])
+    B.coli_dense_linear(ctx, h, x, again, bias=bias, act="relu", resid=resid)
+    assert torch.equal(again, guard[1:-1])
+    B.coli_dense_free(ctx, h)
+
+
+@pytest.mark.parametrize("S,I,O_,x_dtype", [(1, 2048, 3000, "bf16"), (1, 64, 100, "bf16"), (3, 2048, 3000, "f32"), (60, 1030, 4001, "f32"),
+                                            (2100, 1030, 5001, "bf16")])
+def test_a_copy_that_never_comes_ends_the_waits(S, I, O_, x_dtype):
+    """A copy is withheld once: the waits on it give up, the call reports it, and the next one is healthy."""
+    c = Ctx.with_env(COLI_TEST_WAIT_NS=20_000_000, COLI_TEST_WITHHOLD=1)
+    try:
+        g = torch.Generator(device="cuda").manual_seed(S)
+        W = (0.05 * torch.randn(O_, I, device="cuda", generator=g)).bfloat16()
+        x = torch.randn(S, I, device="cuda", generator=g).to(DT[x_dtype])
+        y = torch.empty(S, O_, device="cuda")
+        h = B.coli_dense_upload(c.ctx, W)
+        B.coli_dense_linear(c.ctx, h, x, y)
+        assert B.coli_check_error(c.ctx) == B.COLI_E_TIMEOUT
+        for _ in range(2):
+            B.coli_dense_linear(c.ctx, h, x, y)
+            assert B.coli_check_error(c.ctx) == 0
+            want = x.double() @ W.double().t()
+            assert (y - want).norm() <= 4e-6 * want.norm()
+    finally:
+        c.close()
+
+
+def test_reserve_is_enough_and_moves_nothing():
+    """After coli_reserve a captured product outlives larger ones: nothing is allocated, nothing moves."""
+    c = Ctx()
+    try:
+        B.coli_reserve(c.ctx, 300, 16, 4, 2048, 512)
+        x = torch.randn(40, 1000, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+        _, h = weight(c.ctx, 700, 1000)
+        _, big = weight(c.ctx, 600, 2048)
+        y, z, xb = torch.empty(40, 700, device="cuda"), torch.empty(300, 600, device="cuda"), torch.randn(300, 2048, device="cuda")
+        B.coli_dense_linear(c.ctx, h, x, y)
+        first = y.clone()
+        stream, before, graph = torch.cuda.Stream(), torch.cuda.current_stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            B.coli_set_stream(c.ctx, stream)
+            B.coli_dense_linear(c.ctx, h, x, y)
+        B.coli_set_stream(c.ctx, before)
+        B.coli_dense_linear(c.ctx, big, xb, z)
+        torch.cuda.synchronize()
+        free = torch.cuda.mem_get_info()[0]
+        B.coli_dense_linear(c.ctx, big, xb, z)
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, first) and torch.cuda.mem_get_info()[0] == free
+        assert B.coli_check_error(c.ctx) == 0
+    finally:
+        c.close()
