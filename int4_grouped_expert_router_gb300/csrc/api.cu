@@ -1202,7 +1202,7 @@ int coli_logprobs(coli_ctx* ctx, const void* logits, long long stride, int dtype
     return fail(ctx, COLI_E_INVAL, "logprobs: tokens and logp come together, with their number n");
   if ((top_id != nullptr) != (top_logp != nullptr) || (top_id ? k < 1 || k > COLI_MAX_TOP : k != 0))
     return fail(ctx, COLI_E_INVAL, "logprobs: top_id and top_logp come together, with their number k");
-  if (!(scale > 0.f) || !(scale <= 1e30f)) return fail(ctx, COLI_E_INVAL, "logprobs: scale must be above 0 and at most 1e30");
+  if (!(scale >= 1e-30f) || !(scale <= 1e30f)) return fail(ctx, COLI_E_INVAL, "logprobs: scale must lie between 1e-30 and 1e30");
   if (S == 1) stride = V;  // of one row it says nothing
   if (stride < V) return fail(ctx, COLI_E_INVAL, "logprobs: row stride below V");
   if ((uintptr_t)logits % (dtype == COLI_DTYPE_F32 ? 4 : 2) != 0 ||

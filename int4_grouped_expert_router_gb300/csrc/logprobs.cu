@@ -1,14 +1,16 @@
 // Log probabilities: a row's log-sum-exp, entropy and largest entries in one pass over its logits.
 //
 // Bound by memory: every logit is read once. A CTA takes a row, or a part of one where there are few rows; the last CTA of a
-// row to arrive joins the parts, in their order. A thread keeps the maximum m of what it has seen, s = sum e^(x - m) and
-// t = sum (x - m) e^(x - m) (entropy = log s - t / s), and moves them when m grows.
+// row to arrive joins the parts, in their order. A thread keeps s = sum e^(x - b) and t = sum (x - b) e^(x - b) (entropy =
+// log s - t / s, relative to the base b) for two streams of entries at a time, which the packed instructions take together. The
+// base follows the largest entry with a slack of 2^16, so that it hardly ever moves.
 //
 // The largest entries cost the pass nothing but the place of each thread's maximum. An entry's key is its value with its index
-// below, so keys never tie and the lower index wins. The maxima of 32 groups of threads are 32 entries, so the k-th largest of
-// them is a bound that k entries reach at least; only threads whose own maximum reaches it look through their entries again
-// (out of L2), and what they find, about k ln k entries, is ranked by comparison with one another. Where ties make it more
-// than there is room for, the k-th largest of those found is a higher bound of the same kind, and the search repeats.
+// below, so keys never tie and the lower index wins. The maxima of 64 groups of threads are 64 entries, so the k-th largest of
+// them is a bound that k entries reach at least; only entries of threads whose own maximum reaches it are looked through again
+// (out of L2, all threads together), and what is found, about k ln k entries, is ranked by comparison with one another.
+// Where ties make it more than there is room for, the k-th largest of those found is a higher bound of the same kind, and the
+// search repeats.
 #include "logprobs.h"
 #include "pipe.h"
 
@@ -16,15 +18,17 @@ namespace coli {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRoom = kLogprobMostParts * COLI_MAX_TOP;  // entries that reach the bound
-constexpr int kUnroll = 4;   // vectors of a thread in flight
+constexpr int kFlight = 6;   // vectors of a thread on their way
+constexpr int kGroups = 64, kPerGroup = kThreads / kGroups;  // groups of threads whose maxima make the bound
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // 2^y is 0 in binary32 below this, and y 2^y then too
 constexpr float kNothing = -300.f;
+constexpr float kSlack = 16.f;  // by which an entry may pass the base, in powers of two
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
@@ -36,6 +40,31 @@ __device__ __forceinline__ float max_nan(float x, float y) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
   return r;
 }
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+// Arithmetic on two binary32 values in a register pair.
+__device__ __forceinline__ uint64_t pack2(float x, float y) { return (uint64_t)__float_as_uint(x) | (uint64_t)__float_as_uint(y) << 32; }
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ float low(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float high(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
 // Keys: whole numbers in the order of (value, then lower index). Zeros of both signs are the same value.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -51,21 +80,21 @@ __device__ __forceinline__ float value_of(uint64_t key) {
 // Above every key of -infinity, which is no alternative; not above any other.
 constexpr uint64_t kLeast = (uint64_t)0x00800000u << 32;
 
-// m, s, t of a set of entries.
+// Sums over a set of entries relative to a base b, -infinity where there is none yet.
 struct Sums {
-  float m, s, t;
+  float b, s, t;
   // where differences are taken from: finite, so that entries of -infinity add nothing
-  __device__ __forceinline__ float base() const { return fmaxf(m, kLowest); }
-  // to the larger maximum `to`; c = scale log2 e
+  static __device__ __forceinline__ float from(float b) { return fmaxf(b, kLowest); }
+  // what carries sums over from base b to `to`, which is no smaller; c = scale log2 e
+  static __device__ __forceinline__ float shift(float b, float to, float c) { return max_nan((from(b) - from(to)) * c, kNothing); }
   __device__ __forceinline__ void move(float to, float c) {
-    const float old = base();
-    m = to;
-    const float y = max_nan((old - base()) * c, kNothing), f = exp2_fast(y);
+    const float y = shift(b, to, c), f = exp2_fast(y);
     t = f * fmaf(s, y, t);
     s *= f;
+    b = to;
   }
   __device__ __forceinline__ void join(Sums o, float c) {
-    const float to = fmaxf(m, o.m);
+    const float to = fmaxf(b, o.b);
     move(to, c);
     o.move(to, c);
     s += o.s;
@@ -73,17 +102,46 @@ struct Sums {
   }
 };
 
+// The sums of a thread, over the even and the odd entries of its vectors.
+template <int E>
+struct Stream {
+  float b = -kInf, limit = -kInf;
+  uint64_t minus = pack2(-kLowest, -kLowest), s = 0, t = 0;
+
+  __device__ __forceinline__ void add(const float (&x)[E], float top, float c, float slack) {
+    if (top > limit) {
+      const float y = Sums::shift(b, top, c), f = exp2_fast(y);
+      t = mul2(fma2(s, pack2(y, y), t), pack2(f, f));
+      s = mul2(s, pack2(f, f));
+      b = top;
+      limit = top + slack;
+      minus = pack2(-Sums::from(top), -Sums::from(top));
+    }
+    const uint64_t cc = pack2(c, c);
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      const uint64_t d = mul2(add2(pack2(x[i], x[i + 1]), minus), cc);
+      const uint64_t y = pack2(max_nan(low(d), kNothing), max_nan(high(d), kNothing));
+      const uint64_t e = pack2(exp2_fast(low(y)), exp2_fast(high(y)));
+      s = add2(s, e);
+      t = fma2(e, y, t);
+    }
+  }
+  __device__ __forceinline__ Sums sums() const { return Sums{b, low(s) + high(s), low(t) + high(t)}; }
+};
+
 template <bool BF16>
 struct Row {
   static constexpr int E = BF16 ? 8 : 4;  // elements of a vector
   const char* at;                         // the boundary at or before the row's first element
   int shift, V;
+  int whole0, wholes;  // the first vector that lies within the row, and how many do
 
   // vector j; elements outside the row are -infinity
   __device__ __forceinline__ uint4 load(int j) const {
-    const int e0 = j * E - shift;
     const char* p = at + (size_t)j * 16;
-    if (e0 >= 0 && e0 + E <= V) return __ldcg(reinterpret_cast<const uint4*>(p));
+    if ((unsigned)(j - whole0) < (unsigned)wholes) return __ldcg(reinterpret_cast<const uint4*>(p));
+    const int e0 = j * E - shift;
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -122,42 +180,77 @@ __device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b
 
 struct Shared {
   Sums sums[kWarps];
-  uint64_t group[32];
+  float most[kWarps];
+  uint64_t group[kGroups];
   uint64_t found[kRoom];
   uint64_t best[COLI_MAX_TOP];
   uint64_t bound;
-  int n;
+  int n, hits;
   bool last;
+  uint16_t hit[kThreads];  // threads whose largest entry reaches the bound
 };
 
-// The keys of s.found[0..n) that fewer than k others exceed, in order, into s.best; 0 behind them. The CTA's threads, which
-// then agree.
-__device__ __forceinline__ void rank_found(Shared& s, int n, int k) {
-  if (threadIdx.x < COLI_MAX_TOP) s.best[threadIdx.x] = 0;
+// The k-th largest of s.group (no two alike, but for 0), or kLeast if that is none or less. s.bound holds kLeast when all threads
+// come here, after a barrier.
+__device__ __forceinline__ uint64_t find_bound(Shared& s, int k) {
+  const uint64_t mine = s.group[threadIdx.x / kPerGroup];
+  int above = 0;
+#pragma unroll
+  for (int j = 0; j < kGroups; j += kPerGroup) above += s.group[j + threadIdx.x % kPerGroup] > mine;
+#pragma unroll
+  for (int o = 1; o < kPerGroup; o *= 2) above += __shfl_xor_sync(0xffffffffu, above, o);
+  if (threadIdx.x % kPerGroup == 0 && above == k - 1) s.bound = max64(mine, kLeast);
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const uint64_t mine = s.found[i];
-    int above = 0;
-    for (int j = 0; j < n; j++) above += s.found[j] > mine;
-    if (above < k) s.best[above] = mine;
-  }
-  __syncthreads();
+  return s.bound;
 }
 
-// A warp: the k-th largest of the lanes' keys (no two alike, but for 0), at least kLeast.
-__device__ __forceinline__ uint64_t kth_of_warp(uint64_t key, int k) {
-  int above = 0;
-  for (int l = 0; l < 32; l++) above += __shfl_sync(0xffffffffu, key, l) > key;
-  uint64_t at = above < k ? key : ~0ull;  // the smallest of the first k
-  for (int o = 16; o; o >>= 1) {
-    const uint64_t other = __shfl_xor_sync(0xffffffffu, at, o);
-    at = other < at ? other : at;
+// A group of threads gives its largest key.
+__device__ __forceinline__ void give_group(Shared& s, uint64_t key) {
+#pragma unroll
+  for (int o = 1; o < kPerGroup; o *= 2) key = max64(key, __shfl_xor_sync(0xffffffffu, key, o));
+  if (threadIdx.x % kPerGroup == 0) s.group[threadIdx.x / kPerGroup] = key;
+}
+
+// The k largest of the keys s.found[0..n), in order, into s.best; 0 behind them. All of the CTA's threads, between barriers.
+__device__ __forceinline__ void rank_found(Shared& s, int n, int k) {
+  const int tid = threadIdx.x;
+  constexpr int kEach = kRoom / kThreads;
+  if (tid < COLI_MAX_TOP) s.best[tid] = 0;
+  // Many: the k-th largest of the groups' maxima is a bound again, and what is below it goes. More than kThreads keys give each
+  // of the kGroups groups kPerGroup of them at least, and k groups stay at most.
+  while (n > kThreads) {
+    uint64_t mine[kEach], most = 0;
+#pragma unroll
+    for (int u = 0; u < kEach; u++) {
+      mine[u] = tid + u * kThreads < n ? s.found[tid + u * kThreads] : 0;
+      most = max64(most, mine[u]);
+    }
+    give_group(s, most);
+    if (tid == 0) s.n = 0, s.bound = kLeast;
+    __syncthreads();
+    const uint64_t bound = find_bound(s, k);
+#pragma unroll
+    for (int u = 0; u < kEach; u++)
+      if (mine[u] >= bound) s.found[atomicAdd(&s.n, 1)] = mine[u];
+    __syncthreads();
+    n = s.n;
+    __syncthreads();
   }
-  return max64(at, kLeast);
+  for (int i0 = 0; i0 < n; i0 += kGroups) {
+    const int i = i0 + tid / kPerGroup;
+    const uint64_t mine = i < n ? s.found[i] : 0;
+    int above = 0;
+#pragma unroll 4
+    for (int j = tid % kPerGroup; j < n; j += kPerGroup) above += s.found[j] > mine;
+#pragma unroll
+    for (int o = 1; o < kPerGroup; o *= 2) above += __shfl_xor_sync(0xffffffffu, above, o);
+    if (i < n && above < k) s.best[above] = mine;
+  }
+  __syncthreads();
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 2) logprob_kernel(LogprobArgs a) {
+__global__ void __launch_bounds__(kThreads, kLogprobCtas) logprob_kernel(LogprobArgs a) {
   constexpr int E = Row<BF16>::E;
   __shared__ Shared s;
   griddep_launch_dependents();
@@ -169,105 +262,129 @@ __global__ void __launch_bounds__(kThreads, 2) logprob_kernel(LogprobArgs a) {
   row.shift = (int)(((uint64_t)row_id * (uint64_t)a.stride + a.shift_step) % E);
   row.at = static_cast<const char*>(a.x) + ((long long)row_id * a.stride - row.shift) * (BF16 ? 2 : 4);
   const int vecs = (a.V + row.shift + E - 1) / E;
+  row.whole0 = row.shift > 0;
+  row.wholes = max((a.V + row.shift) / E - row.whole0, 0);
   const int v0 = part_id * a.per, v1 = min(vecs, v0 + a.per);
   const float c = a.scale * kLog2e;
 
   // ---- the pass ----
-  Sums sum{-kInf, 0.f, 0.f};
-  int at = -1;  // the vector that holds the first of the largest entries
-  for (int j0 = v0 + tid; j0 < v1; j0 += kThreads * kUnroll) {
-    uint4 raw[kUnroll];
+  Stream<E> stream;
+  const float slack = kSlack / c;
+  float most = -kInf;  // the largest entry
+  int at = -1;         // the vector that holds the first of it
+  uint4 raw[kFlight];
 #pragma unroll
-    for (int u = 0; u < kUnroll; u++)
-      if (j0 + u * kThreads < v1) raw[u] = row.load(j0 + u * kThreads);
+  for (int u = 0; u < kFlight; u++)
+    if (v0 + tid + u * kThreads < v1) raw[u] = row.load(v0 + tid + u * kThreads);
+  for (int j0 = v0 + tid; j0 < v1; j0 += kThreads * kFlight) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; u++) {
+    for (int u = 0; u < kFlight; u++) {
       const int j = j0 + u * kThreads;
       if (j >= v1) break;
       float x[E];
       Row<BF16>::unpack(raw[u], x);
-      float top = x[0];
+      if (j + kFlight * kThreads < v1) raw[u] = row.load(j + kFlight * kThreads);  // the register's next vector
+      float top = fmaxf(x[0], x[1]);
 #pragma unroll
-      for (int i = 1; i < E; i++) top = fmaxf(top, x[i]);
-      if (top > sum.m) {
-        sum.move(top, c);
-        at = j;
-      }
-      const float base = sum.base();
-#pragma unroll
-      for (int i = 0; i < E; i++) {
-        const float y = max_nan((x[i] - base) * c, kNothing), e = exp2_fast(y);
-        sum.s += e;
-        sum.t = fmaf(e, y, sum.t);
-      }
+      for (int i = 2; i < E; i += 2) top = max3(top, x[i], x[i + 1]);
+      at = top > most ? j : at;
+      most = fmaxf(most, top);
+      stream.add(x, top, c, slack);
     }
   }
 
-  // ---- the thread's largest entry, and the bound ----
+  // ---- the CTA's sums, and each thread's largest entry ----
+  uint4 again;
+  if (a.k > 0 && at >= 0) again = row.load(at);
+  Sums sum = stream.sums();
+  auto over_warp = [&]() {
+    float to = sum.b;
+    for (int o = 16; o; o >>= 1) {
+      to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
+    sum.move(to, c);
+    for (int o = 16; o; o >>= 1) {
+      sum.s += __shfl_xor_sync(0xffffffffu, sum.s, o);
+      sum.t += __shfl_xor_sync(0xffffffffu, sum.t, o);
+    }
+  };
   uint64_t mine = 0;
   if (a.k > 0) {
     if (at >= 0) {
       float x[E];
-      Row<BF16>::unpack(row.load(at), x);
+      Row<BF16>::unpack(again, x);
 #pragma unroll
       for (int i = E - 1; i >= 0; i--)
-        if (x[i] == sum.m) mine = key_of(x[i], at * E - row.shift + i);
+        if (x[i] == most) mine = key_of(x[i], at * E - row.shift + i);
     }
-    uint64_t g = mine;
-    for (int o = 8; o; o >>= 1) g = max64(g, __shfl_xor_sync(0xffffffffu, g, o));
-    if ((lane & 15) == 0) s.group[tid >> 4] = g;
+    give_group(s, mine);
   }
-  for (int o = 16; o; o >>= 1) {
-    Sums other;
-    other.m = __shfl_xor_sync(0xffffffffu, sum.m, o);
-    other.s = __shfl_xor_sync(0xffffffffu, sum.s, o);
-    other.t = __shfl_xor_sync(0xffffffffu, sum.t, o);
-    sum.join(other, c);
-  }
-  if (lane == 0) s.sums[warp] = sum;
-  if (tid == 0) s.n = 0;
+  over_warp();
+  if (lane == 0) s.sums[warp] = sum, s.most[warp] = most;
+  if (tid == 0) s.n = s.hits = 0, s.bound = kLeast;
   __syncthreads();
-  sum = s.sums[0];
-  for (int w = 1; w < kWarps; w++) sum.join(s.sums[w], c);  // the same in every thread
+  float to = s.sums[0].b;
+  most = s.most[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; w++) to = fmaxf(to, s.sums[w].b), most = fmaxf(most, s.most[w]);
+  sum = Sums{to, 0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < kWarps; w++) {  // the same in every thread
+    Sums part = s.sums[w];
+    part.move(to, c);
+    sum.s += part.s;
+    sum.t += part.t;
+  }
+
+  // ---- its largest entries ----
   if (a.k > 0) {
-    if (warp == 0) {
-      const uint64_t b = kth_of_warp(s.group[lane], a.k);
-      if (lane == 0) s.bound = b;
-    }
-    __syncthreads();
-    uint64_t bound = s.bound;
-    for (;;) {
-      if (mine >= bound) {
-        const uint32_t least = (uint32_t)(bound >> 32);
-        for (int j = v0 + tid; j < v1; j += kThreads) {
+    uint64_t bound = find_bound(s, a.k);
+    if (a.k == 1) {  // the largest of all
+      if (tid == 0) s.best[0] = bound > kLeast ? bound : 0;
+      __syncthreads();
+    } else {
+      const int each = (v1 - v0 + kThreads - 1) / kThreads;  // vectors of a thread
+      for (;;) {
+        const float least = value_of(bound);
+        if (mine >= bound) s.hit[atomicAdd(&s.hits, 1)] = (uint16_t)tid;
+        __syncthreads();
+        const int looks = s.hits * each;
+        for (int w = tid; w < looks; w += kThreads) {
+          const int h = w / each, j = v0 + s.hit[h] + (w - h * each) * kThreads;
+          if (j >= v1) continue;
           float x[E];
           Row<BF16>::unpack(row.load(j), x);
+          float top = x[0];
+#pragma unroll
+          for (int i = 1; i < E; i++) top = fmaxf(top, x[i]);
+          if (!(top >= least)) continue;
 #pragma unroll
           for (int i = 0; i < E; i++) {
-            if (ordered(x[i]) < least) continue;
             const uint64_t key = key_of(x[i], j * E - row.shift + i);
             if (key < bound || x[i] != x[i]) continue;
             const int p = atomicAdd(&s.n, 1);
             if (p < kRoom) s.found[p] = key;
           }
         }
+        __syncthreads();
+        const int n = min(s.n, kRoom);
+        const bool more = s.n > kRoom;
+        __syncthreads();
+        rank_found(s, n, a.k);
+        if (!more) break;
+        bound = s.best[a.k - 1];  // reached by k entries, and not by all that reached the last one
+        __syncthreads();
+        if (tid == 0) s.n = s.hits = 0;
+        __syncthreads();
       }
-      __syncthreads();
-      const int n = min(s.n, kRoom);
-      const bool more = s.n > kRoom;
-      rank_found(s, n, a.k);
-      if (!more) break;
-      bound = s.best[a.k - 1];  // reached by k entries, and not by all that reached the last one
-      __syncthreads();
-      if (tid == 0) s.n = 0;
-      __syncthreads();
     }
   }
 
   // ---- the parts of a row ----
   if (a.parts > 1) {
     LogprobPart* part = a.part + (size_t)row_id * a.parts;
-    if (tid == 0) part[part_id].m = sum.m, part[part_id].s = sum.s, part[part_id].t = sum.t;
+    if (tid == 0) part[part_id].most = most, part[part_id].b = sum.b, part[part_id].s = sum.s, part[part_id].t = sum.t;
     if (tid < a.k) part[part_id].top[tid] = s.best[tid];
     __threadfence();
     __syncthreads();
@@ -278,46 +395,54 @@ __global__ void __launch_bounds__(kThreads, 2) logprob_kernel(LogprobArgs a) {
     __syncthreads();
     if (!s.last) return;
     __threadfence();
+    // all that the parts left is asked for at once
+    constexpr int kEach = kRoom / kThreads;
+    uint64_t key[kEach];
+    auto of_part = [&](int p, int i) { return __ldcg(reinterpret_cast<const unsigned long long*>(&part[p].top[i])); };
+    if (a.k > 0) {
+#pragma unroll
+      for (int u = 0; u < kEach; u++) {
+        const int i = tid + u * kThreads;
+        key[u] = i < a.parts * a.k ? of_part(i / a.k, i % a.k) : 0;
+      }
+      if (tid < kGroups) s.group[tid] = tid < a.parts ? of_part(tid, 0) : 0;
+    }
     Sums two[2];
+    most = -kInf;
     for (int h = 0; h < 2; h++) {
       const int p = lane + 32 * h;
       two[h] = Sums{-kInf, 0.f, 0.f};
-      if (p < a.parts) two[h] = Sums{__ldcg(&part[p].m), __ldcg(&part[p].s), __ldcg(&part[p].t)};
+      if (p < a.parts) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(part + p));
+        two[h] = Sums{v.y, v.z, v.w};
+        most = fmaxf(most, v.x);
+      }
     }
     sum = two[0];
     sum.join(two[1], c);
-    for (int o = 16; o; o >>= 1) {
-      Sums other;
-      other.m = __shfl_xor_sync(0xffffffffu, sum.m, o);
-      other.s = __shfl_xor_sync(0xffffffffu, sum.s, o);
-      other.t = __shfl_xor_sync(0xffffffffu, sum.t, o);
-      sum.join(other, c);
-    }
+    over_warp();
     if (a.k > 0) {
-      // of the parts' largest entries the k-th largest bounds again; with fewer parts than k there is none
-      auto of_part = [&](int p, int i) { return p < a.parts ? __ldcg(reinterpret_cast<const unsigned long long*>(&part[p].top[i])) : 0ull; };
-      if (tid == 0) s.n = 0;
-      if (warp == 0) {
-        const uint64_t b = kth_of_warp(max64(of_part(lane, 0), of_part(lane + 32, 0)), a.k);
-        if (lane == 0) s.bound = b;
-      }
+      // of the parts' largest entries the k-th largest is a bound; with fewer parts than k there is none
+      if (tid == 0) s.n = 0, s.bound = kLeast;
       __syncthreads();
-      const uint64_t bound = s.bound;
-      for (int i = tid; i < a.parts * a.k; i += kThreads) {
-        const uint64_t key = of_part(i / a.k, i % a.k);
-        if (key >= bound) s.found[atomicAdd(&s.n, 1)] = key;  // at most kRoom: see launch_logprobs
-      }
+      const uint64_t bound = find_bound(s, a.k);
+#pragma unroll
+      for (int u = 0; u < kEach; u++)
+        if (key[u] >= bound) s.found[atomicAdd(&s.n, 1)] = key[u];
       __syncthreads();
-      rank_found(s, s.n, a.k);
+      const int n = s.n;
+      __syncthreads();
+      rank_found(s, n, a.k);
     }
   }
 
   // ---- the answers ----
+  sum.move(most, c);  // of the largest entry: what is close to certain keeps its digits
   const bool bad = !(sum.s < kInf);  // a NaN, or an infinity among the entries
   const bool empty = sum.s == 0.f;
   const float nan = __uint_as_float(0x7fc00000u);
   if (bad && tid == 0) set_error(a.err, COLI_E_NONFINITE);
-  const float base = sum.base(), log_s = logf(sum.s);
+  const float base = Sums::from(most), log_s = logf(sum.s);
   auto log_p = [&](float x) { return bad ? nan : empty ? -kInf : fmaf(x - base, a.scale, -log_s); };
   if (a.entropy && tid == 0) a.entropy[row_id] = bad ? nan : empty ? 0.f : fmaxf(log_s - kLn2 * (sum.t / sum.s), 0.f);
   if (a.logp)

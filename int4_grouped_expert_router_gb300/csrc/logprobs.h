@@ -5,15 +5,15 @@
 
 namespace coli {
 
-// What a CTA that has read a part of a row leaves: the part's largest entry, sum e^(z - max), sum (z - max) e^(z - max) (in
-// powers of two), and its largest entries in descending order, 0 behind the last.
-struct LogprobPart {
-  float m, s, t, unused;
+// What a CTA that has read a part of a row leaves: the part's largest entry, the sums s = sum e^(z - b) and t = sum (z - b)
+// e^(z - b) (in powers of two) over its base b, and its largest entries in descending order, 0 behind the last.
+struct alignas(16) LogprobPart {
+  float most, b, s, t;
   uint64_t top[COLI_MAX_TOP];
 };
 
 // Rows are shared where there are fewer than kLogprobCtas per SM, by at most as many CTAs as that makes in all.
-constexpr int kLogprobCtas = 2;
+constexpr int kLogprobCtas = 4;
 constexpr int kLogprobMostParts = 64;
 
 // Memory of a context for it: the parts, then an arrival counter per row, zero between calls.

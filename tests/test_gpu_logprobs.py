@@ -176,6 +176,30 @@ def test_forbidden_tokens_and_huge_entries(ctx):
     assert got["logp"][4, 0] == NEG and got["entropy"][4] == 0 and (got["top_id"][4] == -1).all()
 
 
+@pytest.mark.parametrize("scale", [1e-30, 1e-3, 50.0, 1e30])
+@pytest.mark.parametrize("S", [2, 200])
+def test_scales(ctx, S, scale):
+    """Inverse temperatures from almost even to almost certain: log p of the largest entry keeps an absolute error of 2^-20."""
+    x, xt = logits(S, 3000, "f32")
+    lp, h = O.logprobs(x, scale)
+    got = call(ctx, xt, torch.zeros(S, 1, dtype=torch.int32, device="cuda"), 3, scale=scale)
+    ids = O.top(x, 3)
+    want = np.take_along_axis(lp, ids, 1)
+    assert np.array_equal(got["top_id"], ids)
+    assert (np.abs(got["top_logp"] - want) <= 2.0 ** -18 + 2.0 ** -21 * np.abs(want)).all()
+    assert (np.abs(got["entropy"] - h) <= 1e-4).all()
+
+
+def test_entries_far_above_those_before_them(ctx):
+    """Steps up of many powers of two between one vector and the next, in every thread and CTA."""
+    for S in (1, 300):
+        x = np.zeros((S, 40000), np.float32)
+        x += (np.arange(40000) // 2500 * 25).astype(np.float32)
+        x += rng("steps", S).normal(size=x.shape).astype(np.float32)
+        check(ctx, x, torch.from_numpy(x).cuda(), k=9)
+        check(ctx, x[:, ::-1].copy(), torch.from_numpy(x[:, ::-1].copy()).cuda(), k=9)
+
+
 def test_each_output_alone(ctx):
     x, xt = logits(2, 3000, "f32")
     tokens = torch.tensor([[5], [6]], dtype=torch.int32, device="cuda")
