@@ -21,7 +21,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRoom = kLogprobMostParts * COLI_MAX_TOP;  // entries that reach the bound
-constexpr int kFlight = 6;   // vectors of a thread on their way
+constexpr int kLooks = 4;    // vectors that a thread looks through together
+constexpr int kFlight = 7;   // vectors of a thread on their way
 constexpr int kGroups = 64, kPerGroup = kThreads / kGroups;  // groups of threads whose maxima make the bound
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLowest = -3.402823466e38f;
@@ -137,10 +138,11 @@ struct Row {
   int shift, V;
   int whole0, wholes;  // the first vector that lies within the row, and how many do
 
+  __device__ __forceinline__ bool is_whole(int j) const { return (unsigned)(j - whole0) < (unsigned)wholes; }
   // vector j; elements outside the row are -infinity
   __device__ __forceinline__ uint4 load(int j) const {
     const char* p = at + (size_t)j * 16;
-    if ((unsigned)(j - whole0) < (unsigned)wholes) return __ldcg(reinterpret_cast<const uint4*>(p));
+    if (is_whole(j)) return __ldcg(reinterpret_cast<const uint4*>(p));
     const int e0 = j * E - shift;
     uint32_t w[4];
 #pragma unroll
@@ -176,9 +178,20 @@ struct Row {
   }
 };
 
+// 16 bytes into shared memory, waited for by groups: the copies on their way take no registers.
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
 struct Shared {
+  uint4 ring[kFlight][kThreads];  // each thread's vectors on their way
   Sums sums[kWarps];
   float most[kWarps];
   uint64_t group[kGroups];
@@ -272,27 +285,30 @@ __global__ void __launch_bounds__(kThreads, kLogprobCtas) logprob_kernel(Logprob
   const float slack = kSlack / c;
   float most = -kInf;  // the largest entry
   int at = -1;         // the vector that holds the first of it
-  uint4 raw[kFlight];
+  auto ask = [&](int j, int u) {
+    if (j < v1 && row.is_whole(j)) copy_async(&s.ring[u][tid], row.at + (size_t)j * 16);
+    copy_commit();
+  };
 #pragma unroll
-  for (int u = 0; u < kFlight; u++)
-    if (v0 + tid + u * kThreads < v1) raw[u] = row.load(v0 + tid + u * kThreads);
+  for (int u = 0; u < kFlight; u++) ask(v0 + tid + u * kThreads, u);
   for (int j0 = v0 + tid; j0 < v1; j0 += kThreads * kFlight) {
 #pragma unroll
     for (int u = 0; u < kFlight; u++) {
       const int j = j0 + u * kThreads;
       if (j >= v1) break;
+      copy_wait<kFlight - 1>();
       float x[E];
-      Row<BF16>::unpack(raw[u], x);
-      if (j + kFlight * kThreads < v1) raw[u] = row.load(j + kFlight * kThreads);  // the register's next vector
+      Row<BF16>::unpack(row.is_whole(j) ? s.ring[u][tid] : row.load(j), x);
       float top = fmaxf(x[0], x[1]);
 #pragma unroll
       for (int i = 2; i < E; i += 2) top = max3(top, x[i], x[i + 1]);
       at = top > most ? j : at;
       most = fmaxf(most, top);
       stream.add(x, top, c, slack);
+      ask(j + kFlight * kThreads, u);  // its values have been used
     }
   }
-
+  copy_wait<0>();
   // ---- the CTA's sums, and each thread's largest entry ----
   uint4 again;
   if (a.k > 0 && at >= 0) again = row.load(at);
@@ -350,21 +366,31 @@ __global__ void __launch_bounds__(kThreads, kLogprobCtas) logprob_kernel(Logprob
         if (mine >= bound) s.hit[atomicAdd(&s.hits, 1)] = (uint16_t)tid;
         __syncthreads();
         const int looks = s.hits * each;
-        for (int w = tid; w < looks; w += kThreads) {
-          const int h = w / each, j = v0 + s.hit[h] + (w - h * each) * kThreads;
-          if (j >= v1) continue;
-          float x[E];
-          Row<BF16>::unpack(row.load(j), x);
-          float top = x[0];
+        for (int w0 = tid; w0 < looks; w0 += kThreads * kLooks) {
+          uint4 r[kLooks];
+          int j[kLooks];
 #pragma unroll
-          for (int i = 1; i < E; i++) top = fmaxf(top, x[i]);
-          if (!(top >= least)) continue;
+          for (int u = 0; u < kLooks; u++) {
+            const int w = w0 + u * kThreads, h = w / each;
+            j[u] = w < looks ? v0 + s.hit[h] + (w - h * each) * kThreads : v1;
+            if (j[u] < v1) r[u] = row.load(j[u]);
+          }
 #pragma unroll
-          for (int i = 0; i < E; i++) {
-            const uint64_t key = key_of(x[i], j * E - row.shift + i);
-            if (key < bound || x[i] != x[i]) continue;
-            const int p = atomicAdd(&s.n, 1);
-            if (p < kRoom) s.found[p] = key;
+          for (int u = 0; u < kLooks; u++) {
+            if (j[u] >= v1) continue;
+            float x[E];
+            Row<BF16>::unpack(r[u], x);
+            float top = x[0];
+#pragma unroll
+            for (int i = 1; i < E; i++) top = fmaxf(top, x[i]);
+            if (!(top >= least)) continue;
+#pragma unroll
+            for (int i = 0; i < E; i++) {
+              const uint64_t key = key_of(x[i], j[u] * E - row.shift + i);
+              if (key < bound || x[i] != x[i]) continue;
+              const int p = atomicAdd(&s.n, 1);
+              if (p < kRoom) s.found[p] = key;
+            }
           }
         }
         __syncthreads();
