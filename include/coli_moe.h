@@ -526,7 +526,7 @@ COLI_API int coli_dense_shape(coli_ctx *ctx, uint64_t handle, int *O, int *I);
 COLI_API int coli_dense_free(coli_ctx *ctx, uint64_t handle);
 
 /*
- * x [S x I] in x_dtype; y, mul, resid [S x O] in y_dtype (any pairing of the two); rows a stride apart (elements). bias [O] f32.
+ * I and O have to be the weight's. x [S x I] in x_dtype; y, mul, resid [S x O] in y_dtype (any pairing of the two); rows a stride apart (elements). bias [O] f32.
  * bias, mul, resid: NULL for none. act:
  *   COLI_ACT_NONE       z
  *   COLI_ACT_SILU       z / (1 + exp(-z))
@@ -546,7 +546,7 @@ COLI_API int coli_dense_free(coli_ctx *ctx, uint64_t handle);
 #define COLI_ACT_GELU_TANH 3
 #define COLI_ACT_RELU 4
 #define COLI_ACT_RELU2 5
-COLI_API int coli_dense_linear(coli_ctx *ctx, uint64_t W, const void *x, long long x_stride, int x_dtype, int S,
+COLI_API int coli_dense_linear(coli_ctx *ctx, uint64_t W, int I, int O, const void *x, long long x_stride, int x_dtype, int S,
                                const float *bias, int act, const void *mul, long long mul_stride, const void *resid,
                                long long resid_stride, void *y, long long y_stride, int y_dtype);
 

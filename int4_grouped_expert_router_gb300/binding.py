@@ -93,7 +93,7 @@ SIGNATURES = {
     "coli_dense_upload": (_U64, [_P, _P, _I, _I]),
     "coli_dense_shape": (_I, [_P, _U64, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]),
     "coli_dense_free": (_I, [_P, _U64]),
-    "coli_dense_linear": (_I, [_P, _U64, _P, _L, _I, _I, _P, _I, _P, _L, _P, _L, _P, _L, _I]),
+    "coli_dense_linear": (_I, [_P, _U64, _I, _I, _P, _L, _I, _I, _P, _I, _P, _L, _P, _L, _P, _L, _I]),
     "coli_logprobs": (_I, [_P, _P, _L, _I, _I, _I, _F, _P, _I, _P, _P, _I, _P, _P]),
     "coli_profile_enable": (_I, [_P, _I]),
     "coli_profile_read": (_I, [_P, _I, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_longlong)]),
@@ -554,25 +554,32 @@ def coli_rotary(ctx, q, k, freqs, q_out, k_out, lens=None, q_start=None, positio
     T, hd, dtype = first.shape[0], first.shape[2], first.dtype
     at = []
     for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None and out is None:
+            at += (None, 0, None, 0, 0)
+            continue
         if x is None or out is None:
-            if x is not None or out is not None:
-                raise ValueError(f"rotary: {name} and {name}_out come together")
-            at += [None, 0, None, 0, 0]
-        elif x.dtype != dtype or out.dtype != dtype or x.dim() != 3:
-            raise ValueError("rotary: q, k and their outputs must be [T x heads x head_dim] of one dtype")
-        else:
-            heads = x.shape[1]
-            at += [x.data_ptr(), _rows3(x, T, heads, hd, name), out.data_ptr(), _rows3(out, T, heads, hd, name + "_out"), heads]
+            raise ValueError(f"rotary: {name} and {name}_out come together")
+        shape = x.shape
+        for t in (x, out):
+            if not t.is_cuda or t.dtype != dtype or t.shape != shape or len(shape) != 3 or shape[0] != T or shape[2] != hd:
+                raise ValueError("rotary: q, k and their outputs must be [T x heads x head_dim] CUDA tensors of one dtype")
+            row, head, one = t.stride()
+            if one != 1 or (head != hd and shape[1] > 1):
+                raise ValueError("rotary: the heads and channels of a row must be contiguous")
+            at += (t.data_ptr(), row)
+        at.append(shape[1])
     if freqs.dtype != torch.int64 or not freqs.is_cuda or not freqs.is_contiguous():
         raise ValueError("rotary: freqs must be a contiguous int64 CUDA tensor (coli_rotary_freqs)")
-    for t, size, name in ((positions, T, "positions"), (lens, None, "lens"), (q_start, None, "q_start")):
-        if t is not None and (t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or size not in (None, t.numel())):
-            raise ValueError(f"rotary: {name} must be a contiguous int32 CUDA tensor" + (f" of {size} entries" if size else ""))
     B = 0 if lens is None else lens.numel()
-    if q_start is not None and q_start.numel() != B + 1:
-        raise ValueError("rotary: q_start must have B + 1 entries")
-    rc = (_lib or library()).coli_rotary(ctx, *at, act_dtype(first), hd, 2 * freqs.numel(), interleaved, freqs.data_ptr(), scale, T,
-                                         *(None if t is None else t.data_ptr() for t in (positions, q_start, lens)), B)
+    for t, size, name in ((positions, T, "positions"), (q_start, B + 1, "q_start"), (lens, B, "lens")):
+        if t is None:
+            at.append(None)
+        elif t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() != size:
+            raise ValueError(f"rotary: {name} must be a contiguous int32 CUDA tensor (positions [T], lens [B], q_start [B + 1])")
+        else:
+            at.append(t.data_ptr())
+    rc = (_lib or library()).coli_rotary(ctx, *at[:10], act_dtype(first), hd, 2 * freqs.numel(), interleaved, freqs.data_ptr(), scale,
+                                         T, *at[10:], B)
     return rc if rc == COLI_OK else _check(ctx, rc, "coli_rotary")
 
 
@@ -612,22 +619,27 @@ def coli_dense_linear(ctx, W, x, y, bias=None, act="none", mul=None, resid=None)
     [S x O] in y's dtype, bias [O] float32, act one of ACTIVATIONS. y may be mul or resid."""
     if act not in ACTIVATIONS:
         raise ValueError(f"dense_linear: act must be one of {sorted(ACTIVATIONS)}")
-    O, I = coli_dense_shape(ctx, W)
-    if x.dim() != 2:
-        raise ValueError("dense_linear: x must be [S x I]")
-    S = x.shape[0]
-    xs, out = _rows2(x, (S, I), "x"), torch.Size((S, O))
+    if x.dim() != 2 or y.dim() != 2:
+        raise ValueError("dense_linear: x must be [S x I] and y [S x O]")
+    (S, I), out, dtype = x.shape, y.shape, y.dtype
+    O = out[1]
     at = []
-    for t, name in ((mul, "mul"), (resid, "resid"), (y, "y")):
+    for t in (mul, resid, y):
         if t is None:
-            at += [None, 0]
-        elif t.dtype != y.dtype:
-            raise ValueError("dense_linear: mul, resid and y must have one dtype")
-        else:
-            at += [t.data_ptr(), _rows2(t, out, name)]
+            at += (None, 0)
+            continue
+        if t.dtype != dtype or t.shape != out or out[0] != S or not t.is_cuda:
+            raise ValueError("dense_linear: mul, resid and y must be [S x O] CUDA tensors of one dtype")
+        row, one = t.stride()
+        if one != 1 and O > 1:
+            raise ValueError("dense_linear: the elements of a row must be contiguous")
+        at += (t.data_ptr(), row)
+    xs, one = x.stride()
+    if (one != 1 and I > 1) or not x.is_cuda:
+        raise ValueError("dense_linear: x must be a CUDA tensor with contiguous rows")
     if bias is not None and (bias.dtype != torch.float32 or not bias.is_cuda or not bias.is_contiguous() or bias.numel() != O):
         raise ValueError("dense_linear: bias must be a contiguous float32 CUDA tensor [O]")
-    rc = (_lib or library()).coli_dense_linear(ctx, W, x.data_ptr(), xs, act_dtype(x), S, None if bias is None else bias.data_ptr(),
+    rc = (_lib or library()).coli_dense_linear(ctx, W, I, O, x.data_ptr(), xs, act_dtype(x), S, None if bias is None else bias.data_ptr(),
                                                ACTIVATIONS[act], *at, act_dtype(y))
     return rc if rc == COLI_OK else _check(ctx, rc, "coli_dense_linear")
 

@@ -1146,13 +1146,14 @@ int coli_dense_free(coli_ctx* ctx, uint64_t handle) {
   return COLI_OK;
 }
 
-int coli_dense_linear(coli_ctx* ctx, uint64_t W, const void* x, long long x_stride, int x_dtype, int S, const float* bias,
+int coli_dense_linear(coli_ctx* ctx, uint64_t W, int I, int O, const void* x, long long x_stride, int x_dtype, int S, const float* bias,
                       int act, const void* mul, long long mul_stride, const void* resid, long long resid_stride, void* y,
                       long long y_stride, int y_dtype) {
   if (!ctx) return COLI_E_INVAL;
   if (!x || !y) return fail(ctx, COLI_E_INVAL, "dense_linear: NULL pointer");
   const DenseTensor* t = dense_tensor(ctx, W);
   if (!t) return fail(ctx, COLI_E_INVAL, "dense_linear: unknown handle");
+  if (I != t->I || O != t->O) return fail(ctx, COLI_E_INVAL, "dense_linear: I and O must be the weight's");
   for (int dtype : {x_dtype, y_dtype})
     if (dtype != COLI_DTYPE_F32 && dtype != COLI_DTYPE_BF16) return fail(ctx, COLI_E_INVAL, "dense_linear: dtype");
   if (S < 1 || S > COLI_MAX_TOKENS) return fail(ctx, COLI_E_INVAL, "dense_linear: S out of range");

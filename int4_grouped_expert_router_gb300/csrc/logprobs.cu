@@ -423,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, kLogprobCtas) logprob_kernel(Logprob
     __threadfence();
     // all that the parts left is asked for at once
     constexpr int kEach = kRoom / kThreads;
+    static_assert(kLogprobMostParts <= kGroups, "a group for each part");
     uint64_t key[kEach];
     auto of_part = [&](int p, int i) { return __ldcg(reinterpret_cast<const unsigned long long*>(&part[p].top[i])); };
     if (a.k > 0) {
@@ -431,7 +432,10 @@ __global__ void __launch_bounds__(kThreads, kLogprobCtas) logprob_kernel(Logprob
         const int i = tid + u * kThreads;
         key[u] = i < a.parts * a.k ? of_part(i / a.k, i % a.k) : 0;
       }
-      if (tid < kGroups) s.group[tid] = tid < a.parts ? of_part(tid, 0) : 0;
+      // groups are runs of `run` of a part's keys, which descend: their first ones are their largest
+      const int most_runs = kGroups / a.parts, run = (a.k + most_runs - 1) / most_runs;
+      const int runs = (a.k + run - 1) / run;
+      if (tid < kGroups) s.group[tid] = tid < a.parts * runs ? of_part(tid / runs, tid % runs * run) : 0;
     }
     Sums two[2];
     most = -kInf;
@@ -448,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, kLogprobCtas) logprob_kernel(Logprob
     sum.join(two[1], c);
     over_warp();
     if (a.k > 0) {
-      // of the parts' largest entries the k-th largest is a bound; with fewer parts than k there is none
+      // of the groups' largest entries the k-th largest is a bound; with fewer groups than k there is none
       if (tid == 0) s.n = 0, s.bound = kLeast;
       __syncthreads();
       const uint64_t bound = find_bound(s, a.k);

@@ -5,7 +5,13 @@
 // thousand turns on. Its upper 32 bits, read as a signed part of a half turn, go to sincospif.
 //
 // Bound by memory: q and k are read and written once. The sines and cosines of a row are shared by all of its heads, so a CTA
-// takes whole rows and makes their table in shared memory while its first loads are on their way.
+// takes whole rows and makes their table in shared memory while its first loads are on their way; few heads are several rows.
+//
+// Measured: 8191 rows of 64 + 8 heads of 128 (bf16) 52 us, 5.8 TB/s, 0.85 of a copy's rate, neighbouring channels 60 us, f32
+// 90 us (0.99); 3001 f32 rows of 40 heads of 80, 36 channels turned, 18.0 us (4.3 TB/s); one row 3.5 us on the device, less
+// than the call takes on the host (8.5 us). Bound by the table's latency (plan, frequency, sine) at the start of each CTA. Five
+// CTAs of 256 threads in 48 registers beat three of 384 in 56 (57 us) and four of 384 in 40 (67 us, spills); copies behind the
+// turned part two vectors at a time took the f32 case from 22 to 18 us.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -52,8 +58,58 @@ int rotary_freqs(int rot, double base, int scaling, double factor, double origin
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kMostThreads = 256, kCtas = 5;  // CTAs of an SM; 48 registers
 constexpr int kMostRows = 16;  // rows of a CTA
+constexpr long long kGone = 1ll << 40, kCopied = 1ll << 41;  // not of any sequence; before its sequence's first position
+
+// Positions of the `here` rows from row0 on, by a warp.
+__device__ __forceinline__ void find_positions(const RotaryArgs& a, int row0, int here, long long* to) {
+  const int lane = threadIdx.x & 31, row = row0 + lane;
+  if (a.positions) {
+    if (lane < here) to[lane] = __ldcg(a.positions + row);
+    return;
+  }
+  int b = row, r0 = row, r1 = row + 1, len = 0;
+  if (!a.q_start) {
+    if (lane < here) len = __ldcg(a.lens + b);
+  } else if (a.B < 32) {
+    // the whole plan in the warp's registers: one round trip
+    const int start = lane <= a.B ? __ldcg(a.q_start + lane) : 0, length = lane < a.B ? __ldcg(a.lens + lane) : 0;
+    for (int l = 0; l < here; l++) {
+      const unsigned le = __ballot_sync(0xffffffffu, lane < a.B && start <= row0 + l);
+      const int at = max(0, __popc(le) - 1);
+      const int from = __shfl_sync(0xffffffffu, start, at), until = __shfl_sync(0xffffffffu, start, at + 1);
+      const int have = __shfl_sync(0xffffffffu, length, at);
+      if (lane == l) r0 = from, r1 = until, len = have;
+    }
+  } else {
+    b = kv4_seq_of(a.q_start, a.B, row0);
+    if (lane < here) {
+      while (b + 1 < a.B && __ldcg(a.q_start + b + 1) <= row) b++;  // a few steps: rows are neighbours
+      r0 = __ldcg(a.q_start + b);
+      r1 = __ldcg(a.q_start + b + 1);
+      len = __ldcg(a.lens + b);
+    }
+  }
+  if (lane >= here) return;
+  // a range or a length that does not fit is reported by check_plan
+  const bool owned = r0 >= 0 && r1 <= a.T && row >= r0 && row < r1;
+  const long long pos = (long long)max(len, 0) - (r1 - row);
+  to[lane] = !owned ? kGone : pos < 0 ? kCopied : pos;
+}
+
+// Row ranges and lengths that do not fit are reported whether or not a row falls in them.
+__device__ __forceinline__ void check_plan(const RotaryArgs& a) {
+  if (a.positions) return;
+  for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < a.B; b += gridDim.x * blockDim.x) {
+    bool bad = __ldcg(a.lens + b) < 0;
+    if (a.q_start) {
+      const int r0 = __ldcg(a.q_start + b), r1 = __ldcg(a.q_start + b + 1);
+      bad |= r0 < 0 || r1 < r0 || r1 > a.T;
+    }
+    if (bad) set_error(a.err, COLI_E_RANGE);
+  }
+}
 
 template <int V>
 struct Vec;  // V bf16 or f32 elements as they lie in memory
@@ -108,21 +164,25 @@ __device__ __forceinline__ R pack(const float (&v)[V]) {
   return raw;
 }
 
-// Vectors of V elements. A task is two of them (two halves' worth of V pairs, or 2 V neighbouring channels), or, behind the
-// turned part, one that is copied.
-template <bool BF16, int V, bool HALF>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a, int rows) {
-  constexpr int E = BF16 ? 2 : 4, U = V == 1 ? 4 : 2;
+// Tasks of a thread whose loads are under way together.
+template <int V>
+constexpr int kTasks = V == 1 ? 4 : 2;
+
+// Vectors of V elements. A task is two of them (two halves' worth of V pairs, or 2 V neighbouring channels); behind the turned
+// part (COPY) two neighbouring ones that are copied, where there is an even number of them (`wide`), or one.
+template <bool BF16, int V, bool HALF, bool COPY>
+__global__ void __launch_bounds__(kMostThreads, kCtas) rotary_kernel(RotaryArgs a, int rows, bool wide) {
+  constexpr int E = BF16 ? 2 : 4, U = kTasks<V>;
   using R = typename Vec<V * E>::T;
   extern __shared__ float2 s_turn[];  // [rows][rot / 2] cosine, sine
   __shared__ long long s_pos[kMostRows];
-  constexpr long long kGone = 1ll << 40, kCopied = 1ll << 41;  // not of any sequence; before its sequence's first position
   griddep_launch_dependents();
   griddep_wait();
-  const int tid = threadIdx.x, lane = tid & 31, half = a.rot / 2;
+  const int tid = threadIdx.x, threads = blockDim.x, half = a.rot / 2;
   const int row0 = blockIdx.x * rows;
   const int here = min(rows, a.T - row0);
-  const int turned = half / V, copied = (a.hd - a.rot) / V, per_head = turned + copied;
+  const int copy = wide ? 2 * V : V;  // elements of a copied vector
+  const int turned = half / V, copied = COPY ? (a.hd - a.rot) / copy : 0, per_head = turned + copied;
   const int per_row = per_head * (a.side[0].heads + a.side[1].heads);
   const int tasks = per_row * here;
 
@@ -141,8 +201,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a, int rows
     const bool k = head >= a.side[0].heads;
     if (k) head -= a.side[0].heads;
     const RotarySide& s = a.side[k];
-    const int channel = head * a.hd + (v < turned ? (HALF ? v * V : v * 2 * V) : a.rot + (v - turned) * V);
-    t.pair = v < turned ? v * V : -1;
+    const int channel = head * a.hd + (!COPY || v < turned ? (HALF ? v * V : v * 2 * V) : a.rot + (v - turned) * copy);
+    t.pair = !COPY || v < turned ? v * V : -1;
     t.in = static_cast<const char*>(s.in) + ((row0 + t.row) * s.in_stride + channel) * E;
     t.out = static_cast<char*>(s.out) + ((row0 + t.row) * s.out_stride + channel) * E;
     return t;
@@ -150,51 +210,34 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a, int rows
   const int apart = (HALF ? half : V) * E;  // bytes between a task's vectors
 
   bool made = false;
-  for (int first = 0; first < tasks; first += kThreads * U) {
+  const unsigned long long* freqs = reinterpret_cast<const unsigned long long*>(a.freqs);
+  const unsigned long long my_freq = tid < half * here ? __ldcg(freqs + tid % half) : 0;  // of the thread's first pair
+  for (int first = 0; first < tasks; first += threads * U) {
     Task t[U];
     R x[U][2];
 #pragma unroll
     for (int u = 0; u < U; u++) {
-      const int i = first + u * kThreads + tid;
+      const int i = first + u * threads + tid;
       t[u].row = -1;
       if (i < tasks) {
         t[u] = task_of(i);
         x[u][0] = load_cg<R>(t[u].in);
-        if (t[u].pair >= 0) x[u][1] = load_cg<R>(t[u].in + apart);
+        if (!COPY || t[u].pair >= 0)
+          x[u][1] = load_cg<R>(t[u].in + apart);
+        else if (wide)
+          x[u][1] = load_cg<R>(t[u].in + V * E);
       }
     }
     if (!made) {
       made = true;
-      if (a.positions) {
-        if (tid < here) s_pos[tid] = __ldcg(a.positions + row0 + tid);
-      } else if (!a.q_start) {
-        if (tid < here) {
-          const int len = __ldcg(a.lens + row0 + tid);
-          if (len < 0) set_error(a.err, COLI_E_RANGE);
-          s_pos[tid] = len > 0 ? len - 1 : kCopied;
-        }
-      } else {
-        for (int r = tid >> 5; r < here; r += kThreads / 32) {
-          const int row = row0 + r, b = kv4_seq_of(a.q_start, a.B, row);
-          if (lane == 0) {
-            const int r0 = __ldcg(a.q_start + b), r1 = __ldcg(a.q_start + b + 1), len = __ldcg(a.lens + b);
-            const bool owned = r0 >= 0 && r1 <= a.T && row >= r0 && row < r1;
-            const long long pos = (long long)max(len, 0) - (r1 - row);
-            s_pos[r] = !owned ? kGone : pos < 0 ? kCopied : pos;
-          }
-        }
-        // ranges and lengths that do not fit are reported whether or not a row falls in them
-        for (int b = blockIdx.x * kThreads + tid; b < a.B; b += gridDim.x * kThreads) {
-          const int r0 = __ldcg(a.q_start + b), r1 = __ldcg(a.q_start + b + 1);
-          if (r0 < 0 || r1 < r0 || r1 > a.T || __ldcg(a.lens + b) < 0) set_error(a.err, COLI_E_RANGE);
-        }
-      }
+      if (tid < 32) find_positions(a, row0, here, s_pos);
       __syncthreads();
-      for (int i = tid; i < here * half; i += kThreads) {
+      for (int i = tid; i < here * half; i += threads) {
         const int r = i / half;
         const long long pos = s_pos[r];
         if (pos < kGone) {
-          const uint32_t turn = (uint32_t)(((uint64_t)pos * __ldcg(reinterpret_cast<const unsigned long long*>(a.freqs) + (i - r * half))) >> 32);
+          const unsigned long long freq = i == tid ? my_freq : __ldcg(freqs + (i - r * half));
+          const uint32_t turn = (uint32_t)(((uint64_t)pos * freq) >> 32);
           float sine, cosine;
           sincospif((float)(int)turn * 4.656612873077393e-10f, &sine, &cosine);  // 2^-31
           s_turn[i] = make_float2(cosine * a.scale, sine * a.scale);
@@ -207,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a, int rows
       if (t[u].row < 0) continue;
       const long long pos = s_pos[t[u].row];
       if (pos == kGone) continue;
-      if (pos != kCopied && t[u].pair >= 0) {
+      if (pos != kCopied && (!COPY || t[u].pair >= 0)) {
         const float2* turn = s_turn + t[u].row * half + t[u].pair;
         float v[2][V];
         unpack<BF16, V>(x[u][0], v[0]);
@@ -227,17 +270,23 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a, int rows
         x[u][1] = pack<BF16, V, R>(v[1]);
       }
       *reinterpret_cast<R*>(t[u].out) = x[u][0];
-      if (t[u].pair >= 0) *reinterpret_cast<R*>(t[u].out + apart) = x[u][1];
+      if (!COPY || t[u].pair >= 0 || wide) *reinterpret_cast<R*>(t[u].out + (!COPY || t[u].pair >= 0 ? apart : V * E)) = x[u][1];
     }
   }
+  check_plan(a);
 }
 
 template <bool BF16, int V, bool HALF>
 cudaError_t launch_one(coli_ctx* ctx, const RotaryArgs& a) {
-  const int per_row = ((a.rot / 2 + a.hd - a.rot) / V) * (a.side[0].heads + a.side[1].heads);
-  const int rows = per_row >= kThreads ? 1 : min(kMostRows, kThreads / per_row);
-  const size_t smem = (size_t)rows * (a.rot / 2) * sizeof(float2);  // at most kThreads * V pairs: 16 KB
-  return launch_k(rotary_kernel<BF16, V, HALF>, (a.T + rows - 1) / rows, kThreads, smem, ctx->stream, true, false, a, rows);
+  const bool wide = (a.hd - a.rot) % (2 * V) == 0;
+  const int per_row = (a.rot / 2 / V + (a.hd - a.rot) / (wide ? 2 * V : V)) * (a.side[0].heads + a.side[1].heads);
+  // whole rows, as many as keep a CTA busy, and threads that share their tasks evenly
+  constexpr int U = kTasks<V>;
+  const int rows = max(1, min(kMostRows, 256 * U / per_row));
+  const int rounds = (rows * per_row + U * kMostThreads - 1) / (U * kMostThreads);
+  const int threads = ((rows * per_row + U * rounds - 1) / (U * rounds) + 31) / 32 * 32;
+  const size_t smem = (size_t)rows * (a.rot / 2) * sizeof(float2);  // rows of 256 U tasks at most, or one: 32 KB
+  return launch_k(a.hd > a.rot ? rotary_kernel<BF16, V, HALF, true> : rotary_kernel<BF16, V, HALF, false>, (a.T + rows - 1) / rows, threads, smem, ctx->stream, true, false, a, rows, wide);
 }
 
 }  // namespace
