@@ -1,12 +1,13 @@
 """Run a synthetic decoder layer through the C ABI: a prompt, then one token at a time.
 
     python -m int4_grouped_expert_router_gb300.run_decoder [--workload tiny] [--batch B] [--prompt N] [--steps N]
+                                                           [--rotary] [--vocab V]
 
-The layer on the device, with nothing but library calls between the residual stream going in and coming out. It has no
-positions: the library has no rotary step, which a model's q and k get between the projection and the append.
+The layer on the device, with nothing but library calls between the residual stream going in and coming out:
 
     n      = rmsnorm(h, w_in)                                    coli_norm_residual (no block)
     q,k,v  = Wqkv n                                              coli_w4_linear
+    q,k    = turned by their positions (--rotary)                coli_rotary, in place in the projection's rows
     the new k, v quantised into the paged 4-bit cache            coli_kv4_append
     a      = attention of q over the cache                       coli_kv4_attention
     o      = Wo a                                                coli_w4_linear
@@ -14,8 +15,13 @@ positions: the library has no rotary step, which a model's q and k get between t
     y      = routed int4 experts of n                            coli_router_select, coli_expert_group
     h, n   = h + rmsnorm(y, w_post2), rmsnorm(h, w_next)         coli_norm_residual
 
+and with --vocab an output head on each sequence's last row, which answers with the token to go on with:
+
+    logits = Whead n, Whead not quantised                        coli_dense_linear
+    log p of the largest entries, the entropy                    coli_logprobs
+
 Prints the event-timed microseconds of the prompt pass and of a decode step (the median), after the device error word has
-come back clean.
+come back clean, and with --vocab the mean entropy and log probability of the tokens that were taken.
 """
 from __future__ import annotations
 
@@ -36,7 +42,9 @@ class DecoderLayer:
 
     PAGE = 64
 
-    def __init__(self, ctx, cfg, q_heads, kv_heads, head_dim, gs, batch, max_len, device="cuda"):
+    def __init__(self, ctx, cfg, q_heads, kv_heads, head_dim, gs, batch, max_len, device="cuda", rotary=None):
+        """rotary: a table of coli_rotary_freqs by which q and k are turned, or None: no positions."""
+        self.rotary = rotary
         self.ctx, self.cfg, self.q_heads, self.kv_heads, self.head_dim = ctx, cfg, q_heads, kv_heads, head_dim
         self.eps = 1e-5
         self.moe = DeviceLayer(ctx, cfg)
@@ -70,6 +78,8 @@ class DecoderLayer:
         B_.coli_w4_linear(ctx, self.linear["qkv"], n, None, qkv)
         q, k, v = (t.unflatten(1, (-1, self.head_dim)) for t in
                    qkv.split([self.q_heads * self.head_dim, self.kv_heads * self.head_dim, self.kv_heads * self.head_dim], 1))
+        if self.rotary is not None:
+            B_.coli_rotary(ctx, q, k, self.rotary, q, k, lens=self.lens, q_start=start)
         B_.coli_kv4_append(ctx, self.cache, k, v, **plan)
         a = torch.empty(T, self.q_heads, self.head_dim, dtype=dt, device=dev)
         B_.coli_kv4_attention(ctx, self.cache, q, out=a, **plan)
@@ -89,6 +99,29 @@ class DecoderLayer:
             B.coli_expert_free(self.ctx, t)
 
 
+class Head:
+    """An output head: logits of a layer's normed output, the most likely token of each row and what the model makes of it."""
+
+    def __init__(self, ctx, cfg, vocab, device="cuda"):
+        self.ctx, self.vocab = ctx, vocab
+        w = synth.normal(synth.stream_seed(cfg.seed, "head"), vocab * cfg.D).reshape(vocab, cfg.D)
+        self.weight = torch.from_numpy((w * cfg.D ** -0.5).astype(np.float32)).to(torch.bfloat16)
+        self.handle = B.coli_dense_upload(ctx, self.weight)
+
+    def forward(self, n, top=1):
+        """For rows n [S x D]: dict(logits [S x V], entropy [S], top_id, top_logp [S x top])."""
+        S, dev = n.shape[0], n.device
+        out = dict(entropy=torch.empty(S, device=dev), top_id=torch.empty(S, top, dtype=torch.int32, device=dev),
+                   top_logp=torch.empty(S, top, device=dev))
+        logits = torch.empty(S, self.vocab, device=dev)
+        B.coli_dense_linear(self.ctx, self.handle, n, logits)
+        B.coli_logprobs(self.ctx, logits, **out)
+        return dict(out, logits=logits)
+
+    def free(self):
+        B.coli_dense_free(self.ctx, self.handle)
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--workload", default="tiny", choices=sorted(CONFIGS))
@@ -99,6 +132,8 @@ def main(argv=None):
     ap.add_argument("--batch", type=int, default=2)
     ap.add_argument("--prompt", type=int, default=100, help="tokens of each prompt")
     ap.add_argument("--steps", type=int, default=20, help="tokens decoded after it")
+    ap.add_argument("--rotary", action="store_true", help="turn q and k by their positions")
+    ap.add_argument("--vocab", type=int, default=0, help="end with an output head over that many tokens")
     args = ap.parse_args(argv)
     import dataclasses
     build()
@@ -106,19 +141,27 @@ def main(argv=None):
     if args.experts:
         cfg = dataclasses.replace(cfg, E=args.experts, K=min(cfg.K, args.experts))
     ctx = B.coli_init(0)
-    layer = DecoderLayer(ctx, cfg, args.heads, args.kv_heads, args.head_dim, 64, args.batch, args.prompt + args.steps)
-    times = []
+    layer = DecoderLayer(ctx, cfg, args.heads, args.kv_heads, args.head_dim, 64, args.batch, args.prompt + args.steps,
+                         rotary=B.coli_rotary_freqs(args.head_dim) if args.rotary else None)
+    head = Head(ctx, cfg, args.vocab) if args.vocab else None
+    times, answers = [], []
     for step in range(args.steps + 1):
         new = [args.prompt if step == 0 else 1] * args.batch
         h = layer.moe.act_tensor(synth.normal(synth.stream_seed(cfg.seed, "hidden", step), sum(new) * cfg.D)
                                  .reshape(-1, cfg.D))
         a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
         a.record()
-        layer.forward(h, new)
+        _, n = layer.forward(h, new)
+        if head is not None:
+            last = torch.tensor(np.cumsum(new) - 1, device=n.device)
+            answers.append(head.forward(n[last]))
         b.record()
         b.synchronize()
         times.append(a.elapsed_time(b) * 1000.0)
     rc = B.coli_check_error(ctx)
+    if head is not None:
+        entropy, logp = (torch.stack([a[name] for a in answers]).mean().item() for name in ("entropy", "top_logp"))
+        head.free()
     layer.free()
     B.coli_destroy(ctx)
     if rc != 0:
@@ -127,6 +170,8 @@ def main(argv=None):
     decode = sorted(times[1:])
     print(f"{cfg.name} batch {args.batch}: prompt of {args.prompt} {times[0]:.1f} us, decode step "
           f"{decode[len(decode) // 2] if decode else float('nan'):.1f} us (median of {len(decode)})")
+    if head is not None:
+        print(f"vocabulary of {args.vocab}: mean entropy {entropy:.3f}, mean log probability of the tokens taken {logp:.3f}")
     return 0
 
 
