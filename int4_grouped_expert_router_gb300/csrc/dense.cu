@@ -13,6 +13,8 @@
 // way. Where y is binary32 a chunk of kChunk column tiles is formed at a time and the chunks are added in registers.
 // Binary32 activations enter as parts of 8 bits by truncation, x = h + m + l exactly (two parts, 16 bits, where y is
 // rounded to 8), each multiplied with the same staged tile of W.
+#include <cuda_bf16.h>
+
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -26,7 +28,6 @@ namespace coli {
 
 namespace {
 
-constexpr float kInf = __builtin_huge_valf();
 constexpr int kEpiWarps = 16, kWarpEpi = 4;  // warps 0 and 1: producer, products; a quarter of the lanes goes by warp % 4
 constexpr int kThreads = (kWarpEpi + kEpiWarps) * 32;
 constexpr int kChunk = 4;   // column tiles
@@ -56,7 +57,7 @@ struct Shape {
   static constexpr int kAccs = EXACT && N <= 128 ? 4 : 2;
   static constexpr int kTmem = N == 192 ? 512 : kAccs * N;  // a power of two from 32 on
   static constexpr int kGroups = N / kGroup;
-  static constexpr int kMine = (kGroups + kSets - 1) / kSets;  // groups of a warp
+  static constexpr int kMine = EXACT ? (kGroups + kSets - 1) / kSets : 0;  // groups of a warp whose sums it holds
 };
 
 struct TileArgs {
@@ -142,20 +143,72 @@ __global__ void dense_x_kernel(const void* x, long long stride, int S, int I, bo
   }
 }
 
-template <int N>
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float reciprocal_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 1 / (1 + e^-x). A result that is rounded to 8 bits takes the exponential of an argument that rounds, off by about |x| units
+// in the last place, and below 2^-126 is 0. EXACT: to a few units; e^-|x| = 2^t (1 + r ln 2), t + r the product -|x| log2(e) with what its rounding and
+// the factor's lose.
+template <bool EXACT>
+__device__ __forceinline__ float dense_sigmoid(float x) {
+  if constexpr (!EXACT) {
+    return reciprocal_fast(1.f + exp2_fast(-x * kLog2e));
+  } else {
+    constexpr float kRest = (float)(1.4426950408889634074 - (double)kLog2e), kLn2 = 0.69314718f;
+    const float a = fabsf(x) > 128.f ? 128.f : fabsf(x);  // NaN stays
+    const float t = -a * kLog2e, r = fmaf(-a, kRest, fmaf(-a, kLog2e, -t));
+    float e;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));  // numbers below the normal ones stay
+    e = fmaf(e, r * kLn2, e);
+    const float s = reciprocal_fast(1.f + e);
+    return x < 0.f ? e * s : s;
+  }
+}
+
+// x/2 (1 + erf(x / sqrt 2)) = x/2 erfc(-x / sqrt 2), without cancellation on either side. erfc(a) = t 2^(P(t) - a^2 log2 e) for
+// a >= 0 and t = 1 / (1 + a/2); P is a least-squares polynomial of degree 9 at 400 Chebyshev nodes of t for a up to 10.5, fitted
+// to 40-digit values. Against those the whole is off by 3e-7 relative for a < 1 and 3e-7 a^2 above (binary32's rounding of the
+// exponent).
+__device__ __forceinline__ float dense_gelu(float x) {
+  const float a = fabsf(x) * 0.70710678118654752f, t = reciprocal_fast(fmaf(0.5f, a, 1.f));
+  float p = 0.21466025710105896f;
+  p = fmaf(p, t, -1.0125515460968018f);
+  p = fmaf(p, t, 1.740134835243225f);
+  p = fmaf(p, t, -1.0993107557296753f);
+  p = fmaf(p, t, -0.03750240430235863f);
+  p = fmaf(p, t, -0.03969155624508858f);
+  p = fmaf(p, t, 0.06400132924318314f);
+  p = fmaf(p, t, 0.5548697113990784f);
+  p = fmaf(p, t, 1.4410624504089355f);
+  p = fmaf(p, t, -1.8256721496582031f);
+  const float h = 0.5f * fabsf(x) * (t * exp2_fast(fmaf(a * a, -kLog2e, p)));
+  return x > 0.f ? x - h : -h;
+}
+
+template <bool EXACT, int N>
 __device__ __forceinline__ void dense_act(float (&z)[N], int act) {
   switch (act) {
     case COLI_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < N; i++) z[i] = z[i] / (1.f + expf(-z[i]));
+      for (int i = 0; i < N; i++) z[i] *= dense_sigmoid<EXACT>(z[i]);
       break;
     case COLI_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < N; i++) z[i] = 0.5f * z[i] * erfcf(z[i] * -0.70710678118654752f);
+      for (int i = 0; i < N; i++) z[i] = dense_gelu(z[i]);
       break;
-    case COLI_ACT_GELU_TANH:
+    case COLI_ACT_GELU_TANH:  // (1 + tanh u) / 2 = sigmoid(2 u)
 #pragma unroll
-      for (int i = 0; i < N; i++) z[i] = z[i] / (1.f + expf(-1.5957691216057308f * fmaf(0.044715f * z[i] * z[i], z[i], z[i])));
+      for (int i = 0; i < N; i++) z[i] *= dense_sigmoid<EXACT>(1.5957691216057308f * fmaf(0.044715f * z[i] * z[i], z[i], z[i]));
       break;
     case COLI_ACT_RELU:
 #pragma unroll
@@ -352,9 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   } else if (warp >= kWarpEpi) {
     // ------------------------------------- what follows -------------------------------------
     griddep_wait();
-    const int set = (warp - kWarpEpi) >> 2, row = (warp & 3) * 32 + lane;
+    // the same in a warp, and visibly: what follows from it (tokens, their rows' addresses) stays out of the lanes
+    const int set = __shfl_sync(0xffffffffu, (warp - kWarpEpi) >> 2, 0), row = (warp & 3) * 32 + lane;
     const uint32_t tm = tmem + ((uint32_t)(warp & 3) << 21);  // lanes 32 (warp % 4) on
-    bool broken = false;
+    float broken = 0.f;  // not a number once a sum was not finite
     const uint32_t acc_empty0 = PAIR ? cluster_address(smem_u32(acc_empty), 0) : 0;
     auto free_acc = [&](uint32_t i) {
       if constexpr (PAIR)
@@ -368,28 +422,32 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       uint32_t f[kTake], r[kTake];
     };
     int o, t0;  // of the tile: this thread's row, the first token
+    float bias;
+    constexpr size_t kE = EXACT ? 4 : 2;
     auto ask = [&](Beside& v, int g) {
       if (g >= H::kGroups || o >= a.d.O) return;
-      const int n = a.d.S - t0 - g * kTake;
+      const int t = t0 + g * kTake, n = a.d.S - t;
+      const uint32_t off = (uint32_t)o * kE;
       auto load = [&](const void* p, long long stride, uint32_t (&to)[kTake]) {
-        const char* at = static_cast<const char*>(p) + ((size_t)(t0 + g * kTake) * stride + o) * (EXACT ? 4 : 2);
-        const size_t step = (size_t)stride * (EXACT ? 4 : 2);
 #pragma unroll
-        for (int i = 0; i < kTake; i++, at += step)
+        for (int i = 0; i < kTake; i++) {
+          const char* at = static_cast<const char*>(p) + (t + i) * stride * kE + off;
           if (i < n) {
             if constexpr (EXACT)
               to[i] = __ldcg(reinterpret_cast<const unsigned int*>(at));
             else
               to[i] = __ldcg(reinterpret_cast<const unsigned short*>(at));
           }
+        }
       };
       if (a.d.mul) load(a.d.mul, a.d.mul_stride, v.f);
       if (a.d.resid) load(a.d.resid, a.d.resid_stride, v.r);
     };
     auto value = [](uint32_t u) { return __uint_as_float(EXACT ? u : u << 16); };
-    auto finish = [&](float (&sum)[kGroup], const Beside& v, int g, float bias) {
+    auto finish = [&](float (&sum)[kGroup], const Beside& v, int g) {
       if (o >= a.d.O) return;
-      const int n = a.d.S - t0 - g * kTake;
+      const int t = t0 + g * kTake, n = a.d.S - t;
+      const uint32_t off = (uint32_t)o * kE;
       float z[kTake];
 #pragma unroll
       for (int i = 0; i < kTake; i++) {
@@ -397,36 +455,38 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           z[i] = (sum[4 * i + 2] + sum[4 * i + 1]) + sum[4 * i];
         else
           z[i] = sum[i];
-        broken |= i < n && !(fabsf(z[i]) < kInf);
+        if (i < n) broken = fmaf(z[i], 0.f, broken);
         z[i] += bias;
       }
-      dense_act(z, a.d.act);
+      dense_act<EXACT>(z, a.d.act);
       if (a.d.mul)
 #pragma unroll
         for (int i = 0; i < kTake; i++) z[i] *= value(v.f[i]);
       if (a.d.resid)
 #pragma unroll
         for (int i = 0; i < kTake; i++) z[i] += value(v.r[i]);
-      char* at = static_cast<char*>(a.d.y) + ((size_t)(t0 + g * kTake) * a.d.y_stride + o) * (EXACT ? 4 : 2);
-      const size_t step = (size_t)a.d.y_stride * (EXACT ? 4 : 2);
 #pragma unroll
-      for (int i = 0; i < kTake; i++, at += step)
+      for (int i = 0; i < kTake; i++) {
+        char* at = static_cast<char*>(a.d.y) + (t + i) * a.d.y_stride * kE + off;
         if (i < n) {
           if constexpr (EXACT)
             *reinterpret_cast<float*>(at) = z[i];
           else
-            *reinterpret_cast<uint16_t*>(at) = f32_to_bf16_rn(z[i]);
+            *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16_rn(z[i]);
         }
+      }
+    };
+    auto at_tile = [&](int tile) {
+      o = (tile % a.rt * H::kCtas + rank) * kDenseRows + row;
+      t0 = tile / a.rt * H::kTokens;
+      bias = a.d.bias && o < a.d.O ? __ldcg(a.d.bias + o) : 0.f;
     };
     uint32_t chunk = 0;
     int k = k0, tile = tile0;
-    long long w = w0;
-    while (w < w1) {
-      const int seg = (int)min((long long)(a.kt - k), w1 - w);
+    uint32_t left = (uint32_t)(w1 - w0);
+    while (left > 0) {
+      const int seg = min(a.kt - k, (int)left);
       const bool whole = seg == a.kt;
-      o = (tile % a.rt * H::kCtas + rank) * kDenseRows + row;
-      t0 = tile / a.rt * H::kTokens;
-      const float bias = a.d.bias && o < a.d.O ? __ldcg(a.d.bias + o) : 0.f;
       Beside next;
       if constexpr (EXACT) {
         float sum[H::kMine][kGroup] = {};
@@ -455,8 +515,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           chunk++;
         }
         tmem_wait_st();
+        at_tile(tile);
         if (whole) ask(next, set);
       } else {
+        at_tile(tile);
         if (whole) ask(next, set);
         wait(&acc_full[chunk % H::kAccs], chunk / H::kAccs & 1);
         __syncwarp();
@@ -470,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           tmem_ld8(acc + g * kGroup, z);
           const Beside now = next;
           ask(next, g + kSets);
-          finish(z, now, g, bias);
+          finish(z, now, g);
         }
       } else {
         // a tile's beginning goes to the CTA's second part, a continuation to its first; four tokens of a row together
@@ -533,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
 #pragma unroll
               for (int i = 0; i < 2; i++) z[4 * i] += v[i].x, z[4 * i + 1] += v[i].y, z[4 * i + 2] += v[i].z, z[4 * i + 3] += v[i].w;
             }
-            finish(z, now, g, bias);
+            finish(z, now, g);
           }
         }
         named_sync(1 + set, 128);  // s_last is read before it is written again
@@ -542,11 +604,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       __syncwarp();
       if (lane == 0) free_acc(chunk % H::kAccs);
       chunk++;
-      w += seg;
+      left -= seg;
       k = 0;
       tile++;
     }
-    if (broken) set_error(a.d.err, COLI_E_NONFINITE);
+    if (broken != 0.f) set_error(a.d.err, COLI_E_NONFINITE);
   }
   tc_fence_before_sync();
   if constexpr (PAIR)
