@@ -34,11 +34,13 @@ constexpr int kChunk = 4;   // column tiles
 constexpr int kGroup = 8;   // tokens that a thread of the last warps takes at a time
 constexpr int kSets = kEpiWarps / 4;
 constexpr int kQuad = 4;
+constexpr size_t kInL2 = (size_t)96 << 20;  // a weight of more bytes does not stay in L2 (129 MB) beside the activations
 static_assert(kSets == kDenseCounters, "a counter for each set");
 
 // P parts of x for a staged tile of W, or kQuad: the parts of a token are four neighbouring rows of one tile (the last of them
 // 0), and their columns are added at the end. EXACT: y is binary32. PAIR: two CTAs of a cluster form 256 rows x N tokens with one
 // instruction (cta_group::2), each staging its 128 rows and half of the tokens.
+// The most tokens of a pair's tile: more running sums than 48 of a thread would not stay in registers.
 template <bool EXACT>
 constexpr int kPairTokens = EXACT ? 192 : 256;
 
@@ -406,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     // ------------------------------------- what follows -------------------------------------
     griddep_wait();
     // the same in a warp, and visibly: what follows from it (tokens, their rows' addresses) stays out of the lanes
-    const int set = __shfl_sync(0xffffffffu, (warp - kWarpEpi) >> 2, 0), row = (warp & 3) * 32 + lane;
+    const int set = EXACT ? (warp - kWarpEpi) >> 2 : __shfl_sync(0xffffffffu, (warp - kWarpEpi) >> 2, 0), row = (warp & 3) * 32 + lane;
     const uint32_t tm = tmem + ((uint32_t)(warp & 3) << 21);  // lanes 32 (warp % 4) on
     float broken = 0.f;  // not a number once a sum was not finite
     const uint32_t acc_empty0 = PAIR ? cluster_address(smem_u32(acc_empty), 0) : 0;
@@ -630,7 +632,7 @@ int launch_one(coli_ctx* ctx, TileArgs& a, const CUtensorMap& x_map, const CUten
   a.stream = nt == 1;
   // Where the weight is larger than L2 and a few tiles of tokens read it, they do so in step: as many shares for each.
   int shares = ctx->num_sms / H::kCtas;
-  if (nt > 1 && nt <= 8 && dense_bytes(a.d.O, a.d.I) > ((size_t)96 << 20)) shares = shares / nt * nt;
+  if (nt > 1 && nt <= 8 && dense_bytes(a.d.O, a.d.I) > kInL2) shares = shares / nt * nt;
   auto kern = dense_kernel<N, P, EXACT, PAIR>;
   static std::atomic<uint64_t> ready{0};  // devices (below 64) on which this instance has its attribute
   const uint64_t bit = ctx->device < 64 ? 1ull << ctx->device : 0;
@@ -657,23 +659,33 @@ int launch_one(coli_ctx* ctx, TileArgs& a, const CUtensorMap& x_map, const CUten
   return COLI_OK;
 }
 
-// Tokens of a tile, kPair for pairs of CTAs: what takes the fewest cycles by what was measured on O, I of 768 to 50021 and S
-// to 2048. A column tile takes its bytes from L2 at 64 a cycle, or its products; a shared tile takes 30 N cycles and 17 N for
-// every share of it but one. (O = I = 6144, 256 tokens: 64 a tile 34.8 us, 128 32.5, pairs 35.1; O = 2048: 17.3, 21.7, 37.5;
-// 1024 tokens: 100.5, 73.0, 63.7 and 38.5, 29.8, 36.4.)
-constexpr int kPair = 256;
-int dense_tokens(int S, int O, int I, int parts, bool exact, int num_sms) {
-  if (S <= 16) return 16;
-  const double kt = (I + kDenseCols - 1) / kDenseCols;
-  int best = 32;
+// A call's tiles: what takes the fewest cycles by what was measured on O, I of 768 to 50021 and S to 4096. A column tile takes
+// its bytes from L2 at 64 a cycle, or its products; the weight comes from memory at 22 a cycle and SM, and other tiles of tokens
+// find a tenth of it gone from L2 again, a quarter where it is larger than that; a shared tile takes 30 N
+// cycles and 17 N for every share of it but one; a pair of CTAs, which halves the tokens' bytes, 3000 (us, single CTAs and
+// pairs of 64, 128 and the most tokens a tile; O = I = 6144, 64 bf16 tokens: 17.9 21.8, 20.0 24.2 32.7; 512: 57.9 38.4, 51.5
+// 35.5 39.3; 512 f32: 115 83, 87 73 84; 4096 bf16: 414 234, - - 183; O = 2048, 256 bf16: 17.2 19.4, 17.5 20.3 33.8).
+struct Tiles {
+  int tokens;
+  bool pair;
+};
+Tiles dense_tiles(int S, int O, int I, int parts, bool exact, int num_sms) {
+  if (S <= 16) return Tiles{16, false};
+  const int most = exact ? kPairTokens<true> : kPairTokens<false>;
+  const Tiles all[] = {{32, false}, {64, false}, {128, false}, {64, true}, {128, true}, {most, true}};
+  const double kt = (I + kDenseCols - 1) / kDenseCols, bytes = (double)dense_bytes(O, I);
+  Tiles best = all[0];
   double least = 0;
-  for (int N : {32, 64, 128, kPair}) {
-    const int ctas = N == kPair ? 2 : 1, tokens = N < kPair ? N : exact ? kPairTokens<true> : kPairTokens<false>;
-    const double tiles = (double)((O + kDenseRows * ctas - 1) / (kDenseRows * ctas)) * ((S + tokens - 1) / tokens);
+  for (const Tiles& t : all) {
+    const int ctas = t.pair ? 2 : 1, N = t.tokens;
+    const int nt = (S + N - 1) / N;
+    const double tiles = (double)((O + kDenseRows * ctas - 1) / (kDenseRows * ctas)) * nt;
+    const double stream = bytes / (22.0 * num_sms) * (1 + (nt - 1) * (bytes > kInL2 ? 0.25 : 0.1));
     const double shares = std::min<double>(num_sms / ctas, tiles * kt);
-    const double unit = std::max((kDenseTile + parts * tokens / ctas * 128.0) / 64 + 16, parts * tokens * 2.0 + 80);
-    const double cycles = tiles * kt / shares * unit + tokens * (30 + 17 * std::max(1.0, std::ceil(shares / tiles)));
-    if (N == 32 || cycles < least) best = N, least = cycles;
+    const double unit = std::max((kDenseTile + parts * N / ctas * 128.0) / 64 + 16, parts * N * 2.0 + 80);
+    const double cycles = std::max(tiles * kt / shares * unit, stream) + N * (30 + 17 * std::max(1.0, std::ceil(shares / tiles))) +
+                          (t.pair ? 3000 : 0);
+    if (least == 0 || cycles < least) best = t, least = cycles;
   }
   return best;
 }
@@ -708,8 +720,8 @@ int launch_dense(coli_ctx* ctx, const DenseArgs& args, const CUtensorMap& w_map,
   const long long row = a.d.S == 1 ? (a.d.I + 7) / 8 * 8 : a.d.x_stride;
   const bool direct = parts == 1 && (uintptr_t)a.d.x % 16 == 0 && row % 8 == 0;
   const int S = a.d.S;
-  const int N = dense_tokens(S, a.d.O, a.d.I, parts, exact, ctx->num_sms);
-  const int box = N < kPair ? N : (exact ? kPairTokens<true> : kPairTokens<false>) / 2;
+  const Tiles t = dense_tiles(S, a.d.O, a.d.I, parts, exact, ctx->num_sms);
+  const int box = t.pair ? t.tokens / 2 : t.tokens;
   CUtensorMap map{};
   if (direct) {
     rc = encode_rows_map(ctx, &map, const_cast<void*>(a.d.x), S, a.d.I, row, kDenseCols, box, true);
@@ -732,13 +744,15 @@ int launch_dense(coli_ctx* ctx, const DenseArgs& args, const CUtensorMap& w_map,
   auto tokens = [&](auto p, auto y32) {
     constexpr int P = decltype(p)::value;
     constexpr bool E = decltype(y32)::value;
-    switch (N) {
-      case 16: return launch_one<16, P, E, false>(ctx, a, map, w_map);
-      case 32: return launch_one<32, P, E, false>(ctx, a, map, w_map);
-      case 64: return launch_one<64, P, E, false>(ctx, a, map, w_map);
-      case 128: return launch_one<128, P, E, false>(ctx, a, map, w_map);
+    if (t.pair) {
+      if (t.tokens == 64) return launch_one<64, P, E, true>(ctx, a, map, w_map);
+      if (t.tokens == 128) return launch_one<128, P, E, true>(ctx, a, map, w_map);
+      return launch_one<kPairTokens<E>, P, E, true>(ctx, a, map, w_map);
     }
-    return launch_one<kPairTokens<E>, P, E, true>(ctx, a, map, w_map);
+    if (t.tokens == 16) return launch_one<16, P, E, false>(ctx, a, map, w_map);
+    if (t.tokens == 32) return launch_one<32, P, E, false>(ctx, a, map, w_map);
+    if (t.tokens == 64) return launch_one<64, P, E, false>(ctx, a, map, w_map);
+    return launch_one<128, P, E, false>(ctx, a, map, w_map);
   };
   if (parts == kQuad) return launch_one<16, kQuad, true, false>(ctx, a, map, w_map);
   if (parts == 3) return tokens(std::integral_constant<int, 3>{}, std::true_type{});

@@ -285,9 +285,10 @@ def test_refusals(ctx):
 
 @pytest.mark.parametrize("x_dtype,y", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f32", "bf16")])
 @pytest.mark.parametrize("S,I,O_", [(60, 1030, 4001), (300, 320, 6100), (600, 700, 4000), (2100, 1030, 5001), (700, 2050, 12001),
-                                    (260, 6144, 9001)])
+                                    (260, 6144, 9001), (100, 2048, 6144), (512, 2048, 6144), (225, 76, 53865), (396, 66, 61170),
+                                    (134, 73, 82442)])
 def test_every_tile_of_tokens(ctx, S, I, O_, x_dtype, y):
-    """Sizes at which tiles of 32, 64, 128 tokens and pairs of CTAs are chosen, shared by CTAs or not, and a weight larger than
+    """Sizes at which tiles of 32, 64, 128 tokens and pairs of CTAs with 64, 128 and more are chosen, shared by CTAs or not, and a weight larger than
     L2 that two tiles of tokens read in step. In norm: see close(); a bf16 result rounds to 2^-9 on average."""
     g = torch.Generator(device="cuda").manual_seed(S)
     W = (0.05 * torch.randn(O_, I, device="cuda", generator=g)).bfloat16()
