@@ -106,8 +106,9 @@ COLI_API int coli_check_error(coli_ctx *ctx);
 /* Pre-size the workspace for calls up to these sizes so that no later compute call allocates.
  * Without it, a compute call that needs more workspace than the last one allocates (once) and frees
  * the old one, whose address a graph captured before still holds: reserve before capturing. The sizes
- * are those of the router and expert calls; coli_kv4_attention has memory of its own, of one size (two
- * partial results of 256 rows per SM, 40 MB), which this call also allocates. */
+ * are those of the router and expert calls, and of coli_dense_linear with rows of up to the larger of max_D and max_I columns;
+ * coli_kv4_attention and coli_dense_linear share memory for partial results, of one size (two of 256 rows per SM, 40 MB), which
+ * this call also allocates. */
 COLI_API int coli_reserve(coli_ctx *ctx, int max_S, int max_E, int max_K, int max_D, int max_I);
 
 /* Per-kernel timing: when on, every kernel launch of this context is bracketed by two CUDA events
@@ -526,8 +527,9 @@ COLI_API int coli_dense_shape(coli_ctx *ctx, uint64_t handle, int *O, int *I);
 COLI_API int coli_dense_free(coli_ctx *ctx, uint64_t handle);
 
 /*
- * I and O have to be the weight's. x [S x I] in x_dtype; y, mul, resid [S x O] in y_dtype (any pairing of the two); rows a stride apart (elements). bias [O] f32.
- * bias, mul, resid: NULL for none. act:
+ * I and O have to be the weight's. x [S x I] in x_dtype; y, mul, resid [S x O] in y_dtype (any pairing of the two); the elements
+ * of a row contiguous, rows a stride apart (elements; of one row it says nothing). bias [O] f32. bias, mul, resid: NULL for none.
+ * act:
  *   COLI_ACT_NONE       z
  *   COLI_ACT_SILU       z / (1 + exp(-z))
  *   COLI_ACT_GELU       z/2 (1 + erf(z / sqrt 2))
@@ -535,10 +537,14 @@ COLI_API int coli_dense_free(coli_ctx *ctx, uint64_t handle);
  *   COLI_ACT_RELU       max(z, 0)
  *   COLI_ACT_RELU2      max(z, 0)^2
  * y may be mul or resid (same address and stride); no other overlap of y with an input. 1 <= S <= COLI_MAX_TOKENS.
- * Products of bfloat16 values are exact, binary32 activations enter as three bfloat16 parts that add up to them, and sums are
- * held in binary32; y is rounded once. Results do not change from run to run. A product that is not finite sets
- * COLI_E_NONFINITE, and spoils its row of x (its row of W) alone. Binary32 activations, and rows of x that do not start at
- * 16-byte boundaries, are first laid out in the workspace (coli_reserve). Profiled as COLI_KERNEL_LINEAR.
+ * Products of bfloat16 values are exact; binary32 activations enter as three bfloat16 parts that add up to them (two, 16 bits,
+ * where y is bfloat16). Sums are held in binary32, as the tensor core cuts them off (towards zero); where y is binary32 they are
+ * added in registers every 256 columns. y is rounded once. Results do not change from run to run; a row's depend on S (tiles are
+ * chosen by the sizes). A sum of products that is not finite sets COLI_E_NONFINITE; what is not finite in x or W spoils the outputs
+ * of its own row alone.
+ * Binary32 activations, and rows of x that do not start at 16-byte boundaries, are first laid out in the workspace: for a call
+ * that is captured, coli_reserve first, or run a call of the size; it also allocates the memory for shared tiles. A wait inside
+ * a kernel is bounded (2 s), after which the call sets COLI_E_TIMEOUT and its output is void. Profiled as COLI_KERNEL_LINEAR.
  */
 #define COLI_ACT_NONE 0
 #define COLI_ACT_SILU 1
@@ -555,7 +561,7 @@ COLI_API int coli_dense_linear(coli_ctx *ctx, uint64_t W, int I, int O, const vo
  *   z = scale x,  log p_v = z_v - log(sum_u exp(z_u)).
  * Outputs, each NULL if not wanted (one at least is):
  *   logp [S x n] f32: log p of the given tokens [S x n] (int32); a negative token stands for none and gives 0, one >= V sets
- *     COLI_E_RANGE and gives NaN. tokens and logp come together, 1 <= n <= V of any size.
+ *     COLI_E_RANGE and gives NaN. tokens and logp come together, n >= 1.
  *   entropy [S] f32: -sum p log p.
  *   top_id, top_logp [S x k]: the k entries with the largest logits in descending order and their log p, equal ones by index;
  *     k <= COLI_MAX_TOP, both or neither. Entries of -infinity (forbidden tokens) are no alternatives: slots that are left over

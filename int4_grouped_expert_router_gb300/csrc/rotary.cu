@@ -164,15 +164,43 @@ __device__ __forceinline__ R pack(const float (&v)[V]) {
   return raw;
 }
 
-// Tasks of a thread whose loads are under way together.
-template <int V>
-constexpr int kTasks = V == 1 ? 4 : 2;
+// Positions of the CTA's rows, and the scaled cosine and sine of each pair; `my_freq` is the frequency of the thread's first
+// entry of the table, asked for ahead.
+__device__ __forceinline__ unsigned long long first_freq(const RotaryArgs& a, int here) {
+  const int half = a.rot / 2;
+  return (int)threadIdx.x < half * here ? __ldcg(reinterpret_cast<const unsigned long long*>(a.freqs) + threadIdx.x % half) : 0;
+}
+__device__ __forceinline__ void make_table(const RotaryArgs& a, int row0, int here, unsigned long long my_freq, long long* s_pos,
+                                           float2* s_turn) {
+  const int tid = threadIdx.x, half = a.rot / 2;
+  if (tid < 32) find_positions(a, row0, here, s_pos);
+  __syncthreads();
+  for (int i = tid; i < here * half; i += blockDim.x) {
+    const int r = i / half;
+    const long long pos = s_pos[r];
+    if (pos < kGone) {
+      const unsigned long long freq = i == tid ? my_freq : __ldcg(reinterpret_cast<const unsigned long long*>(a.freqs) + (i - r * half));
+      const uint32_t turn = (uint32_t)(((uint64_t)pos * freq) >> 32);
+      float sine, cosine;
+      sincospif((float)(int)turn * 4.656612873077393e-10f, &sine, &cosine);  // 2^-31
+      s_turn[i] = make_float2(cosine * a.scale, sine * a.scale);
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void rotate(float& p, float& q, float2 cs) {
+  const float c = fmaf(p, cs.x, -q * cs.y), d = fmaf(q, cs.x, p * cs.y);
+  p = c, q = d;
+}
+
+constexpr int kTasks = 2;  // tasks of a thread whose loads are under way together
 
 // Vectors of V elements. A task is two of them (two halves' worth of V pairs, or 2 V neighbouring channels); behind the turned
 // part (COPY) two neighbouring ones that are copied, where there is an even number of them (`wide`), or one.
 template <bool BF16, int V, bool HALF, bool COPY>
 __global__ void __launch_bounds__(kMostThreads, kCtas) rotary_kernel(RotaryArgs a, int rows, bool wide) {
-  constexpr int E = BF16 ? 2 : 4, U = kTasks<V>;
+  constexpr int E = BF16 ? 2 : 4, U = kTasks;
   using R = typename Vec<V * E>::T;
   extern __shared__ float2 s_turn[];  // [rows][rot / 2] cosine, sine
   __shared__ long long s_pos[kMostRows];
@@ -210,8 +238,7 @@ __global__ void __launch_bounds__(kMostThreads, kCtas) rotary_kernel(RotaryArgs 
   const int apart = (HALF ? half : V) * E;  // bytes between a task's vectors
 
   bool made = false;
-  const unsigned long long* freqs = reinterpret_cast<const unsigned long long*>(a.freqs);
-  const unsigned long long my_freq = tid < half * here ? __ldcg(freqs + tid % half) : 0;  // of the thread's first pair
+  const unsigned long long my_freq = first_freq(a, here);
   for (int first = 0; first < tasks; first += threads * U) {
     Task t[U];
     R x[U][2];
@@ -230,20 +257,7 @@ __global__ void __launch_bounds__(kMostThreads, kCtas) rotary_kernel(RotaryArgs 
     }
     if (!made) {
       made = true;
-      if (tid < 32) find_positions(a, row0, here, s_pos);
-      __syncthreads();
-      for (int i = tid; i < here * half; i += threads) {
-        const int r = i / half;
-        const long long pos = s_pos[r];
-        if (pos < kGone) {
-          const unsigned long long freq = i == tid ? my_freq : __ldcg(freqs + (i - r * half));
-          const uint32_t turn = (uint32_t)(((uint64_t)pos * freq) >> 32);
-          float sine, cosine;
-          sincospif((float)(int)turn * 4.656612873077393e-10f, &sine, &cosine);  // 2^-31
-          s_turn[i] = make_float2(cosine * a.scale, sine * a.scale);
-        }
-      }
-      __syncthreads();
+      make_table(a, row0, here, my_freq, s_pos, s_turn);
     }
 #pragma unroll
     for (int u = 0; u < U; u++) {
@@ -255,13 +269,9 @@ __global__ void __launch_bounds__(kMostThreads, kCtas) rotary_kernel(RotaryArgs 
         float v[2][V];
         unpack<BF16, V>(x[u][0], v[0]);
         unpack<BF16, V>(x[u][1], v[1]);
-        auto rotate = [&](float& p, float& q, float2 cs) {
-          const float c = fmaf(p, cs.x, -q * cs.y), d = fmaf(q, cs.x, p * cs.y);
-          p = c, q = d;
-        };
 #pragma unroll
         for (int i = 0; i < V; i++) {
-          if constexpr (HALF || V == 1)
+          if constexpr (HALF)
             rotate(v[0][i], v[1][i], turn[i]);
           else
             rotate(v[2 * i / V][2 * i % V], v[2 * i / V][2 * i % V + 1], turn[i]);
@@ -276,12 +286,94 @@ __global__ void __launch_bounds__(kMostThreads, kCtas) rotary_kernel(RotaryArgs 
   check_plan(a);
 }
 
+// Rows whose pairs do not lie in whole vectors (an odd half, an odd stride): runs of heads pass through shared memory, read and
+// written in 16-byte vectors as far as the run's own alignment goes, and are turned there element by element. A CTA takes `heads`
+// heads (of q, then of k) of `rows` rows. 3001 rows of 40 heads of 80, 38 channels turned, bf16: 21.4 us; two elements a task of
+// the other kernel took 31 us.
+template <bool BF16, bool HALF>
+__global__ void __launch_bounds__(kMostThreads) rotary_run_kernel(RotaryArgs a, int rows, int heads, int runs_q, int runs) {
+  using T = std::conditional_t<BF16, uint16_t, uint32_t>;  // an element's bits
+  constexpr int E = sizeof(T);
+  extern __shared__ uint4 s_raw[];  // [rows][the run, from its offset in a vector on], then the table
+  __shared__ long long s_pos[kMostRows];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x, lane = tid & 31, half = a.rot / 2;
+  const int group = blockIdx.x / runs, run = blockIdx.x - group * runs;
+  const int row0 = group * rows, here = min(rows, a.T - row0);
+  const RotarySide& side = a.side[run >= runs_q];
+  const int head0 = (run >= runs_q ? run - runs_q : run) * heads, n = min(heads, side.heads - head0);
+  const int bytes = n * a.hd * E, pitch = (heads * a.hd * E + 15) / 16 + 1;  // of a row in shared memory, in vectors
+  float2* s_turn = reinterpret_cast<float2*>(s_raw + rows * pitch);
+  auto at = [&](const void* p, long long stride, int r) {
+    return static_cast<const char*>(p) + ((row0 + r) * stride + (long long)head0 * a.hd) * E;
+  };
+  const unsigned long long my_freq = first_freq(a, here);
+  // vector v of row r: whole, or its elements that belong to the run
+  auto each = [&](auto&& whole, auto&& element) {
+    for (int i = tid; i < here * pitch; i += blockDim.x) {
+      const int r = i / pitch, v = i - r * pitch, off = (int)((uintptr_t)at(side.in, side.in_stride, r) & 15);
+      if (v * 16 >= off && v * 16 + 16 <= off + bytes)
+        whole(r, i, v * 16 - off);
+      else
+#pragma unroll 1
+        for (int b = max(v * 16, off); b < min(v * 16 + 16, off + bytes); b += E) element(r, i * 16 + b - v * 16, b - off);
+    }
+  };
+  char* s_bytes = reinterpret_cast<char*>(s_raw);
+  each([&](int r, int i, int b) { s_raw[i] = __ldcg(reinterpret_cast<const uint4*>(at(side.in, side.in_stride, r) + b)); },
+       [&](int r, int i, int b) { *reinterpret_cast<T*>(s_bytes + i) = load_cg<T>(at(side.in, side.in_stride, r) + b); });
+  make_table(a, row0, here, my_freq, s_pos, s_turn);
+  for (int w = tid >> 5; w < here * n; w += blockDim.x >> 5) {
+    const int r = w / n;
+    if (s_pos[r] >= kGone) continue;
+    const int off = (int)((uintptr_t)at(side.in, side.in_stride, r) & 15);
+    T* x = reinterpret_cast<T*>(s_bytes + r * pitch * 16 + off) + (w - r * n) * a.hd;
+    for (int i = lane; i < half; i += 32) {
+      T &p = x[HALF ? i : 2 * i], &q = x[HALF ? half + i : 2 * i + 1];
+      float u = BF16 ? bf16_to_f32((uint16_t)p) : __uint_as_float(p), v = BF16 ? bf16_to_f32((uint16_t)q) : __uint_as_float(q);
+      rotate(u, v, s_turn[r * half + i]);
+      p = BF16 ? f32_to_bf16_rn(u) : __float_as_uint(u), q = BF16 ? f32_to_bf16_rn(v) : __float_as_uint(v);
+    }
+  }
+  __syncthreads();
+  auto out = [&](int r) { return const_cast<char*>(at(side.out, side.out_stride, r)); };
+  each(
+      [&](int r, int i, int b) {
+        if (s_pos[r] == kGone) return;
+        char* to = out(r) + b;
+        if (((uintptr_t)to & 15) == 0)
+          *reinterpret_cast<uint4*>(to) = s_raw[i];
+        else
+#pragma unroll
+          for (int e = 0; e < 16 / E; e++) reinterpret_cast<T*>(to)[e] = reinterpret_cast<const T*>(s_raw + i)[e];
+      },
+      [&](int r, int i, int b) {
+        if (s_pos[r] != kGone) *reinterpret_cast<T*>(out(r) + b) = *reinterpret_cast<const T*>(s_bytes + i);
+      });
+  check_plan(a);
+}
+
+template <bool BF16, bool HALF>
+cudaError_t launch_runs(coli_ctx* ctx, const RotaryArgs& a) {
+  constexpr int E = BF16 ? 2 : 4, kBytes = 12 * 1024;  // of a CTA's runs
+  const int head = a.hd * E, most = max(a.side[0].heads, a.side[1].heads);
+  const int heads = max(1, min(most, kBytes / head));
+  const int runs_q = (a.side[0].heads + heads - 1) / heads, runs = runs_q + (a.side[1].heads + heads - 1) / heads;
+  const int rows = max(1, min(kMostRows, kBytes / (heads * head)));
+  const size_t smem = (size_t)rows * ((heads * head + 15) / 16 + 1) * 16 + (size_t)rows * (a.rot / 2) * sizeof(float2);
+  // at most 12 KB of runs and two vectors a row; a table of rows * rot / 2 pairs, half of the elements at most: 24 KB
+  const long long groups = (a.T + rows - 1) / rows;
+  return launch_k(rotary_run_kernel<BF16, HALF>, (int)(groups * runs), kMostThreads, smem, ctx->stream, true, false, a, rows, heads, runs_q,
+                  runs);
+}
+
 template <bool BF16, int V, bool HALF>
 cudaError_t launch_one(coli_ctx* ctx, const RotaryArgs& a) {
   const bool wide = (a.hd - a.rot) % (2 * V) == 0;
   const int per_row = (a.rot / 2 / V + (a.hd - a.rot) / (wide ? 2 * V : V)) * (a.side[0].heads + a.side[1].heads);
   // whole rows, as many as keep a CTA busy, and threads that share their tasks evenly
-  constexpr int U = kTasks<V>;
+  constexpr int U = kTasks;
   const int rows = max(1, min(kMostRows, 256 * U / per_row));
   const int rounds = (rows * per_row + U * kMostThreads - 1) / (U * kMostThreads);
   const int threads = ((rows * per_row + U * rounds - 1) / (U * rounds) + 31) / 32 * 32;
@@ -311,7 +403,7 @@ int launch_rotary(coli_ctx* ctx, const RotaryArgs& args, int dtype, bool interle
     constexpr bool kBf16 = decltype(bf16)::value;
     if (at % 16 == 0) return interleaved ? launch_one<kBf16, decltype(v16)::value, false>(ctx, a) : launch_one<kBf16, decltype(v16)::value, true>(ctx, a);
     if (at % 8 == 0) return interleaved ? launch_one<kBf16, decltype(v8)::value, false>(ctx, a) : launch_one<kBf16, decltype(v8)::value, true>(ctx, a);
-    return interleaved ? launch_one<kBf16, 1, false>(ctx, a) : launch_one<kBf16, 1, true>(ctx, a);
+    return interleaved ? launch_runs<kBf16, false>(ctx, a) : launch_runs<kBf16, true>(ctx, a);
   };
   if (dtype == COLI_DTYPE_BF16)
     e = pick(std::true_type{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});

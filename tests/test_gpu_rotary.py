@@ -68,6 +68,37 @@ def test_heads(ctx, hd, rot, interleaved, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,hq,hk,hd,rot", [(70, 9, 4, 80, 38), (33, 100, 3, 130, 130), (3, 0, 2, 1022, 1022), (40, 1, 0, 6, 2), (5, 7, 7, 1023, 1022)])
+def test_heads_that_are_no_whole_vectors(ctx, T, hq, hk, hd, rot, interleaved, dtype):
+    """Runs of heads that start anywhere in a vector, outputs that start elsewhere, few and many heads, in place and apart."""
+    freqs = B.coli_rotary_freqs(rot, 1000.0)
+    pos = rng("runs", T).integers(-9000, 9000, size=T)
+    sides = []
+    for heads, out_shift in ((hq, 0), (hk, 3)):
+        if not heads:
+            sides.append((None, None, None))
+            continue
+        x, xt = make(T, heads, hd, dtype, heads)
+        buf = torch.full((T * (heads * hd + 5) + 8,), 7.0, dtype=xt.dtype, device="cuda")
+        out = buf[out_shift:out_shift + T * (heads * hd + 5)].view(T, -1)[:, :heads * hd].unflatten(1, (heads, hd))
+        sides.append((x, xt, (buf, out)))
+    q, k = sides
+    B.coli_rotary(ctx, q[1], k[1], freqs, None if q[0] is None else q[2][1], None if k[0] is None else k[2][1],
+                  positions=i32(pos.tolist()), interleaved=interleaved, scale=0.5)
+    assert B.coli_check_error(ctx) == 0
+    for x, xt, rest in (q, k):
+        if x is None:
+            continue
+        buf, out = rest
+        check(out, x, freqs.cpu().numpy(), pos, interleaved, 0.5, dtype)
+        B.coli_rotary(ctx, xt, None, freqs, xt, None, positions=i32(pos.tolist()), interleaved=interleaved, scale=0.5)
+        assert torch.equal(xt, out)
+        out.fill_(7.0)
+        assert (buf == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,hq,hk", [(1, 64, 8), (1, 1, 1), (300, 1, 1), (700, 5, 1), (65, 40, 3)])
 def test_rows_and_heads(ctx, T, hq, hk, dtype):
     freqs = B.coli_rotary_freqs(16, 500.0)
