@@ -1,18 +1,33 @@
 // y = resid + act(W x + bias) * mul with 16-bit weights (layout: dense.h), on the fifth-generation tensor cores.
 //
-// D = W X^T: the rows of W are the instruction's M (128), the tokens its N (16 to 256, the smallest that covers S, or 256).
-// Units of work are (128 rows x N tokens) tiles times column tiles of 64, dealt out evenly and contiguously to one CTA per SM,
-// so that one token keeps every SM streaming a contiguous run of W, and many tokens leave no part of a wave idle. A tile that
-// several CTAs share is joined by the one that arrives last, in CTA order, so results do not depend on who that is.
+// D = W X^T: the rows of W are the instruction's M (128, or 256 of a pair of CTAs), the tokens its N (16 to 256). Units of work
+// are such tiles times column tiles of 64, dealt out evenly and contiguously to one CTA per SM (or pair), so that one token keeps
+// every SM streaming a contiguous run of W, and many tokens leave no part of a wave idle. A tile that several shares have a part
+// of is joined by the one that arrives last, in the order of the shares, so results do not depend on who that is.
 //
 // One CTA, 20 warps: a producer (W by bulk copies, x by tiled ones, a ring of stages), a thread that issues the products, and
 // sixteen warps for what follows (bias, activation, factor, residual), which take a tile from tensor memory while the next one
-// is being formed in the other half of it. The ring is filled with weights before the work ahead in the stream is waited for.
+// is being formed in another part of it. The ring is filled with weights before the work ahead in the stream is waited for.
+// Threads hold rows of W (128 neighbouring outputs of a token), so that rows of y at any alignment are read and written whole.
 //
-// Sums. The tensor core cuts a sum off where binary32 would round it, always towards zero, and 6144 products leave 2^-17 that
-// way. Where y is binary32 a chunk of kChunk column tiles is formed at a time and the chunks are added in registers.
-// Binary32 activations enter as parts of 8 bits by truncation, x = h + m + l exactly (two parts, 16 bits, where y is
-// rounded to 8), each multiplied with the same staged tile of W.
+// Sums. The tensor core cuts a sum off where binary32 would round it, always towards zero: 6144 products lose some 2^-17 that
+// way. Where y is binary32 chunks of kChunk column tiles are formed by themselves and added in registers (24 us of 203 for the
+// prompt below; twice as long chunks would cost 10 and lose twice as much). Errors against 64 bits, in norm: 2.7e-7 for 6144
+// columns of bf16, 7.6e-7 of binary32; a binary32 product sum by sum: 8.6e-7, 1.4e-6.
+// Binary32 activations enter as parts of 8 bits by truncation, x = h + m + l exactly (two parts, 16 bits, where y is rounded to 8),
+// each multiplied with the same staged tile of W; of up to four tokens the parts are rows of one tile.
+//
+// Measured (us; W = O x I): one token, 6144 x 6144, residual 15.0 (5.0 TB/s, 0.74 of a copy's rate), f32 18.3; 24 tokens, 50021 x
+// 6144, f32 logits 92 (6.7 TB/s, 0.98): bound by W's bytes, and at the small end by launch, first stages and the join of parts (4
+// us). 301 f32 tokens, 2048 x 6144, silu and factor 34: L2 bytes and the join. 4096 tokens, 6144 x 6144, gelu, bias, residual
+// 195 (1590 TFLOP/s, 0.82 of a library product's burst rate; the bare product 179, the library's 160): tensor pipe active 80 %
+// of the time.
+// What it cost to find: factor and residual read where they are used, not a group ahead (prompt 348 us; 252 so); one CTA's 128 x
+// 256 tiles, which ask L2 for 96 bytes a cycle and SM (219 us bare; pairs 183); 24 bytes of spilled registers inside the loop over
+// chunks (480 us instead of 214: the ring leaves no first-level cache); token tiles numbered before rows, so that W came from
+// memory once for each (512 tokens, 50021 rows: 392 us, 192 so); precise exponentials, divisions and erfc (silu of 1748 x 20122:
+// 120 us, 77 so). Dropped: setmaxnreg to give the last warps more registers (the producer spills), spare warps that lay out x
+// stage by stage instead of a kernel ahead (f32 token 23.9 us against 18.3), tiles of 256 running sums (463 us).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -418,7 +433,9 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       else
         mbar_arrive(&acc_empty[i]);
     };
-    // A tile's rows from this thread's, a group of tokens at a time. What is read beside the sums is asked for a group ahead.
+    // A tile's rows from this thread's, a group of tokens at a time. What is read beside the sums is asked for a group ahead. Many
+    // tokens' arrays pass through L2 as the first to go, so that W and x stay (1748 x 1472 x 20122, silu, factor and residual:
+    // 123 us without, 116 so).
     constexpr int kTake = H::kTake;
     struct Beside {
       uint32_t f[kTake], r[kTake];
@@ -434,12 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < kTake; i++) {
           const char* at = static_cast<const char*>(p) + (t + i) * stride * kE + off;
-          if (i < n) {
-            if constexpr (EXACT)
-              to[i] = __ldcg(reinterpret_cast<const unsigned int*>(at));
-            else
-              to[i] = __ldcg(reinterpret_cast<const unsigned short*>(at));
-          }
+          using T = std::conditional_t<EXACT, unsigned int, unsigned short>;
+          if (i < n) to[i] = PAIR ? __ldcs(reinterpret_cast<const T*>(at)) : __ldcg(reinterpret_cast<const T*>(at));
         }
       };
       if (a.d.mul) load(a.d.mul, a.d.mul_stride, v.f);
@@ -470,11 +483,17 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
 #pragma unroll
       for (int i = 0; i < kTake; i++) {
         char* at = static_cast<char*>(a.d.y) + (t + i) * a.d.y_stride * kE + off;
+        using T = std::conditional_t<EXACT, float, unsigned short>;
+        T v;
+        if constexpr (EXACT)
+          v = z[i];
+        else
+          v = __bfloat16_as_ushort(__float2bfloat16_rn(z[i]));
         if (i < n) {
-          if constexpr (EXACT)
-            *reinterpret_cast<float*>(at) = z[i];
+          if constexpr (PAIR)
+            __stcs(reinterpret_cast<T*>(at), v);
           else
-            *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16_rn(z[i]);
+            *reinterpret_cast<T*>(at) = v;
         }
       }
     };
