@@ -569,7 +569,7 @@ COLI_API int coli_dense_linear(coli_ctx *ctx, uint64_t W, int I, int O, const vo
  * Entries of -infinity have probability 0. A row that has nothing else gives log p = -infinity and entropy 0. A NaN or
  * +infinity sets COLI_E_NONFINITE; its row is NaN, its ids -1. Sums and logarithms are held in binary32, relative to the largest
  * entry. scale, the inverse temperature, from 1e-30 to 1e30. 1 <= S <= COLI_MAX_TOKENS, V <= COLI_MAX_VOCAB, n <= COLI_MAX_VOCAB.
- * Results do not change from run to run. Profiled as COLI_KERNEL_LOGPROBS.
+ * No output overlaps another array. Results do not change from run to run. Profiled as COLI_KERNEL_LOGPROBS.
  */
 COLI_API int coli_logprobs(coli_ctx *ctx, const void *logits, long long stride, int dtype, int S, int V, float scale,
                            const int32_t *tokens, int n, float *logp, float *entropy, int k, int32_t *top_id,

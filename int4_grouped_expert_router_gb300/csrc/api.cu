@@ -892,24 +892,35 @@ static int kv4_check(coli_ctx* ctx, const char* who, const coli_kv4_cache* cache
   return COLI_OK;
 }
 
-// Whether T rows of row_a bytes from a on, sa bytes apart, share a byte with T rows of row_b bytes from b on, sb apart (strides
-// of at least a row).
-static bool rows_overlap(uintptr_t a, long long sa, long long row_a, uintptr_t b, long long sb, long long row_b, int T) {
-  const long long d = (long long)(b - a);  // row j of b lies d + j sb - i sa after row i of a
-  if (d >= (T - 1) * sa + row_a || -d >= (T - 1) * sb + row_b) return false;
+// Rows of `row` bytes, `stride` bytes apart (at least a row).
+struct Rows {
+  const void* at;
+  long long stride, row;
+  int n;
+};
+// An array without gaps.
+static Rows one_row(const void* at, long long bytes) { return Rows{at, bytes, bytes, 1}; }
+
+// Whether two arrays of rows share a byte. NULL shares none.
+static bool rows_overlap(const Rows& a, const Rows& b) {
+  if (!a.at || !b.at) return false;
+  const long long d = (long long)((uintptr_t)b.at - (uintptr_t)a.at);  // row j of b lies d + j b.stride - i a.stride after row i of a
+  if (d >= (a.n - 1) * a.stride + a.row || -d >= (b.n - 1) * b.stride + b.row) return false;
   auto meet = [&](long long i, long long j) {
-    const long long off = d + j * sb - i * sa;
-    return i >= 0 && i < T && j >= 0 && j < T && off < row_a && -off < row_b;
+    const long long off = d + j * b.stride - i * a.stride;
+    return i >= 0 && i < a.n && j >= 0 && j < b.n && off < a.row && -off < b.row;
   };
-  if (sa == sb) {  // slices of one array: only i - j counts
-    const long long k = d / sa;
+  if (a.stride == b.stride) {  // slices of one array: only i - j counts
+    const long long k = d / a.stride;
     for (long long i = k - 1; i <= k + 1; i++)
       if (i < 0 ? meet(0, -i) : meet(i, 0)) return true;
     return false;
   }
-  for (long long i = 0; i < T; i++) {
-    const long long j = (i * sa - d) / sb;
-    if (meet(i, j - 1) || meet(i, j) || meet(i, j + 1)) return true;
+  if (a.n > b.n) return rows_overlap(b, a);
+  for (long long i = 0; i < a.n; i++) {
+    // the rows of b that begin before row i of a ends: the last of them, if it reaches that far
+    const long long j = std::min<long long>(b.n - 1, (i * a.stride + a.row - d - 1) / b.stride);
+    if (meet(i, j)) return true;
   }
   return false;
 }
@@ -972,7 +983,7 @@ int coli_kv4_attention(coli_ctx* ctx, const coli_kv4_cache* cache, const void* q
   if (q_stride < row || out_stride < row)
     return fail(ctx, COLI_E_INVAL, "kv4_attention: row stride below q_heads * head_dim");
   const long long elem = dtype == COLI_DTYPE_F32 ? 4 : 2;
-  if (rows_overlap((uintptr_t)q, q_stride * elem, row * elem, (uintptr_t)out, out_stride * elem, row * elem, T))
+  if (rows_overlap(Rows{q, q_stride * elem, row * elem, T}, Rows{out, out_stride * elem, row * elem, T}))
     return fail(ctx, COLI_E_INVAL, "kv4_attention: out overlaps q");
   if (!(scale == scale) || scale - scale != 0.f) return fail(ctx, COLI_E_INVAL, "kv4_attention: scale must be finite");
   if (window < 0) return fail(ctx, COLI_E_INVAL, "kv4_attention: window must not be negative");
@@ -1045,24 +1056,25 @@ int coli_rotary(coli_ctx* ctx, const void* q, long long q_stride, void* q_out, l
     if (T == 1) s.in_stride = s.out_stride = row;  // of one row it says nothing
     if (s.in_stride < row || s.out_stride < row) return fail(ctx, COLI_E_INVAL, "rotary: row stride below heads * head_dim");
   }
-  auto overlap = [&](const RotarySide& out, const RotarySide& other, bool other_in) {
-    if (!out.in || !other.in) return false;
-    const long long e = (long long)elem;
-    return rows_overlap((uintptr_t)out.out, out.out_stride * e, (long long)out.heads * head_dim * e,
-                        (uintptr_t)(other_in ? other.in : other.out), (other_in ? other.in_stride : other.out_stride) * e,
-                        (long long)other.heads * head_dim * e, T);
-  };
-  for (int i = 0; i < 2; i++) {
-    const RotarySide &s = a.side[i], &o = a.side[1 - i];
-    const bool in_place = s.in == s.out && s.in_stride == s.out_stride;
-    if ((!in_place && overlap(s, s, true)) || overlap(s, o, true) || (i == 0 && overlap(s, o, false)))
-      return fail(ctx, COLI_E_INVAL, "rotary: an output overlaps another array");
-  }
   if (positions) {
     if (q_start || lens || B != 0) return fail(ctx, COLI_E_INVAL, "rotary: positions or a plan, not both");
   } else {
     if (!lens || B < 1 || B > COLI_MAX_KV_SEQS) return fail(ctx, COLI_E_INVAL, "rotary: without positions, lens and 1 to COLI_MAX_KV_SEQS sequences");
     if (!q_start && T != B) return fail(ctx, COLI_E_INVAL, "rotary: without q_start there is one row per sequence (T == B)");
+  }
+  auto rows_of = [&](const RotarySide& s, bool in) {
+    const long long e = (long long)elem;
+    return Rows{in ? s.in : s.out, (in ? s.in_stride : s.out_stride) * e, (long long)s.heads * head_dim * e, T};
+  };
+  for (int i = 0; i < 2; i++) {
+    const RotarySide &s = a.side[i], &o = a.side[1 - i];
+    const bool in_place = s.in == s.out && s.in_stride == s.out_stride;
+    const Rows out = rows_of(s, false);
+    if ((!in_place && rows_overlap(out, rows_of(s, true))) || rows_overlap(out, rows_of(o, true)) ||
+        (i == 0 && rows_overlap(out, rows_of(o, false))) || rows_overlap(out, one_row(freqs, 4ll * rot_dim)) ||
+        rows_overlap(out, one_row(positions, 4ll * T)) || rows_overlap(out, one_row(lens, 4ll * B)) ||
+        rows_overlap(out, one_row(q_start, 4ll * (B + 1))))
+      return fail(ctx, COLI_E_INVAL, "rotary: an output overlaps another array");
   }
   if (injected(ctx)) return COLI_E_INJECTED;
   cudaSetDevice(ctx->device);
@@ -1164,11 +1176,12 @@ int coli_dense_linear(coli_ctx* ctx, uint64_t W, int I, int O, const void* x, lo
     return fail(ctx, COLI_E_INVAL, "dense_linear: row stride below the row");
   if ((uintptr_t)x % ex != 0 || ((uintptr_t)y | (uintptr_t)mul | (uintptr_t)resid) % ey != 0 || (uintptr_t)bias % 4 != 0)
     return fail(ctx, COLI_E_INVAL, "dense_linear: array not aligned to its dtype");
-  auto overlaps = [&](const void* p, long long stride, long long row) {
-    return p && rows_overlap((uintptr_t)p, stride, row, (uintptr_t)y, y_stride * ey, t->O * ey, S);
+  auto overlaps = [&](const Rows& in) { return rows_overlap(in, Rows{y, y_stride * ey, t->O * ey, S}); };
+  auto beside = [&](const void* p, long long stride) {
+    return !(p == y && stride == y_stride) && overlaps(Rows{p, stride * ey, t->O * ey, S});
   };
-  if (overlaps(x, x_stride * ex, t->I * ex) || (!(mul == y && mul_stride == y_stride) && overlaps(mul, mul_stride * ey, t->O * ey)) ||
-      (!(resid == y && resid_stride == y_stride) && overlaps(resid, resid_stride * ey, t->O * ey)))
+  if (overlaps(Rows{x, x_stride * ex, t->I * ex, S}) || overlaps(one_row(bias, 4ll * t->O)) || beside(mul, mul_stride) ||
+      beside(resid, resid_stride))
     return fail(ctx, COLI_E_INVAL, "dense_linear: y overlaps an input");
   if (injected(ctx)) return COLI_E_INJECTED;
   cudaSetDevice(ctx->device);
@@ -1209,6 +1222,13 @@ int coli_logprobs(coli_ctx* ctx, const void* logits, long long stride, int dtype
   if ((uintptr_t)logits % (dtype == COLI_DTYPE_F32 ? 4 : 2) != 0 ||
       ((uintptr_t)tokens | (uintptr_t)logp | (uintptr_t)entropy | (uintptr_t)top_id | (uintptr_t)top_logp) % 4 != 0)
     return fail(ctx, COLI_E_INVAL, "logprobs: array not aligned to its dtype");
+  const long long elem = dtype == COLI_DTYPE_F32 ? 4 : 2;
+  const Rows outs[] = {one_row(logp, 4ll * S * n), one_row(entropy, 4ll * S), one_row(top_id, 4ll * S * k), one_row(top_logp, 4ll * S * k)};
+  for (int i = 0; i < 4; i++) {
+    bool bad = rows_overlap(outs[i], Rows{logits, stride * elem, V * elem, S}) || rows_overlap(outs[i], one_row(tokens, 4ll * S * n));
+    for (int j = 0; j < i; j++) bad |= rows_overlap(outs[i], outs[j]);
+    if (bad) return fail(ctx, COLI_E_INVAL, "logprobs: an output overlaps another array");
+  }
   if (injected(ctx)) return COLI_E_INJECTED;
   cudaSetDevice(ctx->device);
   LogprobArgs a{};
