@@ -551,35 +551,38 @@ def coli_rotary(ctx, q, k, freqs, q_out, k_out, lens=None, q_start=None, positio
     first = q if q is not None else k
     if first is None or first.dim() != 3:
         raise ValueError("rotary: q or k must be given, [T x heads x head_dim]")
-    T, hd, dtype = first.shape[0], first.shape[2], first.dtype
+    T, _, hd = first.shape
+    dtype = first.dtype
     at = []
-    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+    for x, out in ((q, q_out), (k, k_out)):
         if x is None and out is None:
             at += (None, 0, None, 0, 0)
             continue
         if x is None or out is None:
-            raise ValueError(f"rotary: {name} and {name}_out come together")
+            raise ValueError("rotary: q and q_out come together, and k and k_out")
         shape = x.shape
-        for t in (x, out):
-            if not t.is_cuda or t.dtype != dtype or t.shape != shape or len(shape) != 3 or shape[0] != T or shape[2] != hd:
-                raise ValueError("rotary: q, k and their outputs must be [T x heads x head_dim] CUDA tensors of one dtype")
-            row, head, one = t.stride()
-            if one != 1 or (head != hd and shape[1] > 1):
-                raise ValueError("rotary: the heads and channels of a row must be contiguous")
-            at += (t.data_ptr(), row)
-        at.append(shape[1])
+        if (x.dtype != dtype or out.dtype != dtype or not x.is_cuda or not out.is_cuda or out.shape != shape or len(shape) != 3
+                or shape[0] != T or shape[2] != hd):
+            raise ValueError("rotary: q, k and their outputs must be [T x heads x head_dim] CUDA tensors of one dtype")
+        heads = shape[1]
+        x_row, x_head, x_one = x.stride()
+        row, head, one = out.stride()
+        if x_one != 1 or one != 1 or (heads > 1 and (x_head != hd or head != hd)):
+            raise ValueError("rotary: the heads and channels of a row must be contiguous")
+        at += (x.data_ptr(), x_row, out.data_ptr(), row, heads)
     if freqs.dtype != torch.int64 or not freqs.is_cuda or not freqs.is_contiguous():
         raise ValueError("rotary: freqs must be a contiguous int64 CUDA tensor (coli_rotary_freqs)")
     B = 0 if lens is None else lens.numel()
-    for t, size, name in ((positions, T, "positions"), (q_start, B + 1, "q_start"), (lens, B, "lens")):
+    where = []
+    for t, size in ((positions, T), (q_start, B + 1), (lens, B)):
         if t is None:
-            at.append(None)
+            where.append(None)
         elif t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() != size:
-            raise ValueError(f"rotary: {name} must be a contiguous int32 CUDA tensor (positions [T], lens [B], q_start [B + 1])")
+            raise ValueError("rotary: positions [T], lens [B] and q_start [B + 1] must be contiguous int32 CUDA tensors")
         else:
-            at.append(t.data_ptr())
-    rc = (_lib or library()).coli_rotary(ctx, *at[:10], act_dtype(first), hd, 2 * freqs.numel(), interleaved, freqs.data_ptr(), scale,
-                                         T, *at[10:], B)
+            where.append(t.data_ptr())
+    rc = (_lib or library()).coli_rotary(ctx, *at, act_dtype(first), hd, 2 * freqs.numel(), interleaved, freqs.data_ptr(), scale, T,
+                                         *where, B)
     return rc if rc == COLI_OK else _check(ctx, rc, "coli_rotary")
 
 
@@ -602,16 +605,6 @@ def coli_dense_shape(ctx, handle):
 
 def coli_dense_free(ctx, handle):
     return _check(ctx, library().coli_dense_free(ctx, handle), "coli_dense_free")
-
-
-def _rows2(t, shape, name):
-    """The row stride of a CUDA tensor [S x n] whose rows may be apart."""
-    if not t.is_cuda or t.shape != shape:
-        raise ValueError(f"{name} must be a CUDA tensor {list(shape)}")
-    row, one = t.stride()
-    if one != 1 and shape[1] > 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return shape[1] if shape[0] == 1 else row
 
 
 def coli_dense_linear(ctx, W, x, y, bias=None, act="none", mul=None, resid=None):
@@ -650,22 +643,26 @@ def coli_logprobs(ctx, logits, scale=1.0, tokens=None, logp=None, entropy=None, 
     if logits.dim() != 2:
         raise ValueError("logprobs: logits must be [S x V]")
     S, V = logits.shape
-    stride = _rows2(logits, logits.shape, "logits")
-    at = []
-    for t, dt, name in ((tokens, torch.int32, "tokens"), (logp, torch.float32, "logp"), (entropy, torch.float32, "entropy"),
-                        (top_id, torch.int32, "top_id"), (top_logp, torch.float32, "top_logp")):
+    row, one = logits.stride()
+    if not logits.is_cuda or (one != 1 and V > 1):
+        raise ValueError("logprobs: logits must be a CUDA tensor with contiguous rows")
+    at, sizes = [], []
+    for t, dt in ((tokens, torch.int32), (logp, torch.float32), (entropy, torch.float32), (top_id, torch.int32), (top_logp, torch.float32)):
         if t is None:
             at.append(None)
-        elif t.dtype != dt or not t.is_cuda or not t.is_contiguous() or t.shape[0] != S or (t is entropy and t.numel() != S):
-            raise ValueError(f"logprobs: {name} must be a contiguous {dt} CUDA tensor with a row for each of logits")
+            sizes.append(0)
+        elif t.dtype != dt or not t.is_cuda or not t.is_contiguous() or t.shape[0] != S:
+            raise ValueError("logprobs: tokens and top_id must be contiguous int32 CUDA tensors with a row for each of logits, logp, "
+                             "entropy and top_logp float32")
         else:
             at.append(t.data_ptr())
-    n = 0 if tokens is None else tokens.numel() // max(1, S)
-    k = 0 if top_id is None else top_id.numel() // max(1, S)
-    if (logp is not None and logp.numel() != n * S) or (top_logp is not None and top_logp.numel() != k * S):
-        raise ValueError("logprobs: logp must have the shape of tokens, top_logp that of top_id")
-    rc = (_lib or library()).coli_logprobs(ctx, logits.data_ptr(), stride, act_dtype(logits), S, V, scale, at[0], n, at[1], at[2], k,
-                                           at[3], at[4])
+            sizes.append(t.numel())
+    n_all, n_logp, n_entropy, k_all, k_logp = sizes
+    if (logp is not None and n_logp != n_all) or (top_logp is not None and k_logp != k_all) or (entropy is not None and n_entropy != S):
+        raise ValueError("logprobs: logp must have the shape of tokens, top_logp that of top_id, and entropy [S]")
+    rows = S or 1
+    rc = (_lib or library()).coli_logprobs(ctx, logits.data_ptr(), row, act_dtype(logits), S, V, scale, at[0], n_all // rows, at[1],
+                                           at[2], k_all // rows, at[3], at[4])
     return rc if rc == COLI_OK else _check(ctx, rc, "coli_logprobs")
 
 
