@@ -49,7 +49,6 @@ constexpr int kChunk = 4;   // column tiles
 constexpr int kGroup = 8;   // tokens that a thread of the last warps takes at a time
 constexpr int kSets = kEpiWarps / 4;
 constexpr int kQuad = 4;
-constexpr size_t kInL2 = (size_t)96 << 20;  // a weight of more bytes does not stay in L2 (129 MB) beside the activations
 static_assert(kSets == kDenseCounters, "a counter for each set");
 
 // P parts of x for a staged tile of W, or kQuad: the parts of a token are four neighbouring rows of one tile (the last of them
@@ -79,15 +78,41 @@ struct Shape {
 
 struct TileArgs {
   DenseArgs d;
-  int kt;       // column tiles
-  int rt;       // tiles of 128 rows, or 256 of a pair. A tile's number counts them first: the shares that have other tokens
-                // then walk through the same rows at the same time, and find them in L2
-  long long total;
+  int kt, rt, nt;       // column tiles; tiles of 128 rows, or 256 of a pair; tiles of tokens
+  int tail0;            // tiles up to this one are whole ones of a share: number `share`, then every `shares`-th
+  int tail_shares;      // the shares of what is left
+  long long tail_total; // its units
   bool stream;  // W is read once
   float* part;  // per CTA two of [N / 4][128][4]
   int* count;   // per CTA, zero between calls
   uint64_t wait_ns;
   bool withhold;  // test hook: the call's first copy is withheld, and the waits on it give up
+};
+
+// The numbers of tiles: groups of kBeside tiles of tokens (the last may be smaller), in each one row tile after another. What
+// shares work on at a time is then a few rows and a few tokens: W passes memory once for a group, however large it is.
+constexpr int kBeside = 8;
+struct Place {
+  int rows, tokens;  // tiles
+};
+__device__ __forceinline__ Place place_of(int tile, int rt, int nt) {
+  const int g = tile / (rt * kBeside), i = tile - g * (rt * kBeside), width = max(1, min(kBeside, nt - g * kBeside)), rows = i / width;
+  return Place{rows, g * kBeside + i - rows * width};
+}
+
+// A share's tiles, one after another.
+struct Walk {
+  int tile, k;  // the column tile from which on it is this share's
+
+  __device__ __forceinline__ void next(const TileArgs& a, int shares, const Walk& tail) {
+    k = 0;
+    if (tile >= a.tail0) {
+      tile++;
+    } else {
+      tile += shares;
+      if (tile >= a.tail0) *this = tail;
+    }
+  }
 };
 
 __device__ __forceinline__ uint8_t* dense_at(uint8_t* w, int col_tiles, int o, int i) {
@@ -271,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   __shared__ int s_last[kSets];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = PAIR ? (int)cluster_ctarank() : 0;
-  const long long shares = gridDim.x / H::kCtas, share = blockIdx.x / H::kCtas;
+  const int shares = gridDim.x / H::kCtas, share = blockIdx.x / H::kCtas;
   griddep_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < H::kStages; i++) {
@@ -293,8 +318,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   tc_fence_after_sync();
   const uint32_t tmem = s_tmem;
 
-  const long long w0 = a.total * share / shares, w1 = a.total * (share + 1) / shares;
-  const int tile0 = (int)(w0 / a.kt), k0 = (int)(w0 - (long long)tile0 * a.kt);
+  // of what the whole tiles leave: units w0 to w1
+  const long long w0 = a.tail_total * min(share, a.tail_shares) / a.tail_shares;
+  const long long w1 = a.tail_total * min(share + 1, a.tail_shares) / a.tail_shares;
+  const Walk tail{a.tail0 + (int)(w0 / a.kt), (int)(w0 % a.kt)}, start = a.tail0 ? Walk{share, 0} : tail;
+  const uint32_t units = (uint32_t)(a.tail0 / shares * a.kt + (w1 - w0));
   bool alive = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (alive && !mbar_wait_suspend(bar, parity, a.wait_ns)) {
@@ -305,7 +333,6 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   const bool holds = a.withhold && share == 0;  // the first copy, in both CTAs of a pair
   // the last arrivals on these barriers come before the CTA's memory goes, and with them the last reads of it
   auto wait_for_products = [&]() {
-    const uint32_t units = (uint32_t)(w1 - w0);
     for (uint32_t i = units > (uint32_t)H::kStages ? units - H::kStages : 0; i < units; i++)
       mbar_wait(&empty[i % H::kStages], (i / H::kStages) & 1, a.wait_ns);
   };
@@ -314,30 +341,27 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     // ------------------------------------ producer ------------------------------------
     if (elect_one()) {
       const uint64_t once = l2_evict_first_policy();
-      const uint32_t units = (uint32_t)(w1 - w0);
       const uint32_t full0 = PAIR ? cluster_address(smem_u32(full), 0) : smem_u32(full);
       struct At {
-        int k, n, rows;  // column tile, tile of tokens, 128 rows
+        Walk walk;
+        Place place;
       };
       auto advance = [&](At& at) {
-        if (++at.k < a.kt) return;
-        at.k = 0;
-        at.rows += H::kCtas;
-        if (at.rows < a.rt * H::kCtas) return;
-        at.rows = rank;
-        at.n++;
+        if (++at.walk.k < a.kt) return;
+        at.walk.next(a, shares, tail);
+        at.place = place_of(at.walk.tile, a.rt, a.nt);
       };
-      const At start{k0, tile0 / a.rt, tile0 % a.rt * H::kCtas + rank};
-      At w_at = start, x_at = start;
+      At w_at{start, place_of(start.tile, a.rt, a.nt)}, x_at = w_at;
       auto copy_w = [&](uint32_t n) {
         const uint32_t s = n % H::kStages;
         uint8_t* to = smem + s * H::kStage;
+        const int tile = (w_at.place.rows * H::kCtas + rank) * a.kt + w_at.walk.k;
         if (!(holds && n == 0)) {
           if (rank == 0) mbar_arrive_expect_tx(&full[s], H::kStage * H::kCtas);
           if constexpr (PAIR) {
-            tma_load_2d_pair(to, &w_map, 0, (w_at.rows * a.kt + w_at.k) * kDenseRows, full0 + s * 8);
+            tma_load_2d_pair(to, &w_map, 0, tile * kDenseRows, full0 + s * 8);
           } else {
-            const uint8_t* from = a.d.w + ((size_t)w_at.rows * a.kt + w_at.k) * kDenseTile;
+            const uint8_t* from = a.d.w + (size_t)tile * kDenseTile;
             if (a.stream)
               bulk_g2s_stream(to, from, kDenseTile, &full[s], once);
             else
@@ -352,11 +376,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
 #pragma unroll
           for (int p = 0; p < H::kPasses; p++) {
             uint8_t* to = smem + s * H::kStage + kDenseTile + p * H::kXRows * 128;
-            const int y = p * a.d.S + x_at.n * N + rank * H::kXRows;
+            const int y = p * a.d.S + x_at.place.tokens * N + rank * H::kXRows;
             if constexpr (PAIR)
-              tma_load_2d_pair(to, &x_map, x_at.k * kDenseCols, y, full0 + s * 8);
+              tma_load_2d_pair(to, &x_map, x_at.walk.k * kDenseCols, y, full0 + s * 8);
             else
-              tma_load_2d(to, &x_map, x_at.k * kDenseCols, y, &full[s]);
+              tma_load_2d(to, &x_map, x_at.walk.k * kDenseCols, y, &full[s]);
           }
         advance(x_at);
       };
@@ -385,10 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     if (rank == 0 && elect_one()) {
       constexpr uint32_t kId = bf16_f32_idesc(kDenseRows * H::kCtas, N);
       uint32_t s = 0, phase = 0, chunk = 0;
-      int k = k0;
-      long long w = w0;
-      while (w < w1) {
-        const int seg = (int)min((long long)(a.kt - k), w1 - w);
+      int left = (int)units;
+      for (Walk walk = start; left > 0; walk.next(a, shares, tail)) {
+        const int seg = min(a.kt - walk.k, left);
         for (int done = 0; done < seg;) {
           const int here = EXACT ? min(kChunk, seg - done) : seg;
           wait(&acc_empty[chunk % H::kAccs], (chunk / H::kAccs + 1) & 1);
@@ -411,8 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           chunk++;
           done += here;
         }
-        w += seg;
-        k = 0;
+        left -= seg;
       }
       wait_for_products();
     } else if (PAIR && rank == 1 && elect_one()) {
@@ -498,15 +520,15 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       }
     };
     auto at_tile = [&](int tile) {
-      o = (tile % a.rt * H::kCtas + rank) * kDenseRows + row;
-      t0 = tile / a.rt * H::kTokens;
+      const Place at = place_of(tile, a.rt, a.nt);
+      o = (at.rows * H::kCtas + rank) * kDenseRows + row;
+      t0 = at.tokens * H::kTokens;
       bias = a.d.bias && o < a.d.O ? __ldcg(a.d.bias + o) : 0.f;
     };
     uint32_t chunk = 0;
-    int k = k0, tile = tile0;
-    uint32_t left = (uint32_t)(w1 - w0);
-    while (left > 0) {
-      const int seg = min(a.kt - k, (int)left);
+    int left = (int)units;
+    for (Walk walk = start; left > 0; walk.next(a, shares, tail)) {
+      const int tile = walk.tile, seg = min(a.kt - walk.k, left);
       const bool whole = seg == a.kt;
       Beside next;
       if constexpr (EXACT) {
@@ -559,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         // a tile's beginning goes to the CTA's second part, a continuation to its first; four tokens of a row together
         constexpr size_t kPart = (size_t)(N / 4) * kDenseRows;
         float4* parts = reinterpret_cast<float4*>(a.part) + row;
-        float4* mine = parts + ((size_t)2 * blockIdx.x + (k == 0)) * kPart;
+        float4* mine = parts + ((size_t)2 * blockIdx.x + (walk.k == 0)) * kPart;
 #pragma unroll 1
         for (int g = set; g < H::kGroups; g += kSets) {
           float z[kGroup];
@@ -569,8 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         }
         // the shares of this tile: from the one that begins it to the one that ends it. The four warps of a set, which hold
         // all rows of their tokens, join them on their own.
-        const long long u0 = (long long)tile * a.kt, u1 = u0 + a.kt - 1;
-        const int first = (int)(((u0 + 1) * shares - 1) / a.total), last = (int)(((u1 + 1) * shares - 1) / a.total);
+        const long long u0 = (long long)(tile - a.tail0) * a.kt, u1 = u0 + a.kt - 1;
+        const int first = (int)(((u0 + 1) * a.tail_shares - 1) / a.tail_total), last = (int)(((u1 + 1) * a.tail_shares - 1) / a.tail_total);
         __threadfence();
         named_sync(1 + set, 128);
         if ((tid & 127) == 0) {
@@ -626,8 +648,6 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       if (lane == 0) free_acc(chunk % H::kAccs);
       chunk++;
       left -= seg;
-      k = 0;
-      tile++;
     }
     if (broken != 0.f) set_error(a.d.err, COLI_E_NONFINITE);
   }
@@ -640,18 +660,78 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   if (warp == 1) tmem_dealloc_n<H::kCtas>(tmem, H::kTmem);
 }
 
+// A call's tiles and how they are dealt out: what takes the fewest cycles by a model that was fitted to 12274 measurements (O, I
+// of 768 to 50021, S of 1 to 4096, each type; what it picks takes 1.6 % more than the best of them on average, 29 % at most).
+//   A column tile takes its bytes from L2 at 64 a cycle and 60, or its products and 50; a tile 300 more. W comes from memory or L2
+//   at 29 bytes a cycle and SM, of which 0.87 are enough, and seven tenths of that once more for each further tile of tokens. A
+//   split tile takes N times 42 cycles and 19.5 for each part, or 3 more where shares begin anywhere (their ends meet two tiles).
+//   A pair of CTAs, which halves the tokens' bytes, 2200.
+// Tiles are dealt out whole as long as there is one for every share. What is left is split evenly over all shares (together with
+// the last whole ones, or by itself), or each tile over as many shares q as there are for it. Measured, us, even shares of
+// everything and as chosen: one token, 6144 x 6144, 15.2 14.1; 301 tokens there 33.7 24.4; 512 tokens, O = I = 4096, 23.2 18.4; 4096
+// tokens, 6144 x 6144, 197 171; 2048 tokens, 20000 x 6144, 370 280 (even runs of many tiles read W from memory again and again).
+struct Plan {
+  int tokens;  // of a tile
+  bool pair;
+  int whole;   // tiles that each share takes whole
+  int q;       // shares of each other tile, 0: all shares of all of them
+};
+
+Plan dense_plan(int S, int O, int I, int parts, bool exact, int num_sms) {
+  const bool quad = parts == kQuad;
+  const int most = exact ? kPairTokens<true> : kPairTokens<false>, passes = quad ? 1 : parts;
+  const Plan all[] = {{16, false}, {32, false}, {64, false}, {128, false}, {64, true}, {128, true}, {most, true}};
+  const int kt = (I + kDenseCols - 1) / kDenseCols;
+  const double bytes = (double)dense_bytes(O, I);
+  Plan best{};
+  double least = 0;
+  for (const Plan& p : all) {
+    if ((p.tokens == 16) != (S <= 16)) continue;
+    const int ctas = p.pair ? 2 : 1, N = p.tokens, shares = num_sms / ctas;
+    const int nt = quad ? 1 : (S + N - 1) / N;
+    const int tiles = (O + kDenseRows * ctas - 1) / (kDenseRows * ctas) * nt, waves = tiles / shares;
+    const double unit = std::max((kDenseTile + passes * N / ctas * 128.0) / 64 + 60, passes * N * 2.0 + 50), tile = kt * unit + 300;
+    auto look = [&](int whole, int q) {
+      const int rest = tiles - whole * shares;
+      const int used = whole ? shares : q ? rest * q : (int)std::min<long long>(shares, (long long)rest * kt);
+      const double each = rest == 0 ? 0 : q ? (double)((kt + q - 1) / q) / kt : (double)rest / std::min<double>(shares, (double)rest * kt);
+      const bool split = rest > 0 && q != 1 && !(q == 0 && rest % shares == 0);
+      const double read = bytes / (29 * std::max<double>(used * ctas, 0.87 * num_sms)) * (1 + 0.7 * (nt - 1));
+      const double join = !split ? 0 : N * (42 + 19.5 * (q ? q : 3 + std::max(1, (shares + rest - 1) / rest)));
+      const double cycles = std::max(tile * (whole + each), read) + join + (p.pair ? 2200 : 0);
+      if (least == 0 || cycles < least) least = cycles, best = Plan{p.tokens, p.pair, whole, q};
+    };
+    look(std::max(0, waves - 1), 0);
+    const int rest = tiles - waves * shares;
+    if (rest == 0) {
+      look(waves, 1);
+      continue;
+    }
+    if (waves) look(waves, 0);
+    const int q_most = std::min(shares / rest, kt);
+    for (int u = (kt + q_most - 1) / q_most, q = q_most;; u += (u + 3) / 4) {  // a share's column tiles
+      q = (kt + u - 1) / u;
+      look(waves, q);
+      if (q == 1) break;
+    }
+  }
+  return best;
+}
+
 template <int N, int P, bool EXACT, bool PAIR>
-int launch_one(coli_ctx* ctx, TileArgs& a, const CUtensorMap& x_map, const CUtensorMap& w_map) {
+int launch_one(coli_ctx* ctx, TileArgs& a, const Plan& plan, const CUtensorMap& x_map, const CUtensorMap& w_map) {
   using H = Shape<N, P, EXACT, PAIR>;
   static_assert((size_t)2 * N * kDenseRows <= kPartFloats, "a CTA leaves more than there is room for");
   a.kt = (a.d.I + kDenseCols - 1) / kDenseCols;
-  const int rows = kDenseRows * H::kCtas, nt = (a.d.S + H::kTokens - 1) / H::kTokens;
+  const int rows = kDenseRows * H::kCtas;
+  a.nt = (a.d.S + H::kTokens - 1) / H::kTokens;
   a.rt = (a.d.O + rows - 1) / rows;
-  a.total = (long long)a.rt * nt * a.kt;
-  a.stream = nt == 1;
-  // Where the weight is larger than L2 and a few tiles of tokens read it, they do so in step: as many shares for each.
-  int shares = ctx->num_sms / H::kCtas;
-  if (nt > 1 && nt <= 8 && dense_bytes(a.d.O, a.d.I) > kInL2) shares = shares / nt * nt;
+  a.stream = a.nt == 1;
+  const int all = ctx->num_sms / H::kCtas, rest = a.rt * a.nt - plan.whole * all;
+  a.tail0 = plan.whole * all;
+  a.tail_total = (long long)rest * a.kt;
+  a.tail_shares = plan.q ? std::max(1, rest * plan.q) : (int)std::min<long long>(all, a.tail_total);
+  const int shares = plan.whole ? all : a.tail_shares;
   auto kern = dense_kernel<N, P, EXACT, PAIR>;
   static std::atomic<uint64_t> ready{0};  // devices (below 64) on which this instance has its attribute
   const uint64_t bit = ctx->device < 64 ? 1ull << ctx->device : 0;
@@ -661,7 +741,7 @@ int launch_one(coli_ctx* ctx, TileArgs& a, const CUtensorMap& x_map, const CUten
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<long long>(shares, a.total) * H::kCtas);
+  cfg.gridDim = dim3((unsigned)(shares * H::kCtas));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = H::kSmem;
   cfg.stream = ctx->stream;
@@ -676,37 +756,6 @@ int launch_one(coli_ctx* ctx, TileArgs& a, const CUtensorMap& x_map, const CUten
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, x_map, w_map, a);
   if (e != cudaSuccess) return cuda_fail(ctx, e, "dense_linear launch");
   return COLI_OK;
-}
-
-// A call's tiles: what takes the fewest cycles by what was measured on O, I of 768 to 50021 and S to 4096. A column tile takes
-// its bytes from L2 at 64 a cycle, or its products; the weight comes from memory at 22 a cycle and SM, and other tiles of tokens
-// find a tenth of it gone from L2 again, a quarter where it is larger than that; a shared tile takes 30 N
-// cycles and 17 N for every share of it but one; a pair of CTAs, which halves the tokens' bytes, 3000 (us, single CTAs and
-// pairs of 64, 128 and the most tokens a tile; O = I = 6144, 64 bf16 tokens: 17.9 21.8, 20.0 24.2 32.7; 512: 57.9 38.4, 51.5
-// 35.5 39.3; 512 f32: 115 83, 87 73 84; 4096 bf16: 414 234, - - 183; O = 2048, 256 bf16: 17.2 19.4, 17.5 20.3 33.8).
-struct Tiles {
-  int tokens;
-  bool pair;
-};
-Tiles dense_tiles(int S, int O, int I, int parts, bool exact, int num_sms) {
-  if (S <= 16) return Tiles{16, false};
-  const int most = exact ? kPairTokens<true> : kPairTokens<false>;
-  const Tiles all[] = {{32, false}, {64, false}, {128, false}, {64, true}, {128, true}, {most, true}};
-  const double kt = (I + kDenseCols - 1) / kDenseCols, bytes = (double)dense_bytes(O, I);
-  Tiles best = all[0];
-  double least = 0;
-  for (const Tiles& t : all) {
-    const int ctas = t.pair ? 2 : 1, N = t.tokens;
-    const int nt = (S + N - 1) / N;
-    const double tiles = (double)((O + kDenseRows * ctas - 1) / (kDenseRows * ctas)) * nt;
-    const double stream = bytes / (22.0 * num_sms) * (1 + (nt - 1) * (bytes > kInL2 ? 0.25 : 0.1));
-    const double shares = std::min<double>(num_sms / ctas, tiles * kt);
-    const double unit = std::max((kDenseTile + parts * N / ctas * 128.0) / 64 + 16, parts * N * 2.0 + 80);
-    const double cycles = std::max(tiles * kt / shares * unit, stream) + N * (30 + 17 * std::max(1.0, std::ceil(shares / tiles))) +
-                          (t.pair ? 3000 : 0);
-    if (least == 0 || cycles < least) best = t, least = cycles;
-  }
-  return best;
 }
 
 template <bool BF16, int P>
@@ -739,7 +788,7 @@ int launch_dense(coli_ctx* ctx, const DenseArgs& args, const CUtensorMap& w_map,
   const long long row = a.d.S == 1 ? (a.d.I + 7) / 8 * 8 : a.d.x_stride;
   const bool direct = parts == 1 && (uintptr_t)a.d.x % 16 == 0 && row % 8 == 0;
   const int S = a.d.S;
-  const Tiles t = dense_tiles(S, a.d.O, a.d.I, parts, exact, ctx->num_sms);
+  const Plan t = dense_plan(S, a.d.O, a.d.I, parts, exact, ctx->num_sms);
   const int box = t.pair ? t.tokens / 2 : t.tokens;
   CUtensorMap map{};
   if (direct) {
@@ -764,16 +813,16 @@ int launch_dense(coli_ctx* ctx, const DenseArgs& args, const CUtensorMap& w_map,
     constexpr int P = decltype(p)::value;
     constexpr bool E = decltype(y32)::value;
     if (t.pair) {
-      if (t.tokens == 64) return launch_one<64, P, E, true>(ctx, a, map, w_map);
-      if (t.tokens == 128) return launch_one<128, P, E, true>(ctx, a, map, w_map);
-      return launch_one<kPairTokens<E>, P, E, true>(ctx, a, map, w_map);
+      if (t.tokens == 64) return launch_one<64, P, E, true>(ctx, a, t, map, w_map);
+      if (t.tokens == 128) return launch_one<128, P, E, true>(ctx, a, t, map, w_map);
+      return launch_one<kPairTokens<E>, P, E, true>(ctx, a, t, map, w_map);
     }
-    if (t.tokens == 16) return launch_one<16, P, E, false>(ctx, a, map, w_map);
-    if (t.tokens == 32) return launch_one<32, P, E, false>(ctx, a, map, w_map);
-    if (t.tokens == 64) return launch_one<64, P, E, false>(ctx, a, map, w_map);
-    return launch_one<128, P, E, false>(ctx, a, map, w_map);
+    if (t.tokens == 16) return launch_one<16, P, E, false>(ctx, a, t, map, w_map);
+    if (t.tokens == 32) return launch_one<32, P, E, false>(ctx, a, t, map, w_map);
+    if (t.tokens == 64) return launch_one<64, P, E, false>(ctx, a, t, map, w_map);
+    return launch_one<128, P, E, false>(ctx, a, t, map, w_map);
   };
-  if (parts == kQuad) return launch_one<16, kQuad, true, false>(ctx, a, map, w_map);
+  if (parts == kQuad) return launch_one<16, kQuad, true, false>(ctx, a, t, map, w_map);
   if (parts == 3) return tokens(std::integral_constant<int, 3>{}, std::true_type{});
   if (parts == 2) return tokens(std::integral_constant<int, 2>{}, std::false_type{});
   if (exact) return tokens(std::integral_constant<int, 1>{}, std::true_type{});
