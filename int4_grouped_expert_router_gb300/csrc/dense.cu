@@ -661,11 +661,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
 }
 
 // A call's tiles and how they are dealt out: what takes the fewest cycles by a model that was fitted to 12274 measurements (O, I
-// of 768 to 50021, S of 1 to 4096, each type; what it picks takes 1.6 % more than the best of them on average, 29 % at most).
-//   A column tile takes its bytes from L2 at 64 a cycle and 60, or its products and 50; a tile 300 more. W comes from memory or L2
-//   at 29 bytes a cycle and SM, of which 0.87 are enough, and seven tenths of that once more for each further tile of tokens. A
-//   split tile takes N times 42 cycles and 19.5 for each part, or 3 more where shares begin anywhere (their ends meet two tiles).
-//   A pair of CTAs, which halves the tokens' bytes, 2200.
+// of 768 to 50021, S of 1 to 4096, each type; what it picks takes 1.5 % more than the best of them on average, 19 % at most).
+//   A column tile takes its bytes from L2 at 64 a cycle and 60, or its products and 60; a tile 220 more. W is read at 26 bytes a
+//   cycle and SM, of which two thirds are enough, and eight tenths of it once more for each further tile of tokens. A split tile
+//   takes N times 40 cycles and 19.6 for each part, or 3.5 more where shares begin anywhere (their ends meet two tiles). A pair of
+//   CTAs, which halves the tokens' bytes, 2100.
 // Tiles are dealt out whole as long as there is one for every share. What is left is split evenly over all shares (together with
 // the last whole ones, or by itself), or each tile over as many shares q as there are for it. Measured, us, even shares of
 // everything and as chosen: one token, 6144 x 6144, 15.2 14.1; 301 tokens there 33.7 24.4; 512 tokens, O = I = 4096, 23.2 18.4; 4096
@@ -690,15 +690,17 @@ Plan dense_plan(int S, int O, int I, int parts, bool exact, int num_sms) {
     const int ctas = p.pair ? 2 : 1, N = p.tokens, shares = num_sms / ctas;
     const int nt = quad ? 1 : (S + N - 1) / N;
     const int tiles = (O + kDenseRows * ctas - 1) / (kDenseRows * ctas) * nt, waves = tiles / shares;
-    const double unit = std::max((kDenseTile + passes * N / ctas * 128.0) / 64 + 60, passes * N * 2.0 + 50), tile = kt * unit + 300;
+    const double unit = std::max((kDenseTile + passes * N / ctas * 128.0) / 64 + 60, passes * N * 2.0 + 60), tile = kt * unit + 220;
+    const double read = bytes / (26.0 * num_sms) * (1 + 0.8 * (nt - 1)) / tiles;  // W for a tile, where all SMs read
     auto look = [&](int whole, int q) {
       const int rest = tiles - whole * shares;
-      const int used = whole ? shares : q ? rest * q : (int)std::min<long long>(shares, (long long)rest * kt);
-      const double each = rest == 0 ? 0 : q ? (double)((kt + q - 1) / q) / kt : (double)rest / std::min<double>(shares, (double)rest * kt);
-      const bool split = rest > 0 && q != 1 && !(q == 0 && rest % shares == 0);
-      const double read = bytes / (29 * std::max<double>(used * ctas, 0.87 * num_sms)) * (1 + 0.7 * (nt - 1));
-      const double join = !split ? 0 : N * (42 + 19.5 * (q ? q : 3 + std::max(1, (shares + rest - 1) / rest)));
-      const double cycles = std::max(tile * (whole + each), read) + join + (p.pair ? 2200 : 0);
+      const long long used = q ? (long long)rest * q : std::min<long long>(shares, (long long)rest * kt);
+      double cycles = std::max(tile, read * shares) * whole + (p.pair ? 2100 : 0);
+      if (rest > 0) {
+        const double each = q ? (double)((kt + q - 1) / q) / kt : (double)rest / used;  // tiles of a share
+        cycles += std::max(tile * each, read * rest / std::min(1.0, used / (0.66 * shares)));
+        if (q != 1 && !(q == 0 && rest % shares == 0)) cycles += N * (40 + 19.6 * (q ? q : 3.5 + std::max(1, (shares + rest - 1) / rest)));
+      }
       if (least == 0 || cycles < least) least = cycles, best = Plan{p.tokens, p.pair, whole, q};
     };
     look(std::max(0, waves - 1), 0);
