@@ -68,6 +68,14 @@ def test_sizes(ctx, S, I, O_, x_dtype, y):
     run(ctx, S, I, O_, x_dtype, y)
 
 
+@pytest.mark.parametrize("S,I,O_,x_dtype,y", [(2700, 100, 4700, "bf16", "bf16"), (2500, 130, 3100, "f32", "f32"), (1100, 70, 20001, "bf16", "f32"),
+                                              (4100, 64, 2049, "f32", "bf16"), (1, 300, 60001, "bf16", "bf16"), (40, 700, 19457, "bf16", "f32"),
+                                              (256, 256, 38912, "bf16", "bf16")])
+def test_many_tiles(ctx, S, I, O_, x_dtype, y):
+    """Several tiles for every share, whole and split ones, token tiles of more than one group, and none left to split."""
+    run(ctx, S, I, O_, x_dtype, y, "relu", bias=True, resid=True)
+
+
 @pytest.mark.parametrize("y", ["bf16", "f32"])
 @pytest.mark.parametrize("kind", list(B.ACTIVATIONS))
 @pytest.mark.parametrize("S", [1, 20, 150])
