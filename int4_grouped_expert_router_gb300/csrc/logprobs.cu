@@ -301,6 +301,13 @@ __global__ void __launch_bounds__(kThreads, kLogprobCtas) logprob_kernel(Logprob
   };
 #pragma unroll
   for (int u = 0; u < kFlight; u++) ask(v0 + tid + u * kThreads, u);
+  // the first of the given tokens, ahead of their use: a chain of two loads
+  int token = -1;
+  float logit = 0.f;
+  if (a.logp && tid < a.n) {
+    token = __ldcg(a.tokens + (size_t)row_id * a.n + tid);
+    if ((unsigned)token < (unsigned)a.V) logit = row.one(token);
+  }
   for (int j0 = v0 + tid; j0 < v1; j0 += kThreads * kFlight) {
 #pragma unroll
     for (int u = 0; u < kFlight; u++) {
@@ -373,19 +380,19 @@ __global__ void __launch_bounds__(kThreads, kLogprobCtas) logprob_kernel(Logprob
       if (tid == 0) s.best[0] = bound > kLeast ? bound : 0;
       __syncthreads();
     } else {
-      const int each = (v1 - v0 + kThreads - 1) / kThreads;  // vectors of a thread
+      const int each_log2 = 32 - __clz((v1 - v0 + kThreads - 1) / kThreads - 1);  // a thread's vectors, up to a power of two
       for (;;) {
         const float least = value_of(bound);
         if (mine >= bound) s.hit[atomicAdd(&s.hits, 1)] = (uint16_t)tid;
         __syncthreads();
-        const int looks = s.hits * each;
+        const int looks = s.hits << each_log2;
         for (int w0 = tid; w0 < looks; w0 += kThreads * kLooks) {
           uint4 r[kLooks];
           int j[kLooks];
 #pragma unroll
           for (int u = 0; u < kLooks; u++) {
-            const int w = w0 + u * kThreads, h = w / each;
-            j[u] = w < looks ? v0 + s.hit[h] + (w - h * each) * kThreads : v1;
+            const int w = w0 + u * kThreads, h = w >> each_log2;
+            j[u] = w < looks ? v0 + s.hit[h] + (w - (h << each_log2)) * kThreads : v1;
             if (j[u] < v1) r[u] = vector(j[u]);
           }
 #pragma unroll
@@ -436,36 +443,34 @@ __global__ void __launch_bounds__(kThreads, kLogprobCtas) logprob_kernel(Logprob
     __threadfence();
     // all that the parts left is asked for at once
     constexpr int kEach = kRoom / kThreads;
-    static_assert(kLogprobMostParts <= kGroups, "a group for each part");
-    uint64_t key[kEach];
+    static_assert(kLogprobMostParts <= kGroups && kGroups <= kThreads, "a group for each part");
+    uint64_t key[kEach], lead = 0;
+    float4 left[2];
     auto of_part = [&](int p, int i) { return __ldcg(reinterpret_cast<const unsigned long long*>(&part[p].top[i])); };
-    if (a.k > 0) {
 #pragma unroll
-      for (int u = 0; u < kEach; u++) {
-        const int i = tid + u * kThreads;
-        key[u] = i < a.parts * a.k ? of_part(i / a.k, i % a.k) : 0;
-      }
+    for (int h = 0; h < 2; h++) left[h] = lane + 32 * h < a.parts ? __ldcg(reinterpret_cast<const float4*>(part + lane + 32 * h)) : make_float4(-kInf, -kInf, 0.f, 0.f);
+    if (a.k > 0) {
       // groups are runs of `run` of a part's keys, which descend: their first ones are their largest
       const int most_runs = kGroups / a.parts, run = (a.k + most_runs - 1) / most_runs;
       const int runs = (a.k + run - 1) / run;
-      if (tid < kGroups) s.group[tid] = tid < a.parts * runs ? of_part(tid / runs, tid % runs * run) : 0;
-    }
-    Sums two[2];
-    most = -kInf;
-    for (int h = 0; h < 2; h++) {
-      const int p = lane + 32 * h;
-      two[h] = Sums{-kInf, 0.f, 0.f};
-      if (p < a.parts) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(part + p));
-        two[h] = Sums{v.y, v.z, v.w};
-        most = fmaxf(most, v.x);
+      if (tid < a.parts * runs) lead = of_part(tid / runs, tid % runs * run);
+#pragma unroll
+      for (int u = 0; u < kEach; u++) {
+        const int i = tid + u * kThreads;
+        key[u] = 0;
+        if (i < a.parts * a.k) key[u] = of_part(i / a.k, i % a.k);
       }
     }
+    Sums two[2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) two[h] = Sums{left[h].y, left[h].z, left[h].w};
+    most = fmaxf(left[0].x, left[1].x);
     sum = two[0];
     sum.join(two[1], c);
     over_warp();
     if (a.k > 0) {
       // of the groups' largest entries the k-th largest is a bound; with fewer groups than k there is none
+      if (tid < kGroups) s.group[tid] = lead;
       if (tid == 0) s.n = 0, s.bound = kLeast;
       __syncthreads();
       const uint64_t bound = find_bound(s, a.k);
@@ -491,9 +496,12 @@ __global__ void __launch_bounds__(kThreads, kLogprobCtas) logprob_kernel(Logprob
   if (a.logp)
     for (int i = tid; i < a.n; i += kThreads) {
       const size_t to = (size_t)row_id * a.n + i;
-      const int token = __ldcg(a.tokens + to);
+      if (i != tid) {
+        token = __ldcg(a.tokens + to);
+        if ((unsigned)token < (unsigned)a.V) logit = row.one(token);
+      }
       if (token >= a.V) set_error(a.err, COLI_E_RANGE);
-      a.logp[to] = token < 0 ? 0.f : token >= a.V ? nan : log_p(row.one(token));
+      a.logp[to] = token < 0 ? 0.f : token >= a.V ? nan : log_p(logit);
     }
   if (tid < a.k) {
     const uint64_t key = bad ? 0 : s.best[tid];
