@@ -28,7 +28,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRoom = kLogprobMostParts * COLI_MAX_TOP;  // entries that reach the bound
-constexpr int kLooks = 4;    // vectors that a thread looks through together
+constexpr int kLooks = 2;    // vectors that a thread looks through together
 constexpr int kFlight = 7;   // vectors of a thread on their way
 // Vectors of a thread that are not worth another CTA of the row: they are on their way together, and fewer parts are joined
 // sooner (15 rows of 32003, 32 alternatives: 9.8 us with 4, 12.5 with 1).
@@ -301,13 +301,9 @@ __global__ void __launch_bounds__(kThreads, kLogprobCtas) logprob_kernel(Logprob
   };
 #pragma unroll
   for (int u = 0; u < kFlight; u++) ask(v0 + tid + u * kThreads, u);
-  // the first of the given tokens, ahead of their use: a chain of two loads
+  // the first of the given tokens and, behind the pass, their logits: a chain of two loads, ahead of their use
   int token = -1;
-  float logit = 0.f;
-  if (a.logp && tid < a.n) {
-    token = __ldcg(a.tokens + (size_t)row_id * a.n + tid);
-    if ((unsigned)token < (unsigned)a.V) logit = row.one(token);
-  }
+  if (a.logp && tid < a.n) token = __ldcg(a.tokens + (size_t)row_id * a.n + tid);
   for (int j0 = v0 + tid; j0 < v1; j0 += kThreads * kFlight) {
 #pragma unroll
     for (int u = 0; u < kFlight; u++) {
@@ -326,6 +322,8 @@ __global__ void __launch_bounds__(kThreads, kLogprobCtas) logprob_kernel(Logprob
     }
   }
   copy_wait<0>();
+  float logit = 0.f;
+  if ((unsigned)token < (unsigned)a.V) logit = row.one(token);
   // ---- the CTA's sums, and each thread's largest entry ----
   // Where they are few, a thread's vectors are still in shared memory.
   const bool kept = v1 - v0 <= kFlight * kThreads;
