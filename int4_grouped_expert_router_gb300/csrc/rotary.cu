@@ -8,8 +8,8 @@
 // takes whole rows and makes their table in shared memory while its first loads are on their way; few heads are several rows.
 //
 // Measured: 8191 rows of 64 + 8 heads of 128 (bf16) 52 us, 5.8 TB/s, 0.85 of a copy's rate, neighbouring channels 60 us, f32
-// 90 us (0.99); 3001 f32 rows of 40 heads of 80, 36 channels turned, 18.0 us (4.3 TB/s); one row 3.5 us on the device, less
-// than the call takes on the host (8.5 us). Bound by the table's latency (plan, frequency, sine) at the start of each CTA. Five
+// 90 us (0.99); 3001 f32 rows of 40 heads of 80, 36 channels turned, 19.8 us (3.9 TB/s); one row 3.5 us on the device, less
+// than the call takes on the host (7.6 us). Bound by the table's latency (plan, frequency, sine) at the start of each CTA. Five
 // CTAs of 256 threads in 48 registers beat three of 384 in 56 (57 us) and four of 384 in 40 (67 us, spills); copies behind the
 // turned part two vectors at a time took the f32 case from 22 to 18 us.
 #include <cuda_bf16.h>
@@ -194,13 +194,24 @@ __device__ __forceinline__ void rotate(float& p, float& q, float2 cs) {
   p = c, q = d;
 }
 
-constexpr int kTasks = 2;  // tasks of a thread whose loads are under way together
+// i / d as a multiplication by 2^31 / d, rounded up: exact while i d < 2^31, the error being below i d.
+struct Divisor {
+  int d;
+  uint32_t inverse;
+  explicit Divisor(int d) : d(d), inverse((uint32_t)(((1ull << 31) + d - 1) / d)) {}
+};
+__device__ __forceinline__ int operator/(int i, const Divisor& by) { return (int)((uint64_t)i * by.inverse >> 31); }
+
+// Tasks of a thread whose loads are under way together. Of two vectors of 8 bytes one more: 3001 f32 rows of 40 heads of 80, 36
+// channels turned, 19.8 us against 21.4; a fourth spills more than it hides.
+template <int BYTES>
+constexpr int kTasks = BYTES <= 8 ? 3 : 2;
 
 // Vectors of V elements. A task is two of them (two halves' worth of V pairs, or 2 V neighbouring channels); behind the turned
 // part (COPY) two neighbouring ones that are copied, where there is an even number of them (`wide`), or one.
 template <bool BF16, int V, bool HALF, bool COPY>
-__global__ void __launch_bounds__(kMostThreads, kCtas) rotary_kernel(RotaryArgs a, int rows, bool wide) {
-  constexpr int E = BF16 ? 2 : 4, U = kTasks;
+__global__ void __launch_bounds__(kMostThreads, kCtas) rotary_kernel(RotaryArgs a, int rows, bool wide, Divisor per_head, Divisor per_row) {
+  constexpr int E = BF16 ? 2 : 4, U = kTasks<V * E>;
   using R = typename Vec<V * E>::T;
   extern __shared__ float2 s_turn[];  // [rows][rot / 2] cosine, sine
   __shared__ long long s_pos[kMostRows];
@@ -210,9 +221,7 @@ __global__ void __launch_bounds__(kMostThreads, kCtas) rotary_kernel(RotaryArgs 
   const int row0 = blockIdx.x * rows;
   const int here = min(rows, a.T - row0);
   const int copy = wide ? 2 * V : V;  // elements of a copied vector
-  const int turned = half / V, copied = COPY ? (a.hd - a.rot) / copy : 0, per_head = turned + copied;
-  const int per_row = per_head * (a.side[0].heads + a.side[1].heads);
-  const int tasks = per_row * here;
+  const int turned = half / V, tasks = per_row.d * here;
 
   // A task's place: where its vectors are read and written, and which pairs they hold.
   struct Task {
@@ -222,10 +231,10 @@ __global__ void __launch_bounds__(kMostThreads, kCtas) rotary_kernel(RotaryArgs 
   };
   auto task_of = [&](int i) {
     Task t;
-    t.row = i / per_row;
-    i -= t.row * per_row;
+    t.row = rows == 1 ? 0 : i / per_row;  // (a row alone may be longer than the division is exact for)
+    i -= t.row * per_row.d;
     int head = i / per_head;
-    const int v = i - head * per_head;
+    const int v = i - head * per_head.d;
     const bool k = head >= a.side[0].heads;
     if (k) head -= a.side[0].heads;
     const RotarySide& s = a.side[k];
@@ -291,7 +300,7 @@ __global__ void __launch_bounds__(kMostThreads, kCtas) rotary_kernel(RotaryArgs 
 // heads (of q, then of k) of `rows` rows. 3001 rows of 40 heads of 80, 38 channels turned, bf16: 21.4 us; two elements a task of
 // the other kernel took 31 us.
 template <bool BF16, bool HALF>
-__global__ void __launch_bounds__(kMostThreads) rotary_run_kernel(RotaryArgs a, int rows, int heads, int runs_q, int runs) {
+__global__ void __launch_bounds__(kMostThreads) rotary_run_kernel(RotaryArgs a, int rows, int heads, int runs_q, int runs, Divisor pitch) {
   using T = std::conditional_t<BF16, uint16_t, uint32_t>;  // an element's bits
   constexpr int E = sizeof(T);
   extern __shared__ uint4 s_raw[];  // [rows][the run, from its offset in a vector on], then the table
@@ -303,16 +312,16 @@ __global__ void __launch_bounds__(kMostThreads) rotary_run_kernel(RotaryArgs a, 
   const int row0 = group * rows, here = min(rows, a.T - row0);
   const RotarySide& side = a.side[run >= runs_q];
   const int head0 = (run >= runs_q ? run - runs_q : run) * heads, n = min(heads, side.heads - head0);
-  const int bytes = n * a.hd * E, pitch = (heads * a.hd * E + 15) / 16 + 1;  // of a row in shared memory, in vectors
-  float2* s_turn = reinterpret_cast<float2*>(s_raw + rows * pitch);
+  const int bytes = n * a.hd * E;
+  float2* s_turn = reinterpret_cast<float2*>(s_raw + rows * pitch.d);
   auto at = [&](const void* p, long long stride, int r) {
     return static_cast<const char*>(p) + ((row0 + r) * stride + (long long)head0 * a.hd) * E;
   };
   const unsigned long long my_freq = first_freq(a, here);
   // vector v of row r: whole, or its elements that belong to the run
   auto each = [&](auto&& whole, auto&& element) {
-    for (int i = tid; i < here * pitch; i += blockDim.x) {
-      const int r = i / pitch, v = i - r * pitch, off = (int)((uintptr_t)at(side.in, side.in_stride, r) & 15);
+    for (int i = tid; i < here * pitch.d; i += blockDim.x) {
+      const int r = i / pitch, v = i - r * pitch.d, off = (int)((uintptr_t)at(side.in, side.in_stride, r) & 15);
       if (v * 16 >= off && v * 16 + 16 <= off + bytes)
         whole(r, i, v * 16 - off);
       else
@@ -328,7 +337,7 @@ __global__ void __launch_bounds__(kMostThreads) rotary_run_kernel(RotaryArgs a, 
     const int r = w / n;
     if (s_pos[r] >= kGone) continue;
     const int off = (int)((uintptr_t)at(side.in, side.in_stride, r) & 15);
-    T* x = reinterpret_cast<T*>(s_bytes + r * pitch * 16 + off) + (w - r * n) * a.hd;
+    T* x = reinterpret_cast<T*>(s_bytes + r * pitch.d * 16 + off) + (w - r * n) * a.hd;
     for (int i = lane; i < half; i += 32) {
       T &p = x[HALF ? i : 2 * i], &q = x[HALF ? half + i : 2 * i + 1];
       float u = BF16 ? bf16_to_f32((uint16_t)p) : __uint_as_float(p), v = BF16 ? bf16_to_f32((uint16_t)q) : __uint_as_float(q);
@@ -361,24 +370,27 @@ cudaError_t launch_runs(coli_ctx* ctx, const RotaryArgs& a) {
   const int heads = max(1, min(most, kBytes / head));
   const int runs_q = (a.side[0].heads + heads - 1) / heads, runs = runs_q + (a.side[1].heads + heads - 1) / heads;
   const int rows = max(1, min(kMostRows, kBytes / (heads * head)));
-  const size_t smem = (size_t)rows * ((heads * head + 15) / 16 + 1) * 16 + (size_t)rows * (a.rot / 2) * sizeof(float2);
+  const Divisor pitch((heads * head + 15) / 16 + 1);  // of a row in shared memory, in vectors
+  const size_t smem = (size_t)rows * pitch.d * 16 + (size_t)rows * (a.rot / 2) * sizeof(float2);
   // at most 12 KB of runs and two vectors a row; a table of rows * rot / 2 pairs, half of the elements at most: 24 KB
   const long long groups = (a.T + rows - 1) / rows;
   return launch_k(rotary_run_kernel<BF16, HALF>, (int)(groups * runs), kMostThreads, smem, ctx->stream, true, false, a, rows, heads, runs_q,
-                  runs);
+                  runs, pitch);
 }
 
 template <bool BF16, int V, bool HALF>
 cudaError_t launch_one(coli_ctx* ctx, const RotaryArgs& a) {
   const bool wide = (a.hd - a.rot) % (2 * V) == 0;
-  const int per_row = (a.rot / 2 / V + (a.hd - a.rot) / (wide ? 2 * V : V)) * (a.side[0].heads + a.side[1].heads);
+  const Divisor per_head(a.rot / 2 / V + (a.hd - a.rot) / (wide ? 2 * V : V)), per_row(per_head.d * (a.side[0].heads + a.side[1].heads));
+  if ((long long)per_row.d * per_head.d >> 31) return launch_runs<BF16, HALF>(ctx, a);  // beyond what is divided exactly
   // whole rows, as many as keep a CTA busy, and threads that share their tasks evenly
-  constexpr int U = kTasks;
-  const int rows = max(1, min(kMostRows, 256 * U / per_row));
-  const int rounds = (rows * per_row + U * kMostThreads - 1) / (U * kMostThreads);
-  const int threads = ((rows * per_row + U * rounds - 1) / (U * rounds) + 31) / 32 * 32;
+  constexpr int U = kTasks<V * (BF16 ? 2 : 4)>;
+  const int rows = max(1, min(kMostRows, 256 * U / per_row.d));
+  const int rounds = (rows * per_row.d + U * kMostThreads - 1) / (U * kMostThreads);
+  const int threads = ((rows * per_row.d + U * rounds - 1) / (U * rounds) + 31) / 32 * 32;
   const size_t smem = (size_t)rows * (a.rot / 2) * sizeof(float2);  // rows of 256 U tasks at most, or one: 32 KB
-  return launch_k(a.hd > a.rot ? rotary_kernel<BF16, V, HALF, true> : rotary_kernel<BF16, V, HALF, false>, (a.T + rows - 1) / rows, threads, smem, ctx->stream, true, false, a, rows, wide);
+  return launch_k(a.hd > a.rot ? rotary_kernel<BF16, V, HALF, true> : rotary_kernel<BF16, V, HALF, false>, (a.T + rows - 1) / rows, threads, smem, ctx->stream, true, false, a, rows, wide,
+                  per_head, per_row);
 }
 
 }  // namespace

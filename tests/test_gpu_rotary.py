@@ -67,6 +67,19 @@ def test_heads(ctx, hd, rot, interleaved, dtype):
     check(ko, k, turns, pos, interleaved, 1.25, dtype)
 
 
+@pytest.mark.parametrize("hq,hk,hd,rot,interleaved", [(8400, 8100, 1022, 4, False), (16384, 16384, 8, 8, False), (16384, 1, 66, 64, True)])
+def test_many_heads(ctx, hq, hk, hd, rot, interleaved):
+    freqs = B.coli_rotary_freqs(rot, 10000.0)
+    q, qt = make(2, hq, hd, "f32")
+    k, kt = make(2, hk, hd, "f32", 1)
+    pos = np.array([77, -5], np.int64)
+    qo, ko = torch.full_like(qt, 7.0), torch.full_like(kt, 7.0)
+    B.coli_rotary(ctx, qt, kt, freqs, qo, ko, positions=i32(pos.tolist()), interleaved=interleaved)
+    assert B.coli_check_error(ctx) == 0
+    check(qo, q, freqs.cpu().numpy(), pos, interleaved, 1.0, "f32")
+    check(ko, k, freqs.cpu().numpy(), pos, interleaved, 1.0, "f32")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("T,hq,hk,hd,rot", [(70, 9, 4, 80, 38), (33, 100, 3, 130, 130), (3, 0, 2, 1022, 1022), (40, 1, 0, 6, 2), (5, 7, 7, 1023, 1022)])
