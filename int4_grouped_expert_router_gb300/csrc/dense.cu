@@ -1,9 +1,9 @@
 // y = resid + act(W x + bias) * mul with 16-bit weights (layout: dense.h), on the fifth-generation tensor cores.
 //
-// D = W X^T: the rows of W are the instruction's M (128, or 256 of a pair of CTAs), the tokens its N (16 to 256). Units of work
-// are such tiles times column tiles of 64, dealt out evenly and contiguously to one CTA per SM (or pair), so that one token keeps
-// every SM streaming a contiguous run of W, and many tokens leave no part of a wave idle. A tile that several shares have a part
-// of is joined by the one that arrives last, in the order of the shares, so results do not depend on who that is.
+// D = W X^T: the rows of W are the instruction's M (128, or 256 of a pair of CTAs), the tokens its N (16 to 256). Every SM (or pair)
+// has one CTA and takes such tiles whole while there is one for each; what is left is split along the columns, so that one token
+// keeps every SM streaming a run of W, and many tokens leave no part of a wave idle (dense_plan). A tile that several shares have
+// a part of is joined by the one that arrives last, in the order of the shares, so results do not depend on who that is.
 //
 // One CTA, 20 warps: a producer (W by bulk copies, x by tiled ones, a ring of stages), a thread that issues the products, and
 // sixteen warps for what follows (bias, activation, factor, residual), which take a tile from tensor memory while the next one
@@ -11,23 +11,25 @@
 // Threads hold rows of W (128 neighbouring outputs of a token), so that rows of y at any alignment are read and written whole.
 //
 // Sums. The tensor core cuts a sum off where binary32 would round it, always towards zero: 6144 products lose some 2^-17 that
-// way. Where y is binary32 chunks of kChunk column tiles are formed by themselves and added in registers (24 us of 203 for the
-// prompt below; twice as long chunks would cost 10 and lose twice as much). Errors against 64 bits, in norm: 2.7e-7 for 6144
+// way. Where y is binary32 chunks of kChunk column tiles are formed by themselves and added in registers (of 4096 tokens, 6144 x
+// 6144, 195 us for 169; twice as long chunks lose twice as much for half of that; of binary32 activations chunks half as long lose half
+// as much and take 3 to 15 % longer). Errors against 64 bits, in norm: 2.7e-7 for 6144
 // columns of bf16, 7.6e-7 of binary32; a binary32 product sum by sum: 8.6e-7, 1.4e-6.
 // Binary32 activations enter as parts of 8 bits by truncation, x = h + m + l exactly (two parts, 16 bits, where y is rounded to 8),
 // each multiplied with the same staged tile of W; of up to four tokens the parts are rows of one tile.
 //
-// Measured (us; W = O x I): one token, 6144 x 6144, residual 15.0 (5.0 TB/s, 0.74 of a copy's rate), f32 18.3; 24 tokens, 50021 x
+// Measured (us; W = O x I): one token, 6144 x 6144, residual 14.3 (5.3 TB/s, 0.78 of a copy's rate), f32 16.5; 24 tokens, 50021 x
 // 6144, f32 logits 92 (6.7 TB/s, 0.98): bound by W's bytes, and at the small end by launch, first stages and the join of parts (4
-// us). 301 f32 tokens, 2048 x 6144, silu and factor 34: L2 bytes and the join. 4096 tokens, 6144 x 6144, gelu, bias, residual
-// 195 (1590 TFLOP/s, 0.82 of a library product's burst rate; the bare product 179, the library's 160): tensor pipe active 80 %
-// of the time.
+// us). 301 f32 tokens, 2048 x 6144, silu and factor 34: L2 bytes, the join, and x laid out ahead. 4096 tokens, 6144 x 6144, gelu,
+// bias, residual 185 (1670 TFLOP/s); the bare product 168, as long as the library's beside it. Over seconds, at the 1.47 GHz that
+// the power limit leaves, 207, 194 and 189. Tensor pipe active 82 % of the time.
 // What it cost to find: factor and residual read where they are used, not a group ahead (prompt 348 us; 252 so); one CTA's 128 x
 // 256 tiles, which ask L2 for 96 bytes a cycle and SM (219 us bare; pairs 183); 24 bytes of spilled registers inside the loop over
-// chunks (480 us instead of 214: the ring leaves no first-level cache); token tiles numbered before rows, so that W came from
-// memory once for each (512 tokens, 50021 rows: 392 us, 192 so); precise exponentials, divisions and erfc (silu of 1748 x 20122:
+// chunks (480 us instead of 214: the ring leaves no first-level cache); even runs of many tiles for every
+// share, so that W came from memory for each tile of tokens (2048 tokens, 20000 rows: 370 us, 273 so); precise exponentials, divisions and erfc (silu of 1748 x 20122:
 // 120 us, 77 so). Dropped: setmaxnreg to give the last warps more registers (the producer spills), spare warps that lay out x
-// stage by stage instead of a kernel ahead (f32 token 23.9 us against 18.3), tiles of 256 running sums (463 us).
+// stage by stage instead of a kernel ahead (f32 token 23.9 us against 18.3), tiles of 256 running sums (463 us), the parts of a
+// tile all copied into the ring when it is joined (no faster: writing, the fence and the count take as long as reading).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -199,8 +201,8 @@ __device__ __forceinline__ float reciprocal_fast(float x) {
 constexpr float kLog2e = 1.4426950408889634f;
 
 // 1 / (1 + e^-x). A result that is rounded to 8 bits takes the exponential of an argument that rounds, off by about |x| units
-// in the last place, and below 2^-126 is 0. EXACT: to a few units; e^-|x| = 2^t (1 + r ln 2), t + r the product -|x| log2(e) with what its rounding and
-// the factor's lose.
+// in the last place, and below 2^-126 is 0. EXACT: to a few units; e^-|x| = 2^t (1 + r ln 2), t + r the product -|x| log2(e) with
+// what its rounding and the factor's lose.
 template <bool EXACT>
 __device__ __forceinline__ float dense_sigmoid(float x) {
   if constexpr (!EXACT) {

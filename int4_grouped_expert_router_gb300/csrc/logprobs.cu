@@ -12,9 +12,9 @@
 // Where ties make it more than there is room for, the k-th largest of those found is a higher bound of the same kind, and the
 // search repeats.
 //
-// Measured: 2048 rows of 65536 (f32, one alternative) 89 us, 6.0 TB/s, 0.89 of a copy's rate (0.98 without alternatives, 115 us
-// with 20: their entries come from memory again); 64 rows of 151001 (bf16, 20 alternatives, 9 CTAs a row) 14.2 us, 8.3 without
-// alternatives: a chain of round trips to L2 (maxima, entries, parts) and barriers; one row of 50021 7.2 us. A vector on its way in
+// Measured: 2048 rows of 65536 (f32, one alternative) 87 us, 6.2 TB/s, 0.91 of a copy's rate (0.98 without alternatives, 113 us
+// with 20: their entries come from memory again); 64 rows of 151001 (bf16, 20 alternatives, 9 CTAs a row) 14.4 us, 9.6 without
+// alternatives: a chain of round trips to L2 (entries, parts written, counted, read) and barriers; one row of 50021 7 us, 4.4 without. A vector on its way in
 // registers instead of shared memory held the f32 rows to 4.1 TB/s (143 us); a maximum that moves with every larger entry, 151 us
 // then; threads that look through their own entries alone, 290 us with 20 alternatives; bounds from 32 groups, four times the
 // entries to rank for 32 alternatives.
