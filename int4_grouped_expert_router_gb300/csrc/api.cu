@@ -435,8 +435,8 @@ int coli_reserve(coli_ctx* ctx, int max_S, int max_E, int max_K, int max_D, int 
   // one-launch S == 1 FFN: a partial row of y per CTA
   const size_t stream = (size_t)ctx->num_sms * max_D * sizeof(float);
   if (stream > experts) experts = stream;
-  // 16-bit products: activations as up to four planes of 16-bit rows
-  const size_t planes = dense_x_bytes(max_S, std::max(max_D, max_I), 4);
+  // 16-bit products: activations as up to three planes of 16-bit rows
+  const size_t planes = dense_x_bytes(max_S, std::max(max_D, max_I), 3);
   if (planes > experts) experts = planes;
   const size_t slots = (size_t)COLI_MAX_ISSUES * max_S * max_D * sizeof(float);
   cudaSetDevice(ctx->device);

@@ -16,8 +16,8 @@
 // as much and take 3 to 15 % longer). Errors against 64 bits, in norm: 2.7e-7 for 6144
 // columns of bf16, 7.6e-7 of binary32; a binary32 product sum by sum: 8.6e-7, 1.4e-6.
 // Binary32 activations enter as parts of 8 bits by truncation, x = h + m + l exactly (two parts, 16 bits, where y is rounded to 8),
-// each multiplied with the same staged tile of W; of up to four tokens the parts are rows of one tile.
-//
+// each multiplied with the same staged tile of W. Where the parts' columns are 256 at most they are one instruction's, which reads
+// the tile once (24 tokens, 6144 x 6144: 21.1 -> 18.4 us), and their sums are added by the last warps: errors of 2.4e-7 again.
 // Measured (us; W = O x I): one token, 6144 x 6144, residual 14.3 (5.3 TB/s, 0.78 of a copy's rate), f32 16.5; 24 tokens, 50021 x
 // 6144, f32 logits 92 (6.7 TB/s, 0.98): bound by W's bytes, and at the small end by launch, first stages and the join of parts (4
 // us). 301 f32 tokens, 2048 x 6144, silu and factor 34: L2 bytes, the join, and x laid out ahead. 4096 tokens, 6144 x 6144, gelu,
@@ -50,11 +50,9 @@ constexpr int kThreads = (kWarpEpi + kEpiWarps) * 32;
 constexpr int kChunk = 4;   // column tiles
 constexpr int kGroup = 8;   // tokens that a thread of the last warps takes at a time
 constexpr int kSets = kEpiWarps / 4;
-constexpr int kQuad = 4;
 static_assert(kSets == kDenseCounters, "a counter for each set");
 
-// P parts of x for a staged tile of W, or kQuad: the parts of a token are four neighbouring rows of one tile (the last of them
-// 0), and their columns are added at the end. EXACT: y is binary32. PAIR: two CTAs of a cluster form 256 rows x N tokens with one
+// P parts of x for a staged tile of W. EXACT: y is binary32. PAIR: two CTAs of a cluster form 256 rows x N tokens with one
 // instruction (cta_group::2), each staging its 128 rows and half of the tokens.
 // The most tokens of a pair's tile: more running sums than 48 of a thread would not stay in registers.
 template <bool EXACT>
@@ -64,16 +62,18 @@ template <int N, int P, bool EXACT, bool PAIR>
 struct Shape {
   static constexpr int kCtas = PAIR ? 2 : 1;
   static constexpr int kXRows = N / kCtas;
-  static constexpr int kPasses = P == kQuad ? 1 : P;
-  static constexpr int kTokens = P == kQuad ? N / kQuad : N;          // of a tile
-  static constexpr int kTake = P == kQuad ? kGroup / kQuad : kGroup;  // of a group
-  static constexpr uint32_t kX = kPasses * kXRows * 128;
+  static constexpr uint32_t kX = P * kXRows * 128;
   static constexpr uint32_t kStage = kDenseTile + kX;
   static constexpr int kStages = std::min<uint32_t>(12, 224 * 1024 / kStage);
   static constexpr uint32_t kSmem = 1024 + kStages * kStage;
+  // Parts side by side are one instruction's columns as long as those are enough: it reads W's tile once instead of P times, and
+  // the small parts' sums lose nothing to the large ones'.
+  static constexpr bool kWide = P > 1 && P * N <= 256;
+  static constexpr int kCols = kWide ? P * N : N;
   // Accumulators. Chunks of few products are formed faster than a round trip between the two sides takes.
-  static constexpr int kAccs = EXACT && N <= 128 ? 4 : 2;
-  static constexpr int kTmem = N == 192 ? 512 : kAccs * N;  // a power of two from 32 on
+  static constexpr int kAcc = kCols <= 16 ? 16 : kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;  // columns apart
+  static constexpr int kAccs = EXACT && kAcc <= 128 ? 4 : 2;
+  static constexpr int kTmem = kAccs * kAcc;  // a power of two from 32 on
   static constexpr int kGroups = N / kGroup;
   static constexpr int kMine = EXACT ? (kGroups + kSets - 1) / kSets : 0;  // groups of a warp whose sums it holds
 };
@@ -166,7 +166,7 @@ __device__ __forceinline__ void dense_parts(float (&e)[8], uint32_t (&v)[P][4]) 
     }
 }
 
-// x as P planes of bf16 rows that start at 16-byte boundaries, or the parts of a row as kQuad rows of one plane.
+// x as P planes of bf16 rows that start at 16-byte boundaries.
 template <bool BF16, int P>
 __global__ void dense_x_kernel(const void* x, long long stride, int S, int I, bool vec, uint8_t* to) {
   griddep_launch_dependents();
@@ -178,11 +178,10 @@ __global__ void dense_x_kernel(const void* x, long long stride, int S, int I, bo
     float e[8];
     uint32_t v[P][4];
     dense_eight(x, (size_t)s * stride + i0, I - i0, BF16, vec, e);
-    dense_parts<P>(e, v);  // nothing is left for a fourth part
+    dense_parts<P>(e, v);
 #pragma unroll
     for (int p = 0; p < P; p++) {
-      const size_t at = P == kQuad ? n + (3ll * s + p) * chunks : p * n_all + n;
-      *reinterpret_cast<uint4*>(to + at * 16) = make_uint4(v[p][0], v[p][1], v[p][2], v[p][3]);
+      *reinterpret_cast<uint4*>(to + (p * n_all + n) * 16) = make_uint4(v[p][0], v[p][1], v[p][2], v[p][3]);
     }
   }
 }
@@ -376,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         const uint32_t s = n % H::kStages;
         if (!(holds && n == 0))
 #pragma unroll
-          for (int p = 0; p < H::kPasses; p++) {
+          for (int p = 0; p < P; p++) {
             uint8_t* to = smem + s * H::kStage + kDenseTile + p * H::kXRows * 128;
             const int y = p * a.d.S + x_at.place.tokens * N + rank * H::kXRows;
             if constexpr (PAIR)
@@ -409,7 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t w_desc = uniform(sw128_kmajor_desc(smem)), x_desc = uniform(sw128_kmajor_desc(smem + kDenseTile));
     if (rank == 0 && elect_one()) {
-      constexpr uint32_t kId = bf16_f32_idesc(kDenseRows * H::kCtas, N);
+      constexpr uint32_t kId = bf16_f32_idesc(kDenseRows * H::kCtas, H::kCols);
+      constexpr int kSteps = H::kWide ? 1 : P;
       uint32_t s = 0, phase = 0, chunk = 0;
       int left = (int)units;
       for (Walk walk = start; left > 0; walk.next(a, shares, tail)) {
@@ -418,17 +418,17 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           const int here = EXACT ? min(kChunk, seg - done) : seg;
           wait(&acc_empty[chunk % H::kAccs], (chunk / H::kAccs + 1) & 1);
           tc_fence_after_sync();
-          const uint32_t acc = tm + chunk % H::kAccs * N;
+          const uint32_t acc = tm + chunk % H::kAccs * H::kAcc;
           for (int i = 0; i < here; i++) {
             wait(&full[s], phase);
             tc_fence_after_sync();
             const uint32_t at = s * (H::kStage >> 4);  // a descriptor's address field counts 16 bytes
 #pragma unroll
-            for (int p = H::kPasses - 1; p >= 0; p--)  // the small parts first
+            for (int p = kSteps - 1; p >= 0; p--)  // the small parts first
 #pragma unroll
               for (int kk = 0; kk < 4; kk++)
                 tc_mma_bf16_n<H::kCtas>(acc, w_desc + at + kk * 2, x_desc + at + p * (H::kXRows * 8) + kk * 2, kId,
-                                        i > 0 || p < H::kPasses - 1 || kk > 0);
+                                        i > 0 || p < kSteps - 1 || kk > 0);
             tc_commit_n<H::kCtas>(&empty[s]);
             if (++s == (uint32_t)H::kStages) s = 0, phase ^= 1;
           }
@@ -460,20 +460,19 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     // A tile's rows from this thread's, a group of tokens at a time. What is read beside the sums is asked for a group ahead. Many
     // tokens' arrays pass through L2 as the first to go, so that W and x stay (1748 x 1472 x 20122, silu, factor and residual:
     // 123 us without, 116 so).
-    constexpr int kTake = H::kTake;
     struct Beside {
-      uint32_t f[kTake], r[kTake];
+      uint32_t f[kGroup], r[kGroup];
     };
     int o, t0;  // of the tile: this thread's row, the first token
     float bias;
     constexpr size_t kE = EXACT ? 4 : 2;
     auto ask = [&](Beside& v, int g) {
       if (g >= H::kGroups || o >= a.d.O) return;
-      const int t = t0 + g * kTake, n = a.d.S - t;
+      const int t = t0 + g * kGroup, n = a.d.S - t;
       const uint32_t off = (uint32_t)o * kE;
-      auto load = [&](const void* p, long long stride, uint32_t (&to)[kTake]) {
+      auto load = [&](const void* p, long long stride, uint32_t (&to)[kGroup]) {
 #pragma unroll
-        for (int i = 0; i < kTake; i++) {
+        for (int i = 0; i < kGroup; i++) {
           const char* at = static_cast<const char*>(p) + (t + i) * stride * kE + off;
           using T = std::conditional_t<EXACT, unsigned int, unsigned short>;
           if (i < n) to[i] = PAIR ? __ldcs(reinterpret_cast<const T*>(at)) : __ldcg(reinterpret_cast<const T*>(at));
@@ -485,27 +484,23 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     auto value = [](uint32_t u) { return __uint_as_float(EXACT ? u : u << 16); };
     auto finish = [&](float (&sum)[kGroup], const Beside& v, int g) {
       if (o >= a.d.O) return;
-      const int t = t0 + g * kTake, n = a.d.S - t;
+      const int t = t0 + g * kGroup, n = a.d.S - t;
       const uint32_t off = (uint32_t)o * kE;
-      float z[kTake];
+      float z[kGroup];
 #pragma unroll
-      for (int i = 0; i < kTake; i++) {
-        if constexpr (P == kQuad)
-          z[i] = (sum[4 * i + 2] + sum[4 * i + 1]) + sum[4 * i];
-        else
-          z[i] = sum[i];
-        if (i < n) broken = fmaf(z[i], 0.f, broken);
-        z[i] += bias;
+      for (int i = 0; i < kGroup; i++) {
+        if (i < n) broken = fmaf(sum[i], 0.f, broken);
+        z[i] = sum[i] + bias;
       }
       dense_act<EXACT>(z, a.d.act);
       if (a.d.mul)
 #pragma unroll
-        for (int i = 0; i < kTake; i++) z[i] *= value(v.f[i]);
+        for (int i = 0; i < kGroup; i++) z[i] *= value(v.f[i]);
       if (a.d.resid)
 #pragma unroll
-        for (int i = 0; i < kTake; i++) z[i] += value(v.r[i]);
+        for (int i = 0; i < kGroup; i++) z[i] += value(v.r[i]);
 #pragma unroll
-      for (int i = 0; i < kTake; i++) {
+      for (int i = 0; i < kGroup; i++) {
         char* at = static_cast<char*>(a.d.y) + (t + i) * a.d.y_stride * kE + off;
         using T = std::conditional_t<EXACT, float, unsigned short>;
         T v;
@@ -524,8 +519,29 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     auto at_tile = [&](int tile) {
       const Place at = place_of(tile, a.rt, a.nt);
       o = (at.rows * H::kCtas + rank) * kDenseRows + row;
-      t0 = at.tokens * H::kTokens;
+      t0 = at.tokens * N;
       bias = a.d.bias && o < a.d.O ? __ldcg(a.d.bias + o) : 0.f;
+    };
+    // the columns of a group's first part; those of the others are kXRows apart, and of a pair the second CTA's tokens behind all
+    auto column = [&](uint32_t acc, int g) { return acc + g * kGroup + (H::kWide ? g * kGroup / H::kXRows * (P - 1) * H::kXRows : 0); };
+    auto read_parts = [&](uint32_t acc, int g, float (&z)[kGroup]) {
+      const uint32_t at = column(acc, g);
+      tmem_ld8(at + (H::kWide ? P - 1 : 0) * H::kXRows, z);
+      if constexpr (H::kWide) {
+#pragma unroll
+        for (int p = P - 2; p >= 0; p--) {
+          float v[kGroup];
+          tmem_ld8(at + p * H::kXRows, v);
+#pragma unroll
+          for (int i = 0; i < kGroup; i++) z[i] += v[i];
+        }
+      }
+    };
+    auto read_sums = [&](uint32_t acc, int g, float (&z)[kGroup]) {
+      if constexpr (EXACT)
+        tmem_ld8(column(acc, g), z);  // put there chunk by chunk
+      else
+        read_parts(acc, g, z);
     };
     uint32_t chunk = 0;
     int left = (int)units;
@@ -540,18 +556,18 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           wait(&acc_full[chunk % H::kAccs], chunk / H::kAccs & 1);
           __syncwarp();
           tc_fence_after_sync();
-          const uint32_t acc = tm + chunk % H::kAccs * N;
+          const uint32_t acc = tm + chunk % H::kAccs * H::kAcc;
           const bool last = done + kChunk >= seg;
-          if (last && done == 0) break;  // one chunk: it is where it is read from below
+          if (!H::kWide && last && done == 0) break;  // one chunk: it is where it is read from below
 #pragma unroll
           for (int m = 0; m < H::kMine; m++) {
             const int g = kSets * m + set;
             if (g >= H::kGroups) break;
             float v[kGroup];
-            tmem_ld8(acc + g * kGroup, v);
+            read_parts(acc, g, v);
 #pragma unroll
             for (int i = 0; i < kGroup; i++) sum[m][i] += v[i];
-            if (last) tmem_st8(acc + g * kGroup, sum[m]);
+            if (last) tmem_st8(column(acc, g), sum[m]);
           }
           if (last) break;
           tc_fence_before_sync();
@@ -569,12 +585,12 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         __syncwarp();
         tc_fence_after_sync();
       }
-      const uint32_t acc = tm + chunk % H::kAccs * N;
+      const uint32_t acc = tm + chunk % H::kAccs * H::kAcc;
       if (whole) {
 #pragma unroll 1
         for (int g = set; g < H::kGroups; g += kSets) {
           float z[kGroup];
-          tmem_ld8(acc + g * kGroup, z);
+          read_sums(acc, g, z);
           const Beside now = next;
           ask(next, g + kSets);
           finish(z, now, g);
@@ -587,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
 #pragma unroll 1
         for (int g = set; g < H::kGroups; g += kSets) {
           float z[kGroup];
-          tmem_ld8(acc + g * kGroup, z);
+          read_sums(acc, g, z);
 #pragma unroll
           for (int i = 0; i < 2; i++) __stcg(mine + (g * 2 + i) * kDenseRows, make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]));
         }
@@ -619,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
 #pragma unroll 1
           for (int g = set; g < H::kGroups; g += kSets) {
             float mine8[kGroup], z[kGroup];
-            tmem_ld8(acc + g * kGroup, mine8);
+            read_sums(acc, g, mine8);
 #pragma unroll
             for (int i = 0; i < 2; i++) z[4 * i] = p[i].x, z[4 * i + 1] = p[i].y, z[4 * i + 2] = p[i].z, z[4 * i + 3] = p[i].w;
             if (first == own)
@@ -680,8 +696,7 @@ struct Plan {
 };
 
 Plan dense_plan(int S, int O, int I, int parts, bool exact, int num_sms) {
-  const bool quad = parts == kQuad;
-  const int most = exact ? kPairTokens<true> : kPairTokens<false>, passes = quad ? 1 : parts;
+  const int most = exact ? kPairTokens<true> : kPairTokens<false>;
   const Plan all[] = {{16, false}, {32, false}, {64, false}, {128, false}, {64, true}, {128, true}, {most, true}};
   const int kt = (I + kDenseCols - 1) / kDenseCols;
   const double bytes = (double)dense_bytes(O, I);
@@ -690,9 +705,9 @@ Plan dense_plan(int S, int O, int I, int parts, bool exact, int num_sms) {
   for (const Plan& p : all) {
     if ((p.tokens == 16) != (S <= 16)) continue;
     const int ctas = p.pair ? 2 : 1, N = p.tokens, shares = num_sms / ctas;
-    const int nt = quad ? 1 : (S + N - 1) / N;
+    const int nt = (S + N - 1) / N;
     const int tiles = (O + kDenseRows * ctas - 1) / (kDenseRows * ctas) * nt, waves = tiles / shares;
-    const double unit = std::max((kDenseTile + passes * N / ctas * 128.0) / 64 + 60, passes * N * 2.0 + 60), tile = kt * unit + 220;
+    const double unit = std::max((kDenseTile + parts * N / ctas * 128.0) / 64 + 60, parts * N * 2.0 + 60), tile = kt * unit + 220;
     const double read = bytes / (26.0 * num_sms) * (1 + 0.8 * (nt - 1)) / tiles;  // W for a tile, where all SMs read
     auto look = [&](int whole, int q) {
       const int rest = tiles - whole * shares;
@@ -728,7 +743,7 @@ int launch_one(coli_ctx* ctx, TileArgs& a, const Plan& plan, const CUtensorMap& 
   static_assert((size_t)2 * N * kDenseRows <= kPartFloats, "a CTA leaves more than there is room for");
   a.kt = (a.d.I + kDenseCols - 1) / kDenseCols;
   const int rows = kDenseRows * H::kCtas;
-  a.nt = (a.d.S + H::kTokens - 1) / H::kTokens;
+  a.nt = (a.d.S + N - 1) / N;
   a.rt = (a.d.O + rows - 1) / rows;
   a.stream = a.nt == 1;
   const int all = ctx->num_sms / H::kCtas, rest = a.rt * a.nt - plan.whole * all;
@@ -787,7 +802,7 @@ int launch_dense(coli_ctx* ctx, const DenseArgs& args, const CUtensorMap& w_map,
   a.part = ctx->d_part;
   a.count = ctx->d_dense_count;
   const bool exact = y_dtype == COLI_DTYPE_F32;
-  const int parts = x_dtype == COLI_DTYPE_BF16 ? 1 : !exact ? 2 : a.d.S <= kQuad ? kQuad : 3;
+  const int parts = x_dtype == COLI_DTYPE_BF16 ? 1 : !exact ? 2 : 3;
   // rows of x by tiled copies where they lie, or from planes laid out in the workspace
   const long long row = a.d.S == 1 ? (a.d.I + 7) / 8 * 8 : a.d.x_stride;
   const bool direct = parts == 1 && (uintptr_t)a.d.x % 16 == 0 && row % 8 == 0;
@@ -809,8 +824,7 @@ int launch_dense(coli_ctx* ctx, const DenseArgs& args, const CUtensorMap& w_map,
     const bool vec = (uintptr_t)a.d.x % 16 == 0 && row % 4 == 0;
     const cudaError_t e = parts == 1   ? lay_out<true, 1>(ctx, a.d, false, to)
                           : parts == 2 ? lay_out<false, 2>(ctx, a.d, vec, to)
-                          : parts == 3 ? lay_out<false, 3>(ctx, a.d, vec, to)
-                                       : lay_out<false, kQuad>(ctx, a.d, vec, to);
+                                       : lay_out<false, 3>(ctx, a.d, vec, to);
     if (e != cudaSuccess) return cuda_fail(ctx, e, "dense_linear layout launch");
   }
   auto tokens = [&](auto p, auto y32) {
@@ -826,7 +840,6 @@ int launch_dense(coli_ctx* ctx, const DenseArgs& args, const CUtensorMap& w_map,
     if (t.tokens == 64) return launch_one<64, P, E, false>(ctx, a, t, map, w_map);
     return launch_one<128, P, E, false>(ctx, a, t, map, w_map);
   };
-  if (parts == kQuad) return launch_one<16, kQuad, true, false>(ctx, a, t, map, w_map);
   if (parts == 3) return tokens(std::integral_constant<int, 3>{}, std::true_type{});
   if (parts == 2) return tokens(std::integral_constant<int, 2>{}, std::false_type{});
   if (exact) return tokens(std::integral_constant<int, 1>{}, std::true_type{});

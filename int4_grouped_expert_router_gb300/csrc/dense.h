@@ -31,7 +31,7 @@ struct DenseArgs {
   int* err;
 };
 
-// Workspace of a call that lays its activations out first: `parts` planes (up to 4) of S rows, each padded to 16 bytes.
+// Workspace of a call that lays its activations out first: `parts` planes (up to 3) of S rows, each padded to 16 bytes.
 inline size_t dense_x_bytes(long long S, int I, int parts) { return (size_t)S * ((size_t)(I + 7) / 8 * 16) * parts; }
 
 // rows [row0, row0 + rows) of W [. x I], row-major at `src`, into the layout; row0 a multiple of kDenseRows.
