@@ -14,13 +14,13 @@
 // way. Where y is binary32 chunks of kChunk column tiles are formed by themselves and added in registers (of 4096 tokens, 6144 x
 // 6144, 195 us for 169; twice as long chunks lose twice as much for half of that; of binary32 activations chunks half as long lose half
 // as much and take 3 to 15 % longer). Errors against 64 bits, in norm: 2.7e-7 for 6144
-// columns of bf16, 7.6e-7 of binary32; a binary32 product sum by sum: 8.6e-7, 1.4e-6.
+// columns of bf16, 2.4e-7 of binary32 (7.7e-7 in tiles of 128 tokens and more); a binary32 product sum by sum: 8.6e-7, 1.4e-6.
 // Binary32 activations enter as parts of 8 bits by truncation, x = h + m + l exactly (two parts, 16 bits, where y is rounded to 8),
 // each multiplied with the same staged tile of W. Where the parts' columns are 256 at most they are one instruction's, which reads
-// the tile once (24 tokens, 6144 x 6144: 21.1 -> 18.4 us), and their sums are added by the last warps: errors of 2.4e-7 again.
-// Measured (us; W = O x I): one token, 6144 x 6144, residual 14.3 (5.3 TB/s, 0.78 of a copy's rate), f32 16.5; 24 tokens, 50021 x
+// the tile once (24 tokens, 6144 x 6144: 18.4 us against 21.1), and their sums are added by the last warps.
+// Measured (us; W = O x I): one token, 6144 x 6144, residual 14.3 (5.3 TB/s, 0.78 of a copy's rate), f32 17.8; 24 tokens, 50021 x
 // 6144, f32 logits 92 (6.7 TB/s, 0.98): bound by W's bytes, and at the small end by launch, first stages and the join of parts (4
-// us). 301 f32 tokens, 2048 x 6144, silu and factor 34: L2 bytes, the join, and x laid out ahead. 4096 tokens, 6144 x 6144, gelu,
+// us). 301 f32 tokens, 2048 x 6144, silu and factor 32: L2 bytes, the join, and x laid out ahead. 4096 tokens, 6144 x 6144, gelu,
 // bias, residual 185 (1670 TFLOP/s); the bare product 168, as long as the library's beside it. Over seconds, at the 1.47 GHz that
 // the power limit leaves, 207, 194 and 189. Tensor pipe active 82 % of the time.
 // What it cost to find: factor and residual read where they are used, not a group ahead (prompt 348 us; 252 so); one CTA's 128 x
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
 }
 
 // A call's tiles and how they are dealt out: what takes the fewest cycles by a model that was fitted to 12274 measurements (O, I
-// of 768 to 50021, S of 1 to 4096, each type; what it picks takes 1.5 % more than the best of them on average, 19 % at most).
+// of 768 to 50021, S of 1 to 4096, each type; what it picks takes 1.5 to 1.8 % more than the best of them on average, 19 % at most).
 //   A column tile takes its bytes from L2 at 64 a cycle and 60, or its products and 60; a tile 220 more. W is read at 26 bytes a
 //   cycle and SM, of which two thirds are enough, and eight tenths of it once more for each further tile of tokens. A split tile
 //   takes N times 40 cycles and 19.6 for each part, or 3.5 more where shares begin anywhere (their ends meet two tiles). A pair of
