@@ -297,17 +297,17 @@ __global__ void __launch_bounds__(kMostThreads, kCtas) rotary_kernel(RotaryArgs 
 
 // Rows whose pairs do not lie in whole vectors (an odd half, an odd stride): runs of heads pass through shared memory, read and
 // written in 16-byte vectors as far as the run's own alignment goes, and are turned there element by element. A CTA takes `heads`
-// heads (of q, then of k) of `rows` rows. 3001 rows of 40 heads of 80, 38 channels turned, bf16: 21.4 us; two elements a task of
-// the other kernel took 31 us.
+// heads (of q, then of k) of `rows` rows. 3001 rows of 40 heads of 80, 38 channels turned, bf16: 19 us (a
+// warp for each head 25, two elements a task of the other kernel more than 30); 8191 of 72 heads of 96, 73 us (119).
 template <bool BF16, bool HALF>
-__global__ void __launch_bounds__(kMostThreads) rotary_run_kernel(RotaryArgs a, int rows, int heads, int runs_q, int runs, Divisor pitch) {
+__global__ void __launch_bounds__(kMostThreads) rotary_run_kernel(RotaryArgs a, int rows, int heads, int runs_q, int runs, Divisor pitch, Divisor half) {
   using T = std::conditional_t<BF16, uint16_t, uint32_t>;  // an element's bits
   constexpr int E = sizeof(T);
   extern __shared__ uint4 s_raw[];  // [rows][the run, from its offset in a vector on], then the table
   __shared__ long long s_pos[kMostRows];
   griddep_launch_dependents();
   griddep_wait();
-  const int tid = threadIdx.x, lane = tid & 31, half = a.rot / 2;
+  const int tid = threadIdx.x;
   const int group = blockIdx.x / runs, run = blockIdx.x - group * runs;
   const int row0 = group * rows, here = min(rows, a.T - row0);
   const RotarySide& side = a.side[run >= runs_q];
@@ -333,15 +333,15 @@ __global__ void __launch_bounds__(kMostThreads) rotary_run_kernel(RotaryArgs a, 
   each([&](int r, int i, int b) { s_raw[i] = __ldcg(reinterpret_cast<const uint4*>(at(side.in, side.in_stride, r) + b)); },
        [&](int r, int i, int b) { *reinterpret_cast<T*>(s_bytes + i) = load_cg<T>(at(side.in, side.in_stride, r) + b); });
   make_table(a, row0, here, my_freq, s_pos, s_turn);
-  for (int w = tid >> 5; w < here * n; w += blockDim.x >> 5) {
-    const int r = w / n;
+  for (int r = 0; r < here; r++) {
     if (s_pos[r] >= kGone) continue;
     const int off = (int)((uintptr_t)at(side.in, side.in_stride, r) & 15);
-    T* x = reinterpret_cast<T*>(s_bytes + r * pitch.d * 16 + off) + (w - r * n) * a.hd;
-    for (int i = lane; i < half; i += 32) {
-      T &p = x[HALF ? i : 2 * i], &q = x[HALF ? half + i : 2 * i + 1];
+    T* row = reinterpret_cast<T*>(s_bytes + r * pitch.d * 16 + off);
+    for (int w = tid; w < n * half.d; w += blockDim.x) {
+      const int head = w / half, i = w - head * half.d;
+      T *x = row + head * a.hd, &p = x[HALF ? i : 2 * i], &q = x[HALF ? half.d + i : 2 * i + 1];
       float u = BF16 ? bf16_to_f32((uint16_t)p) : __uint_as_float(p), v = BF16 ? bf16_to_f32((uint16_t)q) : __uint_as_float(q);
-      rotate(u, v, s_turn[r * half + i]);
+      rotate(u, v, s_turn[r * half.d + i]);
       p = BF16 ? f32_to_bf16_rn(u) : __float_as_uint(u), q = BF16 ? f32_to_bf16_rn(v) : __float_as_uint(v);
     }
   }
@@ -375,7 +375,7 @@ cudaError_t launch_runs(coli_ctx* ctx, const RotaryArgs& a) {
   // at most 12 KB of runs and two vectors a row; a table of rows * rot / 2 pairs, half of the elements at most: 24 KB
   const long long groups = (a.T + rows - 1) / rows;
   return launch_k(rotary_run_kernel<BF16, HALF>, (int)(groups * runs), kMostThreads, smem, ctx->stream, true, false, a, rows, heads, runs_q,
-                  runs, pitch);
+                  runs, pitch, Divisor(a.rot / 2));
 }
 
 template <bool BF16, int V, bool HALF>
