@@ -171,18 +171,16 @@ template <bool BF16, int P>
 __global__ void dense_x_kernel(const void* x, long long stride, int S, int I, bool vec, uint8_t* to) {
   griddep_launch_dependents();
   griddep_wait();
-  const int chunks = (I + 7) / 8;
-  const long long n_all = (long long)S * chunks;
-  for (long long n = (long long)blockIdx.x * blockDim.x + threadIdx.x; n < n_all; n += (long long)gridDim.x * blockDim.x) {
-    const int s = (int)(n / chunks), i0 = (int)(n - (long long)s * chunks) * 8;
+  const int chunks = (I + 7) / 8, n_all = S * chunks;  // at most 2^28
+  for (int n = blockIdx.x * blockDim.x + threadIdx.x; n < n_all; n += gridDim.x * blockDim.x) {
+    const int s = n / chunks, i0 = (n - s * chunks) * 8;
     float e[8];
     uint32_t v[P][4];
     dense_eight(x, (size_t)s * stride + i0, I - i0, BF16, vec, e);
     dense_parts<P>(e, v);
 #pragma unroll
-    for (int p = 0; p < P; p++) {
-      *reinterpret_cast<uint4*>(to + (p * n_all + n) * 16) = make_uint4(v[p][0], v[p][1], v[p][2], v[p][3]);
-    }
+    for (int p = 0; p < P; p++)
+      *reinterpret_cast<uint4*>(to + ((size_t)p * n_all + n) * 16) = make_uint4(v[p][0], v[p][1], v[p][2], v[p][3]);
   }
 }
 
