@@ -427,14 +427,17 @@ __global__ void __launch_bounds__(kThreads, kLogprobCtas) logprob_kernel(Logprob
 
   // ---- the parts of a row ----
   if (a.parts > 1) {
+    static_assert(COLI_MAX_TOP <= 32, "a lane for each");
     LogprobPart* part = a.part + (size_t)row_id * a.parts;
-    if (tid == 0) part[part_id].most = most, part[part_id].b = sum.b, part[part_id].s = sum.s, part[part_id].t = sum.t;
-    if (tid < a.k) part[part_id].top[tid] = s.best[tid];
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-      s.last = atomicAdd(a.count + row_id, 1) == a.parts - 1;
-      if (s.last) a.count[row_id] = 0;
+    if (warp == 0) {  // one warp's writes: their fence is one wait
+      if (lane == 0) *reinterpret_cast<float4*>(part + part_id) = make_float4(most, sum.b, sum.s, sum.t);
+      if (lane < a.k) part[part_id].top[lane] = s.best[lane];
+      __syncwarp();
+      if (lane == 0) {
+        __threadfence();
+        s.last = atomicAdd(a.count + row_id, 1) == a.parts - 1;
+        if (s.last) a.count[row_id] = 0;
+      }
     }
     __syncthreads();
     if (!s.last) return;
