@@ -238,7 +238,6 @@ __device__ __forceinline__ void give_group(Shared& s, uint64_t key) {
 __device__ __forceinline__ void rank_found(Shared& s, int n, int k) {
   const int tid = threadIdx.x;
   constexpr int kEach = kRoom / kThreads;
-  if (tid < COLI_MAX_TOP) s.best[tid] = 0;
   // Many: the k-th largest of the groups' maxima is a bound again, and what is below it goes. More than kThreads keys give each
   // of the kGroups groups kPerGroup of them at least, and k groups stay at most.
   while (n > kThreads) {
@@ -259,6 +258,8 @@ __device__ __forceinline__ void rank_found(Shared& s, int n, int k) {
     n = s.n;
     __syncthreads();
   }
+  // Ranks are below n: what is cleared here and what is stored below are different entries, whichever warp comes first.
+  if (tid >= n && tid < COLI_MAX_TOP) s.best[tid] = 0;
   for (int i0 = 0; i0 < n; i0 += kGroups) {
     const int i = i0 + tid / kPerGroup;
     const uint64_t mine = i < n ? s.found[i] : 0;
