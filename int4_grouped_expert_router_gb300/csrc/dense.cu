@@ -330,10 +330,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     }
   };
   const bool holds = a.withhold && share == 0;  // the first copy, in both CTAs of a pair
-  // the last arrivals on these barriers come before the CTA's memory goes, and with them the last reads of it
-  auto wait_for_products = [&]() {
-    for (uint32_t i = units > (uint32_t)H::kStages ? units - H::kStages : 0; i < units; i++)
-      mbar_wait(&empty[i % H::kStages], (i / H::kStages) & 1, a.wait_ns);
+  // The last arrivals on these barriers come before the CTA's memory goes, and with them the last reads of it. A parity tells a
+  // phase from its neighbours alone: a thread that waits here has followed the barriers up to the fill before.
+  auto wait_for_products = [&](uint32_t fills) {
+    for (uint32_t i = fills > (uint32_t)H::kStages ? fills - H::kStages : 0; i < fills; i++)
+      wait(&empty[i % H::kStages], (i / H::kStages) & 1);
   };
 
   if (warp == 0) {
@@ -398,6 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       if (rank == 0)
         for (uint32_t i = n > (uint32_t)H::kStages ? n - H::kStages : 0; i < n; i++)
           if (!(holds && i == 0)) mbar_wait(&full[i % H::kStages], (i / H::kStages) & 1, a.wait_ns);
+      // the second one's memory is read by products that the first CTA issues: its producer has seen every fill but the last
+      if (rank == 1) wait_for_products(n);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -408,17 +411,18 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     if (rank == 0 && elect_one()) {
       constexpr uint32_t kId = bf16_f32_idesc(kDenseRows * H::kCtas, H::kCols);
       constexpr int kSteps = H::kWide ? 1 : P;
-      uint32_t s = 0, phase = 0, chunk = 0;
+      uint32_t s = 0, phase = 0, chunk = 0, issued = 0;
       int left = (int)units;
-      for (Walk walk = start; left > 0; walk.next(a, shares, tail)) {
+      for (Walk walk = start; left > 0 && alive; walk.next(a, shares, tail)) {
         const int seg = min(a.kt - walk.k, left);
-        for (int done = 0; done < seg;) {
+        for (int done = 0; done < seg && alive;) {
           const int here = EXACT ? min(kChunk, seg - done) : seg;
           wait(&acc_empty[chunk % H::kAccs], (chunk / H::kAccs + 1) & 1);
           tc_fence_after_sync();
           const uint32_t acc = tm + chunk % H::kAccs * H::kAcc;
           for (int i = 0; i < here; i++) {
             wait(&full[s], phase);
+            if (!alive) break;  // nothing more is issued: what has been is waited for below, and the other side gives up by itself
             tc_fence_after_sync();
             const uint32_t at = s * (H::kStage >> 4);  // a descriptor's address field counts 16 bytes
 #pragma unroll
@@ -428,17 +432,19 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
                 tc_mma_bf16_n<H::kCtas>(acc, w_desc + at + kk * 2, x_desc + at + p * (H::kXRows * 8) + kk * 2, kId,
                                         i > 0 || p < kSteps - 1 || kk > 0);
             tc_commit_n<H::kCtas>(&empty[s]);
+            issued++;
             if (++s == (uint32_t)H::kStages) s = 0, phase ^= 1;
           }
+          if (!alive) break;
           tc_commit_n<H::kCtas>(&acc_full[chunk % H::kAccs]);
           chunk++;
           done += here;
         }
         left -= seg;
       }
-      wait_for_products();
-    } else if (PAIR && rank == 1 && elect_one()) {
-      wait_for_products();
+      alive = true;
+      wait_for_products(issued);
+      if (chunk > 0) wait(&acc_full[(chunk - 1) % H::kAccs], ((chunk - 1) / H::kAccs) & 1);
     }
     __syncwarp();
   } else if (warp >= kWarpEpi) {
