@@ -497,7 +497,8 @@ COLI_API int coli_rotary_freqs(int rot_dim, double base, int scaling, double fac
 /*
  * q, q_out: [T x q_heads x head_dim], k, k_out: [T x k_heads x head_dim] in dtype; the channels and heads of a row contiguous,
  * rows a stride apart (elements; slices of a fused projection's output serve as they are). Either of q and k may be NULL, with
- * its output and 0 heads. An output may be its input (same address and stride): in place; no other overlap. freqs: device.
+ * its output and 0 heads. An output may be its input (same address and stride): in place; no other overlap. freqs: device. Every array
+ * is aligned to its elements (freqs: 8 bytes).
  * Where a row is:
  *   positions [T] (device int32): any value, negative ones too, which turn backwards -- so the call with all positions negated
  *     undoes a turn of scale 1, and is the gradient of the call. q_start and lens are then NULL and B 0;

@@ -1062,6 +1062,8 @@ int coli_rotary(coli_ctx* ctx, const void* q, long long q_stride, void* q_out, l
     if (!lens || B < 1 || B > COLI_MAX_KV_SEQS) return fail(ctx, COLI_E_INVAL, "rotary: without positions, lens and 1 to COLI_MAX_KV_SEQS sequences");
     if (!q_start && T != B) return fail(ctx, COLI_E_INVAL, "rotary: without q_start there is one row per sequence (T == B)");
   }
+  if ((uintptr_t)freqs % 8 != 0 || ((uintptr_t)positions | (uintptr_t)q_start | (uintptr_t)lens) % 4 != 0)
+    return fail(ctx, COLI_E_INVAL, "rotary: freqs, positions, q_start or lens not aligned to its elements");
   auto rows_of = [&](const RotarySide& s, bool in) {
     const long long e = (long long)elem;
     return Rows{in ? s.in : s.out, (in ? s.in_stride : s.out_stride) * e, (long long)s.heads * head_dim * e, T};
