@@ -233,7 +233,8 @@ __device__ __forceinline__ float dense_gelu(float x) {
   p = fmaf(p, t, 1.4410624504089355f);
   p = fmaf(p, t, -1.8256721496582031f);
   const float h = 0.5f * fabsf(x) * (t * exp2_fast(fmaf(a * a, -kLog2e, p)));
-  return x > 0.f ? x - h : -h;
+  if (x > 0.f) return x < __builtin_huge_valf() ? x - h : x;  // t is 0 of an infinity, and h not a number
+  return -h;
 }
 
 template <bool EXACT, int N>
