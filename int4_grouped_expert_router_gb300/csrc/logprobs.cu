@@ -493,7 +493,12 @@ __global__ void __launch_bounds__(kThreads, kLogprobCtas) logprob_kernel(Logprob
   const float nan = __uint_as_float(0x7fc00000u);
   if (bad && tid == 0) set_error(a.err, COLI_E_NONFINITE);
   const float base = Sums::from(most), log_s = logf(sum.s);
-  auto log_p = [&](float x) { return bad ? nan : empty ? -kInf : fmaf(x - base, a.scale, -log_s); };
+  auto log_p = [&](float x) {
+    const float d = x - base;
+    // a difference beyond binary32 of entries that are not, which the scale may bring back
+    const float z = d == -kInf && x > -kInf ? fmaf(0.5f * x - 0.5f * base, 2.f * a.scale, -log_s) : fmaf(d, a.scale, -log_s);
+    return bad ? nan : empty ? -kInf : z;
+  };
   if (a.entropy && tid == 0) a.entropy[row_id] = bad ? nan : empty ? 0.f : fmaxf(log_s - kLn2 * (sum.t / sum.s), 0.f);
   if (a.logp)
     for (int i = tid; i < a.n; i += kThreads) {
