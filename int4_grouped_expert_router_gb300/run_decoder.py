@@ -149,12 +149,12 @@ def main(argv=None):
         new = [args.prompt if step == 0 else 1] * args.batch
         h = layer.moe.act_tensor(synth.normal(synth.stream_seed(cfg.seed, "hidden", step), sum(new) * cfg.D)
                                  .reshape(-1, cfg.D))
+        last = None if sum(new) == len(new) else torch.tensor(np.cumsum(new) - 1, device=h.device)
         a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
         a.record()
         _, n = layer.forward(h, new)
         if head is not None:
-            last = torch.tensor(np.cumsum(new) - 1, device=n.device)
-            answers.append(head.forward(n[last]))
+            answers.append(head.forward(n if last is None else n[last]))
         b.record()
         b.synchronize()
         times.append(a.elapsed_time(b) * 1000.0)
