@@ -539,7 +539,7 @@ COLI_API int coli_dense_free(coli_ctx *ctx, uint64_t handle);
  *   COLI_ACT_RELU2      max(z, 0)^2
  * y may be mul or resid (same address and stride); no other overlap of y with an input. 1 <= S <= COLI_MAX_TOKENS.
  * Products of bfloat16 values are exact; binary32 activations enter as three bfloat16 parts that add up to them (two, 16 bits,
- * where y is bfloat16). Sums are held in binary32, as the tensor core cuts them off (towards zero); where y is binary32 they are
+ * where y is bfloat16), but for what lies below 2^-133, where bfloat16 ends: of values from 2^-110 on nothing does. Sums are held in binary32, as the tensor core cuts them off (towards zero); where y is binary32 they are
  * added in registers every 256 columns. y is rounded once. Results do not change from run to run; a row's depend on S (tiles are
  * chosen by the sizes). A sum of products that is not finite sets COLI_E_NONFINITE; what is not finite in x or W spoils the outputs
  * of its own row alone.

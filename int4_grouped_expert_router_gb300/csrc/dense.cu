@@ -15,7 +15,8 @@
 // 6144, 195 us for 169; twice as long chunks lose twice as much for half of that; of binary32 activations chunks half as long lose half
 // as much and take 3 to 15 % longer). Errors against 64 bits, in norm: 2.7e-7 for 6144
 // columns of bf16, 2.4e-7 of binary32 (7.7e-7 in tiles of 128 tokens and more); a binary32 product sum by sum: 8.6e-7, 1.4e-6.
-// Binary32 activations enter as parts of 8 bits by truncation, x = h + m + l exactly (two parts, 16 bits, where y is rounded to 8),
+// Binary32 activations enter as parts of 8 bits by truncation, x = h + m + l exactly from 2^-110 on, to 2^-133 below (two parts, 16
+// bits, where y is rounded to 8),
 // each multiplied with the same staged tile of W. Where the parts' columns are 256 at most they are one instruction's, which reads
 // the tile once (24 tokens, 6144 x 6144: 18.4 us against 21.1), and their sums are added by the last warps.
 // Measured (us; W = O x I): one token, 6144 x 6144, residual 14.3 (5.3 TB/s, 0.78 of a copy's rate), f32 17.8; 24 tokens, 50021 x

@@ -46,3 +46,18 @@ def test_sums_are_held_in_chunks(ctx, S, I, O_, x_dtype):
     bound = ((times * lost(16)) ** 2 + added ** 2) ** 0.5
     assert bound < 0.5 * times * lost(I // 16)  # what it would be without chunks
     assert off <= 1.1 * bound, (off, bound)  # a tenth for the sample
+
+
+@pytest.mark.parametrize("S", [1, 64, 600])
+def test_tiny_binary32_activations(ctx, S):
+    """W = 1: values from 2^-110 on arrive whole, smaller ones to a multiple of 2^-133, the smallest bfloat16."""
+    h = B.coli_dense_upload(ctx, torch.eye(64, dtype=torch.bfloat16))
+    g = torch.Generator(device="cuda").manual_seed(S)
+    for e in (100, 110, 111, 118, 126, 127, 133, 134, 149):
+        x = ((1 + torch.rand(S, 64, dtype=torch.float64, device="cuda", generator=g)) * 2.0 ** -e).float()
+        y = torch.empty(S, 64, device="cuda")
+        B.coli_dense_linear(ctx, h, x, y)
+        off = (y.double() - x.double()).abs()
+        assert (off == 0).all() if e <= 110 else (off < 2.0 ** -133).all()
+    assert B.coli_check_error(ctx) == 0
+    B.coli_dense_free(ctx, h)
