@@ -569,7 +569,8 @@ COLI_API int coli_dense_linear(coli_ctx *ctx, uint64_t W, int I, int O, const vo
  *     have id -1 and log p -infinity.
  * Entries of -infinity have probability 0. A row that has nothing else gives log p = -infinity and entropy 0. A NaN or
  * +infinity sets COLI_E_NONFINITE; its row is NaN, its ids -1. Sums and logarithms are held in binary32, relative to the largest
- * entry. scale, the inverse temperature, from 1e-30 to 1e30. 1 <= S <= COLI_MAX_TOKENS, V <= COLI_MAX_VOCAB, n <= COLI_MAX_VOCAB.
+ * entry: log p is never above 0, and of a token that is close to certain it has an absolute error, not a relative one (of a probability
+ * of 1 - 10^-8 it is 0). scale, the inverse temperature, from 1e-30 to 1e30. 1 <= S <= COLI_MAX_TOKENS, V <= COLI_MAX_VOCAB, n <= COLI_MAX_VOCAB.
  * No output overlaps another array. Results do not change from run to run. Profiled as COLI_KERNEL_LOGPROBS.
  */
 COLI_API int coli_logprobs(coli_ctx *ctx, const void *logits, long long stride, int dtype, int S, int V, float scale,

@@ -487,12 +487,14 @@ __global__ void __launch_bounds__(kThreads, kLogprobCtas) logprob_kernel(Logprob
   }
 
   // ---- the answers ----
-  sum.move(most, c);  // of the largest entry: what is close to certain keeps its digits
+  // Of the largest entry: s is from 1 on, but for the error of what carried it there. Log p has an absolute error, a few times 2^-24: of
+  // a token that is close to certain the digits of 1 - p are those that s = 1 + ... has.
+  sum.move(most, c);
   const bool bad = !(sum.s < kInf);  // a NaN, or an infinity among the entries
   const bool empty = sum.s == 0.f;
   const float nan = __uint_as_float(0x7fc00000u);
   if (bad && tid == 0) set_error(a.err, COLI_E_NONFINITE);
-  const float base = Sums::from(most), log_s = logf(sum.s);
+  const float base = Sums::from(most), log_s = fmaxf(logf(sum.s), 0.f);
   auto log_p = [&](float x) {
     const float d = x - base;
     // a difference beyond binary32 of entries that are not, which the scale may bring back

@@ -36,3 +36,50 @@ def test_differences_beyond_binary32(S, V, scale, dtype):
         assert (np.abs(out["entropy"].cpu().numpy() - entropy) <= 2.0 ** -18).all()
     finally:
         c.close()
+
+
+@pytest.mark.parametrize("S,V", [(1, 5000), (700, 5000), (2, 70001)])
+def test_close_to_certain(S, V):
+    """One entry takes all but 1e-3 to 1e-12 of a row. Its log p is never above 0; its error and the entropy's are those of at most V / 512 +
+    64 roundings of s = 1 + ... and of the logarithm: absolute ones."""
+    c = Ctx()
+    try:
+        for tail in (1e-3, 1e-5, 1e-7, 1e-9, 1e-12):
+            x = np.full((S, V), np.log(tail / (V - 1)), np.float32)
+            x += 0.1 * np.random.default_rng(7).normal(size=V).astype(np.float32)
+            at = np.arange(S) * 7919 % V
+            x[np.arange(S), at] = 3.0
+            xt = torch.from_numpy(x).cuda()
+            tokens = torch.from_numpy(at.astype(np.int32)).cuda()[:, None].contiguous()
+            logp, entropy = torch.empty(S, 1, device="cuda"), torch.empty(S, device="cuda")
+            B.coli_logprobs(c.ctx, xt, tokens=tokens, logp=logp, entropy=entropy)
+            assert B.coli_check_error(c.ctx) == 0
+            lp, h = O.logprobs(x)
+            got = logp.double().cpu().numpy()[:, 0]
+            tol = (V / 512 + 64) * 2.0 ** -24 + 2.0 ** -22
+            assert (got <= 0).all() and (np.abs(got - lp[np.arange(S), at]) <= tol).all()
+            got = entropy.double().cpu().numpy()
+            assert (got >= 0).all() and (np.abs(got - h) <= tol + 2.0 ** -20 * h).all()
+    finally:
+        c.close()
+
+
+@pytest.mark.parametrize("S", [1, 700])
+def test_log_p_is_never_above_0(S):
+    """Logits so large that the next one above is 8 to 32 further: what precedes the largest entry carries almost nothing, and what is left is 1."""
+    c = Ctx()
+    try:
+        for first in (1e8, 1.5e8, 2.5e8, 5e8, 3e9):
+            for step in (8, 16, 24, 32, 64):
+                x = np.zeros((S, 5000), np.float32)
+                x[:, 0], x[:, 1024] = first, np.float32(first) + np.float32(step)
+                xt = torch.from_numpy(x).cuda()
+                logp, entropy = torch.empty(S, 1, device="cuda"), torch.empty(S, device="cuda")
+                B.coli_logprobs(c.ctx, xt, tokens=torch.full((S, 1), 1024, dtype=torch.int32, device="cuda"), logp=logp, entropy=entropy)
+                assert B.coli_check_error(c.ctx) == 0
+                lp, h = O.logprobs(x[:1])
+                assert (logp <= 0).all() and (np.abs(logp.double().cpu().numpy() - lp[0, 1024]) <= 2.0 ** -20).all()
+                # t adds up terms of up to 2^5 powers of two that round to 2^-24 each
+                assert (entropy >= 0).all() and (np.abs(entropy.double().cpu().numpy() - h) <= 2.0 ** -17).all()
+    finally:
+        c.close()
