@@ -102,3 +102,32 @@ def test_a_copy_that_never_comes_to_a_pair(S, I, O_, x_dtype, y):
             close(out, want, I, x_dtype)
     finally:
         c.close()
+
+
+@pytest.mark.parametrize("x_dtype,y", TYPES)
+@pytest.mark.parametrize("S,I,O_", [(512, 1280, 6144), (300, 6144, 2100)])
+def test_captures_replay(ctx, S, I, O_, x_dtype, y):
+    """Pairs of CTAs, whole and split tiles, in a graph: new activations each replay, the bits of calls outside it."""
+    h, x, want = make(ctx, S, I, O_, x_dtype)
+    out, stream, before = torch.empty(S, O_, dtype=DT[y], device="cuda"), torch.cuda.Stream(), torch.cuda.current_stream()
+    xs = [x.clone(), -x, x.flip(0), x * 2]
+    outside = []
+    for v in xs:
+        B.coli_dense_linear(ctx, h, v, out)
+        outside.append(out.clone())
+    close(outside[0], want, I, x_dtype)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        B.coli_set_stream(ctx, stream)
+        for _ in range(3):
+            B.coli_dense_linear(ctx, h, x, out)
+    B.coli_set_stream(ctx, before)
+    for v, one in zip(xs, outside):
+        x.copy_(v)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, one)
+    assert B.coli_check_error(ctx) == 0
+    B.coli_dense_free(ctx, h)
