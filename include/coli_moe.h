@@ -54,10 +54,10 @@ extern "C" {
 #define COLI_E_CUDA -3       /* a CUDA runtime call or kernel launch failed */
 #define COLI_E_INJECTED -4   /* COLI_FAIL_AFTER test hook fired; nothing was launched */
 #define COLI_E_FORMAT -5     /* weight format rejected: odd I, odd or negative gs, shape mismatch */
-#define COLI_E_NONFINITE -6  /* (device) non-finite activation or router score */
+#define COLI_E_NONFINITE -6  /* (device) non-finite activation, router score, logit or cache entry */
 #define COLI_E_ROUTE -7      /* (device) expert index outside the table or naming an unset entry */
 #define COLI_E_TIMEOUT -8    /* (device) a bounded wait inside a kernel gave up (never expected) */
-#define COLI_E_RANGE -9      /* (device) a cache length, page index or row range outside its array */
+#define COLI_E_RANGE -9      /* (device) a length, page index, token or row range outside its array */
 
 #define COLI_DTYPE_F32 0     /* IEEE binary32 */
 #define COLI_DTYPE_BF16 1    /* bfloat16 (upper half of a binary32) */
@@ -539,8 +539,9 @@ COLI_API int coli_dense_free(coli_ctx *ctx, uint64_t handle);
  *   COLI_ACT_RELU2      max(z, 0)^2
  * y may be mul or resid (same address and stride); no other overlap of y with an input. 1 <= S <= COLI_MAX_TOKENS.
  * Products of bfloat16 values are exact; binary32 activations enter as three bfloat16 parts that add up to them (two, 16 bits,
- * where y is bfloat16), but for what lies below 2^-133, where bfloat16 ends: of values from 2^-110 on nothing does. Sums are held in binary32, as the tensor core cuts them off (towards zero); where y is binary32 they are
- * added in registers every 256 columns. y is rounded once. Results do not change from run to run; a row's depend on S (tiles are
+ * where y is bfloat16), but for what lies below 2^-133, where bfloat16 ends: of values from 2^-110 on nothing does. Sums are
+ * held in binary32, as the tensor core cuts them off (towards zero); where y is binary32 they are added in registers every 256
+ * columns. y is rounded once. Results do not change from run to run; a row's depend on S (tiles are
  * chosen by the sizes). A sum of products that is not finite sets COLI_E_NONFINITE; what is not finite in x or W spoils the outputs
  * of its own row alone.
  * Binary32 activations, and rows of x that do not start at 16-byte boundaries, are first laid out in the workspace: for a call
@@ -569,8 +570,8 @@ COLI_API int coli_dense_linear(coli_ctx *ctx, uint64_t W, int I, int O, const vo
  *     have id -1 and log p -infinity.
  * Entries of -infinity have probability 0. A row that has nothing else gives log p = -infinity and entropy 0. A NaN or
  * +infinity sets COLI_E_NONFINITE; its row is NaN, its ids -1. Sums and logarithms are held in binary32, relative to the largest
- * entry: log p is never above 0, and of a token that is close to certain it has an absolute error, not a relative one (of a probability
- * of 1 - 10^-8 it is 0). scale, the inverse temperature, from 1e-30 to 1e30. 1 <= S <= COLI_MAX_TOKENS, V <= COLI_MAX_VOCAB, n <= COLI_MAX_VOCAB.
+ * entry: log p is never above 0, and its error is absolute, not relative (of a probability of 1 - 10^-8 it is 0). scale, the
+ * inverse temperature, from 1e-30 to 1e30. 1 <= S <= COLI_MAX_TOKENS, V <= COLI_MAX_VOCAB, n <= COLI_MAX_VOCAB.
  * No output overlaps another array. Results do not change from run to run. Profiled as COLI_KERNEL_LOGPROBS.
  */
 COLI_API int coli_logprobs(coli_ctx *ctx, const void *logits, long long stride, int dtype, int S, int V, float scale,

@@ -13,8 +13,8 @@
 // Sums. The tensor core cuts a sum off where binary32 would round it, always towards zero: 6144 products lose some 2^-17 that
 // way. Where y is binary32 chunks of kChunk column tiles are formed by themselves and added in registers (of 4096 tokens, 6144 x
 // 6144, 195 us for 169; twice as long chunks lose twice as much for half of that; of binary32 activations chunks half as long lose half
-// as much and take 3 to 15 % longer). Errors against 64 bits, in norm: 2.7e-7 for 6144
-// columns of bf16, 2.4e-7 of binary32 (7.7e-7 in tiles of 128 tokens and more); a binary32 product sum by sum: 8.6e-7, 1.4e-6.
+// as much and take 3 to 15 % longer). Errors against 64 bits, in norm: 2.4e-7 for 6144
+// columns of bf16 and of binary32 (7.7e-7 in tiles of 128 tokens and more); without chunks 1.2e-6 to 5e-6 (1.8e-5).
 // Binary32 activations enter as parts of 8 bits by truncation, x = h + m + l exactly from 2^-110 on, to 2^-133 below (two parts, 16
 // bits, where y is rounded to 8),
 // each multiplied with the same staged tile of W. Where the parts' columns are 256 at most they are one instruction's, which reads
@@ -22,8 +22,8 @@
 // Measured (us; W = O x I): one token, 6144 x 6144, residual 14.3 (5.3 TB/s, 0.78 of a copy's rate), f32 17.8; 24 tokens, 50021 x
 // 6144, f32 logits 92 (6.7 TB/s, 0.98): bound by W's bytes, and at the small end by launch, first stages and the join of parts (4
 // us). 301 f32 tokens, 2048 x 6144, silu and factor 32: L2 bytes, the join, and x laid out ahead. 4096 tokens, 6144 x 6144, gelu,
-// bias, residual 185 (1670 TFLOP/s); the bare product 168, as long as the library's beside it. Over seconds, at the 1.47 GHz that
-// the power limit leaves, 207, 194 and 189. Tensor pipe active 82 % of the time.
+// bias, residual 211 (1465 TFLOP/s) over seconds, at the 1.47 GHz that the power limit leaves, the bare product 196, the library's 192;
+// in short runs 187, 169 and 169. Tensor pipe active 82 % of the time.
 // What it cost to find: factor and residual read where they are used, not a group ahead (prompt 348 us; 252 so); one CTA's 128 x
 // 256 tiles, which ask L2 for 96 bytes a cycle and SM (219 us bare; pairs 183); 24 bytes of spilled registers inside the loop over
 // chunks (480 us instead of 214: the ring leaves no first-level cache); even runs of many tiles for every

@@ -12,10 +12,10 @@
 // Where ties make it more than there is room for, the k-th largest of those found is a higher bound of the same kind, and the
 // search repeats.
 //
-// Measured: 2048 rows of 65536 (f32, one alternative) 87 us, 6.2 TB/s, 0.91 of a copy's rate (0.98 without alternatives, 113 us
-// with 20: their entries come from memory again); 64 rows of 151001 (bf16, 20 alternatives, 9 CTAs a row) 14.4 us, 9.6 without
-// alternatives: a chain of round trips to L2 (entries, parts written, counted, read) and barriers; one row of 50021 7 us, 4.4 without. A vector on its way in
-// registers instead of shared memory held the f32 rows to 4.1 TB/s (143 us); a maximum that moves with every larger entry, 151 us
+// Measured: 2048 rows of 65536 (f32, one alternative) 89 us, 6.0 TB/s, 0.89 of a copy's rate (0.95 without alternatives, 114 us
+// with 20: their entries come from memory again); 64 rows of 151001 (bf16, 20 alternatives, 9 CTAs a row) 14.2 us, 9.4 without
+// alternatives: a chain of round trips to L2 (entries, parts written, counted, read) and barriers; one row of 50021 6.8 us, 4.2
+// without. A vector on its way in registers instead of shared memory held the f32 rows to 4.1 TB/s (143 us); a maximum that moves with every larger entry, 151 us
 // then; threads that look through their own entries alone, 290 us with 20 alternatives; bounds from 32 groups, four times the
 // entries to rank for 32 alternatives.
 #include "logprobs.h"
@@ -31,7 +31,7 @@ constexpr int kRoom = kLogprobMostParts * COLI_MAX_TOP;  // entries that reach t
 constexpr int kLooks = 2;    // vectors that a thread looks through together
 constexpr int kFlight = 7;   // vectors of a thread on their way
 // Vectors of a thread that are not worth another CTA of the row: they are on their way together, and fewer parts are joined
-// sooner (15 rows of 32003, 32 alternatives: 9.8 us with 4, 12.5 with 1).
+// sooner (15 rows of 32003, 32 alternatives: 9.2 us with 4, 12.5 with 1).
 constexpr int kFew = 4;
 constexpr int kGroups = 64, kPerGroup = kThreads / kGroups;  // groups of threads whose maxima make the bound
 constexpr float kInf = __builtin_huge_valf();

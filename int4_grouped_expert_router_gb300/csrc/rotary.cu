@@ -7,11 +7,11 @@
 // Bound by memory: q and k are read and written once. The sines and cosines of a row are shared by all of its heads, so a CTA
 // takes whole rows and makes their table in shared memory while its first loads are on their way; few heads are several rows.
 //
-// Measured: 8191 rows of 64 + 8 heads of 128 (bf16) 52 us, 5.8 TB/s, 0.85 of a copy's rate, neighbouring channels 60 us, f32
-// 90 us (0.99); 3001 f32 rows of 40 heads of 80, 36 channels turned, 19.8 us (3.9 TB/s); one row 3.5 us on the device, less
-// than the call takes on the host (7.6 us). Bound by the table's latency (plan, frequency, sine) at the start of each CTA. Five
-// CTAs of 256 threads in 48 registers beat three of 384 in 56 (57 us) and four of 384 in 40 (67 us, spills); copies behind the
-// turned part two vectors at a time took the f32 case from 22 to 18 us.
+// Measured: 8191 rows of 64 + 8 heads of 128 (bf16) 53 us, 5.7 TB/s, 0.85 of a copy's rate, neighbouring channels 61 us, f32
+// 90 us (0.99); 3001 f32 rows of 40 heads of 80, 36 channels turned, 18.8 us (4.1 TB/s; 22 before copies behind the turned part went two
+// vectors at a time); one row 2.9 us on the device, less than the call takes on the host (7.9 us). Bound by the table's latency (plan,
+// frequency, sine) at the start of each CTA. Five CTAs of 256 threads in 48 registers, which spill 12 to 20 bytes a thread, beat three
+// of 384 in 56 (57 us) and four of 384 in 40 (67 us, more spills).
 #include <cuda_bf16.h>
 
 #include <cmath>
